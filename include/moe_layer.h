@@ -314,6 +314,51 @@ int moe_read_status(const moe_shape* shape, const void* route_ws, int32_t* out, 
 int moe_selftest_wait_timeout(const moe_shape* shape, void* route_ws, uint64_t limit_ns, int64_t* elapsed_ns,
                               void* stream);
 
+/* ------------------------------------------------------------------------
+ * The rest of a block around the routed experts.  The pages have no
+ * counterpart of these entry points: the norm in front of the router and the
+ * experts, the dense gated feed-forward block that runs beside them (a shared
+ * expert), and both kinds of experts with 4-bit weights for serving.  The
+ * conventions above hold for them too.
+ * ---------------------------------------------------------------------- */
+
+/* Element types of the entry points that take more than one. */
+enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
+
+/* Layer norm over the last axis: for each row r of x [rows, H]
+ *     m = mean_h x        s = 1 / sqrt(mean_h (x - m)^2 + eps)
+ *     y = (x - m) s weight + bias
+ * x_type: type of x and y; w_type: type of weight and bias [H], MOE_F32 or
+ * x_type.  x_stride >= H: elements between the starts of two rows of x (the
+ * last axis is contiguous; y is contiguous).  bias may be NULL (none).
+ * Overwrites y, and mean f32[rows] and rstd f32[rows] (m and s, for the
+ * backward).  Any H >= 1 and any 0 <= rows < 2^31; pointers need only their
+ * element's alignment (16-byte vectors are used where width, stride and
+ * addresses allow).  Statistics are FP32, y is rounded once.  A row that
+ * holds a NaN or an infinity gives NaN, as the formula does.
+ * Errors: MOE_EINVAL for NULL, a size out of range, a stride below H, eps not
+ * finite or negative; MOE_EUNSUPPORTED for a type or an alignment. */
+int moe_layer_norm_forward(int64_t rows, int32_t H, int32_t x_type, int32_t w_type, const void* x, int64_t x_stride,
+                           const void* weight, const void* bias, float eps, void* y, float* mean, float* rstd,
+                           void* stream);
+
+/* Bytes of the workspace of moe_layer_norm_backward.  Host only. */
+int moe_layer_norm_workspace(int64_t rows, int32_t H, size_t* bytes);
+
+/* Backward of moe_layer_norm_forward given dy [rows, H] (x's type, rows
+ * dy_stride elements apart) and the forward's x, weight, mean and rstd:
+ *     z = (x - m) s,  g = dy weight
+ *     dx = s (g - mean_h g - z mean_h(g z))     [rows, H], contiguous, x_type
+ *     dweight = sum_r dy z,  dbias = sum_r dy   [H], w_type; dbias may be NULL
+ * All three are overwritten (rows = 0: dweight and dbias become 0).  ws holds
+ * moe_layer_norm_workspace bytes of scratch (f32 partial sums, 4-byte aligned).  The column
+ * sums are FP32 in a fixed order: deterministic, no atomics.  Errors as for
+ * the forward. */
+int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_type, const void* dy,
+                            int64_t dy_stride, const void* x, int64_t x_stride, const void* weight,
+                            const float* mean, const float* rstd, void* dx, void* dweight, void* dbias, void* ws,
+                            void* stream);
+
 /* Tracing.  moe_trace_begin hands the library `capacity` CUDA events
  * (cudaEvent_t passed as void*, created by the caller with timing enabled).
  * Until moe_trace_end, each kernel the library launches from this thread is

@@ -78,6 +78,12 @@ def lib():
                       "moe_quantize_fp8", "moe_dequantize_fp8", "moe_forward_fp8", "moe_quantize_weights_fp8",
                       "moe_quantize_w2_fp8", "moe_read_status"):
                 getattr(L, n).restype = ctypes.c_int
+            i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+            L.moe_layer_norm_forward.argtypes = [i64, i32, i32, i32, vp, i64, vp, vp, f32, vp, vp, vp, vp]
+            L.moe_layer_norm_workspace.argtypes = [i64, i32, P(ctypes.c_size_t)]
+            L.moe_layer_norm_backward.argtypes = [i64, i32, i32, i32, vp, i64, vp, i64] + [vp] * 8
+            for n in ("moe_layer_norm_forward", "moe_layer_norm_workspace", "moe_layer_norm_backward"):
+                getattr(L, n).restype = ctypes.c_int
             L.moe_trace_begin.argtypes = [vp, ctypes.c_int]
             L.moe_trace_begin.restype = ctypes.c_int
             L.moe_trace_end.argtypes = []
@@ -250,6 +256,70 @@ def moe_read_status(shape: MoeShape, route_ws, stream=None) -> list[int]:
     _check(lib().moe_read_status(ctypes.byref(shape), _ptr(route_ws, torch.uint8, L.route_bytes, "route_ws"),
                                  ctypes.cast(out, ctypes.c_void_p), _stream(stream)))
     return list(out)
+
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # MOE_BF16, MOE_F16, MOE_F32
+
+
+def _type_of(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor")
+    return _TYPES[t.dtype]
+
+
+def _rows_ptr(t, dtype, rows, H, name):
+    """(pointer, row stride) of a CUDA tensor [rows, H] whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (rows, H):
+        raise ValueError(f"{name} must be [{rows}, {H}], got {list(t.shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if H > 1 and t.stride(1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    stride = t.stride(0) if rows > 1 else H
+    if stride < H:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.data_ptr(), stride
+
+
+def moe_layer_norm_workspace(rows: int, H: int) -> int:
+    """Bytes of moe_layer_norm_backward's workspace."""
+    out = ctypes.c_size_t()
+    _check(lib().moe_layer_norm_workspace(rows, H, ctypes.byref(out)))
+    return out.value
+
+
+def moe_layer_norm_forward(x, weight, bias, eps: float, y, mean, rstd, stream=None):
+    """y = (x - mean) * rstd * weight + bias over the last axis of x [rows, H]
+    (bf16, f16 or f32; rows may be strided); weight and bias [H] in x's type
+    or f32, bias may be None.  Overwrites y [rows, H], mean and rstd f32 [rows]."""
+    tx = _type_of(x, "x")
+    rows, H = x.shape
+    px, sx = _rows_ptr(x, x.dtype, rows, H, "x")
+    wt = weight.dtype
+    _check(lib().moe_layer_norm_forward(
+        rows, H, tx, _type_of(weight, "weight"), px, sx, _ptr(weight, wt, H, "weight"), _ptr(bias, wt, H, "bias"), eps,
+        _ptr(y, x.dtype, rows * H, "y"), _ptr(mean, torch.float32, rows, "mean"), _ptr(rstd, torch.float32, rows, "rstd"),
+        _stream(stream)))
+
+
+def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream=None):
+    """Backward of moe_layer_norm_forward: overwrites dx [rows, H] (x's type),
+    dweight and dbias [H] (weight's type; dbias may be None).  ws: uint8 of
+    moe_layer_norm_workspace(rows, H) elements."""
+    tx = _type_of(x, "x")
+    rows, H = x.shape
+    px, sx = _rows_ptr(x, x.dtype, rows, H, "x")
+    pd, sd = _rows_ptr(dy, x.dtype, rows, H, "dy")
+    wt, f32 = weight.dtype, torch.float32
+    _check(lib().moe_layer_norm_backward(
+        rows, H, tx, _type_of(weight, "weight"), pd, sd, px, sx, _ptr(weight, wt, H, "weight"),
+        _ptr(mean, f32, rows, "mean"), _ptr(rstd, f32, rows, "rstd"), _ptr(dx, x.dtype, rows * H, "dx"),
+        _ptr(dweight, wt, H, "dweight"), _ptr(dbias, wt, H, "dbias"),
+        _ptr(ws, torch.uint8, moe_layer_norm_workspace(rows, H), "ws"), _stream(stream)))
 
 
 def moe_last_error() -> str:

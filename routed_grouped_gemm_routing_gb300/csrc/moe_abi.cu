@@ -317,6 +317,23 @@ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 }  // namespace
 
+int abi_fail(int code, const char* msg) { return fail(code, msg); }
+int abi_cuda_fail(int cuda_error, const char* what) { return cuda_fail(cuda_error, what); }
+int abi_select_device(const void* data, int* sms) {
+    Ctx c;
+    const int rc = query_device(&c, data);
+    if (!rc) *sms = c.sms;
+    return rc;
+}
+int abi_map_2d(CUtensorMap* m, const void* p, int elt, long long rows, long long cols, long long stride_elems,
+               int box_cols, int box_rows, const char* what) {
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t str[1] = {(cuuint64_t)stride_elems * (cuuint64_t)elt};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    return make_map(m, p, 2, dims, str, box, what, CU_TENSOR_MAP_SWIZZLE_128B,
+                    elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+
 int compute_layout(const moe_shape* s, moe_layout* L) {
     memset(L, 0, sizeof *L);
     const long long tk = (long long)s->T * s->k;

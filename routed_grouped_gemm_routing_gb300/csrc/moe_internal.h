@@ -78,6 +78,42 @@ struct GemmMaps {
     CUtensorMap a, b, c0, c1, d;
 };
 
+// Host-side helpers of the C ABI, shared by its translation units: they set
+// the thread's error message and return the code (MOE_ECUDA for a CUDA error).
+int abi_fail(int code, const char* msg);
+int abi_cuda_fail(int cuda_error, const char* what);
+// Makes the device that owns `data` current and gives its SM count.
+int abi_select_device(const void* data, int* sms);
+// Tensor map of rank 2, row-major, 128-byte swizzle unless plain: element
+// size 2 (bf16) or 4 (f32); box_cols * element size must be 128 when swizzled.
+int abi_map_2d(CUtensorMap* m, const void* p, int elt, long long rows, long long cols, long long stride_elems,
+               int box_cols, int box_rows, const char* what);
+
+// ------------------------------------------------------------- layer norm
+struct LnFwdArgs {
+    long long rows;
+    int H;
+    const void *x, *weight, *bias;  // bias may be null
+    long long x_stride;             // elements between rows of x
+    float eps;
+    void* y;            // [rows, H]
+    float *mean, *rstd;  // [rows]
+};
+struct LnBwdArgs {
+    long long rows;
+    int H;
+    const void *dy, *x, *weight;
+    long long dy_stride, x_stride;
+    const float *mean, *rstd;
+    void *dx, *dweight, *dbias;  // dbias may be null
+    float* part;                 // [min(rows, kLnBwdBlocks)][2][H]
+};
+// Partial sums of the weight's and bias's gradients that a backward leaves at
+// most: two blocks on each of the 152 SMs.
+constexpr int kLnBwdBlocks = 304;
+int launch_layer_norm_fwd(int x_type, int w_type, const LnFwdArgs& a, cudaStream_t st);
+int launch_layer_norm_bwd(int x_type, int w_type, const LnBwdArgs& a, cudaStream_t st);
+
 // Layout of the three workspaces (host only).
 int compute_layout(const moe_shape* s, moe_layout* L);
 
