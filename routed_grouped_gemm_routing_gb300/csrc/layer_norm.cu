@@ -11,17 +11,35 @@
 // Bound by DRAM: the forward reads x and writes y, the backward reads x and
 // dy and writes dx.
 //
-// A row stays in registers between the passes: one warp per row up to 128
-// vectors, one block per row above, each thread holding NV vectors of V
-// elements (16 bytes; V = 1 where the width, a stride or a base address is
-// not a multiple of 16 bytes).  Rows too long for that are read again for
-// every pass (ln_fwd_long, ln_bwd_long): the second and third time from L2.
+// Three forms, by a rule on sizes and alignment (ln_form):
+//  * ring: widths, strides and addresses that are multiples of 16 bytes, rows
+//    up to 2048 vectors.  Persistent blocks cut into groups; a group takes one
+//    row at a time, each of its gt threads NV 16-byte vectors of it.  Every
+//    thread copies its own vectors of the group's next rows ahead with
+//    cp.async into its own slots of shared memory (so no barrier guards the
+//    copies, and rows stay in flight whatever a row's reduction waits for),
+//    and keeps its columns' weight (and the backward's column sums) in
+//    registers for the life of the block: read per row, an FP32 weight and
+//    bias are four times the bytes of a bf16 row.
+//    At bf16 the instructions of the reductions, not DRAM, bounded a form in
+//    which every warp reduced (two chains of five shuffles per sum and warp:
+//    22 of the forward's 56 us at 8192 x 7168).  So a group of several warps
+//    has one more warp that only reduces: step n of a group is row n's
+//    per-thread partials (one store each), row n - 1's reduction by that warp
+//    and row n - 2's output, side by side, then one barrier.  A group of one
+//    warp reduces by shuffles.
+//  * register: other widths, one element at a time; one warp per row up to
+//    128 elements, one block per row above.
+//  * long: rows too long for the others are read again for every pass (the
+//    second and third time from L2).
 //
 // The weight's and bias's gradients: every block of the backward sums its own
 // rows' dy z and dy per column in registers and leaves one row of partial
 // sums; a second kernel adds the partials of each column in a fixed order
 // (deterministic, no atomics).
 #include "moe_internal.h"
+#include "ptx.cuh"
+#include "smem_limit.h"
 
 #include <cuda_fp16.h>
 
@@ -30,8 +48,13 @@ namespace moe {
 namespace {
 
 constexpr int kLnWarps = 4;         // rows per block of the one-warp-per-row form
-constexpr int kLnWarpVecs = 128;    // vectors of a row up to which one warp takes it
 constexpr int kLnLongThreads = 1024;
+// ring form: threads per block (128 registers each), rows held or in flight
+// per group
+constexpr int kLnRingThreads = 512;
+constexpr int kLnFwdRing = 6;
+__host__ __device__ constexpr int ln_bwd_ring_rows(int nv) { return nv > 2 ? 3 : 6; }
+constexpr int kLnMaxGroups = 16, kLnGroupWarps = 16;
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
@@ -98,45 +121,28 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     return v;
 }
 
-// ------------------------------------------------------------------ forward
-template <typename T, typename W, int V, int NV, bool kWarpRow>
-__global__ void __launch_bounds__(1024) ln_fwd(long long rows, int H, const T* __restrict__ x, long long xs,
-                                               const W* __restrict__ w, const W* __restrict__ b, float eps,
-                                               T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
+// ------------------------------------------------------------ register form
+template <typename T, typename W, int NV, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarps : 1024)
+    ln_fwd(long long rows, int H, const T* __restrict__ x, long long xs, const W* __restrict__ w,
+           const W* __restrict__ b, float eps, T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
     __shared__ float red[64];
     const long long row = kWarpRow ? (long long)blockIdx.x * kLnWarps + (threadIdx.x >> 5) : (long long)blockIdx.x;
     if (row >= rows) return;  // whole warps of the one-warp-per-row form
     const int t = kWarpRow ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int nt = kWarpRow ? 32 : (int)blockDim.x;
-    const int nvec = H / V;
     const T* xr = x + row * xs;
-    float v[NV][V];
+    float v[NV];
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = t + i * nt;
-        if (c < nvec) {
-            load_vec<T, V>(xr + (size_t)c * V, v[i]);
-        } else {
+    for (int i = 0; i < NV; ++i) v[i] = t + i * nt < H ? to_f(__ldg(xr + t + i * nt)) : 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) s += v[i][j];
+    for (int i = 0; i < NV; ++i) s += v[i];
     const float m = row_sum<kWarpRow>(s, red) / (float)H;
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (t + i * nt < nvec) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = v[i][j] - m;
-                q = fmaf(d, d, q);
-            }
-        }
+        if (t + i * nt < H) q = fmaf(v[i] - m, v[i] - m, q);
     const float r = 1.0f / sqrtf(row_sum<kWarpRow>(q, red + 32) / (float)H + eps);
     if (t == 0) {
         mean[row] = m;
@@ -146,18 +152,281 @@ __global__ void __launch_bounds__(1024) ln_fwd(long long rows, int H, const T* _
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = t + i * nt;
-        if (c < nvec) {
-            float wv[V], o[V];
-            load_vec<W, V>(w + (size_t)c * V, wv);
-#pragma unroll
-            for (int j = 0; j < V; ++j) o[j] = (v[i][j] - m) * r * wv[j];
-            if (b) {
-                load_vec<W, V>(b + (size_t)c * V, wv);
-#pragma unroll
-                for (int j = 0; j < V; ++j) o[j] += wv[j];
-            }
-            store_vec<T, V>(yr + (size_t)c * V, o);
+        if (c < H) {
+            float o = (v[i] - m) * r * to_f(__ldg(w + c));
+            if (b) o += to_f(__ldg(b + c));
+            yr[c] = from_f<T>(o);
         }
+    }
+}
+
+// ---------------------------------------------------------------- ring form
+// Named barrier 1 + g over a group's threads (its reducing warp among them).
+__device__ __forceinline__ void group_sync(int g, int n) {
+    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(n) : "memory");
+}
+
+// Two floats in one 64-bit register pair: add, multiply and fused multiply-add
+// take both at once, which halves the instructions of these kernels (at bf16
+// the instruction issue, not DRAM, bounded the scalar form).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_make(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 f2_get(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+    const float2 t = f2_get(v);
+    return t.x + t.y;
+}
+
+// Two elements packed in a word as floats, and back.
+template <typename T>
+__device__ __forceinline__ f2 unpack2(uint32_t u);
+template <>
+__device__ __forceinline__ f2 unpack2<__nv_bfloat16>(uint32_t u) {
+    return f2_make(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ f2 unpack2<__half>(uint32_t u) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+    return f2_make(f.x, f.y);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(f2 v);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(f2 v) {
+    const float2 f = f2_get(v);
+    return pack_bf16x2(f.x, f.y);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(f2 v) {
+    const float2 f = f2_get(v);
+    const __half2 h = __floats2half2_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// A 16-byte vector of T as P = 8 / sizeof(T) pairs, and back.
+template <typename T, int P>
+__device__ __forceinline__ void unpack_vec(const uint4& u, f2 (&f)[P]) {
+    if constexpr (sizeof(T) == 4) {
+        f[0] = f2_make(__uint_as_float(u.x), __uint_as_float(u.y));
+        f[1] = f2_make(__uint_as_float(u.z), __uint_as_float(u.w));
+    } else {
+        f[0] = unpack2<T>(u.x);
+        f[1] = unpack2<T>(u.y);
+        f[2] = unpack2<T>(u.z);
+        f[3] = unpack2<T>(u.w);
+    }
+}
+template <typename T, int P>
+__device__ __forceinline__ uint4 pack_vec(const f2 (&f)[P]) {
+    if constexpr (sizeof(T) == 4) {
+        const float2 a = f2_get(f[0]), b = f2_get(f[1]);
+        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    } else {
+        return make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3]));
+    }
+}
+// 2 P consecutive elements of a weight vector as pairs.
+template <typename W, int P>
+__device__ __forceinline__ void load_pairs(const W* p, f2 (&f)[P]) {
+    float v[2 * P];
+    load_vec<W, 2 * P>(p, v);
+#pragma unroll
+    for (int i = 0; i < P; ++i) f[i] = f2_make(v[2 * i], v[2 * i + 1]);
+}
+
+// Mean and rstd of a row from its threads' sums and their squared distances
+// from their own means (n values each): the sums give the mean m, and
+// sum (x - m)^2 = sum_t M2_t + sum_t n_t (mean_t - m)^2.  No difference of
+// large squares: exact however far the row lies from zero.
+struct LnStat {
+    float mean, rstd;
+};
+
+// gt working threads per group; groups of several warps have a reducing warp
+// after them (kReducer).
+template <typename T, typename W, int NV, bool kBias, bool kReducer>
+__global__ void __launch_bounds__(kLnRingThreads, 1)
+    ln_fwd_ring(long long rows, int H, int gt, const T* __restrict__ x, long long xs, const W* __restrict__ w,
+                const W* __restrict__ b, float eps, T* __restrict__ y, float* __restrict__ mean,
+                float* __restrict__ rstd) {
+    constexpr int V = 16 / sizeof(T), P = V / 2, kRing = kLnFwdRing, kLag = kReducer ? 2 : 0;
+    extern __shared__ uint4 ring[];  // [kRing][NV][blockDim.x]
+    __shared__ float2 psum[kReducer ? 2 : 1][kReducer ? kLnRingThreads : 1];  // sum, M2 of a thread
+    __shared__ LnStat stat[kReducer ? kLnMaxGroups : 1][2];
+    const int gn = kReducer ? gt + 32 : gt;
+    const int g = threadIdx.x / gn, t = threadIdx.x - g * gn, ng = blockDim.x / gn;
+    const int nvec = H / V;
+    const long long step = (long long)gridDim.x * ng;
+    const long long first = (long long)blockIdx.x * ng + g;
+    const float inv_h = 1.0f / (float)H;
+    const long long n = first < rows ? (rows - first + step - 1) / step : 0;  // rows of this group
+    if (kReducer && t >= gt) {
+        // values per partial of this lane
+        const int lane = t - gt, nw = gt >> 5;
+        float cnt[kLnGroupWarps];
+#pragma unroll
+        for (int k = 0; k < kLnGroupWarps; ++k) {
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) c += k < nw && lane + 32 * k + i * gt < nvec ? V : 0;
+            cnt[k] = (float)c;
+        }
+        for (long long i = 0; i < n + kLag; ++i) {
+            if (i >= 1 && i <= n) {
+                const float2* ps = psum[(i - 1) & 1] + g * gn;
+                float2 v[kLnGroupWarps];
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kLnGroupWarps; ++k)
+                    if (k < nw) {
+                        v[k] = ps[lane + 32 * k];
+                        sum += v[k].x;
+                    }
+                const float m = warp_sum(sum) * inv_h;
+                float q = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kLnGroupWarps; ++k)
+                    if (k < nw && cnt[k] > 0.0f) {
+                        const float d = __fdividef(v[k].x, cnt[k]) - m;
+                        q += fmaf(cnt[k] * d, d, v[k].y);
+                    }
+                const float r = rsqrtf(fmaf(warp_sum(q), inv_h, eps));
+                if (lane == 0) {
+                    stat[g][(i - 1) & 1] = {m, r};
+                    mean[first + (i - 1) * step] = m;
+                    rstd[first + (i - 1) * step] = r;
+                }
+            }
+            group_sync(g, gn);
+        }
+        return;
+    }
+    const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16u;
+    const uint32_t vstride = blockDim.x * 16u;
+    bool have[NV];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        have[i] = t + i * gt < nvec;
+        mine += have[i] ? V : 0;
+    }
+    const float inv_mine = mine ? 1.0f / (float)mine : 0.0f;
+    // the next row to copy: its number and this thread's first element of it
+    long long frow = 0;
+    const T* fx = x + first * xs + (size_t)t * V;
+    auto fetch = [&](int s) {
+        if (frow < n) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (have[i]) cp_async_16(slot0 + (uint32_t)(s * NV + i) * vstride, fx + (size_t)(i * gt) * V, 16u);
+        }
+        cp_async_commit();
+        ++frow;
+        fx += step * xs;
+    };
+    // rows in flight: the ring less the rows between arrival and output
+    constexpr int kAhead = kRing - 1 - kLag;
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) fetch(s);
+    f2 wv[NV][P], bv[kBias ? NV : 1][P];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (have[i]) {
+            load_pairs<W, P>(w + (size_t)(t + i * gt) * V, wv[i]);
+            if constexpr (kBias) load_pairs<W, P>(b + (size_t)(t + i * gt) * V, bv[i]);
+        }
+    T* yr = y + first * H + (size_t)t * V;
+    // (x - m) r w + b of the row in slot s
+    auto output = [&](int s, float m, float r) {
+        const f2 nm = f2_make(-m, -m), r2 = f2_make(r, r);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (have[i]) {
+                f2 v[P];
+                unpack_vec<T, P>(ring[(s * NV + i) * blockDim.x + threadIdx.x], v);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    v[j] = f2_mul(f2_add(v[j], nm), r2);
+                    if constexpr (kBias)
+                        v[j] = f2_fma(v[j], wv[i][j], bv[i][j]);
+                    else
+                        v[j] = f2_mul(v[j], wv[i][j]);
+                }
+                *reinterpret_cast<uint4*>(yr + (size_t)(i * gt) * V) = pack_vec<T, P>(v);
+            }
+        yr += step * H;
+    };
+    int s = 0;  // slot of row i
+    for (long long i = 0; i < n + kLag; ++i) {
+        cp_async_wait_group<kAhead - 1>();
+        float sum = 0.0f, m2 = 0.0f;
+        if (i < n) {
+            f2 v[NV][P];
+            f2 acc[2] = {0ull, 0ull};  // (+0, +0)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (have[k]) {
+                    unpack_vec<T, P>(ring[(s * NV + k) * blockDim.x + threadIdx.x], v[k]);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) acc[j & 1] = f2_add(acc[j & 1], v[k][j]);
+                }
+            sum = f2_sum(f2_add(acc[0], acc[1]));
+            // around the thread's own mean, or (one warp) the row's
+            const float c = kReducer ? sum * inv_mine : warp_sum(sum) * inv_h;
+            const f2 nc = f2_make(-c, -c);
+            acc[0] = acc[1] = 0ull;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (have[k]) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        const f2 d = f2_add(v[k][j], nc);
+                        acc[j & 1] = f2_fma(d, d, acc[j & 1]);
+                    }
+                }
+            m2 = f2_sum(f2_add(acc[0], acc[1]));
+            if constexpr (kReducer) {
+                psum[i & 1][threadIdx.x] = make_float2(sum, m2);
+            } else {
+                const float r = rsqrtf(fmaf(warp_sum(m2), inv_h, eps));
+                if (t == 0) {
+                    mean[first + i * step] = c;
+                    rstd[first + i * step] = r;
+                }
+                output(s, c, r);
+            }
+        }
+        if constexpr (kReducer) {
+            if (i >= 2) {
+                const LnStat st = stat[g][i & 1];  // of row i - 2
+                output((s + kRing - 2) % kRing, st.mean, st.rstd);
+            }
+        }
+        fetch((s + kAhead) % kRing);
+        if constexpr (kReducer) group_sync(g, gn);
+        s = (s + 1) % kRing;
     }
 }
 
@@ -216,54 +485,229 @@ struct LnBwd {
     float* part;  // [blocks][2][H]: sums of dy z, sums of dy
 };
 
-// One row's dx in registers plus the block's column sums.  One warp per row:
-// the block's warps join their column sums through shared memory at the end.
-template <typename T, typename W, int V, int NV, bool kWarpRow>
-__global__ void __launch_bounds__(512) ln_bwd(const LnBwd p) {
-    __shared__ float red[2][32];
-    extern __shared__ float colsum[];  // one-warp-per-row form: [2][H]
-    const int t = kWarpRow ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-    const int nt = kWarpRow ? 32 : (int)blockDim.x;
+// Ring form.  The groups of a block leave their column sums in shared memory
+// (the ring's, free by then) and the block adds them in the groups' order.
+// kMode: LN_ONE_WARP groups of one warp, LN_REDUCER with a reducing warp, or
+// LN_ALL_WARPS, for rows of which shared memory does not hold the two more that
+// the reducing warp's lag takes (NV = 4): every warp reduces.
+enum { LN_ONE_WARP, LN_REDUCER, LN_ALL_WARPS };
+template <typename T, typename W, int NV, int kMode>
+__global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, int gt) {
+    constexpr bool kReducer = kMode == LN_REDUCER;
+    constexpr int V = 16 / sizeof(T), P = V / 2, kRing = ln_bwd_ring_rows(NV), kLag = kReducer ? 2 : 0;
+    constexpr bool kHoldW = NV * V <= 16;  // else the weight is read again from L1: its registers go to the sums
+    extern __shared__ uint4 ring[];  // [kRing][2][NV][blockDim.x]: x, dy
+    __shared__ float2 psum[kReducer ? 2 : 1][kReducer ? kLnRingThreads : 1];  // sums of g, g z of a thread
+    __shared__ float2 tot[kReducer ? kLnMaxGroups : 1][2];                     // their means over the row
+    __shared__ float2 red[kMode == LN_ALL_WARPS ? kLnMaxGroups : 1][2][kLnGroupWarps];
+    const int gn = kReducer ? gt + 32 : gt;
+    const int g = threadIdx.x / gn, t = threadIdx.x - g * gn, ng = blockDim.x / gn;
     const int H = p.H, nvec = H / V;
-    const T *dy = static_cast<const T*>(p.dy), *x = static_cast<const T*>(p.x);
-    const W* w = static_cast<const W*>(p.w);
-    T* dx = static_cast<T*>(p.dx);
-    float sw[NV][V], sb[NV][V];
+    const long long step = (long long)gridDim.x * ng;
+    const long long first = (long long)blockIdx.x * ng + g;
+    const long long n = first < p.rows ? (p.rows - first + step - 1) / step : 0;  // rows of this group
+    const float inv_h = 1.0f / (float)H;
+    const bool worker = !kReducer || t < gt;
+    bool have[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) have[i] = worker && t + i * gt < nvec;
+    f2 sw[NV][P], sb[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) sw[i][j] = sb[i][j] = 0.0f;
+        for (int j = 0; j < P; ++j) sw[i][j] = sb[i][j] = 0ull;  // (+0, +0)
+    if (!worker) {
+        const int lane = t - gt, nw = gt >> 5;
+        for (long long i = 0; i < n + kLag; ++i) {
+            if (i >= 1 && i <= n) {
+                const float2* ps = psum[(i - 1) & 1] + g * gn;
+                float a = 0.0f, c = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kLnGroupWarps; ++k)
+                    if (k < nw) {
+                        const float2 v = ps[lane + 32 * k];
+                        a += v.x;
+                        c += v.y;
+                    }
+                a = warp_sum(a);
+                c = warp_sum(c);
+                if (lane == 0) tot[g][(i - 1) & 1] = make_float2(-a * inv_h, -c * inv_h);
+            }
+            group_sync(g, gn);
+        }
+    } else {
+        const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16u;
+        const uint32_t vstride = blockDim.x * 16u;
+        const W* w = static_cast<const W*>(p.w) + (size_t)t * V;
+        long long frow = 0;
+        const T* fx = static_cast<const T*>(p.x) + first * p.xs + (size_t)t * V;
+        const T* fd = static_cast<const T*>(p.dy) + first * p.dys + (size_t)t * V;
+        auto fetch = [&](int s) {
+            if (frow < n) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (have[i]) {
+                        cp_async_16(slot0 + (uint32_t)(s * 2 * NV + i) * vstride, fx + (size_t)(i * gt) * V, 16u);
+                        cp_async_16(slot0 + (uint32_t)(s * 2 * NV + NV + i) * vstride, fd + (size_t)(i * gt) * V,
+                                    16u);
+                    }
+            }
+            cp_async_commit();
+            ++frow;
+            fx += step * p.xs;
+            fd += step * p.dys;
+        };
+        constexpr int kAhead = kRing - 1 - kLag;
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) fetch(s);
+        f2 wv[kHoldW ? NV : 1][P];
+        if constexpr (kHoldW) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (have[i]) load_pairs<W, P>(w + (size_t)(i * gt) * V, wv[i]);
+        }
+        T* out = static_cast<T*>(p.dx) + first * H + (size_t)t * V;
+        // z and dy of vector i of the row in slot s (and the weight, where it is not held)
+        auto vectors = [&](int s, int i, f2 nm, f2 r2, f2 (&z)[P], f2 (&d)[P]) {
+            unpack_vec<T, P>(ring[(s * 2 * NV + i) * blockDim.x + threadIdx.x], z);
+            unpack_vec<T, P>(ring[(s * 2 * NV + NV + i) * blockDim.x + threadIdx.x], d);
+            if constexpr (!kHoldW) load_pairs<W, P>(w + (size_t)(i * gt) * V, wv[0]);
+#pragma unroll
+            for (int j = 0; j < P; ++j) z[j] = f2_mul(f2_add(z[j], nm), r2);
+        };
+        // dx of the row in slot s; c1, c2: minus the means of g and of g z
+        auto output = [&](int s, float m, float r, float c1, float c2) {
+            const f2 nm = f2_make(-m, -m), r2 = f2_make(r, r), d1 = f2_make(c1, c1), d2 = f2_make(c2, c2);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (have[i]) {
+                    f2 z[P], d[P];
+                    vectors(s, i, nm, r2, z, d);
+#pragma unroll
+                    for (int j = 0; j < P; ++j)
+                        d[j] = f2_mul(f2_fma(z[j], d2, f2_fma(d[j], wv[kHoldW ? i : 0][j], d1)), r2);
+                    *reinterpret_cast<uint4*>(out + (size_t)(i * gt) * V) = pack_vec<T, P>(d);
+                }
+            out += step * H;
+        };
+        // mean and rstd of rows i - 2 .. i + 1 (read a step ahead)
+        float m0 = 0.0f, r0 = 0.0f, m1 = 0.0f, r1 = 0.0f, m = 0.0f, r = 0.0f, ma = 0.0f, ra = 0.0f;
+        if (n > 0) m = __ldg(p.mean + first), r = __ldg(p.rstd + first);
+        int s = 0;  // slot of row i
+        for (long long i = 0; i < n + kLag; ++i) {
+            if (i + 1 < n) ma = __ldg(p.mean + first + (i + 1) * step), ra = __ldg(p.rstd + first + (i + 1) * step);
+            cp_async_wait_group<kAhead - 1>();
+            if (i < n) {
+                const f2 nm = f2_make(-m, -m), r2 = f2_make(r, r);
+                f2 a1 = 0ull, a2 = 0ull;
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (have[k]) {
+                        f2 z[P], d[P];
+                        vectors(s, k, nm, r2, z, d);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) {
+                            sb[k][j] = f2_add(sb[k][j], d[j]);
+                            sw[k][j] = f2_fma(d[j], z[j], sw[k][j]);
+                            d[j] = f2_mul(d[j], wv[kHoldW ? k : 0][j]);
+                            a1 = f2_add(a1, d[j]);
+                            a2 = f2_fma(d[j], z[j], a2);
+                        }
+                    }
+                if constexpr (kReducer) {
+                    psum[i & 1][threadIdx.x] = make_float2(f2_sum(a1), f2_sum(a2));
+                } else {
+                    float c1 = warp_sum(f2_sum(a1)), c2 = warp_sum(f2_sum(a2));
+                    if constexpr (kMode == LN_ALL_WARPS) {
+                        // two buffers in turn: row i + 2 reuses this one, after row i + 1's barrier
+                        const int lane = t & 31;
+                        if (lane == 0) red[g][i & 1][t >> 5] = make_float2(c1, c2);
+                        group_sync(g, gt);
+                        const float2 v = lane < (gt >> 5) ? red[g][i & 1][lane] : make_float2(0.0f, 0.0f);
+                        c1 = warp_sum(v.x);
+                        c2 = warp_sum(v.y);
+                    }
+                    output(s, m, r, -c1 * inv_h, -c2 * inv_h);
+                }
+            }
+            if constexpr (kReducer) {
+                if (i >= 2) {
+                    const float2 c = tot[g][i & 1];  // of row i - 2
+                    output((s + kRing - 2) % kRing, m0, r0, c.x, c.y);
+                }
+            }
+            fetch((s + kAhead) % kRing);
+            m0 = m1, r0 = r1, m1 = m, r1 = r, m = ma, r = ra;
+            if constexpr (kReducer) group_sync(g, gn);
+            s = (s + 1) % kRing;
+        }
+    }
+    float* part = p.part + (size_t)blockIdx.x * 2 * H;
+    float* col = reinterpret_cast<float*>(ring) + (size_t)g * 2 * H;  // [groups][2][H]
+    static_assert(kRing * 2 * 16 >= 2 * V * 4, "the ring holds the groups' column sums");
+    float* to = ng > 1 ? col : part;
+    cp_async_wait_all();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (have[i]) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const int h = (t + i * gt) * V + 2 * j;
+                *reinterpret_cast<float2*>(to + h) = f2_get(sw[i][j]);
+                *reinterpret_cast<float2*>(to + H + h) = f2_get(sb[i][j]);
+            }
+        }
+    if (ng > 1) {
+        __syncthreads();
+        for (int h = threadIdx.x; h < 2 * H; h += blockDim.x) {
+            float a = reinterpret_cast<const float*>(ring)[h];
+            for (int gi = 1; gi < ng; ++gi) a += reinterpret_cast<const float*>(ring)[(size_t)gi * 2 * H + h];
+            part[h] = a;
+        }
+    }
+}
+
+// Register form.  One warp per row: the block's warps join their column sums
+// through shared memory at the end.
+template <typename T, typename W, int NV, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarps : 512) ln_bwd(const LnBwd p) {
+    __shared__ float red[2][32];
+    __shared__ float colsum[kWarpRow ? 2 * 32 * NV : 1];  // one warp per row: [2][H]
+    const int t = kWarpRow ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
+    const int nt = kWarpRow ? 32 : (int)blockDim.x;
+    const int H = p.H;
+    const T *dy = static_cast<const T*>(p.dy), *x = static_cast<const T*>(p.x);
+    const W* w = static_cast<const W*>(p.w);
+    T* dx = static_cast<T*>(p.dx);
+    float sw[NV], sb[NV], wv[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        sw[i] = sb[i] = 0.0f;
+        wv[i] = t + i * nt < H ? to_f(__ldg(w + t + i * nt)) : 0.0f;
+    }
     const long long step = kWarpRow ? (long long)gridDim.x * kLnWarps : (long long)gridDim.x;
     const long long first = kWarpRow ? (long long)blockIdx.x * kLnWarps + (threadIdx.x >> 5) : (long long)blockIdx.x;
     for (long long row = first; row < p.rows; row += step) {
         const float m = __ldg(p.mean + row), r = __ldg(p.rstd + row);
-        float z[NV][V], g[NV][V];
+        float z[NV], g[NV];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = t + i * nt;
-            if (c < nvec) {
-                load_vec<T, V>(x + row * p.xs + (size_t)c * V, z[i]);
-                load_vec<T, V>(dy + row * p.dys + (size_t)c * V, g[i]);
-            }
+            z[i] = c < H ? to_f(__ldg(x + row * p.xs + c)) : 0.0f;
+            g[i] = c < H ? to_f(__ldg(dy + row * p.dys + c)) : 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = t + i * nt;
-            if (c < nvec) {
-                float wv[V];
-                load_vec<W, V>(w + (size_t)c * V, wv);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    z[i][j] = (z[i][j] - m) * r;
-                    sb[i][j] += g[i][j];
-                    sw[i][j] = fmaf(g[i][j], z[i][j], sw[i][j]);
-                    g[i][j] *= wv[j];
-                    s1 += g[i][j];
-                    s2 = fmaf(g[i][j], z[i][j], s2);
-                }
+        for (int i = 0; i < NV; ++i)
+            if (t + i * nt < H) {
+                z[i] = (z[i] - m) * r;
+                sb[i] += g[i];
+                sw[i] = fmaf(g[i], z[i], sw[i]);
+                g[i] *= wv[i];
+                s1 += g[i];
+                s2 = fmaf(g[i], z[i], s2);
             }
-        }
         s1 = warp_sum(s1);
         s2 = warp_sum(s2);
         if constexpr (!kWarpRow) {
@@ -280,15 +724,8 @@ __global__ void __launch_bounds__(512) ln_bwd(const LnBwd p) {
         }
         const float c1 = s1 / (float)H, c2 = s2 / (float)H;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = t + i * nt;
-            if (c < nvec) {
-                float o[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = r * (g[i][j] - c1 - z[i][j] * c2);
-                store_vec<T, V>(dx + row * (long long)H + (size_t)c * V, o);
-            }
-        }
+        for (int i = 0; i < NV; ++i)
+            if (t + i * nt < H) dx[row * (long long)H + t + i * nt] = from_f<T>(r * (g[i] - c1 - z[i] * c2));
     }
     float* out = p.part + (size_t)blockIdx.x * 2 * H;
     if constexpr (kWarpRow) {
@@ -297,14 +734,10 @@ __global__ void __launch_bounds__(512) ln_bwd(const LnBwd p) {
             if ((int)(threadIdx.x >> 5) == wi) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = t + i * nt;
-                    if (c < nvec) {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            const int h = c * V + j;
-                            colsum[h] = wi ? colsum[h] + sw[i][j] : sw[i][j];
-                            colsum[H + h] = wi ? colsum[H + h] + sb[i][j] : sb[i][j];
-                        }
+                    const int h = t + i * 32;
+                    if (h < H) {
+                        colsum[h] = wi ? colsum[h] + sw[i] : sw[i];
+                        colsum[H + h] = wi ? colsum[H + h] + sb[i] : sb[i];
                     }
                 }
             }
@@ -313,16 +746,11 @@ __global__ void __launch_bounds__(512) ln_bwd(const LnBwd p) {
         for (int h = threadIdx.x; h < 2 * H; h += blockDim.x) out[h] = colsum[h];
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = t + i * nt;
-            if (c < nvec) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    out[c * V + j] = sw[i][j];
-                    out[H + c * V + j] = sb[i][j];
-                }
+        for (int i = 0; i < NV; ++i)
+            if (t + i * nt < H) {
+                out[t + i * nt] = sw[i];
+                out[H + t + i * nt] = sb[i];
             }
-        }
     }
 }
 
@@ -401,64 +829,82 @@ __global__ void __launch_bounds__(256) ln_bwd_join(const float* __restrict__ par
     }
 }
 
-// Launch shape of a row form: vector width, vectors per thread, threads.
+// Launch shape of a call: form, vectors (or elements) per thread, threads of
+// a group (ring), of a row's block or of a block of warps (register).
+enum { LN_RING, LN_WARP, LN_BLOCK, LN_LONG };
 struct LnForm {
-    bool vec, warp_row, longrow;
-    int nv, threads;
+    int form, nv, threads;
 };
-LnForm ln_form(int H, int elt, bool vec, int max_threads) {
+LnForm ln_form(int H, int elt, bool vec, int max_threads, int wide_nv, int max_ring) {
     LnForm f = {};
-    const int V = vec ? 16 / elt : 1;
-    const int nvec = H / V;
-    f.vec = vec;
-    if (nvec <= kLnWarpVecs) {
-        f.warp_row = true;
-        f.nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
+    if (vec) {
+        const int nvec = H / (16 / elt);
+        f.form = LN_RING;
+        f.nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : nvec <= 2 * (kLnRingThreads - 32) ? wide_nv : 4;
+        f.threads = ((nvec + f.nv - 1) / f.nv + 31) / 32 * 32;
+        if (f.threads > max_ring) f.form = LN_LONG;
+        return f;
+    }
+    if (H <= 128) {
+        f.form = LN_WARP;
+        f.nv = H <= 32 ? 1 : H <= 64 ? 2 : 4;
         f.threads = 32 * kLnWarps;
         return f;
     }
-    for (f.nv = 4; f.nv <= 16 && f.nv * V <= 32; f.nv *= 2) {
-        f.threads = ((nvec + f.nv - 1) / f.nv + 31) / 32 * 32;
+    f.form = LN_BLOCK;
+    for (f.nv = 4; f.nv <= 16; f.nv *= 2) {
+        f.threads = ((H + f.nv - 1) / f.nv + 31) / 32 * 32;
         if (f.threads <= max_threads) return f;
     }
-    f.longrow = true;
+    f.form = LN_LONG;
     return f;
 }
 
 bool mult16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T, typename W, int V, int NV>
-void run_fwd(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
-    const T* x = static_cast<const T*>(a.x);
-    const W *w = static_cast<const W*>(a.weight), *b = static_cast<const W*>(a.bias);
-    T* y = static_cast<T*>(a.y);
-    if constexpr (NV <= 4) {
-        if (f.warp_row) {
-            ln_fwd<T, W, V, NV, true><<<(unsigned)((a.rows + kLnWarps - 1) / kLnWarps), f.threads, 0, st>>>(
-                a.rows, a.H, x, a.x_stride, w, b, a.eps, y, a.mean, a.rstd);
-            return;
-        }
-    }
-    if constexpr (NV >= 4)
-        ln_fwd<T, W, V, NV, false><<<(unsigned)a.rows, f.threads, 0, st>>>(a.rows, a.H, x, a.x_stride, w, b, a.eps, y,
-                                                                            a.mean, a.rstd);
+// Groups of a block and its threads; named barriers 1..15 tell groups of
+// several warps apart.
+int ln_groups(int gt, bool reducer, int* threads) {
+    const int gn = reducer ? gt + 32 : gt;
+    int ng = kLnRingThreads / gn;
+    if (gt > 32 && ng > 15) ng = 15;
+    *threads = ng * gn;
+    return ng;
+}
+template <typename T, typename W, int NV, bool kBias, bool kReducer>
+int run_fwd_ring(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
+    static SmemLimit limit;
+    int threads;
+    const int ng = ln_groups(f.threads, kReducer, &threads);
+    constexpr int per_thread = kLnFwdRing * NV * 16;
+    static_assert(per_thread * kLnRingThreads <= 200 * 1024, "shared memory per block");
+    if (const int e = limit.allow(ln_fwd_ring<T, W, NV, kBias, kReducer>, per_thread * kLnRingThreads)) return e;
+    const long long need = (a.rows + ng - 1) / ng;
+    ln_fwd_ring<T, W, NV, kBias, kReducer><<<(unsigned)(need < 152 ? need : 152), threads, per_thread * threads, st>>>(
+        a.rows, a.H, f.threads, static_cast<const T*>(a.x), a.x_stride, static_cast<const W*>(a.weight),
+        static_cast<const W*>(a.bias), a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
+    return (int)cudaGetLastError();
+}
+template <typename T, typename W, bool kBias>
+int fwd_ring(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
+    if (f.nv == 1) return run_fwd_ring<T, W, 1, kBias, false>(f, a, st);
+    if (f.nv == 2) return run_fwd_ring<T, W, 2, kBias, false>(f, a, st);
+    return f.threads > 32 ? run_fwd_ring<T, W, 4, kBias, true>(f, a, st)
+                          : run_fwd_ring<T, W, 4, kBias, false>(f, a, st);
+}
+template <typename T, typename W, int NV, bool kWarpRow>
+int run_fwd(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
+    const long long blocks = kWarpRow ? (a.rows + kLnWarps - 1) / kLnWarps : a.rows;
+    ln_fwd<T, W, NV, kWarpRow><<<(unsigned)blocks, f.threads, 0, st>>>(
+        a.rows, a.H, static_cast<const T*>(a.x), a.x_stride, static_cast<const W*>(a.weight),
+        static_cast<const W*>(a.bias), a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
+    return (int)cudaGetLastError();
 }
 template <typename T, typename W, int V>
-int fwd_v(const LnFwdArgs& a, cudaStream_t st) {
-    const LnForm f = ln_form(a.H, sizeof(T), V > 1, 1024);
-    if (f.longrow) {
-        ln_fwd_long<T, W, V><<<(unsigned)a.rows, kLnLongThreads, 0, st>>>(
-            a.rows, a.H, static_cast<const T*>(a.x), a.x_stride, static_cast<const W*>(a.weight),
-            static_cast<const W*>(a.bias), a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
-    } else {
-        switch (f.nv) {
-            case 1: run_fwd<T, W, V, 1>(f, a, st); break;
-            case 2: run_fwd<T, W, V, 2>(f, a, st); break;
-            case 4: run_fwd<T, W, V, 4>(f, a, st); break;
-            case 8: if constexpr (8 * V <= 32) run_fwd<T, W, V, 8>(f, a, st); break;
-            default: if constexpr (16 * V <= 32) run_fwd<T, W, V, 16>(f, a, st); break;
-        }
-    }
+int run_fwd_long(const LnFwdArgs& a, cudaStream_t st) {
+    ln_fwd_long<T, W, V><<<(unsigned)a.rows, kLnLongThreads, 0, st>>>(
+        a.rows, a.H, static_cast<const T*>(a.x), a.x_stride, static_cast<const W*>(a.weight),
+        static_cast<const W*>(a.bias), a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
     return (int)cudaGetLastError();
 }
 template <typename T, typename W>
@@ -466,41 +912,49 @@ int fwd_t(const LnFwdArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     const bool vec = a.H % V == 0 && a.x_stride % V == 0 && mult16(a.x) && mult16(a.y) && mult16(a.weight) &&
                      mult16(a.bias);
-    return vec ? fwd_v<T, W, V>(a, st) : fwd_v<T, W, 1>(a, st);
+    const LnForm f = ln_form(a.H, sizeof(T), vec, 1024, 4, kLnRingThreads - 32);
+    const bool b = a.bias != nullptr;
+    switch (f.form) {
+        case LN_RING:
+            return b ? fwd_ring<T, W, true>(f, a, st) : fwd_ring<T, W, false>(f, a, st);
+        case LN_WARP:
+            return f.nv == 1   ? run_fwd<T, W, 1, true>(f, a, st)
+                   : f.nv == 2 ? run_fwd<T, W, 2, true>(f, a, st)
+                               : run_fwd<T, W, 4, true>(f, a, st);
+        case LN_BLOCK:
+            return f.nv == 4   ? run_fwd<T, W, 4, false>(f, a, st)
+                   : f.nv == 8 ? run_fwd<T, W, 8, false>(f, a, st)
+                               : run_fwd<T, W, 16, false>(f, a, st);
+        default: return vec ? run_fwd_long<T, W, V>(a, st) : run_fwd_long<T, W, 1>(a, st);
+    }
 }
 
-template <typename T, typename W, int V, int NV>
-void run_bwd(const LnForm& f, const LnBwd& p, int blocks, cudaStream_t st) {
-    if constexpr (NV <= 4) {
-        if (f.warp_row) {
-            ln_bwd<T, W, V, NV, true><<<blocks, f.threads, sizeof(float) * 2 * p.H, st>>>(p);
-            return;
-        }
-    }
-    if constexpr (NV >= 4) ln_bwd<T, W, V, NV, false><<<blocks, f.threads, 0, st>>>(p);
+template <typename T, typename W, int NV, int kMode>
+int run_bwd_ring(const LnForm& f, const LnBwd& p, int* blocks, cudaStream_t st) {
+    static SmemLimit limit;
+    int threads;
+    const int ng = ln_groups(f.threads, kMode == LN_REDUCER, &threads);
+    constexpr int per_thread = ln_bwd_ring_rows(NV) * 2 * NV * 16;
+    static_assert(per_thread * kLnRingThreads <= 200 * 1024, "shared memory per block");
+    if (const int e = limit.allow(ln_bwd_ring<T, W, NV, kMode>, per_thread * kLnRingThreads)) return e;
+    const long long need = (p.rows + ng - 1) / ng;
+    *blocks = (int)(need < 152 ? need : 152);
+    ln_bwd_ring<T, W, NV, kMode><<<*blocks, threads, per_thread * threads, st>>>(p, f.threads);
+    return (int)cudaGetLastError();
+}
+template <typename T, typename W, int NV, bool kWarpRow>
+int run_bwd(const LnForm& f, const LnBwd& p, int* blocks, cudaStream_t st) {
+    const long long need = kWarpRow ? (p.rows + kLnWarps - 1) / kLnWarps : p.rows;
+    *blocks = (int)(need < kLnBwdBlocks ? need : kLnBwdBlocks);
+    ln_bwd<T, W, NV, kWarpRow><<<*blocks, f.threads, 0, st>>>(p);
+    return (int)cudaGetLastError();
 }
 template <typename T, typename W, int V>
-int bwd_v(const LnBwdArgs& a, cudaStream_t st) {
-    LnBwd p = {a.rows, a.H, a.dy, a.x, a.weight, a.dy_stride, a.x_stride, a.mean, a.rstd, a.dx, a.part};
-    const LnForm f = ln_form(a.H, sizeof(T), V > 1, 512);
-    int blocks;
-    if (f.longrow) {
-        blocks = (int)(a.rows < kLnBwdBlocks ? a.rows : kLnBwdBlocks);  // bands of rows
-        ln_bwd_long<T, W, V><<<(unsigned)a.rows, kLnLongThreads, 0, st>>>(p);
-        ln_bwd_long_cols<T><<<dim3((a.H + 255) / 256, blocks), 256, 0, st>>>(p, blocks);
-    } else {
-        const long long units = f.warp_row ? (a.rows + kLnWarps - 1) / kLnWarps : a.rows;
-        blocks = (int)(units < kLnBwdBlocks ? units : kLnBwdBlocks);
-        switch (f.nv) {
-            case 1: run_bwd<T, W, V, 1>(f, p, blocks, st); break;
-            case 2: run_bwd<T, W, V, 2>(f, p, blocks, st); break;
-            case 4: run_bwd<T, W, V, 4>(f, p, blocks, st); break;
-            case 8: if constexpr (8 * V <= 32) run_bwd<T, W, V, 8>(f, p, blocks, st); break;
-            default: if constexpr (16 * V <= 32) run_bwd<T, W, V, 16>(f, p, blocks, st); break;
-        }
-    }
-    ln_bwd_join<W><<<(2 * a.H + 31) / 32, 256, 0, st>>>(a.part, blocks, a.H, static_cast<W*>(a.dweight),
-                                                         static_cast<W*>(a.dbias));
+int run_bwd_long(const LnBwd& p, int* blocks, cudaStream_t st) {
+    *blocks = (int)(p.rows < kLnBwdBlocks ? p.rows : kLnBwdBlocks);  // bands of rows
+    ln_bwd_long<T, W, V><<<(unsigned)p.rows, kLnLongThreads, 0, st>>>(p);
+    if (const cudaError_t e = cudaGetLastError()) return (int)e;
+    ln_bwd_long_cols<T><<<dim3((p.H + 255) / 256, *blocks), 256, 0, st>>>(p, *blocks);
     return (int)cudaGetLastError();
 }
 template <typename T, typename W>
@@ -508,7 +962,32 @@ int bwd_t(const LnBwdArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     const bool vec = a.H % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 && mult16(a.x) && mult16(a.dy) &&
                      mult16(a.dx) && mult16(a.weight);
-    return vec ? bwd_v<T, W, V>(a, st) : bwd_v<T, W, 1>(a, st);
+    const LnBwd p = {a.rows, a.H, a.dy, a.x, a.weight, a.dy_stride, a.x_stride, a.mean, a.rstd, a.dx, a.part};
+    const LnForm f = ln_form(a.H, sizeof(T), vec, 512, 2, kLnRingThreads);
+    int e, blocks = 0;
+    switch (f.form) {
+        case LN_RING:
+            e = f.nv == 1        ? run_bwd_ring<T, W, 1, LN_ONE_WARP>(f, p, &blocks, st)
+                : f.nv > 2       ? run_bwd_ring<T, W, 4, LN_ALL_WARPS>(f, p, &blocks, st)
+                : f.threads > 32 ? run_bwd_ring<T, W, 2, LN_REDUCER>(f, p, &blocks, st)
+                                 : run_bwd_ring<T, W, 2, LN_ONE_WARP>(f, p, &blocks, st);
+            break;
+        case LN_WARP:
+            e = f.nv == 1   ? run_bwd<T, W, 1, true>(f, p, &blocks, st)
+                : f.nv == 2 ? run_bwd<T, W, 2, true>(f, p, &blocks, st)
+                            : run_bwd<T, W, 4, true>(f, p, &blocks, st);
+            break;
+        case LN_BLOCK:
+            e = f.nv == 4   ? run_bwd<T, W, 4, false>(f, p, &blocks, st)
+                : f.nv == 8 ? run_bwd<T, W, 8, false>(f, p, &blocks, st)
+                            : run_bwd<T, W, 16, false>(f, p, &blocks, st);
+            break;
+        default: e = vec ? run_bwd_long<T, W, V>(p, &blocks, st) : run_bwd_long<T, W, 1>(p, &blocks, st);
+    }
+    if (e) return e;
+    ln_bwd_join<W><<<(2 * a.H + 31) / 32, 256, 0, st>>>(a.part, blocks, a.H, static_cast<W*>(a.dweight),
+                                                         static_cast<W*>(a.dbias));
+    return (int)cudaGetLastError();
 }
 
 }  // namespace
