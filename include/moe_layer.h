@@ -359,6 +359,53 @@ int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_t
                             const float* mean, const float* rstd, void* dx, void* dweight, void* dbias, void* ws,
                             void* stream);
 
+/* 4-bit weights with one scale per group, for serving a few rows at a time
+ * (decoding).  A matrix W [N, K] (y = x W^T) is held as
+ *     W[n, k] = (code[n, k] - 8) * sf[n, k / group],   code in [0, 15],
+ * sf bf16 [N, K / group], group 32, 64 or 128, K a multiple of 128 up to
+ * 65536, any N.  Codes u8 [N, K / 2]: 64 bytes per 128 codes, 16 little-endian
+ * words; word 4 t + j (t, j in 0..3) holds the codes 32 j + 8 t .. + 7 of the
+ * 128: code 2 m (m in 0..3) of the eight in nibble m, code 2 m + 1 in nibble
+ * m + 4.  Sums are FP32, the output is rounded once.  An infinity or NaN in a
+ * row of x gives NaN in that row's outputs only.  All pointers are 16-byte
+ * aligned. */
+
+/* W bf16 [E, K, N] (the layout of moe_forward's W1 with K = H, N = 2 I, and of
+ * W2 with K = I, N = H) -> W_q u8 [E, N, K / 2] and W_sf bf16 [E, N,
+ * K / group]: sf = max|w| of the group / 7 rounded to bf16, code = round(w /
+ * sf) + 8 clamped to [0, 15] (sf = 0 and code 8 for a group of zeros).
+ * Finite weights only.  Kernels on `stream`. */
+int moe_quantize_w4(int32_t E, int32_t K, int32_t N, int32_t group, const void* W, uint8_t* W_q, void* W_sf,
+                    void* stream);
+
+/* y bf16 [M, N] = x bf16 [M, K] times W^T, M in [0, 65535] (each 8 or 16 rows
+ * read the weights once: meant for M up to a few tens). */
+int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, const void* x, const uint8_t* W_q,
+                  const void* W_sf, void* y, void* stream);
+
+/* Shape of moe_forward_w4: H and I multiples of 128 up to 65536, T*k <= 65535. */
+typedef struct moe_w4_shape {
+    int32_t T, H, I, E, k, group;
+} moe_w4_shape;
+
+/* Bytes of moe_forward_w4's workspace.  Host only. */
+int moe_w4_workspace(const moe_w4_shape* shape, size_t* bytes);
+
+/* The layer of moe_forward with 4-bit weights (W1 as [E, 2I, H] codes: row f
+ * the gate's, row I + f the up projection's feature f; W2 as [E, H, I] codes)
+ * straight from topk_idx, without routing tables: for decoding.
+ *     h = x[t] W1[e]^T,  a = silu(h[:I]) h[I:] (rounded to bf16, the operand of
+ *     the second product),  y[t] = sum_j topk_w[t, j] a W2[e]^T
+ * The sum over j is FP32 in slot order (deterministic).  A slot whose id is
+ * outside [0, E) contributes nothing; a token with none gets 0.  topk_idx NULL
+ * (E = k = 1): every token takes the one matrix with weight 1 (a shared
+ * expert); topk_w is not read.  Tokens that share an expert share its reads,
+ * 8 or 16 at a time.  ws: moe_w4_workspace bytes of scratch; y bf16 [T, H] is
+ * overwritten. */
+int moe_forward_w4(const moe_w4_shape* shape, const void* x, const uint8_t* W1_q, const void* W1_sf,
+                   const uint8_t* W2_q, const void* W2_sf, const int32_t* topk_idx, const float* topk_w, void* ws,
+                   void* y, void* stream);
+
 /* Tracing.  moe_trace_begin hands the library `capacity` CUDA events
  * (cudaEvent_t passed as void*, created by the caller with timing enabled).
  * Until moe_trace_end, each kernel the library launches from this thread is

@@ -39,6 +39,10 @@ class MoeLayout(ctypes.Structure):
     ] + [("dw_part_cols", ctypes.c_int32), ("route_blocks", ctypes.c_int32)]
 
 
+class MoeW4Shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I", "E", "k", "group")]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe error {code}: {msg}")
@@ -82,7 +86,12 @@ def lib():
             L.moe_layer_norm_forward.argtypes = [i64, i32, i32, i32, vp, i64, vp, vp, f32, vp, vp, vp, vp]
             L.moe_layer_norm_workspace.argtypes = [i64, i32, P(ctypes.c_size_t)]
             L.moe_layer_norm_backward.argtypes = [i64, i32, i32, i32, vp, i64, vp, i64] + [vp] * 8
-            for n in ("moe_layer_norm_forward", "moe_layer_norm_workspace", "moe_layer_norm_backward"):
+            L.moe_quantize_w4.argtypes = [i32] * 4 + [vp] * 4
+            L.moe_matvec_w4.argtypes = [i32] * 4 + [vp] * 5
+            L.moe_w4_workspace.argtypes = [P(MoeW4Shape), P(ctypes.c_size_t)]
+            L.moe_forward_w4.argtypes = [P(MoeW4Shape)] + [vp] * 10
+            for n in ("moe_layer_norm_forward", "moe_layer_norm_workspace", "moe_layer_norm_backward",
+                      "moe_quantize_w4", "moe_matvec_w4", "moe_w4_workspace", "moe_forward_w4"):
                 getattr(L, n).restype = ctypes.c_int
             L.moe_trace_begin.argtypes = [vp, ctypes.c_int]
             L.moe_trace_begin.restype = ctypes.c_int
@@ -320,6 +329,44 @@ def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, s
         _ptr(mean, f32, rows, "mean"), _ptr(rstd, f32, rows, "rstd"), _ptr(dx, x.dtype, rows * H, "dx"),
         _ptr(dweight, wt, H, "dweight"), _ptr(dbias, wt, H, "dbias"),
         _ptr(ws, torch.uint8, moe_layer_norm_workspace(rows, H), "ws"), _stream(stream)))
+
+
+def moe_quantize_w4(W, W_q, W_sf, group: int, stream=None):
+    """W bf16 [E, K, N] -> W_q uint8 [E, N, K // 2] (4-bit codes) and W_sf bf16
+    [E, N, K // group]."""
+    E, K, N = W.shape
+    _check(lib().moe_quantize_w4(E, K, N, group, _ptr(W, torch.bfloat16, E * K * N, "W"),
+                                 _ptr(W_q, torch.uint8, E * N * K // 2, "W_q"),
+                                 _ptr(W_sf, torch.bfloat16, E * N * K // max(group, 1), "W_sf"), _stream(stream)))
+
+
+def moe_matvec_w4(x, W_q, W_sf, y, group: int, stream=None):
+    """y bf16 [M, N] = x bf16 [M, K] times the 4-bit matrix [N, K] transposed."""
+    M, K = x.shape
+    N = W_q.shape[0]
+    bf = torch.bfloat16
+    _check(lib().moe_matvec_w4(M, N, K, group, _ptr(x, bf, M * K, "x"), _ptr(W_q, torch.uint8, N * K // 2, "W_q"),
+                               _ptr(W_sf, bf, N * K // max(group, 1), "W_sf"), _ptr(y, bf, M * N, "y"), _stream(stream)))
+
+
+def moe_w4_workspace(shape: MoeW4Shape) -> int:
+    """Bytes of moe_forward_w4's workspace."""
+    out = ctypes.c_size_t()
+    _check(lib().moe_w4_workspace(ctypes.byref(shape), ctypes.byref(out)))
+    return out.value
+
+
+def moe_forward_w4(shape: MoeW4Shape, x, W1_q, W1_sf, W2_q, W2_sf, topk_idx, topk_w, ws, y, stream=None):
+    """The routed experts with 4-bit weights (topk_idx None: one expert, every
+    token, weight 1).  ws: uint8 of moe_w4_workspace elements."""
+    T, H, I, E, k, G = shape.T, shape.H, shape.I, shape.E, shape.k, max(shape.group, 1)
+    bf, u8 = torch.bfloat16, torch.uint8
+    _check(lib().moe_forward_w4(
+        ctypes.byref(shape), _ptr(x, bf, T * H, "x"), _ptr(W1_q, u8, E * I * H, "W1_q"),
+        _ptr(W1_sf, bf, E * 2 * I * H // G, "W1_sf"), _ptr(W2_q, u8, E * I * H // 2, "W2_q"),
+        _ptr(W2_sf, bf, E * I * H // G, "W2_sf"), _ptr(topk_idx, torch.int32, T * k, "topk_idx"),
+        _ptr(topk_w, torch.float32, T * k, "topk_w"), _ptr(ws, u8, moe_w4_workspace(shape), "ws"),
+        _ptr(y, bf, T * H, "y"), _stream(stream)))
 
 
 def moe_last_error() -> str:

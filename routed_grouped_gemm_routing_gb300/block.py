@@ -86,3 +86,105 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5):
     """Layer norm over the last axis of x (any number of leading axes), in
     x's type.  Differentiable in x, weight and bias."""
     return LayerNormFunction.apply(x, weight, bias, float(eps))
+
+
+# ---------------------------------------------------------- 4-bit weights
+def quantize_w4(W, group: int = 128):
+    """(codes, scales) of W bf16 [K, N] or [E, K, N] (the layout of the layer's
+    W1 and W2): codes uint8 [.., N, K // 2], scales bf16 [.., N, K // group]."""
+    W3 = W if W.dim() == 3 else W.unsqueeze(0)
+    if W3.dim() != 3:
+        raise ValueError("expected W [K, N] or [E, K, N]")
+    E, K, N = W3.shape
+    if group not in (32, 64, 128) or K % 128:
+        raise ValueError("group must be 32, 64 or 128, and K a multiple of 128")
+    with _on(W):
+        q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=W.device)
+        sf = torch.empty((E, N, K // group), dtype=torch.bfloat16, device=W.device)
+        B.moe_quantize_w4(W3.contiguous(), q, sf, group)
+    return (q, sf) if W.dim() == 3 else (q[0], sf[0])
+
+
+def _check_w4(q, sf, group, *shape):
+    K = shape[-1]
+    if tuple(q.shape) != (*shape[:-1], K // 2) or tuple(sf.shape) != (*shape[:-1], K // group):
+        raise ValueError(f"expected codes {[*shape[:-1], K // 2]} and scales {[*shape[:-1], K // group]}, "
+                         f"got {list(q.shape)} and {list(sf.shape)}")
+    if q.dtype != torch.uint8 or sf.dtype != torch.bfloat16 or not q.is_cuda or not sf.is_cuda:
+        raise TypeError("codes must be uint8 and scales bfloat16 CUDA tensors")
+    return q.contiguous(), sf.contiguous()
+
+
+class W4Linear:
+    """y = x W^T for W [N, K] held as 4-bit codes with one scale per ``group``
+    values of K (quantize_w4), for a few rows of x at a time.  Not
+    differentiable."""
+
+    def __init__(self, q, sf, group: int = 128):
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        N, half = q.shape
+        self.N, self.K, self.group = N, 2 * half, group
+        self.q, self.sf = _check_w4(q, sf, group, N, 2 * half)
+
+    def forward(self, x, out=None):
+        """y bf16 [M, N] for x bf16 [M, K]."""
+        M, K = x.shape
+        if K != self.K:
+            raise ValueError(f"x has {K} columns, the weight {self.K}")
+        with _on(x):
+            if out is None:
+                out = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
+            B.moe_matvec_w4(x if x.is_contiguous() else x.contiguous(), self.q, self.sf, out, self.group)
+        return out
+
+    __call__ = forward
+
+
+class W4Experts:
+    """The layer's experts with 4-bit weights, for decoding: W1 codes
+    [E, 2I, H // 2] (gate rows, then up rows), W2 codes [E, H, I // 2], scales
+    per ``group``.  E = 1 without routing is a shared expert.  Not
+    differentiable."""
+
+    def __init__(self, W1_q, W1_sf, W2_q, W2_sf, group: int = 128):
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        E, I2, half = W1_q.shape
+        self.E, self.H, self.I, self.group = E, 2 * half, I2 // 2, group
+        self.W1_q, self.W1_sf = _check_w4(W1_q, W1_sf, group, E, I2, self.H)
+        self.W2_q, self.W2_sf = _check_w4(W2_q, W2_sf, group, E, self.H, self.I)
+
+    @classmethod
+    def quantize(cls, W1, W2, group: int = 128):
+        """From bf16 W1 [E, H, 2I] (gate | up) and W2 [E, I, H]; a shared
+        expert's may lack the leading axis."""
+        W1, W2 = (W if W.dim() == 3 else W.unsqueeze(0) for W in (W1, W2))
+        return cls(*quantize_w4(W1, group), *quantize_w4(W2, group), group)
+
+    def forward(self, x, topk_idx=None, topk_w=None, out=None):
+        """y bf16 [T, H] for x bf16 [T, H] and the routing (topk_idx int
+        [T, k], topk_w float [T, k]; neither with a single expert)."""
+        T, H = x.shape
+        if H != self.H:
+            raise ValueError("x's hidden size differs from the weights'")
+        if topk_idx is None:
+            if self.E != 1:
+                raise ValueError("several experts need topk_idx and topk_w")
+            k = 1
+        else:
+            k = topk_idx.shape[1]
+            if tuple(topk_idx.shape) != (T, k) or topk_w is None or tuple(topk_w.shape) != (T, k):
+                raise ValueError("expected topk_idx and topk_w [T, k]")
+            topk_idx = topk_idx.to(torch.int32).contiguous()
+            topk_w = topk_w.to(torch.float32).contiguous()
+        s = B.MoeW4Shape(T, H, self.I, self.E, k, self.group)
+        with _on(x):
+            ws = torch.empty((max(B.moe_w4_workspace(s), 16),), dtype=torch.uint8, device=x.device)
+            if out is None:
+                out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+            B.moe_forward_w4(s, x if x.is_contiguous() else x.contiguous(), self.W1_q, self.W1_sf, self.W2_q,
+                             self.W2_sf, topk_idx, topk_w, ws, out)
+        return out
+
+    __call__ = forward

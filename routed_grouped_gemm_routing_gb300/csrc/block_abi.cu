@@ -9,6 +9,8 @@ using namespace moe;
 
 namespace {
 
+constexpr int kMaxW4K = 65536;
+
 // Alignment that an element of the type needs, 0 for an unknown type.
 int elt_size(int type) { return type == MOE_F32 ? 4 : type == MOE_BF16 || type == MOE_F16 ? 2 : 0; }
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
@@ -21,6 +23,24 @@ int check_norm(int64_t rows, int32_t H, int32_t x_type, int32_t w_type) {
         return abi_fail(MOE_EUNSUPPORTED, "w_type must be MOE_F32 or x_type");
     return MOE_OK;
 }
+
+int check_group(int32_t group) {
+    return group == 32 || group == 64 || group == 128
+               ? MOE_OK
+               : abi_fail(MOE_EUNSUPPORTED, "group must be 32, 64 or 128");
+}
+int check_w4(const moe_w4_shape* s) {
+    if (!s) return abi_fail(MOE_EINVAL, "shape is NULL");
+    if (s->T < 0) return abi_fail(MOE_EINVAL, "T must be >= 0");
+    if (s->H <= 0 || s->I <= 0) return abi_fail(MOE_EINVAL, "H and I must be > 0");
+    if (s->E < 1 || s->E > kMaxExperts) return abi_fail(MOE_EINVAL, "E must be in [1, 1024]");
+    if (s->k < 1 || s->k > s->E) return abi_fail(MOE_EINVAL, "k must be in [1, E]");
+    if (s->H % 128 || s->I % 128 || s->H > kMaxW4K || s->I > kMaxW4K)
+        return abi_fail(MOE_EUNSUPPORTED, "H and I must be multiples of 128, at most 65536");
+    if ((long long)s->T * s->k > 65535) return abi_fail(MOE_EUNSUPPORTED, "T*k must be <= 65535");
+    return check_group(s->group);
+}
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -84,6 +104,81 @@ int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_t
     const int e = launch_layer_norm_bwd(x_type, w_type, a, st);
     trace_post(st, "layer_norm_bwd");
     return e ? abi_cuda_fail(e, "layer norm backward launch") : MOE_OK;
+}
+
+int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, const void* x, const uint8_t* W_q,
+                  const void* W_sf, void* y, void* stream) {
+    if (M < 0 || N < 1 || K < 1) return abi_fail(MOE_EINVAL, "M must be >= 0, N and K > 0");
+    if (K % 128 || K > kMaxW4K) return abi_fail(MOE_EUNSUPPORTED, "K must be a multiple of 128, at most 65536");
+    if (M > 65535) return abi_fail(MOE_EUNSUPPORTED, "M must be <= 65535");
+    int rc = check_group(group);
+    if (rc) return rc;
+    if (M == 0) return MOE_OK;
+    if (!x || !W_q || !W_sf || !y) return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    const void* ptrs[] = {x, W_q, W_sf, y};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    int sms = 0;
+    if ((rc = abi_select_device(W_q, &sms))) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    trace_pre(st);
+    const int e = launch_matvec_w4(M, N, K, group, x, W_q, W_sf, y, st);
+    trace_post(st, "matvec_w4");
+    return e ? abi_cuda_fail(e, "4-bit product launch") : MOE_OK;
+}
+
+int moe_w4_workspace(const moe_w4_shape* shape, size_t* bytes) {
+    if (!bytes) return abi_fail(MOE_EINVAL, "bytes is NULL");
+    const int rc = check_w4(shape);
+    if (rc) return rc;
+    const size_t slots = (size_t)shape->T * shape->k;
+    *bytes = up256(slots * shape->I * 2) + slots * shape->H * 4;
+    return MOE_OK;
+}
+
+int moe_forward_w4(const moe_w4_shape* shape, const void* x, const uint8_t* W1_q, const void* W1_sf,
+                   const uint8_t* W2_q, const void* W2_sf, const int32_t* topk_idx, const float* topk_w, void* ws,
+                   void* y, void* stream) {
+    int rc = check_w4(shape);
+    if (rc) return rc;
+    if (!topk_idx && (shape->E != 1 || shape->k != 1))
+        return abi_fail(MOE_EINVAL, "without topk_idx E and k must be 1");
+    if (shape->T == 0) return MOE_OK;
+    if (!x || !W1_q || !W1_sf || !W2_q || !W2_sf || !ws || !y || (topk_idx && !topk_w))
+        return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    const void* ptrs[] = {x, W1_q, W1_sf, W2_q, W2_sf, topk_idx, topk_w, ws, y};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    int sms = 0;
+    if ((rc = abi_select_device(ws, &sms))) return rc;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    const size_t slots = (size_t)shape->T * shape->k;
+    const W4Experts a = {shape->T, shape->H, shape->I, shape->E, shape->k, shape->group, x, W1_q, W2_q, W1_sf, W2_sf,
+                         topk_idx, topk_w, w, reinterpret_cast<float*>(w + up256(slots * shape->I * 2)), y};
+    cudaStream_t st = (cudaStream_t)stream;
+    trace_pre(st);
+    const int e = launch_experts_w4(a, st);
+    trace_post(st, "forward_w4");
+    return e ? abi_cuda_fail(e, "4-bit experts launch") : MOE_OK;
+}
+
+int moe_quantize_w4(int32_t E, int32_t K, int32_t N, int32_t group, const void* W, uint8_t* W_q, void* W_sf,
+                    void* stream) {
+    if (E < 1 || E > kMaxExperts || K < 1 || N < 1) return abi_fail(MOE_EINVAL, "E must be in [1, 1024], K and N > 0");
+    if (K % 128 || K > kMaxW4K) return abi_fail(MOE_EUNSUPPORTED, "K must be a multiple of 128, at most 65536");
+    int rc = check_group(group);
+    if (rc) return rc;
+    if (!W || !W_q || !W_sf) return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    const void* ptrs[] = {W, W_q, W_sf};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    int sms = 0;
+    if ((rc = abi_select_device(W, &sms))) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    trace_pre(st);
+    const int e = launch_quantize_w4(E, K, N, group, W, W_q, W_sf, st);
+    trace_post(st, "quantize_w4");
+    return e ? abi_cuda_fail(e, "4-bit quantization launch") : MOE_OK;
 }
 
 }  // extern "C"

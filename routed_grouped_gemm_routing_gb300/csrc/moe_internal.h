@@ -114,6 +114,23 @@ constexpr int kLnBwdBlocks = 304;
 int launch_layer_norm_fwd(int x_type, int w_type, const LnFwdArgs& a, cudaStream_t st);
 int launch_layer_norm_bwd(int x_type, int w_type, const LnBwdArgs& a, cudaStream_t st);
 
+// ---------------------------------------------------------- 4-bit weights
+struct W4Experts {
+    int T, H, I, E, k, group;
+    const void* x;  // bf16 [T, H]
+    const uint8_t *W1_q, *W2_q;
+    const void *W1_sf, *W2_sf;  // bf16
+    const int32_t* topk_idx;    // null: one expert (E = 1), every token
+    const float* topk_w;
+    void* act;    // bf16 [T k, I]
+    float* part;  // [T k, H] (with topk_idx)
+    void* y;      // bf16 [T, H]
+};
+int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q, const void* sf, void* y,
+                     cudaStream_t st);
+int launch_experts_w4(const W4Experts& w, cudaStream_t st);
+int launch_quantize_w4(int E, int K, int N, int G, const void* W, uint8_t* q, void* sf, cudaStream_t st);
+
 // Layout of the three workspaces (host only).
 int compute_layout(const moe_shape* s, moe_layout* L);
 

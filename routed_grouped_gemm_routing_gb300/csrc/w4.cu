@@ -1,0 +1,523 @@
+// Products with 4-bit weights and one scale per group, for a few rows of
+// activations (decoding): a dense matrix, and the routed experts (both
+// projections of every expert held that way).
+//
+//   y[r, n] = sum_k x[r, k] (code[n, k] - 8) sf[n, k / G]          G = 32, 64, 128
+//
+// Bound by DRAM: K / 2 + 2 K / G bytes per row of W.  At 6.8 TB/s that is 47
+// weights per clock and SM, 2.7 instruction slots per weight and lane, so the
+// products go to the tensor cores and the codes are unpacked two at a time:
+// (w >> 4 m) & 0x000f000f | 0x43004300 is the bf16 pair 128 + code, exactly.
+// The offset is taken out in FP32 through the accumulator's initial value,
+//   sum x (code - 8) = [-136 sum_k x] + sum x (128 + code),
+// one sum of x per row and group, made once per block.  A group's sum is then
+// scaled and added in FP32; nothing is rounded before the output.
+//
+// mma m16n8k16: A = 16 rows of W, B = up to 8 rows of x.  (A tcgen05.mma would
+// need the unpacked weights in shared memory first: the unpacking through
+// registers is what has to be cheap here, and 8 columns are far below its
+// tile.)  The order of the codes in memory makes a lane's 16 bytes of a
+// 128-code block the operands of its eight products: word 4 t + j holds codes
+// 32 j + 8 t .. + 7, code 2 m in nibble m, code 2 m + 1 in nibble m + 4, so
+// that lane t's pair m of group j meets x[32 j + 8 t + 2 m, + 1].
+//
+// A block takes a job (up to 8 NT rows that use the same matrix) and a range
+// of 16-row tiles; KS of its warps share a tile, every KS-th 128-code block
+// each, and join their FP32 sums in shared memory in a fixed order.  Every lane
+// copies its own weights several blocks ahead with cp.async into its own slots
+// (no barrier in the stream), across the tiles of its range.
+#include "moe_internal.h"
+#include "ptx.cuh"
+#include "smem_limit.h"
+
+namespace moe {
+
+namespace {
+
+// 128-code blocks held or in flight per warp, by 16-row fragments of a tile
+__host__ __device__ constexpr int w4_depth(int rt) { return rt == 2 ? 3 : 4; }
+
+enum W4Epi { W4_PLAIN, W4_GATED, W4_SLOT };
+
+struct W4Args {
+    const __nv_bfloat16* x;  // [rows, K]
+    const uint8_t* q;        // [E][N][K / 2]
+    const __nv_bfloat16* sf;  // [E][N][K / G]
+    int N;       // rows of one matrix (W4_GATED: 2 I)
+    int F;       // output features: N, or I
+    int K, E;
+    int rows;    // rows of x (no ids)
+    const int32_t* ids;  // expert of each slot, or null: one matrix, rows of x in order
+    int slots;   // length of ids
+    int xdiv;    // x row of a slot = slot / xdiv
+    int tiles;   // ceil(F / 16)
+    int tpc;     // tiles per block
+    int ks;      // warps per tile
+    int R;       // rows of a job
+    const float* slot_w;  // W4_SLOT: weight of each slot
+    void* out;   // W4_PLAIN, W4_GATED: bf16 [row or slot][F]; W4_SLOT: f32 [slot][F]
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// codes 2 m and 2 m + 1 of a word as the bf16 pair 128 + code
+template <int m>
+__device__ __forceinline__ uint32_t pair128(uint32_t w) {
+    return ((w >> (4 * m)) & 0x000f000fu) | 0x43004300u;
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
+    return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
+
+// Bytes of the parts of a block's shared memory.
+struct W4Smem {
+    int x, xs, ring, sring, red, total;
+};
+template <int NT, int RT, int G>
+__host__ __device__ __forceinline__ W4Smem w4_smem(int K, int nw, int rows) {
+    W4Smem s;
+    s.x = 0;
+    // a row of x and 64 bytes: the eight rows' 16-byte fragments in all banks
+    const int xbytes = rows * (2 * K + 64);
+    s.xs = xbytes;
+    s.ring = (s.xs + (K / G) * 8 * NT * 4 + 15) / 16 * 16;
+    constexpr int kDepth = w4_depth(RT);
+    s.sring = s.ring + nw * kDepth * RT * 2 * 32 * 16;
+    s.red = s.sring + nw * kDepth * RT * 2 * 32 * (G == 32 ? 8 : 4);
+    s.total = s.red + 2 * nw * RT * NT * 128 * 4;
+    return s;
+}
+
+template <int NT, int RT, int G, int EPI>
+__global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
+    constexpr int kR = 8 * NT;
+    const int R = p.R;  // rows of a job, at most kR
+    constexpr int kDepth = w4_depth(RT);
+    constexpr int kSpb = 128 / G;        // scales per 128-code block
+    constexpr int kSBytes = G == 32 ? 8 : 4;
+    static_assert(RT == (EPI == W4_GATED ? 2 : 1), "a gated tile is 16 gate and 16 up rows");
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int row_of[kR];  // row or slot of every row of the job
+    __shared__ int job_n;
+    const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int K = p.K, KB = K / 128, KS = p.ks, NG = nw / KS;
+    const int ks = warp % KS, gi = warp / KS;
+
+    // ---- the job: its matrix and its rows
+    int e = 0;
+    if (p.ids) {
+        const int s = blockIdx.y;
+        e = __ldg(p.ids + s);
+        if (e < 0 || e >= p.E) return;  // a dropped slot
+        if (warp == 0) {
+            // slots of expert e in order; every R-th of them leads a job
+            int before = 0, n = 0;
+            for (int base = 0; base < p.slots && n < R; base += 32) {
+                const int i = base + lane;
+                const bool same = i < p.slots && __ldg(p.ids + i) == e;
+                before += __popc(__ballot_sync(0xffffffffu, same && i < s));
+                const uint32_t from = __ballot_sync(0xffffffffu, same && i >= s);
+                const int pos = n + __popc(from & ((1u << lane) - 1u));
+                if (same && i >= s && pos < R) row_of[pos] = i;
+                n += __popc(from);
+            }
+            if (lane == 0) job_n = before % R == 0 ? (n < R ? n : R) : 0;
+        }
+    } else {
+        const int r0 = blockIdx.y * R;
+        if (threadIdx.x < R) row_of[threadIdx.x] = r0 + threadIdx.x;
+        if (threadIdx.x == 0) job_n = p.rows - r0 < R ? p.rows - r0 : R;
+    }
+    __syncthreads();
+    const int n = job_n;
+    if (n == 0) return;  // not the leading slot
+
+    const W4Smem L = w4_smem<NT, RT, G>(K, nw, n);
+    __nv_bfloat16* xsm = reinterpret_cast<__nv_bfloat16*>(smem + L.x);
+    float* xs = reinterpret_cast<float*>(smem + L.xs);  // [K / G][kR]: -136 sum of x
+    const uint4* ring = reinterpret_cast<const uint4*>(smem + L.ring) + warp * kDepth * RT * 2 * 32;
+    const uint8_t* sring = smem + L.sring + warp * kDepth * RT * 2 * 32 * kSBytes;
+    float* red = reinterpret_cast<float*>(smem + L.red);
+
+    // ---- the stream of this lane's weights: tiles gi, gi + NG, .. of the
+    // block's range, blocks ks, ks + KS, .. of each
+    const int tile0 = blockIdx.x * p.tpc;
+    const int tile1 = tile0 + p.tpc < p.tiles ? tile0 + p.tpc : p.tiles;
+    const uint8_t* q = p.q + (size_t)e * p.N * (K / 2);
+    const __nv_bfloat16* sf = p.sf + (size_t)e * p.N * (K / G);
+    int ft = tile0 + gi, fb = ks, fslot = 0;
+    auto row_index = [&](int tile, int i) {  // row of W of this lane's i-th fragment: clamped, not stored when past F
+        const int f = tile * 16 + g + 8 * (i & 1);
+        return (f < p.F ? f : p.F - 1) + (i >> 1) * p.F;
+    };
+    auto fetch = [&]() {
+        if (ft < tile1 && fb < KB) {
+#pragma unroll
+            for (int i = 0; i < RT * 2; ++i) {
+                const size_t row = (size_t)row_index(ft, i);
+                cp_async_16(smem_addr(ring + (fslot * RT * 2 + i) * 32 + lane), q + row * (K / 2) + fb * 64 + t * 16,
+                            16u);
+                const uint32_t sdst = smem_addr(sring + ((fslot * RT * 2 + i) * 32 + lane) * kSBytes);
+                const __nv_bfloat16* sp = sf + row * (K / G) + fb * kSpb;
+                if constexpr (G == 32) {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(sdst), "l"(sp) : "memory");
+                } else if constexpr (G == 64) {
+                    cp_async_4(sdst, sp, 4u);
+                } else {
+                    // one scale: the aligned word that holds it (of which an
+                    // even last scale has only its own two bytes)
+                    const size_t idx = (size_t)(sp - p.sf);
+                    const bool last = idx + 1 == (size_t)p.E * p.N * (K / G);
+                    cp_async_4(sdst, p.sf + (idx & ~(size_t)1), last && !(idx & 1) ? 2u : 4u);
+                }
+            }
+            fb += KS;
+            if (fb >= KB) {
+                fb = ks;
+                ft += NG;
+            }
+        }
+        cp_async_commit();
+        fslot = (fslot + 1) % kDepth;
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth - 1; ++d) fetch();
+
+    // ---- x and its group sums
+    const int xst = K + 32;  // elements between rows of x in shared memory
+    for (int v = threadIdx.x; v < n * (K / 8); v += blockDim.x) {  // K / 8 is a multiple of 16: whole groups per row
+        const int r = v / (K / 8), c = v - r * (K / 8);
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(row_of[r] / p.xdiv) * K) + c);
+        *reinterpret_cast<uint4*>(xsm + r * xst + c * 8) = u;
+        float f[8], s = 0.0f;
+        unpack_bf16x8(u, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += f[i];
+        // the last warp may be half full: groups of G / 8 <= 16 lanes stay whole
+        const uint32_t act = v - lane + 32 <= n * (K / 8) ? 0xffffffffu : 0x0000ffffu;
+#pragma unroll
+        for (int d = 1; d < G / 8; d <<= 1) s += __shfl_xor_sync(act, s, d);
+        if ((c & (G / 8 - 1)) == 0) xs[(c / (G / 8)) * kR + r] = -136.0f * s;
+    }
+    __syncthreads();
+
+    const uint4* xrow[NT];  // this lane's row of each 8-row tile (a row past the job's repeats the last)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + g;
+        xrow[nt] = reinterpret_cast<const uint4*>(xsm + (r < n ? r : n - 1) * xst) + t;
+    }
+    // y of feature f and row r of the job
+    auto emit = [&](int f, int r, float v, float up) {
+        if (f >= p.F || r >= n) return;
+        const size_t o = (size_t)row_of[r] * p.F + f;
+        if constexpr (EPI == W4_SLOT) {
+            reinterpret_cast<float*>(p.out)[o] = __ldg(p.slot_w + row_of[r]) * v;
+        } else {
+            if constexpr (EPI == W4_GATED) v = v / (1.0f + expf(-v)) * up;
+            reinterpret_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+        }
+    };
+
+    int slot = 0, buf = 0;
+    for (int tile = tile0 + gi; tile < tile1; tile += NG) {
+        float acc[RT][NT][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.0f;
+        for (int kb = ks; kb < KB; kb += KS) {
+            cp_async_wait_group<kDepth - 2>();
+            uint4 w[RT * 2];
+            float sc[RT * 2][kSpb];
+#pragma unroll
+            for (int i = 0; i < RT * 2; ++i) {
+                w[i] = ring[(slot * RT * 2 + i) * 32 + lane];
+                const uint32_t* s = reinterpret_cast<const uint32_t*>(sring + ((slot * RT * 2 + i) * 32 + lane) * kSBytes);
+                if constexpr (G == 128) {
+                    const uint32_t odd = (uint32_t)(((size_t)e * p.N + row_index(tile, i)) * KB + kb) & 1u;
+                    sc[i][0] = __uint_as_float(odd ? s[0] & 0xffff0000u : s[0] << 16);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < kSpb / 2; ++h) {
+                        sc[i][2 * h] = __uint_as_float(s[h] << 16);
+                        sc[i][2 * h + 1] = __uint_as_float(s[h] & 0xffff0000u);
+                    }
+                }
+            }
+            fetch();
+            slot = (slot + 1) % kDepth;
+            float c[RT][NT][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j % (G / 32) == 0) {
+                    const float* xg = xs + ((kb * 128 + j * 32) / G) * kR + 2 * t;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float2 v = *reinterpret_cast<const float2*>(xg + 8 * nt);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            c[rt][nt][0] = c[rt][nt][2] = v.x;
+                            c[rt][nt][1] = c[rt][nt][3] = v.y;
+                        }
+                    }
+                }
+                uint4 b[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) b[nt] = xrow[nt][kb * 16 + j * 4];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const uint32_t u = word_of(w[2 * rt], j), v = word_of(w[2 * rt + 1], j);
+                    const uint32_t u0 = pair128<0>(u), u1 = pair128<1>(u), u2 = pair128<2>(u), u3 = pair128<3>(u);
+                    const uint32_t v0 = pair128<0>(v), v1 = pair128<1>(v), v2 = pair128<2>(v), v3 = pair128<3>(v);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_bf16(c[rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y);
+                        mma_bf16(c[rt][nt], u2, v2, u3, v3, b[nt].z, b[nt].w);
+                    }
+                }
+                if ((j + 1) % (G / 32) == 0) {
+                    const int si = j / (G / 32);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            acc[rt][nt][0] = fmaf(sc[2 * rt][si], c[rt][nt][0], acc[rt][nt][0]);
+                            acc[rt][nt][1] = fmaf(sc[2 * rt][si], c[rt][nt][1], acc[rt][nt][1]);
+                            acc[rt][nt][2] = fmaf(sc[2 * rt + 1][si], c[rt][nt][2], acc[rt][nt][2]);
+                            acc[rt][nt][3] = fmaf(sc[2 * rt + 1][si], c[rt][nt][3], acc[rt][nt][3]);
+                        }
+                }
+            }
+        }
+        // register i of lane (g, t) of tile nt: feature g + 8 (i / 2), row 8 nt + 2 t + i % 2
+        if (KS == 1) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    emit(tile * 16 + g + 8 * (i >> 1), 8 * nt + 2 * t + (i & 1), acc[0][nt][i], acc[RT - 1][nt][i]);
+        } else {
+            constexpr int kPer = RT * NT * 128;  // floats of a warp
+            float* mine = red + (size_t)(buf * nw + warp) * kPer;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mine[((rt * NT + nt) * 4 + i) * 32 + lane] = acc[rt][nt][i];
+            asm volatile("bar.sync %0, %1;" ::"r"(gi + 1), "r"(KS * 32) : "memory");
+            const float* all = red + (size_t)(buf * nw + gi * KS) * kPer;
+            for (int u = ks; u < NT * 4; u += KS) {
+                float v = 0.0f, up = 0.0f;
+                for (int k = 0; k < KS; ++k) {
+                    v += all[k * kPer + u * 32 + lane];
+                    if constexpr (RT == 2) up += all[k * kPer + (NT * 4 + u) * 32 + lane];
+                }
+                emit(tile * 16 + g + 8 * ((u & 3) >> 1), 8 * (u >> 2) + 2 * t + (u & 1), v, up);
+            }
+            buf ^= 1;  // the next tile's sums go to the other half: two tiles on, this barrier has passed
+        }
+    }
+    cp_async_wait_all();
+}
+
+// y[token] = sum over its slots in order of o[slot], skipping dropped ones.
+__global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict__ o, const int32_t* __restrict__ ids,
+                                                         int T, int k, int E, int H, __nv_bfloat16* __restrict__ y) {
+    const long long n4 = (long long)T * H / 4;
+    for (long long v = (long long)blockIdx.x * 256 + threadIdx.x; v < n4; v += (long long)gridDim.x * 256) {
+        const int tok = (int)(v * 4 / H), h = (int)(v * 4 - (long long)tok * H);
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int j = 0; j < k; ++j) {
+            const int e = __ldg(ids + (size_t)tok * k + j);
+            if (e < 0 || e >= E) continue;
+            const float4 a = __ldg(reinterpret_cast<const float4*>(o + ((size_t)tok * k + j) * H + h));
+            s.x += a.x;
+            s.y += a.y;
+            s.z += a.z;
+            s.w += a.w;
+        }
+        uint2 u;
+        u.x = pack_bf16x2(s.x, s.y);
+        u.y = pack_bf16x2(s.z, s.w);
+        *reinterpret_cast<uint2*>(y + (size_t)tok * H + h) = u;
+    }
+}
+
+// W bf16 [E][K][N] -> codes [E][N][K / 2] and scales [E][N][K / G]: one thread
+// per column and 128-code block.  Scale = max|w| / 7 rounded to bf16 (0 for a
+// zero group), code = round(w / scale) + 8 in [0, 15].
+template <int G>
+__global__ void __launch_bounds__(128) w4_quantize_kernel(const __nv_bfloat16* __restrict__ W, int K, int N,
+                                                          uint8_t* __restrict__ q, __nv_bfloat16* __restrict__ sf) {
+    const int n = blockIdx.x * 128 + threadIdx.x;
+    if (n >= N) return;
+    const int kb = blockIdx.y;
+    const size_t e = blockIdx.z;
+    const __nv_bfloat16* w = W + (e * K + (size_t)kb * 128) * N + n;
+    uint32_t words[16];
+    float scale = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j % (G / 32) == 0) {
+            float amax = 0.0f;
+            for (int i = 0; i < G; ++i) amax = fmaxf(amax, fabsf(__bfloat162float(__ldg(w + (size_t)(j * 32 + i) * N))));
+            const __nv_bfloat16 s = __float2bfloat16_rn(amax / 7.0f);
+            sf[(e * N + n) * (size_t)(K / G) + kb * (128 / G) + j / (G / 32)] = s;
+            scale = __bfloat162float(s);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            uint32_t u = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float v = __bfloat162float(__ldg(w + (size_t)(j * 32 + t * 8 + i) * N));
+                const float r = scale > 0.0f ? rintf(v / scale) : 0.0f;
+                const int code = (int)fminf(fmaxf(r, -8.0f), 7.0f) + 8;
+                u |= (uint32_t)code << (4 * (i / 2 + 4 * (i & 1)));
+            }
+            words[t * 4 + j] = u;
+        }
+    }
+    uint4* out = reinterpret_cast<uint4*>(q + (e * N + n) * (size_t)(K / 2) + (size_t)kb * 64);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) out[t] = make_uint4(words[4 * t], words[4 * t + 1], words[4 * t + 2], words[4 * t + 3]);
+}
+
+constexpr int kW4Smem = 224 * 1024;
+
+// Launch shape: warps per tile and tiles per block for blocks of nw warps,
+// per_sm of them on an SM.  What the choice makes small is the longest chain
+// of a warp, in quarters of a 128-code block, over the blocks that run one
+// after the other on an SM: a round of a shared tile costs about one block
+// more (the join), a block's start (job, x) about four.
+void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
+    const int KB = a->K / 128, slots = 152 * per_sm;
+    long long best = -1;
+    for (int ks = 1; ks <= nw; ks *= 2) {
+        const int ng = nw / ks;
+        for (int rounds = 1; rounds <= 64; ++rounds) {
+            const int tpc = ng * rounds;
+            const long long blocks = (long long)jobs * ((a->tiles + tpc - 1) / tpc);
+            const long long waves = (blocks + slots - 1) / slots;
+            const long long cost = waves * (4 * 4 + rounds * (4 * ((KB + ks - 1) / ks) + (ks > 1 ? 4 : 0)));
+            if (best < 0 || cost < best) {
+                best = cost;
+                a->ks = ks;
+                a->tpc = tpc;
+            }
+            if (tpc >= a->tiles) break;
+        }
+    }
+}
+
+// rows: rows that can share a job; groups of rows (no ids) or slots (ids) are
+// the jobs.
+template <int NT, int RT, int G, int EPI>
+int w4_launch(W4Args a, int rows, cudaStream_t st) {
+    static SmemLimit limit;
+    // as many rows per job as leave room for a block of four warps
+    a.R = rows < 8 * NT ? rows : 8 * NT;
+    while (a.R > 1 && w4_smem<NT, RT, G>(a.K, 4, a.R).total > kW4Smem) --a.R;
+    auto bytes = [&](int nw) { return w4_smem<NT, RT, G>(a.K, nw, a.R).total; };
+    const int per_sm = bytes(8) <= kW4Smem / 2 ? 2 : 1;
+    const int nw = per_sm == 2 ? 8 : bytes(16) <= kW4Smem ? 16 : bytes(8) <= kW4Smem ? 8 : 4;
+    const int jobs = a.ids ? a.slots : (a.rows + a.R - 1) / a.R;
+    w4_shape(&a, jobs, nw, per_sm);
+    if (const int e = limit.allow(w4_kernel<NT, RT, G, EPI>, kW4Smem)) return e;
+    w4_kernel<NT, RT, G, EPI><<<dim3((a.tiles + a.tpc - 1) / a.tpc, jobs), nw * 32, bytes(nw), st>>>(a);
+    return (int)cudaGetLastError();
+}
+// Two 8-row tiles per job where more than 8 rows can share a matrix (and, in
+// shared memory, leave room for eight warps), else one.
+template <int G, int EPI>
+int w4_launch_nt(const W4Args& a, int rows, cudaStream_t st) {
+    constexpr int RT = EPI == W4_GATED ? 2 : 1;
+    if (rows > 8 && w4_smem<2, RT, G>(a.K, 8, rows < 16 ? rows : 16).total <= kW4Smem)
+        return w4_launch<2, RT, G, EPI>(a, rows, st);
+    return w4_launch<1, RT, G, EPI>(a, rows, st);
+}
+template <int EPI>
+int w4_launch_g(int G, const W4Args& a, int rows, cudaStream_t st) {
+    return G == 32   ? w4_launch_nt<32, EPI>(a, rows, st)
+           : G == 64 ? w4_launch_nt<64, EPI>(a, rows, st)
+                     : w4_launch_nt<128, EPI>(a, rows, st);
+}
+
+}  // namespace
+
+int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q, const void* sf, void* y,
+                     cudaStream_t st) {
+    W4Args a = {};
+    a.x = static_cast<const __nv_bfloat16*>(x);
+    a.q = q;
+    a.sf = static_cast<const __nv_bfloat16*>(sf);
+    a.N = a.F = N;
+    a.K = K;
+    a.E = 1;
+    a.rows = M;
+    a.xdiv = 1;
+    a.tiles = (N + 15) / 16;
+    a.out = y;
+    return w4_launch_g<W4_PLAIN>(G, a, M, st);
+}
+
+int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
+    W4Args a = {};
+    a.x = static_cast<const __nv_bfloat16*>(w.x);
+    a.q = w.W1_q;
+    a.sf = static_cast<const __nv_bfloat16*>(w.W1_sf);
+    a.N = 2 * w.I;
+    a.F = w.I;
+    a.K = w.H;
+    a.E = w.E;
+    a.rows = w.T;
+    a.ids = w.topk_idx;
+    a.slots = w.T * w.k;
+    a.xdiv = w.topk_idx ? w.k : 1;
+    a.tiles = (w.I + 15) / 16;
+    a.out = w.act;
+    if (const int e = w4_launch_g<W4_GATED>(w.group, a, w.T, st)) return e;
+    a.x = static_cast<const __nv_bfloat16*>(w.act);
+    a.q = w.W2_q;
+    a.sf = static_cast<const __nv_bfloat16*>(w.W2_sf);
+    a.N = a.F = w.H;
+    a.K = w.I;
+    a.xdiv = 1;
+    a.tiles = (w.H + 15) / 16;
+    if (!w.topk_idx) {
+        a.out = w.y;
+        return w4_launch_g<W4_PLAIN>(w.group, a, w.T, st);
+    }
+    a.slot_w = w.topk_w;
+    a.out = w.part;
+    if (const int e = w4_launch_g<W4_SLOT>(w.group, a, w.T, st)) return e;
+    const long long blocks = ((long long)w.T * w.H / 4 + 255) / 256;
+    w4_combine_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), 256, 0, st>>>(
+        w.part, w.topk_idx, w.T, w.k, w.E, w.H, static_cast<__nv_bfloat16*>(w.y));
+    return (int)cudaGetLastError();
+}
+
+int launch_quantize_w4(int E, int K, int N, int G, const void* W, uint8_t* q, void* sf, cudaStream_t st) {
+    const dim3 grid((N + 127) / 128, K / 128, E);
+    auto* w = static_cast<const __nv_bfloat16*>(W);
+    auto* s = static_cast<__nv_bfloat16*>(sf);
+    if (G == 32)
+        w4_quantize_kernel<32><<<grid, 128, 0, st>>>(w, K, N, q, s);
+    else if (G == 64)
+        w4_quantize_kernel<64><<<grid, 128, 0, st>>>(w, K, N, q, s);
+    else
+        w4_quantize_kernel<128><<<grid, 128, 0, st>>>(w, K, N, q, s);
+    return (int)cudaGetLastError();
+}
+
+}  // namespace moe
