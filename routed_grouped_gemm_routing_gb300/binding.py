@@ -58,6 +58,8 @@ def declared_functions() -> list[str]:
 def lib():
     """The loaded library; raises if it has not been built."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _LOCK:
         if _LIB is None:
             path = _build.lib_path()
@@ -268,6 +270,25 @@ def moe_read_status(shape: MoeShape, route_ws, stream=None) -> list[int]:
 
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # MOE_BF16, MOE_F16, MOE_F32
+_BF, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+
+
+# The entry points below serve calls of a few microseconds on the GPU, so their
+# marshalling takes the checks of _ptr in one expression and leaves the message
+# to _ptr, and reads the current stream without making a Stream object.
+def _arg(t, dtype, numel, name, dev):
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+            and t.numel() >= numel):
+        return t.data_ptr()
+    return _ptr(t, dtype, numel, name)
+
+
+def _here(stream):
+    """(current device, stream pointer)."""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _type_of(t, name):
@@ -276,16 +297,18 @@ def _type_of(t, name):
     return _TYPES[t.dtype]
 
 
-def _rows_ptr(t, dtype, rows, H, name):
+def _rows_arg(t, dtype, rows, H, name, dev):
     """(pointer, row stride) of a CUDA tensor [rows, H] whose rows are contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (rows, H):
+    if t.shape != (rows, H):
         raise ValueError(f"{name} must be [{rows}, {H}], got {list(t.shape)}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.is_contiguous():
+        return t.data_ptr(), H
     if H > 1 and t.stride(1) != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
     stride = t.stride(0) if rows > 1 else H
@@ -305,48 +328,55 @@ def moe_layer_norm_forward(x, weight, bias, eps: float, y, mean, rstd, stream=No
     """y = (x - mean) * rstd * weight + bias over the last axis of x [rows, H]
     (bf16, f16 or f32; rows may be strided); weight and bias [H] in x's type
     or f32, bias may be None.  Overwrites y [rows, H], mean and rstd f32 [rows]."""
-    tx = _type_of(x, "x")
+    tx, tw = _type_of(x, "x"), _type_of(weight, "weight")
     rows, H = x.shape
-    px, sx = _rows_ptr(x, x.dtype, rows, H, "x")
-    wt = weight.dtype
-    _check(lib().moe_layer_norm_forward(
-        rows, H, tx, _type_of(weight, "weight"), px, sx, _ptr(weight, wt, H, "weight"), _ptr(bias, wt, H, "bias"), eps,
-        _ptr(y, x.dtype, rows * H, "y"), _ptr(mean, torch.float32, rows, "mean"), _ptr(rstd, torch.float32, rows, "rstd"),
-        _stream(stream)))
+    dev, st = _here(stream)
+    xt, wt = x.dtype, weight.dtype
+    px, sx = _rows_arg(x, xt, rows, H, "x", dev)
+    rc = lib().moe_layer_norm_forward(
+        rows, H, tx, tw, px, sx, _arg(weight, wt, H, "weight", dev), _arg(bias, wt, H, "bias", dev), eps,
+        _arg(y, xt, rows * H, "y", dev), _arg(mean, _F32, rows, "mean", dev), _arg(rstd, _F32, rows, "rstd", dev), st)
+    if rc:
+        _check(rc)
 
 
 def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, stream=None):
     """Backward of moe_layer_norm_forward: overwrites dx [rows, H] (x's type),
     dweight and dbias [H] (weight's type; dbias may be None).  ws: uint8 of
     moe_layer_norm_workspace(rows, H) elements."""
-    tx = _type_of(x, "x")
+    tx, tw = _type_of(x, "x"), _type_of(weight, "weight")
     rows, H = x.shape
-    px, sx = _rows_ptr(x, x.dtype, rows, H, "x")
-    pd, sd = _rows_ptr(dy, x.dtype, rows, H, "dy")
-    wt, f32 = weight.dtype, torch.float32
-    _check(lib().moe_layer_norm_backward(
-        rows, H, tx, _type_of(weight, "weight"), pd, sd, px, sx, _ptr(weight, wt, H, "weight"),
-        _ptr(mean, f32, rows, "mean"), _ptr(rstd, f32, rows, "rstd"), _ptr(dx, x.dtype, rows * H, "dx"),
-        _ptr(dweight, wt, H, "dweight"), _ptr(dbias, wt, H, "dbias"),
-        _ptr(ws, torch.uint8, moe_layer_norm_workspace(rows, H), "ws"), _stream(stream)))
+    dev, st = _here(stream)
+    xt, wt = x.dtype, weight.dtype
+    px, sx = _rows_arg(x, xt, rows, H, "x", dev)
+    pd, sd = _rows_arg(dy, xt, rows, H, "dy", dev)
+    rc = lib().moe_layer_norm_backward(
+        rows, H, tx, tw, pd, sd, px, sx, _arg(weight, wt, H, "weight", dev), _arg(mean, _F32, rows, "mean", dev),
+        _arg(rstd, _F32, rows, "rstd", dev), _arg(dx, xt, rows * H, "dx", dev), _arg(dweight, wt, H, "dweight", dev),
+        _arg(dbias, wt, H, "dbias", dev), _arg(ws, _U8, moe_layer_norm_workspace(rows, H), "ws", dev), st)
+    if rc:
+        _check(rc)
 
 
 def moe_quantize_w4(W, W_q, W_sf, group: int, stream=None):
     """W bf16 [E, K, N] -> W_q uint8 [E, N, K // 2] (4-bit codes) and W_sf bf16
     [E, N, K // group]."""
     E, K, N = W.shape
-    _check(lib().moe_quantize_w4(E, K, N, group, _ptr(W, torch.bfloat16, E * K * N, "W"),
-                                 _ptr(W_q, torch.uint8, E * N * K // 2, "W_q"),
-                                 _ptr(W_sf, torch.bfloat16, E * N * K // max(group, 1), "W_sf"), _stream(stream)))
+    dev, st = _here(stream)
+    _check(lib().moe_quantize_w4(E, K, N, group, _arg(W, _BF, E * K * N, "W", dev),
+                                 _arg(W_q, _U8, E * N * K // 2, "W_q", dev),
+                                 _arg(W_sf, _BF, E * N * K // max(group, 1), "W_sf", dev), st))
 
 
 def moe_matvec_w4(x, W_q, W_sf, y, group: int, stream=None):
     """y bf16 [M, N] = x bf16 [M, K] times the 4-bit matrix [N, K] transposed."""
     M, K = x.shape
     N = W_q.shape[0]
-    bf = torch.bfloat16
-    _check(lib().moe_matvec_w4(M, N, K, group, _ptr(x, bf, M * K, "x"), _ptr(W_q, torch.uint8, N * K // 2, "W_q"),
-                               _ptr(W_sf, bf, N * K // max(group, 1), "W_sf"), _ptr(y, bf, M * N, "y"), _stream(stream)))
+    dev, st = _here(stream)
+    rc = lib().moe_matvec_w4(M, N, K, group, _arg(x, _BF, M * K, "x", dev), _arg(W_q, _U8, N * K // 2, "W_q", dev),
+                             _arg(W_sf, _BF, N * K // max(group, 1), "W_sf", dev), _arg(y, _BF, M * N, "y", dev), st)
+    if rc:
+        _check(rc)
 
 
 def moe_w4_workspace(shape: MoeW4Shape) -> int:
@@ -360,13 +390,15 @@ def moe_forward_w4(shape: MoeW4Shape, x, W1_q, W1_sf, W2_q, W2_sf, topk_idx, top
     """The routed experts with 4-bit weights (topk_idx None: one expert, every
     token, weight 1).  ws: uint8 of moe_w4_workspace elements."""
     T, H, I, E, k, G = shape.T, shape.H, shape.I, shape.E, shape.k, max(shape.group, 1)
-    bf, u8 = torch.bfloat16, torch.uint8
-    _check(lib().moe_forward_w4(
-        ctypes.byref(shape), _ptr(x, bf, T * H, "x"), _ptr(W1_q, u8, E * I * H, "W1_q"),
-        _ptr(W1_sf, bf, E * 2 * I * H // G, "W1_sf"), _ptr(W2_q, u8, E * I * H // 2, "W2_q"),
-        _ptr(W2_sf, bf, E * I * H // G, "W2_sf"), _ptr(topk_idx, torch.int32, T * k, "topk_idx"),
-        _ptr(topk_w, torch.float32, T * k, "topk_w"), _ptr(ws, u8, moe_w4_workspace(shape), "ws"),
-        _ptr(y, bf, T * H, "y"), _stream(stream)))
+    dev, st = _here(stream)
+    rc = lib().moe_forward_w4(
+        ctypes.byref(shape), _arg(x, _BF, T * H, "x", dev), _arg(W1_q, _U8, E * I * H, "W1_q", dev),
+        _arg(W1_sf, _BF, E * 2 * I * H // G, "W1_sf", dev), _arg(W2_q, _U8, E * I * H // 2, "W2_q", dev),
+        _arg(W2_sf, _BF, E * I * H // G, "W2_sf", dev), _arg(topk_idx, _I32, T * k, "topk_idx", dev),
+        _arg(topk_w, _F32, T * k, "topk_w", dev), _arg(ws, _U8, moe_w4_workspace(shape), "ws", dev),
+        _arg(y, _BF, T * H, "y", dev), st)
+    if rc:
+        _check(rc)
 
 
 def moe_last_error() -> str:

@@ -14,21 +14,24 @@ import torch
 from . import binding as B
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(t):
     """Context in which t's device is current (the library launches there)."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise TypeError("expected CUDA tensors")
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 # -------------------------------------------------------------- layer norm
-def _norm_dims(x, weight, *others):
+def _norm_dims(x, weight, bias=None):
     if x.dim() != 2:
         raise ValueError("expected x [rows, H]")
     rows, H = x.shape
-    for t in (weight,) + others:
-        if t is not None and tuple(t.shape) != (H,):
-            raise ValueError(f"expected weight and bias [{H}], got {list(t.shape)}")
+    if weight.shape != (H,) or (bias is not None and bias.shape != (H,)):
+        raise ValueError(f"expected weight and bias [{H}]")
     return rows, H
 
 
@@ -38,9 +41,10 @@ def layer_norm_forward(x, weight, bias=None, eps: float = 1e-5):
     weight and bias [H] in x's type or f32."""
     rows, H = _norm_dims(x, weight, bias)
     with _on(x):
-        y = torch.empty((rows, H), dtype=x.dtype, device=x.device)
-        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
-        mean, rstd = stats[0], stats[1]
+        dev = x.device
+        y = torch.empty((rows, H), dtype=x.dtype, device=dev)
+        mean = torch.empty((rows,), dtype=torch.float32, device=dev)
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
         B.moe_layer_norm_forward(x, weight, bias, eps, y, mean, rstd)
     return y, mean, rstd
 
@@ -50,10 +54,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True):
     dweight and dbias have weight's type."""
     rows, H = _norm_dims(x, weight)
     with _on(x):
-        dx = torch.empty((rows, H), dtype=x.dtype, device=x.device)
-        dw = torch.empty((H,), dtype=weight.dtype, device=x.device)
-        db = torch.empty_like(dw) if bias else None
-        ws = torch.empty((max(B.moe_layer_norm_workspace(rows, H), 4),), dtype=torch.uint8, device=x.device)
+        dev = x.device
+        dx = torch.empty((rows, H), dtype=x.dtype, device=dev)
+        dw = torch.empty((H,), dtype=weight.dtype, device=dev)
+        db = torch.empty((H,), dtype=weight.dtype, device=dev) if bias else None
+        ws = torch.empty((max(B.moe_layer_norm_workspace(rows, H), 4),), dtype=torch.uint8, device=dev)
         B.moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, ws)
     return dx, dw, db
 
@@ -174,10 +179,12 @@ class W4Experts:
             k = 1
         else:
             k = topk_idx.shape[1]
-            if tuple(topk_idx.shape) != (T, k) or topk_w is None or tuple(topk_w.shape) != (T, k):
+            if topk_idx.shape != (T, k) or topk_w is None or topk_w.shape != (T, k):
                 raise ValueError("expected topk_idx and topk_w [T, k]")
-            topk_idx = topk_idx.to(torch.int32).contiguous()
-            topk_w = topk_w.to(torch.float32).contiguous()
+            if topk_idx.dtype is not torch.int32 or not topk_idx.is_contiguous():
+                topk_idx = topk_idx.to(torch.int32).contiguous()
+            if topk_w.dtype is not torch.float32 or not topk_w.is_contiguous():
+                topk_w = topk_w.to(torch.float32).contiguous()
         s = B.MoeW4Shape(T, H, self.I, self.E, k, self.group)
         with _on(x):
             ws = torch.empty((max(B.moe_w4_workspace(s), 16),), dtype=torch.uint8, device=x.device)

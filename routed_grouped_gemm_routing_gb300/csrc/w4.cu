@@ -22,7 +22,7 @@
 // that lane t's pair m of group j meets x[32 j + 8 t + 2 m, + 1].
 //
 // A block takes a job (up to 8 NT rows that use the same matrix) and a range
-// of 16-row tiles; KS of its warps share a tile, every KS-th 128-code block
+// of tiles of 32 rows of W (W4_GATED: 16 gate rows and their 16 up rows); KS of its warps share a tile, every KS-th 128-code block
 // each, and join their FP32 sums in shared memory in a fixed order.  Every lane
 // copies its own weights several blocks ahead with cp.async into its own slots
 // (no barrier in the stream), across the tiles of its range.
@@ -34,8 +34,8 @@ namespace moe {
 
 namespace {
 
-// 128-code blocks held or in flight per warp, by 16-row fragments of a tile
-__host__ __device__ constexpr int w4_depth(int rt) { return rt == 2 ? 3 : 4; }
+constexpr int kDepth = 3;  // 128-code blocks held or in flight per warp
+constexpr int kFrag = 4;    // 8-row fragments of a tile: two 16-row operands of the products
 
 enum W4Epi { W4_PLAIN, W4_GATED, W4_SLOT };
 
@@ -50,10 +50,11 @@ struct W4Args {
     const int32_t* ids;  // expert of each slot, or null: one matrix, rows of x in order
     int slots;   // length of ids
     int xdiv;    // x row of a slot = slot / xdiv
-    int tiles;   // ceil(F / 16)
+    int tiles;   // ceil(F / 32), W4_GATED: ceil(F / 16)
     int tpc;     // tiles per block
     int ks;      // warps per tile
     int R;       // rows of a job
+    uint32_t mask;  // 0x000f000f, unknown to the compiler (see pair128)
     const float* slot_w;  // W4_SLOT: weight of each slot
     void* out;   // W4_PLAIN, W4_GATED: bf16 [row or slot][F]; W4_SLOT: f32 [slot][F]
 };
@@ -65,10 +66,14 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// codes 2 m and 2 m + 1 of a word as the bf16 pair 128 + code
+// Codes 2 m and 2 m + 1 of a word as the bf16 pair 128 + code.  mask is
+// 0x000f000f in a register: with both constants immediate this takes two
+// logic instructions instead of one, and they bound these kernels.
 template <int m>
-__device__ __forceinline__ uint32_t pair128(uint32_t w) {
-    return ((w >> (4 * m)) & 0x000f000fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t pair128(uint32_t w, uint32_t mask) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, 0x43004300, 0xEA;" : "=r"(r) : "r"(w >> (4 * m)), "r"(mask));
+    return r;
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
     return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
@@ -78,7 +83,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
 struct W4Smem {
     int x, xs, ring, sring, red, total;
 };
-template <int NT, int RT, int G>
+template <int NT, int G>
 __host__ __device__ __forceinline__ W4Smem w4_smem(int K, int nw, int rows) {
     W4Smem s;
     s.x = 0;
@@ -86,21 +91,19 @@ __host__ __device__ __forceinline__ W4Smem w4_smem(int K, int nw, int rows) {
     const int xbytes = rows * (2 * K + 64);
     s.xs = xbytes;
     s.ring = (s.xs + (K / G) * 8 * NT * 4 + 15) / 16 * 16;
-    constexpr int kDepth = w4_depth(RT);
-    s.sring = s.ring + nw * kDepth * RT * 2 * 32 * 16;
-    s.red = s.sring + nw * kDepth * RT * 2 * 32 * (G == 32 ? 8 : 4);
-    s.total = s.red + 2 * nw * RT * NT * 128 * 4;
+    s.sring = s.ring + nw * kDepth * kFrag * 32 * 16;
+    s.red = s.sring + nw * kDepth * kFrag * 32 * (G == 32 ? 8 : 4);
+    s.total = s.red + 2 * nw * 2 * NT * 128 * 4;
     return s;
 }
 
-template <int NT, int RT, int G, int EPI>
+template <int NT, int G, int EPI>
 __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
     constexpr int kR = 8 * NT;
     const int R = p.R;  // rows of a job, at most kR
-    constexpr int kDepth = w4_depth(RT);
     constexpr int kSpb = 128 / G;        // scales per 128-code block
     constexpr int kSBytes = G == 32 ? 8 : 4;
-    static_assert(RT == (EPI == W4_GATED ? 2 : 1), "a gated tile is 16 gate and 16 up rows");
+    constexpr int kTile = EPI == W4_GATED ? 16 : 32;  // output features of a tile
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int row_of[kR];  // row or slot of every row of the job
     __shared__ int job_n;
@@ -138,53 +141,69 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
     const int n = job_n;
     if (n == 0) return;  // not the leading slot
 
-    const W4Smem L = w4_smem<NT, RT, G>(K, nw, n);
+    const W4Smem L = w4_smem<NT, G>(K, nw, n);
     __nv_bfloat16* xsm = reinterpret_cast<__nv_bfloat16*>(smem + L.x);
     float* xs = reinterpret_cast<float*>(smem + L.xs);  // [K / G][kR]: -136 sum of x
-    const uint4* ring = reinterpret_cast<const uint4*>(smem + L.ring) + warp * kDepth * RT * 2 * 32;
-    const uint8_t* sring = smem + L.sring + warp * kDepth * RT * 2 * 32 * kSBytes;
+    const uint4* ring = reinterpret_cast<const uint4*>(smem + L.ring) + warp * kDepth * kFrag * 32 + lane;
+    const uint8_t* sring = smem + L.sring + (warp * kDepth * kFrag * 32 + lane) * kSBytes;
     float* red = reinterpret_cast<float*>(smem + L.red);
 
     // ---- the stream of this lane's weights: tiles gi, gi + NG, .. of the
     // block's range, blocks ks, ks + KS, .. of each
     const int tile0 = blockIdx.x * p.tpc;
     const int tile1 = tile0 + p.tpc < p.tiles ? tile0 + p.tpc : p.tiles;
-    const uint8_t* q = p.q + (size_t)e * p.N * (K / 2);
-    const __nv_bfloat16* sf = p.sf + (size_t)e * p.N * (K / G);
-    int ft = tile0 + gi, fb = ks, fslot = 0;
-    auto row_index = [&](int tile, int i) {  // row of W of this lane's i-th fragment: clamped, not stored when past F
-        const int f = tile * 16 + g + 8 * (i & 1);
-        return (f < p.F ? f : p.F - 1) + (i >> 1) * p.F;
+    // Feature and row of this lane's i-th fragment.  A row past the last is
+    // read as the last and not stored.
+    auto row_index = [&](int tile, int i) {
+        const int f = tile * kTile + g + 8 * (EPI == W4_GATED ? i & 1 : i);
+        return (f < p.F ? f : p.F - 1) + (EPI == W4_GATED ? (i >> 1) * p.F : 0);
     };
+    // One scale per block (G = 128) comes as the aligned pair that holds it;
+    // odd: the matrix starts at the second of a pair.
+    const size_t sf0 = (size_t)e * p.N * (K / G);
+    const uint32_t odd = G == 128 ? (uint32_t)(sf0 & 1) : 0u;
+    const uint4* q = reinterpret_cast<const uint4*>(p.q) + (size_t)e * p.N * (K / 32) + t;
+    const __nv_bfloat16* sf = p.sf + sf0 - odd;
+    // the last scale of all, where it is the first of a pair whose second does not exist
+    const uint32_t lone = e == p.E - 1 ? (uint32_t)(p.N * KB - 1) + odd : 0xffffffffu;
+    const uint32_t ring_s = smem_addr(ring), sring_s = smem_addr(sring);
+    int ft = tile0 + gi, fb = ks, fslot = 0;
+    uint32_t qo[kFrag], so[kFrag];  // offsets of the next block: 16-byte units, scales
+    auto start_tile = [&]() {
+#pragma unroll
+        for (int i = 0; i < kFrag; ++i) {
+            const uint32_t row = (uint32_t)row_index(ft, i);
+            qo[i] = row * (uint32_t)(K / 32) + 4 * ks;
+            so[i] = row * (uint32_t)(K / G) + kSpb * ks + odd;
+        }
+    };
+    start_tile();
     auto fetch = [&]() {
         if (ft < tile1 && fb < KB) {
 #pragma unroll
-            for (int i = 0; i < RT * 2; ++i) {
-                const size_t row = (size_t)row_index(ft, i);
-                cp_async_16(smem_addr(ring + (fslot * RT * 2 + i) * 32 + lane), q + row * (K / 2) + fb * 64 + t * 16,
-                            16u);
-                const uint32_t sdst = smem_addr(sring + ((fslot * RT * 2 + i) * 32 + lane) * kSBytes);
-                const __nv_bfloat16* sp = sf + row * (K / G) + fb * kSpb;
+            for (int i = 0; i < kFrag; ++i) {
+                const uint32_t at = (uint32_t)(fslot * kFrag + i) * 32u;
+                cp_async_16(ring_s + at * 16u, q + qo[i], 16u);
+                const uint32_t sdst = sring_s + at * kSBytes;
                 if constexpr (G == 32) {
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(sdst), "l"(sp) : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(sdst), "l"(sf + so[i]) : "memory");
                 } else if constexpr (G == 64) {
-                    cp_async_4(sdst, sp, 4u);
+                    cp_async_4(sdst, sf + so[i], 4u);
                 } else {
-                    // one scale: the aligned word that holds it (of which an
-                    // even last scale has only its own two bytes)
-                    const size_t idx = (size_t)(sp - p.sf);
-                    const bool last = idx + 1 == (size_t)p.E * p.N * (K / G);
-                    cp_async_4(sdst, p.sf + (idx & ~(size_t)1), last && !(idx & 1) ? 2u : 4u);
+                    cp_async_4(sdst, sf + (so[i] & ~1u), so[i] == lone && !(lone & 1u) ? 2u : 4u);
                 }
+                qo[i] += 4 * KS;
+                so[i] += kSpb * KS;
             }
             fb += KS;
             if (fb >= KB) {
                 fb = ks;
                 ft += NG;
+                start_tile();
             }
         }
         cp_async_commit();
-        fslot = (fslot + 1) % kDepth;
+        fslot = fslot + 1 == kDepth ? 0 : fslot + 1;
     };
 #pragma unroll
     for (int d = 0; d < kDepth - 1; ++d) fetch();
@@ -225,37 +244,53 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
         }
     };
 
+    const uint32_t mask = p.mask;
     int slot = 0, buf = 0;
     for (int tile = tile0 + gi; tile < tile1; tile += NG) {
-        float acc[RT][NT][4];
+        float acc[2][NT][4];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.0f;
+        // G = 128: byte selectors that move the block's scale of the pair to the high half
+        uint32_t sel[kFrag];
+        if constexpr (G == 128) {
+#pragma unroll
+            for (int i = 0; i < kFrag; ++i)
+                sel[i] = ((uint32_t)row_index(tile, i) * KB + ks + odd) & 1u ? 0x3244u : 0x1044u;
+        }
         for (int kb = ks; kb < KB; kb += KS) {
             cp_async_wait_group<kDepth - 2>();
-            uint4 w[RT * 2];
-            float sc[RT * 2][kSpb];
+            uint4 w[kFrag];
+            float sc[kFrag][kSpb];
 #pragma unroll
-            for (int i = 0; i < RT * 2; ++i) {
-                w[i] = ring[(slot * RT * 2 + i) * 32 + lane];
-                const uint32_t* s = reinterpret_cast<const uint32_t*>(sring + ((slot * RT * 2 + i) * 32 + lane) * kSBytes);
+            for (int i = 0; i < kFrag; ++i) {
+                w[i] = ring[(slot * kFrag + i) * 32];
+                const uint8_t* s = sring + (slot * kFrag + i) * 32 * kSBytes;
                 if constexpr (G == 128) {
-                    const uint32_t odd = (uint32_t)(((size_t)e * p.N + row_index(tile, i)) * KB + kb) & 1u;
-                    sc[i][0] = __uint_as_float(odd ? s[0] & 0xffff0000u : s[0] << 16);
+                    sc[i][0] = __uint_as_float(__byte_perm(*reinterpret_cast<const uint32_t*>(s), 0u, sel[i]));
+                    if (KS & 1) sel[i] ^= 0x2200u;  // 0x3244 <-> 0x1044
                 } else {
+                    uint32_t u[kSpb / 2];
+                    if constexpr (G == 32) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(s);
+                        u[0] = v.x;
+                        u[1] = v.y;
+                    } else {
+                        u[0] = *reinterpret_cast<const uint32_t*>(s);
+                    }
 #pragma unroll
                     for (int h = 0; h < kSpb / 2; ++h) {
-                        sc[i][2 * h] = __uint_as_float(s[h] << 16);
-                        sc[i][2 * h + 1] = __uint_as_float(s[h] & 0xffff0000u);
+                        sc[i][2 * h] = __uint_as_float(u[h] << 16);
+                        sc[i][2 * h + 1] = __uint_as_float(u[h] & 0xffff0000u);
                     }
                 }
             }
             fetch();
-            slot = (slot + 1) % kDepth;
-            float c[RT][NT][4];
+            slot = slot + 1 == kDepth ? 0 : slot + 1;
+            float c[2][NT][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (j % (G / 32) == 0) {
@@ -264,7 +299,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
                     for (int nt = 0; nt < NT; ++nt) {
                         const float2 v = *reinterpret_cast<const float2*>(xg + 8 * nt);
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
+                        for (int rt = 0; rt < 2; ++rt) {
                             c[rt][nt][0] = c[rt][nt][2] = v.x;
                             c[rt][nt][1] = c[rt][nt][3] = v.y;
                         }
@@ -274,10 +309,12 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) b[nt] = xrow[nt][kb * 16 + j * 4];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
+                for (int rt = 0; rt < 2; ++rt) {
                     const uint32_t u = word_of(w[2 * rt], j), v = word_of(w[2 * rt + 1], j);
-                    const uint32_t u0 = pair128<0>(u), u1 = pair128<1>(u), u2 = pair128<2>(u), u3 = pair128<3>(u);
-                    const uint32_t v0 = pair128<0>(v), v1 = pair128<1>(v), v2 = pair128<2>(v), v3 = pair128<3>(v);
+                    const uint32_t u0 = pair128<0>(u, mask), u1 = pair128<1>(u, mask), u2 = pair128<2>(u, mask),
+                                   u3 = pair128<3>(u, mask);
+                    const uint32_t v0 = pair128<0>(v, mask), v1 = pair128<1>(v, mask), v2 = pair128<2>(v, mask),
+                                   v3 = pair128<3>(v, mask);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         mma_bf16(c[rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y);
@@ -287,7 +324,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
                 if ((j + 1) % (G / 32) == 0) {
                     const int si = j / (G / 32);
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
+                    for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             acc[rt][nt][0] = fmaf(sc[2 * rt][si], c[rt][nt][0], acc[rt][nt][0]);
@@ -298,31 +335,36 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
                 }
             }
         }
-        // register i of lane (g, t) of tile nt: feature g + 8 (i / 2), row 8 nt + 2 t + i % 2
+        // register i of lane (g, t) of operand rt and 8-row tile nt: row
+        // 16 rt + g + 8 (i / 2) of the tile, row 8 nt + 2 t + i % 2 of the job
+        auto put = [&](int u, float v0, float v1) {  // u = 4 nt + i
+            const int f = tile * kTile + g + 8 * ((u & 3) >> 1), r = 8 * (u >> 2) + 2 * t + (u & 1);
+            if constexpr (EPI == W4_GATED) {
+                emit(f, r, v0, v1);
+            } else {
+                emit(f, r, v0, 0.0f);
+                emit(f + 16, r, v1, 0.0f);
+            }
+        };
         if (KS == 1) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    emit(tile * 16 + g + 8 * (i >> 1), 8 * nt + 2 * t + (i & 1), acc[0][nt][i], acc[RT - 1][nt][i]);
+            for (int u = 0; u < 4 * NT; ++u) put(u, acc[0][u >> 2][u & 3], acc[1][u >> 2][u & 3]);
         } else {
-            constexpr int kPer = RT * NT * 128;  // floats of a warp
-            float* mine = red + (size_t)(buf * nw + warp) * kPer;
+            constexpr int kPer = 2 * NT * 128;  // floats of a warp
+            float* mine = red + (size_t)(buf * nw + warp) * kPer + lane;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mine[((rt * NT + nt) * 4 + i) * 32 + lane] = acc[rt][nt][i];
+                for (int u = 0; u < 4 * NT; ++u) mine[(rt * NT * 4 + u) * 32] = acc[rt][u >> 2][u & 3];
             asm volatile("bar.sync %0, %1;" ::"r"(gi + 1), "r"(KS * 32) : "memory");
-            const float* all = red + (size_t)(buf * nw + gi * KS) * kPer;
+            const float* all = red + (size_t)(buf * nw + gi * KS) * kPer + lane;
             for (int u = ks; u < NT * 4; u += KS) {
-                float v = 0.0f, up = 0.0f;
+                float v0 = 0.0f, v1 = 0.0f;
                 for (int k = 0; k < KS; ++k) {
-                    v += all[k * kPer + u * 32 + lane];
-                    if constexpr (RT == 2) up += all[k * kPer + (NT * 4 + u) * 32 + lane];
+                    v0 += all[k * kPer + u * 32];
+                    v1 += all[k * kPer + (NT * 4 + u) * 32];
                 }
-                emit(tile * 16 + g + 8 * ((u & 3) >> 1), 8 * (u >> 2) + 2 * t + (u & 1), v, up);
+                put(u, v0, v1);
             }
             buf ^= 1;  // the next tile's sums go to the other half: two tiles on, this barrier has passed
         }
@@ -422,29 +464,29 @@ void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
 
 // rows: rows that can share a job; groups of rows (no ids) or slots (ids) are
 // the jobs.
-template <int NT, int RT, int G, int EPI>
+template <int NT, int G, int EPI>
 int w4_launch(W4Args a, int rows, cudaStream_t st) {
     static SmemLimit limit;
+    a.mask = 0x000f000fu;
     // as many rows per job as leave room for a block of four warps
     a.R = rows < 8 * NT ? rows : 8 * NT;
-    while (a.R > 1 && w4_smem<NT, RT, G>(a.K, 4, a.R).total > kW4Smem) --a.R;
-    auto bytes = [&](int nw) { return w4_smem<NT, RT, G>(a.K, nw, a.R).total; };
+    while (a.R > 1 && w4_smem<NT, G>(a.K, 4, a.R).total > kW4Smem) --a.R;
+    auto bytes = [&](int nw) { return w4_smem<NT, G>(a.K, nw, a.R).total; };
     const int per_sm = bytes(8) <= kW4Smem / 2 ? 2 : 1;
     const int nw = per_sm == 2 ? 8 : bytes(16) <= kW4Smem ? 16 : bytes(8) <= kW4Smem ? 8 : 4;
     const int jobs = a.ids ? a.slots : (a.rows + a.R - 1) / a.R;
     w4_shape(&a, jobs, nw, per_sm);
-    if (const int e = limit.allow(w4_kernel<NT, RT, G, EPI>, kW4Smem)) return e;
-    w4_kernel<NT, RT, G, EPI><<<dim3((a.tiles + a.tpc - 1) / a.tpc, jobs), nw * 32, bytes(nw), st>>>(a);
+    if (const int e = limit.allow(w4_kernel<NT, G, EPI>, kW4Smem)) return e;
+    w4_kernel<NT, G, EPI><<<dim3((a.tiles + a.tpc - 1) / a.tpc, jobs), nw * 32, bytes(nw), st>>>(a);
     return (int)cudaGetLastError();
 }
 // Two 8-row tiles per job where more than 8 rows can share a matrix (and, in
 // shared memory, leave room for eight warps), else one.
 template <int G, int EPI>
 int w4_launch_nt(const W4Args& a, int rows, cudaStream_t st) {
-    constexpr int RT = EPI == W4_GATED ? 2 : 1;
-    if (rows > 8 && w4_smem<2, RT, G>(a.K, 8, rows < 16 ? rows : 16).total <= kW4Smem)
-        return w4_launch<2, RT, G, EPI>(a, rows, st);
-    return w4_launch<1, RT, G, EPI>(a, rows, st);
+    if (rows > 8 && w4_smem<2, G>(a.K, 8, rows < 16 ? rows : 16).total <= kW4Smem)
+        return w4_launch<2, G, EPI>(a, rows, st);
+    return w4_launch<1, G, EPI>(a, rows, st);
 }
 template <int EPI>
 int w4_launch_g(int G, const W4Args& a, int rows, cudaStream_t st) {
@@ -466,7 +508,7 @@ int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q
     a.E = 1;
     a.rows = M;
     a.xdiv = 1;
-    a.tiles = (N + 15) / 16;
+    a.tiles = (N + 31) / 32;
     a.out = y;
     return w4_launch_g<W4_PLAIN>(G, a, M, st);
 }
@@ -493,7 +535,7 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     a.N = a.F = w.H;
     a.K = w.I;
     a.xdiv = 1;
-    a.tiles = (w.H + 15) / 16;
+    a.tiles = (w.H + 31) / 32;
     if (!w.topk_idx) {
         a.out = w.y;
         return w4_launch_g<W4_PLAIN>(w.group, a, w.T, st);
