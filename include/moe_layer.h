@@ -359,6 +359,48 @@ int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_t
                             const float* mean, const float* rstd, void* dx, void* dweight, void* dbias, void* ws,
                             void* stream);
 
+/* The dense gated feed-forward block, beside the routed experts (a shared
+ * expert) or in a layer without them: for x bf16 [T, H], W1 bf16 [H, 2I]
+ * (columns [0, I) gate, [I, 2I) up) and W2 bf16 [I, H]
+ *     h = x W1,  a = silu(h[:I]) h[I:],  y = a W2
+ * with moe_shape's activation_clamp on both inputs of the activation.  T >= 0
+ * tokens, H and I multiples of 8; all pointers 16-byte aligned, tensors
+ * contiguous. */
+typedef struct moe_ffn_shape {
+    int32_t T, H, I;
+    float activation_clamp;
+} moe_ffn_shape;
+
+/* Byte offsets in the two caller-owned buffers.
+ *  saved (written by moe_ffn_forward, read by moe_ffn_backward):
+ *    a  bf16[T, I]     activation (an operand of y and dW2, rounded once)
+ *    h  f32[T, 2I]     only with for_backward; without it the first h bytes do
+ *  ws (scratch of both calls; calls that share one must not overlap):
+ *    status int32[4]   the caller zeroes word 0 once; bit 0 is set when a
+ *                      kernel gave up on a bounded wait, and stays set
+ *    dh     bf16[T, 2I]
+ *    part   f32        partial sums of the products split over K (few tokens) */
+typedef struct moe_ffn_layout {
+    size_t saved_bytes, a, h;
+    size_t ws_bytes, status, dh, part;
+} moe_ffn_layout;
+
+/* Sizes and offsets for `shape`.  Host only. */
+int moe_ffn_workspace_layout(const moe_ffn_shape* shape, moe_ffn_layout* out);
+
+/* Forward: overwrites y bf16 [T, H] and saved.  for_backward 0 leaves h out of
+ * saved (inference).  Products are bf16 with FP32 accumulation; a and y are
+ * rounded once.  Deterministic. */
+int moe_ffn_forward(const moe_ffn_shape* shape, const void* x, const void* W1, const void* W2, int32_t for_backward,
+                    void* saved, void* ws, void* y, void* stream);
+
+/* Backward of moe_ffn_forward (for_backward 1) given dY bf16 [T, H]:
+ * overwrites dx bf16 [T, H], dW1 bf16 [H, 2I] and dW2 bf16 [I, H] (T = 0: the
+ * weight gradients become 0).  dh is rounded to bf16 once (an operand of dx
+ * and dW1).  Deterministic. */
+int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, const void* W1, const void* W2,
+                     const void* saved, void* ws, void* dx, void* dW1, void* dW2, void* stream);
+
 /* 4-bit weights with one scale per group, for serving a few rows at a time
  * (decoding).  A matrix W [N, K] (y = x W^T) is held as
  *     W[n, k] = (code[n, k] - 8) * sf[n, k / group],   code in [0, 15],

@@ -43,6 +43,14 @@ class MoeW4Shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I", "E", "k", "group")]
 
 
+class MoeFFNShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I")] + [("activation_clamp", ctypes.c_float)]
+
+
+class MoeFFNLayout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("saved_bytes", "a", "h", "ws_bytes", "status", "dh", "part")]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe error {code}: {msg}")
@@ -92,7 +100,11 @@ def lib():
             L.moe_matvec_w4.argtypes = [i32] * 4 + [vp] * 5
             L.moe_w4_workspace.argtypes = [P(MoeW4Shape), P(ctypes.c_size_t)]
             L.moe_forward_w4.argtypes = [P(MoeW4Shape)] + [vp] * 10
-            for n in ("moe_layer_norm_forward", "moe_layer_norm_workspace", "moe_layer_norm_backward",
+            L.moe_ffn_workspace_layout.argtypes = [P(MoeFFNShape), P(MoeFFNLayout)]
+            L.moe_ffn_forward.argtypes = [P(MoeFFNShape), vp, vp, vp, i32, vp, vp, vp, vp]
+            L.moe_ffn_backward.argtypes = [P(MoeFFNShape)] + [vp] * 10
+            for n in ("moe_ffn_workspace_layout", "moe_ffn_forward", "moe_ffn_backward",
+                      "moe_layer_norm_forward", "moe_layer_norm_workspace", "moe_layer_norm_backward",
                       "moe_quantize_w4", "moe_matvec_w4", "moe_w4_workspace", "moe_forward_w4"):
                 getattr(L, n).restype = ctypes.c_int
             L.moe_trace_begin.argtypes = [vp, ctypes.c_int]
@@ -397,6 +409,41 @@ def moe_forward_w4(shape: MoeW4Shape, x, W1_q, W1_sf, W2_q, W2_sf, topk_idx, top
         _arg(W2_sf, _BF, E * I * H // G, "W2_sf", dev), _arg(topk_idx, _I32, T * k, "topk_idx", dev),
         _arg(topk_w, _F32, T * k, "topk_w", dev), _arg(ws, _U8, moe_w4_workspace(shape), "ws", dev),
         _arg(y, _BF, T * H, "y", dev), st)
+    if rc:
+        _check(rc)
+
+
+def moe_ffn_workspace_layout(shape: MoeFFNShape) -> MoeFFNLayout:
+    out = MoeFFNLayout()
+    _check(lib().moe_ffn_workspace_layout(ctypes.byref(shape), ctypes.byref(out)))
+    return out
+
+
+def moe_ffn_forward(shape: MoeFFNShape, x, W1, W2, saved, ws, y, for_backward: bool = True, stream=None, layout=None):
+    """y bf16 [T, H] of the dense gated feed-forward block; saved and ws: uint8
+    of moe_ffn_workspace_layout's sizes (saved without for_backward: h bytes)."""
+    L = moe_ffn_workspace_layout(shape) if layout is None else layout
+    T, H, I = shape.T, shape.H, shape.I
+    dev, st = _here(stream)
+    rc = lib().moe_ffn_forward(
+        ctypes.byref(shape), _arg(x, _BF, T * H, "x", dev), _arg(W1, _BF, H * 2 * I, "W1", dev),
+        _arg(W2, _BF, I * H, "W2", dev), int(for_backward),
+        _arg(saved, _U8, L.saved_bytes if for_backward else L.h, "saved", dev), _arg(ws, _U8, L.ws_bytes, "ws", dev),
+        _arg(y, _BF, T * H, "y", dev), st)
+    if rc:
+        _check(rc)
+
+
+def moe_ffn_backward(shape: MoeFFNShape, dY, x, W1, W2, saved, ws, dx, dW1, dW2, stream=None, layout=None):
+    """Backward of moe_ffn_forward: overwrites dx, dW1 and dW2 (bf16)."""
+    L = moe_ffn_workspace_layout(shape) if layout is None else layout
+    T, H, I = shape.T, shape.H, shape.I
+    dev, st = _here(stream)
+    rc = lib().moe_ffn_backward(
+        ctypes.byref(shape), _arg(dY, _BF, T * H, "dY", dev), _arg(x, _BF, T * H, "x", dev),
+        _arg(W1, _BF, H * 2 * I, "W1", dev), _arg(W2, _BF, I * H, "W2", dev),
+        _arg(saved, _U8, L.saved_bytes, "saved", dev), _arg(ws, _U8, L.ws_bytes, "ws", dev),
+        _arg(dx, _BF, T * H, "dx", dev), _arg(dW1, _BF, H * 2 * I, "dW1", dev), _arg(dW2, _BF, I * H, "dW2", dev), st)
     if rc:
         _check(rc)
 

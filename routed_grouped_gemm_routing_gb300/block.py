@@ -93,6 +93,95 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5):
     return LayerNormFunction.apply(x, weight, bias, float(eps))
 
 
+# ------------------------------------------- dense gated feed-forward block
+class FFNWorkspace:
+    """Device buffers of one block shape, kept from step to step: what the
+    forward saves for its backward (the activation and, with ``train``, h) and
+    scratch.  ``generation`` counts the forwards that wrote into it: a backward
+    raises if another forward has overwritten the workspace since its own."""
+
+    def __init__(self, T: int, H: int, I: int, device=None, activation_clamp: float = 0.0, train: bool = True):
+        self.shape = B.MoeFFNShape(T, H, I, activation_clamp)
+        self.layout = L = B.moe_ffn_workspace_layout(self.shape)
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.train = train
+        self.saved = torch.empty(max(L.saved_bytes if train else L.h, 16), dtype=torch.uint8, device=dev)
+        self.ws = torch.empty(L.ws_bytes, dtype=torch.uint8, device=dev)
+        self.ws[:16].zero_()
+        self.device = dev
+        self.generation = 0
+
+    def status(self) -> int:
+        """The status word (synchronises): nonzero when a kernel gave up on a bounded wait."""
+        return int(self.ws[:4].view(torch.int32).item())
+
+
+def _ffn_check(x, W1, W2, ws):
+    s = ws.shape
+    T, H, I = s.T, s.H, s.I
+    if x.shape != (T, H) or W1.shape != (H, 2 * I) or W2.shape != (I, H):
+        raise ValueError(f"expected x [{T}, {H}], W1 [{H}, {2 * I}], W2 [{I}, {H}] for this workspace")
+
+
+def ffn_forward(x, W1, W2, ws: FFNWorkspace):
+    """y bf16 [T, H] = (silu(x W1[:, :I]) * (x W1[:, I:])) W2 for contiguous
+    bf16 x [T, H], W1 [H, 2I] (gate | up), W2 [I, H]."""
+    _ffn_check(x, W1, W2, ws)
+    with _on(x):
+        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        B.moe_ffn_forward(ws.shape, x, W1, W2, ws.saved, ws.ws, y, ws.train, layout=ws.layout)
+    ws.generation += 1
+    return y
+
+
+def ffn_backward(dy, x, W1, W2, ws: FFNWorkspace):
+    """(dx, dW1, dW2) bf16 for dy [T, H], after ffn_forward on the same inputs
+    and workspace."""
+    _ffn_check(x, W1, W2, ws)
+    if not ws.train:
+        raise ValueError("the workspace was made without train")
+    if dy.shape != x.shape:
+        raise ValueError("dy must have x's shape")
+    with _on(x):
+        dx, dW1, dW2 = (torch.empty(t.shape, dtype=torch.bfloat16, device=x.device) for t in (x, W1, W2))
+        B.moe_ffn_backward(ws.shape, dy, x, W1, W2, ws.saved, ws.ws, dx, dW1, dW2, layout=ws.layout)
+    return dx, dW1, dW2
+
+
+class GatedFFNFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W1, W2, ws, activation_clamp):
+        H, I = x.shape[-1], W2.shape[0]
+        x2 = x.reshape(-1, H).contiguous()
+        W1, W2 = W1.contiguous(), W2.contiguous()
+        s = (x2.shape[0], H, I)
+        if ws is None or (ws.shape.T, ws.shape.H, ws.shape.I) != s or not ws.train:
+            ws = FFNWorkspace(*s, device=x.device, activation_clamp=activation_clamp)
+        ws.shape.activation_clamp = activation_clamp
+        y = ffn_forward(x2, W1, W2, ws)
+        ctx.save_for_backward(x2, W1, W2)
+        ctx.ws, ctx.ws_generation, ctx.clamp = ws, ws.generation, activation_clamp
+        return y.view(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2, W1, W2 = ctx.saved_tensors
+        ws = ctx.ws
+        if ws.generation != ctx.ws_generation:
+            raise RuntimeError("gated_ffn backward: its workspace was overwritten by a later forward; give forwards "
+                               "whose backwards are still pending workspaces of their own")
+        ws.shape.activation_clamp = ctx.clamp
+        dx, dW1, dW2 = ffn_backward(dy.to(torch.bfloat16).reshape(x2.shape).contiguous(), x2, W1, W2, ws)
+        return dx.view(dy.shape), dW1, dW2, None, None
+
+
+def gated_ffn(x, W1, W2, workspace: FFNWorkspace | None = None, activation_clamp: float = 0.0):
+    """The dense gated feed-forward block (a shared expert): bf16 x [..., H],
+    W1 [H, 2I] (gate | up), W2 [I, H]; H and I multiples of 8.  Differentiable
+    in all three.  activation_clamp as in ``layer.moe_layer``."""
+    return GatedFFNFunction.apply(x, W1, W2, workspace, float(activation_clamp))
+
+
 # ---------------------------------------------------------- 4-bit weights
 def quantize_w4(W, group: int = 128):
     """(codes, scales) of W bf16 [K, N] or [E, K, N] (the layout of the layer's

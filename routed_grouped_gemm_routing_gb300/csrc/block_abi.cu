@@ -40,6 +40,16 @@ int check_w4(const moe_w4_shape* s) {
     if ((long long)s->T * s->k > 65535) return abi_fail(MOE_EUNSUPPORTED, "T*k must be <= 65535");
     return check_group(s->group);
 }
+int check_ffn(const moe_ffn_shape* s) {
+    if (!s) return abi_fail(MOE_EINVAL, "shape is NULL");
+    if (s->T < 0) return abi_fail(MOE_EINVAL, "T must be >= 0");
+    if (s->H <= 0 || s->I <= 0) return abi_fail(MOE_EINVAL, "H and I must be > 0");
+    if (s->H % 8 || s->I % 8) return abi_fail(MOE_EUNSUPPORTED, "H and I must be multiples of 8");
+    if (s->T > (1 << 30) || s->H > (1 << 20) || s->I > (1 << 20))
+        return abi_fail(MOE_EUNSUPPORTED, "T must be <= 2^30, H and I <= 2^20");
+    if (!std::isfinite(s->activation_clamp)) return abi_fail(MOE_EINVAL, "activation_clamp must be finite");
+    return MOE_OK;
+}
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
@@ -179,6 +189,82 @@ int moe_quantize_w4(int32_t E, int32_t K, int32_t N, int32_t group, const void* 
     const int e = launch_quantize_w4(E, K, N, group, W, W_q, W_sf, st);
     trace_post(st, "quantize_w4");
     return e ? abi_cuda_fail(e, "4-bit quantization launch") : MOE_OK;
+}
+
+int moe_ffn_workspace_layout(const moe_ffn_shape* shape, moe_ffn_layout* out) {
+    if (!out) return abi_fail(MOE_EINVAL, "out is NULL");
+    const int rc = check_ffn(shape);
+    if (rc) return rc;
+    const size_t T = (size_t)shape->T, I = (size_t)shape->I;
+    out->a = 0;
+    out->h = up256(T * I * 2);
+    out->saved_bytes = out->h + up256(T * 2 * I * 4);
+    out->status = 0;
+    out->dh = 256;
+    out->part = out->dh + up256(T * 2 * I * 2);
+    out->ws_bytes = out->part + up256((size_t)(shape->T > 0 ? ffn_part_bytes(*shape) : 0));
+    return MOE_OK;
+}
+
+int moe_ffn_forward(const moe_ffn_shape* shape, const void* x, const void* W1, const void* W2, int32_t for_backward,
+                    void* saved, void* ws, void* y, void* stream) {
+    moe_ffn_layout L;
+    int rc = moe_ffn_workspace_layout(shape, &L);
+    if (rc) return rc;
+    if (shape->T == 0) return MOE_OK;
+    if (!x || !W1 || !W2 || !saved || !ws || !y) return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    const void* ptrs[] = {x, W1, W2, saved, ws, y};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    int sms = 0;
+    if ((rc = abi_select_device(ws, &sms))) return rc;
+    uint8_t *sv = static_cast<uint8_t*>(saved), *w = static_cast<uint8_t*>(ws);
+    FfnPtrs f = {};
+    f.x = x;
+    f.W1 = W1;
+    f.W2 = W2;
+    f.a = sv + L.a;
+    f.h = for_backward ? reinterpret_cast<float*>(sv + L.h) : nullptr;
+    f.part = reinterpret_cast<float*>(w + L.part);
+    f.status = reinterpret_cast<int32_t*>(w + L.status);
+    f.y = y;
+    return launch_ffn_forward(*shape, f, (cudaStream_t)stream);
+}
+
+int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, const void* W1, const void* W2,
+                     const void* saved, void* ws, void* dx, void* dW1, void* dW2, void* stream) {
+    moe_ffn_layout L;
+    int rc = moe_ffn_workspace_layout(shape, &L);
+    if (rc) return rc;
+    if (!dW1 || !dW2 || (shape->T > 0 && (!dY || !x || !W1 || !W2 || !saved || !ws || !dx)))
+        return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    const void* ptrs[] = {dY, x, W1, W2, saved, ws, dx, dW1, dW2};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    int sms = 0;
+    if ((rc = abi_select_device(dW1, &sms))) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (shape->T == 0) {
+        const size_t HI = (size_t)shape->H * shape->I;
+        cudaError_t ce = cudaMemsetAsync(dW1, 0, HI * 4, st);
+        if (ce == cudaSuccess) ce = cudaMemsetAsync(dW2, 0, HI * 2, st);
+        return ce == cudaSuccess ? MOE_OK : abi_cuda_fail((int)ce, "zeroing weight gradients");
+    }
+    uint8_t *sv = static_cast<uint8_t*>(const_cast<void*>(saved)), *w = static_cast<uint8_t*>(ws);
+    FfnPtrs f = {};
+    f.x = x;
+    f.W1 = W1;
+    f.W2 = W2;
+    f.dY = dY;
+    f.a = sv + L.a;
+    f.h = reinterpret_cast<float*>(sv + L.h);
+    f.dh = w + L.dh;
+    f.part = reinterpret_cast<float*>(w + L.part);
+    f.status = reinterpret_cast<int32_t*>(w + L.status);
+    f.dx = dx;
+    f.dW1 = dW1;
+    f.dW2 = dW2;
+    return launch_ffn_backward(*shape, f, st);
 }
 
 }  // extern "C"

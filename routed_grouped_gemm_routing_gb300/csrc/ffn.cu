@@ -1,0 +1,778 @@
+// The dense gated feed-forward block (a shared expert beside the routed ones),
+// forward and backward:
+//
+//   h = x W1 (gate | up)     a = silu(clamp h_g) clamp h_u     y = a W2
+//   da = dY W2^T             dW2 = a^T dY
+//   dh_g = da u' sig(g')(1 + g'(1 - sig(g'))) [g passes]
+//   dh_u = da silu(g') [u passes]              (g', u': the clamped inputs)
+//   dx = dh W1^T             dW1 = x^T dh
+//
+// Six products of 2 T H I (y, da, dW2) or 4 T H I (h, dx, dW1) operations, all
+// bound by the tensor cores from a few hundred tokens on.  One kernel serves
+// them (dense_pair_kernel): D[256 x 256] per pair of SMs, tcgen05 cta_group::2,
+// operands by TMA (128-byte swizzle, K blocks of 64) straight from the
+// row-major tensors: an operand whose rows run along K is K-major, one whose
+// columns are the output's is MN-major, so nothing is ever transposed.  Each
+// CTA of the pair loads 128 rows of A and 128 columns of B and holds 128 x 256
+// of D in TMEM, twice, so that a tile's epilogue runs under the next one's
+// products.  The epilogues do the rest of the block on the accumulators:
+//   EPI_GATED  the tile's columns are 128 gate features (the first CTA's B) and
+//              the same 128 up features (the second's): both projections, the
+//              activation and the product in one kernel.  Leaves a and, for the
+//              backward, h.
+//   EPI_DGATE  dh from da in TMEM and h by TMA, both halves at once.
+//   EPI_PLAIN  bf16 D.
+//   EPI_PART   FP32 partial sums of a K range (see below).
+//
+// Roundings: a and dh are operands of bf16 products and are rounded once each.
+// h stays FP32 for the backward: its rounding would come on top of dh's (dx and
+// dW1 would err by half as much again), and its bytes, written and read once,
+// are a few percent of the block's time.
+//
+// Few tiles (few tokens): the K range is split over up to kDenseClusters /
+// tiles pairs, each leaving FP32 partial sums, and ffn_join adds them in a
+// fixed order and applies the epilogue; every SM then streams a part of the
+// weights.  Deterministic in every form: no atomics.
+//
+// Roles (6 warps per CTA): 0-3 epilogue (TMEM lanes 32 w .. of the CTA's 128
+// rows), 4 TMA producer, 5 MMA issuer (first CTA of the pair).  Every wait is
+// bounded; one that runs out sets bit 0 of the status word.
+#include "grouped_gemm_2sm.cuh"
+#include "smem_limit.h"
+
+namespace moe {
+
+namespace {
+
+enum DenseMode { KK, KN, NN };  // majorness of A, B: K-major or MN-major (N)
+enum DenseEpi { EPI_PLAIN, EPI_GATED, EPI_DGATE, EPI_PART, EPI_PART_GATED };
+
+constexpr int kDenseThreads = 192;
+constexpr int kDenseWarpTma = 4, kDenseWarpMma = 5;
+constexpr int kDenseClusters = 76;  // pairs of the 152 SMs: what the split of K aims at
+constexpr int kDenseStageBytes = 32768;  // A and B blocks of one CTA: 128 x 64 bf16 each
+
+template <int EPI>
+__host__ __device__ constexpr int dense_stages() {
+    return EPI == EPI_PLAIN || EPI == EPI_PART || EPI == EPI_PART_GATED ? 6 : 5;
+}
+// staging per epilogue warp: 4 KB boxes (EPI_DGATE: two for the incoming h)
+template <int EPI>
+__host__ __device__ constexpr int dense_boxes() {
+    return EPI == EPI_GATED || EPI == EPI_DGATE ? 4 : 2;
+}
+constexpr int kDenseTail = 256;
+template <int EPI>
+__host__ __device__ constexpr int dense_smem() {
+    return 1024 + dense_stages<EPI>() * kDenseStageBytes + kEpiWarps * dense_boxes<EPI>() * 4096 + kDenseTail;
+}
+static_assert(dense_smem<EPI_GATED>() <= 232448 && dense_smem<EPI_PLAIN>() <= 232448, "shared memory per CTA");
+
+struct DenseArgs {
+    int M, N;      // rows; columns (EPI_GATED, EPI_DGATE: features of one half)
+    int tiles_m, tiles_n;
+    int kblocks;   // 64-deep K blocks
+    int splits;    // K ranges (EPI_PART*)
+    float clamp;   // INFINITY: none
+    int save_h;    // EPI_GATED: store h
+    int32_t* status;
+};
+struct DenseMaps {
+    CUtensorMap a, b, c0, c1;
+};
+
+struct DenseBars {
+    uint32_t base;
+    int stages;
+    __device__ __forceinline__ uint32_t full(int s) const { return base + 8u * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return base + 8u * (stages + s); }
+    __device__ __forceinline__ uint32_t tfull(int a) const { return base + 8u * (2 * stages + a); }
+    __device__ __forceinline__ uint32_t tempty(int a) const { return base + 8u * (2 * stages + 2 + a); }
+    __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * stages + 4); }
+    __device__ __forceinline__ uint32_t hin(int w) const { return base + 8u * (2 * stages + 5 + w); }
+};
+static_assert(8 * (2 * 6 + 5 + kEpiWarps) + 8 <= kDenseTail, "barrier area");
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, int c0, int c1, int c2, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, int c0, int c1, int c2, int c3, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+                 : "memory");
+}
+
+// Work items of a cluster: (tile, K range), tiles eight row tiles by all column
+// tiles at a time so that the pairs that run together share their operands in L2.
+struct DenseItem {
+    int m0, n0, kb0, kb1, split;
+};
+template <int EPI>
+struct DenseWalk {
+    const DenseArgs& p;
+    int w, total;
+    __device__ __forceinline__ DenseWalk(const DenseArgs& p_)
+        : p(p_), w((int)blockIdx.x >> 1), total(p_.tiles_m * p_.tiles_n * p_.splits) {}
+    __device__ __forceinline__ bool valid() const { return w < total; }
+    __device__ __forceinline__ void next() { w += (int)gridDim.x >> 1; }
+    __device__ __forceinline__ DenseItem item() const {
+        DenseItem it;
+        const int tile = w / p.splits;
+        it.split = w - tile * p.splits;
+        const int per = 8 * p.tiles_n, group = tile / per, r = tile - group * per;
+        const int rows = p.tiles_m - 8 * group < 8 ? p.tiles_m - 8 * group : 8;
+        const int n = r / rows, m = 8 * group + r - n * rows;
+        it.m0 = m * 256;
+        it.n0 = n * (EPI == EPI_GATED || EPI == EPI_PART_GATED ? 128 : 256);
+        it.kb0 = (int)((long long)p.kblocks * it.split / p.splits);
+        it.kb1 = (int)((long long)p.kblocks * (it.split + 1) / p.splits);
+        return it;
+    }
+};
+
+// ------------------------------------------------------------ TMA producer
+template <int MODE, int EPI>
+__device__ void dense_producer(const CUtensorMap* mA, const CUtensorMap* mB, const DenseArgs& p, uint32_t ring,
+                               DenseBars bars, volatile int* abort, int rank) {
+    constexpr bool kAN = MODE == NN, kBN = MODE != KK;
+    constexpr bool kGated = EPI == EPI_GATED || EPI == EPI_PART_GATED;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (DenseWalk<EPI> w(p); w.valid(); w.next()) {
+        const DenseItem it = w.item();
+        const int m = it.m0 + 128 * rank, n = it.n0 + (kGated ? 0 : 128 * rank);
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+            if (!mbar_wait(bars.empty(stage), phase ^ 1u, abort)) return;
+            if (rank == 0) mbar_arrive_expect_tx(bars.full(stage), 2u * kDenseStageBytes);
+            const uint32_t fb = cluster_addr_of(bars.full(stage), 0);
+            const uint32_t a = ring + stage * kDenseStageBytes, b = a + kDenseStageBytes / 2;
+            const int k0 = kb * 64;
+            if constexpr (kAN) {
+                tma_load_2d_pair(a, mA, m, k0, fb);
+                tma_load_2d_pair(a + 8192, mA, m + 64, k0, fb);
+            } else {
+                tma_load_2d_pair(a, mA, k0, m, fb);
+            }
+            if constexpr (kGated) {  // W1 viewed as [H][2][I]: the gate's or the up projection's columns
+                tma_load_3d_pair(b, mB, n, rank, k0, fb);
+                tma_load_3d_pair(b + 8192, mB, n + 64, rank, k0, fb);
+            } else if constexpr (kBN) {
+                tma_load_2d_pair(b, mB, n, k0, fb);
+                tma_load_2d_pair(b + 8192, mB, n + 64, k0, fb);
+            } else {
+                tma_load_2d_pair(b, mB, k0, n, fb);
+            }
+            if (++stage == dense_stages<EPI>()) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------- MMA issuer
+template <int MODE, int EPI>
+__device__ void dense_mma(const DenseArgs& p, uint32_t ring, DenseBars bars, uint32_t tmem, volatile int* abort) {
+    constexpr bool kAN = MODE == NN, kBN = MODE != KK;
+    constexpr uint32_t idesc = make_idesc_bf16(256, 256, kAN, kBN);
+    int stage = 0, it = 0;
+    uint32_t phase = 0;
+    for (DenseWalk<EPI> w(p); w.valid(); w.next(), ++it) {
+        const DenseItem item = w.item();
+        const int acc = it & 1;
+        if (!warp_wait_uniform<true>(bars.tempty(acc), ((uint32_t)(it >> 1) & 1u) ^ 1u, abort)) return;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * 256);
+        for (int kb = item.kb0; kb < item.kb1; ++kb) {
+            if (!warp_wait_uniform<true>(bars.full(stage), phase, abort)) return;
+            tc_fence_after();
+            const uint32_t a = ring + stage * kDenseStageBytes, b = a + kDenseStageBytes / 2;
+            // the next 16 of K: 16 rows of 128 bytes (MN-major) or 32 bytes (K-major)
+            const uint64_t ad = make_sdesc_sw128(a, kAN ? 8192 : 16, 1024), bd = make_sdesc_sw128(b, kBN ? 8192 : 16, 1024);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_bf16_pair(d, ad + (kAN ? 128u : 2u) * kk, bd + (kBN ? 128u : 2u) * kk, idesc,
+                                     kb > item.kb0 || kk ? 1u : 0u);
+                tc_commit_pair(bars.empty(stage));
+            }
+            __syncwarp();
+            if (++stage == dense_stages<EPI>()) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (elect_one()) tc_commit_pair(bars.tfull(acc));
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------- epilogue
+// Half a row (32 bf16) of a 32 x 64 bf16 box in the 128-byte swizzle.
+__device__ __forceinline__ void stage_half_row(uint32_t box, int r, int half, const uint32_t (&p)[16]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        st_shared_v4(box + r * 128 + (((4 * half + c) ^ (r & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2],
+                     p[4 * c + 3]);
+}
+// Row r of a 32 x 32 f32 box in the 128-byte swizzle.
+__device__ __forceinline__ void read_row_f32(uint32_t box, int r, float (&v)[32]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const int4 u = ld_shared_v4s(box + r * 128 + ((c ^ (r & 7)) << 4));
+        v[4 * c] = __int_as_float(u.x);
+        v[4 * c + 1] = __int_as_float(u.y);
+        v[4 * c + 2] = __int_as_float(u.z);
+        v[4 * c + 3] = __int_as_float(u.w);
+    }
+}
+
+// a = silu(clamp g) clamp u
+__device__ __forceinline__ float gate_fwd(float g, float u, float c) {
+    g = clamp_in(g, c);
+    u = clamp_in(u, c);
+    return g / (1.0f + __expf(-g)) * u;
+}
+// (dh_g, dh_u) of da
+__device__ __forceinline__ float2 gate_bwd(float da, float g, float u, float c) {
+    const float pg = clamp_pass(g, c), pu = clamp_pass(u, c);
+    g = clamp_in(g, c);
+    u = clamp_in(u, c);
+    const float s = 1.0f / (1.0f + __expf(-g));
+    return make_float2(pg * da * u * s * (1.0f + g * (1.0f - s)), pu * da * g * s);
+}
+
+template <int EPI>
+__device__ void dense_epilogue(const CUtensorMap* m0, const CUtensorMap* m1, const DenseArgs& p, DenseBars bars,
+                               uint32_t tmem, uint32_t stage, volatile int* abort, int warp, int lane, int rank) {
+    const uint32_t tempty[2] = {cluster_addr_of(bars.tempty(0), 0), cluster_addr_of(bars.tempty(1), 0)};
+    int it = 0;
+    uint32_t hphase = 0;  // EPI_DGATE: h boxes waited for
+    uint32_t nbox = 0;
+    for (DenseWalk<EPI> w(p); w.valid(); w.next(), ++it) {
+        const DenseItem item = w.item();
+        const int acc = it & 1;
+        const int row0 = item.m0 + 128 * rank + 32 * warp;
+        const bool rows_live = row0 < p.M;
+        // EPI_DGATE: the first h boxes of the tile come while its products run
+        auto fetch_h = [&](int c32) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bars.hin(warp), 8192u);
+                tma_load_3d(stage, m1, item.n0 + 32 * c32, 0, row0, bars.hin(warp));
+                tma_load_3d(stage + 4096, m1, item.n0 + 32 * c32, 1, row0, bars.hin(warp));
+            }
+        };
+        if constexpr (EPI == EPI_DGATE) {
+            if (rows_live) fetch_h(0);
+        }
+        if (!warp_wait(bars.tfull(acc), (uint32_t)(it >> 1) & 1u, abort)) break;
+        tc_fence_after();
+        const uint32_t t = tmem + (uint32_t)(acc * 256) + ((uint32_t)(warp * 32) << 16);
+        bool ok = true;
+        if (rows_live) {
+            if constexpr (EPI == EPI_PLAIN) {
+#pragma unroll 1
+                for (int c = 0; c < 4 && item.n0 + 64 * c < p.N; ++c) {
+                    uint32_t r0[32], r1[32], pk[32];
+                    tmem_ld32_nowait(t + 64 * c, r0);
+                    tmem_ld32_nowait(t + 64 * c + 32, r1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        pk[j] = pack_bf16x2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
+                        pk[16 + j] = pack_bf16x2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
+                    }
+                    const uint32_t box = stage + (nbox & 1u) * 4096u;
+                    if (lane == 0) bulk_wait_read<1>();
+                    __syncwarp();
+                    stage_row_sw128(box, lane, pk);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(m0, item.n0 + 64 * c, row0, box);
+                        bulk_commit();
+                    }
+                    ++nbox;
+                }
+            } else if constexpr (EPI == EPI_PART || EPI == EPI_PART_GATED) {
+                constexpr bool kGated = EPI == EPI_PART_GATED;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    const int half = kGated ? c >> 2 : 0, n = item.n0 + 32 * (kGated ? c & 3 : c);
+                    if (n >= p.N) continue;
+                    uint32_t r0[32];
+                    tmem_ld32_nowait(t + 32 * c, r0);
+                    tmem_ld_wait();
+                    const uint32_t box = stage + (nbox & 1u) * 4096u;
+                    if (lane == 0) bulk_wait_read<1>();
+                    __syncwarp();
+                    stage_row_sw128(box, lane, r0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_4d(m0, n, half, row0, item.split, box);
+                        bulk_commit();
+                    }
+                    ++nbox;
+                }
+            } else if constexpr (EPI == EPI_GATED) {
+                // boxes: 0 a, 1..3 h in turn
+#pragma unroll 1
+                for (int c = 0; c < 4 && item.n0 + 32 * c < p.N; ++c) {
+                    uint32_t g[32], u[32], pk[16];
+                    tmem_ld32_nowait(t + 32 * c, g);
+                    tmem_ld32_nowait(t + 128 + 32 * c, u);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        pk[j] = pack_bf16x2(
+                            gate_fwd(__uint_as_float(g[2 * j]), __uint_as_float(u[2 * j]), p.clamp),
+                            gate_fwd(__uint_as_float(g[2 * j + 1]), __uint_as_float(u[2 * j + 1]), p.clamp));
+                    if (p.save_h) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t box = stage + 4096u * (1u + nbox % 3u);
+                            if (lane == 0) bulk_wait_read<2>();
+                            __syncwarp();
+                            stage_row_sw128(box, lane, half ? u : g);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_3d(m1, item.n0 + 32 * c, half, row0, box);
+                                bulk_commit();
+                            }
+                            ++nbox;
+                        }
+                    }
+                    if ((c & 1) == 0) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                    }
+                    stage_half_row(stage, lane, c & 1, pk);
+                    if ((c & 1) || item.n0 + 32 * (c + 1) >= p.N) {  // columns past N are not stored
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(m0, item.n0 + 32 * (c & ~1), row0, stage);
+                            bulk_commit();
+                        }
+                    }
+                }
+            } else {
+                // boxes: 0, 1 h in; 2, 3 dh out (64 columns of each half)
+#pragma unroll 1
+                for (int c = 0; c < 8 && item.n0 + 32 * c < p.N; ++c) {
+                    uint32_t da[32], pg[16], pu[16];
+                    tmem_ld32_nowait(t + 32 * c, da);
+                    if (!warp_wait(bars.hin(warp), hphase, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    hphase ^= 1u;
+                    float g[32], u[32];
+                    read_row_f32(stage, lane, g);
+                    read_row_f32(stage + 4096u, lane, u);
+                    __syncwarp();
+                    if (c + 1 < 8 && item.n0 + 32 * (c + 1) < p.N) fetch_h(c + 1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 d0 = gate_bwd(__uint_as_float(da[2 * j]), g[2 * j], u[2 * j], p.clamp);
+                        const float2 d1 = gate_bwd(__uint_as_float(da[2 * j + 1]), g[2 * j + 1], u[2 * j + 1], p.clamp);
+                        pg[j] = pack_bf16x2(d0.x, d1.x);
+                        pu[j] = pack_bf16x2(d0.y, d1.y);
+                    }
+                    if ((c & 1) == 0) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                    }
+                    stage_half_row(stage + 8192u, lane, c & 1, pg);
+                    stage_half_row(stage + 12288u, lane, c & 1, pu);
+                    if ((c & 1) || item.n0 + 32 * (c + 1) >= p.N) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(m0, item.n0 + 32 * (c & ~1), 0, row0, stage + 8192u);
+                            tma_store_3d(m0, item.n0 + 32 * (c & ~1), 1, row0, stage + 12288u);
+                            bulk_commit();
+                        }
+                    }
+                }
+            }
+        }
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+}
+
+// Maps: a, b operands; c0 output (EPI_GATED: a; EPI_DGATE: dh; EPI_PART: the
+// partial sums); c1 h (EPI_GATED: store, EPI_DGATE: load).
+template <int MODE, int EPI>
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
+                      const __grid_constant__ CUtensorMap mC0, const __grid_constant__ CUtensorMap mC1,
+                      const DenseArgs p) {
+    constexpr int kStages = dense_stages<EPI>();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t boxes = base + kStages * kDenseStageBytes;
+    const uint32_t bar0 = boxes + kEpiWarps * dense_boxes<EPI>() * 4096;
+    uint8_t* tail = smem_raw + (bar0 - raw);
+    const DenseBars bars{bar0, kStages};
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 8 * (2 * kStages + 5 + kEpiWarps));
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bars.full(s), 1);
+            mbar_init(bars.empty(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(bars.tfull(a), 1);
+            mbar_init(bars.tempty(a), 2 * kEpiWarps);
+        }
+        mbar_init(bars.drain(), 1);
+        for (int w = 0; w < kEpiWarps; ++w) mbar_init(bars.hin(w), 1);
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kDenseWarpMma) {
+        tmem_alloc_pair(smem_addr(tmem_slot), 512);
+        tmem_relinquish_pair();
+    }
+    if (warp == kDenseWarpTma && lane == 0) {
+        tma_prefetch_map(&mA);
+        tma_prefetch_map(&mB);
+        tma_prefetch_map(&mC0);
+        if (EPI == EPI_GATED || EPI == EPI_DGATE) tma_prefetch_map(&mC1);
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == kDenseWarpTma) {
+        if (lane == 0) dense_producer<MODE, EPI>(&mA, &mB, p, base, bars, abort, rank);
+    } else if (warp == kDenseWarpMma) {
+        if (rank == 0) {
+            dense_mma<MODE, EPI>(p, base, bars, tmem, abort);
+            const bool aborted = __any_sync(0xffffffffu, *abort != 0);
+            if (elect_one() && aborted) {
+                // let every MMA already issued (by this same elected lane)
+                // finish before TMEM is released
+                tc_commit_pair_local(bars.drain());
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(bars.drain(), 0) && global_timer_ns() - t0 < 100000000ull) {
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        dense_epilogue<EPI>(&mC0, &mC1, p, bars, tmem, boxes + warp * dense_boxes<EPI>() * 4096, abort, warp, lane,
+                            rank);
+    }
+    if (warp == kDenseWarpTma && lane == 0 && *abort) {
+        // copies in flight land before the CTA's shared memory goes
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    if (warp == kDenseWarpMma) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort) atomicOr(reinterpret_cast<int*>(p.status), 1);
+}
+
+// ---------------------------------------------------------------- the join
+// Sums of the K ranges' partial sums [splits][T][halves][n] in order, and the
+// epilogue.  Eight columns per thread and half.
+enum JoinEpi { JOIN_PLAIN, JOIN_GATED, JOIN_DGATE };
+struct JoinArgs {
+    const float* part;
+    long long rows;
+    int n, splits, halves;
+    float clamp;
+    void* out;   // JOIN_PLAIN: bf16 [rows][n]; JOIN_GATED: a; JOIN_DGATE: dh [rows][2][n]
+    float* h;    // [rows][2][n]: JOIN_GATED written (may be null), JOIN_DGATE read
+};
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+template <int EPI>
+__global__ void __launch_bounds__(128) ffn_join_kernel(const JoinArgs p) {
+    constexpr int kHalves = EPI == JOIN_GATED ? 2 : 1;
+    const int per = p.n / 8;
+    const long long total = p.rows * per;
+    const size_t stride = (size_t)p.rows * p.halves * p.n;
+    for (long long i = (long long)blockIdx.x * 128 + threadIdx.x; i < total; i += (long long)gridDim.x * 128) {
+        const long long row = i / per;
+        const int c = (int)(i - row * per) * 8;
+        float v[kHalves][8];
+#pragma unroll
+        for (int hf = 0; hf < kHalves; ++hf) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[hf][j] = 0.0f;
+            const float* src = p.part + ((size_t)row * p.halves + hf) * p.n + c;
+            for (int s = 0; s < p.splits; ++s) {
+                const float4 a = __ldg(reinterpret_cast<const float4*>(src + s * stride));
+                const float4 b = __ldg(reinterpret_cast<const float4*>(src + s * stride) + 1);
+                v[hf][0] += a.x, v[hf][1] += a.y, v[hf][2] += a.z, v[hf][3] += a.w;
+                v[hf][4] += b.x, v[hf][5] += b.y, v[hf][6] += b.z, v[hf][7] += b.w;
+            }
+        }
+        auto* out = static_cast<__nv_bfloat16*>(p.out);
+        float o[8];
+        if constexpr (EPI == JOIN_PLAIN) {
+            *reinterpret_cast<uint4*>(out + (size_t)row * p.n + c) = pack8(v[0]);
+        } else if constexpr (EPI == JOIN_GATED) {
+            if (p.h) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float4* h = reinterpret_cast<float4*>(p.h + ((size_t)row * 2 + hf) * p.n + c);
+                    h[0] = make_float4(v[hf][0], v[hf][1], v[hf][2], v[hf][3]);
+                    h[1] = make_float4(v[hf][4], v[hf][5], v[hf][6], v[hf][7]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = gate_fwd(v[0][j], v[kHalves - 1][j], p.clamp);
+            *reinterpret_cast<uint4*>(out + (size_t)row * p.n + c) = pack8(o);
+        } else {
+            const float* h = p.h + (size_t)row * 2 * p.n + c;
+            float du[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 d = gate_bwd(v[0][j], __ldg(h + j), __ldg(h + p.n + j), p.clamp);
+                o[j] = d.x;
+                du[j] = d.y;
+            }
+            *reinterpret_cast<uint4*>(out + (size_t)row * 2 * p.n + c) = pack8(o);
+            *reinterpret_cast<uint4*>(out + (size_t)row * 2 * p.n + p.n + c) = pack8(du);
+        }
+    }
+}
+template <int EPI>
+int launch_join(const JoinArgs& a, cudaStream_t st) {
+    const long long blocks = (a.rows * (a.n / 8) + 127) / 128;
+    trace_pre(st);
+    ffn_join_kernel<EPI><<<(unsigned)(blocks < 2432 ? blocks : 2432), 128, 0, st>>>(a);
+    trace_post(st, "ffn_join");
+    return (int)cudaGetLastError();
+}
+
+// ----------------------------------------------------------------- launches
+template <int MODE, int EPI>
+int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaStream_t st) {
+    static std::atomic<int> clusters_fit[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return (int)e;
+    if (dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(kDenseThreads, 1, 1);
+    cfg.dynamicSmemBytes = dense_smem<EPI>();
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto kernel = dense_pair_kernel<MODE, EPI>;
+    int fit = clusters_fit[dev].load(std::memory_order_relaxed);
+    if (fit == 0) {
+        // set once per device, outside any stream capture (on the first call)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_smem<EPI>());
+        if (e != cudaSuccess) return (int)e;
+        int sms = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return (int)e;
+        cfg.gridDim = dim3((unsigned)(sms & ~1), 1, 1);
+        e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+        if (e != cudaSuccess) return (int)e;
+        if (fit < 1) return (int)cudaErrorInvalidConfiguration;
+        clusters_fit[dev].store(fit, std::memory_order_relaxed);
+    }
+    const long long items = (long long)a.tiles_m * a.tiles_n * a.splits;
+    if (items <= 0) return 0;
+    cfg.gridDim = dim3(2u * (unsigned)(items < fit ? items : fit), 1, 1);
+    trace_pre(st);
+    e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.c0, m.c1, a);
+    trace_post(st, name);
+    return (int)(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+int cdiv(long long a, int b) { return (int)((a + b - 1) / b); }
+
+// K ranges: as many as give every pair of SMs a tile, of at least four K
+// blocks (256 deep), where the tiles alone would leave more than half idle.
+int dense_splits(int tiles, int kblocks) {
+    if (tiles <= 0 || 2 * tiles > kDenseClusters) return 1;
+    const int most = kblocks / 4, want = kDenseClusters / tiles;
+    const int s = want < most ? want : most;
+    return s > 1 ? s : 1;
+}
+
+// One product of the block.
+struct Product {
+    int M, N, K;            // N: columns, or features of one half
+    bool gated;             // B's columns are [2][N]
+    long long bytes() const {  // of the partial sums (0: one K range)
+        const int s = splits();
+        return s > 1 ? (long long)s * M * (gated ? 2 : 1) * N * 4 : 0;
+    }
+    int tiles_m() const { return cdiv(M, 256); }
+    int tiles_n() const { return cdiv(N, gated ? 128 : 256); }
+    int splits() const { return dense_splits(tiles_m() * tiles_n(), cdiv(K, 64)); }
+    DenseArgs args(float clamp, int32_t* status) const {
+        DenseArgs a = {};
+        a.M = M;
+        a.N = N;
+        a.tiles_m = tiles_m();
+        a.tiles_n = tiles_n();
+        a.kblocks = cdiv(K, 64);
+        a.splits = 1;
+        a.clamp = clamp;
+        a.status = status;
+        return a;
+    }
+};
+
+// Tensor maps.  bf16 rows x cols, row-major: K-major operands take 64 columns x
+// 128 rows, MN-major ones 64 x 64, stores 64 x 32.
+int map_op(CUtensorMap* m, const void* p, long long rows, int cols, int box_rows, const char* what) {
+    return abi_map_2d(m, p, 2, rows, cols, cols, 64, box_rows, what);
+}
+
+Product fwd1(const moe_ffn_shape& s) { return {s.T, s.I, s.H, true}; }
+Product fwd2(const moe_ffn_shape& s) { return {s.T, s.H, s.I, false}; }
+Product dgate(const moe_ffn_shape& s) { return {s.T, s.I, s.H, false}; }
+Product dgrad(const moe_ffn_shape& s) { return {s.T, s.H, 2 * s.I, false}; }
+
+}  // namespace
+
+long long ffn_part_bytes(const moe_ffn_shape& s) {
+    long long most = 0;
+    for (const Product& q : {fwd1(s), fwd2(s), dgate(s), dgrad(s)})
+        if (q.bytes() > most) most = q.bytes();
+    return most;
+}
+
+int launch_ffn_forward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st) {
+    const float clamp = s.activation_clamp > 0.0f ? s.activation_clamp : INFINITY;
+    int rc;
+    {
+        const Product q = fwd1(s);
+        DenseArgs a = q.args(clamp, f.status);
+        a.save_h = f.h != nullptr;
+        DenseMaps m = {};
+        if ((rc = map_op(&m.a, f.x, s.T, s.H, 128, "x"))) return rc;
+        if ((rc = abi_map_nd(&m.b, f.W1, 2, {s.I, 2, s.H}, {64, 1, 64}, "W1 (gate/up halves)"))) return rc;
+        int e;
+        if (q.splits() > 1) {
+            a.splits = q.splits();
+            if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.I, 2, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
+            e = launch_dense<KN, EPI_PART_GATED>(a, m, "ffn_gate_up", st);
+            if (!e) e = launch_join<JOIN_GATED>({f.part, s.T, s.I, a.splits, 2, clamp, f.a, f.h}, st);
+        } else {
+            if ((rc = map_op(&m.c0, f.a, s.T, s.I, 32, "a (store)"))) return rc;
+            if (f.h && (rc = abi_map_nd(&m.c1, f.h, 4, {s.I, 2, s.T}, {32, 1, 32}, "h (store)"))) return rc;
+            e = launch_dense<KN, EPI_GATED>(a, m, "ffn_gate_up", st);
+        }
+        if (e) return abi_cuda_fail(e, "gate and up projection launch");
+    }
+    const Product q = fwd2(s);
+    DenseArgs a = q.args(clamp, f.status);
+    DenseMaps m = {};
+    if ((rc = map_op(&m.a, f.a, s.T, s.I, 128, "a"))) return rc;
+    if ((rc = map_op(&m.b, f.W2, s.I, s.H, 64, "W2"))) return rc;
+    int e;
+    if (q.splits() > 1) {
+        a.splits = q.splits();
+        if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.H, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
+        e = launch_dense<KN, EPI_PART>(a, m, "ffn_down", st);
+        if (!e) e = launch_join<JOIN_PLAIN>({f.part, s.T, s.H, a.splits, 1, clamp, f.y, nullptr}, st);
+    } else {
+        if ((rc = map_op(&m.c0, f.y, s.T, s.H, 32, "y (store)"))) return rc;
+        e = launch_dense<KN, EPI_PLAIN>(a, m, "ffn_down", st);
+    }
+    return e ? abi_cuda_fail(e, "down projection launch") : MOE_OK;
+}
+
+int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st) {
+    const float clamp = s.activation_clamp > 0.0f ? s.activation_clamp : INFINITY;
+    int rc, e;
+    {  // da = dY W2^T, and dh from it
+        const Product q = dgate(s);
+        DenseArgs a = q.args(clamp, f.status);
+        DenseMaps m = {};
+        if ((rc = map_op(&m.a, f.dY, s.T, s.H, 128, "dY"))) return rc;
+        if ((rc = map_op(&m.b, f.W2, s.I, s.H, 128, "W2 (K-major)"))) return rc;
+        if (q.splits() > 1) {
+            a.splits = q.splits();
+            if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.I, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
+            e = launch_dense<KK, EPI_PART>(a, m, "ffn_dgate", st);
+            if (!e) e = launch_join<JOIN_DGATE>({f.part, s.T, s.I, a.splits, 1, clamp, f.dh, f.h}, st);
+        } else {
+            if ((rc = abi_map_nd(&m.c0, f.dh, 2, {s.I, 2, s.T}, {64, 1, 32}, "dh (store)"))) return rc;
+            if ((rc = abi_map_nd(&m.c1, f.h, 4, {s.I, 2, s.T}, {32, 1, 32}, "h"))) return rc;
+            e = launch_dense<KK, EPI_DGATE>(a, m, "ffn_dgate", st);
+        }
+        if (e) return abi_cuda_fail(e, "dh launch");
+    }
+    {  // dW2 = a^T dY
+        const Product q = {s.I, s.H, s.T, false};
+        DenseMaps m = {};
+        if ((rc = map_op(&m.a, f.a, s.T, s.I, 64, "a (MN-major)"))) return rc;
+        if ((rc = map_op(&m.b, f.dY, s.T, s.H, 64, "dY (MN-major)"))) return rc;
+        if ((rc = map_op(&m.c0, f.dW2, s.I, s.H, 32, "dW2 (store)"))) return rc;
+        if ((e = launch_dense<NN, EPI_PLAIN>(q.args(clamp, f.status), m, "ffn_dw2", st))) return abi_cuda_fail(e, "dW2 launch");
+    }
+    {  // dW1 = x^T dh
+        const Product q = {s.H, 2 * s.I, s.T, false};
+        DenseMaps m = {};
+        if ((rc = map_op(&m.a, f.x, s.T, s.H, 64, "x (MN-major)"))) return rc;
+        if ((rc = map_op(&m.b, f.dh, s.T, 2 * s.I, 64, "dh (MN-major)"))) return rc;
+        if ((rc = map_op(&m.c0, f.dW1, s.H, 2 * s.I, 32, "dW1 (store)"))) return rc;
+        if ((e = launch_dense<NN, EPI_PLAIN>(q.args(clamp, f.status), m, "ffn_dw1", st))) return abi_cuda_fail(e, "dW1 launch");
+    }
+    // dx = dh W1^T
+    const Product q = dgrad(s);
+    DenseArgs a = q.args(clamp, f.status);
+    DenseMaps m = {};
+    if ((rc = map_op(&m.a, f.dh, s.T, 2 * s.I, 128, "dh"))) return rc;
+    if ((rc = map_op(&m.b, f.W1, s.H, 2 * s.I, 128, "W1 (K-major)"))) return rc;
+    if (q.splits() > 1) {
+        a.splits = q.splits();
+        if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.H, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
+        e = launch_dense<KK, EPI_PART>(a, m, "ffn_dx", st);
+        if (!e) e = launch_join<JOIN_PLAIN>({f.part, s.T, s.H, a.splits, 1, clamp, f.dx, nullptr}, st);
+    } else {
+        if ((rc = map_op(&m.c0, f.dx, s.T, s.H, 32, "dx (store)"))) return rc;
+        e = launch_dense<KK, EPI_PLAIN>(a, m, "ffn_dx", st);
+    }
+    return e ? abi_cuda_fail(e, "dx launch") : MOE_OK;
+}
+
+}  // namespace moe

@@ -334,6 +334,23 @@ int abi_map_2d(CUtensorMap* m, const void* p, int elt, long long rows, long long
                     elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
+int abi_map_nd(CUtensorMap* m, const void* p, int elt, std::initializer_list<long long> dims,
+               std::initializer_list<int> box, const char* what) {
+    cuuint64_t d[5], str[5];
+    cuuint32_t b[5];
+    int rank = 0;
+    cuuint64_t bytes = (cuuint64_t)elt;
+    for (long long v : dims) {
+        d[rank] = (cuuint64_t)v;
+        bytes *= (cuuint64_t)v;
+        str[rank++] = bytes;  // stride of the next dimension
+    }
+    int i = 0;
+    for (int v : box) b[i++] = (cuuint32_t)v;
+    return make_map(m, p, rank, d, str, b, what, CU_TENSOR_MAP_SWIZZLE_128B,
+                    elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+
 int compute_layout(const moe_shape* s, moe_layout* L) {
     memset(L, 0, sizeof *L);
     const long long tk = (long long)s->T * s->k;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "moe_layer.h"
 
 namespace moe {
@@ -84,10 +86,15 @@ int abi_fail(int code, const char* msg);
 int abi_cuda_fail(int cuda_error, const char* what);
 // Makes the device that owns `data` current and gives its SM count.
 int abi_select_device(const void* data, int* sms);
-// Tensor map of rank 2, row-major, 128-byte swizzle unless plain: element
-// size 2 (bf16) or 4 (f32); box_cols * element size must be 128 when swizzled.
+// Tensor map of a row-major matrix, 128-byte swizzle: element size 2 (bf16) or
+// 4 (f32); box_cols * element size must be 128.
 int abi_map_2d(CUtensorMap* m, const void* p, int elt, long long rows, long long cols, long long stride_elems,
                int box_cols, int box_rows, const char* what);
+
+// The same for a contiguous row-major tensor of any rank up to 5, dims and box
+// innermost first; box[0] * element size must be 128.
+int abi_map_nd(CUtensorMap* m, const void* p, int elt, std::initializer_list<long long> dims,
+               std::initializer_list<int> box, const char* what);
 
 // ------------------------------------------------------------- layer norm
 struct LnFwdArgs {
@@ -130,6 +137,21 @@ int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q
                      cudaStream_t st);
 int launch_experts_w4(const W4Experts& w, cudaStream_t st);
 int launch_quantize_w4(int E, int K, int N, int G, const void* W, uint8_t* q, void* sf, cudaStream_t st);
+
+// ------------------------------------------- dense gated feed-forward block
+struct FfnPtrs {
+    const void *x, *W1, *W2, *dY;
+    float* h;  // null: not kept
+    void *a, *dh;
+    float* part;
+    int32_t* status;
+    void *y, *dx, *dW1, *dW2;
+};
+// Bytes of the partial sums that the K-split products need at most (0: none).
+long long ffn_part_bytes(const moe_ffn_shape& s);
+// MOE_OK or an error code with its message set.
+int launch_ffn_forward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
+int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
 
 // Layout of the three workspaces (host only).
 int compute_layout(const moe_shape* s, moe_layout* L);
