@@ -34,9 +34,15 @@
 // fixed order and applies the epilogue; every SM then streams a part of the
 // weights.  Deterministic in every form: no atomics.
 //
-// Roles (6 warps per CTA): 0-3 epilogue (TMEM lanes 32 w .. of the CTA's 128
-// rows), 4 TMA producer, 5 MMA issuer (first CTA of the pair).  Every wait is
-// bounded; one that runs out sets bit 0 of the status word.
+// Roles (10 warps per CTA): 0-7 epilogue (warp w: TMEM lanes 32 (w % 4) .. of
+// the CTA's 128 rows, every other group of columns from w / 4 on; with four
+// warps the arithmetic of EPI_DGATE took longer than the products of a
+// 2048-deep tile: 72 -> DG_US us at 4096 x 2048 x 1408), 8 TMA producer, 9 MMA
+// issuer (first CTA of the pair).  Every wait is bounded; one that runs out
+// sets bit 0 of the status word.
+//
+// The tile is 256 x 256, or narrower (192, 128 columns) where that leaves fewer
+// columns' worth of rounds over the pairs (dense_width).
 #include "grouped_gemm_2sm.cuh"
 #include "smem_limit.h"
 
@@ -47,8 +53,9 @@ namespace {
 enum DenseMode { KK, KN, NN };  // majorness of A, B: K-major or MN-major (N)
 enum DenseEpi { EPI_PLAIN, EPI_GATED, EPI_DGATE, EPI_PART, EPI_PART_GATED };
 
-constexpr int kDenseThreads = 192;
-constexpr int kDenseWarpTma = 4, kDenseWarpMma = 5;
+constexpr int kDenseEpiWarps = 8;
+constexpr int kDenseWarpTma = 8, kDenseWarpMma = 9;
+constexpr int kDenseThreads = 320;
 constexpr int kDenseClusters = 76;  // pairs of the 152 SMs: what the split of K aims at
 constexpr int kDenseStageBytes = 32768;  // A and B blocks of one CTA: 128 x 64 bf16 each
 
@@ -56,15 +63,15 @@ template <int EPI>
 __host__ __device__ constexpr int dense_stages() {
     return EPI == EPI_PLAIN || EPI == EPI_PART || EPI == EPI_PART_GATED ? 6 : 5;
 }
-// staging per epilogue warp: 4 KB boxes (EPI_DGATE: two for the incoming h)
+// staging per epilogue warp: 4 KB boxes (EPI_GATED: h out, EPI_DGATE: h in)
 template <int EPI>
 __host__ __device__ constexpr int dense_boxes() {
-    return EPI == EPI_GATED || EPI == EPI_DGATE ? 4 : 2;
+    return EPI == EPI_GATED || EPI == EPI_DGATE ? 2 : 1;
 }
 constexpr int kDenseTail = 256;
 template <int EPI>
 __host__ __device__ constexpr int dense_smem() {
-    return 1024 + dense_stages<EPI>() * kDenseStageBytes + kEpiWarps * dense_boxes<EPI>() * 4096 + kDenseTail;
+    return 1024 + dense_stages<EPI>() * kDenseStageBytes + kDenseEpiWarps * dense_boxes<EPI>() * 4096 + kDenseTail;
 }
 static_assert(dense_smem<EPI_GATED>() <= 232448 && dense_smem<EPI_PLAIN>() <= 232448, "shared memory per CTA");
 
@@ -73,9 +80,11 @@ struct DenseArgs {
     int tiles_m, tiles_n;
     int kblocks;   // 64-deep K blocks
     int splits;    // K ranges (EPI_PART*)
+    int width;     // columns of a tile (gated forms: both halves')
     float clamp;   // INFINITY: none
     int save_h;    // EPI_GATED: store h
     int32_t* status;
+    __nv_bfloat16* out;  // EPI_GATED: a [M][N]; EPI_DGATE: dh [M][2][N]
 };
 struct DenseMaps {
     CUtensorMap a, b, c0, c1;
@@ -91,7 +100,7 @@ struct DenseBars {
     __device__ __forceinline__ uint32_t drain() const { return base + 8u * (2 * stages + 4); }
     __device__ __forceinline__ uint32_t hin(int w) const { return base + 8u * (2 * stages + 5 + w); }
 };
-static_assert(8 * (2 * 6 + 5 + kEpiWarps) + 8 <= kDenseTail, "barrier area");
+static_assert(8 * (2 * 6 + 5 + kDenseEpiWarps) + 8 <= kDenseTail, "barrier area");
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
@@ -134,7 +143,7 @@ struct DenseWalk {
         const int rows = p.tiles_m - 8 * group < 8 ? p.tiles_m - 8 * group : 8;
         const int n = r / rows, m = 8 * group + r - n * rows;
         it.m0 = m * 256;
-        it.n0 = n * (EPI == EPI_GATED || EPI == EPI_PART_GATED ? 128 : 256);
+        it.n0 = n * (EPI == EPI_GATED || EPI == EPI_PART_GATED ? p.width / 2 : p.width);
         it.kb0 = (int)((long long)p.kblocks * it.split / p.splits);
         it.kb1 = (int)((long long)p.kblocks * (it.split + 1) / p.splits);
         return it;
@@ -149,12 +158,15 @@ __device__ void dense_producer(const CUtensorMap* mA, const CUtensorMap* mB, con
     constexpr bool kGated = EPI == EPI_GATED || EPI == EPI_PART_GATED;
     int stage = 0;
     uint32_t phase = 0;
+    const int half = p.width / 2;      // this CTA's columns of B
+    const bool two = half > 64;        // MN-major: boxes of 64 columns
+    const uint32_t tx = 2u * (kDenseStageBytes / 2 + (kBN ? (two ? 16384u : 8192u) : (uint32_t)half * 128u));
     for (DenseWalk<EPI> w(p); w.valid(); w.next()) {
         const DenseItem it = w.item();
-        const int m = it.m0 + 128 * rank, n = it.n0 + (kGated ? 0 : 128 * rank);
+        const int m = it.m0 + 128 * rank, n = it.n0 + (kGated ? 0 : half * rank);
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
             if (!mbar_wait(bars.empty(stage), phase ^ 1u, abort)) return;
-            if (rank == 0) mbar_arrive_expect_tx(bars.full(stage), 2u * kDenseStageBytes);
+            if (rank == 0) mbar_arrive_expect_tx(bars.full(stage), tx);
             const uint32_t fb = cluster_addr_of(bars.full(stage), 0);
             const uint32_t a = ring + stage * kDenseStageBytes, b = a + kDenseStageBytes / 2;
             const int k0 = kb * 64;
@@ -166,10 +178,10 @@ __device__ void dense_producer(const CUtensorMap* mA, const CUtensorMap* mB, con
             }
             if constexpr (kGated) {  // W1 viewed as [H][2][I]: the gate's or the up projection's columns
                 tma_load_3d_pair(b, mB, n, rank, k0, fb);
-                tma_load_3d_pair(b + 8192, mB, n + 64, rank, k0, fb);
+                if (two) tma_load_3d_pair(b + 8192, mB, n + 64, rank, k0, fb);
             } else if constexpr (kBN) {
                 tma_load_2d_pair(b, mB, n, k0, fb);
-                tma_load_2d_pair(b + 8192, mB, n + 64, k0, fb);
+                if (two) tma_load_2d_pair(b + 8192, mB, n + 64, k0, fb);
             } else {
                 tma_load_2d_pair(b, mB, k0, n, fb);
             }
@@ -185,7 +197,7 @@ __device__ void dense_producer(const CUtensorMap* mA, const CUtensorMap* mB, con
 template <int MODE, int EPI>
 __device__ void dense_mma(const DenseArgs& p, uint32_t ring, DenseBars bars, uint32_t tmem, volatile int* abort) {
     constexpr bool kAN = MODE == NN, kBN = MODE != KK;
-    constexpr uint32_t idesc = make_idesc_bf16(256, 256, kAN, kBN);
+    const uint32_t idesc = make_idesc_bf16(256, p.width, kAN, kBN);
     int stage = 0, it = 0;
     uint32_t phase = 0;
     for (DenseWalk<EPI> w(p); w.valid(); w.next(), ++it) {
@@ -219,13 +231,6 @@ __device__ void dense_mma(const DenseArgs& p, uint32_t ring, DenseBars bars, uin
 }
 
 // ---------------------------------------------------------------- epilogue
-// Half a row (32 bf16) of a 32 x 64 bf16 box in the 128-byte swizzle.
-__device__ __forceinline__ void stage_half_row(uint32_t box, int r, int half, const uint32_t (&p)[16]) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        st_shared_v4(box + r * 128 + (((4 * half + c) ^ (r & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2],
-                     p[4 * c + 3]);
-}
 // Row r of a 32 x 32 f32 box in the 128-byte swizzle.
 __device__ __forceinline__ void read_row_f32(uint32_t box, int r, float (&v)[32]) {
 #pragma unroll
@@ -238,52 +243,64 @@ __device__ __forceinline__ void read_row_f32(uint32_t box, int r, float (&v)[32]
     }
 }
 
+// 1 / (1 + e^-g), within a few units of 2^-23: the results are rounded to bf16.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 // a = silu(clamp g) clamp u
 __device__ __forceinline__ float gate_fwd(float g, float u, float c) {
     g = clamp_in(g, c);
     u = clamp_in(u, c);
-    return g / (1.0f + __expf(-g)) * u;
+    return g * sigmoid(g) * u;
 }
 // (dh_g, dh_u) of da
 __device__ __forceinline__ float2 gate_bwd(float da, float g, float u, float c) {
     const float pg = clamp_pass(g, c), pu = clamp_pass(u, c);
     g = clamp_in(g, c);
     u = clamp_in(u, c);
-    const float s = 1.0f / (1.0f + __expf(-g));
-    return make_float2(pg * da * u * s * (1.0f + g * (1.0f - s)), pu * da * g * s);
+    const float s = sigmoid(g), gs = g * s;
+    return make_float2(pg * da * u * (s + gs * (1.0f - s)), pu * da * gs);
+}
+// 32 bf16 of a row: columns [0, n) of it (n >= 8, a multiple of 8).
+__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&p)[16], int n) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (8 * c < n) reinterpret_cast<uint4*>(dst)[c] = make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
 }
 
 template <int EPI>
 __device__ void dense_epilogue(const CUtensorMap* m0, const CUtensorMap* m1, const DenseArgs& p, DenseBars bars,
                                uint32_t tmem, uint32_t stage, volatile int* abort, int warp, int lane, int rank) {
     const uint32_t tempty[2] = {cluster_addr_of(bars.tempty(0), 0), cluster_addr_of(bars.tempty(1), 0)};
+    const int part = warp >> 2, quad = warp & 3;
     int it = 0;
     uint32_t hphase = 0;  // EPI_DGATE: h boxes waited for
-    uint32_t nbox = 0;
     for (DenseWalk<EPI> w(p); w.valid(); w.next(), ++it) {
         const DenseItem item = w.item();
         const int acc = it & 1;
-        const int row0 = item.m0 + 128 * rank + 32 * warp;
+        const int row0 = item.m0 + 128 * rank + 32 * quad;
         const bool rows_live = row0 < p.M;
+        // groups of 32 columns of this tile (gated forms: features), this warp's every other one
+        const int cols = EPI == EPI_GATED || EPI == EPI_PART_GATED ? p.width / 2 : p.width;
+        const int last = cols < p.N - item.n0 ? cols : p.N - item.n0;
         // EPI_DGATE: the first h boxes of the tile come while its products run
-        auto fetch_h = [&](int c32) {
+        auto fetch_h = [&](int c) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(bars.hin(warp), 8192u);
-                tma_load_3d(stage, m1, item.n0 + 32 * c32, 0, row0, bars.hin(warp));
-                tma_load_3d(stage + 4096, m1, item.n0 + 32 * c32, 1, row0, bars.hin(warp));
+                tma_load_3d(stage, m1, item.n0 + 32 * c, 0, row0, bars.hin(warp));
+                tma_load_3d(stage + 4096, m1, item.n0 + 32 * c, 1, row0, bars.hin(warp));
             }
         };
         if constexpr (EPI == EPI_DGATE) {
-            if (rows_live) fetch_h(0);
+            if (rows_live && 32 * part < last) fetch_h(part);
         }
         if (!warp_wait(bars.tfull(acc), (uint32_t)(it >> 1) & 1u, abort)) break;
         tc_fence_after();
-        const uint32_t t = tmem + (uint32_t)(acc * 256) + ((uint32_t)(warp * 32) << 16);
+        const uint32_t t = tmem + (uint32_t)(acc * 256) + ((uint32_t)(quad * 32) << 16);
+        const bool row_live = row0 + lane < p.M;
         bool ok = true;
         if (rows_live) {
             if constexpr (EPI == EPI_PLAIN) {
 #pragma unroll 1
-                for (int c = 0; c < 4 && item.n0 + 64 * c < p.N; ++c) {
+                for (int c = part; 64 * c < last; c += 2) {
                     uint32_t r0[32], r1[32], pk[32];
                     tmem_ld32_nowait(t + 64 * c, r0);
                     tmem_ld32_nowait(t + 64 * c + 32, r1);
@@ -293,88 +310,67 @@ __device__ void dense_epilogue(const CUtensorMap* m0, const CUtensorMap* m1, con
                         pk[j] = pack_bf16x2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
                         pk[16 + j] = pack_bf16x2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
                     }
-                    const uint32_t box = stage + (nbox & 1u) * 4096u;
-                    if (lane == 0) bulk_wait_read<1>();
+                    if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
-                    stage_row_sw128(box, lane, pk);
+                    stage_row_sw128(stage, lane, pk);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_2d(m0, item.n0 + 64 * c, row0, box);
+                        tma_store_2d(m0, item.n0 + 64 * c, row0, stage);
                         bulk_commit();
                     }
-                    ++nbox;
                 }
             } else if constexpr (EPI == EPI_PART || EPI == EPI_PART_GATED) {
-                constexpr bool kGated = EPI == EPI_PART_GATED;
+                constexpr int kHalves = EPI == EPI_PART_GATED ? 2 : 1;
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                    const int half = kGated ? c >> 2 : 0, n = item.n0 + 32 * (kGated ? c & 3 : c);
-                    if (n >= p.N) continue;
+                for (int c = part; c < kHalves * (cols / 32); c += 2) {
+                    const int half = c / (cols / 32), f = 32 * (c - half * (cols / 32));
+                    if (f >= last) continue;
                     uint32_t r0[32];
                     tmem_ld32_nowait(t + 32 * c, r0);
                     tmem_ld_wait();
-                    const uint32_t box = stage + (nbox & 1u) * 4096u;
-                    if (lane == 0) bulk_wait_read<1>();
+                    if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
-                    stage_row_sw128(box, lane, r0);
+                    stage_row_sw128(stage, lane, r0);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_4d(m0, n, half, row0, item.split, box);
+                        tma_store_4d(m0, item.n0 + f, half, row0, item.split, stage);
                         bulk_commit();
                     }
-                    ++nbox;
                 }
             } else if constexpr (EPI == EPI_GATED) {
-                // boxes: 0 a, 1..3 h in turn
 #pragma unroll 1
-                for (int c = 0; c < 4 && item.n0 + 32 * c < p.N; ++c) {
+                for (int c = part; 32 * c < last; c += 2) {
                     uint32_t g[32], u[32], pk[16];
                     tmem_ld32_nowait(t + 32 * c, g);
-                    tmem_ld32_nowait(t + 128 + 32 * c, u);
+                    tmem_ld32_nowait(t + cols + 32 * c, u);
                     tmem_ld_wait();
+                    if (p.save_h) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                        stage_row_sw128(stage, lane, g);
+                        stage_row_sw128(stage + 4096u, lane, u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(m1, item.n0 + 32 * c, 0, row0, stage);
+                            tma_store_3d(m1, item.n0 + 32 * c, 1, row0, stage + 4096u);
+                            bulk_commit();
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         pk[j] = pack_bf16x2(
                             gate_fwd(__uint_as_float(g[2 * j]), __uint_as_float(u[2 * j]), p.clamp),
                             gate_fwd(__uint_as_float(g[2 * j + 1]), __uint_as_float(u[2 * j + 1]), p.clamp));
-                    if (p.save_h) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint32_t box = stage + 4096u * (1u + nbox % 3u);
-                            if (lane == 0) bulk_wait_read<2>();
-                            __syncwarp();
-                            stage_row_sw128(box, lane, half ? u : g);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) {
-                                tma_store_3d(m1, item.n0 + 32 * c, half, row0, box);
-                                bulk_commit();
-                            }
-                            ++nbox;
-                        }
-                    }
-                    if ((c & 1) == 0) {
-                        if (lane == 0) bulk_wait_read<0>();
-                        __syncwarp();
-                    }
-                    stage_half_row(stage, lane, c & 1, pk);
-                    if ((c & 1) || item.n0 + 32 * (c + 1) >= p.N) {  // columns past N are not stored
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_2d(m0, item.n0 + 32 * (c & ~1), row0, stage);
-                            bulk_commit();
-                        }
-                    }
+                    if (row_live)
+                        store_row32(p.out + (size_t)(row0 + lane) * p.N + item.n0 + 32 * c, pk, last - 32 * c);
                 }
             } else {
-                // boxes: 0, 1 h in; 2, 3 dh out (64 columns of each half)
 #pragma unroll 1
-                for (int c = 0; c < 8 && item.n0 + 32 * c < p.N; ++c) {
+                for (int c = part; 32 * c < last; c += 2) {
                     uint32_t da[32], pg[16], pu[16];
-                    tmem_ld32_nowait(t + 32 * c, da);
                     if (!warp_wait(bars.hin(warp), hphase, abort)) {
                         ok = false;
                         break;
@@ -384,7 +380,9 @@ __device__ void dense_epilogue(const CUtensorMap* m0, const CUtensorMap* m1, con
                     read_row_f32(stage, lane, g);
                     read_row_f32(stage + 4096u, lane, u);
                     __syncwarp();
-                    if (c + 1 < 8 && item.n0 + 32 * (c + 1) < p.N) fetch_h(c + 1);
+                    if (32 * (c + 2) < last) fetch_h(c + 2);
+                    // no code between: the registers hold nothing until the wait
+                    tmem_ld32_nowait(t + 32 * c, da);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -393,20 +391,10 @@ __device__ void dense_epilogue(const CUtensorMap* m0, const CUtensorMap* m1, con
                         pg[j] = pack_bf16x2(d0.x, d1.x);
                         pu[j] = pack_bf16x2(d0.y, d1.y);
                     }
-                    if ((c & 1) == 0) {
-                        if (lane == 0) bulk_wait_read<0>();
-                        __syncwarp();
-                    }
-                    stage_half_row(stage + 8192u, lane, c & 1, pg);
-                    stage_half_row(stage + 12288u, lane, c & 1, pu);
-                    if ((c & 1) || item.n0 + 32 * (c + 1) >= p.N) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_3d(m0, item.n0 + 32 * (c & ~1), 0, row0, stage + 8192u);
-                            tma_store_3d(m0, item.n0 + 32 * (c & ~1), 1, row0, stage + 12288u);
-                            bulk_commit();
-                        }
+                    if (row_live) {
+                        __nv_bfloat16* out = p.out + (size_t)(row0 + lane) * 2 * p.N + item.n0 + 32 * c;
+                        store_row32(out, pg, last - 32 * c);
+                        store_row32(out + p.N, pu, last - 32 * c);
                     }
                 }
             }
@@ -420,8 +408,9 @@ __device__ void dense_epilogue(const CUtensorMap* m0, const CUtensorMap* m1, con
     __syncwarp();
 }
 
-// Maps: a, b operands; c0 output (EPI_GATED: a; EPI_DGATE: dh; EPI_PART: the
-// partial sums); c1 h (EPI_GATED: store, EPI_DGATE: load).
+// Maps: a, b operands; c0 output (EPI_PLAIN) or partial sums (EPI_PART); c1 h
+// (EPI_GATED: store, EPI_DGATE: load).  a and dh leave by plain stores, 64
+// contiguous bytes per row and thread.
 template <int MODE, int EPI>
 __global__ void __launch_bounds__(kDenseThreads, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
@@ -432,10 +421,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t boxes = base + kStages * kDenseStageBytes;
-    const uint32_t bar0 = boxes + kEpiWarps * dense_boxes<EPI>() * 4096;
+    const uint32_t bar0 = boxes + kDenseEpiWarps * dense_boxes<EPI>() * 4096;
     uint8_t* tail = smem_raw + (bar0 - raw);
     const DenseBars bars{bar0, kStages};
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 8 * (2 * kStages + 5 + kEpiWarps));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 8 * (2 * kStages + 5 + kDenseEpiWarps));
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
@@ -446,10 +435,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bars.tfull(a), 1);
-            mbar_init(bars.tempty(a), 2 * kEpiWarps);
+            mbar_init(bars.tempty(a), 2 * kDenseEpiWarps);
         }
         mbar_init(bars.drain(), 1);
-        for (int w = 0; w < kEpiWarps; ++w) mbar_init(bars.hin(w), 1);
+        for (int w = 0; w < kDenseEpiWarps; ++w) mbar_init(bars.hin(w), 1);
         *abort = 0;
         fence_mbar_init();
     }
@@ -460,8 +449,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if (warp == kDenseWarpTma && lane == 0) {
         tma_prefetch_map(&mA);
         tma_prefetch_map(&mB);
-        tma_prefetch_map(&mC0);
-        if (EPI == EPI_GATED || EPI == EPI_DGATE) tma_prefetch_map(&mC1);
+        tma_prefetch_map(EPI == EPI_GATED || EPI == EPI_DGATE ? &mC1 : &mC0);
     }
     tc_fence_before();
     cluster_sync();
@@ -581,6 +569,8 @@ int launch_join(const JoinArgs& a, cudaStream_t st) {
 }
 
 // ----------------------------------------------------------------- launches
+int cdiv(long long a, int b) { return (int)((a + b - 1) / b); }
+
 template <int MODE, int EPI>
 int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaStream_t st) {
     static std::atomic<int> clusters_fit[kMaxDevices] = {};
@@ -623,7 +613,6 @@ int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaS
     return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
 
-int cdiv(long long a, int b) { return (int)((a + b - 1) / b); }
 
 // K ranges: as many as give every pair of SMs a tile, of at least four K
 // blocks (256 deep), where the tiles alone would leave more than half idle.
@@ -634,17 +623,39 @@ int dense_splits(int tiles, int kblocks) {
     return s > 1 ? s : 1;
 }
 
+// Columns of a tile (gated: of both halves): the rounds of tiles that the pairs
+// take, times the operand bytes of a tile's K block (256 rows and w columns):
+// at 64 bytes per clock and SM these, not the products, are what a narrower
+// tile runs at (4096 x 2048 x 2816: three rounds at 256 54 us, five at 128
+// 58 us).  256 on a tie.
+int dense_width(int M, int N, bool gated) {
+    int best = 256;
+    long long cost = -1;
+    for (int w = 256; w >= 128; w -= gated ? 128 : 64) {
+        const long long tiles = (long long)cdiv(M, 256) * cdiv(N, gated ? w / 2 : w);
+        const long long c = (tiles + kDenseClusters - 1) / kDenseClusters * (w + 256);
+        if (cost < 0 || c < cost) {
+            cost = c;
+            best = w;
+        }
+    }
+    return best;
+}
+
 // One product of the block.
 struct Product {
     int M, N, K;            // N: columns, or features of one half
     bool gated;             // B's columns are [2][N]
+    bool may_split = true;
     long long bytes() const {  // of the partial sums (0: one K range)
         const int s = splits();
         return s > 1 ? (long long)s * M * (gated ? 2 : 1) * N * 4 : 0;
     }
     int tiles_m() const { return cdiv(M, 256); }
-    int tiles_n() const { return cdiv(N, gated ? 128 : 256); }
-    int splits() const { return dense_splits(tiles_m() * tiles_n(), cdiv(K, 64)); }
+    // K is split over tiles of the full width; where it is not, the width is chosen
+    int splits() const { return may_split ? dense_splits(tiles_m() * cdiv(N, gated ? 128 : 256), cdiv(K, 64)) : 1; }
+    int width() const { return splits() > 1 ? 256 : dense_width(M, N, gated); }
+    int tiles_n() const { return cdiv(N, gated ? width() / 2 : width()); }
     DenseArgs args(float clamp, int32_t* status) const {
         DenseArgs a = {};
         a.M = M;
@@ -653,6 +664,7 @@ struct Product {
         a.tiles_n = tiles_n();
         a.kblocks = cdiv(K, 64);
         a.splits = 1;
+        a.width = width();
         a.clamp = clamp;
         a.status = status;
         return a;
@@ -696,7 +708,7 @@ int launch_ffn_forward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st
             e = launch_dense<KN, EPI_PART_GATED>(a, m, "ffn_gate_up", st);
             if (!e) e = launch_join<JOIN_GATED>({f.part, s.T, s.I, a.splits, 2, clamp, f.a, f.h}, st);
         } else {
-            if ((rc = map_op(&m.c0, f.a, s.T, s.I, 32, "a (store)"))) return rc;
+            a.out = static_cast<__nv_bfloat16*>(f.a);
             if (f.h && (rc = abi_map_nd(&m.c1, f.h, 4, {s.I, 2, s.T}, {32, 1, 32}, "h (store)"))) return rc;
             e = launch_dense<KN, EPI_GATED>(a, m, "ffn_gate_up", st);
         }
@@ -728,21 +740,21 @@ int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t s
         DenseArgs a = q.args(clamp, f.status);
         DenseMaps m = {};
         if ((rc = map_op(&m.a, f.dY, s.T, s.H, 128, "dY"))) return rc;
-        if ((rc = map_op(&m.b, f.W2, s.I, s.H, 128, "W2 (K-major)"))) return rc;
+        if ((rc = map_op(&m.b, f.W2, s.I, s.H, a.width / 2, "W2 (K-major)"))) return rc;
         if (q.splits() > 1) {
             a.splits = q.splits();
             if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.I, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
             e = launch_dense<KK, EPI_PART>(a, m, "ffn_dgate", st);
             if (!e) e = launch_join<JOIN_DGATE>({f.part, s.T, s.I, a.splits, 1, clamp, f.dh, f.h}, st);
         } else {
-            if ((rc = abi_map_nd(&m.c0, f.dh, 2, {s.I, 2, s.T}, {64, 1, 32}, "dh (store)"))) return rc;
+            a.out = static_cast<__nv_bfloat16*>(f.dh);
             if ((rc = abi_map_nd(&m.c1, f.h, 4, {s.I, 2, s.T}, {32, 1, 32}, "h"))) return rc;
             e = launch_dense<KK, EPI_DGATE>(a, m, "ffn_dgate", st);
         }
         if (e) return abi_cuda_fail(e, "dh launch");
     }
     {  // dW2 = a^T dY
-        const Product q = {s.I, s.H, s.T, false};
+        const Product q = {s.I, s.H, s.T, false, false};
         DenseMaps m = {};
         if ((rc = map_op(&m.a, f.a, s.T, s.I, 64, "a (MN-major)"))) return rc;
         if ((rc = map_op(&m.b, f.dY, s.T, s.H, 64, "dY (MN-major)"))) return rc;
@@ -750,7 +762,7 @@ int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t s
         if ((e = launch_dense<NN, EPI_PLAIN>(q.args(clamp, f.status), m, "ffn_dw2", st))) return abi_cuda_fail(e, "dW2 launch");
     }
     {  // dW1 = x^T dh
-        const Product q = {s.H, 2 * s.I, s.T, false};
+        const Product q = {s.H, 2 * s.I, s.T, false, false};
         DenseMaps m = {};
         if ((rc = map_op(&m.a, f.x, s.T, s.H, 64, "x (MN-major)"))) return rc;
         if ((rc = map_op(&m.b, f.dh, s.T, 2 * s.I, 64, "dh (MN-major)"))) return rc;
@@ -762,7 +774,7 @@ int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t s
     DenseArgs a = q.args(clamp, f.status);
     DenseMaps m = {};
     if ((rc = map_op(&m.a, f.dh, s.T, 2 * s.I, 128, "dh"))) return rc;
-    if ((rc = map_op(&m.b, f.W1, s.H, 2 * s.I, 128, "W1 (K-major)"))) return rc;
+    if ((rc = map_op(&m.b, f.W1, s.H, 2 * s.I, a.width / 2, "W1 (K-major)"))) return rc;
     if (q.splits() > 1) {
         a.splits = q.splits();
         if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.H, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
