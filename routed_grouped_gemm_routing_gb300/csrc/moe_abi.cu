@@ -351,6 +351,14 @@ int abi_map_nd(CUtensorMap* m, const void* p, int elt, std::initializer_list<lon
                     elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
+int abi_map_u8(CUtensorMap* m, const void* p, long long rows, long long cols, int box_cols, int box_rows,
+               const char* what) {
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t str[1] = {(cuuint64_t)cols};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    return make_map(m, p, 2, dims, str, box, what, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
 int compute_layout(const moe_shape* s, moe_layout* L) {
     memset(L, 0, sizeof *L);
     const long long tk = (long long)s->T * s->k;

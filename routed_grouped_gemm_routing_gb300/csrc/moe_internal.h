@@ -96,6 +96,10 @@ int abi_map_2d(CUtensorMap* m, const void* p, int elt, long long rows, long long
 int abi_map_nd(CUtensorMap* m, const void* p, int elt, std::initializer_list<long long> dims,
                std::initializer_list<int> box, const char* what);
 
+// A row-major matrix of bytes, 128-byte swizzle, boxes of box_cols (128) bytes.
+int abi_map_u8(CUtensorMap* m, const void* p, long long rows, long long cols, int box_cols, int box_rows,
+               const char* what);
+
 // ------------------------------------------------------------- layer norm
 struct LnFwdArgs {
     long long rows;

@@ -22,26 +22,29 @@
 // that lane t's pair m of group j meets x[32 j + 8 t + 2 m, + 1].
 //
 // A block takes a job (up to 8 NT rows that use the same matrix) and a range
-// of tiles of 32 rows of W (W4_GATED: 16 gate rows and their 16 up rows); KS of its warps share a tile, every KS-th 128-code block
-// each, and join their FP32 sums in shared memory in a fixed order.  Every lane
-// copies its own weights several blocks ahead with cp.async into its own slots
-// (no barrier in the stream), across the tiles of its range.
-#include "moe_internal.h"
-#include "ptx.cuh"
+// of tiles of 32 rows of W (W4_GATED: 16 gate rows and their 16 up rows); KS
+// of its warps share a tile, every KS-th unit of 256 codes each, and join their
+// FP32 sums in shared memory in a fixed order.  One lane copies its warp's next
+// units ahead by TMA (a 32 x 128-byte box in the 128-byte swizzle, so that the
+// fragments' 16-byte reads spread over the banks), across the tiles of the
+// range: with a 16-byte copy per lane and fragment instead, the addresses alone
+// took as many instructions as the products.  Scales come by plain loads, one
+// row per lane and a unit ahead, and go to the fragments by shuffles.
+#include "grouped_gemm_2sm.cuh"
 #include "smem_limit.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kDepth = 3;  // 128-code blocks held or in flight per warp
-constexpr int kFrag = 4;    // 8-row fragments of a tile: two 16-row operands of the products
+constexpr int kSlots = 2;         // units of 256 codes held or in flight per warp
+constexpr int kUnitBytes = 4096;  // 32 rows x 128 bytes
+constexpr int kFrag = 4;          // 8-row fragments of a tile: two 16-row operands of the products
 
 enum W4Epi { W4_PLAIN, W4_GATED, W4_SLOT };
 
 struct W4Args {
     const __nv_bfloat16* x;  // [rows, K]
-    const uint8_t* q;        // [E][N][K / 2]
     const __nv_bfloat16* sf;  // [E][N][K / G]
     int N;       // rows of one matrix (W4_GATED: 2 I)
     int F;       // output features: N, or I
@@ -79,38 +82,71 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
     return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
 }
 
-// Bytes of the parts of a block's shared memory.
+// Byte offsets in a block's shared memory (from its first 1024-byte boundary).
 struct W4Smem {
-    int x, xs, ring, sring, red, total;
+    int x, xs, red, bars, total;
 };
 template <int NT, int G>
 __host__ __device__ __forceinline__ W4Smem w4_smem(int K, int nw, int rows) {
     W4Smem s;
-    s.x = 0;
+    s.x = nw * kSlots * kUnitBytes;
     // a row of x and 64 bytes: the eight rows' 16-byte fragments in all banks
-    const int xbytes = rows * (2 * K + 64);
-    s.xs = xbytes;
-    s.ring = (s.xs + (K / G) * 8 * NT * 4 + 15) / 16 * 16;
-    s.sring = s.ring + nw * kDepth * kFrag * 32 * 16;
-    s.red = s.sring + nw * kDepth * kFrag * 32 * (G == 32 ? 8 : 4);
-    s.total = s.red + 2 * nw * 2 * NT * 128 * 4;
+    s.xs = s.x + rows * (2 * K + 64);
+    s.red = s.xs + (K / G) * 8 * NT * 4;
+    s.bars = s.red + 2 * nw * 2 * NT * 128 * 4;
+    s.total = s.bars + nw * kSlots * 8 + 1024;
     return s;
 }
 
+// The scales of one 128-code block of a row.
+template <int G>
+struct W4Scales;
+template <>
+struct W4Scales<128> {
+    typedef uint16_t T;
+};
+template <>
+struct W4Scales<64> {
+    typedef uint32_t T;
+};
+template <>
+struct W4Scales<32> {
+    typedef uint2 T;
+};
+__device__ __forceinline__ void scales_of(uint16_t v, int src, float (&f)[1]) {
+    f[0] = __uint_as_float(__shfl_sync(0xffffffffu, (uint32_t)v, src) << 16);
+}
+__device__ __forceinline__ void scales_of(uint32_t v, int src, float (&f)[2]) {
+    const uint32_t u = __shfl_sync(0xffffffffu, v, src);
+    f[0] = __uint_as_float(u << 16);
+    f[1] = __uint_as_float(u & 0xffff0000u);
+}
+__device__ __forceinline__ void scales_of(uint2 v, int src, float (&f)[4]) {
+    const uint32_t a = __shfl_sync(0xffffffffu, v.x, src), b = __shfl_sync(0xffffffffu, v.y, src);
+    f[0] = __uint_as_float(a << 16);
+    f[1] = __uint_as_float(a & 0xffff0000u);
+    f[2] = __uint_as_float(b << 16);
+    f[3] = __uint_as_float(b & 0xffff0000u);
+}
+
+// mq: the codes as [E N] rows of K / 2 bytes.
 template <int NT, int G, int EPI>
-__global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
+__global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUtensorMap mq, const W4Args p) {
     constexpr int kR = 8 * NT;
-    const int R = p.R;  // rows of a job, at most kR
-    constexpr int kSpb = 128 / G;        // scales per 128-code block
-    constexpr int kSBytes = G == 32 ? 8 : 4;
+    constexpr int kSpb = 128 / G;                     // scales per 128-code block
     constexpr int kTile = EPI == W4_GATED ? 16 : 32;  // output features of a tile
-    extern __shared__ __align__(16) uint8_t smem[];
+    typedef typename W4Scales<G>::T Scales;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ int row_of[kR];  // row or slot of every row of the job
     __shared__ int job_n;
+    __shared__ int abort_word;
+    volatile int* abort = &abort_word;
+    const int R = p.R;  // rows of a job, at most kR
     const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int K = p.K, KB = K / 128, KS = p.ks, NG = nw / KS;
+    const int K = p.K, KB = K / 128, U = (KB + 1) / 2, KS = p.ks, NG = nw / KS;
     const int ks = warp % KS, gi = warp / KS;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the job: its matrix and its rows
     int e = 0;
@@ -137,82 +173,84 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
         if (threadIdx.x < R) row_of[threadIdx.x] = r0 + threadIdx.x;
         if (threadIdx.x == 0) job_n = p.rows - r0 < R ? p.rows - r0 : R;
     }
+    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    // (the offsets of the block's largest job: they do not wait for job_n)
+    const W4Smem L = w4_smem<NT, G>(K, nw, R);
+    const uint32_t ring = base + warp * kSlots * kUnitBytes, bar = base + L.bars + warp * kSlots * 8;
+    if (lane == 0) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(bar + 8 * i, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) *abort = 0;
     __syncthreads();
     const int n = job_n;
     if (n == 0) return;  // not the leading slot
 
-    const W4Smem L = w4_smem<NT, G>(K, nw, n);
     __nv_bfloat16* xsm = reinterpret_cast<__nv_bfloat16*>(smem + L.x);
     float* xs = reinterpret_cast<float*>(smem + L.xs);  // [K / G][kR]: -136 sum of x
-    const uint4* ring = reinterpret_cast<const uint4*>(smem + L.ring) + warp * kDepth * kFrag * 32 + lane;
-    const uint8_t* sring = smem + L.sring + (warp * kDepth * kFrag * 32 + lane) * kSBytes;
     float* red = reinterpret_cast<float*>(smem + L.red);
 
-    // ---- the stream of this lane's weights: tiles gi, gi + NG, .. of the
-    // block's range, blocks ks, ks + KS, .. of each
+    // ---- the stream of this warp's weights: tiles gi, gi + NG, .. of the
+    // block's range, units ks, ks + KS, .. of each.  Rows past the last of the
+    // matrix are another's or zeros, and are not stored.
     const int tile0 = blockIdx.x * p.tpc;
     const int tile1 = tile0 + p.tpc < p.tiles ? tile0 + p.tpc : p.tiles;
-    // Feature and row of this lane's i-th fragment.  A row past the last is
-    // read as the last and not stored.
-    auto row_index = [&](int tile, int i) {
-        const int f = tile * kTile + g + 8 * (EPI == W4_GATED ? i & 1 : i);
-        return (f < p.F ? f : p.F - 1) + (EPI == W4_GATED ? (i >> 1) * p.F : 0);
-    };
-    // One scale per block (G = 128) comes as the aligned pair that holds it;
-    // odd: the matrix starts at the second of a pair.
-    const size_t sf0 = (size_t)e * p.N * (K / G);
-    const uint32_t odd = G == 128 ? (uint32_t)(sf0 & 1) : 0u;
-    const uint4* q = reinterpret_cast<const uint4*>(p.q) + (size_t)e * p.N * (K / 32) + t;
-    const __nv_bfloat16* sf = p.sf + sf0 - odd;
-    // the last scale of all, where it is the first of a pair whose second does not exist
-    const uint32_t lone = e == p.E - 1 ? (uint32_t)(p.N * KB - 1) + odd : 0xffffffffu;
-    const uint32_t ring_s = smem_addr(ring), sring_s = smem_addr(sring);
-    int ft = tile0 + gi, fb = ks, fslot = 0;
-    uint32_t qo[kFrag], so[kFrag];  // offsets of the next block: 16-byte units, scales
-    auto start_tile = [&]() {
-#pragma unroll
-        for (int i = 0; i < kFrag; ++i) {
-            const uint32_t row = (uint32_t)row_index(ft, i);
-            qo[i] = row * (uint32_t)(K / 32) + 4 * ks;
-            so[i] = row * (uint32_t)(K / G) + kSpb * ks + odd;
-        }
-    };
-    start_tile();
+    const long long row0 = (long long)e * p.N;
+    int ft = tile0 + gi, fu = ks, fslot = 0;
     auto fetch = [&]() {
-        if (ft < tile1 && fb < KB) {
-#pragma unroll
-            for (int i = 0; i < kFrag; ++i) {
-                const uint32_t at = (uint32_t)(fslot * kFrag + i) * 32u;
-                cp_async_16(ring_s + at * 16u, q + qo[i], 16u);
-                const uint32_t sdst = sring_s + at * kSBytes;
-                if constexpr (G == 32) {
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(sdst), "l"(sf + so[i]) : "memory");
-                } else if constexpr (G == 64) {
-                    cp_async_4(sdst, sf + so[i], 4u);
+        if (ft < tile1 && fu < U) {
+            if (lane == 0) {
+                const uint32_t b = bar + 8 * fslot, dst = ring + fslot * kUnitBytes;
+                const int y = (int)(row0 + ft * kTile);
+                mbar_arrive_expect_tx(b, kUnitBytes);
+                if constexpr (EPI == W4_GATED) {
+                    tma_load_2d(dst, &mq, fu * 128, y, b);
+                    tma_load_2d(dst + kUnitBytes / 2, &mq, fu * 128, y + p.F, b);
                 } else {
-                    cp_async_4(sdst, sf + (so[i] & ~1u), so[i] == lone && !(lone & 1u) ? 2u : 4u);
+                    tma_load_2d(dst, &mq, fu * 128, y, b);
                 }
-                qo[i] += 4 * KS;
-                so[i] += kSpb * KS;
             }
-            fb += KS;
-            if (fb >= KB) {
-                fb = ks;
+            fu += KS;
+            if (fu >= U) {
+                fu = ks;
                 ft += NG;
-                start_tile();
             }
         }
-        cp_async_commit();
-        fslot = fslot + 1 == kDepth ? 0 : fslot + 1;
+        fslot = fslot + 1 == kSlots ? 0 : fslot + 1;
     };
-#pragma unroll
-    for (int d = 0; d < kDepth - 1; ++d) fetch();
+    for (int d = 0; d < kSlots - 1; ++d) fetch();
+    // scales of row `lane` of the tile (clamped: a row past the last is not stored)
+    const __nv_bfloat16* sf = p.sf + row0 * (K / G);
+    int st = tile0 + gi, su = ks;
+    const Scales* srow = nullptr;
+    auto scale_row = [&]() {
+        const int f = st * kTile + (EPI == W4_GATED ? lane & 15 : lane);
+        const size_t row = (size_t)(f < p.F ? f : p.F - 1) + (EPI == W4_GATED && lane >= 16 ? p.F : 0);
+        srow = reinterpret_cast<const Scales*>(sf + row * (K / G));
+    };
+    Scales snext[2] = {};
+    auto fetch_scales = [&]() {
+        if (st < tile1 && su < U) {
+            snext[0] = __ldg(srow + 2 * su);
+            if (2 * su + 1 < KB) snext[1] = __ldg(srow + 2 * su + 1);
+            su += KS;
+            if (su >= U) {
+                su = ks;
+                st += NG;
+                scale_row();
+            }
+        }
+    };
+    scale_row();
+    fetch_scales();
 
     // ---- x and its group sums
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // x may be the previous kernel's
     const int xst = K + 32;  // elements between rows of x in shared memory
     for (int v = threadIdx.x; v < n * (K / 8); v += blockDim.x) {  // K / 8 is a multiple of 16: whole groups per row
         const int r = v / (K / 8), c = v - r * (K / 8);
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(row_of[r] / p.xdiv) * K) + c);
+        const uint4 u = *(reinterpret_cast<const uint4*>(p.x + (size_t)(row_of[r] / p.xdiv) * K) + c);
         *reinterpret_cast<uint4*>(xsm + r * xst + c * 8) = u;
         float f[8], s = 0.0f;
         unpack_bf16x8(u, f);
@@ -245,7 +283,10 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
     };
 
     const uint32_t mask = p.mask;
+    // 16-byte chunk 4 h + t of this lane's row of a fragment: swizzled by the row
+    const uint32_t chunk[2] = {(uint32_t)(g * 128 + ((t ^ g) << 4)), (uint32_t)(g * 128 + (((4 + t) ^ g) << 4))};
     int slot = 0, buf = 0;
+    uint32_t phase = 0;
     for (int tile = tile0 + gi; tile < tile1; tile += NG) {
         float acc[2][NT][4];
 #pragma unroll
@@ -254,85 +295,77 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.0f;
-        // G = 128: byte selectors that move the block's scale of the pair to the high half
-        uint32_t sel[kFrag];
-        if constexpr (G == 128) {
+        for (int u = ks; u < U; u += KS) {
+            const Scales sc2[2] = {snext[0], snext[1]};
+            fetch_scales();
+            fetch();
+            // a wait that gave up leaves NaN in the outputs and lets the others go
+            if (!warp_wait(bar + 8 * slot, phase, abort)) {
 #pragma unroll
-            for (int i = 0; i < kFrag; ++i)
-                sel[i] = ((uint32_t)row_index(tile, i) * KB + ks + odd) & 1u ? 0x3244u : 0x1044u;
-        }
-        for (int kb = ks; kb < KB; kb += KS) {
-            cp_async_wait_group<kDepth - 2>();
-            uint4 w[kFrag];
-            float sc[kFrag][kSpb];
+                for (int i = 0; i < 8 * NT; ++i) acc[i / (4 * NT)][i / 4 % NT][i % 4] = __uint_as_float(0x7fc00000u);
+            }
+            const uint32_t unit = ring + slot * kUnitBytes;
 #pragma unroll
-            for (int i = 0; i < kFrag; ++i) {
-                w[i] = ring[(slot * kFrag + i) * 32];
-                const uint8_t* s = sring + (slot * kFrag + i) * 32 * kSBytes;
-                if constexpr (G == 128) {
-                    sc[i][0] = __uint_as_float(__byte_perm(*reinterpret_cast<const uint32_t*>(s), 0u, sel[i]));
-                    if (KS & 1) sel[i] ^= 0x2200u;  // 0x3244 <-> 0x1044
-                } else {
-                    uint32_t u[kSpb / 2];
-                    if constexpr (G == 32) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(s);
-                        u[0] = v.x;
-                        u[1] = v.y;
-                    } else {
-                        u[0] = *reinterpret_cast<const uint32_t*>(s);
+            for (int h = 0; h < 2; ++h) {
+                const int kb = 2 * u + h;
+                if (kb >= KB) break;
+                uint4 w[kFrag];
+                float sc[kFrag][kSpb];
+#pragma unroll
+                for (int i = 0; i < kFrag; ++i) {
+                    const int4 v = ld_shared_v4s(unit + i * 1024 + chunk[h]);
+                    w[i] = make_uint4(v.x, v.y, v.z, v.w);
+                    scales_of(sc2[h], g + 8 * i, sc[i]);
+                }
+                float c[2][NT][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j % (G / 32) == 0) {
+                        const float* xg = xs + ((kb * 128 + j * 32) / G) * kR + 2 * t;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float2 v = *reinterpret_cast<const float2*>(xg + 8 * nt);
+#pragma unroll
+                            for (int rt = 0; rt < 2; ++rt) {
+                                c[rt][nt][0] = c[rt][nt][2] = v.x;
+                                c[rt][nt][1] = c[rt][nt][3] = v.y;
+                            }
+                        }
                     }
+                    uint4 b[NT];
 #pragma unroll
-                    for (int h = 0; h < kSpb / 2; ++h) {
-                        sc[i][2 * h] = __uint_as_float(u[h] << 16);
-                        sc[i][2 * h + 1] = __uint_as_float(u[h] & 0xffff0000u);
+                    for (int nt = 0; nt < NT; ++nt) b[nt] = xrow[nt][kb * 16 + j * 4];
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt) {
+                        const uint32_t a0 = word_of(w[2 * rt], j), a1 = word_of(w[2 * rt + 1], j);
+                        const uint32_t u0 = pair128<0>(a0, mask), u1 = pair128<1>(a0, mask), u2 = pair128<2>(a0, mask),
+                                       u3 = pair128<3>(a0, mask);
+                        const uint32_t v0 = pair128<0>(a1, mask), v1 = pair128<1>(a1, mask), v2 = pair128<2>(a1, mask),
+                                       v3 = pair128<3>(a1, mask);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_bf16(c[rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y);
+                            mma_bf16(c[rt][nt], u2, v2, u3, v3, b[nt].z, b[nt].w);
+                        }
+                    }
+                    if ((j + 1) % (G / 32) == 0) {
+                        const int si = j / (G / 32);
+#pragma unroll
+                        for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                acc[rt][nt][0] = fmaf(sc[2 * rt][si], c[rt][nt][0], acc[rt][nt][0]);
+                                acc[rt][nt][1] = fmaf(sc[2 * rt][si], c[rt][nt][1], acc[rt][nt][1]);
+                                acc[rt][nt][2] = fmaf(sc[2 * rt + 1][si], c[rt][nt][2], acc[rt][nt][2]);
+                                acc[rt][nt][3] = fmaf(sc[2 * rt + 1][si], c[rt][nt][3], acc[rt][nt][3]);
+                            }
                     }
                 }
             }
-            fetch();
-            slot = slot + 1 == kDepth ? 0 : slot + 1;
-            float c[2][NT][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j % (G / 32) == 0) {
-                    const float* xg = xs + ((kb * 128 + j * 32) / G) * kR + 2 * t;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float2 v = *reinterpret_cast<const float2*>(xg + 8 * nt);
-#pragma unroll
-                        for (int rt = 0; rt < 2; ++rt) {
-                            c[rt][nt][0] = c[rt][nt][2] = v.x;
-                            c[rt][nt][1] = c[rt][nt][3] = v.y;
-                        }
-                    }
-                }
-                uint4 b[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) b[nt] = xrow[nt][kb * 16 + j * 4];
-#pragma unroll
-                for (int rt = 0; rt < 2; ++rt) {
-                    const uint32_t u = word_of(w[2 * rt], j), v = word_of(w[2 * rt + 1], j);
-                    const uint32_t u0 = pair128<0>(u, mask), u1 = pair128<1>(u, mask), u2 = pair128<2>(u, mask),
-                                   u3 = pair128<3>(u, mask);
-                    const uint32_t v0 = pair128<0>(v, mask), v1 = pair128<1>(v, mask), v2 = pair128<2>(v, mask),
-                                   v3 = pair128<3>(v, mask);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16(c[rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y);
-                        mma_bf16(c[rt][nt], u2, v2, u3, v3, b[nt].z, b[nt].w);
-                    }
-                }
-                if ((j + 1) % (G / 32) == 0) {
-                    const int si = j / (G / 32);
-#pragma unroll
-                    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            acc[rt][nt][0] = fmaf(sc[2 * rt][si], c[rt][nt][0], acc[rt][nt][0]);
-                            acc[rt][nt][1] = fmaf(sc[2 * rt][si], c[rt][nt][1], acc[rt][nt][1]);
-                            acc[rt][nt][2] = fmaf(sc[2 * rt + 1][si], c[rt][nt][2], acc[rt][nt][2]);
-                            acc[rt][nt][3] = fmaf(sc[2 * rt + 1][si], c[rt][nt][3], acc[rt][nt][3]);
-                        }
-                }
+            __syncwarp();  // every lane has read the slot before it is filled again
+            if (++slot == kSlots) {
+                slot = 0;
+                phase ^= 1u;
             }
         }
         // register i of lane (g, t) of operand rt and 8-row tile nt: row
@@ -369,12 +402,17 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const W4Args p) {
             buf ^= 1;  // the next tile's sums go to the other half: two tiles on, this barrier has passed
         }
     }
-    cp_async_wait_all();
+    if (*abort) {  // copies in flight land before the block's shared memory goes
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+    }
 }
 
 // y[token] = sum over its slots in order of o[slot], skipping dropped ones.
-__global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict__ o, const int32_t* __restrict__ ids,
+__global__ void __launch_bounds__(256) w4_combine_kernel(const float* o, const int32_t* __restrict__ ids,
                                                          int T, int k, int E, int H, __nv_bfloat16* __restrict__ y) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long n4 = (long long)T * H / 4;
     for (long long v = (long long)blockIdx.x * 256 + threadIdx.x; v < n4; v += (long long)gridDim.x * 256) {
         const int tok = (int)(v * 4 / H), h = (int)(v * 4 - (long long)tok * H);
@@ -382,7 +420,7 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const float* __restrict
         for (int j = 0; j < k; ++j) {
             const int e = __ldg(ids + (size_t)tok * k + j);
             if (e < 0 || e >= E) continue;
-            const float4 a = __ldg(reinterpret_cast<const float4*>(o + ((size_t)tok * k + j) * H + h));
+            const float4 a = *reinterpret_cast<const float4*>(o + ((size_t)tok * k + j) * H + h);
             s.x += a.x;
             s.y += a.y;
             s.z += a.z;
@@ -439,11 +477,11 @@ constexpr int kW4Smem = 224 * 1024;
 
 // Launch shape: warps per tile and tiles per block for blocks of nw warps,
 // per_sm of them on an SM.  What the choice makes small is the longest chain
-// of a warp, in quarters of a 128-code block, over the blocks that run one
-// after the other on an SM: a round of a shared tile costs about one block
-// more (the join), a block's start (job, x) about four.
+// of a warp, in 128-code blocks, over the blocks that run one after the other
+// on an SM: a round of a shared tile costs about one block more (the join), a
+// block's start (job, x) about four.
 void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
-    const int KB = a->K / 128, slots = 152 * per_sm;
+    const int U = (a->K + 255) / 256, slots = 152 * per_sm;
     long long best = -1;
     for (int ks = 1; ks <= nw; ks *= 2) {
         const int ng = nw / ks;
@@ -451,7 +489,7 @@ void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
             const int tpc = ng * rounds;
             const long long blocks = (long long)jobs * ((a->tiles + tpc - 1) / tpc);
             const long long waves = (blocks + slots - 1) / slots;
-            const long long cost = waves * (4 * 4 + rounds * (4 * ((KB + ks - 1) / ks) + (ks > 1 ? 4 : 0)));
+            const long long cost = waves * (4 + rounds * (2 * ((U + ks - 1) / ks) + (ks > 1 ? 1 : 0)));
             if (best < 0 || cost < best) {
                 best = cost;
                 a->ks = ks;
@@ -463,9 +501,11 @@ void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
 }
 
 // rows: rows that can share a job; groups of rows (no ids) or slots (ids) are
-// the jobs.
+// the jobs.  after_own: the kernel before it in the stream is this file's and
+// writes x only, so this one may start, find its job and fetch weights, while
+// that one drains (it waits before it reads x).
 template <int NT, int G, int EPI>
-int w4_launch(W4Args a, int rows, cudaStream_t st) {
+int w4_launch(W4Args a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
     static SmemLimit limit;
     a.mask = 0x000f000fu;
     // as many rows per job as leave room for a block of four warps
@@ -477,22 +517,35 @@ int w4_launch(W4Args a, int rows, cudaStream_t st) {
     const int jobs = a.ids ? a.slots : (a.rows + a.R - 1) / a.R;
     w4_shape(&a, jobs, nw, per_sm);
     if (const int e = limit.allow(w4_kernel<NT, G, EPI>, kW4Smem)) return e;
-    w4_kernel<NT, G, EPI><<<dim3((a.tiles + a.tpc - 1) / a.tpc, jobs), nw * 32, bytes(nw), st>>>(a);
-    return (int)cudaGetLastError();
+    CUtensorMap m;
+    if (abi_map_u8(&m, q, (long long)a.E * a.N, a.K / 2, 128, EPI == W4_GATED ? 16 : 32, "4-bit codes"))
+        return (int)cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((a.tiles + a.tpc - 1) / a.tpc, jobs);
+    cfg.blockDim = dim3(nw * 32);
+    cfg.dynamicSmemBytes = bytes(nw);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_own ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_kernel<NT, G, EPI>, m, a);
+    return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
 // Two 8-row tiles per job where more than 8 rows can share a matrix (and, in
 // shared memory, leave room for eight warps), else one.
 template <int G, int EPI>
-int w4_launch_nt(const W4Args& a, int rows, cudaStream_t st) {
+int w4_launch_nt(const W4Args& a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
     if (rows > 8 && w4_smem<2, G>(a.K, 8, rows < 16 ? rows : 16).total <= kW4Smem)
-        return w4_launch<2, G, EPI>(a, rows, st);
-    return w4_launch<1, G, EPI>(a, rows, st);
+        return w4_launch<2, G, EPI>(a, q, rows, after_own, st);
+    return w4_launch<1, G, EPI>(a, q, rows, after_own, st);
 }
 template <int EPI>
-int w4_launch_g(int G, const W4Args& a, int rows, cudaStream_t st) {
-    return G == 32   ? w4_launch_nt<32, EPI>(a, rows, st)
-           : G == 64 ? w4_launch_nt<64, EPI>(a, rows, st)
-                     : w4_launch_nt<128, EPI>(a, rows, st);
+int w4_launch_g(int G, const W4Args& a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
+    return G == 32   ? w4_launch_nt<32, EPI>(a, q, rows, after_own, st)
+           : G == 64 ? w4_launch_nt<64, EPI>(a, q, rows, after_own, st)
+                     : w4_launch_nt<128, EPI>(a, q, rows, after_own, st);
 }
 
 }  // namespace
@@ -501,7 +554,6 @@ int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q
                      cudaStream_t st) {
     W4Args a = {};
     a.x = static_cast<const __nv_bfloat16*>(x);
-    a.q = q;
     a.sf = static_cast<const __nv_bfloat16*>(sf);
     a.N = a.F = N;
     a.K = K;
@@ -510,13 +562,12 @@ int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q
     a.xdiv = 1;
     a.tiles = (N + 31) / 32;
     a.out = y;
-    return w4_launch_g<W4_PLAIN>(G, a, M, st);
+    return w4_launch_g<W4_PLAIN>(G, a, q, M, false, st);
 }
 
 int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     W4Args a = {};
     a.x = static_cast<const __nv_bfloat16*>(w.x);
-    a.q = w.W1_q;
     a.sf = static_cast<const __nv_bfloat16*>(w.W1_sf);
     a.N = 2 * w.I;
     a.F = w.I;
@@ -528,9 +579,8 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     a.xdiv = w.topk_idx ? w.k : 1;
     a.tiles = (w.I + 15) / 16;
     a.out = w.act;
-    if (const int e = w4_launch_g<W4_GATED>(w.group, a, w.T, st)) return e;
+    if (const int e = w4_launch_g<W4_GATED>(w.group, a, w.W1_q, w.T, false, st)) return e;
     a.x = static_cast<const __nv_bfloat16*>(w.act);
-    a.q = w.W2_q;
     a.sf = static_cast<const __nv_bfloat16*>(w.W2_sf);
     a.N = a.F = w.H;
     a.K = w.I;
@@ -538,15 +588,24 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     a.tiles = (w.H + 31) / 32;
     if (!w.topk_idx) {
         a.out = w.y;
-        return w4_launch_g<W4_PLAIN>(w.group, a, w.T, st);
+        return w4_launch_g<W4_PLAIN>(w.group, a, w.W2_q, w.T, true, st);
     }
     a.slot_w = w.topk_w;
     a.out = w.part;
-    if (const int e = w4_launch_g<W4_SLOT>(w.group, a, w.T, st)) return e;
+    if (const int e = w4_launch_g<W4_SLOT>(w.group, a, w.W2_q, w.T, true, st)) return e;
     const long long blocks = ((long long)w.T * w.H / 4 + 255) / 256;
-    w4_combine_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), 256, 0, st>>>(
-        w.part, w.topk_idx, w.T, w.k, w.E, w.H, static_cast<__nv_bfloat16*>(w.y));
-    return (int)cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(blocks < 1216 ? blocks : 1216));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_combine_kernel, (const float*)w.part, w.topk_idx, w.T, w.k, w.E,
+                                             w.H, static_cast<__nv_bfloat16*>(w.y));
+    return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 int launch_quantize_w4(int E, int K, int N, int G, const void* W, uint8_t* q, void* sf, cudaStream_t st) {
