@@ -30,6 +30,8 @@
 // range: with a 16-byte copy per lane and fragment instead, the addresses alone
 // took as many instructions as the products.  Scales come by plain loads, one
 // row per lane and a unit ahead, and go to the fragments by shuffles.
+#include <cmath>
+
 #include "grouped_gemm_2sm.cuh"
 #include "smem_limit.h"
 
@@ -37,9 +39,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kSlots = 2;         // units of 256 codes held or in flight per warp
+constexpr int kSlots = 2;  // units of 256 codes held or in flight per warp
 constexpr int kUnitBytes = 4096;  // 32 rows x 128 bytes
-constexpr int kFrag = 4;          // 8-row fragments of a tile: two 16-row operands of the products
+// 8-row fragments of a tile: two 16-row operands of the products.  (One operand,
+// 64 registers and 32 warps per SM instead of 16 was slower: 16384 x 7168 at one
+// row 20.6 us against 17.5, twice the bookkeeping and reads of x per weight.)
+constexpr int kFrag = 4;
 
 enum W4Epi { W4_PLAIN, W4_GATED, W4_SLOT };
 
@@ -52,8 +57,9 @@ struct W4Args {
     int rows;    // rows of x (no ids)
     const int32_t* ids;  // expert of each slot, or null: one matrix, rows of x in order
     int slots;   // length of ids
+    int busy;    // jobs to expect of them
     int xdiv;    // x row of a slot = slot / xdiv
-    int tiles;   // ceil(F / 32), W4_GATED: ceil(F / 16)
+    int tiles;   // of F
     int tpc;     // tiles per block
     int ks;      // warps per tile
     int R;       // rows of a job
@@ -64,10 +70,18 @@ struct W4Args {
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The first product of a chain: c = (x, y, x, y) + a b.
+__device__ __forceinline__ void mma_bf16_from(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, float x, float y) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(x), "f"(y));
 }
 // Codes 2 m and 2 m + 1 of a word as the bf16 pair 128 + code.  mask is
 // 0x000f000f in a register: with both constants immediate this takes two
@@ -91,8 +105,9 @@ __host__ __device__ __forceinline__ W4Smem w4_smem(int K, int nw, int rows) {
     W4Smem s;
     s.x = nw * kSlots * kUnitBytes;
     // a row of x and 64 bytes: the eight rows' 16-byte fragments in all banks
-    s.xs = s.x + rows * (2 * K + 64);
-    s.red = s.xs + (K / G) * 8 * NT * 4;
+    const int kpad = (K + 255) / 256 * 256;
+    s.xs = s.x + rows * (2 * kpad + 64);
+    s.red = s.xs + (kpad / G) * 8 * NT * 4;
     s.bars = s.red + 2 * nw * 2 * NT * 128 * 4;
     s.total = s.bars + nw * kSlots * 8 + 1024;
     return s;
@@ -113,28 +128,26 @@ template <>
 struct W4Scales<32> {
     typedef uint2 T;
 };
-__device__ __forceinline__ void scales_of(uint16_t v, int src, float (&f)[1]) {
-    f[0] = __uint_as_float(__shfl_sync(0xffffffffu, (uint32_t)v, src) << 16);
+// The scales of lane src's row, packed, and the i-th of them as a float.
+__device__ __forceinline__ void scales_of(uint16_t v, int src, uint32_t (&u)[1]) {
+    u[0] = __shfl_sync(0xffffffffu, (uint32_t)v, src);
 }
-__device__ __forceinline__ void scales_of(uint32_t v, int src, float (&f)[2]) {
-    const uint32_t u = __shfl_sync(0xffffffffu, v, src);
-    f[0] = __uint_as_float(u << 16);
-    f[1] = __uint_as_float(u & 0xffff0000u);
+__device__ __forceinline__ void scales_of(uint32_t v, int src, uint32_t (&u)[1]) { u[0] = __shfl_sync(0xffffffffu, v, src); }
+__device__ __forceinline__ void scales_of(uint2 v, int src, uint32_t (&u)[2]) {
+    u[0] = __shfl_sync(0xffffffffu, v.x, src);
+    u[1] = __shfl_sync(0xffffffffu, v.y, src);
 }
-__device__ __forceinline__ void scales_of(uint2 v, int src, float (&f)[4]) {
-    const uint32_t a = __shfl_sync(0xffffffffu, v.x, src), b = __shfl_sync(0xffffffffu, v.y, src);
-    f[0] = __uint_as_float(a << 16);
-    f[1] = __uint_as_float(a & 0xffff0000u);
-    f[2] = __uint_as_float(b << 16);
-    f[3] = __uint_as_float(b & 0xffff0000u);
-}
+__device__ __forceinline__ float scale(uint32_t u, int i) { return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16); }
 
 // mq: the codes as [E N] rows of K / 2 bytes.
 template <int NT, int G, int EPI>
 __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUtensorMap mq, const W4Args p) {
     constexpr int kR = 8 * NT;
-    constexpr int kSpb = 128 / G;                     // scales per 128-code block
+    constexpr int kSw = G == 32 ? 2 : 1;              // words of a row's scales of a 128-code block
     constexpr int kTile = EPI == W4_GATED ? 16 : 32;  // output features of a tile
+    // 128-code blocks worked on side by side: both of a unit while the registers
+    // hold their four chains of dependent products
+    constexpr int kSide = NT == 1 ? 2 : 1;
     typedef typename W4Scales<G>::T Scales;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ int row_of[kR];  // row or slot of every row of the job
@@ -233,7 +246,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     auto fetch_scales = [&]() {
         if (st < tile1 && su < U) {
             snext[0] = __ldg(srow + 2 * su);
-            if (2 * su + 1 < KB) snext[1] = __ldg(srow + 2 * su + 1);
+            snext[1] = 2 * su + 1 < KB ? __ldg(srow + 2 * su + 1) : Scales{};
             su += KS;
             if (su >= U) {
                 su = ks;
@@ -247,7 +260,14 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
 
     // ---- x and its group sums
     asm volatile("griddepcontrol.wait;" ::: "memory");  // x may be the previous kernel's
-    const int xst = K + 32;  // elements between rows of x in shared memory
+    // A unit past an odd last block meets zeros: codes beyond the matrix's rows
+    // (filled by the copy), x, its sums and the scales.
+    const int xst = U * 256 + 32;  // elements between rows of x in shared memory
+    if (KB & 1) {
+        for (int v = threadIdx.x; v < n * 16; v += blockDim.x)
+            *reinterpret_cast<uint4*>(xsm + (v >> 4) * xst + K + (v & 15) * 8) = make_uint4(0u, 0u, 0u, 0u);
+        for (int v = threadIdx.x; v < (128 / G) * kR; v += blockDim.x) xs[(K / G) * kR + v] = 0.0f;
+    }
     for (int v = threadIdx.x; v < n * (K / 8); v += blockDim.x) {  // K / 8 is a multiple of 16: whole groups per row
         const int r = v / (K / 8), c = v - r * (K / 8);
         const uint4 u = *(reinterpret_cast<const uint4*>(p.x + (size_t)(row_of[r] / p.xdiv) * K) + c);
@@ -306,59 +326,65 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
             }
             const uint32_t unit = ring + slot * kUnitBytes;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int kb = 2 * u + h;
-                if (kb >= KB) break;
-                uint4 w[kFrag];
-                float sc[kFrag][kSpb];
+            for (int h0 = 0; h0 < 2; h0 += kSide) {
+                uint4 w[kSide][kFrag];
+                uint32_t sc[kSide][kFrag][kSw];
 #pragma unroll
-                for (int i = 0; i < kFrag; ++i) {
-                    const int4 v = ld_shared_v4s(unit + i * 1024 + chunk[h]);
-                    w[i] = make_uint4(v.x, v.y, v.z, v.w);
-                    scales_of(sc2[h], g + 8 * i, sc[i]);
-                }
-                float c[2][NT][4];
+                for (int h = 0; h < kSide; ++h)
+#pragma unroll
+                    for (int i = 0; i < kFrag; ++i) {
+                        const int4 v = ld_shared_v4s(unit + i * 1024 + chunk[h0 + h]);
+                        w[h][i] = make_uint4(v.x, v.y, v.z, v.w);
+                        scales_of(sc2[h0 + h], g + 8 * i, sc[h][i]);
+                    }
+                float c[kSide][2][NT][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (j % (G / 32) == 0) {
-                        const float* xg = xs + ((kb * 128 + j * 32) / G) * kR + 2 * t;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float2 v = *reinterpret_cast<const float2*>(xg + 8 * nt);
+                    for (int h = 0; h < kSide; ++h) {
+                        const int kb = 2 * u + h0 + h;
+                        uint4 b[NT];
 #pragma unroll
-                            for (int rt = 0; rt < 2; ++rt) {
-                                c[rt][nt][0] = c[rt][nt][2] = v.x;
-                                c[rt][nt][1] = c[rt][nt][3] = v.y;
-                            }
+                        for (int nt = 0; nt < NT; ++nt) b[nt] = xrow[nt][kb * 16 + j * 4];
+                        float2 start[NT];
+                        if (j % (G / 32) == 0) {
+                            const float* xg = xs + ((kb * 128 + j * 32) / G) * kR + 2 * t;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) start[nt] = *reinterpret_cast<const float2*>(xg + 8 * nt);
                         }
-                    }
-                    uint4 b[NT];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) b[nt] = xrow[nt][kb * 16 + j * 4];
+                        for (int rt = 0; rt < 2; ++rt) {
+                            const uint32_t a0 = word_of(w[h][2 * rt], j), a1 = word_of(w[h][2 * rt + 1], j);
+                            const uint32_t u0 = pair128<0>(a0, mask), u1 = pair128<1>(a0, mask),
+                                           u2 = pair128<2>(a0, mask), u3 = pair128<3>(a0, mask);
+                            const uint32_t v0 = pair128<0>(a1, mask), v1 = pair128<1>(a1, mask),
+                                           v2 = pair128<2>(a1, mask), v3 = pair128<3>(a1, mask);
 #pragma unroll
-                    for (int rt = 0; rt < 2; ++rt) {
-                        const uint32_t a0 = word_of(w[2 * rt], j), a1 = word_of(w[2 * rt + 1], j);
-                        const uint32_t u0 = pair128<0>(a0, mask), u1 = pair128<1>(a0, mask), u2 = pair128<2>(a0, mask),
-                                       u3 = pair128<3>(a0, mask);
-                        const uint32_t v0 = pair128<0>(a1, mask), v1 = pair128<1>(a1, mask), v2 = pair128<2>(a1, mask),
-                                       v3 = pair128<3>(a1, mask);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_bf16(c[rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y);
-                            mma_bf16(c[rt][nt], u2, v2, u3, v3, b[nt].z, b[nt].w);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if (j % (G / 32) == 0)
+                                    mma_bf16_from(c[h][rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y, start[nt].x,
+                                                  start[nt].y);
+                                else
+                                    mma_bf16(c[h][rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y);
+                                mma_bf16(c[h][rt][nt], u2, v2, u3, v3, b[nt].z, b[nt].w);
+                            }
                         }
                     }
                     if ((j + 1) % (G / 32) == 0) {
                         const int si = j / (G / 32);
 #pragma unroll
-                        for (int rt = 0; rt < 2; ++rt)
+                        for (int h = 0; h < kSide; ++h)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                acc[rt][nt][0] = fmaf(sc[2 * rt][si], c[rt][nt][0], acc[rt][nt][0]);
-                                acc[rt][nt][1] = fmaf(sc[2 * rt][si], c[rt][nt][1], acc[rt][nt][1]);
-                                acc[rt][nt][2] = fmaf(sc[2 * rt + 1][si], c[rt][nt][2], acc[rt][nt][2]);
-                                acc[rt][nt][3] = fmaf(sc[2 * rt + 1][si], c[rt][nt][3], acc[rt][nt][3]);
-                            }
+                            for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const float s0 = scale(sc[h][2 * rt][si / 2], si),
+                                                s1 = scale(sc[h][2 * rt + 1][si / 2], si);
+                                    acc[rt][nt][0] = fmaf(s0, c[h][rt][nt][0], acc[rt][nt][0]);
+                                    acc[rt][nt][1] = fmaf(s0, c[h][rt][nt][1], acc[rt][nt][1]);
+                                    acc[rt][nt][2] = fmaf(s1, c[h][rt][nt][2], acc[rt][nt][2]);
+                                    acc[rt][nt][3] = fmaf(s1, c[h][rt][nt][3], acc[rt][nt][3]);
+                                }
                     }
                 }
             }
@@ -473,23 +499,31 @@ __global__ void __launch_bounds__(128) w4_quantize_kernel(const __nv_bfloat16* _
     for (int t = 0; t < 4; ++t) out[t] = make_uint4(words[4 * t], words[4 * t + 1], words[4 * t + 2], words[4 * t + 3]);
 }
 
-constexpr int kW4Smem = 224 * 1024;
+constexpr int kW4Smem = 224 * 1024;  // dynamic shared memory of a block
+constexpr int kSmSmem = 228 * 1024;  // of an SM, with 1 KB taken by every block
+constexpr int kFewRows = 0;
 
 // Launch shape: warps per tile and tiles per block for blocks of nw warps,
-// per_sm of them on an SM.  What the choice makes small is the longest chain
-// of a warp, in 128-code blocks, over the blocks that run one after the other
-// on an SM: a round of a shared tile costs about one block more (the join), a
-// block's start (job, x) about four.
+// per_sm of them on an SM.  Two times bound a choice, and the larger one is
+// made small: the busiest SM's units at the rate of its warps, and the longest
+// chain of a warp over the blocks that follow one another.  In clocks, fitted
+// to sweeps of both at 1, 8 and 32 tokens: an SM takes 280 per unit with 16
+// warps, 437 with 8; a warp alone 2200; a join 600, and 100 of the SM's per warp
+// of it; a block's start (job, x) 3000 and a fifth per element of x.
 void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
-    const int U = (a->K + 255) / 256, slots = 152 * per_sm;
+    const long long U = (a->K + 255) / 256, slots = 152 * per_sm, start = 3000 + (long long)a->R * a->K / 5;
     long long best = -1;
     for (int ks = 1; ks <= nw; ks *= 2) {
-        const int ng = nw / ks;
+        const int ng = nw / ks, join = ks > 1;
         for (int rounds = 1; rounds <= 64; ++rounds) {
             const int tpc = ng * rounds;
-            const long long blocks = (long long)jobs * ((a->tiles + tpc - 1) / tpc);
-            const long long waves = (blocks + slots - 1) / slots;
-            const long long cost = waves * (4 + rounds * (2 * ((U + ks - 1) / ks) + (ks > 1 ? 1 : 0)));
+            const long long tiles = tpc < a->tiles ? tpc : a->tiles;
+            const long long blocks = (long long)jobs * ((a->tiles + tpc - 1) / tpc), on_sm = (blocks + 151) / 152;
+            const long long warps = (on_sm < per_sm ? on_sm : per_sm) * nw;
+            const long long unit = 3500 / warps > 280 ? 3500 / warps : 280;
+            const long long rate = on_sm * (tiles * (U * unit + join * 100 * ks) + start);
+            const long long lat = (blocks + slots - 1) / slots * (3000 + rounds * (2200 * ((U + ks - 1) / ks) + join * 600));
+            const long long cost = (lat > rate ? lat : rate) * 8 + (lat < rate ? lat : rate);
             if (best < 0 || cost < best) {
                 best = cost;
                 a->ks = ks;
@@ -508,14 +542,15 @@ template <int NT, int G, int EPI>
 int w4_launch(W4Args a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
     static SmemLimit limit;
     a.mask = 0x000f000fu;
+    a.tiles = EPI == W4_GATED ? (a.F + 15) / 16 : (a.F + 31) / 32;
     // as many rows per job as leave room for a block of four warps
     a.R = rows < 8 * NT ? rows : 8 * NT;
     while (a.R > 1 && w4_smem<NT, G>(a.K, 4, a.R).total > kW4Smem) --a.R;
     auto bytes = [&](int nw) { return w4_smem<NT, G>(a.K, nw, a.R).total; };
-    const int per_sm = bytes(8) <= kW4Smem / 2 ? 2 : 1;
+    const int per_sm = 2 * (bytes(8) + 1024) <= kSmSmem ? 2 : 1;
     const int nw = per_sm == 2 ? 8 : bytes(16) <= kW4Smem ? 16 : bytes(8) <= kW4Smem ? 8 : 4;
     const int jobs = a.ids ? a.slots : (a.rows + a.R - 1) / a.R;
-    w4_shape(&a, jobs, nw, per_sm);
+    w4_shape(&a, a.ids ? a.busy : jobs, nw, per_sm);
     if (const int e = limit.allow(w4_kernel<NT, G, EPI>, kW4Smem)) return e;
     CUtensorMap m;
     if (abi_map_u8(&m, q, (long long)a.E * a.N, a.K / 2, 128, EPI == W4_GATED ? 16 : 32, "4-bit codes"))
@@ -560,7 +595,6 @@ int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q
     a.E = 1;
     a.rows = M;
     a.xdiv = 1;
-    a.tiles = (N + 31) / 32;
     a.out = y;
     return w4_launch_g<W4_PLAIN>(G, a, q, M, false, st);
 }
@@ -576,23 +610,30 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     a.rows = w.T;
     a.ids = w.topk_idx;
     a.slots = w.T * w.k;
+    // experts that uniform routing would touch, at most one per slot
+    const double touched = w.E * (1.0 - pow(1.0 - (double)w.k / w.E, (double)w.T));
+    a.busy = touched < 1.0 ? 1 : touched < a.slots ? (int)(touched + 0.5) : a.slots;
     a.xdiv = w.topk_idx ? w.k : 1;
-    a.tiles = (w.I + 15) / 16;
     a.out = w.act;
-    if (const int e = w4_launch_g<W4_GATED>(w.group, a, w.W1_q, w.T, false, st)) return e;
+    // Rows that a job is made for: twice an expert's mean share of the slots,
+    // and one (an expert with more has several jobs).  More would cost shared
+    // memory, so warps, and 16-row products at three rows each: 32 tokens of
+    // top-6 over 64 experts took 138 us at up to 16 rows, 104 us at up to 8.
+    const long long share = w.topk_idx ? (2ll * w.T * w.k + w.E - 1) / w.E + 1 : w.T;
+    const int rows = (int)(share < w.T ? share : w.T);
+    if (const int e = w4_launch_g<W4_GATED>(w.group, a, w.W1_q, rows, false, st)) return e;
     a.x = static_cast<const __nv_bfloat16*>(w.act);
     a.sf = static_cast<const __nv_bfloat16*>(w.W2_sf);
     a.N = a.F = w.H;
     a.K = w.I;
     a.xdiv = 1;
-    a.tiles = (w.H + 31) / 32;
     if (!w.topk_idx) {
         a.out = w.y;
-        return w4_launch_g<W4_PLAIN>(w.group, a, w.W2_q, w.T, true, st);
+        return w4_launch_g<W4_PLAIN>(w.group, a, w.W2_q, rows, true, st);
     }
     a.slot_w = w.topk_w;
     a.out = w.part;
-    if (const int e = w4_launch_g<W4_SLOT>(w.group, a, w.W2_q, w.T, true, st)) return e;
+    if (const int e = w4_launch_g<W4_SLOT>(w.group, a, w.W2_q, rows, true, st)) return e;
     const long long blocks = ((long long)w.T * w.H / 4 + 255) / 256;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
