@@ -21,7 +21,7 @@
 // 32 j + 8 t .. + 7, code 2 m in nibble m, code 2 m + 1 in nibble m + 4, so
 // that lane t's pair m of group j meets x[32 j + 8 t + 2 m, + 1].
 //
-// A block takes a job (up to 8 NT rows that use the same matrix) and a range
+// A block takes a job (up to 8 rows that use the same matrix) and a range
 // of tiles of 32 rows of W (W4_GATED: 16 gate rows and their 16 up rows); KS
 // of its warps share a tile, every KS-th unit of 256 codes each, and join their
 // FP32 sums in shared memory in a fixed order.  One lane copies its warp's next
@@ -45,6 +45,11 @@ constexpr int kUnitBytes = 4096;  // 32 rows x 128 bytes
 // 64 registers and 32 warps per SM instead of 16 was slower: 16384 x 7168 at one
 // row 20.6 us against 17.5, twice the bookkeeping and reads of x per weight.)
 constexpr int kFrag = 4;
+// Rows of a job: the columns of one product.  (Two column tiles per job, the
+// weights unpacked once for 16 rows, took longer than two jobs: 16 rows of a
+// 16384 x 7168 matrix 52.6 us against 39.6; their registers left no room for
+// both blocks of a unit.)
+constexpr int kR = 8;
 
 enum W4Epi { W4_PLAIN, W4_GATED, W4_SLOT };
 
@@ -63,6 +68,7 @@ struct W4Args {
     int tpc;     // tiles per block
     int ks;      // warps per tile
     int R;       // rows of a job
+    int kparts;  // blocks of a cluster that split K
     uint32_t mask;  // 0x000f000f, unknown to the compiler (see pair128)
     const float* slot_w;  // W4_SLOT: weight of each slot
     void* out;   // W4_PLAIN, W4_GATED: bf16 [row or slot][F]; W4_SLOT: f32 [slot][F]
@@ -97,18 +103,21 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
 }
 
 // Byte offsets in a block's shared memory (from its first 1024-byte boundary).
+// kparts: blocks of a cluster that share the tiles and split K; x and its sums
+// are those of a block's own units, and the first block takes all partial sums.
 struct W4Smem {
     int x, xs, red, bars, total;
 };
-template <int NT, int G>
-__host__ __device__ __forceinline__ W4Smem w4_smem(int K, int nw, int rows) {
+__host__ __device__ __forceinline__ int w4_units(int K, int kparts) { return ((K + 255) / 256 + kparts - 1) / kparts; }
+template <int G>
+__host__ __device__ __forceinline__ W4Smem w4_smem(int K, int nw, int rows, int kparts) {
     W4Smem s;
+    const int kpad = w4_units(K, kparts) * 256;
     s.x = nw * kSlots * kUnitBytes;
     // a row of x and 64 bytes: the eight rows' 16-byte fragments in all banks
-    const int kpad = (K + 255) / 256 * 256;
     s.xs = s.x + rows * (2 * kpad + 64);
-    s.red = s.xs + (kpad / G) * 8 * NT * 4;
-    s.bars = s.red + 2 * nw * 2 * NT * 128 * 4;
+    s.red = s.xs + (kpad / G) * kR * 4;
+    s.bars = s.red + (kparts > 1 ? kparts : 2) * nw * 256 * 4;
     s.total = s.bars + nw * kSlots * 8 + 1024;
     return s;
 }
@@ -140,14 +149,11 @@ __device__ __forceinline__ void scales_of(uint2 v, int src, uint32_t (&u)[2]) {
 __device__ __forceinline__ float scale(uint32_t u, int i) { return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16); }
 
 // mq: the codes as [E N] rows of K / 2 bytes.
-template <int NT, int G, int EPI>
+template <int G, int EPI>
 __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUtensorMap mq, const W4Args p) {
-    constexpr int kR = 8 * NT;
     constexpr int kSw = G == 32 ? 2 : 1;              // words of a row's scales of a 128-code block
     constexpr int kTile = EPI == W4_GATED ? 16 : 32;  // output features of a tile
-    // 128-code blocks worked on side by side: both of a unit while the registers
-    // hold their four chains of dependent products
-    constexpr int kSide = NT == 1 ? 2 : 1;
+    constexpr int kSide = G == 32 ? 1 : 2;  // 128-code blocks worked on side by side: four chains of dependent products
     typedef typename W4Scales<G>::T Scales;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ int row_of[kR];  // row or slot of every row of the job
@@ -157,8 +163,12 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     const int R = p.R;  // rows of a job, at most kR
     const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int K = p.K, KB = K / 128, U = (KB + 1) / 2, KS = p.ks, NG = nw / KS;
+    const int K = p.K, KB = K / 128, KS = p.ks, NG = nw / KS;
     const int ks = warp % KS, gi = warp / KS;
+    // this block's units [U0, U) and elements [k0, k0 + kn) of K
+    const int part = blockIdx.z, per = w4_units(K, p.kparts), U0 = part * per;
+    const int U = U0 + per < (KB + 1) / 2 ? U0 + per : (KB + 1) / 2;
+    const int k0 = U0 * 256, kn = (U * 256 < K ? U * 256 : K) - k0;  // w4_launch splits so that every part has units
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the job: its matrix and its rows
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     // (the offsets of the block's largest job: they do not wait for job_n)
-    const W4Smem L = w4_smem<NT, G>(K, nw, R);
+    const W4Smem L = w4_smem<G>(K, nw, R, p.kparts);
     const uint32_t ring = base + warp * kSlots * kUnitBytes, bar = base + L.bars + warp * kSlots * 8;
     if (lane == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(bar + 8 * i, 1);
@@ -210,7 +220,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     const int tile0 = blockIdx.x * p.tpc;
     const int tile1 = tile0 + p.tpc < p.tiles ? tile0 + p.tpc : p.tiles;
     const long long row0 = (long long)e * p.N;
-    int ft = tile0 + gi, fu = ks, fslot = 0;
+    int ft = tile0 + gi, fu = U0 + ks, fslot = 0;
     auto fetch = [&]() {
         if (ft < tile1 && fu < U) {
             if (lane == 0) {
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
             }
             fu += KS;
             if (fu >= U) {
-                fu = ks;
+                fu = U0 + ks;
                 ft += NG;
             }
         }
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     for (int d = 0; d < kSlots - 1; ++d) fetch();
     // scales of row `lane` of the tile (clamped: a row past the last is not stored)
     const __nv_bfloat16* sf = p.sf + row0 * (K / G);
-    int st = tile0 + gi, su = ks;
+    int st = tile0 + gi, su = U0 + ks;
     const Scales* srow = nullptr;
     auto scale_row = [&]() {
         const int f = st * kTile + (EPI == W4_GATED ? lane & 15 : lane);
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
             snext[1] = 2 * su + 1 < KB ? __ldg(srow + 2 * su + 1) : Scales{};
             su += KS;
             if (su >= U) {
-                su = ks;
+                su = U0 + ks;
                 st += NG;
                 scale_row();
             }
@@ -262,34 +272,30 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     asm volatile("griddepcontrol.wait;" ::: "memory");  // x may be the previous kernel's
     // A unit past an odd last block meets zeros: codes beyond the matrix's rows
     // (filled by the copy), x, its sums and the scales.
-    const int xst = U * 256 + 32;  // elements between rows of x in shared memory
-    if (KB & 1) {
+    const int xst = per * 256 + 32;  // elements between rows of x in shared memory
+    if (kn & 255) {  // an odd last block
         for (int v = threadIdx.x; v < n * 16; v += blockDim.x)
-            *reinterpret_cast<uint4*>(xsm + (v >> 4) * xst + K + (v & 15) * 8) = make_uint4(0u, 0u, 0u, 0u);
-        for (int v = threadIdx.x; v < (128 / G) * kR; v += blockDim.x) xs[(K / G) * kR + v] = 0.0f;
+            *reinterpret_cast<uint4*>(xsm + (v >> 4) * xst + kn + (v & 15) * 8) = make_uint4(0u, 0u, 0u, 0u);
+        for (int v = threadIdx.x; v < (128 / G) * kR; v += blockDim.x) xs[(kn / G) * kR + v] = 0.0f;
     }
-    for (int v = threadIdx.x; v < n * (K / 8); v += blockDim.x) {  // K / 8 is a multiple of 16: whole groups per row
-        const int r = v / (K / 8), c = v - r * (K / 8);
-        const uint4 u = *(reinterpret_cast<const uint4*>(p.x + (size_t)(row_of[r] / p.xdiv) * K) + c);
+    for (int v = threadIdx.x; v < n * (kn / 8); v += blockDim.x) {  // kn / 8 is a multiple of 16: whole groups per row
+        const int r = v / (kn / 8), c = v - r * (kn / 8);
+        const uint4 u = *(reinterpret_cast<const uint4*>(p.x + (size_t)(row_of[r] / p.xdiv) * K + k0) + c);
         *reinterpret_cast<uint4*>(xsm + r * xst + c * 8) = u;
         float f[8], s = 0.0f;
         unpack_bf16x8(u, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s += f[i];
         // the last warp may be half full: groups of G / 8 <= 16 lanes stay whole
-        const uint32_t act = v - lane + 32 <= n * (K / 8) ? 0xffffffffu : 0x0000ffffu;
+        const uint32_t act = v - lane + 32 <= n * (kn / 8) ? 0xffffffffu : 0x0000ffffu;
 #pragma unroll
         for (int d = 1; d < G / 8; d <<= 1) s += __shfl_xor_sync(act, s, d);
         if ((c & (G / 8 - 1)) == 0) xs[(c / (G / 8)) * kR + r] = -136.0f * s;
     }
     __syncthreads();
 
-    const uint4* xrow[NT];  // this lane's row of each 8-row tile (a row past the job's repeats the last)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = 8 * nt + g;
-        xrow[nt] = reinterpret_cast<const uint4*>(xsm + (r < n ? r : n - 1) * xst) + t;
-    }
+    // this lane's row (a row past the job's repeats the last)
+    const uint4* xrow = reinterpret_cast<const uint4*>(xsm + (g < n ? g : n - 1) * xst) + t;
     // y of feature f and row r of the job
     auto emit = [&](int f, int r, float v, float up) {
         if (f >= p.F || r >= n) return;
@@ -307,22 +313,24 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     const uint32_t chunk[2] = {(uint32_t)(g * 128 + ((t ^ g) << 4)), (uint32_t)(g * 128 + (((4 + t) ^ g) << 4))};
     int slot = 0, buf = 0;
     uint32_t phase = 0;
-    for (int tile = tile0 + gi; tile < tile1; tile += NG) {
-        float acc[2][NT][4];
+    // every warp of a cluster takes part in its barriers: as many rounds for all
+    const int rounds = (tile1 - tile0 + NG - 1) / NG;
+    if (p.kparts > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    for (int round = 0; round < rounds; ++round) {
+        const int tile = tile0 + gi + round * NG;
+        const bool live = tile < tile1;
+        if (p.kparts == 1 && !live) break;
+        float acc[2][4];
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.0f;
-        for (int u = ks; u < U; u += KS) {
+        for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.0f;
+        for (int u = live ? U0 + ks : U; u < U; u += KS) {
             const Scales sc2[2] = {snext[0], snext[1]};
             fetch_scales();
             fetch();
             // a wait that gave up leaves NaN in the outputs and lets the others go
             if (!warp_wait(bar + 8 * slot, phase, abort)) {
 #pragma unroll
-                for (int i = 0; i < 8 * NT; ++i) acc[i / (4 * NT)][i / 4 % NT][i % 4] = __uint_as_float(0x7fc00000u);
+                for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = __uint_as_float(0x7fc00000u);
             }
             const uint32_t unit = ring + slot * kUnitBytes;
 #pragma unroll
@@ -337,21 +345,16 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
                         w[h][i] = make_uint4(v.x, v.y, v.z, v.w);
                         scales_of(sc2[h0 + h], g + 8 * i, sc[h][i]);
                     }
-                float c[kSide][2][NT][4];
+                float c[kSide][2][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
 #pragma unroll
                     for (int h = 0; h < kSide; ++h) {
-                        const int kb = 2 * u + h0 + h;
-                        uint4 b[NT];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) b[nt] = xrow[nt][kb * 16 + j * 4];
-                        float2 start[NT];
-                        if (j % (G / 32) == 0) {
-                            const float* xg = xs + ((kb * 128 + j * 32) / G) * kR + 2 * t;
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) start[nt] = *reinterpret_cast<const float2*>(xg + 8 * nt);
-                        }
+                        const int kb = 2 * (u - U0) + h0 + h;  // of this block's part
+                        const uint4 b = xrow[kb * 16 + j * 4];
+                        float2 start;
+                        if (j % (G / 32) == 0)
+                            start = *reinterpret_cast<const float2*>(xs + ((kb * 128 + j * 32) / G) * kR + 2 * t);
 #pragma unroll
                         for (int rt = 0; rt < 2; ++rt) {
                             const uint32_t a0 = word_of(w[h][2 * rt], j), a1 = word_of(w[h][2 * rt + 1], j);
@@ -359,15 +362,11 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
                                            u2 = pair128<2>(a0, mask), u3 = pair128<3>(a0, mask);
                             const uint32_t v0 = pair128<0>(a1, mask), v1 = pair128<1>(a1, mask),
                                            v2 = pair128<2>(a1, mask), v3 = pair128<3>(a1, mask);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                if (j % (G / 32) == 0)
-                                    mma_bf16_from(c[h][rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y, start[nt].x,
-                                                  start[nt].y);
-                                else
-                                    mma_bf16(c[h][rt][nt], u0, v0, u1, v1, b[nt].x, b[nt].y);
-                                mma_bf16(c[h][rt][nt], u2, v2, u3, v3, b[nt].z, b[nt].w);
-                            }
+                            if (j % (G / 32) == 0)
+                                mma_bf16_from(c[h][rt], u0, v0, u1, v1, b.x, b.y, start.x, start.y);
+                            else
+                                mma_bf16(c[h][rt], u0, v0, u1, v1, b.x, b.y);
+                            mma_bf16(c[h][rt], u2, v2, u3, v3, b.z, b.w);
                         }
                     }
                     if ((j + 1) % (G / 32) == 0) {
@@ -375,16 +374,14 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
 #pragma unroll
                         for (int h = 0; h < kSide; ++h)
 #pragma unroll
-                            for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    const float s0 = scale(sc[h][2 * rt][si / 2], si),
-                                                s1 = scale(sc[h][2 * rt + 1][si / 2], si);
-                                    acc[rt][nt][0] = fmaf(s0, c[h][rt][nt][0], acc[rt][nt][0]);
-                                    acc[rt][nt][1] = fmaf(s0, c[h][rt][nt][1], acc[rt][nt][1]);
-                                    acc[rt][nt][2] = fmaf(s1, c[h][rt][nt][2], acc[rt][nt][2]);
-                                    acc[rt][nt][3] = fmaf(s1, c[h][rt][nt][3], acc[rt][nt][3]);
-                                }
+                            for (int rt = 0; rt < 2; ++rt) {
+                                const float s0 = scale(sc[h][2 * rt][si / 2], si),
+                                            s1 = scale(sc[h][2 * rt + 1][si / 2], si);
+                                acc[rt][0] = fmaf(s0, c[h][rt][0], acc[rt][0]);
+                                acc[rt][1] = fmaf(s0, c[h][rt][1], acc[rt][1]);
+                                acc[rt][2] = fmaf(s1, c[h][rt][2], acc[rt][2]);
+                                acc[rt][3] = fmaf(s1, c[h][rt][3], acc[rt][3]);
+                            }
                     }
                 }
             }
@@ -394,10 +391,10 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
                 phase ^= 1u;
             }
         }
-        // register i of lane (g, t) of operand rt and 8-row tile nt: row
-        // 16 rt + g + 8 (i / 2) of the tile, row 8 nt + 2 t + i % 2 of the job
-        auto put = [&](int u, float v0, float v1) {  // u = 4 nt + i
-            const int f = tile * kTile + g + 8 * ((u & 3) >> 1), r = 8 * (u >> 2) + 2 * t + (u & 1);
+        // register i of lane (g, t) of operand rt: row 16 rt + g + 8 (i / 2) of
+        // the tile, row 2 t + i % 2 of the job
+        auto put = [&](int i, float v0, float v1) {
+            const int f = tile * kTile + g + 8 * (i >> 1), r = 2 * t + (i & 1);
             if constexpr (EPI == W4_GATED) {
                 emit(f, r, v0, v1);
             } else {
@@ -405,29 +402,47 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
                 emit(f + 16, r, v1, 0.0f);
             }
         };
-        if (KS == 1) {
+        if (KS == 1 && p.kparts == 1) {
 #pragma unroll
-            for (int u = 0; u < 4 * NT; ++u) put(u, acc[0][u >> 2][u & 3], acc[1][u >> 2][u & 3]);
+            for (int i = 0; i < 4; ++i) put(i, acc[0][i], acc[1][i]);
         } else {
-            constexpr int kPer = 2 * NT * 128;  // floats of a warp
-            float* mine = red + (size_t)(buf * nw + warp) * kPer + lane;
+            constexpr int kPer = 256;  // floats of a warp
+            const bool split = p.kparts > 1;
+            // split: one set of sums, in the cluster's first block: that block
+            // has started, and the last round's sums have been read
+            if (split) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            float* mine = red + (size_t)((split ? part : buf) * nw + warp) * kPer + lane;
+            if (split && part > 0) {
+                const uint32_t to = cluster_addr_of(smem_addr(mine), 0);
 #pragma unroll
-            for (int rt = 0; rt < 2; ++rt)
+                for (int i = 0; i < 8; ++i)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 128), "f"(acc[i >> 2][i & 3]) : "memory");
+            } else {
 #pragma unroll
-                for (int u = 0; u < 4 * NT; ++u) mine[(rt * NT * 4 + u) * 32] = acc[rt][u >> 2][u & 3];
-            asm volatile("bar.sync %0, %1;" ::"r"(gi + 1), "r"(KS * 32) : "memory");
-            const float* all = red + (size_t)(buf * nw + gi * KS) * kPer + lane;
-            for (int u = ks; u < NT * 4; u += KS) {
-                float v0 = 0.0f, v1 = 0.0f;
-                for (int k = 0; k < KS; ++k) {
-                    v0 += all[k * kPer + u * 32];
-                    v1 += all[k * kPer + (NT * 4 + u) * 32];
-                }
-                put(u, v0, v1);
+                for (int i = 0; i < 8; ++i) mine[i * 32] = acc[i >> 2][i & 3];
             }
-            buf ^= 1;  // the next tile's sums go to the other half: two tiles on, this barrier has passed
+            if (split) {
+                asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            } else {
+                asm volatile("bar.sync %0, %1;" ::"r"(gi + 1), "r"(KS * 32) : "memory");
+            }
+            if (live && part == 0) {
+                const float* all = red + (size_t)((split ? 0 : buf) * nw + gi * KS) * kPer + lane;
+                for (int i = ks; i < 4; i += KS) {
+                    float v0 = 0.0f, v1 = 0.0f;
+                    for (int c = 0; c < p.kparts; ++c)
+                        for (int k = 0; k < KS; ++k) {
+                            v0 += all[(c * nw + k) * kPer + i * 32];
+                            v1 += all[(c * nw + k) * kPer + (4 + i) * 32];
+                        }
+                    put(i, v0, v1);
+                }
+            }
+            if (split) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            buf ^= 1;  // not split: the next tile's sums go to the other half; two tiles on, this barrier has passed
         }
     }
+    if (p.kparts > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (*abort) {  // copies in flight land before the block's shared memory goes
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 2000000ull) {
@@ -511,14 +526,15 @@ constexpr int kFewRows = 0;
 // warps, 437 with 8; a warp alone 2200; a join 600, and 100 of the SM's per warp
 // of it; a block's start (job, x) 3000 and a fifth per element of x.
 void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
-    const long long U = (a->K + 255) / 256, slots = 152 * per_sm, start = 3000 + (long long)a->R * a->K / 5;
+    const long long U = w4_units(a->K, a->kparts), slots = 152 * per_sm;
+    const long long start = 3000 + (long long)a->R * a->K / a->kparts / 5;
     long long best = -1;
     for (int ks = 1; ks <= nw; ks *= 2) {
-        const int ng = nw / ks, join = ks > 1;
+        const int ng = nw / ks, join = ks * a->kparts > 1;
         for (int rounds = 1; rounds <= 64; ++rounds) {
             const int tpc = ng * rounds;
             const long long tiles = tpc < a->tiles ? tpc : a->tiles;
-            const long long blocks = (long long)jobs * ((a->tiles + tpc - 1) / tpc), on_sm = (blocks + 151) / 152;
+            const long long blocks = (long long)jobs * a->kparts * ((a->tiles + tpc - 1) / tpc), on_sm = (blocks + 151) / 152;
             const long long warps = (on_sm < per_sm ? on_sm : per_sm) * nw;
             const long long unit = 3500 / warps > 280 ? 3500 / warps : 280;
             const long long rate = on_sm * (tiles * (U * unit + join * 100 * ks) + start);
@@ -538,49 +554,57 @@ void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
 // the jobs.  after_own: the kernel before it in the stream is this file's and
 // writes x only, so this one may start, find its job and fetch weights, while
 // that one drains (it waits before it reads x).
-template <int NT, int G, int EPI>
+template <int G, int EPI>
 int w4_launch(W4Args a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
     static SmemLimit limit;
     a.mask = 0x000f000fu;
     a.tiles = EPI == W4_GATED ? (a.F + 15) / 16 : (a.F + 31) / 32;
-    // as many rows per job as leave room for a block of four warps
-    a.R = rows < 8 * NT ? rows : 8 * NT;
-    while (a.R > 1 && w4_smem<NT, G>(a.K, 4, a.R).total > kW4Smem) --a.R;
-    auto bytes = [&](int nw) { return w4_smem<NT, G>(a.K, nw, a.R).total; };
+    a.R = (rows + (rows + kR - 1) / kR - 1) / ((rows + kR - 1) / kR);  // 12 rows: 6 and 6
+    // K is split over a cluster where the rows of x leave an SM fewer than 16
+    // warps (8 rows of a 7168 x 7168 matrix: 26.6 us with 8 warps, 17.2 us with
+    // 16 and half of K each); where four parts are not enough, fewer rows per job.
+    a.kparts = 1;
+    auto sixteen = [&](int parts) {  // one block of 16 warps or two of 8 fit an SM
+        return w4_smem<G>(a.K, 16, a.R, parts).total <= kW4Smem ||
+               2 * (w4_smem<G>(a.K, 8, a.R, parts).total + 1024) <= kSmSmem;
+    };
+    while (a.kparts < 4 && !sixteen(a.kparts) && w4_units(a.K, 2 * a.kparts) >= 8) a.kparts *= 2;
+    while (a.R > 1 && w4_smem<G>(a.K, 4, a.R, a.kparts).total > kW4Smem) --a.R;
+    auto bytes = [&](int nw) { return w4_smem<G>(a.K, nw, a.R, a.kparts).total; };
     const int per_sm = 2 * (bytes(8) + 1024) <= kSmSmem ? 2 : 1;
     const int nw = per_sm == 2 ? 8 : bytes(16) <= kW4Smem ? 16 : bytes(8) <= kW4Smem ? 8 : 4;
     const int jobs = a.ids ? a.slots : (a.rows + a.R - 1) / a.R;
     w4_shape(&a, a.ids ? a.busy : jobs, nw, per_sm);
-    if (const int e = limit.allow(w4_kernel<NT, G, EPI>, kW4Smem)) return e;
+    if (const int e = limit.allow(w4_kernel<G, EPI>, kW4Smem)) return e;
     CUtensorMap m;
     if (abi_map_u8(&m, q, (long long)a.E * a.N, a.K / 2, 128, EPI == W4_GATED ? 16 : 32, "4-bit codes"))
         return (int)cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((a.tiles + a.tpc - 1) / a.tpc, jobs);
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (after_own) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (a.kparts > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = attr[na].val.clusterDim.y = 1;
+        attr[na++].val.clusterDim.z = a.kparts;
+    }
+    cfg.gridDim = dim3((a.tiles + a.tpc - 1) / a.tpc, jobs, a.kparts);
     cfg.blockDim = dim3(nw * 32);
     cfg.dynamicSmemBytes = bytes(nw);
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = after_own ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_kernel<NT, G, EPI>, m, a);
+    cfg.numAttrs = na;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_kernel<G, EPI>, m, a);
     return (int)(e != cudaSuccess ? e : cudaGetLastError());
-}
-// Two 8-row tiles per job where more than 8 rows can share a matrix (and, in
-// shared memory, leave room for eight warps), else one.
-template <int G, int EPI>
-int w4_launch_nt(const W4Args& a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
-    if (rows > 8 && w4_smem<2, G>(a.K, 8, rows < 16 ? rows : 16).total <= kW4Smem)
-        return w4_launch<2, G, EPI>(a, q, rows, after_own, st);
-    return w4_launch<1, G, EPI>(a, q, rows, after_own, st);
 }
 template <int EPI>
 int w4_launch_g(int G, const W4Args& a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
-    return G == 32   ? w4_launch_nt<32, EPI>(a, q, rows, after_own, st)
-           : G == 64 ? w4_launch_nt<64, EPI>(a, q, rows, after_own, st)
-                     : w4_launch_nt<128, EPI>(a, q, rows, after_own, st);
+    return G == 32   ? w4_launch<32, EPI>(a, q, rows, after_own, st)
+           : G == 64 ? w4_launch<64, EPI>(a, q, rows, after_own, st)
+                     : w4_launch<128, EPI>(a, q, rows, after_own, st);
 }
 
 }  // namespace
@@ -617,8 +641,7 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     a.out = w.act;
     // Rows that a job is made for: twice an expert's mean share of the slots,
     // and one (an expert with more has several jobs).  More would cost shared
-    // memory, so warps, and 16-row products at three rows each: 32 tokens of
-    // top-6 over 64 experts took 138 us at up to 16 rows, 104 us at up to 8.
+    // memory, so warps.
     const long long share = w.topk_idx ? (2ll * w.T * w.k + w.E - 1) / w.E + 1 : w.T;
     const int rows = (int)(share < w.T ? share : w.T);
     if (const int e = w4_launch_g<W4_GATED>(w.group, a, w.W1_q, rows, false, st)) return e;

@@ -68,6 +68,17 @@ def test_matvec(M, N, K, G):
     assert torch.equal(y, lin(x))  # fixed order
 
 
+@pytest.mark.parametrize("M,N,K,G", [(12, 1000, 7168, 128), (16, 333, 7168, 32), (13, 70, 8064, 64), (30, 64, 4224, 128)])
+def test_matvec_split_over_k(M, N, K, G):
+    """Rows that do not fit one block's shared memory with all of K."""
+    q, sf = _weights(N, K, G, M + N)
+    x = torch.randn(M, K, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").to(BF)
+    lin = W4Linear(q, sf, G)
+    y = lin(x)
+    _check_product(x, q, sf, G, y)
+    assert torch.equal(y, lin(x))
+
+
 def test_matvec_last_scale_and_guards():
     """Odd counts of scales (group 128, odd K / 128): nothing past the ends is read into a result or written."""
     N, K, G = 33, 128 * 11, 128
