@@ -524,10 +524,10 @@ constexpr int kFewRows = 0;
 // chain of a warp over the blocks that follow one another.  In clocks, fitted
 // to sweeps of both at 1, 8 and 32 tokens: an SM takes 280 per unit with 16
 // warps, 437 with 8; a warp alone 2200; a join 600, and 100 of the SM's per warp
-// of it; a block's start (job, x) 3000 and a fifth per element of x.
+// of it; a block's start (job, x) 1200 and a third per element of x.
 void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
     const long long U = w4_units(a->K, a->kparts), slots = 152 * per_sm;
-    const long long start = 3000 + (long long)a->R * a->K / a->kparts / 5;
+    const long long start = 1200 + (long long)a->R * a->K / a->kparts / 3;
     long long best = -1;
     for (int ks = 1; ks <= nw; ks *= 2) {
         const int ng = nw / ks, join = ks * a->kparts > 1;
