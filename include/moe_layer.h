@@ -351,7 +351,7 @@ int moe_layer_norm_workspace(int64_t rows, int32_t H, size_t* bytes);
  *     dx = s (g - mean_h g - z mean_h(g z))     [rows, H], contiguous, x_type
  *     dweight = sum_r dy z,  dbias = sum_r dy   [H], w_type; dbias may be NULL
  * All three are overwritten (rows = 0: dweight and dbias become 0).  ws holds
- * moe_layer_norm_workspace bytes of scratch (f32 partial sums, 4-byte aligned).  The column
+ * moe_layer_norm_workspace bytes of scratch (16-byte aligned).  The column
  * sums are FP32 in a fixed order: deterministic, no atomics.  Errors as for
  * the forward. */
 int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_type, const void* dy,

@@ -329,11 +329,26 @@ def _rows_arg(t, dtype, rows, H, name, dev):
     return t.data_ptr(), stride
 
 
+_SIZE = threading.local()
+
+
+def _size_out():
+    """(a c_size_t of this thread, a reference to it)."""
+    try:
+        return _SIZE.out
+    except AttributeError:
+        v = ctypes.c_size_t()
+        _SIZE.out = (v, ctypes.byref(v))
+        return _SIZE.out
+
+
 def moe_layer_norm_workspace(rows: int, H: int) -> int:
     """Bytes of moe_layer_norm_backward's workspace."""
-    out = ctypes.c_size_t()
-    _check(lib().moe_layer_norm_workspace(rows, H, ctypes.byref(out)))
-    return out.value
+    v, ref = _size_out()
+    rc = lib().moe_layer_norm_workspace(rows, H, ref)
+    if rc:
+        _check(rc)
+    return v.value
 
 
 def moe_layer_norm_forward(x, weight, bias, eps: float, y, mean, rstd, stream=None):
@@ -393,9 +408,11 @@ def moe_matvec_w4(x, W_q, W_sf, y, group: int, stream=None):
 
 def moe_w4_workspace(shape: MoeW4Shape) -> int:
     """Bytes of moe_forward_w4's workspace."""
-    out = ctypes.c_size_t()
-    _check(lib().moe_w4_workspace(ctypes.byref(shape), ctypes.byref(out)))
-    return out.value
+    v, ref = _size_out()
+    rc = lib().moe_w4_workspace(ctypes.byref(shape), ref)
+    if rc:
+        _check(rc)
+    return v.value
 
 
 def moe_forward_w4(shape: MoeW4Shape, x, W1_q, W1_sf, W2_q, W2_sf, topk_idx, topk_w, ws, y, stream=None):

@@ -83,7 +83,7 @@ int moe_layer_norm_workspace(int64_t rows, int32_t H, size_t* bytes) {
     if (!bytes) return abi_fail(MOE_EINVAL, "bytes is NULL");
     const int rc = check_norm(rows, H, MOE_F32, MOE_F32);
     if (rc) return rc;
-    *bytes = (size_t)(rows < kLnBwdBlocks ? rows : kLnBwdBlocks) * 2 * (size_t)H * sizeof(float);
+    *bytes = (size_t)ln_bwd_parts(rows) * 2 * (size_t)H * sizeof(float);
     return MOE_OK;
 }
 
@@ -98,8 +98,8 @@ int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_t
     if (rows > 0 && (x_stride < H || dy_stride < H)) return abi_fail(MOE_EINVAL, "strides must be >= H");
     const int xe = elt_size(x_type), we = elt_size(w_type);
     if (!aligned(x, xe) || !aligned(dy, xe) || !aligned(dx, xe) || !aligned(weight, we) || !aligned(dweight, we) ||
-        !aligned(dbias, we) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(ws, 4))
-        return abi_fail(MOE_EUNSUPPORTED, "pointers must be aligned to their elements");
+        !aligned(dbias, we) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(ws, 16))
+        return abi_fail(MOE_EUNSUPPORTED, "pointers must be aligned to their elements, ws to 16 bytes");
     int sms = 0;
     if ((rc = abi_select_device(dweight, &sms))) return rc;
     cudaStream_t st = (cudaStream_t)stream;

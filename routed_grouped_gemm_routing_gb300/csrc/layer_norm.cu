@@ -132,10 +132,15 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarps : 1024)
     const int t = kWarpRow ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int nt = kWarpRow ? 32 : (int)blockDim.x;
     const T* xr = x + row * xs;
-    float v[NV];
+    float v[NV], wv[NV], bv[NV];  // all loads at once: the reductions would hide none of the later ones
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = t + i * nt < H ? to_f(__ldg(xr + t + i * nt)) : 0.0f;
+    for (int i = 0; i < NV; ++i) {
+        const int c = t + i * nt;
+        v[i] = c < H ? to_f(__ldg(xr + c)) : 0.0f;
+        wv[i] = c < H ? to_f(__ldg(w + c)) : 0.0f;
+        bv[i] = b && c < H ? to_f(__ldg(b + c)) : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) s += v[i];
     const float m = row_sum<kWarpRow>(s, red) / (float)H;
@@ -153,9 +158,7 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarps : 1024)
     for (int i = 0; i < NV; ++i) {
         const int c = t + i * nt;
         if (c < H) {
-            float o = (v[i] - m) * r * to_f(__ldg(w + c));
-            if (b) o += to_f(__ldg(b + c));
-            yr[c] = from_f<T>(o);
+            yr[c] = from_f<T>(fmaf((v[i] - m) * r, wv[i], bv[i]));
         }
     }
 }
@@ -256,6 +259,56 @@ __device__ __forceinline__ void load_pairs(const W* p, f2 (&f)[P]) {
     for (int i = 0; i < P; ++i) f[i] = f2_make(v[2 * i], v[2 * i + 1]);
 }
 
+// Vector c of a row whose first element lies m elements past a 16-byte boundary
+// holds columns c V - m .. + V - 1; bit j of the mask: column j of it exists.
+template <int V>
+__device__ __forceinline__ uint32_t vec_mask(int c, int m, int H) {
+    const int c0 = c * V - m;
+    uint32_t e = (1u << V) - 1u;
+    if (c0 < 0) e &= e << (-c0 < V ? -c0 : V);
+    if (c0 + V > H) e &= H > c0 ? (1u << (H - c0)) - 1u : 0u;
+    return e;
+}
+// Zero in the columns that do not exist.
+template <int P>
+__device__ __forceinline__ void keep(f2 (&v)[P], uint32_t e) {
+    if (e != (1u << (2 * P)) - 1u) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const float2 f = f2_get(v[j]);
+            v[j] = f2_make(e >> (2 * j) & 1u ? f.x : 0.0f, e >> (2 * j + 1) & 1u ? f.y : 0.0f);
+        }
+    }
+}
+// The columns that exist of 2 P weights from p on.
+template <typename W, int P>
+__device__ __forceinline__ void load_some(const W* p, uint32_t e, f2 (&f)[P]) {
+    float v[2 * P];
+#pragma unroll
+    for (int j = 0; j < 2 * P; ++j) v[j] = e >> j & 1u ? to_f(__ldg(p + j)) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) f[j] = f2_make(v[2 * j], v[2 * j + 1]);
+}
+template <typename T, int P>
+__device__ __forceinline__ void store_some(T* p, const f2 (&v)[P], uint32_t e) {
+    if (e == (1u << (2 * P)) - 1u) {
+        *reinterpret_cast<uint4*>(p) = pack_vec<T, P>(v);
+    } else {  // the row's ends: their other columns are its neighbours'
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const float2 f = f2_get(v[j]);
+            if (e >> (2 * j) & 1u) p[2 * j] = from_f<T>(f.x);
+            if (e >> (2 * j + 1) & 1u) p[2 * j + 1] = from_f<T>(f.y);
+        }
+    }
+}
+// Copies a vector whose end may pass the tensor's: nothing past `end` is read.
+template <typename T>
+__device__ __forceinline__ void copy_some(uint32_t dst, const T* src, const T* end) {
+    constexpr int V = 16 / sizeof(T);
+    cp_async_16(dst, src, end - src >= V ? 16u : (uint32_t)((end - src) * (long long)sizeof(T)));
+}
+
 // Mean and rstd of a row from its threads' sums and their squared distances
 // from their own means (n values each): the sums give the mean m, and
 // sum (x - m)^2 = sum_t M2_t + sum_t n_t (mean_t - m)^2.  No difference of
@@ -266,7 +319,9 @@ struct LnStat {
 
 // gt working threads per group; groups of several warps have a reducing warp
 // after them (kReducer).
-template <typename T, typename W, int NV, bool kBias, bool kReducer>
+// kShift: rows that start between 16-byte boundaries.  A group's rows are then a
+// multiple of 8 apart, so that they all start equally far past one.
+template <typename T, typename W, int NV, bool kBias, bool kReducer, bool kShift>
 __global__ void __launch_bounds__(kLnRingThreads, 1)
     ln_fwd_ring(long long rows, int H, int gt, const T* __restrict__ x, long long xs, const W* __restrict__ w,
                 const W* __restrict__ b, float eps, T* __restrict__ y, float* __restrict__ mean,
@@ -277,9 +332,10 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
     __shared__ LnStat stat[kReducer ? kLnMaxGroups : 1][2];
     const int gn = kReducer ? gt + 32 : gt;
     const int g = threadIdx.x / gn, t = threadIdx.x - g * gn, ng = blockDim.x / gn;
-    const int nvec = H / V;
     const long long step = (long long)gridDim.x * ng;
     const long long first = (long long)blockIdx.x * ng + g;
+    const int m0 = kShift ? (int)((first * H) & (V - 1)) : 0;
+    const int nvec = (H + m0 + V - 1) / V;
     const float inv_h = 1.0f / (float)H;
     const long long n = first < rows ? (rows - first + step - 1) / step : 0;  // rows of this group
     if (kReducer && t >= gt) {
@@ -290,7 +346,10 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
         for (int k = 0; k < kLnGroupWarps; ++k) {
             int c = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) c += k < nw && lane + 32 * k + i * gt < nvec ? V : 0;
+            for (int i = 0; i < NV; ++i) {
+                const int v = lane + 32 * k + i * gt;
+                if (k < nw && v < nvec) c += kShift ? __popc(vec_mask<V>(v, m0, H)) : V;
+            }
             cnt[k] = (float)c;
         }
         for (long long i = 0; i < n + kLag; ++i) {
@@ -326,21 +385,30 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
     const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16u;
     const uint32_t vstride = blockDim.x * 16u;
     bool have[NV];
+    uint32_t cols[kShift ? NV : 1];  // the columns that exist of each vector
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         have[i] = t + i * gt < nvec;
-        mine += have[i] ? V : 0;
+        if constexpr (kShift) cols[i] = have[i] ? vec_mask<V>(t + i * gt, m0, H) : 0u;
+        mine += kShift ? __popc(cols[kShift ? i : 0]) : have[i] ? V : 0;
     }
     const float inv_mine = mine ? 1.0f / (float)mine : 0.0f;
     // the next row to copy: its number and this thread's first element of it
     long long frow = 0;
-    const T* fx = x + first * xs + (size_t)t * V;
+    const T* fx = x + first * xs - m0 + (size_t)t * V;
+    const T* end = x + (rows - 1) * xs + H;
     auto fetch = [&](int s) {
         if (frow < n) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (have[i]) cp_async_16(slot0 + (uint32_t)(s * NV + i) * vstride, fx + (size_t)(i * gt) * V, 16u);
+                if (have[i]) {
+                    const uint32_t dst = slot0 + (uint32_t)(s * NV + i) * vstride;
+                    if constexpr (kShift)
+                        copy_some<T>(dst, fx + (size_t)(i * gt) * V, end);
+                    else
+                        cp_async_16(dst, fx + (size_t)(i * gt) * V, 16u);
+                }
         }
         cp_async_commit();
         ++frow;
@@ -354,10 +422,16 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (have[i]) {
-            load_pairs<W, P>(w + (size_t)(t + i * gt) * V, wv[i]);
-            if constexpr (kBias) load_pairs<W, P>(b + (size_t)(t + i * gt) * V, bv[i]);
+            const int c0 = (t + i * gt) * V - m0;
+            if constexpr (kShift) {
+                load_some<W, P>(w + c0, cols[i], wv[i]);
+                if constexpr (kBias) load_some<W, P>(b + c0, cols[i], bv[i]);
+            } else {
+                load_pairs<W, P>(w + c0, wv[i]);
+                if constexpr (kBias) load_pairs<W, P>(b + c0, bv[i]);
+            }
         }
-    T* yr = y + first * H + (size_t)t * V;
+    T* yr = y + first * H - m0 + (size_t)t * V;
     // (x - m) r w + b of the row in slot s
     auto output = [&](int s, float m, float r) {
         const f2 nm = f2_make(-m, -m), r2 = f2_make(r, r);
@@ -374,7 +448,10 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
                     else
                         v[j] = f2_mul(v[j], wv[i][j]);
                 }
-                *reinterpret_cast<uint4*>(yr + (size_t)(i * gt) * V) = pack_vec<T, P>(v);
+                if constexpr (kShift)
+                    store_some<T, P>(yr + (size_t)(i * gt) * V, v, cols[i]);
+                else
+                    *reinterpret_cast<uint4*>(yr + (size_t)(i * gt) * V) = pack_vec<T, P>(v);
             }
         yr += step * H;
     };
@@ -389,6 +466,7 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
             for (int k = 0; k < NV; ++k)
                 if (have[k]) {
                     unpack_vec<T, P>(ring[(s * NV + k) * blockDim.x + threadIdx.x], v[k]);
+                    if constexpr (kShift) keep<P>(v[k], cols[k]);
 #pragma unroll
                     for (int j = 0; j < P; ++j) acc[j & 1] = f2_add(acc[j & 1], v[k][j]);
                 }
@@ -401,10 +479,10 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
             for (int k = 0; k < NV; ++k)
                 if (have[k]) {
 #pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        const f2 d = f2_add(v[k][j], nc);
-                        acc[j & 1] = f2_fma(d, d, acc[j & 1]);
-                    }
+                    for (int j = 0; j < P; ++j) v[k][j] = f2_add(v[k][j], nc);
+                    if constexpr (kShift) keep<P>(v[k], cols[k]);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) acc[j & 1] = f2_fma(v[k][j], v[k][j], acc[j & 1]);
                 }
             m2 = f2_sum(f2_add(acc[0], acc[1]));
             if constexpr (kReducer) {
@@ -491,7 +569,7 @@ struct LnBwd {
 // LN_ALL_WARPS, for rows of which shared memory does not hold the two more that
 // the reducing warp's lag takes (NV = 4): every warp reduces.
 enum { LN_ONE_WARP, LN_REDUCER, LN_ALL_WARPS };
-template <typename T, typename W, int NV, int kMode>
+template <typename T, typename W, int NV, int kMode, bool kShift>
 __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, int gt) {
     constexpr bool kReducer = kMode == LN_REDUCER;
     constexpr int V = 16 / sizeof(T), P = V / 2, kRing = ln_bwd_ring_rows(NV), kLag = kReducer ? 2 : 0;
@@ -502,15 +580,20 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
     __shared__ float2 red[kMode == LN_ALL_WARPS ? kLnMaxGroups : 1][2][kLnGroupWarps];
     const int gn = kReducer ? gt + 32 : gt;
     const int g = threadIdx.x / gn, t = threadIdx.x - g * gn, ng = blockDim.x / gn;
-    const int H = p.H, nvec = H / V;
+    const int H = p.H;
     const long long step = (long long)gridDim.x * ng;
     const long long first = (long long)blockIdx.x * ng + g;
+    const int s0 = kShift ? (int)((first * H) & (V - 1)) : 0;  // elements of a row's first vector before the row
+    const int nvec = (H + s0 + V - 1) / V;
     const long long n = first < p.rows ? (p.rows - first + step - 1) / step : 0;  // rows of this group
     const float inv_h = 1.0f / (float)H;
     const bool worker = !kReducer || t < gt;
     bool have[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) have[i] = worker && t + i * gt < nvec;
+    uint32_t cols[kShift ? NV : 1];  // the columns that exist of each vector
+#pragma unroll
+    for (int i = 0; i < (kShift ? NV : 0); ++i) cols[i] = have[i] ? vec_mask<V>(t + i * gt, s0, H) : 0u;
     f2 sw[NV][P], sb[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -538,18 +621,25 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
     } else {
         const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16u;
         const uint32_t vstride = blockDim.x * 16u;
-        const W* w = static_cast<const W*>(p.w) + (size_t)t * V;
+        const W* w = static_cast<const W*>(p.w) + (t * V - s0);
         long long frow = 0;
-        const T* fx = static_cast<const T*>(p.x) + first * p.xs + (size_t)t * V;
-        const T* fd = static_cast<const T*>(p.dy) + first * p.dys + (size_t)t * V;
+        const T* fx = static_cast<const T*>(p.x) + first * p.xs - s0 + (size_t)t * V;
+        const T* fd = static_cast<const T*>(p.dy) + first * p.dys - s0 + (size_t)t * V;
+        const T* endx = static_cast<const T*>(p.x) + (p.rows - 1) * p.xs + H;
+        const T* endd = static_cast<const T*>(p.dy) + (p.rows - 1) * p.dys + H;
         auto fetch = [&](int s) {
             if (frow < n) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (have[i]) {
-                        cp_async_16(slot0 + (uint32_t)(s * 2 * NV + i) * vstride, fx + (size_t)(i * gt) * V, 16u);
-                        cp_async_16(slot0 + (uint32_t)(s * 2 * NV + NV + i) * vstride, fd + (size_t)(i * gt) * V,
-                                    16u);
+                        const uint32_t dst = slot0 + (uint32_t)(s * 2 * NV + i) * vstride;
+                        if constexpr (kShift) {
+                            copy_some<T>(dst, fx + (size_t)(i * gt) * V, endx);
+                            copy_some<T>(dst + NV * vstride, fd + (size_t)(i * gt) * V, endd);
+                        } else {
+                            cp_async_16(dst, fx + (size_t)(i * gt) * V, 16u);
+                            cp_async_16(dst + NV * vstride, fd + (size_t)(i * gt) * V, 16u);
+                        }
                     }
             }
             cp_async_commit();
@@ -561,19 +651,29 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
 #pragma unroll
         for (int s = 0; s < kAhead; ++s) fetch(s);
         f2 wv[kHoldW ? NV : 1][P];
+        auto load_w = [&](int i, f2 (&v)[P]) {
+            if constexpr (kShift)
+                load_some<W, P>(w + i * gt * V, cols[i], v);
+            else
+                load_pairs<W, P>(w + i * gt * V, v);
+        };
         if constexpr (kHoldW) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (have[i]) load_pairs<W, P>(w + (size_t)(i * gt) * V, wv[i]);
+                if (have[i]) load_w(i, wv[i]);
         }
-        T* out = static_cast<T*>(p.dx) + first * H + (size_t)t * V;
+        T* out = static_cast<T*>(p.dx) + first * H - s0 + (size_t)t * V;
         // z and dy of vector i of the row in slot s (and the weight, where it is not held)
         auto vectors = [&](int s, int i, f2 nm, f2 r2, f2 (&z)[P], f2 (&d)[P]) {
             unpack_vec<T, P>(ring[(s * 2 * NV + i) * blockDim.x + threadIdx.x], z);
             unpack_vec<T, P>(ring[(s * 2 * NV + NV + i) * blockDim.x + threadIdx.x], d);
-            if constexpr (!kHoldW) load_pairs<W, P>(w + (size_t)(i * gt) * V, wv[0]);
+            if constexpr (!kHoldW) load_w(i, wv[0]);
 #pragma unroll
             for (int j = 0; j < P; ++j) z[j] = f2_mul(f2_add(z[j], nm), r2);
+            if constexpr (kShift) {  // the neighbouring rows' values may be anything
+                keep<P>(z, cols[i]);
+                keep<P>(d, cols[i]);
+            }
         };
         // dx of the row in slot s; c1, c2: minus the means of g and of g z
         auto output = [&](int s, float m, float r, float c1, float c2) {
@@ -586,7 +686,10 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
 #pragma unroll
                     for (int j = 0; j < P; ++j)
                         d[j] = f2_mul(f2_fma(z[j], d2, f2_fma(d[j], wv[kHoldW ? i : 0][j], d1)), r2);
-                    *reinterpret_cast<uint4*>(out + (size_t)(i * gt) * V) = pack_vec<T, P>(d);
+                    if constexpr (kShift)
+                        store_some<T, P>(out + (size_t)(i * gt) * V, d, cols[i]);
+                    else
+                        *reinterpret_cast<uint4*>(out + (size_t)(i * gt) * V) = pack_vec<T, P>(d);
                 }
             out += step * H;
         };
@@ -653,9 +756,15 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
         if (have[i]) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const int h = (t + i * gt) * V + 2 * j;
-                *reinterpret_cast<float2*>(to + h) = f2_get(sw[i][j]);
-                *reinterpret_cast<float2*>(to + H + h) = f2_get(sb[i][j]);
+                const int h = (t + i * gt) * V - s0 + 2 * j;
+                const float2 a = f2_get(sw[i][j]), b = f2_get(sb[i][j]);
+                if constexpr (kShift) {
+                    if (cols[i] >> (2 * j) & 1u) to[h] = a.x, to[H + h] = b.x;
+                    if (cols[i] >> (2 * j + 1) & 1u) to[h + 1] = a.y, to[H + h + 1] = b.y;
+                } else {
+                    *reinterpret_cast<float2*>(to + h) = a;
+                    *reinterpret_cast<float2*>(to + H + h) = b;
+                }
             }
         }
     if (ng > 1) {
@@ -834,11 +943,26 @@ __global__ void __launch_bounds__(256) ln_bwd_join(const float* __restrict__ par
 enum { LN_RING, LN_WARP, LN_BLOCK, LN_LONG };
 struct LnForm {
     int form, nv, threads;
+    bool shift;  // ring: rows start between 16-byte boundaries
 };
+// Whether the ring form can take rows of width H, its tensors' rows `stride`
+// apart and starting at p: rows of all tensors start equally far past a 16-byte
+// boundary.
+bool ring_rows(const void* p, long long stride, int H, int elt) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride - H) * elt % 16 == 0;
+}
+// Blocks of a ring launch: up to one per SM, and a multiple of 8 for shifted
+// rows (152 is one).
+int ring_blocks(long long need, bool shift) {
+    if (need > 152) need = 152;
+    return (int)(shift ? (need + 7) / 8 * 8 : need);
+}
 LnForm ln_form(int H, int elt, bool vec, int max_threads, int wide_nv, int max_ring) {
     LnForm f = {};
     if (vec) {
-        const int nvec = H / (16 / elt);
+        const int V = 16 / elt;
+        f.shift = H % V != 0;
+        const int nvec = (H + V - 1) / V + (f.shift ? 1 : 0);  // at most
         f.form = LN_RING;
         f.nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : nvec <= 2 * (kLnRingThreads - 32) ? wide_nv : 4;
         f.threads = ((nvec + f.nv - 1) / f.nv + 31) / 32 * 32;
@@ -871,26 +995,33 @@ int ln_groups(int gt, bool reducer, int* threads) {
     *threads = ng * gn;
     return ng;
 }
-template <typename T, typename W, int NV, bool kBias, bool kReducer>
+// Shifted rows load their weights one by one: a group that takes fewer than
+// three rows does not earn that back (777 x 1001 f16 forward: 8.8 us, 3.3 us in
+// the register form; 8192 x 1001 backward 24.9 us, 37.8 us).
+bool ring_pays(const LnForm& f, bool reducer, long long rows) {
+    int threads;
+    return f.form != LN_RING || !f.shift || rows >= 3ll * 152 * ln_groups(f.threads, reducer, &threads);
+}
+template <typename T, typename W, int NV, bool kBias, bool kReducer, bool kShift>
 int run_fwd_ring(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
     static SmemLimit limit;
     int threads;
     const int ng = ln_groups(f.threads, kReducer, &threads);
     constexpr int per_thread = kLnFwdRing * NV * 16;
     static_assert(per_thread * kLnRingThreads <= 200 * 1024, "shared memory per block");
-    if (const int e = limit.allow(ln_fwd_ring<T, W, NV, kBias, kReducer>, per_thread * kLnRingThreads)) return e;
+    if (const int e = limit.allow(ln_fwd_ring<T, W, NV, kBias, kReducer, kShift>, per_thread * kLnRingThreads)) return e;
     const long long need = (a.rows + ng - 1) / ng;
-    ln_fwd_ring<T, W, NV, kBias, kReducer><<<(unsigned)(need < 152 ? need : 152), threads, per_thread * threads, st>>>(
+    ln_fwd_ring<T, W, NV, kBias, kReducer, kShift><<<ring_blocks(need, kShift), threads, per_thread * threads, st>>>(
         a.rows, a.H, f.threads, static_cast<const T*>(a.x), a.x_stride, static_cast<const W*>(a.weight),
         static_cast<const W*>(a.bias), a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
     return (int)cudaGetLastError();
 }
-template <typename T, typename W, bool kBias>
+template <typename T, typename W, bool kBias, bool kShift>
 int fwd_ring(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
-    if (f.nv == 1) return run_fwd_ring<T, W, 1, kBias, false>(f, a, st);
-    if (f.nv == 2) return run_fwd_ring<T, W, 2, kBias, false>(f, a, st);
-    return f.threads > 32 ? run_fwd_ring<T, W, 4, kBias, true>(f, a, st)
-                          : run_fwd_ring<T, W, 4, kBias, false>(f, a, st);
+    if (f.nv == 1) return run_fwd_ring<T, W, 1, kBias, false, kShift>(f, a, st);
+    if (f.nv == 2) return run_fwd_ring<T, W, 2, kBias, false, kShift>(f, a, st);
+    return f.threads > 32 ? run_fwd_ring<T, W, 4, kBias, true, kShift>(f, a, st)
+                          : run_fwd_ring<T, W, 4, kBias, false, kShift>(f, a, st);
 }
 template <typename T, typename W, int NV, bool kWarpRow>
 int run_fwd(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
@@ -910,13 +1041,16 @@ int run_fwd_long(const LnFwdArgs& a, cudaStream_t st) {
 template <typename T, typename W>
 int fwd_t(const LnFwdArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = a.H % V == 0 && a.x_stride % V == 0 && mult16(a.x) && mult16(a.y) && mult16(a.weight) &&
-                     mult16(a.bias);
-    const LnForm f = ln_form(a.H, sizeof(T), vec, 1024, 4, kLnRingThreads - 32);
+    const bool ring = ring_rows(a.x, a.x_stride, a.H, sizeof(T)) && ring_rows(a.y, a.H, a.H, sizeof(T)) &&
+                      (a.H % V || (mult16(a.weight) && mult16(a.bias)));
+    const bool vec = ring && a.H % V == 0;
+    LnForm f = ln_form(a.H, sizeof(T), ring, 1024, 4, kLnRingThreads - 32);
+    if (!ring_pays(f, f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 1024, 4, 0);
     const bool b = a.bias != nullptr;
     switch (f.form) {
         case LN_RING:
-            return b ? fwd_ring<T, W, true>(f, a, st) : fwd_ring<T, W, false>(f, a, st);
+            if (f.shift) return b ? fwd_ring<T, W, true, true>(f, a, st) : fwd_ring<T, W, false, true>(f, a, st);
+            return b ? fwd_ring<T, W, true, false>(f, a, st) : fwd_ring<T, W, false, false>(f, a, st);
         case LN_WARP:
             return f.nv == 1   ? run_fwd<T, W, 1, true>(f, a, st)
                    : f.nv == 2 ? run_fwd<T, W, 2, true>(f, a, st)
@@ -929,18 +1063,25 @@ int fwd_t(const LnFwdArgs& a, cudaStream_t st) {
     }
 }
 
-template <typename T, typename W, int NV, int kMode>
+template <typename T, typename W, int NV, int kMode, bool kShift>
 int run_bwd_ring(const LnForm& f, const LnBwd& p, int* blocks, cudaStream_t st) {
     static SmemLimit limit;
     int threads;
     const int ng = ln_groups(f.threads, kMode == LN_REDUCER, &threads);
     constexpr int per_thread = ln_bwd_ring_rows(NV) * 2 * NV * 16;
     static_assert(per_thread * kLnRingThreads <= 200 * 1024, "shared memory per block");
-    if (const int e = limit.allow(ln_bwd_ring<T, W, NV, kMode>, per_thread * kLnRingThreads)) return e;
+    if (const int e = limit.allow(ln_bwd_ring<T, W, NV, kMode, kShift>, per_thread * kLnRingThreads)) return e;
     const long long need = (p.rows + ng - 1) / ng;
-    *blocks = (int)(need < 152 ? need : 152);
-    ln_bwd_ring<T, W, NV, kMode><<<*blocks, threads, per_thread * threads, st>>>(p, f.threads);
+    *blocks = ring_blocks(need, kShift);
+    ln_bwd_ring<T, W, NV, kMode, kShift><<<*blocks, threads, per_thread * threads, st>>>(p, f.threads);
     return (int)cudaGetLastError();
+}
+template <typename T, typename W, bool kShift>
+int bwd_ring(const LnForm& f, const LnBwd& p, int* blocks, cudaStream_t st) {
+    return f.nv == 1        ? run_bwd_ring<T, W, 1, LN_ONE_WARP, kShift>(f, p, blocks, st)
+           : f.nv > 2       ? run_bwd_ring<T, W, 4, LN_ALL_WARPS, kShift>(f, p, blocks, st)
+           : f.threads > 32 ? run_bwd_ring<T, W, 2, LN_REDUCER, kShift>(f, p, blocks, st)
+                            : run_bwd_ring<T, W, 2, LN_ONE_WARP, kShift>(f, p, blocks, st);
 }
 template <typename T, typename W, int NV, bool kWarpRow>
 int run_bwd(const LnForm& f, const LnBwd& p, int* blocks, cudaStream_t st) {
@@ -960,17 +1101,16 @@ int run_bwd_long(const LnBwd& p, int* blocks, cudaStream_t st) {
 template <typename T, typename W>
 int bwd_t(const LnBwdArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = a.H % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 && mult16(a.x) && mult16(a.dy) &&
-                     mult16(a.dx) && mult16(a.weight);
+    const bool ring = ring_rows(a.x, a.x_stride, a.H, sizeof(T)) && ring_rows(a.dy, a.dy_stride, a.H, sizeof(T)) &&
+                      ring_rows(a.dx, a.H, a.H, sizeof(T)) && (a.H % V || mult16(a.weight));
+    const bool vec = ring && a.H % V == 0;
     const LnBwd p = {a.rows, a.H, a.dy, a.x, a.weight, a.dy_stride, a.x_stride, a.mean, a.rstd, a.dx, a.part};
-    const LnForm f = ln_form(a.H, sizeof(T), vec, 512, 2, kLnRingThreads);
+    LnForm f = ln_form(a.H, sizeof(T), ring, 512, 2, kLnRingThreads);
+    if (!ring_pays(f, f.nv == 2 && f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 512, 2, 0);
     int e, blocks = 0;
     switch (f.form) {
         case LN_RING:
-            e = f.nv == 1        ? run_bwd_ring<T, W, 1, LN_ONE_WARP>(f, p, &blocks, st)
-                : f.nv > 2       ? run_bwd_ring<T, W, 4, LN_ALL_WARPS>(f, p, &blocks, st)
-                : f.threads > 32 ? run_bwd_ring<T, W, 2, LN_REDUCER>(f, p, &blocks, st)
-                                 : run_bwd_ring<T, W, 2, LN_ONE_WARP>(f, p, &blocks, st);
+            e = f.shift ? bwd_ring<T, W, true>(f, p, &blocks, st) : bwd_ring<T, W, false>(f, p, &blocks, st);
             break;
         case LN_WARP:
             e = f.nv == 1   ? run_bwd<T, W, 1, true>(f, p, &blocks, st)

@@ -117,11 +117,12 @@ struct LnBwdArgs {
     long long dy_stride, x_stride;
     const float *mean, *rstd;
     void *dx, *dweight, *dbias;  // dbias may be null
-    float* part;                 // [min(rows, kLnBwdBlocks)][2][H]
+    float* part;                 // [ln_bwd_parts(rows)][2][H]
 };
 // Partial sums of the weight's and bias's gradients that a backward leaves at
 // most: two blocks on each of the 152 SMs.
 constexpr int kLnBwdBlocks = 304;
+inline long long ln_bwd_parts(long long rows) { return ((rows < kLnBwdBlocks ? rows : kLnBwdBlocks) + 7) / 8 * 8; }
 int launch_layer_norm_fwd(int x_type, int w_type, const LnFwdArgs& a, cudaStream_t st);
 int launch_layer_norm_bwd(int x_type, int w_type, const LnBwdArgs& a, cudaStream_t st);
 

@@ -93,6 +93,23 @@ def test_against_64_bits(rows, H, t, wt, bias):
     _check(*_inputs(rows, H, t, wt, bias, seed=rows * 31 + H))
 
 
+@pytest.mark.parametrize("rows,H,t,wt,bias,pad", [
+    (8001, 33, BF, F32, True, 0), (7700, 333, F32, F32, False, 0), (7400, 1001, F16, F16, True, 0),
+    (7400, 250, BF, BF, False, 8), (2600, 2047, F32, F32, True, 0), (1500, 5003, BF, F32, True, 0),
+    (1400, 5002, BF, F32, False, 16), (1000, 10001, F16, F32, True, 0), (950, 7161, F32, F32, True, 0),
+])
+def test_many_rows_between_vector_boundaries(rows, H, t, wt, bias, pad):
+    """Widths that 16 bytes do not divide, enough rows for persistent blocks: rows start anywhere in a vector, the last
+    one's vector ends past the tensor."""
+    x, dy, w, b = _inputs(rows, H, t, wt, bias, seed=H, pad=pad)
+    if not pad:  # nothing behind the last row is read into a result or written
+        es = x.element_size()
+        buf = torch.full((rows * H + 64 // es,), float("nan"), dtype=t, device="cuda")
+        buf[: rows * H] = x.flatten()
+        x = buf[: rows * H].view(rows, H)
+    _check(x, dy, w, b)
+
+
 @pytest.mark.parametrize("pad", [1, 8])
 def test_strided_rows(pad):
     x, dy, w, b = _inputs(77, 520, BF, F32, True, 5, pad=pad)
