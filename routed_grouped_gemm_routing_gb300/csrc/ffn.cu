@@ -29,10 +29,14 @@
 // dW1 would err by half as much again), and its bytes, written and read once,
 // are a few percent of the block's time.
 //
-// Few tiles (few tokens): the K range is split over up to kDenseClusters /
-// tiles pairs, each leaving FP32 partial sums, and ffn_join adds them in a
-// fixed order and applies the epilogue; every SM then streams a part of the
-// weights.  Deterministic in every form: no atomics.
+// Few tiles (few tokens): the K range is split over several pairs per tile, each
+// leaving FP32 partial sums, and ffn_join adds them in a fixed order and applies
+// the epilogue; every SM then streams a part of the weights (dense_shape).
+// Deterministic in every form: no atomics.
+//
+// The kernels of a call follow one another by programmatic launches: each
+// starts, sets up its barriers and TMEM where an SM is free, and waits for the
+// one before it before it touches any tensor.
 //
 // Roles (10 warps per CTA): 0-7 epilogue (warp w: TMEM lanes 32 (w % 4) .. of
 // the CTA's 128 rows, every other group of columns from w / 4 on; with four
@@ -41,8 +45,8 @@
 // issuer (first CTA of the pair).  Every wait is bounded; one that runs out
 // sets bit 0 of the status word.
 //
-// The tile is 256 x 256, or narrower (192, 128 columns) where that leaves fewer
-// columns' worth of rounds over the pairs (dense_width).
+// The tile is 256 x 256, or narrower (192, 128 columns) where that wastes less of
+// the last round over the pairs (dense_shape).
 #include "grouped_gemm_2sm.cuh"
 #include "smem_limit.h"
 
@@ -428,6 +432,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(bars.full(s), 1);
@@ -455,6 +460,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == kDenseWarpTma) {
         if (lane == 0) dense_producer<MODE, EPI>(&mA, &mB, p, base, bars, abort, rank);
@@ -510,6 +516,7 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 template <int EPI>
 __global__ void __launch_bounds__(128) ffn_join_kernel(const JoinArgs p) {
     constexpr int kHalves = EPI == JOIN_GATED ? 2 : 1;
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
     const int per = p.n / 8;
     const long long total = p.rows * per;
     const size_t stride = (size_t)p.rows * p.halves * p.n;
@@ -523,8 +530,8 @@ __global__ void __launch_bounds__(128) ffn_join_kernel(const JoinArgs p) {
             for (int j = 0; j < 8; ++j) v[hf][j] = 0.0f;
             const float* src = p.part + ((size_t)row * p.halves + hf) * p.n + c;
             for (int s = 0; s < p.splits; ++s) {
-                const float4 a = __ldg(reinterpret_cast<const float4*>(src + s * stride));
-                const float4 b = __ldg(reinterpret_cast<const float4*>(src + s * stride) + 1);
+                const float4 a = *reinterpret_cast<const float4*>(src + s * stride);
+                const float4 b = *(reinterpret_cast<const float4*>(src + s * stride) + 1);
                 v[hf][0] += a.x, v[hf][1] += a.y, v[hf][2] += a.z, v[hf][3] += a.w;
                 v[hf][4] += b.x, v[hf][5] += b.y, v[hf][6] += b.z, v[hf][7] += b.w;
             }
@@ -550,7 +557,7 @@ __global__ void __launch_bounds__(128) ffn_join_kernel(const JoinArgs p) {
             float du[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float2 d = gate_bwd(v[0][j], __ldg(h + j), __ldg(h + p.n + j), p.clamp);
+                const float2 d = gate_bwd(v[0][j], h[j], h[p.n + j], p.clamp);
                 o[j] = d.x;
                 du[j] = d.y;
             }
@@ -562,28 +569,40 @@ __global__ void __launch_bounds__(128) ffn_join_kernel(const JoinArgs p) {
 template <int EPI>
 int launch_join(const JoinArgs& a, cudaStream_t st) {
     const long long blocks = (a.rows * (a.n / 8) + 127) / 128;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(blocks < 2432 ? blocks : 2432));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     trace_pre(st);
-    ffn_join_kernel<EPI><<<(unsigned)(blocks < 2432 ? blocks : 2432), 128, 0, st>>>(a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_join_kernel<EPI>, a);
     trace_post(st, "ffn_join");
-    return (int)cudaGetLastError();
+    return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 // ----------------------------------------------------------------- launches
 int cdiv(long long a, int b) { return (int)((a + b - 1) / b); }
 
+// first: the call's first kernel, which waits for all of the stream's earlier work.
 template <int MODE, int EPI>
-int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaStream_t st) {
+int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaStream_t st, bool first = false) {
     static std::atomic<int> clusters_fit[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return (int)e;
     if (dev < 0 || dev >= kMaxDevices) return (int)cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.blockDim = dim3(kDenseThreads, 1, 1);
     cfg.dynamicSmemBytes = dense_smem<EPI>();
     cfg.stream = st;
@@ -607,6 +626,7 @@ int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaS
     const long long items = (long long)a.tiles_m * a.tiles_n * a.splits;
     if (items <= 0) return 0;
     cfg.gridDim = dim3(2u * (unsigned)(items < fit ? items : fit), 1, 1);
+    cfg.numAttrs = first ? 1 : 2;
     trace_pre(st);
     e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.c0, m.c1, a);
     trace_post(st, name);
@@ -614,29 +634,30 @@ int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaS
 }
 
 
-// K ranges: as many as give every pair of SMs a tile, of at least four K
-// blocks (256 deep), where the tiles alone would leave more than half idle.
-int dense_splits(int tiles, int kblocks) {
-    if (tiles <= 0 || 2 * tiles > kDenseClusters) return 1;
-    const int most = kblocks / 4, want = kDenseClusters / tiles;
-    const int s = want < most ? want : most;
-    return s > 1 ? s : 1;
-}
-
-// Columns of a tile (gated: of both halves): the rounds of tiles that the pairs
-// take, times the operand bytes of a tile's K block (256 rows and w columns):
-// at 64 bytes per clock and SM these, not the products, are what a narrower
-// tile runs at (4096 x 2048 x 2816: three rounds at 256 54 us, five at 128
-// 58 us).  256 on a tie.
-int dense_width(int M, int N, bool gated) {
-    int best = 256;
+// Columns of a tile (gated: of both halves) and K ranges of a product: the
+// cheapest in clocks of a pair, as measured.  A K block takes w + 256 (the
+// bytes of its operands at 64 per clock and SM: 512 for the products of a 256
+// wide tile too, but 384, not 256, at 128; 4096 x 2048 x 2816: three rounds at
+// 256 54 us, five at 128 58 us).  K ranges cost the join's launch, 7000, and
+// its reads and the partial sums' writes; without that term a block of 777
+// tokens ran four joins for 16 us of its 66.
+struct Shape {
+    int width, splits;
+};
+Shape dense_shape(int M, int N, int kblocks, bool gated, bool may_split) {
+    Shape best = {256, 1};
     long long cost = -1;
     for (int w = 256; w >= 128; w -= gated ? 128 : 64) {
         const long long tiles = (long long)cdiv(M, 256) * cdiv(N, gated ? w / 2 : w);
-        const long long c = (tiles + kDenseClusters - 1) / kDenseClusters * (w + 256);
-        if (cost < 0 || c < cost) {
-            cost = c;
-            best = w;
+        const int most = w == 256 && may_split ? (int)(tiles < kDenseClusters ? kDenseClusters / tiles : 1) : 1;
+        for (int s = 1; s <= most && s <= kblocks; ++s) {
+            const long long rounds = (tiles * s + kDenseClusters - 1) / kDenseClusters;
+            long long c = rounds * cdiv(kblocks, s) * (w + 256);
+            if (s > 1) c += 7000 + (long long)M * N * (gated ? 2 : 1) * s * 8 / 2000;
+            if (cost < 0 || c < cost) {
+                cost = c;
+                best = {w, s};
+            }
         }
     }
     return best;
@@ -644,27 +665,24 @@ int dense_width(int M, int N, bool gated) {
 
 // One product of the block.
 struct Product {
-    int M, N, K;            // N: columns, or features of one half
-    bool gated;             // B's columns are [2][N]
+    int M, N, K;  // N: columns, or features of one half
+    bool gated;   // B's columns are [2][N]
     bool may_split = true;
-    long long bytes() const {  // of the partial sums (0: one K range)
-        const int s = splits();
+    Shape shape() const { return dense_shape(M, N, cdiv(K, 64), gated, may_split); }
+    long long part_bytes() const {  // of the partial sums (0: one K range)
+        const int s = shape().splits;
         return s > 1 ? (long long)s * M * (gated ? 2 : 1) * N * 4 : 0;
     }
-    int tiles_m() const { return cdiv(M, 256); }
-    // K is split over tiles of the full width; where it is not, the width is chosen
-    int splits() const { return may_split ? dense_splits(tiles_m() * cdiv(N, gated ? 128 : 256), cdiv(K, 64)) : 1; }
-    int width() const { return splits() > 1 ? 256 : dense_width(M, N, gated); }
-    int tiles_n() const { return cdiv(N, gated ? width() / 2 : width()); }
     DenseArgs args(float clamp, int32_t* status) const {
+        const Shape f = shape();
         DenseArgs a = {};
         a.M = M;
         a.N = N;
-        a.tiles_m = tiles_m();
-        a.tiles_n = tiles_n();
+        a.tiles_m = cdiv(M, 256);
+        a.tiles_n = cdiv(N, gated ? f.width / 2 : f.width);
         a.kblocks = cdiv(K, 64);
-        a.splits = 1;
-        a.width = width();
+        a.splits = f.splits;
+        a.width = f.width;
         a.clamp = clamp;
         a.status = status;
         return a;
@@ -687,7 +705,7 @@ Product dgrad(const moe_ffn_shape& s) { return {s.T, s.H, 2 * s.I, false}; }
 long long ffn_part_bytes(const moe_ffn_shape& s) {
     long long most = 0;
     for (const Product& q : {fwd1(s), fwd2(s), dgate(s), dgrad(s)})
-        if (q.bytes() > most) most = q.bytes();
+        if (q.part_bytes() > most) most = q.part_bytes();
     return most;
 }
 
@@ -702,15 +720,14 @@ int launch_ffn_forward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st
         if ((rc = map_op(&m.a, f.x, s.T, s.H, 128, "x"))) return rc;
         if ((rc = abi_map_nd(&m.b, f.W1, 2, {s.I, 2, s.H}, {64, 1, 64}, "W1 (gate/up halves)"))) return rc;
         int e;
-        if (q.splits() > 1) {
-            a.splits = q.splits();
+        if (a.splits > 1) {
             if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.I, 2, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
-            e = launch_dense<KN, EPI_PART_GATED>(a, m, "ffn_gate_up", st);
+            e = launch_dense<KN, EPI_PART_GATED>(a, m, "ffn_gate_up", st, true);
             if (!e) e = launch_join<JOIN_GATED>({f.part, s.T, s.I, a.splits, 2, clamp, f.a, f.h}, st);
         } else {
             a.out = static_cast<__nv_bfloat16*>(f.a);
             if (f.h && (rc = abi_map_nd(&m.c1, f.h, 4, {s.I, 2, s.T}, {32, 1, 32}, "h (store)"))) return rc;
-            e = launch_dense<KN, EPI_GATED>(a, m, "ffn_gate_up", st);
+            e = launch_dense<KN, EPI_GATED>(a, m, "ffn_gate_up", st, true);
         }
         if (e) return abi_cuda_fail(e, "gate and up projection launch");
     }
@@ -720,8 +737,7 @@ int launch_ffn_forward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st
     if ((rc = map_op(&m.a, f.a, s.T, s.I, 128, "a"))) return rc;
     if ((rc = map_op(&m.b, f.W2, s.I, s.H, 64, "W2"))) return rc;
     int e;
-    if (q.splits() > 1) {
-        a.splits = q.splits();
+    if (a.splits > 1) {
         if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.H, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
         e = launch_dense<KN, EPI_PART>(a, m, "ffn_down", st);
         if (!e) e = launch_join<JOIN_PLAIN>({f.part, s.T, s.H, a.splits, 1, clamp, f.y, nullptr}, st);
@@ -741,15 +757,14 @@ int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t s
         DenseMaps m = {};
         if ((rc = map_op(&m.a, f.dY, s.T, s.H, 128, "dY"))) return rc;
         if ((rc = map_op(&m.b, f.W2, s.I, s.H, a.width / 2, "W2 (K-major)"))) return rc;
-        if (q.splits() > 1) {
-            a.splits = q.splits();
+        if (a.splits > 1) {
             if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.I, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
-            e = launch_dense<KK, EPI_PART>(a, m, "ffn_dgate", st);
+            e = launch_dense<KK, EPI_PART>(a, m, "ffn_dgate", st, true);
             if (!e) e = launch_join<JOIN_DGATE>({f.part, s.T, s.I, a.splits, 1, clamp, f.dh, f.h}, st);
         } else {
             a.out = static_cast<__nv_bfloat16*>(f.dh);
             if ((rc = abi_map_nd(&m.c1, f.h, 4, {s.I, 2, s.T}, {32, 1, 32}, "h"))) return rc;
-            e = launch_dense<KK, EPI_DGATE>(a, m, "ffn_dgate", st);
+            e = launch_dense<KK, EPI_DGATE>(a, m, "ffn_dgate", st, true);
         }
         if (e) return abi_cuda_fail(e, "dh launch");
     }
@@ -775,8 +790,7 @@ int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t s
     DenseMaps m = {};
     if ((rc = map_op(&m.a, f.dh, s.T, 2 * s.I, 128, "dh"))) return rc;
     if ((rc = map_op(&m.b, f.W1, s.H, 2 * s.I, a.width / 2, "W1 (K-major)"))) return rc;
-    if (q.splits() > 1) {
-        a.splits = q.splits();
+    if (a.splits > 1) {
         if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.H, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
         e = launch_dense<KK, EPI_PART>(a, m, "ffn_dx", st);
         if (!e) e = launch_join<JOIN_PLAIN>({f.part, s.T, s.H, a.splits, 1, clamp, f.dx, nullptr}, st);

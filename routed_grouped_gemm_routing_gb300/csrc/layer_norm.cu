@@ -588,6 +588,7 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
     const long long n = first < p.rows ? (p.rows - first + step - 1) / step : 0;  // rows of this group
     const float inv_h = 1.0f / (float)H;
     const bool worker = !kReducer || t < gt;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
     bool have[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) have[i] = worker && t + i * gt < nvec;
@@ -918,14 +919,15 @@ __global__ void __launch_bounds__(256) ln_bwd_long_cols(const LnBwd p, int bands
 // dw[h] (and db[h]) = sum over the nb partial rows, in order.  32 columns per
 // block; warp k takes every 8th partial row, then the eight are added.
 template <typename W>
-__global__ void __launch_bounds__(256) ln_bwd_join(const float* __restrict__ part, int nb, int H, W* __restrict__ dw,
+__global__ void __launch_bounds__(256) ln_bwd_join(const float* part, int nb, int H, W* __restrict__ dw,
                                                    W* __restrict__ db) {
     __shared__ float s[8][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;  // of 2 H
     float a = 0.0f;
     if (col < 2 * H)
-        for (int i = k; i < nb; i += 8) a += __ldg(part + (size_t)i * 2 * H + col);
+        for (int i = k; i < nb; i += 8) a += part[(size_t)i * 2 * H + col];
     s[k][lane] = a;
     __syncthreads();
     if (k == 0 && col < 2 * H) {
@@ -1125,9 +1127,18 @@ int bwd_t(const LnBwdArgs& a, cudaStream_t st) {
         default: e = vec ? run_bwd_long<T, W, V>(p, &blocks, st) : run_bwd_long<T, W, 1>(p, &blocks, st);
     }
     if (e) return e;
-    ln_bwd_join<W><<<(2 * a.H + 31) / 32, 256, 0, st>>>(a.part, blocks, a.H, static_cast<W*>(a.dweight),
-                                                         static_cast<W*>(a.dbias));
-    return (int)cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((2 * a.H + 31) / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t ce = cudaLaunchKernelEx(&cfg, ln_bwd_join<W>, (const float*)a.part, blocks, a.H,
+                                              static_cast<W*>(a.dweight), static_cast<W*>(a.dbias));
+    return (int)(ce != cudaSuccess ? ce : cudaGetLastError());
 }
 
 }  // namespace
