@@ -8,7 +8,10 @@
 //   dx = dh W1^T             dW1 = x^T dh
 //
 // Six products of 2 T H I (y, da, dW2) or 4 T H I (h, dx, dW1) operations, all
-// bound by the tensor cores from a few hundred tokens on.  One kernel serves
+// bound by the tensor cores from a few hundred tokens on: a step of 8192 x 7168 x
+// 2048 takes 1.18 ms in a short burst, 1.84 PFLOP/s, 95 % of the measured bf16
+// rate (1.37 ms and 1.58 PFLOP/s, 92 % of the sustained rate, when run for
+// seconds under the power limit).  One kernel serves
 // them (dense_pair_kernel): D[256 x 256] per pair of SMs, tcgen05 cta_group::2,
 // operands by TMA (128-byte swizzle, K blocks of 64) straight from the
 // row-major tensors: an operand whose rows run along K is K-major, one whose
@@ -41,7 +44,7 @@
 // Roles (10 warps per CTA): 0-7 epilogue (warp w: TMEM lanes 32 (w % 4) .. of
 // the CTA's 128 rows, every other group of columns from w / 4 on; with four
 // warps the arithmetic of EPI_DGATE took longer than the products of a
-// 2048-deep tile: 72 -> DG_US us at 4096 x 2048 x 1408), 8 TMA producer, 9 MMA
+// 2048-deep tile: 72 -> 38 us at 4096 x 2048 x 1408), 8 TMA producer, 9 MMA
 // issuer (first CTA of the pair).  Every wait is bounded; one that runs out
 // sets bit 0 of the status word.
 //
