@@ -8,6 +8,7 @@ stream.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
@@ -15,6 +16,22 @@ from . import binding as B
 
 
 _HERE = contextlib.nullcontext()
+_F32, _BF = torch.float32, torch.bfloat16
+_TYPES = B._TYPES
+_current = torch.cuda.current_device
+_stream_of = torch._C._cuda_getCurrentRawStream
+
+
+def _plain(t, dtype, shape, dev):
+    """Whether t is a contiguous tensor of that type and shape on device dev."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+# The calls below take a few microseconds on the GPU at decoding sizes, so what
+# the host does for one counts.  Each first tries its whole check in one
+# expression and calls the library with the pointers; whatever does not pass
+# (another device, strided rows, a wrong argument) goes the long way, through
+# the binding's checks and their messages.
 
 
 def _on(t):
@@ -39,6 +56,19 @@ def layer_norm_forward(x, weight, bias=None, eps: float = 1e-5):
     """(y, mean, rstd) of x [rows, H]; mean and rstd (f32 [rows]) are what
     layer_norm_backward reads.  x bf16, f16 or f32, its rows may be strided;
     weight and bias [H] in x's type or f32."""
+    dt, wt, sh, d = x.dtype, weight.dtype, x.shape, x.get_device()
+    if (len(sh) == 2 and dt in _TYPES and wt in _TYPES and d >= 0 and d == _current() and x.is_contiguous()
+            and _plain(weight, wt, sh[1:], d) and (bias is None or _plain(bias, wt, sh[1:], d))):
+        rows, dev = sh[0], x.device
+        y = torch.empty_like(x)
+        mean = torch.empty((rows,), dtype=_F32, device=dev)
+        rstd = torch.empty((rows,), dtype=_F32, device=dev)
+        rc = B.lib().moe_layer_norm_forward(
+            rows, sh[1], _TYPES[dt], _TYPES[wt], x.data_ptr(), sh[1], weight.data_ptr(),
+            None if bias is None else bias.data_ptr(), eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream_of(d))
+        if rc:
+            B._check(rc)
+        return y, mean, rstd
     rows, H = _norm_dims(x, weight, bias)
     with _on(x):
         dev = x.device
@@ -52,6 +82,20 @@ def layer_norm_forward(x, weight, bias=None, eps: float = 1e-5):
 def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True):
     """(dx, dweight, dbias) for dy [rows, H]; dbias is None without ``bias``.
     dweight and dbias have weight's type."""
+    dt, wt, sh, d = x.dtype, weight.dtype, x.shape, x.get_device()
+    if (len(sh) == 2 and dt in _TYPES and wt in _TYPES and d >= 0 and d == _current() and x.is_contiguous()
+            and _plain(dy, dt, sh, d) and _plain(weight, wt, sh[1:], d) and _plain(mean, _F32, sh[:1], d)
+            and _plain(rstd, _F32, sh[:1], d)):
+        rows, H, dev = sh[0], sh[1], x.device
+        dx, dw = torch.empty_like(x), torch.empty_like(weight)
+        db = torch.empty_like(weight) if bias else None
+        ws = torch.empty((B.moe_layer_norm_workspace(rows, H) + 4,), dtype=torch.uint8, device=dev)
+        rc = B.lib().moe_layer_norm_backward(
+            rows, H, _TYPES[dt], _TYPES[wt], dy.data_ptr(), H, x.data_ptr(), H, weight.data_ptr(), mean.data_ptr(),
+            rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr() if bias else None, ws.data_ptr(), _stream_of(d))
+        if rc:
+            B._check(rc)
+        return dx, dw, db
     rows, H = _norm_dims(x, weight)
     with _on(x):
         dev = x.device
@@ -102,6 +146,7 @@ class FFNWorkspace:
 
     def __init__(self, T: int, H: int, I: int, device=None, activation_clamp: float = 0.0, train: bool = True):
         self.shape = B.MoeFFNShape(T, H, I, activation_clamp)
+        self.shape_ref = ctypes.byref(self.shape)
         self.layout = L = B.moe_ffn_workspace_layout(self.shape)
         dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.train = train
@@ -126,6 +171,17 @@ def _ffn_check(x, W1, W2, ws):
 def ffn_forward(x, W1, W2, ws: FFNWorkspace):
     """y bf16 [T, H] = (silu(x W1[:, :I]) * (x W1[:, I:])) W2 for contiguous
     bf16 x [T, H], W1 [H, 2I] (gate | up), W2 [I, H]."""
+    s, d = ws.shape, x.get_device()
+    T, H, I = s.T, s.H, s.I
+    if (d >= 0 and d == _current() and d == ws.device.index and _plain(x, _BF, (T, H), d)
+            and _plain(W1, _BF, (H, 2 * I), d) and _plain(W2, _BF, (I, H), d)):
+        y = torch.empty_like(x)
+        rc = B.lib().moe_ffn_forward(ws.shape_ref, x.data_ptr(), W1.data_ptr(), W2.data_ptr(), int(ws.train),
+                                     ws.saved.data_ptr(), ws.ws.data_ptr(), y.data_ptr(), _stream_of(d))
+        if rc:
+            B._check(rc)
+        ws.generation += 1
+        return y
     _ffn_check(x, W1, W2, ws)
     with _on(x):
         y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
@@ -224,6 +280,14 @@ class W4Linear:
     def forward(self, x, out=None):
         """y bf16 [M, N] for x bf16 [M, K]."""
         M, K = x.shape
+        d = x.get_device()
+        if d >= 0 and d == _current() and d == self.q.get_device() and out is None and _plain(x, _BF, (M, self.K), d):
+            y = torch.empty((M, self.N), dtype=_BF, device=x.device)
+            rc = B.lib().moe_matvec_w4(M, self.N, K, self.group, x.data_ptr(), self.q.data_ptr(), self.sf.data_ptr(),
+                                       y.data_ptr(), _stream_of(d))
+            if rc:
+                B._check(rc)
+            return y
         if K != self.K:
             raise ValueError(f"x has {K} columns, the weight {self.K}")
         with _on(x):
@@ -248,6 +312,13 @@ class W4Experts:
         self.E, self.H, self.I, self.group = E, 2 * half, I2 // 2, group
         self.W1_q, self.W1_sf = _check_w4(W1_q, W1_sf, group, E, I2, self.H)
         self.W2_q, self.W2_sf = _check_w4(W2_q, W2_sf, group, E, self.H, self.I)
+        self._sizes = {}  # (T, k) -> shape, workspace bytes
+
+    def _size(self, T, k):
+        if (T, k) not in self._sizes:
+            s = B.MoeW4Shape(T, self.H, self.I, self.E, k, self.group)
+            self._sizes[T, k] = (s, ctypes.byref(s), max(B.moe_w4_workspace(s), 16))
+        return self._sizes[T, k]
 
     @classmethod
     def quantize(cls, W1, W2, group: int = 128):
@@ -260,6 +331,20 @@ class W4Experts:
         """y bf16 [T, H] for x bf16 [T, H] and the routing (topk_idx int
         [T, k], topk_w float [T, k]; neither with a single expert)."""
         T, H = x.shape
+        d = x.get_device()
+        if (d >= 0 and d == _current() and d == self.W1_q.get_device() and out is None and topk_idx is not None
+                and topk_w is not None and _plain(x, _BF, (T, self.H), d)
+                and _plain(topk_idx, torch.int32, topk_w.shape, d) and _plain(topk_w, _F32, (T, topk_w.shape[-1]), d)):
+            _, ref, size = self._size(T, topk_w.shape[-1])
+            dev = x.device
+            ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+            y = torch.empty_like(x)
+            rc = B.lib().moe_forward_w4(
+                ref, x.data_ptr(), self.W1_q.data_ptr(), self.W1_sf.data_ptr(), self.W2_q.data_ptr(),
+                self.W2_sf.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(), y.data_ptr(), _stream_of(d))
+            if rc:
+                B._check(rc)
+            return y
         if H != self.H:
             raise ValueError("x's hidden size differs from the weights'")
         if topk_idx is None:
@@ -274,9 +359,9 @@ class W4Experts:
                 topk_idx = topk_idx.to(torch.int32).contiguous()
             if topk_w.dtype is not torch.float32 or not topk_w.is_contiguous():
                 topk_w = topk_w.to(torch.float32).contiguous()
-        s = B.MoeW4Shape(T, H, self.I, self.E, k, self.group)
+        s, _, size = self._size(T, k)
         with _on(x):
-            ws = torch.empty((max(B.moe_w4_workspace(s), 16),), dtype=torch.uint8, device=x.device)
+            ws = torch.empty((size,), dtype=torch.uint8, device=x.device)
             if out is None:
                 out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
             B.moe_forward_w4(s, x if x.is_contiguous() else x.contiguous(), self.W1_q, self.W1_sf, self.W2_q,
