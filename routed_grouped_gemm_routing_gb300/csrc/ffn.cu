@@ -39,7 +39,10 @@
 //
 // The kernels of a call follow one another by programmatic launches: each
 // starts, sets up its barriers and TMEM where an SM is free, and waits for the
-// one before it before it touches any tensor.
+// one before it before it touches any tensor.  dW2, dW1 and dx need nothing of
+// each other once dh is there: one launch takes the tiles of all three, the
+// deepest products first, so that one last round is ragged instead of three
+// (PLAIN_NOTE).
 //
 // Roles (10 warps per CTA): 0-7 epilogue (warp w: TMEM lanes 32 (w % 4) .. of
 // the CTA's 128 rows, every other group of columns from w / 4 on; with four
@@ -51,14 +54,13 @@
 // The tile is 256 x 256, or narrower (192, 128 columns) where that wastes less of
 // the last round over the pairs (dense_shape).
 #include "grouped_gemm_2sm.cuh"
-#include "smem_limit.h"
 
 namespace moe {
 
 namespace {
 
 enum DenseMode { KK, KN, NN };  // majorness of A, B: K-major or MN-major (N)
-enum DenseEpi { EPI_PLAIN, EPI_GATED, EPI_DGATE, EPI_PART, EPI_PART_GATED };
+enum DenseEpi { EPI_PLAIN, EPI_GATED, EPI_DGATE, EPI_PART, EPI_PART_GATED };  // EPI_PLAIN: plain_kernel below
 
 constexpr int kDenseEpiWarps = 8;
 constexpr int kDenseWarpTma = 8, kDenseWarpMma = 9;
@@ -305,29 +307,7 @@ __device__ void dense_epilogue(const CUtensorMap* m0, const CUtensorMap* m1, con
         const bool row_live = row0 + lane < p.M;
         bool ok = true;
         if (rows_live) {
-            if constexpr (EPI == EPI_PLAIN) {
-#pragma unroll 1
-                for (int c = part; 64 * c < last; c += 2) {
-                    uint32_t r0[32], r1[32], pk[32];
-                    tmem_ld32_nowait(t + 64 * c, r0);
-                    tmem_ld32_nowait(t + 64 * c + 32, r1);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        pk[j] = pack_bf16x2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
-                        pk[16 + j] = pack_bf16x2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
-                    }
-                    if (lane == 0) bulk_wait_read<0>();
-                    __syncwarp();
-                    stage_row_sw128(stage, lane, pk);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(m0, item.n0 + 64 * c, row0, stage);
-                        bulk_commit();
-                    }
-                }
-            } else if constexpr (EPI == EPI_PART || EPI == EPI_PART_GATED) {
+            if constexpr (EPI == EPI_PART || EPI == EPI_PART_GATED) {
                 constexpr int kHalves = EPI == EPI_PART_GATED ? 2 : 1;
 #pragma unroll 1
                 for (int c = part; c < kHalves * (cols / 32); c += 2) {
@@ -415,77 +395,73 @@ __device__ void dense_epilogue(const CUtensorMap* m0, const CUtensorMap* m1, con
     __syncwarp();
 }
 
-// Maps: a, b operands; c0 output (EPI_PLAIN) or partial sums (EPI_PART); c1 h
+// Maps: a, b operands; c0 partial sums (EPI_PART); c1 h
 // (EPI_GATED: store, EPI_DGATE: load).  a and dh leave by plain stores, 64
 // contiguous bytes per row and thread.
-template <int MODE, int EPI>
-__global__ void __launch_bounds__(kDenseThreads, 1)
-    dense_pair_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
-                      const __grid_constant__ CUtensorMap mC0, const __grid_constant__ CUtensorMap mC1,
-                      const DenseArgs p) {
+struct DenseCta {
+    uint32_t ring, boxes, tmem;
+    DenseBars bars;
+    volatile int* abort;
+    int warp, lane, rank;
+};
+// Shared memory, barriers and TMEM of a CTA; returns when the pair is set up and
+// the kernel before this one in the stream has ended.
+template <int EPI>
+__device__ __forceinline__ DenseCta dense_begin() {
     constexpr int kStages = dense_stages<EPI>();
     extern __shared__ uint8_t smem_raw[];
+    DenseCta c;
     const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t boxes = base + kStages * kDenseStageBytes;
-    const uint32_t bar0 = boxes + kDenseEpiWarps * dense_boxes<EPI>() * 4096;
+    c.ring = (raw + 1023u) & ~1023u;
+    c.boxes = c.ring + kStages * kDenseStageBytes;
+    const uint32_t bar0 = c.boxes + kDenseEpiWarps * dense_boxes<EPI>() * 4096;
     uint8_t* tail = smem_raw + (bar0 - raw);
-    const DenseBars bars{bar0, kStages};
+    c.bars = DenseBars{bar0, kStages};
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 8 * (2 * kStages + 5 + kDenseEpiWarps));
-    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_ctarank();
+    c.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    c.warp = threadIdx.x >> 5;
+    c.lane = threadIdx.x & 31;
+    c.rank = (int)cluster_ctarank();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(bars.full(s), 1);
-            mbar_init(bars.empty(s), 1);
+            mbar_init(c.bars.full(s), 1);
+            mbar_init(c.bars.empty(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
-            mbar_init(bars.tfull(a), 1);
-            mbar_init(bars.tempty(a), 2 * kDenseEpiWarps);
+            mbar_init(c.bars.tfull(a), 1);
+            mbar_init(c.bars.tempty(a), 2 * kDenseEpiWarps);
         }
-        mbar_init(bars.drain(), 1);
-        for (int w = 0; w < kDenseEpiWarps; ++w) mbar_init(bars.hin(w), 1);
-        *abort = 0;
+        mbar_init(c.bars.drain(), 1);
+        for (int w = 0; w < kDenseEpiWarps; ++w) mbar_init(c.bars.hin(w), 1);
+        *c.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kDenseWarpMma) {
+    if (c.warp == kDenseWarpMma) {
         tmem_alloc_pair(smem_addr(tmem_slot), 512);
         tmem_relinquish_pair();
-    }
-    if (warp == kDenseWarpTma && lane == 0) {
-        tma_prefetch_map(&mA);
-        tma_prefetch_map(&mB);
-        tma_prefetch_map(EPI == EPI_GATED || EPI == EPI_DGATE ? &mC1 : &mC0);
     }
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    c.tmem = *tmem_slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    if (warp == kDenseWarpTma) {
-        if (lane == 0) dense_producer<MODE, EPI>(&mA, &mB, p, base, bars, abort, rank);
-    } else if (warp == kDenseWarpMma) {
-        if (rank == 0) {
-            dense_mma<MODE, EPI>(p, base, bars, tmem, abort);
-            const bool aborted = __any_sync(0xffffffffu, *abort != 0);
-            if (elect_one() && aborted) {
-                // let every MMA already issued (by this same elected lane)
-                // finish before TMEM is released
-                tc_commit_pair_local(bars.drain());
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(bars.drain(), 0) && global_timer_ns() - t0 < 100000000ull) {
-                }
-            }
-            __syncwarp();
+    return c;
+}
+// The MMA warp's end: where a wait gave up, every MMA already issued (by this
+// same elected lane) finishes before TMEM is released.
+__device__ __forceinline__ void dense_drain(const DenseCta& c) {
+    const bool aborted = __any_sync(0xffffffffu, *c.abort != 0);
+    if (elect_one() && aborted) {
+        tc_commit_pair_local(c.bars.drain());
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(c.bars.drain(), 0) && global_timer_ns() - t0 < 100000000ull) {
         }
-    } else {
-        dense_epilogue<EPI>(&mC0, &mC1, p, bars, tmem, boxes + warp * dense_boxes<EPI>() * 4096, abort, warp, lane,
-                            rank);
     }
-    if (warp == kDenseWarpTma && lane == 0 && *abort) {
+    __syncwarp();
+}
+__device__ __forceinline__ void dense_end(const DenseCta& c, int32_t* status) {
+    if (c.warp == kDenseWarpTma && c.lane == 0 && *c.abort) {
         // copies in flight land before the CTA's shared memory goes
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 2000000ull) {
@@ -494,11 +470,209 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     __syncwarp();
     tc_fence_before();
     cluster_sync();
-    if (warp == kDenseWarpMma) {
+    if (c.warp == kDenseWarpMma) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 512);
+        tmem_dealloc_pair(c.tmem, 512);
     }
-    if (threadIdx.x == 0 && *abort) atomicOr(reinterpret_cast<int*>(p.status), 1);
+    if (threadIdx.x == 0 && *c.abort) atomicOr(reinterpret_cast<int*>(status), 1);
+}
+
+template <int MODE, int EPI>
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
+                      const __grid_constant__ CUtensorMap mC0, const __grid_constant__ CUtensorMap mC1,
+                      const DenseArgs p) {
+    if (threadIdx.x == 32 * kDenseWarpTma) {
+        tma_prefetch_map(&mA);
+        tma_prefetch_map(&mB);
+        tma_prefetch_map(EPI == EPI_GATED || EPI == EPI_DGATE ? &mC1 : &mC0);
+    }
+    const DenseCta c = dense_begin<EPI>();
+    if (c.warp == kDenseWarpTma) {
+        if (c.lane == 0) dense_producer<MODE, EPI>(&mA, &mB, p, c.ring, c.bars, c.abort, c.rank);
+    } else if (c.warp == kDenseWarpMma) {
+        if (c.rank == 0) {
+            dense_mma<MODE, EPI>(p, c.ring, c.bars, c.tmem, c.abort);
+            dense_drain(c);
+        }
+    } else {
+        dense_epilogue<EPI>(&mC0, &mC1, p, c.bars, c.tmem, c.boxes + c.warp * dense_boxes<EPI>() * 4096, c.abort, c.warp,
+                            c.lane, c.rank);
+    }
+    dense_end(c, p.status);
+}
+
+// ------------------------------------------------- products with bf16 output
+// Up to three products in one launch, each with its own operands' majorness.
+constexpr int kPlainMost = 3;
+struct PlainProblem {
+    int M, N, tiles_m, tiles_n, kblocks, width;
+    int a_mn, b_mn;  // MN-major operands
+};
+struct PlainArgs {
+    int n;
+    PlainProblem p[kPlainMost];
+    int32_t* status;
+};
+struct PlainMaps {
+    CUtensorMap m[3 * kPlainMost];  // A, B, D of each
+};
+struct PlainItem {
+    int p, m0, n0;
+};
+// Round r of a cluster: item r n + c of the problems in order, or, every other
+// round, from the far end, so that the costlier items of a round that straddles
+// two problems go to the clusters that had the cheaper ones.
+struct PlainWalk {
+    const PlainArgs& a;
+    int r, n, c, total;
+    __device__ __forceinline__ PlainWalk(const PlainArgs& a_)
+        : a(a_), r(0), n((int)gridDim.x >> 1), c((int)blockIdx.x >> 1), total(0) {
+        for (int i = 0; i < a.n; ++i) total += a.p[i].tiles_m * a.p[i].tiles_n;
+    }
+    __device__ __forceinline__ int at() const { return r * n + ((r & 1) ? n - 1 - c : c); }
+    // (a cluster past the end of one round may have an item in no later one)
+    __device__ __forceinline__ bool valid() const { return at() < total; }
+    __device__ __forceinline__ void next() { ++r; }
+    __device__ __forceinline__ PlainItem item() const {
+        int w = at(), i = 0;
+        while (w >= a.p[i].tiles_m * a.p[i].tiles_n) w -= a.p[i].tiles_m * a.p[i].tiles_n, ++i;
+        const PlainProblem& q = a.p[i];
+        // eight row tiles by all column tiles at a time share their operands in L2
+        const int per = 8 * q.tiles_n, group = w / per, l = w - group * per;
+        const int rows = q.tiles_m - 8 * group < 8 ? q.tiles_m - 8 * group : 8;
+        const int nt = l / rows, mt = 8 * group + l - nt * rows;
+        return {i, mt * 256, nt * q.width};
+    }
+};
+
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    plain_kernel(const __grid_constant__ PlainMaps maps, const __grid_constant__ PlainArgs a) {
+    if (threadIdx.x == 32 * kDenseWarpTma)
+        for (int i = 0; i < 3 * a.n; ++i) tma_prefetch_map(&maps.m[i]);
+    const DenseCta c = dense_begin<EPI_PLAIN>();
+    constexpr int kStages = dense_stages<EPI_PLAIN>();
+    if (c.warp == kDenseWarpTma && c.lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (PlainWalk w(a); w.valid() && ok; w.next()) {
+            const PlainItem it = w.item();
+            const PlainProblem& q = a.p[it.p];
+            const CUtensorMap *mA = &maps.m[3 * it.p], *mB = mA + 1;
+            const int half = q.width / 2, m = it.m0 + 128 * c.rank, n = it.n0 + half * c.rank;
+            const bool two = half > 64;  // MN-major: boxes of 64 columns
+            const uint32_t tx = 2u * (kDenseStageBytes / 2 + (q.b_mn ? (two ? 16384u : 8192u) : (uint32_t)half * 128u));
+            for (int kb = 0; kb < q.kblocks; ++kb) {
+                if (!mbar_wait(c.bars.empty(stage), phase ^ 1u, c.abort)) {
+                    ok = false;
+                    break;
+                }
+                if (c.rank == 0) mbar_arrive_expect_tx(c.bars.full(stage), tx);
+                const uint32_t fb = cluster_addr_of(c.bars.full(stage), 0);
+                const uint32_t sa = c.ring + stage * kDenseStageBytes, sb = sa + kDenseStageBytes / 2;
+                const int k0 = kb * 64;
+                if (q.a_mn) {
+                    tma_load_2d_pair(sa, mA, m, k0, fb);
+                    tma_load_2d_pair(sa + 8192, mA, m + 64, k0, fb);
+                } else {
+                    tma_load_2d_pair(sa, mA, k0, m, fb);
+                }
+                if (q.b_mn) {
+                    tma_load_2d_pair(sb, mB, n, k0, fb);
+                    if (two) tma_load_2d_pair(sb + 8192, mB, n + 64, k0, fb);
+                } else {
+                    tma_load_2d_pair(sb, mB, k0, n, fb);
+                }
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (c.warp == kDenseWarpMma && c.rank == 0) {
+        int stage = 0, i = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (PlainWalk w(a); w.valid() && ok; w.next(), ++i) {
+            const PlainProblem& q = a.p[w.item().p];
+            const int acc = i & 1;
+            if (!warp_wait_uniform<true>(c.bars.tempty(acc), ((uint32_t)(i >> 1) & 1u) ^ 1u, c.abort)) break;
+            tc_fence_after();
+            const uint32_t d = c.tmem + (uint32_t)(acc * 256);
+            const uint32_t idesc = make_idesc_bf16(256, q.width, q.a_mn, q.b_mn);
+            const uint32_t da = q.a_mn ? 128u : 2u, db = q.b_mn ? 128u : 2u;  // 16 of K, in 16 bytes
+            for (int kb = 0; kb < q.kblocks; ++kb) {
+                if (!warp_wait_uniform<true>(c.bars.full(stage), phase, c.abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = c.ring + stage * kDenseStageBytes, sb = sa + kDenseStageBytes / 2;
+                const uint64_t ad = make_sdesc_sw128(sa, q.a_mn ? 8192 : 16, 1024);
+                const uint64_t bd = make_sdesc_sw128(sb, q.b_mn ? 8192 : 16, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_bf16_pair(d, ad + da * kk, bd + db * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
+                    tc_commit_pair(c.bars.empty(stage));
+                }
+                __syncwarp();
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if (elect_one()) tc_commit_pair(c.bars.tfull(acc));
+            __syncwarp();
+        }
+        dense_drain(c);
+    } else if (c.warp < kDenseEpiWarps) {
+        const uint32_t tempty[2] = {cluster_addr_of(c.bars.tempty(0), 0), cluster_addr_of(c.bars.tempty(1), 0)};
+        const uint32_t box = c.boxes + c.warp * 4096u;
+        const int part = c.warp >> 2, quad = c.warp & 3;
+        int i = 0;
+        for (PlainWalk w(a); w.valid(); w.next(), ++i) {
+            const PlainItem it = w.item();
+            const PlainProblem& q = a.p[it.p];
+            const int acc = i & 1, row0 = it.m0 + 128 * c.rank + 32 * quad;
+            const int last = q.width < q.N - it.n0 ? q.width : q.N - it.n0;
+            if (!warp_wait(c.bars.tfull(acc), (uint32_t)(i >> 1) & 1u, c.abort)) break;
+            tc_fence_after();
+            const uint32_t t = c.tmem + (uint32_t)(acc * 256) + ((uint32_t)(quad * 32) << 16);
+            if (row0 < q.M) {
+#pragma unroll 1
+                for (int k = part; 64 * k < last; k += 2) {
+                    uint32_t r0[32], r1[32], pk[32];
+                    tmem_ld32_nowait(t + 64 * k, r0);
+                    tmem_ld32_nowait(t + 64 * k + 32, r1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        pk[j] = pack_bf16x2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]));
+                        pk[16 + j] = pack_bf16x2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]));
+                    }
+                    if (c.lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+                    stage_row_sw128(box, c.lane, pk);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (c.lane == 0) {
+                        tma_store_2d(&maps.m[3 * it.p + 2], it.n0 + 64 * k, row0, box);
+                        bulk_commit();
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (c.lane == 0) mbar_arrive_cluster(tempty[acc]);
+        }
+        if (c.lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+    __syncwarp();
+    dense_end(c, a.status);
 }
 
 // ---------------------------------------------------------------- the join
@@ -590,10 +764,12 @@ int launch_join(const JoinArgs& a, cudaStream_t st) {
 // ----------------------------------------------------------------- launches
 int cdiv(long long a, int b) { return (int)((a + b - 1) / b); }
 
-// first: the call's first kernel, which waits for all of the stream's earlier work.
-template <int MODE, int EPI>
-int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaStream_t st, bool first = false) {
-    static std::atomic<int> clusters_fit[kMaxDevices] = {};
+// Launches a kernel on pairs of SMs: one cluster per item up to those that fit
+// at once.  first: the call's first kernel, which waits for all of the stream's
+// earlier work.
+template <typename K, typename... A>
+int launch_pairs(K kernel, std::atomic<int> (&fits)[kMaxDevices], int smem, long long items, bool first,
+                 const char* name, cudaStream_t st, const A&... args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return (int)e;
@@ -607,15 +783,14 @@ int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaS
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.blockDim = dim3(kDenseThreads, 1, 1);
-    cfg.dynamicSmemBytes = dense_smem<EPI>();
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto kernel = dense_pair_kernel<MODE, EPI>;
-    int fit = clusters_fit[dev].load(std::memory_order_relaxed);
+    int fit = fits[dev].load(std::memory_order_relaxed);
     if (fit == 0) {
         // set once per device, outside any stream capture (on the first call)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, dense_smem<EPI>());
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return (int)e;
         int sms = 0;
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -624,18 +799,28 @@ int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaS
         e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
         if (e != cudaSuccess) return (int)e;
         if (fit < 1) return (int)cudaErrorInvalidConfiguration;
-        clusters_fit[dev].store(fit, std::memory_order_relaxed);
+        fits[dev].store(fit, std::memory_order_relaxed);
     }
-    const long long items = (long long)a.tiles_m * a.tiles_n * a.splits;
     if (items <= 0) return 0;
     cfg.gridDim = dim3(2u * (unsigned)(items < fit ? items : fit), 1, 1);
     cfg.numAttrs = first ? 1 : 2;
     trace_pre(st);
-    e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.c0, m.c1, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
     trace_post(st, name);
     return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
-
+template <int MODE, int EPI>
+int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaStream_t st, bool first = false) {
+    static std::atomic<int> fits[kMaxDevices] = {};
+    return launch_pairs(dense_pair_kernel<MODE, EPI>, fits, dense_smem<EPI>(),
+                        (long long)a.tiles_m * a.tiles_n * a.splits, first, name, st, m.a, m.b, m.c0, m.c1, a);
+}
+int launch_plain(const PlainArgs& a, const PlainMaps& m, const char* name, cudaStream_t st) {
+    static std::atomic<int> fits[kMaxDevices] = {};
+    long long items = 0;
+    for (int i = 0; i < a.n; ++i) items += (long long)a.p[i].tiles_m * a.p[i].tiles_n;
+    return launch_pairs(plain_kernel, fits, dense_smem<EPI_PLAIN>(), items, false, name, st, m, a);
+}
 
 // Columns of a tile (gated: of both halves) and K ranges of a product: the
 // cheapest in clocks of a pair, as measured.  A K block takes w + 256 (the
@@ -692,22 +877,51 @@ struct Product {
     }
 };
 
+// Columns of a tile for several products in one launch: the cheapest of 256,
+// 192 and 128 for all of them, in clocks of the busiest pair as PlainWalk deals
+// the items out (256 once that is four rounds: the last one's waste is small).
+int joint_width(const Product* q, int n) {
+    int best = 256;
+    long long cost = -1;
+    for (int w = 256; w >= 128; w -= 64) {
+        long long items = 0, most = 0, load[kDenseClusters] = {};
+        for (int i = 0; i < n; ++i) {
+            const long long tiles = (long long)cdiv(q[i].M, 256) * cdiv(q[i].N, w);
+            if (items + tiles > 8 * kDenseClusters) return w == 256 ? 256 : best;
+            for (long long t = 0; t < tiles; ++t, ++items) {
+                const long long r = items / kDenseClusters, c = items % kDenseClusters;
+                load[(r & 1) ? kDenseClusters - 1 - c : c] += (long long)cdiv(q[i].K, 64) * (w + 256) + 3000;
+            }
+        }
+        for (long long l : load) most = l > most ? l : most;
+        if (cost < 0 || most < cost) {
+            cost = most;
+            best = w;
+        }
+        if (items > 4 * kDenseClusters) return best;
+    }
+    return best;
+}
+
 // Tensor maps.  bf16 rows x cols, row-major: K-major operands take 64 columns x
 // 128 rows, MN-major ones 64 x 64, stores 64 x 32.
 int map_op(CUtensorMap* m, const void* p, long long rows, int cols, int box_rows, const char* what) {
     return abi_map_2d(m, p, 2, rows, cols, cols, 64, box_rows, what);
 }
 
+PlainProblem plain(const Product& q, int width, bool a_mn, bool b_mn) {
+    return {q.M, q.N, cdiv(q.M, 256), cdiv(q.N, width), cdiv(q.K, 64), width, a_mn, b_mn};
+}
+
 Product fwd1(const moe_ffn_shape& s) { return {s.T, s.I, s.H, true}; }
 Product fwd2(const moe_ffn_shape& s) { return {s.T, s.H, s.I, false}; }
 Product dgate(const moe_ffn_shape& s) { return {s.T, s.I, s.H, false}; }
-Product dgrad(const moe_ffn_shape& s) { return {s.T, s.H, 2 * s.I, false}; }
 
 }  // namespace
 
 long long ffn_part_bytes(const moe_ffn_shape& s) {
     long long most = 0;
-    for (const Product& q : {fwd1(s), fwd2(s), dgate(s), dgrad(s)})
+    for (const Product& q : {fwd1(s), fwd2(s), dgate(s)})
         if (q.part_bytes() > most) most = q.part_bytes();
     return most;
 }
@@ -736,17 +950,21 @@ int launch_ffn_forward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st
     }
     const Product q = fwd2(s);
     DenseArgs a = q.args(clamp, f.status);
-    DenseMaps m = {};
-    if ((rc = map_op(&m.a, f.a, s.T, s.I, 128, "a"))) return rc;
-    if ((rc = map_op(&m.b, f.W2, s.I, s.H, 64, "W2"))) return rc;
     int e;
     if (a.splits > 1) {
+        DenseMaps m = {};
+        if ((rc = map_op(&m.a, f.a, s.T, s.I, 128, "a"))) return rc;
+        if ((rc = map_op(&m.b, f.W2, s.I, s.H, 64, "W2"))) return rc;
         if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.H, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
         e = launch_dense<KN, EPI_PART>(a, m, "ffn_down", st);
         if (!e) e = launch_join<JOIN_PLAIN>({f.part, s.T, s.H, a.splits, 1, clamp, f.y, nullptr}, st);
     } else {
-        if ((rc = map_op(&m.c0, f.y, s.T, s.H, 32, "y (store)"))) return rc;
-        e = launch_dense<KN, EPI_PLAIN>(a, m, "ffn_down", st);
+        PlainMaps m = {};
+        PlainArgs pa = {1, {plain(q, a.width, false, true)}, f.status};
+        if ((rc = map_op(&m.m[0], f.a, s.T, s.I, 128, "a"))) return rc;
+        if ((rc = map_op(&m.m[1], f.W2, s.I, s.H, 64, "W2"))) return rc;
+        if ((rc = map_op(&m.m[2], f.y, s.T, s.H, 32, "y (store)"))) return rc;
+        e = launch_plain(pa, m, "ffn_down", st);
     }
     return e ? abi_cuda_fail(e, "down projection launch") : MOE_OK;
 }
@@ -771,37 +989,41 @@ int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t s
         }
         if (e) return abi_cuda_fail(e, "dh launch");
     }
-    {  // dW2 = a^T dY
-        const Product q = {s.I, s.H, s.T, false, false};
-        DenseMaps m = {};
-        if ((rc = map_op(&m.a, f.a, s.T, s.I, 64, "a (MN-major)"))) return rc;
-        if ((rc = map_op(&m.b, f.dY, s.T, s.H, 64, "dY (MN-major)"))) return rc;
-        if ((rc = map_op(&m.c0, f.dW2, s.I, s.H, 32, "dW2 (store)"))) return rc;
-        if ((e = launch_dense<NN, EPI_PLAIN>(q.args(clamp, f.status), m, "ffn_dw2", st))) return abi_cuda_fail(e, "dW2 launch");
+    // dW2 = a^T dY, dW1 = x^T dh, dx = dh W1^T: the deepest products first
+    struct {
+        Product q;
+        bool a_mn, b_mn;
+        const void *A, *B;
+        void* D;
+    } job[3] = {{{s.I, s.H, s.T, false, false}, true, true, f.a, f.dY, f.dW2},
+                {{s.H, 2 * s.I, s.T, false, false}, true, true, f.x, f.dh, f.dW1},
+                {{s.T, s.H, 2 * s.I, false, false}, false, false, f.dh, f.W1, f.dx}};
+    if (2 * s.I > s.T) {
+        const auto dx = job[2];
+        job[2] = job[1];
+        job[1] = job[0];
+        job[0] = dx;
     }
-    {  // dW1 = x^T dh
-        const Product q = {s.H, 2 * s.I, s.T, false, false};
-        DenseMaps m = {};
-        if ((rc = map_op(&m.a, f.x, s.T, s.H, 64, "x (MN-major)"))) return rc;
-        if ((rc = map_op(&m.b, f.dh, s.T, 2 * s.I, 64, "dh (MN-major)"))) return rc;
-        if ((rc = map_op(&m.c0, f.dW1, s.H, 2 * s.I, 32, "dW1 (store)"))) return rc;
-        if ((e = launch_dense<NN, EPI_PLAIN>(q.args(clamp, f.status), m, "ffn_dw1", st))) return abi_cuda_fail(e, "dW1 launch");
+    const Product qs[3] = {job[0].q, job[1].q, job[2].q};
+    const int width = joint_width(qs, 3);
+    PlainMaps m = {};
+    PlainArgs a = {};
+    a.n = 3;
+    a.status = f.status;
+    for (int i = 0; i < 3; ++i) {
+        const auto& j = job[i];
+        a.p[i] = plain(j.q, width, j.a_mn, j.b_mn);
+        // rows and columns of the stored tensors: K x M or M x K, K x N or N x K
+        if ((rc = j.a_mn ? map_op(&m.m[3 * i], j.A, j.q.K, j.q.M, 64, "A (MN-major)")
+                         : map_op(&m.m[3 * i], j.A, j.q.M, j.q.K, 128, "A")))
+            return rc;
+        if ((rc = j.b_mn ? map_op(&m.m[3 * i + 1], j.B, j.q.K, j.q.N, 64, "B (MN-major)")
+                         : map_op(&m.m[3 * i + 1], j.B, j.q.N, j.q.K, width / 2, "B")))
+            return rc;
+        if ((rc = map_op(&m.m[3 * i + 2], j.D, j.q.M, j.q.N, 32, "gradient (store)"))) return rc;
     }
-    // dx = dh W1^T
-    const Product q = dgrad(s);
-    DenseArgs a = q.args(clamp, f.status);
-    DenseMaps m = {};
-    if ((rc = map_op(&m.a, f.dh, s.T, 2 * s.I, 128, "dh"))) return rc;
-    if ((rc = map_op(&m.b, f.W1, s.H, 2 * s.I, a.width / 2, "W1 (K-major)"))) return rc;
-    if (a.splits > 1) {
-        if ((rc = abi_map_nd(&m.c0, f.part, 4, {s.H, 1, s.T, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
-        e = launch_dense<KK, EPI_PART>(a, m, "ffn_dx", st);
-        if (!e) e = launch_join<JOIN_PLAIN>({f.part, s.T, s.H, a.splits, 1, clamp, f.dx, nullptr}, st);
-    } else {
-        if ((rc = map_op(&m.c0, f.dx, s.T, s.H, 32, "dx (store)"))) return rc;
-        e = launch_dense<KK, EPI_PLAIN>(a, m, "ffn_dx", st);
-    }
-    return e ? abi_cuda_fail(e, "dx launch") : MOE_OK;
+    e = launch_plain(a, m, "ffn_grads", st);
+    return e ? abi_cuda_fail(e, "gradient launch") : MOE_OK;
 }
 
 }  // namespace moe
