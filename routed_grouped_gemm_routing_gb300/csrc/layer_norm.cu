@@ -931,8 +931,17 @@ __global__ void __launch_bounds__(256) ln_bwd_join(const float* part, int nb, in
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;  // of 2 H
     float a = 0.0f;
-    if (col < 2 * H)
-        for (int i = k; i < nb; i += 8) a += part[(size_t)i * 2 * H + col];
+    if (col < 2 * H) {
+        int i = k;
+        for (; i + 56 < nb; i += 64) {  // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = part[(size_t)(i + 8 * j) * 2 * H + col];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a += v[j];
+        }
+        for (; i < nb; i += 8) a += part[(size_t)i * 2 * H + col];
+    }
     s[k][lane] = a;
     __syncthreads();
     if (k == 0 && col < 2 * H) {

@@ -458,10 +458,11 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(const float* o, const i
     for (long long v = (long long)blockIdx.x * 256 + threadIdx.x; v < n4; v += (long long)gridDim.x * 256) {
         const int tok = (int)(v * 4 / H), h = (int)(v * 4 - (long long)tok * H);
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
         for (int j = 0; j < k; ++j) {
             const int e = __ldg(ids + (size_t)tok * k + j);
-            if (e < 0 || e >= E) continue;
-            const float4 a = *reinterpret_cast<const float4*>(o + ((size_t)tok * k + j) * H + h);
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (e >= 0 && e < E) a = *reinterpret_cast<const float4*>(o + ((size_t)tok * k + j) * H + h);
             s.x += a.x;
             s.y += a.y;
             s.z += a.z;
