@@ -228,7 +228,8 @@ int moe_ffn_forward(const moe_ffn_shape* shape, const void* x, const void* W1, c
     f.part = reinterpret_cast<float*>(w + L.part);
     f.status = reinterpret_cast<int32_t*>(w + L.status);
     f.y = y;
-    return launch_ffn_forward(*shape, f, (cudaStream_t)stream);
+    return ffn_few_takes(*shape) ? launch_ffn_few(*shape, f, (cudaStream_t)stream)
+                                 : launch_ffn_forward(*shape, f, (cudaStream_t)stream);
 }
 
 int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, const void* W1, const void* W2,

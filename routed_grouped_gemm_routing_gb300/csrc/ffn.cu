@@ -9,7 +9,7 @@
 //
 // Six products of 2 T H I (y, da, dW2) or 4 T H I (h, dx, dW1) operations, all
 // bound by the tensor cores from a few hundred tokens on: a step of 8192 x 7168 x
-// 2048 takes 1.18 ms in a short burst, 1.84 PFLOP/s, 95 % of the measured bf16
+// 2048 takes 1.17 ms in a short burst, 1.85 PFLOP/s, 96 % of the measured bf16
 // rate (1.37 ms and 1.58 PFLOP/s, 92 % of the sustained rate, when run for
 // seconds under the power limit).  One kernel serves
 // them (dense_pair_kernel): D[256 x 256] per pair of SMs, tcgen05 cta_group::2,
@@ -42,8 +42,10 @@
 // one before it before it touches any tensor.  dW2, dW1 and dx need nothing of
 // each other once dh is there: one launch takes the tiles of all three, the
 // deepest products first, so that one last round is ragged instead of three
-// (4096 x 2048 x
-// 1408: 188 -> 166 us a step; 777 x 1160 x 712: 56 -> 44 us).
+// (4096 x 2048 x 1408: 164 us a step, 186 in three launches; 777 x 1160 x 712:
+// 44 and 56 us).
+//
+// The forward of up to 16 tokens is ffn_few.cu's.
 //
 // Roles (10 warps per CTA): 0-7 epilogue (warp w: TMEM lanes 32 (w % 4) .. of
 // the CTA's 128 rows, every other group of columns from w / 4 on; with four
@@ -112,13 +114,6 @@ struct DenseBars {
 };
 static_assert(8 * (2 * 6 + 5 + kDenseEpiWarps) + 8 <= kDenseTail, "barrier area");
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-            "r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, int c0, int c1, int c2, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                      reinterpret_cast<uint64_t>(m)),

@@ -330,7 +330,11 @@ int abi_map_2d(CUtensorMap* m, const void* p, int elt, long long rows, long long
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t str[1] = {(cuuint64_t)stride_elems * (cuuint64_t)elt};
     cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    return make_map(m, p, 2, dims, str, box, what, CU_TENSOR_MAP_SWIZZLE_128B,
+    const int width = box_cols * elt;
+    return make_map(m, p, 2, dims, str, box, what,
+                    width == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                    : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : CU_TENSOR_MAP_SWIZZLE_128B,
                     elt == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 

@@ -86,8 +86,8 @@ int abi_fail(int code, const char* msg);
 int abi_cuda_fail(int cuda_error, const char* what);
 // Makes the device that owns `data` current and gives its SM count.
 int abi_select_device(const void* data, int* sms);
-// Tensor map of a row-major matrix, 128-byte swizzle: element size 2 (bf16) or
-// 4 (f32); box_cols * element size must be 128.
+// Tensor map of a row-major matrix: element size 2 (bf16) or 4 (f32);
+// box_cols * element size must be 128, 64 or 32 and is the swizzle's width.
 int abi_map_2d(CUtensorMap* m, const void* p, int elt, long long rows, long long cols, long long stride_elems,
                int box_cols, int box_rows, const char* what);
 
@@ -157,6 +157,10 @@ long long ffn_part_bytes(const moe_ffn_shape& s);
 // MOE_OK or an error code with its message set.
 int launch_ffn_forward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
 int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
+// The forward's form for few tokens.
+constexpr int kFfnFewTokens = 16;
+bool ffn_few_takes(const moe_ffn_shape& s);
+int launch_ffn_few(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
 
 // Layout of the three workspaces (host only).
 int compute_layout(const moe_shape* s, moe_layout* L);

@@ -6,11 +6,12 @@ of the products' sizes for the K used here: A = 2^-19 |x||w|.  a, dh and the
 outputs are rounded to bf16 once (unit roundoff 2^-8: 8-bit significands).
 The device exp errs by 2^-20 relative: 2^-18 |a| covers it.  |silu'| <= 1.1,
 |silu''| <= 0.5.  These bounds add up worst cases; so each output's error in
-the 2-norm is bounded too: three independent roundings at most, each 2^-9 /
-sqrt(3) = 1.13e-3 rms of a value at the worst place of its binade, are below
-3e-3 of the output's norm.  That is an average over independent roundings: it
-holds where a row has at least 64 of them (at H = I = 8 and one token the norm
-of dW1 is one or two values', whose two roundings may err by 7.8e-3)."""
+the 2-norm is bounded too: three independent roundings at most, each at
+most 2^-8 / sqrt(3) = 2.3e-3 rms of a value at the foot of its binade and 1.6e-3
+over a whole binade, are below 3e-3 of the output's norm.  That is an average
+over independent roundings: it holds where a row has at least 64 of them (at H =
+I = 8 and one token the norm of dW1 is one or two values', whose two roundings
+may err by 7.8e-3)."""
 import pytest
 import torch
 
@@ -234,3 +235,61 @@ def test_refusals():
         ffn_forward(x.cpu(), W1, W2, ws)
     with pytest.raises(ValueError):
         ffn_backward(dy[:2], x, W1, W2, ws)
+
+
+@pytest.mark.parametrize("T,H,I", [
+    (2, 1160, 712),    # K in four parts, the last one shorter
+    (9, 1160, 712),    # two jobs of eight tokens
+    (16, 520, 136),
+    (7, 16, 4104),     # one unit of K; a tile of eight features
+    (9, 520, 2056),    # sixteen tokens a job, ragged tiles
+    (16, 4096, 1024), (13, 2048, 1408), (15, 1032, 4096),
+    (17, 1160, 712),   # the large form again
+    (4, 4096, 10248), (16, 4096, 10248),  # more tiles than SMs, K in four parts
+    (3, 10248, 4096),  # the same in the down projection's tiles, K whole
+    (5, 10248, 8200),  # and K in four parts
+])
+def test_few_tokens_forward(T, H, I):
+    x, W1, W2, dy = _inputs(T, H, I, T + I)
+    ws = FFNWorkspace(T, H, I, train=False)
+    y = ffn_forward(x, W1, W2, ws)
+    assert ws.status() == 0
+    x64 = x.double()
+    h, eh = x64 @ W1.double(), A * (x64.abs() @ W1.double().abs())
+    g, u, eg, eu = h[:, :I], h[:, I:], eh[:, :I], eh[:, I:]
+    s = torch.sigmoid(g)
+    a = g * s * u
+    ea = 1.1 * eg * u.abs() + (g * s).abs() * eu + (2.0 ** -8 + 2.0 ** -18) * a.abs()
+    v = a @ W2.double()
+    w = W2.double().abs()
+    _close("y", y, (v, ea @ w + A * (a.abs() @ w) + 2.0 ** -8 * v.abs()), many=min(H, I) >= 64)
+
+
+@pytest.mark.parametrize("T,H,I", [(5, 136, 72), (12, 136, 72), (11, 1032, 1096)])
+def test_few_tokens_rows_and_guards(T, H, I):
+    """Each row is its own token's alone, and nothing is written around the outputs."""
+    x, W1, W2, _ = _inputs(T, H, I, 12)
+    ws = FFNWorkspace(T, H, I)
+    out = torch.full((T + 40, H), 3.0, dtype=BF, device="cuda")
+    B.moe_ffn_forward(ws.shape, x, W1, W2, ws.saved, ws.ws, out[:T])
+    good = ffn_forward(x, W1, W2, ws)
+    assert torch.equal(out[:T], good) and (out[T:] == 3.0).all()
+    x2 = x.clone()
+    x2[1, 3], x2[4, H - 1] = float("nan"), float("inf")
+    y = ffn_forward(x2, W1, W2, ws)
+    keep = [t for t in range(T) if t not in (1, 4)]
+    assert torch.equal(y[keep], good[keep]) and y[1].isnan().all() and not torch.isfinite(y[4]).any()
+
+
+def test_few_tokens_clamped_training():
+    """The h that the form for few tokens leaves, read by the backward."""
+    H, I, c = 2048, 1408, 0.7
+    x, W1, W2, dy = _inputs(16, H, I, 13)
+    ws = FFNWorkspace(16, H, I, activation_clamp=c)
+    y = ffn_forward(x, W1, W2, ws)
+    dx, dW1, dW2 = ffn_backward(dy, x, W1, W2, ws)
+    ref, near = _ref(x, W1, W2, dy, c)
+    _close("y", y, ref["y"])
+    _close("dW2", dW2, ref["dW2"])
+    _close("dW1", dW1[:, ~near.any(0)], tuple(t[:, ~near.any(0)] for t in ref["dW1"]))
+    _close("dx", dx[~near.any(1)], tuple(t[~near.any(1)] for t in ref["dx"]))
