@@ -13,7 +13,8 @@
 // one sum of x per row and group, made once per block.  A group's sum is then
 // scaled and added in FP32; nothing is rounded before the output.
 //
-// mma m16n8k16: A = 16 rows of W, B = up to 8 rows of x.  (A tcgen05.mma would
+// mma m16n8k16: A = 16 rows of W, B = up to 8 rows of x (kNt column tiles of
+// them: 8 or 16 rows to a job).  (A tcgen05.mma would
 // need the unpacked weights in shared memory first: the unpacking through
 // registers is what has to be cheap here, and 8 columns are far below its
 // tile.)  The order of the codes in memory makes a lane's 16 bytes of a
@@ -21,7 +22,7 @@
 // 32 j + 8 t .. + 7, code 2 m in nibble m, code 2 m + 1 in nibble m + 4, so
 // that lane t's pair m of group j meets x[32 j + 8 t + 2 m, + 1].
 //
-// A block takes a job (up to 8 rows that use the same matrix) and a range
+// A block takes a job (up to 8 or 16 rows that use the same matrix) and a range
 // of tiles of 32 rows of W (W4_GATED: 16 gate rows and their 16 up rows); KS
 // of its warps share a tile, every KS-th unit of 256 codes each, and join their
 // FP32 sums in shared memory in a fixed order.  One lane copies its warp's next
@@ -30,6 +31,12 @@
 // range: with a 16-byte copy per lane and fragment instead, the addresses alone
 // took as many instructions as the products.  Scales come by plain loads, one
 // row per lane and a unit ahead, and go to the fragments by shuffles.
+//
+// Measured (the bytes at the copy rate): one row of a 131072 x 7168 matrix
+// 88.7 us, 5.3 TB/s (74); 16384 x 7168, G = 128: one row 17.2 us, 8 rows 20.3
+// (9.0); 16380 x 7168, G = 32, 12 rows 30.1 (9.8).  In the steady state 51 % of
+// the issue slots and 62 % of the ALU's are taken: what is left of the floor is
+// latency of the unpacking, four warps to a scheduler.
 #include <cmath>
 
 #include "grouped_gemm_2sm.cuh"
@@ -45,11 +52,7 @@ constexpr int kUnitBytes = 4096;  // 32 rows x 128 bytes
 // 64 registers and 32 warps per SM instead of 16 was slower: 16384 x 7168 at one
 // row 20.6 us against 17.5, twice the bookkeeping and reads of x per weight.)
 constexpr int kFrag = 4;
-// Rows of a job: the columns of one product.  (Two column tiles per job, the
-// weights unpacked once for 16 rows, took longer than two jobs: 16 rows of a
-// 16384 x 7168 matrix 52.6 us against 39.6; their registers left no room for
-// both blocks of a unit.)
-constexpr int kR = 8;
+constexpr int kR = 8;  // rows of x that one product takes; a job has kNt times as many
 
 enum W4Epi { W4_PLAIN, W4_GATED, W4_SLOT };
 
@@ -109,15 +112,15 @@ struct W4Smem {
     int x, xs, red, bars, total;
 };
 __host__ __device__ __forceinline__ int w4_units(int K, int kparts) { return ((K + 255) / 256 + kparts - 1) / kparts; }
-template <int G>
+template <int G, int kNt>
 __host__ __device__ __forceinline__ W4Smem w4_smem(int K, int nw, int rows, int kparts) {
     W4Smem s;
     const int kpad = w4_units(K, kparts) * 256;
     s.x = nw * kSlots * kUnitBytes;
     // a row of x and 64 bytes: the eight rows' 16-byte fragments in all banks
     s.xs = s.x + rows * (2 * kpad + 64);
-    s.red = s.xs + (kpad / G) * kR * 4;
-    s.bars = s.red + (kparts > 1 ? kparts : 2) * nw * 256 * 4;
+    s.red = s.xs + (kpad / G) * kR * kNt * 4;
+    s.bars = s.red + (kparts > 1 || kNt > 1 ? 1 : 2) * nw * 256 * kNt * 4;
     s.total = s.bars + nw * kSlots * 8 + 1024;
     return s;
 }
@@ -149,18 +152,19 @@ __device__ __forceinline__ void scales_of(uint2 v, int src, uint32_t (&u)[2]) {
 __device__ __forceinline__ float scale(uint32_t u, int i) { return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16); }
 
 // mq: the codes as [E N] rows of K / 2 bytes.
-template <int G, int EPI>
+template <int G, int EPI, int kNt>
 __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUtensorMap mq, const W4Args p) {
     constexpr int kSw = G == 32 ? 2 : 1;              // words of a row's scales of a 128-code block
     constexpr int kTile = EPI == W4_GATED ? 16 : 32;  // output features of a tile
-    constexpr int kSide = G == 32 ? 1 : 2;  // 128-code blocks worked on side by side: four chains of dependent products
+    constexpr int kSide = G == 32 || kNt > 1 ? 1 : 2;  // 128-code blocks worked on side by side: four chains of dependent products
+    constexpr int kRows = kR * kNt;
     typedef typename W4Scales<G>::T Scales;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ int row_of[kR];  // row or slot of every row of the job
+    __shared__ int row_of[kRows];  // row or slot of every row of the job
     __shared__ int job_n;
     __shared__ int abort_word;
     volatile int* abort = &abort_word;
-    const int R = p.R;  // rows of a job, at most kR
+    const int R = p.R;  // rows of a job, at most kRows
     const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int K = p.K, KB = K / 128, KS = p.ks, NG = nw / KS;
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     // (the offsets of the block's largest job: they do not wait for job_n)
-    const W4Smem L = w4_smem<G>(K, nw, R, p.kparts);
+    const W4Smem L = w4_smem<G, kNt>(K, nw, R, p.kparts);
     const uint32_t ring = base + warp * kSlots * kUnitBytes, bar = base + L.bars + warp * kSlots * 8;
     if (lane == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(bar + 8 * i, 1);
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     if (n == 0) return;  // not the leading slot
 
     __nv_bfloat16* xsm = reinterpret_cast<__nv_bfloat16*>(smem + L.x);
-    float* xs = reinterpret_cast<float*>(smem + L.xs);  // [K / G][kR]: -136 sum of x
+    float* xs = reinterpret_cast<float*>(smem + L.xs);  // [K / G][kRows]: -136 sum of x
     float* red = reinterpret_cast<float*>(smem + L.red);
 
     // ---- the stream of this warp's weights: tiles gi, gi + NG, .. of the
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     if (kn & 255) {  // an odd last block
         for (int v = threadIdx.x; v < n * 16; v += blockDim.x)
             *reinterpret_cast<uint4*>(xsm + (v >> 4) * xst + kn + (v & 15) * 8) = make_uint4(0u, 0u, 0u, 0u);
-        for (int v = threadIdx.x; v < (128 / G) * kR; v += blockDim.x) xs[(kn / G) * kR + v] = 0.0f;
+        for (int v = threadIdx.x; v < (128 / G) * kRows; v += blockDim.x) xs[(kn / G) * kRows + v] = 0.0f;
     }
     for (int v = threadIdx.x; v < n * (kn / 8); v += blockDim.x) {  // kn / 8 is a multiple of 16: whole groups per row
         const int r = v / (kn / 8), c = v - r * (kn / 8);
@@ -290,12 +294,15 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
         const uint32_t act = v - lane + 32 <= n * (kn / 8) ? 0xffffffffu : 0x0000ffffu;
 #pragma unroll
         for (int d = 1; d < G / 8; d <<= 1) s += __shfl_xor_sync(act, s, d);
-        if ((c & (G / 8 - 1)) == 0) xs[(c / (G / 8)) * kR + r] = -136.0f * s;
+        if ((c & (G / 8 - 1)) == 0) xs[(c / (G / 8)) * kRows + r] = -136.0f * s;
     }
     __syncthreads();
 
-    // this lane's row (a row past the job's repeats the last)
-    const uint4* xrow = reinterpret_cast<const uint4*>(xsm + (g < n ? g : n - 1) * xst) + t;
+    // this lane's rows (a row past the job's repeats the last)
+    const uint4* xrow[kNt];
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt)
+        xrow[nt] = reinterpret_cast<const uint4*>(xsm + (8 * nt + g < n ? 8 * nt + g : n - 1) * xst) + t;
     // y of feature f and row r of the job
     auto emit = [&](int f, int r, float v, float up) {
         if (f >= p.F || r >= n) return;
@@ -319,19 +326,19 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
     for (int round = 0; round < rounds; ++round) {
         const int tile = tile0 + gi + round * NG;
         const bool live = tile < tile1;
-        if (p.kparts == 1 && !live) break;
-        float acc[2][4];
+        if (kNt == 1 && p.kparts == 1 && !live) break;
+        float acc[kNt][2][4];
+        auto fill = [&](float v) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.0f;
+            for (int i = 0; i < 8 * kNt; ++i) acc[i >> 3][(i >> 2) & 1][i & 3] = v;
+        };
+        fill(0.0f);
         for (int u = live ? U0 + ks : U; u < U; u += KS) {
             const Scales sc2[2] = {snext[0], snext[1]};
             fetch_scales();
             fetch();
             // a wait that gave up leaves NaN in the outputs and lets the others go
-            if (!warp_wait(bar + 8 * slot, phase, abort)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = __uint_as_float(0x7fc00000u);
-            }
+            if (!warp_wait(bar + 8 * slot, phase, abort)) fill(__uint_as_float(0x7fc00000u));
             const uint32_t unit = ring + slot * kUnitBytes;
 #pragma unroll
             for (int h0 = 0; h0 < 2; h0 += kSide) {
@@ -345,16 +352,21 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
                         w[h][i] = make_uint4(v.x, v.y, v.z, v.w);
                         scales_of(sc2[h0 + h], g + 8 * i, sc[h][i]);
                     }
-                float c[kSide][2][4];
+                float c[kSide][kNt][2][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
 #pragma unroll
                     for (int h = 0; h < kSide; ++h) {
                         const int kb = 2 * (u - U0) + h0 + h;  // of this block's part
-                        const uint4 b = xrow[kb * 16 + j * 4];
-                        float2 start;
-                        if (j % (G / 32) == 0)
-                            start = *reinterpret_cast<const float2*>(xs + ((kb * 128 + j * 32) / G) * kR + 2 * t);
+                        uint4 b[kNt];
+                        float2 start[kNt];
+#pragma unroll
+                        for (int nt = 0; nt < kNt; ++nt) {
+                            b[nt] = xrow[nt][kb * 16 + j * 4];
+                            if (j % (G / 32) == 0)
+                                start[nt] = *reinterpret_cast<const float2*>(xs + ((kb * 128 + j * 32) / G) * kRows +
+                                                                             8 * nt + 2 * t);
+                        }
 #pragma unroll
                         for (int rt = 0; rt < 2; ++rt) {
                             const uint32_t a0 = word_of(w[h][2 * rt], j), a1 = word_of(w[h][2 * rt + 1], j);
@@ -362,11 +374,16 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
                                            u2 = pair128<2>(a0, mask), u3 = pair128<3>(a0, mask);
                             const uint32_t v0 = pair128<0>(a1, mask), v1 = pair128<1>(a1, mask),
                                            v2 = pair128<2>(a1, mask), v3 = pair128<3>(a1, mask);
-                            if (j % (G / 32) == 0)
-                                mma_bf16_from(c[h][rt], u0, v0, u1, v1, b.x, b.y, start.x, start.y);
-                            else
-                                mma_bf16(c[h][rt], u0, v0, u1, v1, b.x, b.y);
-                            mma_bf16(c[h][rt], u2, v2, u3, v3, b.z, b.w);
+#pragma unroll
+                            for (int nt = 0; nt < kNt; ++nt) {
+                                float(&d)[4] = c[h][nt][rt];
+                                if (j % (G / 32) == 0)
+                                    mma_bf16_from(d, u0, v0, u1, v1, b[nt].x, b[nt].y, start[nt].x, start[nt].y);
+                                else
+                                    mma_bf16(d, u0, v0, u1, v1, b[nt].x, b[nt].y);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < kNt; ++nt) mma_bf16(c[h][nt][rt], u2, v2, u3, v3, b[nt].z, b[nt].w);
                         }
                     }
                     if ((j + 1) % (G / 32) == 0) {
@@ -377,10 +394,15 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
                             for (int rt = 0; rt < 2; ++rt) {
                                 const float s0 = scale(sc[h][2 * rt][si / 2], si),
                                             s1 = scale(sc[h][2 * rt + 1][si / 2], si);
-                                acc[rt][0] = fmaf(s0, c[h][rt][0], acc[rt][0]);
-                                acc[rt][1] = fmaf(s0, c[h][rt][1], acc[rt][1]);
-                                acc[rt][2] = fmaf(s1, c[h][rt][2], acc[rt][2]);
-                                acc[rt][3] = fmaf(s1, c[h][rt][3], acc[rt][3]);
+#pragma unroll
+                                for (int nt = 0; nt < kNt; ++nt) {
+                                    float(&o)[4] = acc[nt][rt];
+                                    const float(&d)[4] = c[h][nt][rt];
+                                    o[0] = fmaf(s0, d[0], o[0]);
+                                    o[1] = fmaf(s0, d[1], o[1]);
+                                    o[2] = fmaf(s1, d[2], o[2]);
+                                    o[3] = fmaf(s1, d[3], o[3]);
+                                }
                             }
                     }
                 }
@@ -392,9 +414,9 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
             }
         }
         // register i of lane (g, t) of operand rt: row 16 rt + g + 8 (i / 2) of
-        // the tile, row 2 t + i % 2 of the job
-        auto put = [&](int i, float v0, float v1) {
-            const int f = tile * kTile + g + 8 * (i >> 1), r = 2 * t + (i & 1);
+        // the tile, row 2 t + i % 2 of the column tile nt: pair q = 4 nt + i of them
+        auto put = [&](int q, float v0, float v1) {
+            const int f = tile * kTile + g + 8 * ((q >> 1) & 1), r = 8 * (q >> 2) + 2 * t + (q & 1);
             if constexpr (EPI == W4_GATED) {
                 emit(f, r, v0, v1);
             } else {
@@ -402,44 +424,58 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
                 emit(f + 16, r, v1, 0.0f);
             }
         };
-        if (KS == 1 && p.kparts == 1) {
+        constexpr int kPairs = 4 * kNt;
+        if (kNt == 1 && KS == 1 && p.kparts == 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) put(i, acc[0][i], acc[1][i]);
+            for (int q = 0; q < kPairs; ++q) put(q, acc[q >> 2][0][q & 3], acc[q >> 2][1][q & 3]);
         } else {
-            constexpr int kPer = 256;  // floats of a warp
-            const bool split = p.kparts > 1;
-            // split: one set of sums, in the cluster's first block: that block
-            // has started, and the last round's sums have been read
-            if (split) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-            float* mine = red + (size_t)((split ? part : buf) * nw + warp) * kPer + lane;
-            if (split && part > 0) {
-                const uint32_t to = cluster_addr_of(smem_addr(mine), 0);
+            // The pairs of a tile: [warp][pair][operand][lane].  A cluster's blocks
+            // finish a share of them each: [part][warp][pair of the share].. there
+            constexpr int kPer = kPairs * 64;  // floats of a warp
+            if (kNt > 1 || p.kparts > 1) {
+                const int log_share = 31 - __clz(kPairs / p.kparts), share = 1 << log_share;  // kparts is 2 or 4
+                const float* mine = red + ((part * nw + warp) << log_share) * 64 + lane;
+                // every block has started, and has read the last round's sums
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 128), "f"(acc[i >> 2][i & 3]) : "memory");
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mine[i * 32] = acc[i >> 2][i & 3];
-            }
-            if (split) {
-                asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-            } else {
-                asm volatile("bar.sync %0, %1;" ::"r"(gi + 1), "r"(KS * 32) : "memory");
-            }
-            if (live && part == 0) {
-                const float* all = red + (size_t)((split ? 0 : buf) * nw + gi * KS) * kPer + lane;
-                for (int i = ks; i < 4; i += KS) {
-                    float v0 = 0.0f, v1 = 0.0f;
-                    for (int c = 0; c < p.kparts; ++c)
-                        for (int k = 0; k < KS; ++k) {
-                            v0 += all[(c * nw + k) * kPer + i * 32];
-                            v1 += all[(c * nw + k) * kPer + (4 + i) * 32];
-                        }
-                    put(i, v0, v1);
+                for (int q = 0; q < kPairs; ++q) {
+                    const uint32_t to = cluster_addr_of(smem_addr(mine + (q & (share - 1)) * 64), q >> log_share);
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(acc[q >> 2][0][q & 3]) : "memory");
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 128), "f"(acc[q >> 2][1][q & 3]) : "memory");
                 }
+                asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+                if (live) {
+                    for (int i = ks; i < share; i += KS) {
+                        float v0 = 0.0f, v1 = 0.0f;
+                        for (int c = 0; c < p.kparts; ++c)
+                            for (int k = 0; k < KS; ++k) {
+                                const float* o = red + (((c * nw + gi * KS + k) << log_share) + i) * 64 + lane;
+                                v0 += o[0];
+                                v1 += o[32];
+                            }
+                        put(part * share + i, v0, v1);
+                    }
+                }
+                asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            } else {
+                float* mine = red + (size_t)(buf * nw + warp) * kPer + lane;
+#pragma unroll
+                for (int q = 0; q < kPairs; ++q) {
+                    mine[q * 64] = acc[q >> 2][0][q & 3];
+                    mine[q * 64 + 32] = acc[q >> 2][1][q & 3];
+                }
+                asm volatile("bar.sync %0, %1;" ::"r"(gi + 1), "r"(KS * 32) : "memory");
+                const float* all = red + (size_t)(buf * nw + gi * KS) * kPer + lane;
+                for (int q = ks; q < kPairs; q += KS) {
+                    float v0 = 0.0f, v1 = 0.0f;
+                    for (int k = 0; k < KS; ++k) {
+                        v0 += all[k * kPer + q * 64];
+                        v1 += all[k * kPer + q * 64 + 32];
+                    }
+                    put(q, v0, v1);
+                }
+                buf ^= 1;  // two halves in turn: two tiles on, this barrier has passed
             }
-            if (split) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-            buf ^= 1;  // not split: the next tile's sums go to the other half; two tiles on, this barrier has passed
         }
     }
     if (p.kparts > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -517,29 +553,31 @@ __global__ void __launch_bounds__(128) w4_quantize_kernel(const __nv_bfloat16* _
 
 constexpr int kW4Smem = 224 * 1024;  // dynamic shared memory of a block
 constexpr int kSmSmem = 228 * 1024;  // of an SM, with 1 KB taken by every block
-constexpr int kFewRows = 0;
 
 // Launch shape: warps per tile and tiles per block for blocks of nw warps,
 // per_sm of them on an SM.  Two times bound a choice, and the larger one is
 // made small: the busiest SM's units at the rate of its warps, and the longest
 // chain of a warp over the blocks that follow one another.  In clocks, fitted
-// to sweeps of both at 1, 8 and 32 tokens: an SM takes 280 per unit with 16
-// warps, 437 with 8; a warp alone 2200; a join 600, and 100 of the SM's per warp
-// of it; a block's start (job, x) 1200 and a third per element of x.
-void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
-    const long long U = w4_units(a->K, a->kparts), slots = 152 * per_sm;
+// to sweeps of both at 1 to 32 tokens: an SM takes 280 per unit with 16 warps,
+// 437 with 8 (two column tiles: 340, 675); a warp alone 2200 (3200); a join of
+// warps 600, and 100 of the SM's per warp of it, of a cluster 4000, in which all
+// its blocks stand still; a block's start (job, x) 1200 and a third per element
+// of x.  Clusters of four find room for 144 blocks on the 152 SMs (148 take
+// twice as long); a few are left to another GPU's layout.
+void w4_shape(W4Args* a, int jobs, int nw, int per_sm, int nt) {
+    const long long U = w4_units(a->K, a->kparts), sms = a->kparts > 2 ? 136 : 152, slots = sms * per_sm;
     const long long start = 1200 + (long long)a->R * a->K / a->kparts / 3;
     long long best = -1;
     for (int ks = 1; ks <= nw; ks *= 2) {
-        const int ng = nw / ks, join = ks * a->kparts > 1;
+        const int ng = nw / ks, join = a->kparts > 1 ? 4000 : ks > 1 ? 600 : 0, lone = nt > 1 ? 3200 : 2200;
         for (int rounds = 1; rounds <= 64; ++rounds) {
             const int tpc = ng * rounds;
             const long long tiles = tpc < a->tiles ? tpc : a->tiles;
-            const long long blocks = (long long)jobs * a->kparts * ((a->tiles + tpc - 1) / tpc), on_sm = (blocks + 151) / 152;
+            const long long blocks = (long long)jobs * a->kparts * ((a->tiles + tpc - 1) / tpc), on_sm = (blocks + sms - 1) / sms;
             const long long warps = (on_sm < per_sm ? on_sm : per_sm) * nw;
-            const long long unit = 3500 / warps > 280 ? 3500 / warps : 280;
-            const long long rate = on_sm * (tiles * (U * unit + join * 100 * ks) + start);
-            const long long lat = (blocks + slots - 1) / slots * (3000 + rounds * (2200 * ((U + ks - 1) / ks) + join * 600));
+            const long long unit = nt > 1 ? 5400 / warps : 3500 / warps > 280 ? 3500 / warps : 280;
+            const long long rate = on_sm * (tiles * (U * unit + (join ? 100 * ks : 0)) + (a->kparts > 1 ? rounds * join : 0) + start);
+            const long long lat = (blocks + slots - 1) / slots * (3000 + rounds * (lone * ((U + ks - 1) / ks) + join));
             const long long cost = (lat > rate ? lat : rate) * 8 + (lat < rate ? lat : rate);
             if (best < 0 || cost < best) {
                 best = cost;
@@ -555,28 +593,29 @@ void w4_shape(W4Args* a, int jobs, int nw, int per_sm) {
 // the jobs.  after_own: the kernel before it in the stream is this file's and
 // writes x only, so this one may start, find its job and fetch weights, while
 // that one drains (it waits before it reads x).
-template <int G, int EPI>
+template <int G, int EPI, int kNt>
 int w4_launch(W4Args a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
     static SmemLimit limit;
     a.mask = 0x000f000fu;
     a.tiles = EPI == W4_GATED ? (a.F + 15) / 16 : (a.F + 31) / 32;
-    a.R = (rows + (rows + kR - 1) / kR - 1) / ((rows + kR - 1) / kR);  // 12 rows: 6 and 6
+    constexpr int kRows = kR * kNt;
+    a.R = (rows + (rows + kRows - 1) / kRows - 1) / ((rows + kRows - 1) / kRows);  // 20 rows: 10 and 10
     // K is split over a cluster where the rows of x leave an SM fewer than 16
     // warps (8 rows of a 7168 x 7168 matrix: 26.6 us with 8 warps, 17.2 us with
     // 16 and half of K each); where four parts are not enough, fewer rows per job.
-    a.kparts = 1;
+    a.kparts = kNt;  // (two column tiles: the joins of a cluster alone)
     auto sixteen = [&](int parts) {  // one block of 16 warps or two of 8 fit an SM
-        return w4_smem<G>(a.K, 16, a.R, parts).total <= kW4Smem ||
-               2 * (w4_smem<G>(a.K, 8, a.R, parts).total + 1024) <= kSmSmem;
+        return w4_smem<G, kNt>(a.K, 16, a.R, parts).total <= kW4Smem ||
+               2 * (w4_smem<G, kNt>(a.K, 8, a.R, parts).total + 1024) <= kSmSmem;
     };
-    while (a.kparts < 4 && !sixteen(a.kparts) && w4_units(a.K, 2 * a.kparts) >= 8) a.kparts *= 2;
-    while (a.R > 1 && w4_smem<G>(a.K, 4, a.R, a.kparts).total > kW4Smem) --a.R;
-    auto bytes = [&](int nw) { return w4_smem<G>(a.K, nw, a.R, a.kparts).total; };
+    while (a.kparts < 4 && !sixteen(a.kparts) && w4_units(a.K, 2 * a.kparts) >= (kNt > 1 ? 4 : 8)) a.kparts *= 2;
+    while (a.R > 1 && w4_smem<G, kNt>(a.K, 4, a.R, a.kparts).total > kW4Smem) --a.R;
+    auto bytes = [&](int nw) { return w4_smem<G, kNt>(a.K, nw, a.R, a.kparts).total; };
     const int per_sm = 2 * (bytes(8) + 1024) <= kSmSmem ? 2 : 1;
     const int nw = per_sm == 2 ? 8 : bytes(16) <= kW4Smem ? 16 : bytes(8) <= kW4Smem ? 8 : 4;
     const int jobs = a.ids ? a.slots : (a.rows + a.R - 1) / a.R;
-    w4_shape(&a, a.ids ? a.busy : jobs, nw, per_sm);
-    if (const int e = limit.allow(w4_kernel<G, EPI>, kW4Smem)) return e;
+    w4_shape(&a, a.ids ? a.busy : jobs, nw, per_sm, kNt);
+    if (const int e = limit.allow(w4_kernel<G, EPI, kNt>, kW4Smem)) return e;
     CUtensorMap m;
     if (abi_map_u8(&m, q, (long long)a.E * a.N, a.K / 2, 128, EPI == W4_GATED ? 16 : 32, "4-bit codes"))
         return (int)cudaErrorInvalidValue;
@@ -598,14 +637,30 @@ int w4_launch(W4Args a, const uint8_t* q, int rows, bool after_own, cudaStream_t
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_kernel<G, EPI>, m, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_kernel<G, EPI, kNt>, m, a);
     return (int)(e != cudaSuccess ? e : cudaGetLastError());
+}
+template <int G, int EPI>
+int w4_launch_n(const W4Args& a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
+    // More than eight rows of one matrix: two column tiles, the weights unpacked
+    // once for 16 rows, where x leaves an SM 16 warps (16 rows, one or two tiles,
+    // us: 16384 x 7168 G = 32 40.6 | 32.1, G = 128 34.6 | 25.6, 4096 x 4096 G =
+    // 128 11.1 | 9.2) and the matrix has work for them (2048 x 2048 G = 32 6.3 |
+    // 8.0, 1408 x 4096 at 12 rows 8.0 | 9.5).  An expert seldom has so many rows
+    // that its second tile pays (32 tokens, top 2 of 8 experts of 2048 x 1408:
+    // 35.4 | 51.5).
+    if constexpr (EPI != W4_SLOT) {
+        const bool two = rows > kR && !a.ids && (long long)a.N * a.K > (1 << 23) && a.K >= 1024 &&
+                         w4_smem<G, 2>(a.K, 16, 2 * kR, 4).total <= kW4Smem;
+        if (two) return w4_launch<G, EPI, 2>(a, q, rows, after_own, st);
+    }
+    return w4_launch<G, EPI, 1>(a, q, rows, after_own, st);
 }
 template <int EPI>
 int w4_launch_g(int G, const W4Args& a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
-    return G == 32   ? w4_launch<32, EPI>(a, q, rows, after_own, st)
-           : G == 64 ? w4_launch<64, EPI>(a, q, rows, after_own, st)
-                     : w4_launch<128, EPI>(a, q, rows, after_own, st);
+    return G == 32   ? w4_launch_n<32, EPI>(a, q, rows, after_own, st)
+           : G == 64 ? w4_launch_n<64, EPI>(a, q, rows, after_own, st)
+                     : w4_launch_n<128, EPI>(a, q, rows, after_own, st);
 }
 
 }  // namespace

@@ -247,3 +247,32 @@ def test_refusals():
     q3, s3 = _weights(32, 192, 64, 20)  # K not a multiple of 128
     with pytest.raises(B.MoeError):
         W4Linear(q3, s3, 64)(torch.zeros(1, 192, dtype=BF, device="cuda"))
+
+
+@pytest.mark.parametrize("M,N,K,G", [
+    (9, 8200, 1152, 32), (12, 16380, 7168, 32), (16, 4100, 2304, 64), (17, 4096, 4096, 128), (32, 3001, 3328, 128),
+    (10, 70000, 1024, 128), (16, 1100, 8064, 64), (13, 9000, 1408, 32), (40, 2049, 5120, 64),
+])
+def test_matvec_sixteen_rows_of_a_large_matrix(M, N, K, G):
+    q, sf = _weights(N, K, G, M + N)
+    x = torch.randn(M, K, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").to(BF)
+    lin = W4Linear(q, sf, G)
+    out = torch.full((M * N + 64,), 7.0, dtype=BF, device="cuda")
+    y = lin.forward(x, out=out[: M * N].view(M, N))
+    _check_product(x, q, sf, G, y)
+    assert torch.equal(y, lin(x)) and (out[M * N:] == 7.0).all()
+    x2 = x.clone()
+    x2[1, 3], x2[M - 1, K - 1] = float("nan"), float("inf")
+    y2 = lin(x2)
+    assert torch.equal(y2[2: M - 1], y[2: M - 1]) and torch.equal(y2[0], y[0]) and y2[[1, M - 1]].isnan().all()
+
+
+@pytest.mark.parametrize("T,H,I,G", [(9, 2048, 2816, 64), (16, 7168, 640, 128), (23, 4096, 2048, 32)])
+def test_shared_expert_of_many_rows(T, H, I, G):
+    W1, W2 = _weights(2 * I, H, G, 21, 1), _weights(H, I, G, 22, 1)
+    x = torch.randn(T, H, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)).to(BF)
+    ex = W4Experts(*W1, *W2, G)
+    y = ex(x)
+    want, tol = _experts_ref(x, W1, W2, G, torch.zeros(T, 1, dtype=torch.int32, device="cuda"),
+                             torch.ones(T, 1, device="cuda"))
+    assert ((y.double() - want).abs() <= tol).all() and torch.equal(y, ex(x))
