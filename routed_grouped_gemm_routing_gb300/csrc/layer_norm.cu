@@ -314,6 +314,14 @@ __device__ __forceinline__ void copy_some(uint32_t dst, const T* src, const T* e
     cp_async_16(dst, src, end - src >= V ? 16u : (uint32_t)((end - src) * (long long)sizeof(T)));
 }
 
+// Rows first, first + step, .. whose last vector, up to V - 1 elements past the
+// row, lies within the tensor.
+template <int V>
+__device__ __forceinline__ long long rows_inside(long long rows, long long stride, long long first, long long step) {
+    const long long last = rows - (V - 2 + stride) / stride;  // (rows - 1 - r) stride >= V - 1
+    return first < last ? (last - first + step - 1) / step : 0;
+}
+
 // Mean and rstd of a row from its threads' sums and their squared distances
 // from their own means (n values each): the sums give the mean m, and
 // sum (x - m)^2 = sum_t M2_t + sum_t n_t (mean_t - m)^2.  No difference of
@@ -325,7 +333,11 @@ struct LnStat {
 // gt working threads per group; groups of several warps have a reducing warp
 // after them (kReducer).
 // kShift: rows that start between 16-byte boundaries.  A group's rows are then a
-// multiple of 8 apart, so that they all start equally far past one.
+// multiple of 8 apart, so that they all start equally far past one: the groups'
+// threads take the whole vectors between the first boundary and the last, and
+// the few columns around them are the reducing (or the only) warp's, one a lane,
+// which has time for them (masked vectors at the ends held their warps up, and
+// so every row's barrier: 8192 x 7161 bf16 114 us, 48 us with the ends apart, 7168 43 us).
 template <typename T, typename W, int NV, bool kBias, bool kReducer, bool kShift>
 __global__ void __launch_bounds__(kLnRingThreads, 1)
     ln_fwd_ring(long long rows, int H, int gt, const T* __restrict__ x, long long xs, const W* __restrict__ w,
@@ -339,8 +351,24 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
     const int g = threadIdx.x / gn, t = threadIdx.x - g * gn, ng = blockDim.x / gn;
     const long long step = (long long)gridDim.x * ng;
     const long long first = (long long)blockIdx.x * ng + g;
-    const int m0 = kShift ? (int)((first * H) & (V - 1)) : 0;
-    const int nvec = (H + m0 + V - 1) / V;
+    // columns before the row's first 16-byte boundary, vectors, columns after the
+    // last; every lane of one warp has at most one column outside the vectors
+    int head = kShift ? (int)(-(first * H) & (V - 1)) : 0;
+    if (kShift && head > H) head = H;
+    const int nvec = (H - head) / V, tail = H - head - nvec * V;
+    const int el = threadIdx.x & 31;
+    const int ec = !kShift ? -1 : el < head ? el : el >= 16 && el - 16 < tail ? H - tail + el - 16 : -1;
+    const float ew = kShift && ec >= 0 ? to_f(__ldg(w + ec)) : 0.0f;
+    const float eb = kShift && kBias && ec >= 0 ? to_f(__ldg(b + ec)) : 0.0f;
+    auto edge = [&](long long i) {  // this lane's column of row i of the group
+        return kShift && ec >= 0 && first + i * step < rows ? x[(first + i * step) * xs + ec] : T(0.0f);
+    };
+    auto store_edge = [&](long long i, float v, float m, float r) {
+        if (kShift && ec >= 0) {
+            v = (v - m) * r;
+            y[(first + i * step) * H + ec] = from_f<T>(kBias ? fmaf(v, ew, eb) : v * ew);
+        }
+    };
     const float inv_h = 1.0f / (float)H;
     const long long n = first < rows ? (rows - first + step - 1) / step : 0;  // rows of this group
     if (kReducer && t >= gt) {
@@ -353,11 +381,13 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int v = lane + 32 * k + i * gt;
-                if (k < nw && v < nvec) c += kShift ? __popc(vec_mask<V>(v, m0, H)) : V;
+                if (k < nw && v < nvec) c += V;
             }
             cnt[k] = (float)c;
         }
+        T ex = T(0.0f);
         for (long long i = 0; i < n + kLag; ++i) {
+            const T next = edge(i);  // its vectors' copies are under way
             if (i >= 1 && i <= n) {
                 const float2* ps = psum[(i - 1) & 1] + g * gn;
                 float2 v[kLnGroupWarps];
@@ -368,8 +398,9 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
                         v[k] = ps[lane + 32 * k];
                         sum += v[k].x;
                     }
-                const float m = warp_sum(sum) * inv_h;
-                float q = 0.0f;
+                const float ef = kShift ? to_f(ex) : 0.0f;
+                const float m = warp_sum(kShift ? sum + ef : sum) * inv_h;
+                float q = kShift && ec >= 0 ? (ef - m) * (ef - m) : 0.0f;
 #pragma unroll
                 for (int k = 0; k < kLnGroupWarps; ++k)
                     if (k < nw && cnt[k] > 0.0f) {
@@ -382,7 +413,9 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
                     mean[first + (i - 1) * step] = m;
                     rstd[first + (i - 1) * step] = r;
                 }
+                store_edge(i - 1, ef, m, r);
             }
+            ex = next;
             group_sync(g, gn);
         }
         return;
@@ -390,30 +423,22 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
     const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16u;
     const uint32_t vstride = blockDim.x * 16u;
     bool have[NV];
-    uint32_t cols[kShift ? NV : 1];  // the columns that exist of each vector
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         have[i] = t + i * gt < nvec;
-        if constexpr (kShift) cols[i] = have[i] ? vec_mask<V>(t + i * gt, m0, H) : 0u;
-        mine += kShift ? __popc(cols[kShift ? i : 0]) : have[i] ? V : 0;
+        mine += have[i] ? V : 0;
     }
     const float inv_mine = mine ? 1.0f / (float)mine : 0.0f;
     // the next row to copy: its number and this thread's first element of it
     long long frow = 0;
-    const T* fx = x + first * xs - m0 + (size_t)t * V;
-    const T* end = x + (rows - 1) * xs + H;
+    const T* fx = x + first * xs + head + (size_t)t * V;
     auto fetch = [&](int s) {
         if (frow < n) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (have[i]) {
-                    const uint32_t dst = slot0 + (uint32_t)(s * NV + i) * vstride;
-                    if constexpr (kShift)
-                        copy_some<T>(dst, fx + (size_t)(i * gt) * V, end);
-                    else
-                        cp_async_16(dst, fx + (size_t)(i * gt) * V, 16u);
-                }
+                if (have[i])
+                    cp_async_16(slot0 + (uint32_t)(s * NV + i) * vstride, fx + (size_t)(i * gt) * V, 16u);
         }
         cp_async_commit();
         ++frow;
@@ -427,16 +452,16 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (have[i]) {
-            const int c0 = (t + i * gt) * V - m0;
+            const int c0 = (t + i * gt) * V + head;
             if constexpr (kShift) {
-                load_some<W, P>(w + c0, cols[i], wv[i]);
-                if constexpr (kBias) load_some<W, P>(b + c0, cols[i], bv[i]);
+                load_some<W, P>(w + c0, (1u << V) - 1u, wv[i]);
+                if constexpr (kBias) load_some<W, P>(b + c0, (1u << V) - 1u, bv[i]);
             } else {
                 load_pairs<W, P>(w + c0, wv[i]);
                 if constexpr (kBias) load_pairs<W, P>(b + c0, bv[i]);
             }
         }
-    T* yr = y + first * H - m0 + (size_t)t * V;
+    T* yr = y + first * H + head + (size_t)t * V;
     // (x - m) r w + b of the row in slot s
     auto output = [&](int s, float m, float r) {
         const f2 nm = f2_make(-m, -m), r2 = f2_make(r, r);
@@ -453,29 +478,30 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
                     else
                         v[j] = f2_mul(v[j], wv[i][j]);
                 }
-                if constexpr (kShift)
-                    store_some<T, P>(yr + (size_t)(i * gt) * V, v, cols[i]);
-                else
-                    *reinterpret_cast<uint4*>(yr + (size_t)(i * gt) * V) = pack_vec<T, P>(v);
+                *reinterpret_cast<uint4*>(yr + (size_t)(i * gt) * V) = pack_vec<T, P>(v);
             }
         yr += step * H;
     };
+    constexpr bool kEdge = kShift && !kReducer;
+    T ex = kEdge ? edge(0) : T(0.0f);
     int s = 0;  // slot of row i
     for (long long i = 0; i < n + kLag; ++i) {
         cp_async_wait_group<kAhead - 1>();
         float sum = 0.0f, m2 = 0.0f;
         if (i < n) {
+            const float ef = kEdge ? to_f(ex) : 0.0f;
+            if constexpr (kEdge) ex = edge(i + 1);
             f2 v[NV][P];
             f2 acc[2] = {0ull, 0ull};  // (+0, +0)
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 if (have[k]) {
                     unpack_vec<T, P>(ring[(s * NV + k) * blockDim.x + threadIdx.x], v[k]);
-                    if constexpr (kShift) keep<P>(v[k], cols[k]);
 #pragma unroll
                     for (int j = 0; j < P; ++j) acc[j & 1] = f2_add(acc[j & 1], v[k][j]);
                 }
             sum = f2_sum(f2_add(acc[0], acc[1]));
+            if constexpr (kEdge) sum += ef;
             // around the thread's own mean, or (one warp) the row's
             const float c = kReducer ? sum * inv_mine : warp_sum(sum) * inv_h;
             const f2 nc = f2_make(-c, -c);
@@ -485,11 +511,11 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
                 if (have[k]) {
 #pragma unroll
                     for (int j = 0; j < P; ++j) v[k][j] = f2_add(v[k][j], nc);
-                    if constexpr (kShift) keep<P>(v[k], cols[k]);
 #pragma unroll
                     for (int j = 0; j < P; ++j) acc[j & 1] = f2_fma(v[k][j], v[k][j], acc[j & 1]);
                 }
             m2 = f2_sum(f2_add(acc[0], acc[1]));
+            if (kEdge && ec >= 0) m2 = fmaf(ef - c, ef - c, m2);
             if constexpr (kReducer) {
                 psum[i & 1][threadIdx.x] = make_float2(sum, m2);
             } else {
@@ -498,6 +524,7 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
                     mean[first + i * step] = c;
                     rstd[first + i * step] = r;
                 }
+                store_edge(i, ef, c, r);
                 output(s, c, r);
             }
         }
@@ -597,9 +624,10 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
     bool have[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) have[i] = worker && t + i * gt < nvec;
-    uint32_t cols[kShift ? NV : 1];  // the columns that exist of each vector
+    auto cols = [&](int i) { return vec_mask<V>(t + i * gt, s0, H); };  // the columns that exist of vector i
+    bool edge = false;  // this thread has a vector with fewer
 #pragma unroll
-    for (int i = 0; i < (kShift ? NV : 0); ++i) cols[i] = have[i] ? vec_mask<V>(t + i * gt, s0, H) : 0u;
+    for (int i = 0; i < (kShift ? NV : 0); ++i) edge |= have[i] && cols(i) != (1u << V) - 1u;
     f2 sw[NV][P], sb[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -633,19 +661,22 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
         const T* fd = static_cast<const T*>(p.dy) + first * p.dys - s0 + (size_t)t * V;
         const T* endx = static_cast<const T*>(p.x) + (p.rows - 1) * p.xs + H;
         const T* endd = static_cast<const T*>(p.dy) + (p.rows - 1) * p.dys + H;
+        const long long inner = kShift ? rows_inside<V>(p.rows, p.xs < p.dys ? p.xs : p.dys, first, step) : n;
         auto fetch = [&](int s) {
-            if (frow < n) {
+            const uint32_t dst = slot0 + (uint32_t)(s * 2 * NV) * vstride;
+            if (frow < inner) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (have[i]) {
-                        const uint32_t dst = slot0 + (uint32_t)(s * 2 * NV + i) * vstride;
-                        if constexpr (kShift) {
-                            copy_some<T>(dst, fx + (size_t)(i * gt) * V, endx);
-                            copy_some<T>(dst + NV * vstride, fd + (size_t)(i * gt) * V, endd);
-                        } else {
-                            cp_async_16(dst, fx + (size_t)(i * gt) * V, 16u);
-                            cp_async_16(dst + NV * vstride, fd + (size_t)(i * gt) * V, 16u);
-                        }
+                        cp_async_16(dst + i * vstride, fx + (size_t)(i * gt) * V, 16u);
+                        cp_async_16(dst + (NV + i) * vstride, fd + (size_t)(i * gt) * V, 16u);
+                    }
+            } else if (kShift && frow < n) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (have[i]) {
+                        copy_some<T>(dst + i * vstride, fx + (size_t)(i * gt) * V, endx);
+                        copy_some<T>(dst + (NV + i) * vstride, fd + (size_t)(i * gt) * V, endd);
                     }
             }
             cp_async_commit();
@@ -659,7 +690,7 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
         f2 wv[kHoldW ? NV : 1][P];
         auto load_w = [&](int i, f2 (&v)[P]) {
             if constexpr (kShift)
-                load_some<W, P>(w + i * gt * V, cols[i], v);
+                load_some<W, P>(w + i * gt * V, cols(i), v);
             else
                 load_pairs<W, P>(w + i * gt * V, v);
         };
@@ -676,10 +707,6 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
             if constexpr (!kHoldW) load_w(i, wv[0]);
 #pragma unroll
             for (int j = 0; j < P; ++j) z[j] = f2_mul(f2_add(z[j], nm), r2);
-            if constexpr (kShift) {  // the neighbouring rows' values may be anything
-                keep<P>(z, cols[i]);
-                keep<P>(d, cols[i]);
-            }
         };
         // dx of the row in slot s; c1, c2: minus the means of g and of g z
         auto output = [&](int s, float m, float r, float c1, float c2) {
@@ -692,8 +719,8 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
 #pragma unroll
                     for (int j = 0; j < P; ++j)
                         d[j] = f2_mul(f2_fma(z[j], d2, f2_fma(d[j], wv[kHoldW ? i : 0][j], d1)), r2);
-                    if constexpr (kShift)
-                        store_some<T, P>(out + (size_t)(i * gt) * V, d, cols[i]);
+                    if (kShift && edge)
+                        store_some<T, P>(out + (size_t)(i * gt) * V, d, cols(i));
                     else
                         *reinterpret_cast<uint4*>(out + (size_t)(i * gt) * V) = pack_vec<T, P>(d);
                 }
@@ -714,6 +741,10 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
                     if (have[k]) {
                         f2 z[P], d[P];
                         vectors(s, k, nm, r2, z, d);
+                        if (kShift && edge) {  // the neighbouring rows' values may be anything
+                            keep<P>(z, cols(k));
+                            keep<P>(d, cols(k));
+                        }
 #pragma unroll
                         for (int j = 0; j < P; ++j) {
                             sb[k][j] = f2_add(sb[k][j], d[j]);
@@ -765,8 +796,8 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
                 const int h = (t + i * gt) * V - s0 + 2 * j;
                 const float2 a = f2_get(sw[i][j]), b = f2_get(sb[i][j]);
                 if constexpr (kShift) {
-                    if (cols[i] >> (2 * j) & 1u) to[h] = a.x, to[H + h] = b.x;
-                    if (cols[i] >> (2 * j + 1) & 1u) to[h + 1] = a.y, to[H + h + 1] = b.y;
+                    if (cols(i) >> (2 * j) & 1u) to[h] = a.x, to[H + h] = b.x;
+                    if (cols(i) >> (2 * j + 1) & 1u) to[h + 1] = a.y, to[H + h + 1] = b.y;
                 } else {
                     *reinterpret_cast<float2*>(to + h) = a;
                     *reinterpret_cast<float2*>(to + H + h) = b;
@@ -973,12 +1004,15 @@ int ring_blocks(long long need, bool shift) {
     if (need > 152) need = 152;
     return (int)(shift ? (need + 7) / 8 * 8 : need);
 }
-LnForm ln_form(int H, int elt, bool vec, int max_threads, int wide_nv, int max_ring) {
+// whole: the ring form's vectors are whole ones (forward), the columns around
+// them apart; else they cover the row with its ends masked (backward).
+LnForm ln_form(int H, int elt, bool vec, int max_threads, int wide_nv, int max_ring, bool whole) {
     LnForm f = {};
     if (vec) {
         const int V = 16 / elt;
         f.shift = H % V != 0;
-        const int nvec = (H + V - 1) / V + (f.shift ? 1 : 0);  // at most
+        const int odd = H & -H;  // rows start up to V - odd elements past a boundary
+        const int nvec = whole ? (H >= V ? H / V : 1) : (H + (f.shift ? V - odd : 0) + V - 1) / V;
         f.form = LN_RING;
         f.nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : nvec <= 2 * (kLnRingThreads - 32) ? wide_nv : 4;
         f.threads = ((nvec + f.nv - 1) / f.nv + 31) / 32 * 32;
@@ -1060,8 +1094,8 @@ int fwd_t(const LnFwdArgs& a, cudaStream_t st) {
     const bool ring = ring_rows(a.x, a.x_stride, a.H, sizeof(T)) && ring_rows(a.y, a.H, a.H, sizeof(T)) &&
                       (a.H % V || (mult16(a.weight) && mult16(a.bias)));
     const bool vec = ring && a.H % V == 0;
-    LnForm f = ln_form(a.H, sizeof(T), ring, 1024, 4, kLnRingThreads - 32);
-    if (!ring_pays(f, f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 1024, 4, 0);
+    LnForm f = ln_form(a.H, sizeof(T), ring, 1024, 4, kLnRingThreads - 32, true);
+    if (!ring_pays(f, f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 1024, 4, 0, true);
     const bool b = a.bias != nullptr;
     switch (f.form) {
         case LN_RING:
@@ -1121,8 +1155,8 @@ int bwd_t(const LnBwdArgs& a, cudaStream_t st) {
                       ring_rows(a.dx, a.H, a.H, sizeof(T)) && (a.H % V || mult16(a.weight));
     const bool vec = ring && a.H % V == 0;
     const LnBwd p = {a.rows, a.H, a.dy, a.x, a.weight, a.dy_stride, a.x_stride, a.mean, a.rstd, a.dx, a.part};
-    LnForm f = ln_form(a.H, sizeof(T), ring, 512, 2, kLnRingThreads);
-    if (!ring_pays(f, f.nv == 2 && f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 512, 2, 0);
+    LnForm f = ln_form(a.H, sizeof(T), ring, 512, 2, kLnRingThreads, false);
+    if (!ring_pays(f, f.nv == 2 && f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 512, 2, 0, false);
     int e, blocks = 0;
     switch (f.form) {
         case LN_RING:
