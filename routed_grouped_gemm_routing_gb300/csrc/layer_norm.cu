@@ -32,7 +32,7 @@
 //    then one barrier.  A group of one warp reduces by shuffles.
 //    Widths that are no multiple of 16 bytes: rows start anywhere in a vector,
 //    but a group's rows are a multiple of 8 apart and so start equally far into
-//    one; the ends are masked and stored by element (kShift).
+//    one; the columns around the whole vectors go to one warp's lanes (kShift).
 //  * register: other addresses and strides, and few rows of such widths, one
 //    element at a time; one warp per row up to 128 elements, one block above.
 //  * long: rows too long for the others are read again for every pass (the
@@ -264,62 +264,11 @@ __device__ __forceinline__ void load_pairs(const W* p, f2 (&f)[P]) {
     for (int i = 0; i < P; ++i) f[i] = f2_make(v[2 * i], v[2 * i + 1]);
 }
 
-// Vector c of a row whose first element lies m elements past a 16-byte boundary
-// holds columns c V - m .. + V - 1; bit j of the mask: column j of it exists.
-template <int V>
-__device__ __forceinline__ uint32_t vec_mask(int c, int m, int H) {
-    const int c0 = c * V - m;
-    uint32_t e = (1u << V) - 1u;
-    if (c0 < 0) e &= e << (-c0 < V ? -c0 : V);
-    if (c0 + V > H) e &= H > c0 ? (1u << (H - c0)) - 1u : 0u;
-    return e;
-}
-// Zero in the columns that do not exist.
-template <int P>
-__device__ __forceinline__ void keep(f2 (&v)[P], uint32_t e) {
-    if (e != (1u << (2 * P)) - 1u) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const float2 f = f2_get(v[j]);
-            v[j] = f2_make(e >> (2 * j) & 1u ? f.x : 0.0f, e >> (2 * j + 1) & 1u ? f.y : 0.0f);
-        }
-    }
-}
-// The columns that exist of 2 P weights from p on.
+// 2 P weights from anywhere, one by one.
 template <typename W, int P>
-__device__ __forceinline__ void load_some(const W* p, uint32_t e, f2 (&f)[P]) {
-    float v[2 * P];
+__device__ __forceinline__ void load_each(const W* p, f2 (&f)[P]) {
 #pragma unroll
-    for (int j = 0; j < 2 * P; ++j) v[j] = e >> j & 1u ? to_f(__ldg(p + j)) : 0.0f;
-#pragma unroll
-    for (int j = 0; j < P; ++j) f[j] = f2_make(v[2 * j], v[2 * j + 1]);
-}
-template <typename T, int P>
-__device__ __forceinline__ void store_some(T* p, const f2 (&v)[P], uint32_t e) {
-    if (e == (1u << (2 * P)) - 1u) {
-        *reinterpret_cast<uint4*>(p) = pack_vec<T, P>(v);
-    } else {  // the row's ends: their other columns are its neighbours'
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const float2 f = f2_get(v[j]);
-            if (e >> (2 * j) & 1u) p[2 * j] = from_f<T>(f.x);
-            if (e >> (2 * j + 1) & 1u) p[2 * j + 1] = from_f<T>(f.y);
-        }
-    }
-}
-// Copies a vector whose end may pass the tensor's: nothing past `end` is read.
-template <typename T>
-__device__ __forceinline__ void copy_some(uint32_t dst, const T* src, const T* end) {
-    constexpr int V = 16 / sizeof(T);
-    cp_async_16(dst, src, end - src >= V ? 16u : (uint32_t)((end - src) * (long long)sizeof(T)));
-}
-
-// Rows first, first + step, .. whose last vector, up to V - 1 elements past the
-// row, lies within the tensor.
-template <int V>
-__device__ __forceinline__ long long rows_inside(long long rows, long long stride, long long first, long long step) {
-    const long long last = rows - (V - 2 + stride) / stride;  // (rows - 1 - r) stride >= V - 1
-    return first < last ? (last - first + step - 1) / step : 0;
+    for (int j = 0; j < P; ++j) f[j] = f2_make(to_f(__ldg(p + 2 * j)), to_f(__ldg(p + 2 * j + 1)));
 }
 
 // Mean and rstd of a row from its threads' sums and their squared distances
@@ -454,8 +403,8 @@ __global__ void __launch_bounds__(kLnRingThreads, 1)
         if (have[i]) {
             const int c0 = (t + i * gt) * V + head;
             if constexpr (kShift) {
-                load_some<W, P>(w + c0, (1u << V) - 1u, wv[i]);
-                if constexpr (kBias) load_some<W, P>(b + c0, (1u << V) - 1u, bv[i]);
+                load_each<W, P>(w + c0, wv[i]);
+                if constexpr (kBias) load_each<W, P>(b + c0, bv[i]);
             } else {
                 load_pairs<W, P>(w + c0, wv[i]);
                 if constexpr (kBias) load_pairs<W, P>(b + c0, bv[i]);
@@ -615,8 +564,9 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
     const int H = p.H;
     const long long step = (long long)gridDim.x * ng;
     const long long first = (long long)blockIdx.x * ng + g;
-    const int s0 = kShift ? (int)((first * H) & (V - 1)) : 0;  // elements of a row's first vector before the row
-    const int nvec = (H + s0 + V - 1) / V;
+    int head = kShift ? (int)(-(first * H) & (V - 1)) : 0;  // as in the forward
+    if (kShift && head > H) head = H;
+    const int nvec = (H - head) / V, tail = H - head - nvec * V;
     const long long n = first < p.rows ? (p.rows - first + step - 1) / step : 0;  // rows of this group
     const float inv_h = 1.0f / (float)H;
     const bool worker = !kReducer || t < gt;
@@ -624,10 +574,20 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
     bool have[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) have[i] = worker && t + i * gt < nvec;
-    auto cols = [&](int i) { return vec_mask<V>(t + i * gt, s0, H); };  // the columns that exist of vector i
-    bool edge = false;  // this thread has a vector with fewer
-#pragma unroll
-    for (int i = 0; i < (kShift ? NV : 0); ++i) edge |= have[i] && cols(i) != (1u << V) - 1u;
+    // the reducing (or the group's first) warp's lanes: a column outside the vectors
+    const int el = threadIdx.x & 31;
+    const int ec = !kShift || (kReducer ? worker : t >= 32)        ? -1
+                   : el < head                                       ? el
+                   : el >= 16 && el - 16 < tail ? H - tail + el - 16 : -1;
+    const float ew = kShift && ec >= 0 ? to_f(__ldg(static_cast<const W*>(p.w) + ec)) : 0.0f;
+    float esw = 0.0f, esb = 0.0f;
+    auto edge = [&](const void* v, long long stride, long long i) {  // that column of row i of the group
+        return kShift && ec >= 0 && i < n ? static_cast<const T*>(v)[(first + i * step) * stride + ec] : T(0.0f);
+    };
+    auto store_edge = [&](long long i, float z, float d, float r, float c1, float c2) {
+        if (kShift && ec >= 0)
+            static_cast<T*>(p.dx)[(first + i * step) * H + ec] = from_f<T>(fmaf(z, c2, fmaf(d, ew, c1)) * r);
+    };
     f2 sw[NV][P], sb[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -635,10 +595,19 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
         for (int j = 0; j < P; ++j) sw[i][j] = sb[i][j] = 0ull;  // (+0, +0)
     if (!worker) {
         const int lane = t - gt, nw = gt >> 5;
+        T ex = T(0.0f), ed = T(0.0f);
+        float em = 0.0f, er = 0.0f;  // of row i - 1
         for (long long i = 0; i < n + kLag; ++i) {
+            const T nx = edge(p.x, p.xs, i), nd = edge(p.dy, p.dys, i);  // their vectors' copies are under way
+            const bool load = kShift && ec >= 0 && i < n;
+            const float nmean = load ? __ldg(p.mean + first + i * step) : 0.0f;
+            const float nrstd = load ? __ldg(p.rstd + first + i * step) : 0.0f;
             if (i >= 1 && i <= n) {
                 const float2* ps = psum[(i - 1) & 1] + g * gn;
-                float a = 0.0f, c = 0.0f;
+                const float ez = kShift ? (to_f(ex) - em) * er : 0.0f, ef = kShift ? to_f(ed) : 0.0f;
+                float a = ef * ew, c = a * ez;
+                esb += ef;
+                esw = fmaf(ef, ez, esw);
 #pragma unroll
                 for (int k = 0; k < kLnGroupWarps; ++k)
                     if (k < nw) {
@@ -649,34 +618,26 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
                 a = warp_sum(a);
                 c = warp_sum(c);
                 if (lane == 0) tot[g][(i - 1) & 1] = make_float2(-a * inv_h, -c * inv_h);
+                store_edge(i - 1, ez, ef, er, -a * inv_h, -c * inv_h);
             }
+            ex = nx, ed = nd, em = nmean, er = nrstd;
             group_sync(g, gn);
         }
     } else {
         const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16u;
         const uint32_t vstride = blockDim.x * 16u;
-        const W* w = static_cast<const W*>(p.w) + (t * V - s0);
+        const W* w = static_cast<const W*>(p.w) + (t * V + head);
         long long frow = 0;
-        const T* fx = static_cast<const T*>(p.x) + first * p.xs - s0 + (size_t)t * V;
-        const T* fd = static_cast<const T*>(p.dy) + first * p.dys - s0 + (size_t)t * V;
-        const T* endx = static_cast<const T*>(p.x) + (p.rows - 1) * p.xs + H;
-        const T* endd = static_cast<const T*>(p.dy) + (p.rows - 1) * p.dys + H;
-        const long long inner = kShift ? rows_inside<V>(p.rows, p.xs < p.dys ? p.xs : p.dys, first, step) : n;
+        const T* fx = static_cast<const T*>(p.x) + first * p.xs + head + (size_t)t * V;
+        const T* fd = static_cast<const T*>(p.dy) + first * p.dys + head + (size_t)t * V;
         auto fetch = [&](int s) {
-            const uint32_t dst = slot0 + (uint32_t)(s * 2 * NV) * vstride;
-            if (frow < inner) {
+            if (frow < n) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (have[i]) {
-                        cp_async_16(dst + i * vstride, fx + (size_t)(i * gt) * V, 16u);
-                        cp_async_16(dst + (NV + i) * vstride, fd + (size_t)(i * gt) * V, 16u);
-                    }
-            } else if (kShift && frow < n) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (have[i]) {
-                        copy_some<T>(dst + i * vstride, fx + (size_t)(i * gt) * V, endx);
-                        copy_some<T>(dst + (NV + i) * vstride, fd + (size_t)(i * gt) * V, endd);
+                        const uint32_t dst = slot0 + (uint32_t)(s * 2 * NV + i) * vstride;
+                        cp_async_16(dst, fx + (size_t)(i * gt) * V, 16u);
+                        cp_async_16(dst + NV * vstride, fd + (size_t)(i * gt) * V, 16u);
                     }
             }
             cp_async_commit();
@@ -690,7 +651,7 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
         f2 wv[kHoldW ? NV : 1][P];
         auto load_w = [&](int i, f2 (&v)[P]) {
             if constexpr (kShift)
-                load_some<W, P>(w + i * gt * V, cols(i), v);
+                load_each<W, P>(w + i * gt * V, v);
             else
                 load_pairs<W, P>(w + i * gt * V, v);
         };
@@ -699,7 +660,7 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
             for (int i = 0; i < NV; ++i)
                 if (have[i]) load_w(i, wv[i]);
         }
-        T* out = static_cast<T*>(p.dx) + first * H - s0 + (size_t)t * V;
+        T* out = static_cast<T*>(p.dx) + first * H + head + (size_t)t * V;
         // z and dy of vector i of the row in slot s (and the weight, where it is not held)
         auto vectors = [&](int s, int i, f2 nm, f2 r2, f2 (&z)[P], f2 (&d)[P]) {
             unpack_vec<T, P>(ring[(s * 2 * NV + i) * blockDim.x + threadIdx.x], z);
@@ -719,16 +680,15 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
 #pragma unroll
                     for (int j = 0; j < P; ++j)
                         d[j] = f2_mul(f2_fma(z[j], d2, f2_fma(d[j], wv[kHoldW ? i : 0][j], d1)), r2);
-                    if (kShift && edge)
-                        store_some<T, P>(out + (size_t)(i * gt) * V, d, cols(i));
-                    else
-                        *reinterpret_cast<uint4*>(out + (size_t)(i * gt) * V) = pack_vec<T, P>(d);
+                    *reinterpret_cast<uint4*>(out + (size_t)(i * gt) * V) = pack_vec<T, P>(d);
                 }
             out += step * H;
         };
         // mean and rstd of rows i - 2 .. i + 1 (read a step ahead)
         float m0 = 0.0f, r0 = 0.0f, m1 = 0.0f, r1 = 0.0f, m = 0.0f, r = 0.0f, ma = 0.0f, ra = 0.0f;
         if (n > 0) m = __ldg(p.mean + first), r = __ldg(p.rstd + first);
+        constexpr bool kEdge = kShift && !kReducer;
+        T ex = kEdge ? edge(p.x, p.xs, 0) : T(0.0f), ed = kEdge ? edge(p.dy, p.dys, 0) : T(0.0f);
         int s = 0;  // slot of row i
         for (long long i = 0; i < n + kLag; ++i) {
             if (i + 1 < n) ma = __ldg(p.mean + first + (i + 1) * step), ra = __ldg(p.rstd + first + (i + 1) * step);
@@ -741,10 +701,6 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
                     if (have[k]) {
                         f2 z[P], d[P];
                         vectors(s, k, nm, r2, z, d);
-                        if (kShift && edge) {  // the neighbouring rows' values may be anything
-                            keep<P>(z, cols(k));
-                            keep<P>(d, cols(k));
-                        }
 #pragma unroll
                         for (int j = 0; j < P; ++j) {
                             sb[k][j] = f2_add(sb[k][j], d[j]);
@@ -757,7 +713,19 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
                 if constexpr (kReducer) {
                     psum[i & 1][threadIdx.x] = make_float2(f2_sum(a1), f2_sum(a2));
                 } else {
-                    float c1 = warp_sum(f2_sum(a1)), c2 = warp_sum(f2_sum(a2));
+                    float p1 = f2_sum(a1), p2 = f2_sum(a2), ez = 0.0f, ef = 0.0f;
+                    if constexpr (kEdge) {
+                        ez = (to_f(ex) - m) * r;
+                        ef = to_f(ed);
+                        ex = edge(p.x, p.xs, i + 1);
+                        ed = edge(p.dy, p.dys, i + 1);
+                        if (ec < 0) ez = 0.0f;
+                        esb += ef;
+                        esw = fmaf(ef, ez, esw);
+                        p1 = fmaf(ef, ew, p1);
+                        p2 = fmaf(ef * ew, ez, p2);
+                    }
+                    float c1 = warp_sum(p1), c2 = warp_sum(p2);
                     if constexpr (kMode == LN_ALL_WARPS) {
                         // two buffers in turn: row i + 2 reuses this one, after row i + 1's barrier
                         const int lane = t & 31;
@@ -767,6 +735,7 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
                         c1 = warp_sum(v.x);
                         c2 = warp_sum(v.y);
                     }
+                    store_edge(i, ez, ef, r, -c1 * inv_h, -c2 * inv_h);
                     output(s, m, r, -c1 * inv_h, -c2 * inv_h);
                 }
             }
@@ -793,17 +762,18 @@ __global__ void __launch_bounds__(kLnRingThreads, 1) ln_bwd_ring(const LnBwd p, 
         if (have[i]) {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const int h = (t + i * gt) * V - s0 + 2 * j;
+                const int h = (t + i * gt) * V + head + 2 * j;
                 const float2 a = f2_get(sw[i][j]), b = f2_get(sb[i][j]);
                 if constexpr (kShift) {
-                    if (cols(i) >> (2 * j) & 1u) to[h] = a.x, to[H + h] = b.x;
-                    if (cols(i) >> (2 * j + 1) & 1u) to[h + 1] = a.y, to[H + h + 1] = b.y;
+                    to[h] = a.x, to[H + h] = b.x;
+                    to[h + 1] = a.y, to[H + h + 1] = b.y;
                 } else {
                     *reinterpret_cast<float2*>(to + h) = a;
                     *reinterpret_cast<float2*>(to + H + h) = b;
                 }
             }
         }
+    if (kShift && ec >= 0) to[ec] = esw, to[H + ec] = esb;
     if (ng > 1) {
         __syncthreads();
         for (int h = threadIdx.x; h < 2 * H; h += blockDim.x) {
@@ -1004,15 +974,12 @@ int ring_blocks(long long need, bool shift) {
     if (need > 152) need = 152;
     return (int)(shift ? (need + 7) / 8 * 8 : need);
 }
-// whole: the ring form's vectors are whole ones (forward), the columns around
-// them apart; else they cover the row with its ends masked (backward).
-LnForm ln_form(int H, int elt, bool vec, int max_threads, int wide_nv, int max_ring, bool whole) {
+LnForm ln_form(int H, int elt, bool vec, int max_threads, int wide_nv, int max_ring) {
     LnForm f = {};
     if (vec) {
         const int V = 16 / elt;
         f.shift = H % V != 0;
-        const int odd = H & -H;  // rows start up to V - odd elements past a boundary
-        const int nvec = whole ? (H >= V ? H / V : 1) : (H + (f.shift ? V - odd : 0) + V - 1) / V;
+        const int nvec = H >= V ? H / V : 1;  // whole ones, at most
         f.form = LN_RING;
         f.nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : nvec <= 2 * (kLnRingThreads - 32) ? wide_nv : 4;
         f.threads = ((nvec + f.nv - 1) / f.nv + 31) / 32 * 32;
@@ -1094,8 +1061,8 @@ int fwd_t(const LnFwdArgs& a, cudaStream_t st) {
     const bool ring = ring_rows(a.x, a.x_stride, a.H, sizeof(T)) && ring_rows(a.y, a.H, a.H, sizeof(T)) &&
                       (a.H % V || (mult16(a.weight) && mult16(a.bias)));
     const bool vec = ring && a.H % V == 0;
-    LnForm f = ln_form(a.H, sizeof(T), ring, 1024, 4, kLnRingThreads - 32, true);
-    if (!ring_pays(f, f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 1024, 4, 0, true);
+    LnForm f = ln_form(a.H, sizeof(T), ring, 1024, 4, kLnRingThreads - 32);
+    if (!ring_pays(f, f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 1024, 4, 0);
     const bool b = a.bias != nullptr;
     switch (f.form) {
         case LN_RING:
@@ -1155,8 +1122,8 @@ int bwd_t(const LnBwdArgs& a, cudaStream_t st) {
                       ring_rows(a.dx, a.H, a.H, sizeof(T)) && (a.H % V || mult16(a.weight));
     const bool vec = ring && a.H % V == 0;
     const LnBwd p = {a.rows, a.H, a.dy, a.x, a.weight, a.dy_stride, a.x_stride, a.mean, a.rstd, a.dx, a.part};
-    LnForm f = ln_form(a.H, sizeof(T), ring, 512, 2, kLnRingThreads, false);
-    if (!ring_pays(f, f.nv == 2 && f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 512, 2, 0, false);
+    LnForm f = ln_form(a.H, sizeof(T), ring, 512, 2, kLnRingThreads);
+    if (!ring_pays(f, f.nv == 2 && f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 512, 2, 0);
     int e, blocks = 0;
     switch (f.form) {
         case LN_RING:
