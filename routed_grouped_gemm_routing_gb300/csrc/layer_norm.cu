@@ -10,7 +10,7 @@
 // row's, or the thread's own and joined exactly), never as E[x^2] - m^2.
 // Bound by DRAM: the forward reads x and writes y, the backward reads x and
 // dy and writes dx.  Measured at 8192 x 7168: FP32 6.1 (forward) and 6.4 TB/s
-// (backward), bf16 5.4 and 5.0 TB/s (43.3 and 70.4 us; half the bytes for the
+// (backward), bf16 5.4 and 5.0 TB/s (43.3 and 70.0 us; half the bytes for the
 // same arithmetic leaves the instructions, not DRAM, as the bound), of 6.8 TB/s
 // for a plain copy.
 //
@@ -1012,12 +1012,14 @@ int ln_groups(int gt, bool reducer, int* threads) {
     *threads = ng * gn;
     return ng;
 }
-// Shifted rows load their weights one by one: a group that takes fewer than
-// three rows does not earn that back (777 x 1001 f16 forward: 8.8 us, 3.3 us in
-// the register form; 8192 x 1001 backward 24.9 us, 37.8 us).
-bool ring_pays(const LnForm& f, bool reducer, long long rows) {
+// Shifted rows load their weights one by one: a group that takes few rows does
+// not earn that back.  us, ring | register form, at rows per group: forward,
+// groups of several warps 1.6: 7.4 | 10.0 (500 x 5001 bf16), 1.0: 8.4 | 6.8 (300
+// x 7161); of one warp 1.6: 5.4 | 4.9 (4000 x 333), 1.2: 9.5 | 7.5 (3000 x 777);
+// backward 1.6: 10.6 | 15.1 (4000 x 333), 1.0: 9.8 | 7.2 (777 x 1001).
+bool ring_pays(const LnForm& f, bool reducer, long long rows, int half_rows) {
     int threads;
-    return f.form != LN_RING || !f.shift || rows >= 3ll * 152 * ln_groups(f.threads, reducer, &threads);
+    return f.form != LN_RING || !f.shift || 2 * rows >= half_rows * 152ll * ln_groups(f.threads, reducer, &threads);
 }
 template <typename T, typename W, int NV, bool kBias, bool kReducer, bool kShift>
 int run_fwd_ring(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
@@ -1062,7 +1064,7 @@ int fwd_t(const LnFwdArgs& a, cudaStream_t st) {
                       (a.H % V || (mult16(a.weight) && mult16(a.bias)));
     const bool vec = ring && a.H % V == 0;
     LnForm f = ln_form(a.H, sizeof(T), ring, 1024, 4, kLnRingThreads - 32);
-    if (!ring_pays(f, f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 1024, 4, 0);
+    if (!ring_pays(f, f.threads > 32, a.rows, f.threads > 32 ? 3 : 6)) f = ln_form(a.H, sizeof(T), false, 1024, 4, 0);
     const bool b = a.bias != nullptr;
     switch (f.form) {
         case LN_RING:
@@ -1123,7 +1125,7 @@ int bwd_t(const LnBwdArgs& a, cudaStream_t st) {
     const bool vec = ring && a.H % V == 0;
     const LnBwd p = {a.rows, a.H, a.dy, a.x, a.weight, a.dy_stride, a.x_stride, a.mean, a.rstd, a.dx, a.part};
     LnForm f = ln_form(a.H, sizeof(T), ring, 512, 2, kLnRingThreads);
-    if (!ring_pays(f, f.nv == 2 && f.threads > 32, a.rows)) f = ln_form(a.H, sizeof(T), false, 512, 2, 0);
+    if (!ring_pays(f, f.nv == 2 && f.threads > 32, a.rows, 3)) f = ln_form(a.H, sizeof(T), false, 512, 2, 0);
     int e, blocks = 0;
     switch (f.form) {
         case LN_RING:
