@@ -45,7 +45,7 @@
 // (4096 x 2048 x 1408: 164 us a step, 186 in three launches; 777 x 1160 x 712:
 // 44 and 56 us).
 //
-// The forward of up to 16 tokens is ffn_few.cu's.
+// The forward of few tokens (ffn_few_takes) is ffn_few.cu's.
 //
 // Roles (10 warps per CTA): 0-7 epilogue (warp w: TMEM lanes 32 (w % 4) .. of
 // the CTA's 128 rows, every other group of columns from w / 4 on; with four

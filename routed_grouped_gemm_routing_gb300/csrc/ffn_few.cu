@@ -16,7 +16,7 @@
 // Measured, 8 tokens (the 256-row tiles of the large form; the weights' bytes at
 // the copy rate): 7168 x 2048 20.0 us (32.1; 13.0), 2048 x 1408 8.9 us (20.1;
 // 2.6), 7168 x 18432 127 us (165; 117), and 16 tokens 21.7, 10.3 and 133 us
-// (29.7, 20.5 and 137).  From 17 tokens on the large form is as fast.
+// (29.7, 20.5 and 137).
 #include "grouped_gemm_2sm.cuh"
 #include "smem_limit.h"
 
@@ -298,14 +298,24 @@ int launch_few(FewArgs a, const CUtensorMap& mw, const CUtensorMap& mx, bool aft
 
 }  // namespace
 
-bool ffn_few_takes(const moe_ffn_shape& s) { return s.T <= kFfnFewTokens; }
+// More than eight tokens: sixteen a job, each weight read once for them.  A
+// small block's weights stay in the L2, and two jobs of eight have less to start
+// (16 tokens, 512 x 256: 5.8 against 7.7 us; 1160 x 712: 7.8 against 9.0; but
+// 2048 x 1408: 11.4 against 10.3, 7168 x 2048: 36.2 against 21.7).
+static bool few_two(const moe_ffn_shape& s) { return s.T > 8 && (long long)s.H * s.I > (1 << 20); }
+
+// Up to 16 tokens always; up to 128 while the jobs' tiles are not many more
+// than the SMs (us, this form | the large one: 512 x 256, 128 tokens 6.2 | 11.3;
+// 1160 x 712, 64: 9.7 | 14.4; 2048 x 1408, 32: 12.2 | 20.9, 96: 16.3 | 22.3, but
+// 128, 256 tiles: 33.8 | 22.9; 4096 x 2048, 32: 18.3 | 25.8, but 64, 256 tiles:
+// 29.1 | 27.6).
+bool ffn_few_takes(const moe_ffn_shape& s) {
+    const int per = few_two(s) ? 16 : 8, wide = s.H > s.I ? s.H : s.I;
+    return s.T <= 16 || (s.T <= 128 && (long long)((s.T + per - 1) / per) * ((wide + 63) / 64) <= 200);
+}
 
 int launch_ffn_few(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st) {
-    // More than eight tokens: sixteen a job, each weight read once.  A small
-    // block's weights stay in the L2, and two jobs of eight have less to start
-    // (16 tokens, 512 x 256: 5.8 against 7.7 us; 1160 x 712: 7.8 against 9.0;
-    // but 2048 x 1408: 11.4 against 10.3, 7168 x 2048: 36.2 against 21.7).
-    const bool two = s.T > 8 && (long long)s.H * s.I > (1 << 20);
+    const bool two = few_two(s);
     int rc;
     CUtensorMap w1, w2, x, act;
     if ((rc = abi_map_nd(&w1, f.W1, 2, {s.I, 2, s.H}, {64, 1, 16}, "W1 (gate/up halves)"))) return rc;

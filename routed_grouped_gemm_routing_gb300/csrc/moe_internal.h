@@ -157,8 +157,7 @@ long long ffn_part_bytes(const moe_ffn_shape& s);
 // MOE_OK or an error code with its message set.
 int launch_ffn_forward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
 int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
-// The forward's form for few tokens.
-constexpr int kFfnFewTokens = 16;
+// The forward's form for few tokens, and whether it takes a shape.
 bool ffn_few_takes(const moe_ffn_shape& s);
 int launch_ffn_few(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
 

@@ -244,7 +244,9 @@ def test_refusals():
     (7, 16, 4104),     # one unit of K; a tile of eight features
     (9, 520, 2056),    # sixteen tokens a job, ragged tiles
     (16, 4096, 1024), (13, 2048, 1408), (15, 1032, 4096),
-    (17, 1160, 712),   # the large form again
+    (17, 1160, 712),   # three jobs of eight tokens
+    (33, 2048, 1408), (96, 2048, 1408), (128, 512, 256), (127, 264, 72),
+    (129, 512, 256), (100, 2048, 1408),  # the large form
     (4, 4096, 10248), (16, 4096, 10248),  # more tiles than SMs, K in four parts
     (3, 10248, 4096),  # the same in the down projection's tiles, K whole
     (5, 10248, 8200),  # and K in four parts
