@@ -363,9 +363,9 @@ int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_t
  * expert) or in a layer without them: for x bf16 [T, H], W1 bf16 [H, 2I]
  * (columns [0, I) gate, [I, 2I) up) and W2 bf16 [I, H]
  *     h = x W1,  a = silu(h[:I]) h[I:],  y = a W2
- * with moe_shape's activation_clamp on both inputs of the activation.  T >= 0
- * tokens, H and I multiples of 8; all pointers 16-byte aligned, tensors
- * contiguous. */
+ * with moe_shape's activation_clamp on both inputs of the activation; a NaN is
+ * not clamped and stays NaN, in the gradients too.  T >= 0 tokens, H and I
+ * multiples of 8; all pointers 16-byte aligned, tensors contiguous. */
 typedef struct moe_ffn_shape {
     int32_t T, H, I;
     float activation_clamp;

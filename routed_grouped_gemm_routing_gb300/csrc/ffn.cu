@@ -56,6 +56,7 @@
 //
 // The tile is 256 x 256, or narrower (192, 128 columns) where that wastes less of
 // the last round over the pairs (dense_shape).
+#include "clamp.cuh"
 #include "grouped_gemm_2sm.cuh"
 
 namespace moe {
@@ -252,15 +253,15 @@ __device__ __forceinline__ void read_row_f32(uint32_t box, int r, float (&v)[32]
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 // a = silu(clamp g) clamp u
 __device__ __forceinline__ float gate_fwd(float g, float u, float c) {
-    g = clamp_in(g, c);
-    u = clamp_in(u, c);
+    g = clamp_keep_nan(g, c);
+    u = clamp_keep_nan(u, c);
     return g * sigmoid(g) * u;
 }
 // (dh_g, dh_u) of da
 __device__ __forceinline__ float2 gate_bwd(float da, float g, float u, float c) {
-    const float pg = clamp_pass(g, c), pu = clamp_pass(u, c);
-    g = clamp_in(g, c);
-    u = clamp_in(u, c);
+    const float pg = clamp_passes(g, c), pu = clamp_passes(u, c);
+    g = clamp_keep_nan(g, c);
+    u = clamp_keep_nan(u, c);
     const float s = sigmoid(g), gs = g * s;
     return make_float2(pg * da * u * (s + gs * (1.0f - s)), pu * da * gs);
 }

@@ -17,6 +17,7 @@
 // the copy rate): 7168 x 2048 20.0 us (32.1; 13.0), 2048 x 1408 8.9 us (20.1;
 // 2.6), 7168 x 18432 127 us (165; 117), and 16 tokens 21.7, 10.3 and 133 us
 // (29.7, 20.5 and 137).
+#include "clamp.cuh"
 #include "grouped_gemm_2sm.cuh"
 #include "smem_limit.h"
 
@@ -236,7 +237,7 @@ ffn_few_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
                 p.h[row * 2 * p.F + f] = v;
                 p.h[row * 2 * p.F + p.F + f] = up;
             }
-            const float gc = clamp_in(v, p.clamp), uc = clamp_in(up, p.clamp);
+            const float gc = clamp_keep_nan(v, p.clamp), uc = clamp_keep_nan(up, p.clamp);
             v = gc / (1.0f + expf(-gc)) * uc;
         }
         p.out[row * p.F + f] = __float2bfloat16_rn(v);
