@@ -168,15 +168,22 @@ def _ffn_check(x, W1, W2, ws):
         raise ValueError(f"expected x [{T}, {H}], W1 [{H}, {2 * I}], W2 [{I}, {H}] for this workspace")
 
 
-def ffn_forward(x, W1, W2, ws: FFNWorkspace):
-    """y bf16 [T, H] = (silu(x W1[:, :I]) * (x W1[:, I:])) W2 for contiguous
-    bf16 x [T, H], W1 [H, 2I] (gate | up), W2 [I, H]."""
-    s, d = ws.shape, x.get_device()
+def _ffn_shape(ws, activation_clamp):
+    """(shape, reference to it) of ws with another clamp, or its own for None."""
+    s = ws.shape
+    if activation_clamp is None or activation_clamp == s.activation_clamp:
+        return s, ws.shape_ref
+    s = B.MoeFFNShape(s.T, s.H, s.I, activation_clamp)
+    return s, ctypes.byref(s)
+
+
+def _ffn_forward(x, W1, W2, ws, s, s_ref):
+    d = x.get_device()
     T, H, I = s.T, s.H, s.I
     if (d >= 0 and d == _current() and d == ws.device.index and _plain(x, _BF, (T, H), d)
             and _plain(W1, _BF, (H, 2 * I), d) and _plain(W2, _BF, (I, H), d)):
         y = torch.empty_like(x)
-        rc = B.lib().moe_ffn_forward(ws.shape_ref, x.data_ptr(), W1.data_ptr(), W2.data_ptr(), int(ws.train),
+        rc = B.lib().moe_ffn_forward(s_ref, x.data_ptr(), W1.data_ptr(), W2.data_ptr(), int(ws.train),
                                      ws.saved.data_ptr(), ws.ws.data_ptr(), y.data_ptr(), _stream_of(d))
         if rc:
             B._check(rc)
@@ -185,14 +192,18 @@ def ffn_forward(x, W1, W2, ws: FFNWorkspace):
     _ffn_check(x, W1, W2, ws)
     with _on(x):
         y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        B.moe_ffn_forward(ws.shape, x, W1, W2, ws.saved, ws.ws, y, ws.train, layout=ws.layout)
+        B.moe_ffn_forward(s, x, W1, W2, ws.saved, ws.ws, y, ws.train, layout=ws.layout)
     ws.generation += 1
     return y
 
 
-def ffn_backward(dy, x, W1, W2, ws: FFNWorkspace):
-    """(dx, dW1, dW2) bf16 for dy [T, H], after ffn_forward on the same inputs
-    and workspace."""
+def ffn_forward(x, W1, W2, ws: FFNWorkspace):
+    """y bf16 [T, H] = (silu(x W1[:, :I]) * (x W1[:, I:])) W2 for contiguous
+    bf16 x [T, H], W1 [H, 2I] (gate | up), W2 [I, H]."""
+    return _ffn_forward(x, W1, W2, ws, ws.shape, ws.shape_ref)
+
+
+def _ffn_backward(dy, x, W1, W2, ws, s):
     _ffn_check(x, W1, W2, ws)
     if not ws.train:
         raise ValueError("the workspace was made without train")
@@ -200,8 +211,14 @@ def ffn_backward(dy, x, W1, W2, ws: FFNWorkspace):
         raise ValueError("dy must have x's shape")
     with _on(x):
         dx, dW1, dW2 = (torch.empty(t.shape, dtype=torch.bfloat16, device=x.device) for t in (x, W1, W2))
-        B.moe_ffn_backward(ws.shape, dy, x, W1, W2, ws.saved, ws.ws, dx, dW1, dW2, layout=ws.layout)
+        B.moe_ffn_backward(s, dy, x, W1, W2, ws.saved, ws.ws, dx, dW1, dW2, layout=ws.layout)
     return dx, dW1, dW2
+
+
+def ffn_backward(dy, x, W1, W2, ws: FFNWorkspace):
+    """(dx, dW1, dW2) bf16 for dy [T, H], after ffn_forward on the same inputs
+    and workspace."""
+    return _ffn_backward(dy, x, W1, W2, ws, ws.shape)
 
 
 class GatedFFNFunction(torch.autograd.Function):
@@ -212,11 +229,12 @@ class GatedFFNFunction(torch.autograd.Function):
         W1, W2 = W1.contiguous(), W2.contiguous()
         s = (x2.shape[0], H, I)
         if ws is None or (ws.shape.T, ws.shape.H, ws.shape.I) != s or not ws.train:
-            ws = FFNWorkspace(*s, device=x.device, activation_clamp=activation_clamp)
-        ws.shape.activation_clamp = activation_clamp
-        y = ffn_forward(x2, W1, W2, ws)
+            clamp = ws.shape.activation_clamp if ws is not None and activation_clamp is None else activation_clamp or 0.0
+            ws = FFNWorkspace(*s, device=x.device, activation_clamp=clamp)
+        shape, ref = _ffn_shape(ws, activation_clamp)
+        y = _ffn_forward(x2, W1, W2, ws, shape, ref)
         ctx.save_for_backward(x2, W1, W2)
-        ctx.ws, ctx.ws_generation, ctx.clamp = ws, ws.generation, activation_clamp
+        ctx.ws, ctx.ws_generation, ctx.clamp = ws, ws.generation, shape.activation_clamp
         return y.view(x.shape)
 
     @staticmethod
@@ -226,16 +244,18 @@ class GatedFFNFunction(torch.autograd.Function):
         if ws.generation != ctx.ws_generation:
             raise RuntimeError("gated_ffn backward: its workspace was overwritten by a later forward; give forwards "
                                "whose backwards are still pending workspaces of their own")
-        ws.shape.activation_clamp = ctx.clamp
-        dx, dW1, dW2 = ffn_backward(dy.to(torch.bfloat16).reshape(x2.shape).contiguous(), x2, W1, W2, ws)
+        dy2 = dy.to(torch.bfloat16).reshape(x2.shape).contiguous()
+        dx, dW1, dW2 = _ffn_backward(dy2, x2, W1, W2, ws, _ffn_shape(ws, ctx.clamp)[0])
         return dx.view(dy.shape), dW1, dW2, None, None
 
 
-def gated_ffn(x, W1, W2, workspace: FFNWorkspace | None = None, activation_clamp: float = 0.0):
+def gated_ffn(x, W1, W2, workspace: FFNWorkspace | None = None, activation_clamp: float | None = None):
     """The dense gated feed-forward block (a shared expert): bf16 x [..., H],
     W1 [H, 2I] (gate | up), W2 [I, H]; H and I multiples of 8.  Differentiable
-    in all three.  activation_clamp as in ``layer.moe_layer``."""
-    return GatedFFNFunction.apply(x, W1, W2, workspace, float(activation_clamp))
+    in all three.  activation_clamp as in ``layer.moe_layer``, for this call
+    alone; None: the workspace's, or none without one."""
+    clamp = None if activation_clamp is None else float(activation_clamp)
+    return GatedFFNFunction.apply(x, W1, W2, workspace, clamp)
 
 
 # ---------------------------------------------------------- 4-bit weights
