@@ -141,8 +141,9 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5):
 class FFNWorkspace:
     """Device buffers of one block shape, kept from step to step: what the
     forward saves for its backward (the activation and, with ``train``, h) and
-    scratch.  ``generation`` counts the forwards that wrote into it: a backward
-    raises if another forward has overwritten the workspace since its own."""
+    scratch.  ``generation`` counts the forwards that wrote into it: gated_ffn's
+    backward raises if another forward has overwritten the workspace since its
+    own, and ffn_backward does where it is given its forward's generation."""
 
     def __init__(self, T: int, H: int, I: int, device=None, activation_clamp: float = 0.0, train: bool = True):
         self.shape = B.MoeFFNShape(T, H, I, activation_clamp)
@@ -203,7 +204,11 @@ def ffn_forward(x, W1, W2, ws: FFNWorkspace):
     return _ffn_forward(x, W1, W2, ws, ws.shape, ws.shape_ref)
 
 
-def _ffn_backward(dy, x, W1, W2, ws, s):
+def _ffn_backward(dy, x, W1, W2, ws, s, generation):
+    if generation is not None and ws.generation != generation:
+        raise RuntimeError("feed-forward backward: its workspace was overwritten by a later forward (this one wrote "
+                           f"generation {generation}, the workspace now holds {ws.generation}); give forwards whose "
+                           "backwards are still pending workspaces of their own")
     _ffn_check(x, W1, W2, ws)
     if not ws.train:
         raise ValueError("the workspace was made without train")
@@ -215,10 +220,12 @@ def _ffn_backward(dy, x, W1, W2, ws, s):
     return dx, dW1, dW2
 
 
-def ffn_backward(dy, x, W1, W2, ws: FFNWorkspace):
+def ffn_backward(dy, x, W1, W2, ws: FFNWorkspace, generation: int | None = None):
     """(dx, dW1, dW2) bf16 for dy [T, H], after ffn_forward on the same inputs
-    and workspace."""
-    return _ffn_backward(dy, x, W1, W2, ws, ws.shape)
+    and workspace.  generation: ``ws.generation`` as that forward left it;
+    raises if another forward has overwritten the workspace since.  None: the
+    caller sees to it that the last forward was this one."""
+    return _ffn_backward(dy, x, W1, W2, ws, ws.shape, generation)
 
 
 class GatedFFNFunction(torch.autograd.Function):
@@ -241,11 +248,8 @@ class GatedFFNFunction(torch.autograd.Function):
     def backward(ctx, dy):
         x2, W1, W2 = ctx.saved_tensors
         ws = ctx.ws
-        if ws.generation != ctx.ws_generation:
-            raise RuntimeError("gated_ffn backward: its workspace was overwritten by a later forward; give forwards "
-                               "whose backwards are still pending workspaces of their own")
         dy2 = dy.to(torch.bfloat16).reshape(x2.shape).contiguous()
-        dx, dW1, dW2 = _ffn_backward(dy2, x2, W1, W2, ws, _ffn_shape(ws, ctx.clamp)[0])
+        dx, dW1, dW2 = _ffn_backward(dy2, x2, W1, W2, ws, _ffn_shape(ws, ctx.clamp)[0], ctx.ws_generation)
         return dx.view(dy.shape), dW1, dW2, None, None
 
 
