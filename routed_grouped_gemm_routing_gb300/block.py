@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -40,6 +41,36 @@ def _on(t):
     if dev < 0:
         raise TypeError("expected CUDA tensors")
     return _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+class _NoSecondOrder(torch.autograd.Function):
+    """Passes gradients on; differentiating them raises."""
+
+    @staticmethod
+    def forward(ctx, *grads):
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the block operators have first-order gradients only")
+
+
+def _first_order(backward):
+    """A backward whose kernels no graph records.  Under create_graph its
+    gradients raise when they are differentiated themselves, whatever dy is
+    (torch's once_differentiable lets them through where dy is a constant, and
+    the second-order part would be missing without a word)."""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, dy):
+        if not torch.is_grad_enabled():
+            return backward(ctx, dy)
+        with torch.no_grad():
+            out = backward(ctx, dy)
+        marked = iter(_NoSecondOrder.apply(*(t.detach().requires_grad_() for t in out if t is not None)))
+        return tuple(None if t is None else next(marked) for t in out)
+
+    return wrapped
 
 
 # -------------------------------------------------------------- layer norm
@@ -125,6 +156,7 @@ class LayerNormFunction(torch.autograd.Function):
         return y.view(x.shape)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x2, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = layer_norm_backward(_rows_of(dy.to(x2.dtype), x2.shape[1]), x2, weight, mean, rstd, ctx.has_bias)
@@ -133,7 +165,7 @@ class LayerNormFunction(torch.autograd.Function):
 
 def layer_norm(x, weight, bias=None, eps: float = 1e-5):
     """Layer norm over the last axis of x (any number of leading axes), in
-    x's type.  Differentiable in x, weight and bias."""
+    x's type.  Differentiable in x, weight and bias, once."""
     return LayerNormFunction.apply(x, weight, bias, float(eps))
 
 
@@ -245,6 +277,7 @@ class GatedFFNFunction(torch.autograd.Function):
         return y.view(x.shape)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy):
         x2, W1, W2 = ctx.saved_tensors
         ws = ctx.ws
@@ -256,7 +289,7 @@ class GatedFFNFunction(torch.autograd.Function):
 def gated_ffn(x, W1, W2, workspace: FFNWorkspace | None = None, activation_clamp: float | None = None):
     """The dense gated feed-forward block (a shared expert): bf16 x [..., H],
     W1 [H, 2I] (gate | up), W2 [I, H]; H and I multiples of 8.  Differentiable
-    in all three.  activation_clamp as in ``layer.moe_layer``, for this call
+    in all three, once.  activation_clamp as in ``layer.moe_layer``, for this call
     alone; None: the workspace's, or none without one."""
     clamp = None if activation_clamp is None else float(activation_clamp)
     return GatedFFNFunction.apply(x, W1, W2, workspace, clamp)
