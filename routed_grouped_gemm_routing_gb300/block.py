@@ -260,18 +260,23 @@ def ffn_backward(dy, x, W1, W2, ws: FFNWorkspace, generation: int | None = None)
     return _ffn_backward(dy, x, W1, W2, ws, ws.shape, generation)
 
 
+def _ffn_call(x, W1, W2, ws, activation_clamp, train):
+    """(x [T, H], W1, W2, workspace, shape, y [T, H]) of a gated_ffn call; the
+    workspace is ws where its shape and form allow, else a new one."""
+    H, I = x.shape[-1], W2.shape[0]
+    x, W1, W2 = x.reshape(-1, H).contiguous(), W1.contiguous(), W2.contiguous()
+    s = (x.shape[0], H, I)
+    if ws is None or (ws.shape.T, ws.shape.H, ws.shape.I) != s or (train and not ws.train):
+        clamp = ws.shape.activation_clamp if ws is not None and activation_clamp is None else activation_clamp or 0.0
+        ws = FFNWorkspace(*s, device=x.device, activation_clamp=clamp, train=train)
+    shape, ref = _ffn_shape(ws, activation_clamp)
+    return x, W1, W2, ws, shape, _ffn_forward(x, W1, W2, ws, shape, ref)
+
+
 class GatedFFNFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W1, W2, ws, activation_clamp):
-        H, I = x.shape[-1], W2.shape[0]
-        x2 = x.reshape(-1, H).contiguous()
-        W1, W2 = W1.contiguous(), W2.contiguous()
-        s = (x2.shape[0], H, I)
-        if ws is None or (ws.shape.T, ws.shape.H, ws.shape.I) != s or not ws.train:
-            clamp = ws.shape.activation_clamp if ws is not None and activation_clamp is None else activation_clamp or 0.0
-            ws = FFNWorkspace(*s, device=x.device, activation_clamp=clamp)
-        shape, ref = _ffn_shape(ws, activation_clamp)
-        y = _ffn_forward(x2, W1, W2, ws, shape, ref)
+        x2, W1, W2, ws, shape, y = _ffn_call(x, W1, W2, ws, activation_clamp, True)
         ctx.save_for_backward(x2, W1, W2)
         ctx.ws, ctx.ws_generation, ctx.clamp = ws, ws.generation, shape.activation_clamp
         return y.view(x.shape)
@@ -290,8 +295,14 @@ def gated_ffn(x, W1, W2, workspace: FFNWorkspace | None = None, activation_clamp
     """The dense gated feed-forward block (a shared expert): bf16 x [..., H],
     W1 [H, 2I] (gate | up), W2 [I, H]; H and I multiples of 8.  Differentiable
     in all three, once.  activation_clamp as in ``layer.moe_layer``, for this call
-    alone; None: the workspace's, or none without one."""
+    alone; None: the workspace's, or none without one.  A workspace of another
+    shape, or one made without ``train`` where gradients are wanted, is left
+    alone and a new one made.  Without gradients (no_grad, or no input that
+    requires one) the workspace's form is taken, without one the inference
+    form."""
     clamp = None if activation_clamp is None else float(activation_clamp)
+    if not (torch.is_grad_enabled() and (x.requires_grad or W1.requires_grad or W2.requires_grad)):
+        return _ffn_call(x, W1, W2, workspace, clamp, False)[-1].view(x.shape)
     return GatedFFNFunction.apply(x, W1, W2, workspace, clamp)
 
 
