@@ -184,10 +184,14 @@ class FFNWorkspace:
         dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.train = train
         self.saved = torch.empty(max(L.saved_bytes if train else L.h, 16), dtype=torch.uint8, device=dev)
-        self.ws = torch.empty(L.ws_bytes, dtype=torch.uint8, device=dev)
-        self.ws[:16].zero_()
         self.device = dev
+        self.ws = self._scratch()
         self.generation = 0
+
+    def _scratch(self):
+        ws = torch.empty(self.layout.ws_bytes, dtype=torch.uint8, device=self.device)
+        ws[:16].zero_()
+        return ws
 
     def status(self) -> int:
         """The status word (synchronises): nonzero when a kernel gave up on a bounded wait."""
@@ -276,7 +280,10 @@ def _ffn_call(x, W1, W2, ws, activation_clamp, train):
 class GatedFFNFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W1, W2, ws, activation_clamp):
-        x2, W1, W2, ws, shape, y = _ffn_call(x, W1, W2, ws, activation_clamp, True)
+        given = ws
+        x2, W1, W2, ws, shape, y = _ffn_call(x, W1, W2, given, activation_clamp, True)
+        if ws is not given:
+            ws.ws = None  # what is pending holds the saved values alone; the backward takes scratch of its own
         ctx.save_for_backward(x2, W1, W2)
         ctx.ws, ctx.ws_generation, ctx.clamp = ws, ws.generation, shape.activation_clamp
         return y.view(x.shape)
@@ -287,7 +294,12 @@ class GatedFFNFunction(torch.autograd.Function):
         x2, W1, W2 = ctx.saved_tensors
         ws = ctx.ws
         dy2 = dy.to(torch.bfloat16).reshape(x2.shape).contiguous()
+        own = ws.ws is None
+        if own:
+            ws.ws = ws._scratch()
         dx, dW1, dW2 = _ffn_backward(dy2, x2, W1, W2, ws, _ffn_shape(ws, ctx.clamp)[0], ctx.ws_generation)
+        if own:
+            ws.ws = None
         return dx.view(dy.shape), dW1, dW2, None, None
 
 
