@@ -410,8 +410,9 @@ int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, 
  * 128: code 2 m (m in 0..3) of the eight in nibble m, code 2 m + 1 in nibble
  * m + 4.  Sums are FP32, the output is rounded once.  An infinity or NaN in a
  * row of x gives NaN in that row's outputs only (finite |x| up to 1e35 is
- * meant: the sums carry 136 x).  All pointers are 16-byte aligned.  A kernel that
- * gives up on a bounded wait leaves NaN in its outputs. */
+ * meant: the sums carry 136 x).  All pointers are 16-byte aligned, but
+ * topk_idx and topk_w need only their element's alignment.  A kernel that gives
+ * up on a bounded wait leaves NaN in its outputs. */
 
 /* W bf16 [E, K, N] (the layout of moe_forward's W1 with K = H, N = 2 I, and of
  * W2 with K = I, N = H) -> W_q u8 [E, N, K / 2] and W_sf bf16 [E, N,

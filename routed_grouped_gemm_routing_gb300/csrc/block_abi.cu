@@ -156,9 +156,12 @@ int moe_forward_w4(const moe_w4_shape* shape, const void* x, const uint8_t* W1_q
     if (shape->T == 0) return MOE_OK;
     if (!x || !W1_q || !W1_sf || !W2_q || !W2_sf || !ws || !y || (topk_idx && !topk_w))
         return abi_fail(MOE_EINVAL, "NULL pointer argument");
-    const void* ptrs[] = {x, W1_q, W1_sf, W2_q, W2_sf, topk_idx, topk_w, ws, y};
+    const void* ptrs[] = {x, W1_q, W1_sf, W2_q, W2_sf, ws, y};
     for (const void* p : ptrs)
         if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    // read element by element: one token's routing may start anywhere in a batch's
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return abi_fail(MOE_EUNSUPPORTED, "topk_idx and topk_w must be 4-byte aligned");
     int sms = 0;
     if ((rc = abi_select_device(ws, &sms))) return rc;
     uint8_t* w = static_cast<uint8_t*>(ws);
