@@ -409,8 +409,10 @@ int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, 
  * words; word 4 t + j (t, j in 0..3) holds the codes 32 j + 8 t .. + 7 of the
  * 128: code 2 m (m in 0..3) of the eight in nibble m, code 2 m + 1 in nibble
  * m + 4.  Sums are FP32, the output is rounded once.  An infinity or NaN in a
- * row of x gives NaN in that row's outputs only (finite |x| up to 1e35 is
- * meant: the sums carry 136 x).  All pointers are 16-byte aligned, but
+ * row of x gives NaN in that row's outputs only.  The sums of a group carry up
+ * to 143 sum |x| (the codes' offset, taken out in FP32): |x| <= 1.8e34 is finite
+ * for every group (143 * 128 * 1.8e34 = 3.3e38); larger x may give infinities or
+ * NaN in its row.  All pointers are 16-byte aligned, but
  * topk_idx and topk_w need only their element's alignment.  A kernel that gives
  * up on a bounded wait leaves NaN in its outputs. */
 
