@@ -332,7 +332,7 @@ enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
  * x_type.  x_stride >= H: elements between the starts of two rows of x (the
  * last axis is contiguous; y is contiguous).  bias may be NULL (none).
  * Overwrites y, and mean f32[rows] and rstd f32[rows] (m and s, for the
- * backward).  Any H >= 1 and any 0 <= rows < 2^31; pointers need only their
+ * backward).  Any 1 <= H <= 2^29 and 0 <= rows < 2^31; pointers need only their
  * element's alignment (16-byte vectors are used where width, stride and
  * addresses allow).  Statistics are FP32, y is rounded once.  A row that
  * holds a NaN or an infinity gives NaN, as the formula does.

@@ -329,6 +329,16 @@ def _rows_arg(t, dtype, rows, H, name, dev):
     return t.data_ptr(), stride
 
 
+NORM_MAX_H = 1 << 29
+
+
+def _norm_width(H):
+    """H, refused here where the C type would cut it to its low bits."""
+    if H > NORM_MAX_H:
+        raise MoeError(MOE_EINVAL, "H must be in [1, 2^29]")
+    return H
+
+
 _SIZE = threading.local()
 
 
@@ -345,7 +355,7 @@ def _size_out():
 def moe_layer_norm_workspace(rows: int, H: int) -> int:
     """Bytes of moe_layer_norm_backward's workspace."""
     v, ref = _size_out()
-    rc = lib().moe_layer_norm_workspace(rows, H, ref)
+    rc = lib().moe_layer_norm_workspace(rows, _norm_width(H), ref)
     if rc:
         _check(rc)
     return v.value
@@ -357,6 +367,7 @@ def moe_layer_norm_forward(x, weight, bias, eps: float, y, mean, rstd, stream=No
     or f32, bias may be None.  Overwrites y [rows, H], mean and rstd f32 [rows]."""
     tx, tw = _type_of(x, "x"), _type_of(weight, "weight")
     rows, H = x.shape
+    _norm_width(H)
     dev, st = _here(stream)
     xt, wt = x.dtype, weight.dtype
     px, sx = _rows_arg(x, xt, rows, H, "x", dev)
@@ -373,6 +384,7 @@ def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, s
     moe_layer_norm_workspace(rows, H) elements."""
     tx, tw = _type_of(x, "x"), _type_of(weight, "weight")
     rows, H = x.shape
+    _norm_width(H)
     dev, st = _here(stream)
     xt, wt = x.dtype, weight.dtype
     px, sx = _rows_arg(x, xt, rows, H, "x", dev)

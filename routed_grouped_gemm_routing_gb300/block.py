@@ -88,8 +88,8 @@ def layer_norm_forward(x, weight, bias=None, eps: float = 1e-5):
     layer_norm_backward reads.  x bf16, f16 or f32, its rows may be strided;
     weight and bias [H] in x's type or f32."""
     dt, wt, sh, d = x.dtype, weight.dtype, x.shape, x.get_device()
-    if (len(sh) == 2 and dt in _TYPES and wt in _TYPES and d >= 0 and d == _current() and x.is_contiguous()
-            and _plain(weight, wt, sh[1:], d) and (bias is None or _plain(bias, wt, sh[1:], d))):
+    if (len(sh) == 2 and sh[1] <= B.NORM_MAX_H and dt in _TYPES and wt in _TYPES and d >= 0 and d == _current()
+            and x.is_contiguous() and _plain(weight, wt, sh[1:], d) and (bias is None or _plain(bias, wt, sh[1:], d))):
         rows, dev = sh[0], x.device
         y = torch.empty_like(x)
         mean = torch.empty((rows,), dtype=_F32, device=dev)
@@ -114,8 +114,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True):
     """(dx, dweight, dbias) for dy [rows, H]; dbias is None without ``bias``.
     dweight and dbias have weight's type."""
     dt, wt, sh, d = x.dtype, weight.dtype, x.shape, x.get_device()
-    if (len(sh) == 2 and dt in _TYPES and wt in _TYPES and d >= 0 and d == _current() and x.is_contiguous()
-            and _plain(dy, dt, sh, d) and _plain(weight, wt, sh[1:], d) and _plain(mean, _F32, sh[:1], d)
+    if (len(sh) == 2 and sh[1] <= B.NORM_MAX_H and dt in _TYPES and wt in _TYPES and d >= 0 and d == _current()
+            and x.is_contiguous() and _plain(dy, dt, sh, d) and _plain(weight, wt, sh[1:], d) and _plain(mean, _F32, sh[:1], d)
             and _plain(rstd, _F32, sh[:1], d)):
         rows, H, dev = sh[0], sh[1], x.device
         dx, dw = torch.empty_like(x), torch.empty_like(weight)

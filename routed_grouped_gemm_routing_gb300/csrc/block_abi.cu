@@ -10,6 +10,7 @@ using namespace moe;
 namespace {
 
 constexpr int kMaxW4K = 65536;
+constexpr int kMaxNormH = 1 << 29;  // 2 H columns of sums, and a block's stride past the last, in 32 bits
 
 // Alignment that an element of the type needs, 0 for an unknown type.
 int elt_size(int type) { return type == MOE_F32 ? 4 : type == MOE_BF16 || type == MOE_F16 ? 2 : 0; }
@@ -17,7 +18,7 @@ bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) %
 
 int check_norm(int64_t rows, int32_t H, int32_t x_type, int32_t w_type) {
     if (rows < 0 || rows >= (1ll << 31)) return abi_fail(MOE_EINVAL, "rows must be in [0, 2^31)");
-    if (H < 1) return abi_fail(MOE_EINVAL, "H must be >= 1");
+    if (H < 1 || H > kMaxNormH) return abi_fail(MOE_EINVAL, "H must be in [1, 2^29]");
     if (!elt_size(x_type)) return abi_fail(MOE_EUNSUPPORTED, "x_type must be MOE_BF16, MOE_F16 or MOE_F32");
     if (w_type != MOE_F32 && w_type != x_type)
         return abi_fail(MOE_EUNSUPPORTED, "w_type must be MOE_F32 or x_type");
