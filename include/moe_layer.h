@@ -405,7 +405,7 @@ int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, 
  * (decoding).  A matrix W [N, K] (y = x W^T) is held as
  *     W[n, k] = (code[n, k] - 8) * sf[n, k / group],   code in [0, 15],
  * sf bf16 [N, K / group], group 32, 64 or 128, K a multiple of 128 up to
- * 65536, any N.  Codes u8 [N, K / 2]: 64 bytes per 128 codes, 16 little-endian
+ * 65536, N up to 2^30.  Codes u8 [N, K / 2]: 64 bytes per 128 codes, 16 little-endian
  * words; word 4 t + j (t, j in 0..3) holds the codes 32 j + 8 t .. + 7 of the
  * 128: code 2 m (m in 0..3) of the eight in nibble m, code 2 m + 1 in nibble
  * m + 4.  Sums are FP32, the output is rounded once.  An infinity or NaN in a

@@ -397,10 +397,17 @@ def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, s
         _check(rc)
 
 
+def _w4_sizes(N, K):
+    """Refuses what the library would, before a C type cuts a size to its low bits."""
+    if N > 1 << 30 or K > 1 << 16:
+        raise MoeError(MOE_EUNSUPPORTED, f"a 4-bit weight has up to 2^30 rows of up to 65536 values, got [{N}, {K}]")
+
+
 def moe_quantize_w4(W, W_q, W_sf, group: int, stream=None):
     """W bf16 [E, K, N] -> W_q uint8 [E, N, K // 2] (4-bit codes) and W_sf bf16
     [E, N, K // group]."""
     E, K, N = W.shape
+    _w4_sizes(N, K)
     dev, st = _here(stream)
     _check(lib().moe_quantize_w4(E, K, N, group, _arg(W, _BF, E * K * N, "W", dev),
                                  _arg(W_q, _U8, E * N * K // 2, "W_q", dev),
@@ -411,6 +418,7 @@ def moe_matvec_w4(x, W_q, W_sf, y, group: int, stream=None):
     """y bf16 [M, N] = x bf16 [M, K] times the 4-bit matrix [N, K] transposed."""
     M, K = x.shape
     N = W_q.shape[0]
+    _w4_sizes(N, K)
     dev, st = _here(stream)
     rc = lib().moe_matvec_w4(M, N, K, group, _arg(x, _BF, M * K, "x", dev), _arg(W_q, _U8, N * K // 2, "W_q", dev),
                              _arg(W_sf, _BF, N * K // max(group, 1), "W_sf", dev), _arg(y, _BF, M * N, "y", dev), st)

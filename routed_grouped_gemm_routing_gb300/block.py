@@ -328,6 +328,7 @@ def quantize_w4(W, group: int = 128):
     E, K, N = W3.shape
     if group not in (32, 64, 128) or K % 128:
         raise ValueError("group must be 32, 64 or 128, and K a multiple of 128")
+    B._w4_sizes(N, K)
     with _on(W):
         q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=W.device)
         sf = torch.empty((E, N, K // group), dtype=torch.bfloat16, device=W.device)
@@ -337,6 +338,7 @@ def quantize_w4(W, group: int = 128):
 
 def _check_w4(q, sf, group, *shape):
     K = shape[-1]
+    B._w4_sizes(*shape[-2:])
     if tuple(q.shape) != (*shape[:-1], K // 2) or tuple(sf.shape) != (*shape[:-1], K // group):
         raise ValueError(f"expected codes {[*shape[:-1], K // 2]} and scales {[*shape[:-1], K // group]}, "
                          f"got {list(q.shape)} and {list(sf.shape)}")

@@ -10,6 +10,7 @@ using namespace moe;
 namespace {
 
 constexpr int kMaxW4K = 65536;
+constexpr int kMaxW4N = 1 << 30;  // tiles' and blocks' rows past the last, in 32 bits
 constexpr int kMaxNormH = 1 << 29;  // 2 H columns of sums, and a block's stride past the last, in 32 bits
 
 // Alignment that an element of the type needs, 0 for an unknown type.
@@ -122,6 +123,7 @@ int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, const void* x,
     if (M < 0 || N < 1 || K < 1) return abi_fail(MOE_EINVAL, "M must be >= 0, N and K > 0");
     if (K % 128 || K > kMaxW4K) return abi_fail(MOE_EUNSUPPORTED, "K must be a multiple of 128, at most 65536");
     if (M > 65535) return abi_fail(MOE_EUNSUPPORTED, "M must be <= 65535");
+    if (N > kMaxW4N) return abi_fail(MOE_EUNSUPPORTED, "N must be <= 2^30");
     int rc = check_group(group);
     if (rc) return rc;
     if (M == 0) return MOE_OK;
@@ -180,6 +182,7 @@ int moe_quantize_w4(int32_t E, int32_t K, int32_t N, int32_t group, const void* 
                     void* stream) {
     if (E < 1 || E > kMaxExperts || K < 1 || N < 1) return abi_fail(MOE_EINVAL, "E must be in [1, 1024], K and N > 0");
     if (K % 128 || K > kMaxW4K) return abi_fail(MOE_EUNSUPPORTED, "K must be a multiple of 128, at most 65536");
+    if (N > kMaxW4N) return abi_fail(MOE_EUNSUPPORTED, "N must be <= 2^30");
     int rc = check_group(group);
     if (rc) return rc;
     if (!W || !W_q || !W_sf) return abi_fail(MOE_EINVAL, "NULL pointer argument");
