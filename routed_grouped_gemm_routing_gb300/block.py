@@ -344,6 +344,8 @@ def _check_w4(q, sf, group, *shape):
                          f"got {list(q.shape)} and {list(sf.shape)}")
     if q.dtype != torch.uint8 or sf.dtype != torch.bfloat16 or not q.is_cuda or not sf.is_cuda:
         raise TypeError("codes must be uint8 and scales bfloat16 CUDA tensors")
+    if q.get_device() != sf.get_device():
+        raise ValueError(f"codes on cuda:{q.get_device()} and scales on cuda:{sf.get_device()}")
     return q.contiguous(), sf.contiguous()
 
 
@@ -394,6 +396,8 @@ class W4Experts:
         self.E, self.H, self.I, self.group = E, 2 * half, I2 // 2, group
         self.W1_q, self.W1_sf = _check_w4(W1_q, W1_sf, group, E, I2, self.H)
         self.W2_q, self.W2_sf = _check_w4(W2_q, W2_sf, group, E, self.H, self.I)
+        if self.W1_q.get_device() != self.W2_q.get_device():
+            raise ValueError(f"W1 on cuda:{self.W1_q.get_device()} and W2 on cuda:{self.W2_q.get_device()}")
         self._sizes = {}  # (T, k) -> shape, workspace bytes
 
     def _size(self, T, k):
