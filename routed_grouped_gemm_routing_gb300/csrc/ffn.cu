@@ -482,7 +482,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if (threadIdx.x == 32 * kDenseWarpTma) {
         tma_prefetch_map(&mA);
         tma_prefetch_map(&mB);
-        tma_prefetch_map(EPI == EPI_GATED || EPI == EPI_DGATE ? &mC1 : &mC0);
+        // EPI_GATED without save_h has no third map: none was encoded
+        if (EPI != EPI_GATED || p.save_h) tma_prefetch_map(EPI == EPI_GATED || EPI == EPI_DGATE ? &mC1 : &mC0);
     }
     const DenseCta c = dense_begin<EPI>();
     if (c.warp == kDenseWarpTma) {
