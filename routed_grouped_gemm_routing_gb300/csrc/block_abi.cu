@@ -75,9 +75,7 @@ int moe_layer_norm_forward(int64_t rows, int32_t H, int32_t x_type, int32_t w_ty
     if ((rc = abi_select_device(x, &sms))) return rc;
     const LnFwdArgs a = {rows, H, x, weight, bias, x_stride, eps, y, mean, rstd};
     cudaStream_t st = (cudaStream_t)stream;
-    trace_pre(st);
     const int e = launch_layer_norm_fwd(x_type, w_type, a, st);
-    trace_post(st, "layer_norm_fwd");
     return e ? abi_cuda_fail(e, "layer norm launch") : MOE_OK;
 }
 
@@ -112,9 +110,7 @@ int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_t
     }
     const LnBwdArgs a = {rows, H, dy, x, weight, dy_stride, x_stride, mean, rstd, dx, dweight, dbias,
                          static_cast<float*>(ws)};
-    trace_pre(st);
     const int e = launch_layer_norm_bwd(x_type, w_type, a, st);
-    trace_post(st, "layer_norm_bwd");
     return e ? abi_cuda_fail(e, "layer norm backward launch") : MOE_OK;
 }
 
@@ -134,9 +130,7 @@ int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, const void* x,
     int sms = 0;
     if ((rc = abi_select_device(W_q, &sms))) return rc;
     cudaStream_t st = (cudaStream_t)stream;
-    trace_pre(st);
     const int e = launch_matvec_w4(M, N, K, group, x, W_q, W_sf, y, st);
-    trace_post(st, "matvec_w4");
     return e ? abi_cuda_fail(e, "4-bit product launch") : MOE_OK;
 }
 
@@ -172,9 +166,7 @@ int moe_forward_w4(const moe_w4_shape* shape, const void* x, const uint8_t* W1_q
     const W4Experts a = {shape->T, shape->H, shape->I, shape->E, shape->k, shape->group, x, W1_q, W2_q, W1_sf, W2_sf,
                          topk_idx, topk_w, w, reinterpret_cast<float*>(w + up256(slots * shape->I * 2)), y};
     cudaStream_t st = (cudaStream_t)stream;
-    trace_pre(st);
     const int e = launch_experts_w4(a, st);
-    trace_post(st, "forward_w4");
     return e ? abi_cuda_fail(e, "4-bit experts launch") : MOE_OK;
 }
 
@@ -192,9 +184,7 @@ int moe_quantize_w4(int32_t E, int32_t K, int32_t N, int32_t group, const void* 
     int sms = 0;
     if ((rc = abi_select_device(W, &sms))) return rc;
     cudaStream_t st = (cudaStream_t)stream;
-    trace_pre(st);
     const int e = launch_quantize_w4(E, K, N, group, W, W_q, W_sf, st);
-    trace_post(st, "quantize_w4");
     return e ? abi_cuda_fail(e, "4-bit quantization launch") : MOE_OK;
 }
 

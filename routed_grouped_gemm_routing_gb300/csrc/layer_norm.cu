@@ -1030,9 +1030,11 @@ int run_fwd_ring(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
     static_assert(per_thread * kLnRingThreads <= 200 * 1024, "shared memory per block");
     if (const int e = limit.allow(ln_fwd_ring<T, W, NV, kBias, kReducer, kShift>, per_thread * kLnRingThreads)) return e;
     const long long need = (a.rows + ng - 1) / ng;
+    trace_pre(st);
     ln_fwd_ring<T, W, NV, kBias, kReducer, kShift><<<ring_blocks(need, kShift), threads, per_thread * threads, st>>>(
         a.rows, a.H, f.threads, static_cast<const T*>(a.x), a.x_stride, static_cast<const W*>(a.weight),
         static_cast<const W*>(a.bias), a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
+    trace_post(st, "layer_norm_fwd");
     return (int)cudaGetLastError();
 }
 template <typename T, typename W, bool kBias, bool kShift>
@@ -1045,16 +1047,20 @@ int fwd_ring(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
 template <typename T, typename W, int NV, bool kWarpRow>
 int run_fwd(const LnForm& f, const LnFwdArgs& a, cudaStream_t st) {
     const long long blocks = kWarpRow ? (a.rows + kLnWarps - 1) / kLnWarps : a.rows;
+    trace_pre(st);
     ln_fwd<T, W, NV, kWarpRow><<<(unsigned)blocks, f.threads, 0, st>>>(
         a.rows, a.H, static_cast<const T*>(a.x), a.x_stride, static_cast<const W*>(a.weight),
         static_cast<const W*>(a.bias), a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
+    trace_post(st, "layer_norm_fwd");
     return (int)cudaGetLastError();
 }
 template <typename T, typename W, int V>
 int run_fwd_long(const LnFwdArgs& a, cudaStream_t st) {
+    trace_pre(st);
     ln_fwd_long<T, W, V><<<(unsigned)a.rows, kLnLongThreads, 0, st>>>(
         a.rows, a.H, static_cast<const T*>(a.x), a.x_stride, static_cast<const W*>(a.weight),
         static_cast<const W*>(a.bias), a.eps, static_cast<T*>(a.y), a.mean, a.rstd);
+    trace_post(st, "layer_norm_fwd");
     return (int)cudaGetLastError();
 }
 template <typename T, typename W>
@@ -1092,7 +1098,9 @@ int run_bwd_ring(const LnForm& f, const LnBwd& p, int* blocks, cudaStream_t st) 
     if (const int e = limit.allow(ln_bwd_ring<T, W, NV, kMode, kShift>, per_thread * kLnRingThreads)) return e;
     const long long need = (p.rows + ng - 1) / ng;
     *blocks = ring_blocks(need, kShift);
+    trace_pre(st);
     ln_bwd_ring<T, W, NV, kMode, kShift><<<*blocks, threads, per_thread * threads, st>>>(p, f.threads);
+    trace_post(st, "layer_norm_bwd");
     return (int)cudaGetLastError();
 }
 template <typename T, typename W, bool kShift>
@@ -1106,15 +1114,21 @@ template <typename T, typename W, int NV, bool kWarpRow>
 int run_bwd(const LnForm& f, const LnBwd& p, int* blocks, cudaStream_t st) {
     const long long need = kWarpRow ? (p.rows + kLnWarps - 1) / kLnWarps : p.rows;
     *blocks = (int)(need < kLnBwdBlocks ? need : kLnBwdBlocks);
+    trace_pre(st);
     ln_bwd<T, W, NV, kWarpRow><<<*blocks, f.threads, 0, st>>>(p);
+    trace_post(st, "layer_norm_bwd");
     return (int)cudaGetLastError();
 }
 template <typename T, typename W, int V>
 int run_bwd_long(const LnBwd& p, int* blocks, cudaStream_t st) {
     *blocks = (int)(p.rows < kLnBwdBlocks ? p.rows : kLnBwdBlocks);  // bands of rows
+    trace_pre(st);
     ln_bwd_long<T, W, V><<<(unsigned)p.rows, kLnLongThreads, 0, st>>>(p);
+    trace_post(st, "layer_norm_bwd");
     if (const cudaError_t e = cudaGetLastError()) return (int)e;
+    trace_pre(st);
     ln_bwd_long_cols<T><<<dim3((p.H + 255) / 256, *blocks), 256, 0, st>>>(p, *blocks);
+    trace_post(st, "layer_norm_bwd_cols");
     return (int)cudaGetLastError();
 }
 template <typename T, typename W>
@@ -1153,8 +1167,10 @@ int bwd_t(const LnBwdArgs& a, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    trace_pre(st);
     const cudaError_t ce = cudaLaunchKernelEx(&cfg, ln_bwd_join<W>, (const float*)a.part, blocks, a.H,
                                               static_cast<W*>(a.dweight), static_cast<W*>(a.dbias));
+    trace_post(st, "layer_norm_bwd_join");
     return (int)(ce != cudaSuccess ? ce : cudaGetLastError());
 }
 

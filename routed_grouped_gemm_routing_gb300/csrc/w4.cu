@@ -594,7 +594,7 @@ void w4_shape(W4Args* a, int jobs, int nw, int per_sm, int nt) {
 // writes x only, so this one may start, find its job and fetch weights, while
 // that one drains (it waits before it reads x).
 template <int G, int EPI, int kNt>
-int w4_launch(W4Args a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
+int w4_launch(W4Args a, const uint8_t* q, int rows, bool after_own, const char* name, cudaStream_t st) {
     static SmemLimit limit;
     a.mask = 0x000f000fu;
     a.tiles = EPI == W4_GATED ? (a.F + 15) / 16 : (a.F + 31) / 32;
@@ -637,11 +637,13 @@ int w4_launch(W4Args a, const uint8_t* q, int rows, bool after_own, cudaStream_t
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = na;
+    trace_pre(st);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_kernel<G, EPI, kNt>, m, a);
+    trace_post(st, name);
     return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
 template <int G, int EPI>
-int w4_launch_n(const W4Args& a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
+int w4_launch_n(const W4Args& a, const uint8_t* q, int rows, bool after_own, const char* name, cudaStream_t st) {
     // More than eight rows of one matrix: two column tiles, the weights unpacked
     // once for 16 rows, where x leaves an SM 16 warps (16 rows, one or two tiles,
     // us: 16384 x 7168 G = 32 40.6 | 32.1, G = 128 34.6 | 25.6, 4096 x 4096 G =
@@ -652,15 +654,16 @@ int w4_launch_n(const W4Args& a, const uint8_t* q, int rows, bool after_own, cud
     if constexpr (EPI != W4_SLOT) {
         const bool two = rows > kR && !a.ids && (long long)a.N * a.K > (1 << 23) && a.K >= 1024 &&
                          w4_smem<G, 2>(a.K, 16, 2 * kR, 4).total <= kW4Smem;
-        if (two) return w4_launch<G, EPI, 2>(a, q, rows, after_own, st);
+        if (two) return w4_launch<G, EPI, 2>(a, q, rows, after_own, name, st);
     }
-    return w4_launch<G, EPI, 1>(a, q, rows, after_own, st);
+    return w4_launch<G, EPI, 1>(a, q, rows, after_own, name, st);
 }
 template <int EPI>
-int w4_launch_g(int G, const W4Args& a, const uint8_t* q, int rows, bool after_own, cudaStream_t st) {
-    return G == 32   ? w4_launch_n<32, EPI>(a, q, rows, after_own, st)
-           : G == 64 ? w4_launch_n<64, EPI>(a, q, rows, after_own, st)
-                     : w4_launch_n<128, EPI>(a, q, rows, after_own, st);
+int w4_launch_g(int G, const W4Args& a, const uint8_t* q, int rows, bool after_own, const char* name,
+                cudaStream_t st) {
+    return G == 32   ? w4_launch_n<32, EPI>(a, q, rows, after_own, name, st)
+           : G == 64 ? w4_launch_n<64, EPI>(a, q, rows, after_own, name, st)
+                     : w4_launch_n<128, EPI>(a, q, rows, after_own, name, st);
 }
 
 }  // namespace
@@ -676,7 +679,7 @@ int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q
     a.rows = M;
     a.xdiv = 1;
     a.out = y;
-    return w4_launch_g<W4_PLAIN>(G, a, q, M, false, st);
+    return w4_launch_g<W4_PLAIN>(G, a, q, M, false, "matvec_w4", st);
 }
 
 int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
@@ -700,7 +703,7 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     // memory, so warps.
     const long long share = w.topk_idx ? (2ll * w.T * w.k + w.E - 1) / w.E + 1 : w.T;
     const int rows = (int)(share < w.T ? share : w.T);
-    if (const int e = w4_launch_g<W4_GATED>(w.group, a, w.W1_q, rows, false, st)) return e;
+    if (const int e = w4_launch_g<W4_GATED>(w.group, a, w.W1_q, rows, false, "experts_w4_gate_up", st)) return e;
     a.x = static_cast<const __nv_bfloat16*>(w.act);
     a.sf = static_cast<const __nv_bfloat16*>(w.W2_sf);
     a.N = a.F = w.H;
@@ -708,11 +711,11 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     a.xdiv = 1;
     if (!w.topk_idx) {
         a.out = w.y;
-        return w4_launch_g<W4_PLAIN>(w.group, a, w.W2_q, rows, true, st);
+        return w4_launch_g<W4_PLAIN>(w.group, a, w.W2_q, rows, true, "experts_w4_down", st);
     }
     a.slot_w = w.topk_w;
     a.out = w.part;
-    if (const int e = w4_launch_g<W4_SLOT>(w.group, a, w.W2_q, rows, true, st)) return e;
+    if (const int e = w4_launch_g<W4_SLOT>(w.group, a, w.W2_q, rows, true, "experts_w4_down", st)) return e;
     const long long blocks = ((long long)w.T * w.H / 4 + 255) / 256;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -723,8 +726,10 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    trace_pre(st);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_combine_kernel, (const float*)w.part, w.topk_idx, w.T, w.k, w.E,
                                              w.H, static_cast<__nv_bfloat16*>(w.y));
+    trace_post(st, "experts_w4_combine");
     return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
 
@@ -732,12 +737,14 @@ int launch_quantize_w4(int E, int K, int N, int G, const void* W, uint8_t* q, vo
     const dim3 grid((N + 127) / 128, K / 128, E);
     auto* w = static_cast<const __nv_bfloat16*>(W);
     auto* s = static_cast<__nv_bfloat16*>(sf);
+    trace_pre(st);
     if (G == 32)
         w4_quantize_kernel<32><<<grid, 128, 0, st>>>(w, K, N, q, s);
     else if (G == 64)
         w4_quantize_kernel<64><<<grid, 128, 0, st>>>(w, K, N, q, s);
     else
         w4_quantize_kernel<128><<<grid, 128, 0, st>>>(w, K, N, q, s);
+    trace_post(st, "quantize_w4");
     return (int)cudaGetLastError();
 }
 
