@@ -429,9 +429,11 @@ int moe_quantize_w4(int32_t E, int32_t K, int32_t N, int32_t group, const void* 
 int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, const void* x, const uint8_t* W_q,
                   const void* W_sf, void* y, void* stream);
 
-/* Shape of moe_forward_w4: H and I multiples of 128 up to 65536, T*k <= 65535. */
+/* Shape of moe_forward_w4: H and I multiples of 128 up to 65536, T*k <= 65535;
+ * activation_clamp as moe_shape's (0: none), except that a NaN stays NaN. */
 typedef struct moe_w4_shape {
     int32_t T, H, I, E, k, group;
+    float activation_clamp;
 } moe_w4_shape;
 
 /* Bytes of moe_forward_w4's workspace.  Host only. */
@@ -440,8 +442,8 @@ int moe_w4_workspace(const moe_w4_shape* shape, size_t* bytes);
 /* The layer of moe_forward with 4-bit weights (W1 as [E, 2I, H] codes: row f
  * the gate's, row I + f the up projection's feature f; W2 as [E, H, I] codes)
  * straight from topk_idx, without routing tables: for decoding.
- *     h = x[t] W1[e]^T,  a = silu(h[:I]) h[I:] (rounded to bf16, the operand of
- *     the second product),  y[t] = sum_j topk_w[t, j] a W2[e]^T
+ *     h = x[t] W1[e]^T,  a = silu(h[:I]) h[I:] (inputs clamped as the shape
+ *     says; rounded to bf16, the operand of the second product),  y[t] = sum_j topk_w[t, j] a W2[e]^T
  * The sum over j is FP32 in slot order (deterministic).  A slot whose id is
  * outside [0, E) contributes nothing; a token with none gets 0.  topk_idx NULL
  * (E = k = 1): every token takes the one matrix with weight 1 (a shared

@@ -40,7 +40,7 @@ class MoeLayout(ctypes.Structure):
 
 
 class MoeW4Shape(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I", "E", "k", "group")]
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I", "E", "k", "group")] + [("activation_clamp", ctypes.c_float)]
 
 
 class MoeFFNShape(ctypes.Structure):

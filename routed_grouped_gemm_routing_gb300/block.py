@@ -386,10 +386,10 @@ class W4Linear:
 class W4Experts:
     """The layer's experts with 4-bit weights, for decoding: W1 codes
     [E, 2I, H // 2] (gate rows, then up rows), W2 codes [E, H, I // 2], scales
-    per ``group``.  E = 1 without routing is a shared expert.  Not
-    differentiable."""
+    per ``group``.  E = 1 without routing is a shared expert.
+    activation_clamp as in ``layer.moe_layer``.  Not differentiable."""
 
-    def __init__(self, W1_q, W1_sf, W2_q, W2_sf, group: int = 128):
+    def __init__(self, W1_q, W1_sf, W2_q, W2_sf, group: int = 128, activation_clamp: float = 0.0):
         if group not in (32, 64, 128):
             raise ValueError("group must be 32, 64 or 128")
         E, I2, half = W1_q.shape
@@ -398,20 +398,21 @@ class W4Experts:
         self.W2_q, self.W2_sf = _check_w4(W2_q, W2_sf, group, E, self.H, self.I)
         if self.W1_q.get_device() != self.W2_q.get_device():
             raise ValueError(f"W1 on cuda:{self.W1_q.get_device()} and W2 on cuda:{self.W2_q.get_device()}")
+        self.activation_clamp = float(activation_clamp)
         self._sizes = {}  # (T, k) -> shape, workspace bytes
 
     def _size(self, T, k):
         if (T, k) not in self._sizes:
-            s = B.MoeW4Shape(T, self.H, self.I, self.E, k, self.group)
+            s = B.MoeW4Shape(T, self.H, self.I, self.E, k, self.group, self.activation_clamp)
             self._sizes[T, k] = (s, ctypes.byref(s), max(B.moe_w4_workspace(s), 16))
         return self._sizes[T, k]
 
     @classmethod
-    def quantize(cls, W1, W2, group: int = 128):
+    def quantize(cls, W1, W2, group: int = 128, activation_clamp: float = 0.0):
         """From bf16 W1 [E, H, 2I] (gate | up) and W2 [E, I, H]; a shared
         expert's may lack the leading axis."""
         W1, W2 = (W if W.dim() == 3 else W.unsqueeze(0) for W in (W1, W2))
-        return cls(*quantize_w4(W1, group), *quantize_w4(W2, group), group)
+        return cls(*quantize_w4(W1, group), *quantize_w4(W2, group), group, activation_clamp)
 
     def forward(self, x, topk_idx=None, topk_w=None, out=None):
         """y bf16 [T, H] for x bf16 [T, H] and the routing (topk_idx int

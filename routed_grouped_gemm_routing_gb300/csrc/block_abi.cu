@@ -40,6 +40,7 @@ int check_w4(const moe_w4_shape* s) {
     if (s->H % 128 || s->I % 128 || s->H > kMaxW4K || s->I > kMaxW4K)
         return abi_fail(MOE_EUNSUPPORTED, "H and I must be multiples of 128, at most 65536");
     if ((long long)s->T * s->k > 65535) return abi_fail(MOE_EUNSUPPORTED, "T*k must be <= 65535");
+    if (!std::isfinite(s->activation_clamp)) return abi_fail(MOE_EINVAL, "activation_clamp must be finite");
     return check_group(s->group);
 }
 int check_ffn(const moe_ffn_shape* s) {
@@ -164,7 +165,8 @@ int moe_forward_w4(const moe_w4_shape* shape, const void* x, const uint8_t* W1_q
     uint8_t* w = static_cast<uint8_t*>(ws);
     const size_t slots = (size_t)shape->T * shape->k;
     const W4Experts a = {shape->T, shape->H, shape->I, shape->E, shape->k, shape->group, x, W1_q, W2_q, W1_sf, W2_sf,
-                         topk_idx, topk_w, w, reinterpret_cast<float*>(w + up256(slots * shape->I * 2)), y};
+                         topk_idx, topk_w, w, reinterpret_cast<float*>(w + up256(slots * shape->I * 2)), y,
+                         shape->activation_clamp > 0.0f ? shape->activation_clamp : INFINITY};
     cudaStream_t st = (cudaStream_t)stream;
     const int e = launch_experts_w4(a, st);
     return e ? abi_cuda_fail(e, "4-bit experts launch") : MOE_OK;

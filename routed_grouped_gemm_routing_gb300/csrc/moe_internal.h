@@ -137,6 +137,7 @@ struct W4Experts {
     void* act;    // bf16 [T k, I]
     float* part;  // [T k, H] (with topk_idx)
     void* y;      // bf16 [T, H]
+    float clamp;  // of the activation's inputs, INFINITY: none
 };
 int launch_matvec_w4(int M, int N, int K, int G, const void* x, const uint8_t* q, const void* sf, void* y,
                      cudaStream_t st);

@@ -39,6 +39,7 @@
 // latency of the unpacking, four warps to a scheduler.
 #include <cmath>
 
+#include "clamp.cuh"
 #include "grouped_gemm_2sm.cuh"
 #include "smem_limit.h"
 
@@ -72,6 +73,7 @@ struct W4Args {
     int ks;      // warps per tile
     int R;       // rows of a job
     int kparts;  // blocks of a cluster that split K
+    float clamp;    // W4_GATED: of gate and up, INFINITY: none
     uint32_t mask;  // 0x000f000f, unknown to the compiler (see pair128)
     const float* slot_w;  // W4_SLOT: weight of each slot
     void* out;   // W4_PLAIN, W4_GATED: bf16 [row or slot][F]; W4_SLOT: f32 [slot][F]
@@ -310,7 +312,10 @@ __global__ void __launch_bounds__(512, 1) w4_kernel(const __grid_constant__ CUte
         if constexpr (EPI == W4_SLOT) {
             reinterpret_cast<float*>(p.out)[o] = __ldg(p.slot_w + row_of[r]) * v;
         } else {
-            if constexpr (EPI == W4_GATED) v = v / (1.0f + expf(-v)) * up;
+            if constexpr (EPI == W4_GATED) {
+                v = clamp_keep_nan(v, p.clamp);
+                v = v / (1.0f + expf(-v)) * clamp_keep_nan(up, p.clamp);
+            }
             reinterpret_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
         }
     };
@@ -698,6 +703,7 @@ int launch_experts_w4(const W4Experts& w, cudaStream_t st) {
     a.busy = touched < 1.0 ? 1 : touched < a.slots ? (int)(touched + 0.5) : a.slots;
     a.xdiv = w.topk_idx ? w.k : 1;
     a.out = w.act;
+    a.clamp = w.clamp;
     // Rows that a job is made for: twice an expert's mean share of the slots,
     // and one (an expert with more has several jobs).  More would cost shared
     // memory, so warps.
