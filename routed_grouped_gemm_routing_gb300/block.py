@@ -186,12 +186,11 @@ class FFNWorkspace:
         self.saved = torch.empty(max(L.saved_bytes if train else L.h, 16), dtype=torch.uint8, device=dev)
         self.device = dev
         self.ws = self._scratch()
+        self.ws[:16].zero_()
         self.generation = 0
 
     def _scratch(self):
-        ws = torch.empty(self.layout.ws_bytes, dtype=torch.uint8, device=self.device)
-        ws[:16].zero_()
-        return ws
+        return torch.empty(self.layout.ws_bytes, dtype=torch.uint8, device=self.device)
 
     def status(self) -> int:
         """The status word (synchronises): nonzero when a kernel gave up on a bounded wait."""
@@ -296,7 +295,7 @@ class GatedFFNFunction(torch.autograd.Function):
         dy2 = dy.to(torch.bfloat16).reshape(x2.shape).contiguous()
         own = ws.ws is None
         if own:
-            ws.ws = ws._scratch()
+            ws.ws = ws._scratch()  # its status word is not cleared: nobody can read it
         dx, dW1, dW2 = _ffn_backward(dy2, x2, W1, W2, ws, _ffn_shape(ws, ctx.clamp)[0], ctx.ws_generation)
         if own:
             ws.ws = None
