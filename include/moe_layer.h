@@ -319,7 +319,10 @@ int moe_selftest_wait_timeout(const moe_shape* shape, void* route_ws, uint64_t l
  * counterpart of these entry points: the norm in front of the router and the
  * experts, the dense gated feed-forward block that runs beside them (a shared
  * expert), and both kinds of experts with 4-bit weights for serving.  The
- * conventions above hold for them too.
+ * conventions above hold for them too.  Each is deterministic for its shape,
+ * but its kernels and the order of its sums are chosen by the number of rows
+ * (and, in the norm, by alignment): the same row can differ in its last bits
+ * between batches of different sizes.
  * ---------------------------------------------------------------------- */
 
 /* Element types of the entry points that take more than one. */

@@ -10,9 +10,10 @@
 // row's, or the thread's own and joined exactly), never as E[x^2] - m^2.
 // Bound by DRAM: the forward reads x and writes y, the backward reads x and
 // dy and writes dx.  Measured at 8192 x 7168: FP32 6.1 (forward) and 6.4 TB/s
-// (backward), bf16 5.4 and 5.0 TB/s (43.3 and 70.0 us; half the bytes for the
-// same arithmetic leaves the instructions, not DRAM, as the bound), of 6.8 TB/s
-// for a plain copy.
+// (backward), bf16 5.4 and 5.0 TB/s (43.3 and 70.0 us), of 6.8 TB/s for a plain
+// copy.  The two-byte types fill neither the issue slots (54-57 %) nor DRAM
+// (51-61 % of its nominal peak): with one block of 15 or 16 warps on an SM and a
+// barrier for every row, what is left is latency.
 //
 // Three forms, by a rule on sizes, alignment and rows (ln_form, ring_pays):
 //  * ring: tensors that start on 16-byte boundaries, rows up to 1920 vectors of
@@ -1013,10 +1014,17 @@ int ln_groups(int gt, bool reducer, int* threads) {
     return ng;
 }
 // Shifted rows load their weights one by one: a group that takes few rows does
-// not earn that back.  us, ring | register form, at rows per group: forward,
-// groups of several warps 1.6: 7.4 | 10.0 (500 x 5001 bf16), 1.0: 8.4 | 6.8 (300
-// x 7161); of one warp 1.6: 5.4 | 4.9 (4000 x 333), 1.2: 9.5 | 7.5 (3000 x 777);
-// backward 1.6: 10.6 | 15.1 (4000 x 333), 1.0: 9.8 | 7.2 (777 x 1001).
+// not earn that back.  us, ring | register form, at rows per group:
+//   forward, groups of several warps: 1.0 8.4 | 6.8 (300 x 7161 bf16), 1.6 7.4 |
+//   10.0 (500 x 5001 bf16)
+//   forward, groups of one warp (2432 of them), by width:
+//      333 bf16   1.6  5.4 |  4.9   2.0  5.5 |  5.7   2.8  6.4 |  7.1   3.2  7.4 |  7.9
+//      777 bf16   1.6 10.1 |  9.6   2.0 10.7 | 12.1   2.8 13.2 | 16.1   3.2 15.2 | 18.0
+//     1001 f16    1.6 11.8 | 10.8   2.0 12.4 | 13.2   2.8 15.0 | 17.4   3.2 17.1 | 19.4
+//      251 f32    2.0  4.6 |  4.7   2.8  6.2 |  6.1   3.2  7.0 |  6.8   4.0  7.5 |  7.9
+//       33 bf16   2.0  3.2 |  1.9   3.2  4.8 |  2.7   4.0  4.8 |  2.9   6.0  6.1 |  3.8
+//   (from 333 columns on two rows would do; at 33 the register form stays ahead)
+//   backward: 1.0 9.8 | 7.2 (777 x 1001 f16), 1.6 10.6 | 15.1 (4000 x 333 bf16)
 bool ring_pays(const LnForm& f, bool reducer, long long rows, int half_rows) {
     int threads;
     return f.form != LN_RING || !f.shift || 2 * rows >= half_rows * 152ll * ln_groups(f.threads, reducer, &threads);

@@ -14,13 +14,13 @@
 // scaled and added in FP32; nothing is rounded before the output.
 //
 // mma m16n8k16: A = 16 rows of W, B = up to 8 rows of x (kNt column tiles of
-// them: 8 or 16 rows to a job).  (A tcgen05.mma would
-// need the unpacked weights in shared memory first: the unpacking through
-// registers is what has to be cheap here, and 8 columns are far below its
-// tile.)  The order of the codes in memory makes a lane's 16 bytes of a
-// 128-code block the operands of its eight products: word 4 t + j holds codes
-// 32 j + 8 t .. + 7, code 2 m in nibble m, code 2 m + 1 in nibble m + 4, so
-// that lane t's pair m of group j meets x[32 j + 8 t + 2 m, + 1].
+// them: 8 or 16 rows to a job).  (tcgen05.mma would take the unpacked weights
+// from shared memory or TMEM, one more trip from the registers that unpack them,
+// for 8 of its columns.  That form has not been built or measured.)  The order of
+// the codes in memory makes a lane's 16 bytes of a 128-code block the operands of
+// its eight products: word 4 t + j holds codes 32 j + 8 t .. + 7, code 2 m in
+// nibble m, code 2 m + 1 in nibble m + 4, so that lane t's pair m of group j meets
+// x[32 j + 8 t + 2 m, + 1].
 //
 // A block takes a job (up to 8 or 16 rows that use the same matrix) and a range
 // of tiles of 32 rows of W (W4_GATED: 16 gate rows and their 16 up rows); KS
@@ -32,9 +32,9 @@
 // took as many instructions as the products.  Scales come by plain loads, one
 // row per lane and a unit ahead, and go to the fragments by shuffles.
 //
-// Measured (the bytes at the copy rate): one row of a 131072 x 7168 matrix
-// 88.7 us, 5.3 TB/s (74); 16384 x 7168, G = 128: one row 17.2 us, 8 rows 20.3
-// (9.0); 16380 x 7168, G = 32, 12 rows 30.1 (9.8).  In the steady state 51 % of
+// Measured (the bytes at the copy rate): one row of a 131072 x 7168 matrix, G =
+// 128, 84.9 us, 5.7 TB/s (71); 16384 x 7168, G = 128: one row 17.2 us, 8 rows 20.3
+// (8.9); 16380 x 7168, G = 32, 12 rows 30.2 (9.8).  In the steady state 51 % of
 // the issue slots and 62 % of the ALU's are taken: what is left of the floor is
 // latency of the unpacking, four warps to a scheduler.
 #include <cmath>
