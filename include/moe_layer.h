@@ -404,6 +404,48 @@ int moe_ffn_forward(const moe_ffn_shape* shape, const void* x, const void* W1, c
 int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, const void* W1, const void* W2,
                      const void* saved, void* ws, void* dx, void* dW1, void* dW2, void* stream);
 
+/* A projection with what surrounds its product: for x bf16 [T, K] and W bf16
+ * [K, N]
+ *     z = x W + bias,   y = act(z) + residual
+ * activation: MOE_ACT_NONE, MOE_ACT_SILU (z sigmoid(z)), MOE_ACT_GELU (z times
+ * the normal distribution's P(X <= z)) or MOE_ACT_GELU_TANH (its tanh form, z (1
+ * + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2).  T >= 0 rows, K and N multiples
+ * of 8.  x_stride, residual_stride, dy_stride: elements between rows, multiples
+ * of 8, at least the row's length; everything else is contiguous.  All pointers
+ * are 16-byte aligned. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3 };
+typedef struct moe_linear_shape {
+    int32_t T, K, N;
+    int32_t activation;
+} moe_linear_shape;
+
+/* Bytes of the scratch of both calls (calls that share one must not overlap;
+ * nothing in it lasts from call to call but the status).  Word 0 is a status
+ * word: the caller zeroes it once; bit 0 is set when a kernel gave up on a
+ * bounded wait, and stays set.  Host only. */
+int moe_linear_workspace(const moe_linear_shape* shape, size_t* bytes);
+
+/* Forward: overwrites y bf16 [T, N], and z f32 [T, N] where it is not NULL (what
+ * the backward of an activation reads).  bias [N] of bias_type (MOE_BF16 or
+ * MOE_F32) and residual bf16 [T, N] may be NULL.  The product is bf16 with FP32
+ * accumulation; bias, activation and residual are FP32; y is rounded once.  y
+ * may be the residual itself (in place, the same stride), nothing else.
+ * Deterministic. */
+int moe_linear_forward(const moe_linear_shape* shape, const void* x, int64_t x_stride, const void* W, const void* bias,
+                       int32_t bias_type, const void* residual, int64_t residual_stride, float* z, void* ws, void* y,
+                       void* stream);
+
+/* Backward of moe_linear_forward given dy bf16 [T, N]: with dz = dy act'(z)
+ *     dx = dz W^T  bf16 [T, K]     dW = x^T dz  bf16 [K, N]     dbias = sum_rows dz  [N], bias_type
+ * overwritten; each may be NULL (not wanted; W is read for dx alone, x for dW
+ * alone).  z: the forward's, NULL without an activation.  T = 0: dW and dbias
+ * become 0.  dz is rounded to bf16 once as an operand of dx and dW; dbias sums
+ * it unrounded, in a fixed order.  The residual's gradient is dy.
+ * Deterministic. */
+int moe_linear_backward(const moe_linear_shape* shape, const void* dy, int64_t dy_stride, const void* x,
+                        int64_t x_stride, const void* W, const float* z, void* ws, void* dx, void* dW, void* dbias,
+                        int32_t bias_type, void* stream);
+
 /* 4-bit weights with one scale per group, for serving a few rows at a time
  * (decoding).  A matrix W [N, K] (y = x W^T) is held as
  *     W[n, k] = (code[n, k] - 8) * sf[n, k / group],   code in [0, 15],

@@ -51,6 +51,10 @@ class MoeFFNLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("saved_bytes", "a", "h", "ws_bytes", "status", "dh", "part")]
 
 
+class MoeLinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "activation")]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe error {code}: {msg}")
@@ -103,7 +107,11 @@ def lib():
             L.moe_ffn_workspace_layout.argtypes = [P(MoeFFNShape), P(MoeFFNLayout)]
             L.moe_ffn_forward.argtypes = [P(MoeFFNShape), vp, vp, vp, i32, vp, vp, vp, vp]
             L.moe_ffn_backward.argtypes = [P(MoeFFNShape)] + [vp] * 10
-            for n in ("moe_ffn_workspace_layout", "moe_ffn_forward", "moe_ffn_backward",
+            L.moe_linear_workspace.argtypes = [P(MoeLinearShape), P(ctypes.c_size_t)]
+            L.moe_linear_forward.argtypes = [P(MoeLinearShape), vp, i64, vp, vp, i32, vp, i64, vp, vp, vp, vp]
+            L.moe_linear_backward.argtypes = [P(MoeLinearShape), vp, i64, vp, i64] + [vp] * 6 + [i32, vp]
+            for n in ("moe_linear_workspace", "moe_linear_forward", "moe_linear_backward",
+                      "moe_ffn_workspace_layout", "moe_ffn_forward", "moe_ffn_backward",
                       "moe_layer_norm_forward", "moe_layer_norm_workspace", "moe_layer_norm_backward",
                       "moe_quantize_w4", "moe_matvec_w4", "moe_w4_workspace", "moe_forward_w4"):
                 getattr(L, n).restype = ctypes.c_int
@@ -481,6 +489,68 @@ def moe_ffn_backward(shape: MoeFFNShape, dY, x, W1, W2, saved, ws, dx, dW1, dW2,
         _arg(W1, _BF, H * 2 * I, "W1", dev), _arg(W2, _BF, I * H, "W2", dev),
         _arg(saved, _U8, L.saved_bytes, "saved", dev), _arg(ws, _U8, L.ws_bytes, "ws", dev),
         _arg(dx, _BF, T * H, "dx", dev), _arg(dW1, _BF, H * 2 * I, "dW1", dev), _arg(dW2, _BF, I * H, "dW2", dev), st)
+    if rc:
+        _check(rc)
+
+
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}  # MOE_ACT_*
+
+
+def linear_shape(T: int, K: int, N: int, activation=None) -> MoeLinearShape:
+    """Refuses a size that a C type would cut to its low bits, and an unknown activation."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    if T > 1 << 30 or K > 1 << 20 or N > 1 << 20:
+        raise MoeError(MOE_EUNSUPPORTED, "T must be <= 2^30, K and N <= 2^20")
+    return MoeLinearShape(T, K, N, ACTIVATIONS[activation])
+
+
+def moe_linear_workspace(shape: MoeLinearShape) -> int:
+    """Bytes of the linear layer's scratch (both directions)."""
+    v, ref = _size_out()
+    rc = lib().moe_linear_workspace(ctypes.byref(shape), ref)
+    if rc:
+        _check(rc)
+    return v.value
+
+
+def _bias_arg(bias, N, name, dev):
+    """(pointer, type) of a bias or its gradient."""
+    if bias is None:
+        return None, 0
+    if not isinstance(bias, torch.Tensor) or bias.dtype not in (_BF, _F32):
+        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+    return _arg(bias, bias.dtype, N, name, dev), _TYPES[bias.dtype]
+
+
+def moe_linear_forward(shape: MoeLinearShape, x, W, bias, residual, z, ws, y, stream=None):
+    """y = act(x W + bias) + residual (bf16; rows of x [T, K] and residual [T, N]
+    may be strided; bias and residual may be None); z: None, or f32 [T, N] that
+    receives x W + bias.  ws: uint8 of moe_linear_workspace elements."""
+    T, K, N = shape.T, shape.K, shape.N
+    dev, st = _here(stream)
+    px, sx = _rows_arg(x, _BF, T, K, "x", dev)
+    pr, sr = (None, 0) if residual is None else _rows_arg(residual, _BF, T, N, "residual", dev)
+    pb, tb = _bias_arg(bias, N, "bias", dev)
+    rc = lib().moe_linear_forward(
+        ctypes.byref(shape), px, sx, _arg(W, _BF, K * N, "W", dev), pb, tb, pr, sr, _arg(z, _F32, T * N, "z", dev),
+        _arg(ws, _U8, moe_linear_workspace(shape), "ws", dev), _arg(y, _BF, T * N, "y", dev), st)
+    if rc:
+        _check(rc)
+
+
+def moe_linear_backward(shape: MoeLinearShape, dy, x, W, z, ws, dx, dW, dbias, stream=None):
+    """Backward of moe_linear_forward: overwrites dx, dW (bf16) and dbias (bf16 or
+    f32), each of which may be None; z: the forward's (None without an activation)."""
+    T, K, N = shape.T, shape.K, shape.N
+    dev, st = _here(stream)
+    pd, sd = _rows_arg(dy, _BF, T, N, "dy", dev)
+    px, sx = (None, 0) if x is None else _rows_arg(x, _BF, T, K, "x", dev)
+    pb, tb = _bias_arg(dbias, N, "dbias", dev)
+    rc = lib().moe_linear_backward(
+        ctypes.byref(shape), pd, sd, px, sx, _arg(W, _BF, K * N, "W", dev), _arg(z, _F32, T * N, "z", dev),
+        _arg(ws, _U8, moe_linear_workspace(shape), "ws", dev), _arg(dx, _BF, T * K, "dx", dev),
+        _arg(dW, _BF, K * N, "dW", dev), pb, tb, st)
     if rc:
         _check(rc)
 

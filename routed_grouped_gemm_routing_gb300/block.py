@@ -317,6 +317,170 @@ def gated_ffn(x, W1, W2, workspace: FFNWorkspace | None = None, activation_clamp
     return GatedFFNFunction.apply(x, W1, W2, workspace, clamp)
 
 
+# ------------------------------------------------------------ linear layer
+@functools.lru_cache(maxsize=256)
+def _linear_plan(T, K, N, activation):
+    """(shape, reference to it, bytes of scratch)."""
+    s = B.linear_shape(T, K, N, activation)
+    return s, ctypes.byref(s), B.moe_linear_workspace(s)
+
+
+class LinearWorkspace:
+    """Scratch of one linear layer's calls, kept from step to step; calls that
+    share one must not overlap.  Without one, each call takes scratch of its own
+    whose status nobody can read."""
+
+    def __init__(self, T: int, K: int, N: int, activation=None, device=None):
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.shape = (T, K, N, activation)
+        self.ws = torch.empty(_linear_plan(*self.shape)[2], dtype=torch.uint8, device=dev)
+        self.ws[:16].zero_()
+
+    def status(self) -> int:
+        """The status word (synchronises): nonzero when a kernel gave up on a bounded wait."""
+        return int(self.ws[:4].view(torch.int32).item())
+
+
+def _linear_ws(workspace, plan_of, size, dev):
+    if workspace is None:
+        return torch.empty((size,), dtype=torch.uint8, device=dev)
+    if workspace.shape != plan_of:
+        raise ValueError(f"the workspace was made for (T, K, N, activation) = {workspace.shape}, the call has {plan_of}")
+    return workspace.ws
+
+
+def _tma_rows(t):
+    """t [rows, n] as it is where the kernels' copies can take its rows, else a contiguous copy."""
+    ok = (t.stride(1) == 1 and t.data_ptr() % 16 == 0
+          and (t.shape[0] <= 1 or (t.stride(0) % 8 == 0 and t.stride(0) >= t.shape[1])))
+    if ok:
+        return t
+    return _whole(t)
+
+
+def _whole(t):
+    """t contiguous from a 16-byte boundary on, without a copy where it is (None stays None)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _linear_dims(x, W, bias, residual, activation):
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[0]:
+        raise ValueError(f"expected x [T, K] and W [K, N], got {list(x.shape)} and {list(W.shape)}")
+    T, K, N = x.shape[0], x.shape[1], W.shape[1]
+    if bias is not None and bias.shape != (N,):
+        raise ValueError(f"expected bias [{N}], got {list(bias.shape)}")
+    if residual is not None and residual.shape != (T, N):
+        raise ValueError(f"expected residual [{T}, {N}], got {list(residual.shape)}")
+    return (T, K, N, activation), _linear_plan(T, K, N, activation)
+
+
+def linear_forward(x, W, bias=None, residual=None, activation=None, for_backward: bool = False,
+                   workspace: LinearWorkspace | None = None):
+    """(y, z) of y bf16 [T, N] = act(x W + bias) + residual for bf16 x [T, K], W
+    [K, N] (K and N multiples of 8), bias [N] bf16 or f32, residual bf16 [T, N];
+    rows of x and residual may be strided by multiples of 8.  activation: None,
+    "silu", "gelu" (with erf) or "gelu_tanh".  z = x W + bias f32 [T, N] with
+    for_backward and an activation, else None."""
+    plan_of, (s, ref, size) = _linear_dims(x, W, bias, residual, activation)
+    T, K, N, _ = plan_of
+    d = x.get_device()
+    with _on(x):
+        y = torch.empty((T, N), dtype=_BF, device=x.device)
+        z = torch.empty((T, N), dtype=_F32, device=x.device) if for_backward and activation is not None else None
+        ws = _linear_ws(workspace, plan_of, size, x.device)
+        if (_plain(x, _BF, (T, K), d) and _plain(W, _BF, (K, N), d) and ws.get_device() == d
+                and (bias is None or (bias.dtype in (_BF, _F32) and _plain(bias, bias.dtype, (N,), d)))
+                and (residual is None or _plain(residual, _BF, (T, N), d))):
+            rc = B.lib().moe_linear_forward(
+                ref, x.data_ptr(), K, W.data_ptr(), None if bias is None else bias.data_ptr(),
+                0 if bias is None else _TYPES[bias.dtype], None if residual is None else residual.data_ptr(), N,
+                None if z is None else z.data_ptr(), ws.data_ptr(), y.data_ptr(), _stream_of(d))
+            if rc:
+                B._check(rc)
+        else:
+            B.moe_linear_forward(s, x, W, bias, residual, z, ws, y)
+    return y, z
+
+
+def linear_backward(dy, x, W, z=None, bias=None, activation=None, want=(True, True),
+                    workspace: LinearWorkspace | None = None):
+    """(dx, dW, dbias) for dy bf16 [T, N], after linear_forward on the same inputs
+    (z: its second output, with for_backward; None without an activation).  dbias
+    has bias's type, None without one.  want: whether dx and dW are; None is
+    returned for one that is not.  The residual's gradient is dy."""
+    plan_of, (s, ref, size) = _linear_dims(x, W, bias, None, activation)
+    T, K, N, _ = plan_of
+    if dy.shape != (T, N):
+        raise ValueError(f"expected dy [{T}, {N}], got {list(dy.shape)}")
+    if activation is not None and (z is None or z.shape != (T, N)):
+        raise ValueError("the backward of an activation needs the forward's z (for_backward=True)")
+    d = x.get_device()
+    with _on(x):
+        dx = torch.empty((T, K), dtype=_BF, device=x.device) if want[0] else None
+        dW = torch.empty((K, N), dtype=_BF, device=x.device) if want[1] else None
+        db = None if bias is None else torch.empty((N,), dtype=bias.dtype, device=x.device)
+        ws = _linear_ws(workspace, plan_of, size, x.device)
+        if activation is None:
+            z = None
+        if (_plain(dy, _BF, (T, N), d) and _plain(x, _BF, (T, K), d) and _plain(W, _BF, (K, N), d)
+                and ws.get_device() == d and (z is None or _plain(z, _F32, (T, N), d))
+                and (db is None or bias.dtype in (_BF, _F32))):
+            rc = B.lib().moe_linear_backward(
+                ref, dy.data_ptr(), N, x.data_ptr(), K, W.data_ptr(), None if z is None else z.data_ptr(), ws.data_ptr(),
+                None if dx is None else dx.data_ptr(), None if dW is None else dW.data_ptr(),
+                None if db is None else db.data_ptr(), 0 if db is None else _TYPES[db.dtype], _stream_of(d))
+            if rc:
+                B._check(rc)
+        else:
+            B.moe_linear_backward(s, dy, x, W, z, ws, dx, dW, db)
+    return dx, dW, db
+
+
+class LinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, bias, residual, activation, workspace):
+        K, N = x.shape[-1], W.shape[-1]
+        x2, W, bias = _tma_rows(x.reshape(-1, K)), _whole(W), _whole(bias)
+        r2 = None if residual is None else _tma_rows(residual.reshape(-1, N))
+        train = any(ctx.needs_input_grad[:3])
+        y, z = linear_forward(x2, W, bias, r2, activation, train, workspace)
+        ctx.save_for_backward(x2, W, z, bias)
+        ctx.activation, ctx.workspace, ctx.x_shape = activation, workspace, x.shape
+        return y.view(*x.shape[:-1], N)
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, dy):
+        x2, W, z, bias = ctx.saved_tensors
+        nx, nW, nb, nr = ctx.needs_input_grad[:4]
+        dx = dW = db = None
+        if nx or nW or nb:
+            dy2 = _tma_rows(dy.to(torch.bfloat16).reshape(x2.shape[0], W.shape[1]))
+            dx, dW, db = linear_backward(dy2, x2, W, z, bias if nb else None, ctx.activation, (nx, nW), ctx.workspace)
+        return None if dx is None else dx.view(ctx.x_shape), dW, db, dy if nr else None, None, None
+
+
+def linear(x, W, bias=None, residual=None, activation=None, workspace: LinearWorkspace | None = None):
+    """act(x W + bias) + residual for bf16 x [..., K], W [K, N] (the layout of the
+    layer's weights; K and N multiples of 8), bias [N] bf16 or f32, residual bf16
+    [..., N]; activation as in linear_forward.  Differentiable in all four, once."""
+    if residual is not None and residual.shape != (*x.shape[:-1], W.shape[-1]):
+        raise ValueError(f"expected residual {[*x.shape[:-1], W.shape[-1]]}, got {list(residual.shape)}")
+    if not torch.is_grad_enabled():
+        return _no_grad_linear(x, W, bias, residual, activation, workspace)
+    return LinearFunction.apply(x, W, bias, residual, activation, workspace)
+
+
+def _no_grad_linear(x, W, bias, residual, activation, workspace):
+    K, N = x.shape[-1], W.shape[-1]
+    y, _ = linear_forward(_tma_rows(x.reshape(-1, K)), _whole(W), _whole(bias),
+                          None if residual is None else _tma_rows(residual.reshape(-1, N)), activation, False, workspace)
+    return y.view(*x.shape[:-1], N)
+
+
 # ---------------------------------------------------------- 4-bit weights
 def quantize_w4(W, group: int = 128):
     """(codes, scales) of W bf16 [K, N] or [E, K, N] (the layout of the layer's

@@ -53,6 +53,23 @@ int check_ffn(const moe_ffn_shape* s) {
     if (!std::isfinite(s->activation_clamp)) return abi_fail(MOE_EINVAL, "activation_clamp must be finite");
     return MOE_OK;
 }
+int check_linear(const moe_linear_shape* s) {
+    if (!s) return abi_fail(MOE_EINVAL, "shape is NULL");
+    if (s->T < 0) return abi_fail(MOE_EINVAL, "T must be >= 0");
+    if (s->K <= 0 || s->N <= 0) return abi_fail(MOE_EINVAL, "K and N must be > 0");
+    if (s->K % 8 || s->N % 8) return abi_fail(MOE_EUNSUPPORTED, "K and N must be multiples of 8");
+    if (s->T > (1 << 30) || s->K > (1 << 20) || s->N > (1 << 20))
+        return abi_fail(MOE_EUNSUPPORTED, "T must be <= 2^30, K and N <= 2^20");
+    if (s->activation < MOE_ACT_NONE || s->activation > MOE_ACT_GELU_TANH)
+        return abi_fail(MOE_EUNSUPPORTED, "activation must be one of MOE_ACT_*");
+    return MOE_OK;
+}
+// The stride of a row-strided operand of TMA copies (rows of n elements).
+int check_stride(int64_t stride, int32_t n) {
+    if (stride < n) return abi_fail(MOE_EINVAL, "strides must be at least the row's length");
+    if (stride % 8 || stride >= (1ll << 36)) return abi_fail(MOE_EUNSUPPORTED, "strides must be multiples of 8 below 2^36");
+    return MOE_OK;
+}
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
@@ -265,6 +282,92 @@ int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, 
     f.dW1 = dW1;
     f.dW2 = dW2;
     return launch_ffn_backward(*shape, f, st);
+}
+
+int moe_linear_workspace(const moe_linear_shape* shape, size_t* bytes) {
+    if (!bytes) return abi_fail(MOE_EINVAL, "bytes is NULL");
+    const int rc = check_linear(shape);
+    if (rc) return rc;
+    const LinearSizes z = linear_sizes(*shape);
+    *bytes = 256 + up256((size_t)z.part) + up256((size_t)z.dz) + up256((size_t)z.sums);
+    return MOE_OK;
+}
+
+int moe_linear_forward(const moe_linear_shape* shape, const void* x, int64_t x_stride, const void* W, const void* bias,
+                       int32_t bias_type, const void* residual, int64_t residual_stride, float* z, void* ws, void* y,
+                       void* stream) {
+    int rc = check_linear(shape);
+    if (rc) return rc;
+    if (bias && bias_type != MOE_BF16 && bias_type != MOE_F32)
+        return abi_fail(MOE_EUNSUPPORTED, "bias_type must be MOE_BF16 or MOE_F32");
+    if (shape->T == 0) return MOE_OK;
+    if (!x || !W || !ws || !y) return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    if ((rc = check_stride(x_stride, shape->K)) || (residual && (rc = check_stride(residual_stride, shape->N)))) return rc;
+    if (y == residual && residual_stride != shape->N)
+        return abi_fail(MOE_EINVAL, "in place the residual must be contiguous");
+    const void* ptrs[] = {x, W, bias, residual, z, ws, y};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    int sms = 0;
+    if ((rc = abi_select_device(ws, &sms))) return rc;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    LinearPtrs f = {};
+    f.x = x;
+    f.x_stride = x_stride;
+    f.W = W;
+    f.bias = bias;
+    f.bias_f32 = bias_type == MOE_F32;
+    f.residual = residual;
+    f.res_stride = residual_stride;
+    f.z = z;
+    f.part = reinterpret_cast<float*>(w + 256);
+    f.status = reinterpret_cast<int32_t*>(w);
+    f.y = y;
+    return launch_linear_forward(*shape, f, (cudaStream_t)stream);
+}
+
+int moe_linear_backward(const moe_linear_shape* shape, const void* dy, int64_t dy_stride, const void* x,
+                        int64_t x_stride, const void* W, const float* z, void* ws, void* dx, void* dW, void* dbias,
+                        int32_t bias_type, void* stream) {
+    int rc = check_linear(shape);
+    if (rc) return rc;
+    if (dbias && bias_type != MOE_BF16 && bias_type != MOE_F32)
+        return abi_fail(MOE_EUNSUPPORTED, "bias_type must be MOE_BF16 or MOE_F32");
+    if (!dx && !dW && !dbias) return MOE_OK;
+    const void* ptrs[] = {dy, x, W, z, ws, dx, dW, dbias};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    cudaStream_t st = (cudaStream_t)stream;
+    int sms = 0;
+    if (shape->T == 0) {
+        if (!dW && !dbias) return MOE_OK;
+        if ((rc = abi_select_device(dW ? dW : dbias, &sms))) return rc;
+        cudaError_t ce = cudaSuccess;
+        if (dW) ce = cudaMemsetAsync(dW, 0, (size_t)shape->K * shape->N * 2, st);
+        if (ce == cudaSuccess && dbias) ce = cudaMemsetAsync(dbias, 0, (size_t)shape->N * elt_size(bias_type), st);
+        return ce == cudaSuccess ? MOE_OK : abi_cuda_fail((int)ce, "zeroing gradients");
+    }
+    const bool act = shape->activation != MOE_ACT_NONE;
+    if (!dy || !ws || (dW && !x) || (dx && !W) || (act && !z)) return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    if ((rc = check_stride(dy_stride, shape->N)) || (dW && (rc = check_stride(x_stride, shape->K)))) return rc;
+    if ((rc = abi_select_device(ws, &sms))) return rc;
+    const LinearSizes sz = linear_sizes(*shape);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    LinearPtrs f = {};
+    f.dy = dy;
+    f.dy_stride = dy_stride;
+    f.x = x;
+    f.x_stride = x_stride;
+    f.W = W;
+    f.z = const_cast<float*>(z);
+    f.status = reinterpret_cast<int32_t*>(w);
+    f.dz = w + 256 + up256((size_t)sz.part);
+    f.sums = reinterpret_cast<float*>(w + 256 + up256((size_t)sz.part) + up256((size_t)sz.dz));
+    f.dx = dx;
+    f.dW = dW;
+    f.db = dbias;
+    f.db_f32 = bias_type == MOE_F32;
+    return launch_linear_backward(*shape, f, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,437 @@
+// A projection with everything around its product, forward and backward:
+//
+//   z = x W + b     y = act(z) + r
+//   dz = dy act'(z)     dx = dz W^T     dW = x^T dz     db = sum_rows dz     (dr = dy)
+//
+// 2 T K N operations forward, 4 T K N backward, bound by the tensor cores from a
+// few hundred rows on.  The products are dense_pair.cuh's (256 x 256 tiles on
+// pairs of SMs, tcgen05, operands by TMA as they lie).  The forward's epilogue
+// takes the bias from L1, fetches the residual's boxes by TMA while the tile's
+// products run, and leaves y (and for the backward z) by TMA: nothing of y is
+// read or written twice.  Few tiles: the K range is split, FP32 partial sums
+// are joined in a fixed order (linear_join).  Few rows: few_rows.cuh, every
+// weight read once.
+//
+// z stays FP32 for the backward: a rounding of z would come on top of dz's and
+// go into db without it.  dz is rounded once (an operand of dx and dW); db sums
+// the unrounded FP32 dz in a fixed order.  Without an activation dz is dy itself,
+// z is not kept and db takes one pass over dy.
+#include "dense_pair.cuh"
+#include "few_rows.cuh"
+
+namespace moe {
+
+namespace {
+
+// ---------------------------------------------------------------- forward
+struct LinearArgs {
+    DenseArgs d;
+    LinearEpi e;
+};
+
+// 32 values of the bias, columns from n on; zero past N (a multiple of 8).
+__device__ __forceinline__ void add_bias32(const LinearEpi& e, int n, int N, float (&v)[32]) {
+    if (!e.bias) return;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (n + 8 * c >= N) return;
+        if (e.bias_f32) {
+            const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + n + 8 * c);
+            const float4 lo = __ldg(b), hi = __ldg(b + 1);
+            v[8 * c] += lo.x, v[8 * c + 1] += lo.y, v[8 * c + 2] += lo.z, v[8 * c + 3] += lo.w;
+            v[8 * c + 4] += hi.x, v[8 * c + 5] += hi.y, v[8 * c + 6] += hi.z, v[8 * c + 7] += hi.w;
+        } else {
+            float f[8];
+            unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.bias) + n + 8 * c)), f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * c + j] += f[j];
+        }
+    }
+}
+
+template <int EPI>
+__device__ void linear_epilogue(const CUtensorMap* mY, const CUtensorMap* mR, const CUtensorMap* mZ, const LinearArgs& a,
+                                const DenseCta& c) {
+    constexpr bool kR = EPI == EPI_LIN_R || EPI == EPI_LIN_RZ, kZ = EPI == EPI_LIN_Z || EPI == EPI_LIN_RZ;
+    const DenseArgs& p = a.d;
+    const uint32_t out = c.boxes + c.warp * dense_boxes<EPI>() * 4096, rin = out + 4096, zout = out + (kR ? 8192 : 4096);
+    const uint32_t tempty[2] = {cluster_addr_of(c.bars.tempty(0), 0), cluster_addr_of(c.bars.tempty(1), 0)};
+    const int part = c.warp >> 2, quad = c.warp & 3, lane = c.lane;
+    int it = 0;
+    uint32_t rphase = 0;
+    for (DenseWalk<EPI> w(p); w.valid(); w.next(), ++it) {
+        const DenseItem item = w.item();
+        const int acc = it & 1, row0 = item.m0 + 128 * c.rank + 32 * quad;
+        const bool live = row0 < p.M;
+        const int last = p.width < p.N - item.n0 ? p.width : p.N - item.n0;
+        auto fetch_r = [&](int k) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(c.bars.hin(c.warp), 4096u);
+                tma_load_2d(rin, mR, item.n0 + 64 * k, row0, c.bars.hin(c.warp));
+            }
+        };
+        if (kR && live && 64 * part < last) fetch_r(part);
+        if (!warp_wait(c.bars.tfull(acc), (uint32_t)(it >> 1) & 1u, c.abort)) break;
+        tc_fence_after();
+        const uint32_t t = c.tmem + (uint32_t)(acc * 256) + ((uint32_t)(quad * 32) << 16);
+        bool ok = true;
+        if (live) {
+#pragma unroll 1
+            for (int k = part; 64 * k < last; k += 2) {
+                uint32_t res[32], pk[32];
+                if constexpr (kR) {
+                    if (!warp_wait(c.bars.hin(c.warp), rphase, c.abort)) {
+                        ok = false;
+                        break;
+                    }
+                    rphase ^= 1u;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int4 u = ld_shared_v4s(rin + lane * 128 + ((j ^ (lane & 7)) << 4));
+                        res[4 * j] = u.x, res[4 * j + 1] = u.y, res[4 * j + 2] = u.z, res[4 * j + 3] = u.w;
+                    }
+                    __syncwarp();
+                    if (64 * (k + 2) < last) fetch_r(k + 2);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[32];
+                    tmem_ld32(t + 64 * k + 32 * h, v);
+                    add_bias32(a.e, item.n0 + 64 * k + 32 * h, p.N, v);
+                    if constexpr (kZ) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                        uint32_t zb[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) zb[j] = __float_as_uint(v[j]);
+                        stage_row_sw128(zout, lane, zb);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(mZ, item.n0 + 64 * k + 32 * h, row0, zout);
+                            bulk_commit();
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float lo = act_apply(a.e.act, v[2 * j]), hi = act_apply(a.e.act, v[2 * j + 1]);
+                        if constexpr (kR) {
+                            const uint32_t r2 = res[16 * h + j];
+                            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r2));
+                            lo += f.x, hi += f.y;
+                        }
+                        pk[16 * h + j] = pack_bf16x2(lo, hi);
+                    }
+                }
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+                stage_row_sw128(out, lane, pk);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(mY, item.n0 + 64 * k, row0, out);
+                    bulk_commit();
+                }
+            }
+        }
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
+                       const __grid_constant__ CUtensorMap mY, const __grid_constant__ CUtensorMap mR,
+                       const __grid_constant__ CUtensorMap mZ, const LinearArgs a) {
+    if (threadIdx.x == 32 * kDenseWarpTma) {
+        tma_prefetch_map(&mA);
+        tma_prefetch_map(&mB);
+        tma_prefetch_map(&mY);
+        if (EPI == EPI_LIN_R || EPI == EPI_LIN_RZ) tma_prefetch_map(&mR);
+        if (EPI == EPI_LIN_Z || EPI == EPI_LIN_RZ) tma_prefetch_map(&mZ);
+    }
+    const DenseCta c = dense_begin<EPI>();
+    if (c.warp == kDenseWarpTma) {
+        if (c.lane == 0) dense_producer<KN, EPI>(&mA, &mB, a.d, c.ring, c.bars, c.abort, c.rank);
+    } else if (c.warp == kDenseWarpMma) {
+        if (c.rank == 0) {
+            dense_mma<KN, EPI>(a.d, c.ring, c.bars, c.tmem, c.abort);
+            dense_drain(c);
+        }
+    } else {
+        linear_epilogue<EPI>(&mY, &mR, &mZ, a, c);
+    }
+    dense_end(c, a.d.status);
+}
+
+// The sum of the K ranges' partial sums [splits][T][N] in order and the layer's
+// epilogue, eight columns per thread.
+__global__ void __launch_bounds__(128)
+    linear_join_kernel(const float* part, long long rows, int N, int splits, const LinearEpi e, __nv_bfloat16* y) {
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    const int per = N / 8;
+    const long long total = rows * per;
+    const size_t stride = (size_t)rows * N;
+    for (long long i = (long long)blockIdx.x * 128 + threadIdx.x; i < total; i += (long long)gridDim.x * 128) {
+        const long long row = i / per;
+        const int c = (int)(i - row * per) * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        const float* src = part + (size_t)row * N + c;
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) {
+            const float4 a = *reinterpret_cast<const float4*>(src + s * stride);
+            const float4 b = *(reinterpret_cast<const float4*>(src + s * stride) + 1);
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = e.finish(v[j], row, c + j, N);
+        *reinterpret_cast<uint4*>(y + (size_t)row * N + c) = pack8(v);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// dz of dy and z, and each block's column sums of it (part [gridDim.y][N]), or
+// db itself from a single row of blocks.  A lane takes eight columns, a warp
+// every eighth row of the block's.
+struct DzArgs {
+    const __nv_bfloat16* dy;
+    long long dy_stride, rows;
+    int N, per;  // rows of a block
+    const float* z;
+    __nv_bfloat16* dz;  // null: not wanted (no activation)
+    float* part;        // null: no db
+    void* db;           // with a single row of blocks
+    int db_f32;
+};
+constexpr int kDzWarps = 8;
+
+__device__ __forceinline__ void store_db(void* db, int f32, int n, float v) {
+    if (f32)
+        static_cast<float*>(db)[n] = v;
+    else
+        static_cast<__nv_bfloat16*>(db)[n] = __float2bfloat16_rn(v);
+}
+
+template <int kAct>
+__global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const DzArgs p) {
+    __shared__ float red[kDzWarps][256];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * lane;
+    const long long r0 = (long long)blockIdx.y * p.per, r1 = r0 + p.per < p.rows ? r0 + p.per : p.rows;
+    float sum[8] = {};
+    if (n < p.N) {
+#pragma unroll 2
+        for (long long r = r0 + warp; r < r1; r += kDzWarps) {
+            float d[8];
+            unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.dy + r * p.dy_stride + n)), d);
+            if constexpr (kAct != MOE_ACT_NONE) {
+                const float4* zp = reinterpret_cast<const float4*>(p.z + (size_t)r * p.N + n);
+                const float4 a = __ldg(zp), b = __ldg(zp + 1);
+                const float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] *= act_slope<kAct>(z[j]);
+                *reinterpret_cast<uint4*>(p.dz + (size_t)r * p.N + n) = pack8(d);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += d[j];
+        }
+    }
+    if (!p.part && !p.db) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[warp][8 * lane + j] = sum[j];
+    __syncthreads();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= p.N) return;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kDzWarps; ++w) v += red[w][threadIdx.x];
+    if (gridDim.y == 1)
+        store_db(p.db, p.db_f32, c, v);
+    else
+        p.part[(size_t)blockIdx.y * p.N + c] = v;
+}
+
+// db from the blocks' sums, in order.  32 columns a block, eight threads a column.
+__global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int parts, int N, void* db, int db_f32) {
+    __shared__ float red[8][32];
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    float v = 0.0f;
+    if (c < N)
+#pragma unroll 4
+        for (int i = w; i < parts; i += 8) v += part[(size_t)i * N + c];
+    red[w][threadIdx.x & 31] = v;
+    __syncthreads();
+    if (w || c >= N) return;
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += red[i][threadIdx.x];
+    store_db(db, db_f32, c, v);
+}
+
+// Rows of blocks of linear_dz_kernel: six blocks for an SM, 16 rows each at least.
+int dz_parts(long long T, int N) {
+    const long long cols = cdiv(N, 256), want = (6 * 152 + cols - 1) / cols, most = (T + 15) / 16;
+    const long long n = want < most ? want : most;
+    return (int)(n < 1 ? 1 : n);
+}
+
+// Launches a kernel that starts while the one before it (of the same call) ends.
+template <typename K, typename... A>
+int launch_after(K kernel, dim3 grid, int threads, const char* name, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    trace_pre(st);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    trace_post(st, name);
+    return (int)(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+template <int EPI>
+int launch_linear_pair(const LinearArgs& a, const CUtensorMap (&m)[5], cudaStream_t st) {
+    static std::atomic<int> fits[kMaxDevices] = {};
+    return launch_pairs(linear_pair_kernel<EPI>, fits, dense_smem<EPI>(), (long long)a.d.tiles_m * a.d.tiles_n, true,
+                        "linear", st, m[0], m[1], m[2], m[3], m[4], a);
+}
+
+// Sixteen rows a job from nine rows on, where the matrix is large (ffn_few.cu's measurements).
+bool linear_two(const moe_linear_shape& s) { return s.T > 8 && (long long)s.K * s.N > (1 << 20); }
+bool linear_few(const moe_linear_shape& s) {
+    const int per = linear_two(s) ? 16 : 8;
+    return s.T <= 16 || (s.T <= 128 && (long long)((s.T + per - 1) / per) * ((s.N + 63) / 64) <= 200);
+}
+Product linear_product(const moe_linear_shape& s) { return {s.T, s.N, s.K, false}; }
+
+}  // namespace
+
+LinearSizes linear_sizes(const moe_linear_shape& s) {
+    LinearSizes z = {0, 0, 0};
+    if (s.T == 0) return z;
+    z.part = linear_few(s) ? 0 : linear_product(s).part_bytes();
+    z.dz = s.activation == MOE_ACT_NONE ? 0 : (long long)s.T * s.N * 2;
+    const int parts = dz_parts(s.T, s.N);
+    z.sums = parts > 1 ? (long long)parts * s.N * 4 : 0;
+    return z;
+}
+
+int launch_linear_forward(const moe_linear_shape& s, const LinearPtrs& f, cudaStream_t st) {
+    int rc, e;
+    const LinearEpi epi = {s.activation, f.bias_f32, f.bias, static_cast<const __nv_bfloat16*>(f.residual), f.res_stride, f.z};
+    if (linear_few(s)) {
+        const bool two = linear_two(s);
+        CUtensorMap w, x;
+        if ((rc = abi_map_2d(&w, f.W, 2, s.K, s.N, s.N, 64, 32, "W"))) return rc;
+        if ((rc = abi_map_2d(&x, f.x, 2, s.T, s.K, f.x_stride, 32, two ? 16 : 8, "x"))) return rc;
+        const FewArgs a = {s.T, s.K, s.N, 0, 0, INFINITY, static_cast<__nv_bfloat16*>(f.y), nullptr, f.status, epi};
+        e = two ? launch_few<FEW_LINEAR, 2>(a, w, x, false, "linear_few", st)
+                : launch_few<FEW_LINEAR, 1>(a, w, x, false, "linear_few", st);
+        return e ? abi_cuda_fail(e, "linear launch") : MOE_OK;
+    }
+    const Product q = linear_product(s);
+    LinearArgs a = {q.args(INFINITY, f.status), epi};
+    CUtensorMap m[5] = {};  // x, W, y, residual, z
+    if ((rc = abi_map_2d(&m[0], f.x, 2, s.T, s.K, f.x_stride, 64, 128, "x"))) return rc;
+    if ((rc = map_op(&m[1], f.W, s.K, s.N, 64, "W"))) return rc;
+    if (a.d.splits > 1) {
+        DenseMaps d = {m[0], m[1], {}, {}};
+        if ((rc = abi_map_nd(&d.c0, f.part, 4, {s.N, 1, s.T, a.d.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
+        e = launch_dense<KN, EPI_PART>(a.d, d, "linear", st, true);
+        const long long blocks = ((long long)s.T * (s.N / 8) + 127) / 128;
+        if (!e)
+            e = launch_after(linear_join_kernel, dim3((unsigned)(blocks < 2432 ? blocks : 2432)), 128, "linear_join", st,
+                             static_cast<const float*>(f.part), (long long)s.T, s.N, a.d.splits, epi,
+                             static_cast<__nv_bfloat16*>(f.y));
+        return e ? abi_cuda_fail(e, "linear launch") : MOE_OK;
+    }
+    if ((rc = map_op(&m[2], f.y, s.T, s.N, 32, "y (store)"))) return rc;
+    if (f.residual && (rc = abi_map_2d(&m[3], f.residual, 2, s.T, s.N, f.res_stride, 64, 32, "residual"))) return rc;
+    if (f.z && (rc = abi_map_2d(&m[4], f.z, 4, s.T, s.N, s.N, 32, 32, "z (store)"))) return rc;
+    e = f.residual ? (f.z ? launch_linear_pair<EPI_LIN_RZ>(a, m, st) : launch_linear_pair<EPI_LIN_R>(a, m, st))
+                   : (f.z ? launch_linear_pair<EPI_LIN_Z>(a, m, st) : launch_linear_pair<EPI_LIN>(a, m, st));
+    return e ? abi_cuda_fail(e, "linear launch") : MOE_OK;
+}
+
+int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaStream_t st) {
+    int rc, e = 0;
+    const void* dz = f.dy;
+    long long dz_stride = f.dy_stride;
+    const int parts = dz_parts(s.T, s.N);
+    const bool grads = f.dx || f.dW, act = s.activation != MOE_ACT_NONE;
+    if ((act && grads) || f.db) {
+        DzArgs a = {static_cast<const __nv_bfloat16*>(f.dy), f.dy_stride, s.T, s.N, (s.T + parts - 1) / parts, f.z,
+                    static_cast<__nv_bfloat16*>(f.dz), f.db && parts > 1 ? f.sums : nullptr, parts > 1 ? nullptr : f.db,
+                    f.db_f32};
+        const dim3 grid(cdiv(s.N, 256), parts);
+        trace_pre(st);
+        switch (s.activation) {
+            case MOE_ACT_SILU: linear_dz_kernel<MOE_ACT_SILU><<<grid, 32 * kDzWarps, 0, st>>>(a); break;
+            case MOE_ACT_GELU: linear_dz_kernel<MOE_ACT_GELU><<<grid, 32 * kDzWarps, 0, st>>>(a); break;
+            case MOE_ACT_GELU_TANH: linear_dz_kernel<MOE_ACT_GELU_TANH><<<grid, 32 * kDzWarps, 0, st>>>(a); break;
+            default: linear_dz_kernel<MOE_ACT_NONE><<<grid, 32 * kDzWarps, 0, st>>>(a); break;
+        }
+        trace_post(st, "linear_dz");
+        if ((e = (int)cudaGetLastError())) return abi_cuda_fail(e, "linear dz launch");
+        if (act) dz = f.dz, dz_stride = s.N;
+        if (f.db && parts > 1) {
+            e = launch_after(linear_db_kernel, dim3(cdiv(s.N, 32)), 256, "linear_db", st, static_cast<const float*>(f.sums),
+                             parts, s.N, f.db, f.db_f32);
+            if (e) return abi_cuda_fail(e, "linear bias gradient launch");
+        }
+    }
+    if (!grads) return MOE_OK;
+    // dW = x^T dz, dx = dz W^T: the deeper product first
+    struct {
+        Product q;
+        bool mn;  // both operands lie along the output
+        const void *A, *B;
+        void* D;
+        long long a_stride, b_stride;
+    } job[2] = {{{s.K, s.N, s.T, false, false}, true, f.x, dz, f.dW, f.x_stride, dz_stride},
+                {{s.T, s.K, s.N, false, false}, false, dz, f.W, f.dx, dz_stride, s.N}};
+    if (s.N > s.T) {
+        const auto t = job[0];
+        job[0] = job[1];
+        job[1] = t;
+    }
+    Product qs[2];
+    int n = 0;
+    for (const auto& j : job)
+        if (j.D) qs[n++] = j.q;
+    const int width = joint_width(qs, n);
+    PlainMaps m = {};
+    PlainArgs a = {};
+    a.n = n;
+    a.status = f.status;
+    int i = 0;
+    for (const auto& j : job) {
+        if (!j.D) continue;
+        a.p[i] = plain(j.q, width, j.mn, j.mn);
+        if ((rc = j.mn ? abi_map_2d(&m.m[3 * i], j.A, 2, j.q.K, j.q.M, j.a_stride, 64, 64, "A (MN-major)")
+                       : abi_map_2d(&m.m[3 * i], j.A, 2, j.q.M, j.q.K, j.a_stride, 64, 128, "A")))
+            return rc;
+        if ((rc = j.mn ? abi_map_2d(&m.m[3 * i + 1], j.B, 2, j.q.K, j.q.N, j.b_stride, 64, 64, "B (MN-major)")
+                       : abi_map_2d(&m.m[3 * i + 1], j.B, 2, j.q.N, j.q.K, j.b_stride, 64, width / 2, "B")))
+            return rc;
+        if ((rc = map_op(&m.m[3 * i + 2], j.D, j.q.M, j.q.N, 32, "gradient (store)"))) return rc;
+        ++i;
+    }
+    e = launch_plain(a, m, "linear_grads", st);
+    return e ? abi_cuda_fail(e, "linear gradient launch") : MOE_OK;
+}
+
+}  // namespace moe

@@ -1,0 +1,68 @@
+// What the linear layer does to its product: bias, activation, residual; and the
+// activations' slopes for its backward.
+//
+//   z = x W + b      y = act(z) + r      dz = dy act'(z)
+//   silu       z sig(z)              sig (1 + z (1 - sig))
+//   gelu       z Phi(z)              Phi + z phi(z)           Phi, phi: of N(0, 1)
+//   gelu_tanh  z sig(2 u)            sig + 2 z u' sig (1 - sig)
+//              u = sqrt(2 / pi) (z + 0.044715 z^3)   (z (1 + tanh u) / 2)
+// All in FP32; the results are rounded once.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+
+// 1 / (1 + e^-v) within a few units of 2^-23.
+__device__ __forceinline__ float sigmoid_fast(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+// P(N(0, 1) <= z); through erfc, whose tail keeps its relative precision.
+__device__ __forceinline__ float normal_below(float z) { return 0.5f * erfcf(-0.70710678f * z); }
+
+__device__ __forceinline__ float act_apply(int act, float z) {
+    if (act == MOE_ACT_SILU) return z * sigmoid_fast(z);
+    if (act == MOE_ACT_GELU) return z * normal_below(z);
+    if (act == MOE_ACT_GELU_TANH) return z * sigmoid_fast(1.5957691f * z * (1.0f + 0.044715f * z * z));
+    return z;
+}
+template <int kAct>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (kAct == MOE_ACT_SILU) {
+        const float s = sigmoid_fast(z);
+        return s + z * s * (1.0f - s);
+    } else if constexpr (kAct == MOE_ACT_GELU) {
+        const float e = __expf(-0.5f * z * z);
+        return normal_below(z) + (e > 0.0f ? z * (0.39894228f * e) : 0.0f);
+    } else if constexpr (kAct == MOE_ACT_GELU_TANH) {
+        const float s = sigmoid_fast(1.5957691f * z * (1.0f + 0.044715f * z * z)), q = s * (1.0f - s);
+        // far out q is 0 and the polynomial may be infinite
+        return q > 0.0f ? s + z * q * (1.5957691f * (1.0f + 0.134145f * z * z)) : s;
+    } else {
+        return 1.0f;
+    }
+}
+
+struct LinearEpi {
+    int act;             // MOE_ACT_*
+    int bias_f32;        // bias: FP32, or bf16
+    const void* bias;    // [F] or null
+    const __nv_bfloat16* residual;  // [T][F], rows res_stride apart, or null
+    long long res_stride;
+    float* z;  // [T][F] or null
+    __device__ __forceinline__ float bias_at(int f) const {
+        if (!bias) return 0.0f;
+        return bias_f32 ? __ldg(static_cast<const float*>(bias) + f)
+                        : __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[f]);
+    }
+    // One element from its product.
+    __device__ __forceinline__ float finish(float v, size_t row, int f, int F) const {
+        v += bias_at(f);
+        if (z) z[row * F + f] = v;
+        v = act_apply(act, v);
+        return residual ? v + __bfloat162float(residual[row * res_stride + f]) : v;
+    }
+};
+
+}  // namespace moe

@@ -162,6 +162,25 @@ int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t s
 bool ffn_few_takes(const moe_ffn_shape& s);
 int launch_ffn_few(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
 
+// ------------------------------------------------------------ linear layer
+struct LinearPtrs {
+    const void *x, *W, *bias, *residual, *dy;
+    long long x_stride, res_stride, dy_stride;
+    int bias_f32, db_f32;
+    float *z, *part, *sums;
+    void *dz, *y, *dx, *dW, *db;
+    int32_t* status;
+};
+// Bytes of the workspace's parts: partial sums of the forward's K ranges, dz, and
+// the partial column sums of db.
+struct LinearSizes {
+    long long part, dz, sums;
+};
+LinearSizes linear_sizes(const moe_linear_shape& s);
+// MOE_OK or an error code with its message set.
+int launch_linear_forward(const moe_linear_shape& s, const LinearPtrs& f, cudaStream_t st);
+int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaStream_t st);
+
 // Layout of the three workspaces (host only).
 int compute_layout(const moe_shape* s, moe_layout* L);
 
