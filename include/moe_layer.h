@@ -362,6 +362,53 @@ int moe_layer_norm_backward(int64_t rows, int32_t H, int32_t x_type, int32_t w_t
                             const float* mean, const float* rstd, void* dx, void* dweight, void* dbias, void* ws,
                             void* stream);
 
+/* The joint between two halves of a block: the first half's output o is normed
+ * (post), gated and added to the residual stream r, and the stream is normed for
+ * the second half.  For each row
+ *     u = N(o) post_weight + post_bias      (post_weight NULL: u = o)
+ *     s = residual_scale r + gate u         n = N(s) weight + bias
+ *     N(v) = (v - m) / sqrt(mean (v - m)^2 + eps),  m = mean v (MOE_NORM_LAYER) or 0 (MOE_NORM_RMS)
+ * x_type: type of o, r, s, n and their gradients; w_type: of the parameters and
+ * the gate, MOE_F32 or x_type.  gate: MOE_GATE_NONE, MOE_GATE_CHANNEL ([H]) or
+ * MOE_GATE_TOKEN ([rows]).  0 <= rows < 2^31, 1 <= H <= 2^24.  Strides: elements
+ * between the starts of two rows, at least H; the last axis and everything
+ * without a stride are contiguous.  Pointers need their element's alignment
+ * (16-byte vectors are used where addresses, strides and H allow).  Everything
+ * between the roundings of s and n is FP32; n comes from the unrounded s.  A row
+ * with a NaN or an infinity gives NaN where the formula does. */
+enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 };
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+typedef struct moe_residual_norm_shape {
+    int64_t rows;
+    int32_t H, x_type, w_type, kind, gate;
+    float residual_scale, eps;
+} moe_residual_norm_shape;
+
+/* Forward: overwrites stream (s) and normed (n) [rows, H], and stats f32[4 rows]
+ * (m and 1 / sqrt of o, then of s; the backward reads them).  post_bias needs
+ * post_weight; post_weight, post_bias and bias may be NULL.  stream may be the
+ * residual itself (contiguous: inference in place), nothing else overlaps. */
+int moe_residual_norm_forward(const moe_residual_norm_shape* shape, const void* out, int64_t out_stride,
+                              const void* residual, int64_t residual_stride, const void* gate, const void* post_weight,
+                              const void* post_bias, const void* weight, const void* bias, void* stream_out,
+                              void* normed, float* stats, void* stream);
+
+/* Bytes of the backward's workspace.  Host only. */
+int moe_residual_norm_workspace(const moe_residual_norm_shape* shape, size_t* bytes);
+
+/* Backward given the gradients of s and n (dstream, dnormed [rows, H]; NULL:
+ * zero) and the forward's inputs and stats: overwrites dout and dresidual
+ * [rows, H], contiguous, and those of dweight, dbias, dpost_weight, dpost_bias
+ * ([H], w_type) and dgate ([H] or [rows], w_type) that are not NULL (rows = 0:
+ * the [H] ones become 0).  ws: moe_residual_norm_workspace bytes, 16-byte
+ * aligned.  Sums are FP32 in a fixed order: deterministic, no atomics. */
+int moe_residual_norm_backward(const moe_residual_norm_shape* shape, const void* dstream, int64_t dstream_stride,
+                               const void* dnormed, int64_t dnormed_stride, const void* out, int64_t out_stride,
+                               const void* residual, int64_t residual_stride, const void* gate, const void* post_weight,
+                               const void* post_bias, const void* weight, const float* stats, void* ws, void* dout,
+                               void* dresidual, void* dweight, void* dbias, void* dpost_weight, void* dpost_bias,
+                               void* dgate, void* stream);
+
 /* The dense gated feed-forward block, beside the routed experts (a shared
  * expert) or in a layer without them: for x bf16 [T, H], W1 bf16 [H, 2I]
  * (columns [0, I) gate, [I, 2I) up) and W2 bf16 [I, H]

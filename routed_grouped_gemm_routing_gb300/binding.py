@@ -55,6 +55,11 @@ class MoeLinearShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "activation")]
 
 
+class MoeResidualNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("H", "x_type", "w_type", "kind", "gate")] + [
+        ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe error {code}: {msg}")
@@ -110,7 +115,12 @@ def lib():
             L.moe_linear_workspace.argtypes = [P(MoeLinearShape), P(ctypes.c_size_t)]
             L.moe_linear_forward.argtypes = [P(MoeLinearShape), vp, i64, vp, vp, i32, vp, i64, vp, vp, vp, vp]
             L.moe_linear_backward.argtypes = [P(MoeLinearShape), vp, i64, vp, i64] + [vp] * 6 + [i32, vp]
-            for n in ("moe_linear_workspace", "moe_linear_forward", "moe_linear_backward",
+            RN = P(MoeResidualNormShape)
+            L.moe_residual_norm_forward.argtypes = [RN, vp, i64, vp, i64] + [vp] * 9
+            L.moe_residual_norm_workspace.argtypes = [RN, P(ctypes.c_size_t)]
+            L.moe_residual_norm_backward.argtypes = [RN] + [vp, i64] * 4 + [vp] * 14
+            for n in ("moe_residual_norm_forward", "moe_residual_norm_workspace", "moe_residual_norm_backward",
+                      "moe_linear_workspace", "moe_linear_forward", "moe_linear_backward",
                       "moe_ffn_workspace_layout", "moe_ffn_forward", "moe_ffn_backward",
                       "moe_layer_norm_forward", "moe_layer_norm_workspace", "moe_layer_norm_backward",
                       "moe_quantize_w4", "moe_matvec_w4", "moe_w4_workspace", "moe_forward_w4"):
@@ -489,6 +499,81 @@ def moe_ffn_backward(shape: MoeFFNShape, dY, x, W1, W2, saved, ws, dx, dW1, dW2,
         _arg(W1, _BF, H * 2 * I, "W1", dev), _arg(W2, _BF, I * H, "W2", dev),
         _arg(saved, _U8, L.saved_bytes, "saved", dev), _arg(ws, _U8, L.ws_bytes, "ws", dev),
         _arg(dx, _BF, T * H, "dx", dev), _arg(dW1, _BF, H * 2 * I, "dW1", dev), _arg(dW2, _BF, I * H, "dW2", dev), st)
+    if rc:
+        _check(rc)
+
+
+NORM_KINDS = {"layer": 0, "rms": 1}  # MOE_NORM_*
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
+RESIDUAL_NORM_MAX_H = 1 << 24
+
+
+def residual_norm_shape(rows, H, x_dtype, w_dtype, kind="layer", gate=GATE_NONE, residual_scale=1.0, eps=1e-5):
+    """Refuses what the library would, before a C type cuts a size to its low bits."""
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind must be one of {list(NORM_KINDS)}, got {kind!r}")
+    for t, n in ((x_dtype, "x"), (w_dtype, "the parameters")):
+        if t not in _TYPES:
+            raise TypeError(f"{n} must be bfloat16, float16 or float32, got {t}")
+    if H > RESIDUAL_NORM_MAX_H:
+        raise MoeError(MOE_EINVAL, "H must be in [1, 2^24]")
+    return MoeResidualNormShape(rows, H, _TYPES[x_dtype], _TYPES[w_dtype], NORM_KINDS[kind], gate, residual_scale, eps)
+
+
+def moe_residual_norm_workspace(shape: MoeResidualNormShape) -> int:
+    """Bytes of moe_residual_norm_backward's workspace."""
+    v, ref = _size_out()
+    rc = lib().moe_residual_norm_workspace(ctypes.byref(shape), ref)
+    if rc:
+        _check(rc)
+    return v.value
+
+
+def _gate_numel(shape):
+    return shape.H if shape.gate == GATE_CHANNEL else shape.rows
+
+
+def moe_residual_norm_forward(shape: MoeResidualNormShape, out, residual, gate, post_weight, post_bias, weight, bias,
+                              stream_out, normed, stats, stream=None):
+    """stream = residual_scale residual + gate (norm(out) post_weight + post_bias),
+    normed = norm(stream) weight + bias over [rows, H] (rows of out and residual
+    may be strided); gate, post_weight, post_bias and bias may be None.  stats
+    f32 [4, rows]."""
+    dev, st = _here(stream)
+    rows, H, xt, wt = shape.rows, shape.H, out.dtype, weight.dtype
+    po, so = _rows_arg(out, xt, rows, H, "out", dev)
+    pr, sr = _rows_arg(residual, xt, rows, H, "residual", dev)
+    rc = lib().moe_residual_norm_forward(
+        ctypes.byref(shape), po, so, pr, sr, _arg(gate, wt, _gate_numel(shape), "gate", dev),
+        _arg(post_weight, wt, H, "post_weight", dev), _arg(post_bias, wt, H, "post_bias", dev),
+        _arg(weight, wt, H, "weight", dev), _arg(bias, wt, H, "bias", dev), _arg(stream_out, xt, rows * H, "stream", dev),
+        _arg(normed, xt, rows * H, "normed", dev), _arg(stats, _F32, 4 * rows, "stats", dev), st)
+    if rc:
+        _check(rc)
+
+
+def moe_residual_norm_backward(shape: MoeResidualNormShape, dstream, dnormed, out, residual, gate, post_weight,
+                               post_bias, weight, stats, ws, dout, dresidual, dweight, dbias, dpost_weight, dpost_bias,
+                               dgate, stream=None):
+    """Backward of moe_residual_norm_forward: overwrites dout and dresidual
+    [rows, H] and those parameters' gradients that are not None; dstream or
+    dnormed None: zero.  ws: uint8 of moe_residual_norm_workspace elements."""
+    dev, st = _here(stream)
+    rows, H, xt, wt = shape.rows, shape.H, out.dtype, weight.dtype
+
+    def strided(t, name):
+        return (None, 0) if t is None else _rows_arg(t, xt, rows, H, name, dev)
+
+    n = _gate_numel(shape)
+    rc = lib().moe_residual_norm_backward(
+        ctypes.byref(shape), *strided(dstream, "dstream"), *strided(dnormed, "dnormed"), *strided(out, "out"),
+        *strided(residual, "residual"), _arg(gate, wt, n, "gate", dev), _arg(post_weight, wt, H, "post_weight", dev),
+        _arg(post_bias, wt, H, "post_bias", dev), _arg(weight, wt, H, "weight", dev),
+        _arg(stats, _F32, 4 * rows, "stats", dev), _arg(ws, _U8, moe_residual_norm_workspace(shape), "ws", dev),
+        _arg(dout, xt, rows * H, "dout", dev), _arg(dresidual, xt, rows * H, "dresidual", dev),
+        _arg(dweight, wt, H, "dweight", dev), _arg(dbias, wt, H, "dbias", dev),
+        _arg(dpost_weight, wt, H, "dpost_weight", dev), _arg(dpost_bias, wt, H, "dpost_bias", dev),
+        _arg(dgate, wt, n, "dgate", dev), st)
     if rc:
         _check(rc)
 

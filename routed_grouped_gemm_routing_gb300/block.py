@@ -169,6 +169,115 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5):
     return LayerNormFunction.apply(x, weight, bias, float(eps))
 
 
+# ---------------------------------------------------------- residual joint
+def _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate):
+    """(rows, H, gate kind) of a call."""
+    if out.dim() != 2 or out.shape != residual.shape:
+        raise ValueError(f"expected out and residual [rows, H], got {list(out.shape)} and {list(residual.shape)}")
+    rows, H = out.shape
+    for t, n in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias")):
+        if t is not None and t.shape != (H,):
+            raise ValueError(f"expected {n} [{H}], got {list(t.shape)}")
+    if post_bias is not None and post_weight is None:
+        raise ValueError("post_bias without post_weight")
+    if gate is None:
+        return rows, H, B.GATE_NONE
+    if gate.shape == (H,):
+        return rows, H, B.GATE_CHANNEL
+    if gate.shape != (rows, 1):
+        raise ValueError(f"expected gate [{H}] (per channel) or [{rows}, 1] (per token), got {list(gate.shape)}")
+    return rows, H, B.GATE_TOKEN
+
+
+def residual_norm_forward(out, residual, weight, bias=None, post_weight=None, post_bias=None, gate=None,
+                          residual_scale: float = 1.0, eps: float = 1e-5, kind: str = "layer"):
+    """(stream, normed, stats) of
+        stream = residual_scale residual + gate (norm(out) post_weight + post_bias)
+        normed = norm(stream) weight + bias
+    for out and residual [rows, H] (bf16, f16 or f32; rows may be strided).
+    norm: a layer norm, or with kind "rms" without its means.  Without post_weight
+    out goes in as it is.  gate: [H] per channel, [rows, 1] per token, or None.
+    Parameters and gate in out's type or all f32.  stats (f32 [4, rows]) is what
+    residual_norm_backward reads."""
+    rows, H, gk = _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate)
+    s = B.residual_norm_shape(rows, H, out.dtype, weight.dtype, kind, gk, residual_scale, eps)
+    with _on(out):
+        dev = out.device
+        stream = torch.empty((rows, H), dtype=out.dtype, device=dev)
+        normed = torch.empty((rows, H), dtype=out.dtype, device=dev)
+        stats = torch.empty((4, rows), dtype=_F32, device=dev)
+        B.moe_residual_norm_forward(s, out, residual, gate, post_weight, post_bias, weight, bias, stream, normed, stats)
+    return stream, normed, stats
+
+
+def residual_norm_backward(dstream, dnormed, out, residual, weight, stats, bias=None, post_weight=None, post_bias=None,
+                           gate=None, residual_scale: float = 1.0, kind: str = "layer"):
+    """(dout, dresidual, dweight, dbias, dpost_weight, dpost_bias, dgate) for the
+    gradients of both outputs (either may be None), after residual_norm_forward
+    on the same arguments; None for a parameter that is not there."""
+    rows, H, gk = _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate)
+    for t, n in ((dstream, "dstream"), (dnormed, "dnormed")):
+        if t is not None and t.shape != (rows, H):
+            raise ValueError(f"expected {n} [{rows}, {H}], got {list(t.shape)}")
+    if stats.shape != (4, rows):
+        raise ValueError(f"expected the forward's stats [4, {rows}], got {list(stats.shape)}")
+    s = B.residual_norm_shape(rows, H, out.dtype, weight.dtype, kind, gk, residual_scale)
+    with _on(out):
+        dev = out.device
+        dout = torch.empty((rows, H), dtype=out.dtype, device=dev)
+        dres = torch.empty((rows, H), dtype=out.dtype, device=dev)
+        dw, db, dpw, dpb, dg = (None if p is None else torch.empty(p.shape, dtype=weight.dtype, device=dev)
+                                for p in (weight, bias, post_weight, post_bias, gate))
+        ws = torch.empty((max(B.moe_residual_norm_workspace(s), 16),), dtype=torch.uint8, device=dev)
+        B.moe_residual_norm_backward(s, dstream, dnormed, out, residual, gate, post_weight, post_bias, weight, stats, ws,
+                                     dout, dres, dw, db, dpw, dpb, dg)
+    return dout, dres, dw, db, dpw, dpb, dg
+
+
+class ResidualNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, out, residual, weight, bias, post_weight, post_bias, gate, residual_scale, eps, kind):
+        ctx.set_materialize_grads(False)
+        H = out.shape[-1]
+        o2, r2 = _rows_of(out, H), _rows_of(residual, H)
+        params = [None if p is None else p.contiguous() for p in (weight, bias, post_weight, post_bias)]
+        g2 = gate if gate is None or gate.dim() == 1 else gate.reshape(-1, 1)
+        g2 = None if g2 is None else g2.contiguous()
+        stream, normed, stats = residual_norm_forward(o2, r2, *params, g2, residual_scale, eps, kind)
+        ctx.save_for_backward(o2, r2, *params, g2, stats)
+        ctx.options = residual_scale, kind, out.shape, None if gate is None else gate.shape
+        return stream.view(out.shape), normed.view(out.shape)
+
+    @staticmethod
+    def backward(ctx, dstream, dnormed):
+        # the outputs' gradients go through one tuple: _first_order's wrapper takes one
+        return ResidualNormFunction._backward(ctx, (dstream, dnormed))
+
+    @staticmethod
+    @_first_order
+    def _backward(ctx, grads):
+        o2, r2, weight, bias, post_weight, post_bias, gate, stats = ctx.saved_tensors
+        scale, kind, shape, gate_shape = ctx.options
+        ds, dn = (None if t is None else _rows_of(t.to(o2.dtype), o2.shape[1]) for t in grads)
+        dout, dres, dw, db, dpw, dpb, dg = residual_norm_backward(
+            ds, dn, o2, r2, weight, stats, bias, post_weight, post_bias, gate, scale, kind)
+        return (dout.view(shape), dres.view(shape), dw, db, dpw, dpb, None if dg is None else dg.view(gate_shape), None,
+                None, None)
+
+
+def residual_norm(out, residual, weight, bias=None, post_weight=None, post_bias=None, gate=None,
+                  residual_scale: float = 1.0, eps: float = 1e-5, kind: str = "layer"):
+    """(stream, normed) as residual_norm_forward's, over the last axis of out and
+    residual (any number of leading axes; a gate per token has them too, and a
+    last axis of 1).  Differentiable in every tensor, once."""
+    if out.shape != residual.shape:
+        raise ValueError(f"out {list(out.shape)} and residual {list(residual.shape)} differ")
+    if gate is not None and gate.dim() > 1 and gate.shape != (*out.shape[:-1], 1):
+        raise ValueError(f"expected gate [{out.shape[-1]}] or {[*out.shape[:-1], 1]}, got {list(gate.shape)}")
+    return ResidualNormFunction.apply(out, residual, weight, bias, post_weight, post_bias, gate, float(residual_scale),
+                                      float(eps), kind)
+
+
 # ------------------------------------------- dense gated feed-forward block
 class FFNWorkspace:
     """Device buffers of one block shape, kept from step to step: what the

@@ -26,6 +26,21 @@ int check_norm(int64_t rows, int32_t H, int32_t x_type, int32_t w_type) {
     return MOE_OK;
 }
 
+int check_residual_norm(const moe_residual_norm_shape* s) {
+    if (!s) return abi_fail(MOE_EINVAL, "shape is NULL");
+    if (s->rows < 0 || s->rows >= (1ll << 31)) return abi_fail(MOE_EINVAL, "rows must be in [0, 2^31)");
+    if (s->H < 1 || s->H > (1 << 24)) return abi_fail(MOE_EINVAL, "H must be in [1, 2^24]");
+    if (!elt_size(s->x_type)) return abi_fail(MOE_EUNSUPPORTED, "x_type must be MOE_BF16, MOE_F16 or MOE_F32");
+    if (s->w_type != MOE_F32 && s->w_type != s->x_type)
+        return abi_fail(MOE_EUNSUPPORTED, "w_type must be MOE_F32 or x_type");
+    if (s->kind != MOE_NORM_LAYER && s->kind != MOE_NORM_RMS)
+        return abi_fail(MOE_EUNSUPPORTED, "kind must be MOE_NORM_LAYER or MOE_NORM_RMS");
+    if (s->gate < MOE_GATE_NONE || s->gate > MOE_GATE_TOKEN)
+        return abi_fail(MOE_EUNSUPPORTED, "gate must be one of MOE_GATE_*");
+    if (!std::isfinite(s->residual_scale)) return abi_fail(MOE_EINVAL, "residual_scale must be finite");
+    if (!std::isfinite(s->eps) || s->eps < 0.0f) return abi_fail(MOE_EINVAL, "eps must be finite and >= 0");
+    return MOE_OK;
+}
 int check_group(int32_t group) {
     return group == 32 || group == 64 || group == 128
                ? MOE_OK
@@ -368,6 +383,117 @@ int moe_linear_backward(const moe_linear_shape* shape, const void* dy, int64_t d
     f.db = dbias;
     f.db_f32 = bias_type == MOE_F32;
     return launch_linear_backward(*shape, f, st);
+}
+
+int moe_residual_norm_forward(const moe_residual_norm_shape* shape, const void* out, int64_t out_stride,
+                              const void* residual, int64_t residual_stride, const void* gate, const void* post_weight,
+                              const void* post_bias, const void* weight, const void* bias, void* stream_out,
+                              void* normed, float* stats, void* stream) {
+    int rc = check_residual_norm(shape);
+    if (rc) return rc;
+    if (shape->rows == 0) return MOE_OK;
+    if (!out || !residual || !weight || !stream_out || !normed || !stats || (shape->gate != MOE_GATE_NONE && !gate) ||
+        (post_bias && !post_weight))
+        return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    if (out_stride < shape->H || residual_stride < shape->H) return abi_fail(MOE_EINVAL, "strides must be >= H");
+    if (stream_out == residual && residual_stride != shape->H)
+        return abi_fail(MOE_EINVAL, "in place the residual must be contiguous");
+    const int xe = elt_size(shape->x_type), we = elt_size(shape->w_type);
+    if (!aligned(out, xe) || !aligned(residual, xe) || !aligned(stream_out, xe) || !aligned(normed, xe) ||
+        !aligned(gate, we) || !aligned(post_weight, we) || !aligned(post_bias, we) || !aligned(weight, we) ||
+        !aligned(bias, we) || !aligned(stats, 4))
+        return abi_fail(MOE_EUNSUPPORTED, "pointers must be aligned to their elements");
+    int sms = 0;
+    if ((rc = abi_select_device(out, &sms))) return rc;
+    ResNormPtrs f = {};
+    f.out = out;
+    f.out_stride = out_stride;
+    f.residual = residual;
+    f.residual_stride = residual_stride;
+    f.gate = gate;
+    f.post_weight = post_weight;
+    f.post_bias = post_bias;
+    f.weight = weight;
+    f.bias = bias;
+    f.stream = stream_out;
+    f.normed = normed;
+    f.stats = stats;
+    const int e = launch_residual_norm_fwd(*shape, f, (cudaStream_t)stream);
+    return e ? abi_cuda_fail(e, "residual norm launch") : MOE_OK;
+}
+
+int moe_residual_norm_workspace(const moe_residual_norm_shape* shape, size_t* bytes) {
+    if (!bytes) return abi_fail(MOE_EINVAL, "bytes is NULL");
+    const int rc = check_residual_norm(shape);
+    if (rc) return rc;
+    *bytes = (size_t)residual_norm_part_bytes(*shape);
+    return MOE_OK;
+}
+
+int moe_residual_norm_backward(const moe_residual_norm_shape* shape, const void* dstream, int64_t dstream_stride,
+                               const void* dnormed, int64_t dnormed_stride, const void* out, int64_t out_stride,
+                               const void* residual, int64_t residual_stride, const void* gate, const void* post_weight,
+                               const void* post_bias, const void* weight, const float* stats, void* ws, void* dout,
+                               void* dresidual, void* dweight, void* dbias, void* dpost_weight, void* dpost_bias,
+                               void* dgate, void* stream) {
+    int rc = check_residual_norm(shape);
+    if (rc) return rc;
+    const bool channel = shape->gate == MOE_GATE_CHANNEL;
+    if ((post_bias || dpost_weight || dpost_bias) && !post_weight && shape->rows > 0)
+        return abi_fail(MOE_EINVAL, "post_bias and the post norm's gradients need post_weight");
+    if (dgate && shape->gate == MOE_GATE_NONE) return abi_fail(MOE_EINVAL, "dgate without a gate");
+    const int xe = elt_size(shape->x_type), we = elt_size(shape->w_type);
+    const void* params[] = {gate, post_weight, post_bias, weight, dweight, dbias, dpost_weight, dpost_bias, dgate};
+    for (const void* p : params)
+        if (!aligned(p, we)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be aligned to their elements");
+    const void* rows[] = {dstream, dnormed, out, residual, dout, dresidual};
+    for (const void* p : rows)
+        if (!aligned(p, xe)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be aligned to their elements");
+    if (!aligned(stats, 4) || !aligned(ws, 16)) return abi_fail(MOE_EUNSUPPORTED, "stats must be 4-, ws 16-byte aligned");
+    cudaStream_t st = (cudaStream_t)stream;
+    int sms = 0;
+    if (shape->rows == 0) {
+        void* zero[] = {dweight, dbias, dpost_weight, dpost_bias, channel ? dgate : nullptr};
+        for (void* p : zero) {
+            if (!p) continue;
+            if ((rc = abi_select_device(p, &sms))) return rc;
+            const cudaError_t ce = cudaMemsetAsync(p, 0, (size_t)shape->H * we, st);
+            if (ce != cudaSuccess) return abi_cuda_fail((int)ce, "zeroing the joint's gradients");
+        }
+        return MOE_OK;
+    }
+    const bool sums = dweight || dbias || dpost_weight || dpost_bias || (channel && dgate);
+    if (!out || !residual || !weight || !stats || !dout || !dresidual || (sums && !ws) ||
+        (shape->gate != MOE_GATE_NONE && !gate))
+        return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    if (out_stride < shape->H || residual_stride < shape->H || (dstream && dstream_stride < shape->H) ||
+        (dnormed && dnormed_stride < shape->H))
+        return abi_fail(MOE_EINVAL, "strides must be >= H");
+    if ((rc = abi_select_device(out, &sms))) return rc;
+    ResNormPtrs f = {};
+    f.dstream = dstream;
+    f.dstream_stride = dstream_stride;
+    f.dnormed = dnormed;
+    f.dnormed_stride = dnormed_stride;
+    f.out = out;
+    f.out_stride = out_stride;
+    f.residual = residual;
+    f.residual_stride = residual_stride;
+    f.gate = gate;
+    f.post_weight = post_weight;
+    f.post_bias = post_bias;
+    f.weight = weight;
+    f.stats = const_cast<float*>(stats);
+    f.part = static_cast<float*>(ws);
+    f.dout = dout;
+    f.dresidual = dresidual;
+    f.dweight = dweight;
+    f.dbias = dbias;
+    f.dpost_weight = dpost_weight;
+    f.dpost_bias = dpost_bias;
+    f.dgate = dgate;
+    const int e = launch_residual_norm_bwd(*shape, f, st);
+    return e ? abi_cuda_fail(e, "residual norm backward launch") : MOE_OK;
 }
 
 }  // extern "C"

@@ -162,6 +162,19 @@ int launch_ffn_backward(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t s
 bool ffn_few_takes(const moe_ffn_shape& s);
 int launch_ffn_few(const moe_ffn_shape& s, const FfnPtrs& f, cudaStream_t st);
 
+// ------------------------------------------------------ residual joint
+struct ResNormPtrs {
+    const void *out, *residual, *gate, *post_weight, *post_bias, *weight, *bias, *dstream, *dnormed;
+    long long out_stride, residual_stride, dstream_stride, dnormed_stride;
+    void *stream, *normed;
+    float* stats;  // [4][rows]
+    float* part;   // [blocks][4][H]
+    void *dout, *dresidual, *dweight, *dbias, *dpost_weight, *dpost_bias, *dgate;
+};
+long long residual_norm_part_bytes(const moe_residual_norm_shape& s);
+int launch_residual_norm_fwd(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
+int launch_residual_norm_bwd(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
+
 // ------------------------------------------------------------ linear layer
 struct LinearPtrs {
     const void *x, *W, *bias, *residual, *dy;
