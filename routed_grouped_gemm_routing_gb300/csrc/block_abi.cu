@@ -418,7 +418,10 @@ int moe_residual_norm_forward(const moe_residual_norm_shape* shape, const void* 
     f.stream = stream_out;
     f.normed = normed;
     f.stats = stats;
-    const int e = launch_residual_norm_fwd(*shape, f, (cudaStream_t)stream);
+    const auto run = shape->x_type == MOE_F32   ? residual_norm_fwd_f32
+                     : shape->x_type == MOE_F16 ? residual_norm_fwd_f16
+                                                : residual_norm_fwd_bf16;
+    const int e = run(*shape, f, (cudaStream_t)stream);
     return e ? abi_cuda_fail(e, "residual norm launch") : MOE_OK;
 }
 
@@ -492,7 +495,10 @@ int moe_residual_norm_backward(const moe_residual_norm_shape* shape, const void*
     f.dpost_weight = dpost_weight;
     f.dpost_bias = dpost_bias;
     f.dgate = dgate;
-    const int e = launch_residual_norm_bwd(*shape, f, st);
+    const auto run = shape->x_type == MOE_F32   ? residual_norm_bwd_f32
+                     : shape->x_type == MOE_F16 ? residual_norm_bwd_f16
+                                                : residual_norm_bwd_bf16;
+    const int e = run(*shape, f, st);
     return e ? abi_cuda_fail(e, "residual norm backward launch") : MOE_OK;
 }
 

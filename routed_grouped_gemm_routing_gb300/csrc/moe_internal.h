@@ -172,8 +172,12 @@ struct ResNormPtrs {
     void *dout, *dresidual, *dweight, *dbias, *dpost_weight, *dpost_bias, *dgate;
 };
 long long residual_norm_part_bytes(const moe_residual_norm_shape& s);
-int launch_residual_norm_fwd(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
-int launch_residual_norm_bwd(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
+int residual_norm_fwd_bf16(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
+int residual_norm_fwd_f16(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
+int residual_norm_fwd_f32(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
+int residual_norm_bwd_bf16(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
+int residual_norm_bwd_f16(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
+int residual_norm_bwd_f32(const moe_residual_norm_shape& s, const ResNormPtrs& f, cudaStream_t st);
 
 // ------------------------------------------------------------ linear layer
 struct LinearPtrs {
