@@ -546,6 +546,36 @@ int moe_forward_w4(const moe_w4_shape* shape, const void* x, const uint8_t* W1_q
                    const uint8_t* W2_q, const void* W2_sf, const int32_t* topk_idx, const float* topk_w, void* ws,
                    void* y, void* stream);
 
+/* The whole expert layer for the few tokens of decoding, from the hidden state to
+ * the experts' sum, in two kernels: for x bf16 [T, H]
+ *     l = x router                      router bf16 [H, E]; FP32 sums
+ *     topk_idx[t] = the k largest of l[t] (equal ones: the lower id; a NaN counts
+ *     as -infinity),  topk_w[t] = softmax over them   as moe_router_topk
+ *     y[t] = sum_j topk_w[t, j] a[t, j] W2[e] + a_s[t] S2,  e = topk_idx[t, j]
+ *     a[t, j] = silu(x[t] W1[e][:, :I]) x[t] W1[e][:, I:],  a_s likewise of S1
+ * with W1 bf16 [E, H, 2I] (gate | up) and W2 bf16 [E, I, H] as in moe_forward, and
+ * optionally (Is > 0) a shared expert S1 bf16 [H, 2 Is], S2 bf16 [Is, H].
+ * activation_clamp as moe_shape's for both (0: none), except that a NaN stays NaN.
+ * 0 <= T <= 64, T k <= 1024, H, I and Is multiples of 8, k <= E <= 1024; all
+ * pointers 16-byte aligned, topk_idx and topk_w 4-byte.  a is rounded to bf16 once
+ * (an operand), sums are FP32, y is rounded once.  Deterministic: K ranges and slots
+ * are added in a fixed order (which goes by the shape). */
+typedef struct moe_decode_shape {
+    int32_t T, H, I, E, k, Is;
+    float activation_clamp;
+} moe_decode_shape;
+
+/* Bytes of the scratch: activations, partial sums, logits and counters.  Nothing in
+ * it lasts from call to call, it needs no clearing, and calls that overlap on the
+ * GPU need scratch of their own.  Host only. */
+int moe_decode_workspace(const moe_decode_shape* shape, size_t* bytes);
+
+/* router NULL: topk_idx int32 [T, k] and topk_w float [T, k] are inputs (an id
+ * outside [0, E) contributes nothing; ids may repeat); else both are overwritten.
+ * y bf16 [T, H] is overwritten.  A wait that runs out leaves NaN in y. */
+int moe_decode_forward(const moe_decode_shape* shape, const void* x, const void* router, const void* W1, const void* W2,
+                       const void* S1, const void* S2, int32_t* topk_idx, float* topk_w, void* ws, void* y, void* stream);
+
 /* Tracing.  moe_trace_begin hands the library `capacity` CUDA events
  * (cudaEvent_t passed as void*, created by the caller with timing enabled).
  * Until moe_trace_end, each kernel the library launches from this thread is

@@ -60,6 +60,10 @@ class MoeResidualNormShape(ctypes.Structure):
         ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class MoeDecodeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I", "E", "k", "Is")] + [("activation_clamp", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe error {code}: {msg}")
@@ -115,11 +119,13 @@ def lib():
             L.moe_linear_workspace.argtypes = [P(MoeLinearShape), P(ctypes.c_size_t)]
             L.moe_linear_forward.argtypes = [P(MoeLinearShape), vp, i64, vp, vp, i32, vp, i64, vp, vp, vp, vp]
             L.moe_linear_backward.argtypes = [P(MoeLinearShape), vp, i64, vp, i64] + [vp] * 6 + [i32, vp]
+            L.moe_decode_workspace.argtypes = [P(MoeDecodeShape), P(ctypes.c_size_t)]
+            L.moe_decode_forward.argtypes = [P(MoeDecodeShape)] + [vp] * 11
             RN = P(MoeResidualNormShape)
             L.moe_residual_norm_forward.argtypes = [RN, vp, i64, vp, i64] + [vp] * 9
             L.moe_residual_norm_workspace.argtypes = [RN, P(ctypes.c_size_t)]
             L.moe_residual_norm_backward.argtypes = [RN] + [vp, i64] * 4 + [vp] * 14
-            for n in ("moe_residual_norm_forward", "moe_residual_norm_workspace", "moe_residual_norm_backward",
+            for n in ("moe_decode_workspace", "moe_decode_forward", "moe_residual_norm_forward", "moe_residual_norm_workspace", "moe_residual_norm_backward",
                       "moe_linear_workspace", "moe_linear_forward", "moe_linear_backward",
                       "moe_ffn_workspace_layout", "moe_ffn_forward", "moe_ffn_backward",
                       "moe_layer_norm_forward", "moe_layer_norm_workspace", "moe_layer_norm_backward",
@@ -499,6 +505,34 @@ def moe_ffn_backward(shape: MoeFFNShape, dY, x, W1, W2, saved, ws, dx, dW1, dW2,
         _arg(W1, _BF, H * 2 * I, "W1", dev), _arg(W2, _BF, I * H, "W2", dev),
         _arg(saved, _U8, L.saved_bytes, "saved", dev), _arg(ws, _U8, L.ws_bytes, "ws", dev),
         _arg(dx, _BF, T * H, "dx", dev), _arg(dW1, _BF, H * 2 * I, "dW1", dev), _arg(dW2, _BF, I * H, "dW2", dev), st)
+    if rc:
+        _check(rc)
+
+
+DECODE_MAX_T, DECODE_MAX_SLOTS = 64, 1024
+
+
+def moe_decode_workspace(shape: MoeDecodeShape) -> int:
+    """Bytes of moe_decode_forward's scratch."""
+    v, ref = _size_out()
+    rc = lib().moe_decode_workspace(ctypes.byref(shape), ref)
+    if rc:
+        _check(rc)
+    return v.value
+
+
+def moe_decode_forward(shape: MoeDecodeShape, x, router, W1, W2, S1, S2, topk_idx, topk_w, ws, y, stream=None):
+    """The whole expert layer for a few tokens: overwrites y bf16 [T, H], topk_idx
+    int32 [T, k] and topk_w f32 [T, k]; with router None the last two are inputs.
+    S1, S2: the shared expert, or None with shape.Is = 0.  ws: uint8 of
+    moe_decode_workspace elements."""
+    T, H, I, E, k, Is = shape.T, shape.H, shape.I, shape.E, shape.k, shape.Is
+    dev, st = _here(stream)
+    rc = lib().moe_decode_forward(
+        ctypes.byref(shape), _arg(x, _BF, T * H, "x", dev), _arg(router, _BF, H * E, "router", dev),
+        _arg(W1, _BF, E * H * 2 * I, "W1", dev), _arg(W2, _BF, E * I * H, "W2", dev), _arg(S1, _BF, H * 2 * Is, "S1", dev),
+        _arg(S2, _BF, Is * H, "S2", dev), _arg(topk_idx, _I32, T * k, "topk_idx", dev), _arg(topk_w, _F32, T * k, "topk_w", dev),
+        _arg(ws, _U8, moe_decode_workspace(shape), "ws", dev), _arg(y, _BF, T * H, "y", dev), st)
     if rc:
         _check(rc)
 

@@ -41,6 +41,19 @@ int check_residual_norm(const moe_residual_norm_shape* s) {
     if (!std::isfinite(s->eps) || s->eps < 0.0f) return abi_fail(MOE_EINVAL, "eps must be finite and >= 0");
     return MOE_OK;
 }
+int check_decode(const moe_decode_shape* s) {
+    if (!s) return abi_fail(MOE_EINVAL, "shape is NULL");
+    if (s->T < 0) return abi_fail(MOE_EINVAL, "T must be >= 0");
+    if (s->H <= 0 || s->I <= 0 || s->Is < 0) return abi_fail(MOE_EINVAL, "H and I must be > 0, Is >= 0");
+    if (s->E < 1 || s->E > kMaxExperts) return abi_fail(MOE_EINVAL, "E must be in [1, 1024]");
+    if (s->k < 1 || s->k > s->E) return abi_fail(MOE_EINVAL, "k must be in [1, E]");
+    if (s->H % 8 || s->I % 8 || s->Is % 8) return abi_fail(MOE_EUNSUPPORTED, "H, I and Is must be multiples of 8");
+    if (s->H > 65536 || s->I > 65536 || s->Is > 65536)
+        return abi_fail(MOE_EUNSUPPORTED, "H, I and Is must be at most 65536");
+    if (s->T > 64 || (long long)s->T * s->k > 1024) return abi_fail(MOE_EUNSUPPORTED, "T must be <= 64 and T*k <= 1024");
+    if (!std::isfinite(s->activation_clamp)) return abi_fail(MOE_EINVAL, "activation_clamp must be finite");
+    return MOE_OK;
+}
 int check_group(int32_t group) {
     return group == 32 || group == 64 || group == 128
                ? MOE_OK
@@ -500,6 +513,32 @@ int moe_residual_norm_backward(const moe_residual_norm_shape* shape, const void*
                                                 : residual_norm_bwd_bf16;
     const int e = run(*shape, f, st);
     return e ? abi_cuda_fail(e, "residual norm backward launch") : MOE_OK;
+}
+
+int moe_decode_workspace(const moe_decode_shape* shape, size_t* bytes) {
+    if (!bytes) return abi_fail(MOE_EINVAL, "bytes is NULL");
+    const int rc = check_decode(shape);
+    if (rc) return rc;
+    *bytes = shape->T ? decode_workspace_bytes(*shape) : 0;
+    return MOE_OK;
+}
+
+int moe_decode_forward(const moe_decode_shape* shape, const void* x, const void* router, const void* W1, const void* W2,
+                       const void* S1, const void* S2, int32_t* topk_idx, float* topk_w, void* ws, void* y, void* stream) {
+    int rc = check_decode(shape);
+    if (rc) return rc;
+    if (shape->T == 0) return MOE_OK;
+    if (!x || !W1 || !W2 || !topk_idx || !topk_w || !ws || !y || (shape->Is && (!S1 || !S2)))
+        return abi_fail(MOE_EINVAL, "NULL pointer argument");
+    const void* ptrs[] = {x, router, W1, W2, S1, S2, ws, y};
+    for (const void* p : ptrs)
+        if (!aligned(p, 16)) return abi_fail(MOE_EUNSUPPORTED, "pointers must be 16-byte aligned");
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return abi_fail(MOE_EUNSUPPORTED, "topk_idx and topk_w must be 4-byte aligned");
+    int sms = 0;
+    if ((rc = abi_select_device(ws, &sms))) return rc;
+    const DecodePtrs f = {x, router, W1, W2, S1, S2, topk_idx, topk_w, static_cast<uint8_t*>(ws), y};
+    return launch_decode(*shape, f, sms, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,825 @@
+// The whole expert layer for the few tokens of decoding, in two kernels:
+//
+//   l = x R,  idx = the k largest (equal ones: the lower id),  w = softmax over them
+//   a[t, j] = silu(clamp x W1_g[e]) clamp(x W1_u[e])   e = idx[t, j]   (bf16, rounded once)
+//   y[t] = sum_j w[t, j] a[t, j] W2[e] + a_s[t] S2     (a_s: of the shared expert S1)
+//
+// Bound by DRAM: every weight of an expert that some token picks is read once, and
+// used for the few tokens that picked it.
+//
+// decode_router_kernel: the logits, 32 experts x eight tokens to a cluster of
+// eight blocks that split the width; FP32 sums of at most H / 512 terms a thread, joined in a
+// fixed order.  It also clears the counters of the second kernel.
+//
+// decode_experts_kernel: one block on each SM.  Every block takes the top k of all
+// tokens for itself (a few kilobytes of logits) and lists the experts' tokens.
+// The work is a list of jobs that all blocks know: first, for each expert in use
+// (the shared one first), 64 features of gate and up projection and a range of K;
+// then, for each expert, 128 columns of the down projection and a range of K.
+// Blocks draw jobs from a counter.  A warp streams a job's weights by TMA, 64 of K
+// x 2 x 64 columns a stage, and goes on to the next job's while this one's end is
+// still computed, so that some 200 KB are in flight on every SM all the time.
+// Another warp gathers the tokens' rows (cp.async) and, for the down projection,
+// waits until the expert's activations are there: they come from jobs drawn
+// earlier, by blocks that are running and that wait for nothing before them, so
+// the wait ends whichever blocks are resident.  Eight warps multiply (mma
+// m16n8k16, weights as A straight out of the boxes by transposed ldmatrix): eight
+// gate and the same eight up features a warp, so that the activation needs no
+// exchange; eight tokens as B, kNt such groups.  tcgen05 would want 128-row tiles
+// of tokens or weights out of TMEM: at 8 to 64 tokens the weights' bytes, not the
+// products, set the pace.
+//
+// FP32 partial sums of a K range are added by whichever block finishes a tile
+// last, in the order of the ranges; a token's slots in the order of its routing.
+// Deterministic.
+#include <math.h>
+
+#include "clamp.cuh"
+#include "grouped_gemm_2sm.cuh"
+#include "smem_limit.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kDcConsumers = 8, kDcWarpTma = 8, kDcWarpGather = 9;
+constexpr int kDcThreads = 320;
+constexpr int kDcBox = 8192;    // 64 of K x 64 columns
+constexpr int kDcJobs = 4;      // jobs drawn ahead
+constexpr int kDcMaxSplit = 16;
+constexpr int kRtCluster = 8, kRtRows = 512;  // of the router: blocks of a cluster, rows of x held at once
+
+// ----------------------------------------------------------------- router
+template <int kTok>
+__global__ void __launch_bounds__(256)
+    decode_router_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ R, int T, int H, int E,
+                         float* __restrict__ logits, int* __restrict__ counters, int n_counters) {
+    __shared__ __align__(16) float xs[kRtRows][kTok];
+    __shared__ float red[8][kTok][32];
+    __shared__ float all[kRtCluster][kTok][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, cv = tid & 3, rl = tid >> 2, rank = (int)cluster_ctarank();
+    {
+        const int blocks = gridDim.x * gridDim.y * gridDim.z;
+        const int b = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+        for (int i = b * 256 + tid; i < n_counters; i += blocks * 256) counters[i] = 0;
+    }
+    const int e0 = blockIdx.x * 32, t0 = blockIdx.y * kTok, e = e0 + 8 * cv;
+    const int per = (H + kRtCluster - 1) / kRtCluster, h0 = rank * per, h1 = h0 + per < H ? h0 + per : H;
+    const bool whole = E % 8 == 0;  // rows of R on 16-byte boundaries
+    float acc[kTok][8];
+#pragma unroll
+    for (int t = 0; t < kTok; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[t][j] = 0.0f;
+    for (int c0 = h0; c0 < h1; c0 += kRtRows) {
+        const int rows = h1 - c0 < kRtRows ? h1 - c0 : kRtRows;
+        __syncthreads();
+        for (int i = tid; i < kTok * rows; i += 256) {
+            const int t = i / rows, r = i - t * rows;
+            xs[r][t] = t0 + t < T ? __bfloat162float(x[(size_t)(t0 + t) * H + c0 + r]) : 0.0f;
+        }
+        __syncthreads();
+        if (e < E) {
+#pragma unroll 2
+            for (int r = rl; r < rows; r += 64) {
+                float w[8];
+                const __nv_bfloat16* src = R + (size_t)(c0 + r) * E + e;
+                if (whole) {
+                    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(src)), w);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = e + j < E ? __bfloat162float(src[j]) : 0.0f;
+                }
+#pragma unroll
+                for (int t = 0; t < kTok; ++t)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xs[r][t], w[j], acc[t][j]);
+            }
+        }
+    }
+    // eight rows of lanes, eight warps, eight blocks
+#pragma unroll
+    for (int t = 0; t < kTok; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float v = acc[t][j];
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            if ((tid & 31) < 4) red[tid >> 5][t][8 * cv + j] = v;
+        }
+    __syncthreads();
+    // a block's sums go to the block that finishes their token (one token: all to the first)
+    for (int i = tid; i < kTok * 32; i += 256) {
+        const int t = i >> 5, c = i & 31;
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += red[w][t][c];
+        const uint32_t dst = cluster_addr_of(smem_addr(&all[rank][t][c]), t);
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
+    }
+    cluster_sync();
+    const int t = rank, c = tid;
+    if (t < kTok && t0 + t < T && c < 32 && e0 + c < E) {
+        float v = 0.0f;
+#pragma unroll
+        for (int b = 0; b < kRtCluster; ++b) v += all[b][t][c];
+        logits[(size_t)(t0 + t) * E + e0 + c] = v;
+    }
+}
+
+// ----------------------------------------------------------------- experts
+struct DecodeArgs {
+    int T, H, I, E, k, Is;
+    float clamp;
+    int kp1, kp1s, kp2, kp2s;  // K ranges: gate and up, down; of a routed expert and of the shared one
+    int stages, groups_cap;
+    const __nv_bfloat16* x;
+    const float* logits;  // null: the routing is given
+    int32_t* topk_idx;    // [T][k], written, or read without logits
+    float* topk_w;
+    __nv_bfloat16 *act, *act_s;  // [T k][I], [T][Is]
+    float *part1, *part1s;       // [T k][kp1][2][I], [T][kp1s][2][Is]
+    float *part2, *part2s;       // [T k][kp2][H], [T][kp2s][H]
+    int *ticket, *done, *tiles_done, *joined;  // counters: jobs drawn, tiles of a group's activations that are there,
+                                               // jobs of a column tile that are done, K ranges of a group's tile
+    int32_t* status;
+    __nv_bfloat16* y;
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void dc_ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void dc_ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void dc_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A barrier of the multiplying warps that ends when one of them gave up.
+struct ConsumerBarrier {
+    uint32_t bar, phase;
+    volatile int* abort;
+    __device__ __forceinline__ bool sync() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+        const bool ok = warp_wait(bar, phase, abort);
+        phase ^= 1u;
+        return ok;
+    }
+};
+
+// Counts a block's finished part (its threads have met at a barrier since they
+// wrote it); whether it was the last of n, whose parts it may then read.
+__device__ __forceinline__ int draw_last(int* counter, int n) {
+    __threadfence();
+    const int last = atomicAdd(counter, 1) == n - 1;
+    __threadfence();
+    return last;
+}
+
+// What every block keeps of the routing, in shared memory behind the ring.
+struct Routing {
+    float* w;         // [T k]
+    int16_t* idx;     // [T k], -1: dropped
+    uint16_t* list;   // slots by expert
+    uint16_t *ge, *gb, *gn;  // groups: expert, start in list, slots
+    int* n;           // groups
+};
+__host__ __device__ constexpr int dc_table_bytes(int slots) {
+    return slots * 4 + (slots * 2 + 15) / 16 * 16 * 2 + (slots + 8) * 2 * 3 + 32;
+}
+__host__ __device__ constexpr int dc_stage_bytes(int nt) { return 2 * kDcBox + nt * 1024; }
+__host__ __device__ constexpr int dc_bar_bytes(int stages) { return 8 * (2 * stages + 2 * kDcJobs) + 4 * kDcJobs + 16; }
+
+// One warp: the k largest of a token's E logits, as the layer's router takes them
+// (equal ones by id, a NaN as -infinity, softmax over the chosen ones).
+template <int P>
+__device__ __forceinline__ void warp_topk(const float* row, int E, int k, int* idx, float* w) {
+    const int lane = threadIdx.x & 31;
+    uint32_t v[P];  // order-preserving codes
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int e = lane + 32 * i;
+        float f = e < E ? __ldcg(row + e) : -INFINITY;
+        if (isnan(f)) f = -INFINITY;
+        const uint32_t u = __float_as_uint(f == 0.0f ? 0.0f : f);
+        v[i] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    }
+    uint32_t taken = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        if (lane + 32 * i >= E) taken |= 1u << i;
+    float m = 0.0f, sum = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = 0, at = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (!(taken >> i & 1u) && (at == 0xffffffffu || v[i] > best)) best = v[i], at = lane + 32 * i;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, at == 0xffffffffu ? 0u : best);
+        const uint32_t id = __reduce_min_sync(0xffffffffu, best == top ? at : 0xffffffffu);
+        if ((id & 31) == lane) taken |= 1u << (id >> 5);
+        const float key = __uint_as_float((top & 0x80000000u) ? (top & 0x7fffffffu) : ~top);
+        if (j == 0) m = key;
+        // limits of the softmax where the largest is infinite: 1 for each equal to it
+        const float ex = isinf(m) ? (key == m ? 1.0f : 0.0f) : expf(key - m);
+        sum += ex;
+        if (lane == 0) idx[j] = (int)id, w[j] = ex;
+    }
+    __syncwarp();
+    for (int j = lane; j < k; j += 32) w[j] = w[j] / sum;
+    __syncwarp();
+}
+__device__ __forceinline__ void warp_topk_any(const float* row, int E, int k, int* idx, float* w) {
+    const int p = (E + 31) / 32;
+    if (p <= 1)
+        warp_topk<1>(row, E, k, idx, w);
+    else if (p <= 2)
+        warp_topk<2>(row, E, k, idx, w);
+    else if (p <= 4)
+        warp_topk<4>(row, E, k, idx, w);
+    else if (p <= 8)
+        warp_topk<8>(row, E, k, idx, w);
+    else
+        warp_topk<32>(row, E, k, idx, w);
+}
+
+// The routing and the groups of at most `cap` slots of an expert.  Scratch (the
+// ring's place): ids [slots], counts, starts and first groups [E + 1].
+__device__ void build_routing(const DecodeArgs& p, const Routing& r, int cap, int* scratch) {
+    const int slots = p.T * p.k, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int *ids = scratch, *cnt = ids + slots, *start = cnt + p.E + 1, *first = start + p.E + 1;
+    for (int i = tid; i <= p.E; i += kDcThreads) cnt[i] = 0;
+    if (p.logits) {
+        for (int t = warp; t < p.T; t += kDcThreads / 32)
+            warp_topk_any(p.logits + (size_t)t * p.E, p.E, p.k, ids + t * p.k, r.w + t * p.k);
+    } else {
+        for (int i = tid; i < slots; i += kDcThreads) ids[i] = __ldg(p.topk_idx + i), r.w[i] = __ldg(p.topk_w + i);
+    }
+    __syncthreads();
+    for (int i = tid; i < slots; i += kDcThreads) {
+        const int e = ids[i];
+        const bool ok = e >= 0 && e < p.E;
+        r.idx[i] = (int16_t)(ok ? e : -1);
+        if (ok) atomicAdd(cnt + e, 1);
+        if (p.logits && blockIdx.x == 0) p.topk_idx[i] = e, p.topk_w[i] = r.w[i];
+    }
+    __syncthreads();
+    if (warp == 0) {  // prefix sums of the counts and of the groups
+        int s = 0, g = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane, c = e < p.E ? cnt[e] : 0, q = (c + cap - 1) / cap;
+            int cs = c, qs = q;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, cs, d), b = __shfl_up_sync(0xffffffffu, qs, d);
+                if (lane >= d) cs += a, qs += b;
+            }
+            if (e < p.E) start[e] = s + cs - c, first[e] = g + qs - q;
+            s += __shfl_sync(0xffffffffu, cs, 31);
+            g += __shfl_sync(0xffffffffu, qs, 31);
+        }
+        if (lane == 0) *r.n = g;
+    }
+    __syncthreads();
+    for (int i = tid; i < slots; i += kDcThreads) {
+        const int e = r.idx[i];
+        if (e < 0) continue;
+        int rank = 0;
+        for (int j = 0; j < i; ++j) rank += r.idx[j] == e;
+        r.list[start[e] + rank] = (uint16_t)i;
+    }
+    for (int e = tid; e < p.E; e += kDcThreads)
+        for (int q = 0; q * cap < cnt[e]; ++q) {
+            r.ge[first[e] + q] = (uint16_t)e;
+            r.gb[first[e] + q] = (uint16_t)(start[e] + q * cap);
+            r.gn[first[e] + q] = (uint16_t)(cnt[e] - q * cap < cap ? cnt[e] - q * cap : cap);
+        }
+    __syncthreads();
+}
+
+// The jobs, in the order in which they are drawn.
+struct Jobs {
+    int tiles1, tiles1s, tiles2, st1, st2, st2s;  // column tiles; stages of K
+    int n1s, n1, n2s, total, per1, per2;          // jobs; of a routed group
+    __device__ __forceinline__ Jobs(const DecodeArgs& p, int groups) {
+        tiles1 = (p.I + 63) / 64, tiles1s = (p.Is + 63) / 64, tiles2 = (p.H + 127) / 128;
+        st1 = (p.H + 63) / 64, st2 = (p.I + 63) / 64, st2s = (p.Is + 63) / 64;
+        per1 = tiles1 * p.kp1, per2 = tiles2 * p.kp2;
+        n1s = p.Is ? tiles1s * p.kp1s : 0;
+        n1 = n1s + groups * per1;
+        n2s = p.Is ? tiles2 * p.kp2s : 0;
+        total = n1 + n2s + groups * per2;
+    }
+};
+struct Job {
+    bool down, shared;
+    int group, tile, part, kb0, kb1;  // group: of the routed ones
+};
+__device__ __forceinline__ Job job_of(const DecodeArgs& p, const Jobs& n, int j) {
+    Job q;
+    q.down = j >= n.n1;
+    if (q.down) j -= n.n1;
+    const int ns = q.down ? n.n2s : n.n1s;
+    q.shared = j < ns;
+    if (!q.shared) j -= ns;
+    const int per = q.down ? n.per2 : n.per1;
+    const int kp = q.down ? (q.shared ? p.kp2s : p.kp2) : (q.shared ? p.kp1s : p.kp1);
+    q.group = q.shared ? 0 : j / per;
+    if (!q.shared) j -= q.group * per;
+    q.tile = j / kp;
+    q.part = j - q.tile * kp;
+    const int st = q.down ? (q.shared ? n.st2s : n.st2) : n.st1;
+    q.kb0 = st * q.part / kp;
+    q.kb1 = st * (q.part + 1) / kp;
+    return q;
+}
+
+template <int kNt>
+__global__ void __launch_bounds__(kDcThreads, 1)
+    decode_experts_kernel(const __grid_constant__ CUtensorMap mW1, const __grid_constant__ CUtensorMap mW2,
+                          const __grid_constant__ CUtensorMap mS1, const __grid_constant__ CUtensorMap mS2,
+                          const DecodeArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int abort_word, last_word;
+    volatile int* abort = &abort_word;
+    const uint32_t raw = smem_addr(smem_raw), ring = (raw + 1023u) & ~1023u;
+    constexpr uint32_t kStage = dc_stage_bytes(kNt);
+    uint8_t* tail = smem_raw + (ring - raw) + p.stages * kStage;
+    const uint32_t bar0 = smem_addr(tail);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (p.stages + s); };
+    auto jfull = [&](int s) { return bar0 + 8u * (2 * p.stages + s); };
+    auto jempty = [&](int s) { return bar0 + 8u * (2 * p.stages + kDcJobs + s); };
+    volatile int* jobs = reinterpret_cast<volatile int*>(tail + 8 * (2 * p.stages + 2 * kDcJobs));
+    ConsumerBarrier cbar = {bar0 + 8u * (2 * p.stages + 2 * kDcJobs) + 4u * kDcJobs, 0, abort};
+    const int slots = p.T * p.k;
+    uint8_t* tab = tail + dc_bar_bytes(p.stages);
+    Routing rt;
+    rt.n = reinterpret_cast<int*>(tab);
+    rt.w = reinterpret_cast<float*>(tab + 16);
+    rt.idx = reinterpret_cast<int16_t*>(rt.w + slots);
+    rt.list = reinterpret_cast<uint16_t*>(rt.idx + (slots + 7) / 8 * 8);
+    rt.ge = rt.list + (slots + 7) / 8 * 8;
+    rt.gb = rt.ge + slots + 8;
+    rt.gn = rt.gb + slots + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full(s), 1 + 32);  // the TMA thread's arrival and the gathering lanes'
+            mbar_init(empty(s), kDcConsumers);
+        }
+        for (int s = 0; s < kDcJobs; ++s) {
+            mbar_init(jfull(s), 1);
+            mbar_init(jempty(s), kDcConsumers + 1);
+        }
+        mbar_init(cbar.bar, kDcConsumers);
+        *abort = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&mW1);
+        tma_prefetch_map(&mW2);
+        if (p.Is) {
+            tma_prefetch_map(&mS1);
+            tma_prefetch_map(&mS2);
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    build_routing(p, rt, 8 * kNt, reinterpret_cast<int*>(smem_raw + (ring - raw)));
+    fence_proxy_async_smem();  // the scratch was the ring's
+    __syncthreads();
+    const int groups = *rt.n;
+    const Jobs n(p, groups);
+    const int down_jobs = (p.Is ? p.kp2s : 0) + groups * p.kp2;  // of a column tile
+
+    if (warp == kDcWarpTma) {
+        if (lane == 0) {
+            int stage = 0, slot = 0;
+            uint32_t phase = 0, jphase = 0;
+            int ticket = blockIdx.x;
+            for (;;) {
+                const int j = ticket < n.total ? ticket : -1;
+                // drawn ahead: its latency passes under this job's copies
+                if (j >= 0) ticket = (int)gridDim.x + atomicAdd(p.ticket, 1);
+                if (!mbar_wait(jempty(slot), jphase ^ 1u, abort)) break;
+                jobs[slot] = j;
+                mbar_arrive(jfull(slot));
+                if (++slot == kDcJobs) slot = 0, jphase ^= 1u;
+                if (j < 0) break;
+                const Job q = job_of(p, n, j);
+                const int e = q.shared ? 0 : rt.ge[q.group];
+                const CUtensorMap* m = q.down ? (q.shared ? &mS2 : &mW2) : (q.shared ? &mS1 : &mW1);
+                bool ok = true;
+                for (int kb = q.kb0; kb < q.kb1; ++kb) {
+                    if (!(ok = mbar_wait(empty(stage), phase ^ 1u, abort))) break;
+                    const uint32_t b = full(stage), dst = ring + stage * kStage;
+                    mbar_arrive_expect_tx(b, 2 * kDcBox);
+                    if (q.down) {
+                        tma_load_3d(dst, m, 128 * q.tile, 64 * kb, e, b);
+                        tma_load_3d(dst + kDcBox, m, 128 * q.tile + 64, 64 * kb, e, b);
+                    } else {
+                        tma_load_4d(dst, m, 64 * q.tile, 0, 64 * kb, e, b);
+                        tma_load_4d(dst + kDcBox, m, 64 * q.tile, 1, 64 * kb, e, b);
+                    }
+                    if (++stage == p.stages) stage = 0, phase ^= 1u;
+                }
+                if (!ok) break;
+            }
+        }
+    } else if (warp == kDcWarpGather) {
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, jphase = 0;
+        for (;;) {
+            if (!warp_wait(jfull(slot), jphase, abort)) break;
+            const int j = jobs[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(jempty(slot));
+            if (++slot == kDcJobs) slot = 0, jphase ^= 1u;
+            if (j < 0) break;
+            const Job q = job_of(p, n, j);
+            const int rows = q.shared ? p.T : rt.gn[q.group], K = q.down ? (q.shared ? p.Is : p.I) : p.H;
+            const __nv_bfloat16* src = q.down ? (q.shared ? p.act_s : p.act) : p.x;
+            // this lane's rows: lane / 8, + 4, ..; a piece of 8 of K of each
+            int at[2 * kNt];
+#pragma unroll
+            for (int i = 0; i < 2 * kNt; ++i) {
+                const int r = (lane >> 3) + 4 * i;
+                at[i] = -1;
+                if (r < rows) {
+                    int s = r;
+                    if (!q.shared) {
+                        s = rt.list[rt.gb[q.group] + r];
+                        if (!q.down) s /= p.k;
+                    }
+                    at[i] = s * K;
+                }
+            }
+            bool ok = true;
+            if (q.down) {  // the activations of this expert
+                const int want = q.shared ? n.tiles1s : n.tiles1;
+                const int* flag = p.done + (q.shared ? 0 : 1 + q.group);
+                if (lane == 0) {
+                    const uint64_t t0 = global_timer_ns();
+                    for (uint32_t it = 1;; ++it) {
+                        int v;
+                        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+                        if (v >= want) break;
+                        if ((it & 63u) == 0 && (*abort || global_timer_ns() - t0 > kWaitLimitNs)) {
+                            *abort = 1;
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            const int live = (rows + 7) / 8 * 2;  // of the lanes' rows
+            for (int kb = q.kb0; ok && kb < q.kb1; ++kb) {
+                if (!(ok = warp_wait(empty(stage), phase ^ 1u, abort))) break;
+                const uint32_t dst = ring + stage * kStage + 2 * kDcBox;
+                const int k0 = 64 * kb + 8 * (lane & 7);
+#pragma unroll
+                for (int i = 0; i < 2 * kNt; ++i) {
+                    if (i >= live) break;
+                    const int r = (lane >> 3) + 4 * i;
+                    const bool there = at[i] >= 0 && k0 < K;
+                    cp_async_16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4), there ? src + at[i] + k0 : src, there ? 16 : 0);
+                }
+                cp_async_arrive_noinc(full(stage));
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
+            }
+            if (!ok) break;
+        }
+        cp_async_wait_all();
+    } else {
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, jphase = 0;
+        const int tid = threadIdx.x, fl = lane >> 2, tk = 2 * (lane & 3);
+        // weights: K row l % 8 (+ 8 from lane 16 on), first or second box, this warp's eight columns
+        const int ak = (lane & 7) + (lane >= 16 ? 8 : 0);
+        const uint32_t abase = ((lane >> 3) & 1) * kDcBox + ak * 128 + ((warp ^ (ak & 7)) << 4);
+        for (;;) {
+            if (!warp_wait(jfull(slot), jphase, abort)) break;
+            const int j = jobs[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(jempty(slot));
+            if (++slot == kDcJobs) slot = 0, jphase ^= 1u;
+            if (j < 0) break;
+            const Job q = job_of(p, n, j);
+            const int rows = q.shared ? p.T : rt.gn[q.group], tiles = (rows + 7) / 8;
+            float acc[kNt][4];
+#pragma unroll
+            for (int i = 0; i < kNt; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+            bool ok = true;
+            for (int kb = q.kb0; kb < q.kb1; ++kb) {
+                if (!(ok = warp_wait(full(stage), phase, abort))) break;
+                const uint32_t a0 = ring + stage * kStage, b0 = a0 + 2 * kDcBox;
+                uint32_t a[4][4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) dc_ldmatrix_x4_trans(a0 + abase + s * 2048, a[s]);
+#pragma unroll
+                for (int i = 0; i < kNt; ++i) {
+                    if (i >= tiles) break;
+                    uint32_t b[4];
+                    const int r = lane & 7, v = lane >> 3;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        dc_ldmatrix_x4(b0 + (8 * i + r) * 128 + (((4 * h + v) ^ r) << 4), b);
+                        dc_mma(acc[i], a[2 * h], b[0], b[1]);
+                        dc_mma(acc[i], a[2 * h + 1], b[2], b[3]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty(stage));
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
+            }
+            if (!ok) break;
+            // ---- the end of a job.  acc: first box's column fl (8 a warp), tokens tk and
+            // tk + 1 of each eight; then the second box's
+            auto slot_of = [&](int r) { return q.shared ? r : (int)rt.list[rt.gb[q.group] + r]; };
+            if (!q.down) {
+                const int I = q.shared ? p.Is : p.I, kp = q.shared ? p.kp1s : p.kp1, f = 64 * q.tile + 8 * warp + fl;
+                __nv_bfloat16* act = q.shared ? p.act_s : p.act;
+                float* part = q.shared ? p.part1s : p.part1;
+                const int g = q.shared ? 0 : 1 + q.group;
+                bool mine = true;
+                if (kp > 1) {
+#pragma unroll
+                    for (int i = 0; i < kNt; ++i)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int r = 8 * i + tk + c;
+                            if (r >= rows || f >= I) continue;
+                            float* d = part + ((size_t)slot_of(r) * kp + q.part) * 2 * I + f;
+                            __stcg(d, acc[i][c]);
+                            __stcg(d + I, acc[i][2 + c]);
+                        }
+                    if (!cbar.sync()) break;
+                    if (tid == 0) {
+                        int* c = p.joined + (size_t)g * (n.tiles1 > n.tiles1s ? n.tiles1 : n.tiles1s) + q.tile;
+                        last_word = draw_last(c, kp);
+                    }
+                    if (!cbar.sync()) break;
+                    mine = last_word != 0;
+                }
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < kNt; ++i)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int r = 8 * i + tk + c;
+                            if (r >= rows || f >= I) continue;
+                            const int s = slot_of(r);
+                            float gate = acc[i][c], up = acc[i][2 + c];
+                            if (kp > 1) {
+                                gate = up = 0.0f;
+                                const float* d = part + (size_t)s * kp * 2 * I + f;
+#pragma unroll 4
+                                for (int b = 0; b < kp; ++b) {
+                                    gate += __ldcg(d + (size_t)b * 2 * I);
+                                    up += __ldcg(d + (size_t)b * 2 * I + I);
+                                }
+                            }
+                            gate = clamp_keep_nan(gate, p.clamp);
+                            up = clamp_keep_nan(up, p.clamp);
+                            act[(size_t)s * I + f] = __float2bfloat16_rn(gate / (1.0f + expf(-gate)) * up);
+                        }
+                    if (!cbar.sync()) break;
+                    if (tid == 0) {
+                        __threadfence();
+                        atomicAdd(p.done + g, 1);
+                    }
+                }
+            } else {
+                const int kp = q.shared ? p.kp2s : p.kp2, c0 = 128 * q.tile + 8 * warp + fl;
+                float* part = q.shared ? p.part2s : p.part2;
+#pragma unroll
+                for (int i = 0; i < kNt; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int r = 8 * i + tk + c;
+                        if (r >= rows) continue;
+                        float* d = part + ((size_t)slot_of(r) * kp + q.part) * p.H;
+                        if (c0 < p.H) __stcg(d + c0, acc[i][c]);
+                        if (c0 + 64 < p.H) __stcg(d + c0 + 64, acc[i][2 + c]);
+                    }
+                if (!cbar.sync()) break;
+                if (tid == 0) last_word = draw_last(p.tiles_done + q.tile, down_jobs);
+                if (!cbar.sync()) break;
+                if (last_word) {  // every part of these columns is there: y
+                    for (int i = tid; i < p.T * 32; i += 256) {
+                        const int t = i >> 5, c = 128 * q.tile + 4 * (i & 31);
+                        if (c >= p.H) continue;
+                        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                        for (int jj = 0; jj < p.k; ++jj) {
+                            const int sl = t * p.k + jj;
+                            if (rt.idx[sl] < 0) continue;
+                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            const float* d = p.part2 + (size_t)sl * p.kp2 * p.H + c;
+                            for (int b = 0; b < p.kp2; ++b) {
+                                const float4 u = __ldcg(reinterpret_cast<const float4*>(d + (size_t)b * p.H));
+                                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+                            }
+                            const float w = rt.w[sl];
+                            s.x += w * v.x, s.y += w * v.y, s.z += w * v.z, s.w += w * v.w;
+                        }
+                        if (p.Is) {
+                            const float* d = p.part2s + (size_t)t * p.kp2s * p.H + c;
+#pragma unroll 4
+                            for (int b = 0; b < p.kp2s; ++b) {
+                                const float4 u = __ldcg(reinterpret_cast<const float4*>(d + (size_t)b * p.H));
+                                s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+                            }
+                        }
+                        *reinterpret_cast<uint2*>(p.y + (size_t)t * p.H + c) =
+                            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const bool gave_up = *abort != 0;
+    if (gave_up) {  // copies in flight land before the block's shared memory goes
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+        if (threadIdx.x == 0) atomicOr(reinterpret_cast<int*>(p.status), 1);
+    }
+    // no expert at all: zeros; a wait that ran out: NaN
+    if (gave_up || n.total == 0) {
+        const __nv_bfloat16 v = __float2bfloat16_rn(gave_up ? __int_as_float(0x7fffffff) : 0.0f);
+        const int at = gave_up ? 0 : (int)blockIdx.x, step = gave_up ? 1 : (int)gridDim.x;
+        for (long long i = (long long)at * kDcThreads + threadIdx.x; i < (long long)p.T * p.H; i += (long long)step * kDcThreads)
+            p.y[i] = v;
+    }
+}
+
+// ----------------------------------------------------------------- launches
+int cdiv_i(long long a, int b) { return (int)((a + b - 1) / b); }
+size_t up256_d(size_t v) { return (v + 255) / 256 * 256; }
+
+// K ranges: jobs of about an eighth of an SM's share, so that the last ones to end
+// end together, and of eight stages (128 KB of weights) at least, whose ends still
+// hide under the copies in flight.
+int split_of(int stages, long long target) {
+    long long s = (stages + target / 2) / target;
+    if (s > kDcMaxSplit) s = kDcMaxSplit;
+    return (int)(s < 1 ? 1 : s);
+}
+
+struct DecodePlan {
+    int kp1, kp1s, kp2, kp2s, counters, joined, nt;
+    size_t logits, count, act, act_s, part1, part1s, part2, part2s, bytes;
+};
+DecodePlan decode_plan(const moe_decode_shape& s) {
+    DecodePlan d = {};
+    const long long slots = (long long)s.T * s.k;
+    // experts in use, as even routing has it
+    const double used = s.E * (1.0 - pow(1.0 - (double)s.k / s.E, (double)s.T));
+    const int st1 = cdiv_i(s.H, 64), st2 = cdiv_i(s.I, 64), st2s = cdiv_i(s.Is, 64);
+    const int tiles1 = cdiv_i(s.I, 64), tiles1s = cdiv_i(s.Is, 64), tiles2 = cdiv_i(s.H, 128);
+    const double total = used * ((double)tiles1 * st1 + (double)tiles2 * st2) + (double)tiles1s * st1 + (double)tiles2 * st2s;
+    long long target = (long long)(total / (152 * 8));
+    if (target < 8) target = 8;
+    d.kp1 = split_of(st1, target);
+    d.kp1s = s.Is ? split_of(st1, target) : 1;
+    d.kp2 = split_of(st2, target);
+    d.kp2s = s.Is ? split_of(st2s, target) : 1;
+    d.nt = s.T <= 8 ? 1 : s.T <= 16 ? 2 : s.T <= 32 ? 4 : 8;
+    const int groups = (int)slots + 1;
+    d.joined = 16 + tiles2 + groups;  // ticket and status; column tiles; groups
+    d.counters = d.joined + (d.kp1 > 1 || d.kp1s > 1 ? groups * (tiles1 > tiles1s ? tiles1 : tiles1s) : 0);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up256_d(bytes);
+        return o;
+    };
+    d.count = take((size_t)d.counters * 4);
+    d.logits = take((size_t)s.T * s.E * 4);
+    d.act = take((size_t)slots * s.I * 2);
+    d.act_s = take((size_t)s.T * s.Is * 2);
+    d.part1 = take(d.kp1 > 1 ? (size_t)slots * d.kp1 * 2 * s.I * 4 : 0);
+    d.part1s = take(d.kp1s > 1 ? (size_t)s.T * d.kp1s * 2 * s.Is * 4 : 0);
+    d.part2 = take((size_t)slots * d.kp2 * s.H * 4);
+    d.part2s = take(s.Is ? (size_t)s.T * d.kp2s * s.H * 4 : 0);
+    d.bytes = at;
+    return d;
+}
+
+template <int kNt>
+int launch_experts(const DecodeArgs& a0, const CUtensorMap (&m)[4], int sms, bool after_own, cudaStream_t st) {
+    static SmemLimit limit;
+    DecodeArgs a = a0;
+    const int slots = a.T * a.k, most = 227 * 1024 - 64;
+    a.stages = (most - 1024 - dc_table_bytes(slots) - dc_bar_bytes(16)) / dc_stage_bytes(kNt);
+    if (a.stages > 16) a.stages = 16;
+    const int bytes = 1024 + a.stages * dc_stage_bytes(kNt) + dc_bar_bytes(a.stages) + dc_table_bytes(slots);
+    if (const int e = limit.allow(decode_experts_kernel<kNt>, most)) return e;
+    long long jobs = (long long)(slots < a.E ? slots : a.E) * cdiv_i(a.I, 64) * a.kp1 + (long long)cdiv_i(a.Is, 64) * a.kp1s;
+    const long long down = (long long)(slots < a.E ? slots : a.E) * cdiv_i(a.H, 128) * a.kp2;
+    if (down > jobs) jobs = down;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(jobs < sms ? jobs : sms));
+    cfg.blockDim = dim3(kDcThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_own ? 1 : 0;
+    trace_pre(st);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_experts_kernel<kNt>, m[0], m[1], m[2], m[3], a);
+    trace_post(st, "decode_experts");
+    return (int)(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+template <int kTok>
+int launch_router(const moe_decode_shape& s, const DecodePtrs& f, const DecodePlan& d, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = kRtCluster;
+    cfg.gridDim = dim3((unsigned)cdiv_i(s.E, 32), (unsigned)cdiv_i(s.T, kTok), kRtCluster);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    trace_pre(st);
+    const cudaError_t e = cudaLaunchKernelEx(
+        &cfg, decode_router_kernel<kTok>, static_cast<const __nv_bfloat16*>(f.x), static_cast<const __nv_bfloat16*>(f.router),
+        s.T, s.H, s.E, reinterpret_cast<float*>(f.ws + d.logits), reinterpret_cast<int*>(f.ws + d.count), d.counters);
+    trace_post(st, "decode_router");
+    return (int)(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes(const moe_decode_shape& s) { return decode_plan(s).bytes; }
+
+int launch_decode(const moe_decode_shape& s, const DecodePtrs& f, int sms, cudaStream_t st) {
+    const DecodePlan d = decode_plan(s);
+    int* count = reinterpret_cast<int*>(f.ws + d.count);
+    DecodeArgs a = {};
+    a.T = s.T, a.H = s.H, a.I = s.I, a.E = s.E, a.k = s.k, a.Is = s.Is;
+    a.clamp = s.activation_clamp > 0.0f ? s.activation_clamp : INFINITY;
+    a.kp1 = d.kp1, a.kp1s = d.kp1s, a.kp2 = d.kp2, a.kp2s = d.kp2s;
+    a.x = static_cast<const __nv_bfloat16*>(f.x);
+    a.logits = f.router ? reinterpret_cast<const float*>(f.ws + d.logits) : nullptr;
+    a.topk_idx = f.topk_idx;
+    a.topk_w = f.topk_w;
+    a.act = reinterpret_cast<__nv_bfloat16*>(f.ws + d.act);
+    a.act_s = reinterpret_cast<__nv_bfloat16*>(f.ws + d.act_s);
+    a.part1 = reinterpret_cast<float*>(f.ws + d.part1);
+    a.part1s = reinterpret_cast<float*>(f.ws + d.part1s);
+    a.part2 = reinterpret_cast<float*>(f.ws + d.part2);
+    a.part2s = reinterpret_cast<float*>(f.ws + d.part2s);
+    a.ticket = count;
+    a.status = count + 1;
+    a.tiles_done = count + 16;
+    a.done = a.tiles_done + cdiv_i(s.H, 128);
+    a.joined = count + d.joined;
+    a.y = static_cast<__nv_bfloat16*>(f.y);
+    int rc;
+    CUtensorMap m[4] = {};
+    if ((rc = abi_map_nd(&m[0], f.W1, 2, {s.I, 2, s.H, s.E}, {64, 1, 64, 1}, "W1 (gate/up halves)"))) return rc;
+    if ((rc = abi_map_nd(&m[1], f.W2, 2, {s.H, s.I, s.E}, {64, 64, 1}, "W2"))) return rc;
+    if (s.Is) {
+        if ((rc = abi_map_nd(&m[2], f.S1, 2, {s.Is, 2, s.H, 1}, {64, 1, 64, 1}, "S1 (gate/up halves)"))) return rc;
+        if ((rc = abi_map_nd(&m[3], f.S2, 2, {s.H, s.Is, 1}, {64, 64, 1}, "S2"))) return rc;
+    }
+    int e;
+    if (f.router) {
+        e = s.T == 1 ? launch_router<1>(s, f, d, st) : launch_router<8>(s, f, d, st);
+    } else {
+        e = (int)cudaMemsetAsync(count, 0, (size_t)d.counters * 4, st);
+    }
+    if (e) return abi_cuda_fail(e, "router launch");
+    const bool own = f.router != nullptr;
+    e = d.nt == 1   ? launch_experts<1>(a, m, sms, own, st)
+        : d.nt == 2 ? launch_experts<2>(a, m, sms, own, st)
+        : d.nt == 4 ? launch_experts<4>(a, m, sms, own, st)
+                    : launch_experts<8>(a, m, sms, own, st);
+    return e ? abi_cuda_fail(e, "decoding experts launch") : MOE_OK;
+}
+
+}  // namespace moe

@@ -198,6 +198,18 @@ LinearSizes linear_sizes(const moe_linear_shape& s);
 int launch_linear_forward(const moe_linear_shape& s, const LinearPtrs& f, cudaStream_t st);
 int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaStream_t st);
 
+// ------------------------------------------------ expert layer of decoding
+struct DecodePtrs {
+    const void *x, *router, *W1, *W2, *S1, *S2;
+    int32_t* topk_idx;
+    float* topk_w;
+    uint8_t* ws;
+    void* y;
+};
+size_t decode_workspace_bytes(const moe_decode_shape& s);
+// MOE_OK or an error code with its message set.
+int launch_decode(const moe_decode_shape& s, const DecodePtrs& f, int sms, cudaStream_t st);
+
 // Layout of the three workspaces (host only).
 int compute_layout(const moe_shape* s, moe_layout* L);
 

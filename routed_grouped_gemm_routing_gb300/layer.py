@@ -8,6 +8,9 @@ PyTorch only allocates the buffers and supplies the stream.
 """
 from __future__ import annotations
 
+import contextlib
+import ctypes
+
 import torch
 
 from . import binding as B
@@ -168,6 +171,99 @@ class FP8Experts:
         return y
 
     __call__ = forward
+
+
+class DecodeLayer:
+    """The whole expert layer for the few tokens of decoding (up to 64, k times
+    which up to 1024): router, top-k and softmax, routed experts, shared expert and
+    their sum, from the bf16 weights of training, in two kernels.
+
+    router bf16 [H, E] (None: the routing is given to each call); W1 bf16 [E, H, 2I]
+    (gate | up) and W2 bf16 [E, I, H] as ``moe_layer``'s; S1 [H, 2 Is] and S2 [Is, H]
+    a shared expert, or None.  H, I and Is multiples of 8.  Keeps the weights as they
+    are (contiguous ones are not copied).  activation_clamp as in ``moe_layer``, for
+    both kinds of experts.  Not differentiable."""
+
+    def __init__(self, router, W1, W2, k: int, S1=None, S2=None, activation_clamp: float = 0.0):
+        E, H, I2 = W1.shape
+        I = I2 // 2
+        if I2 % 2 or tuple(W2.shape) != (E, I, H):
+            raise ValueError("expected W1 [E,H,2I], W2 [E,I,H]")
+        if router is not None and tuple(router.shape) != (H, E):
+            raise ValueError(f"expected router [{H}, {E}], got {list(router.shape)}")
+        if (S1 is None) != (S2 is None):
+            raise ValueError("a shared expert needs both S1 and S2")
+        Is = 0 if S1 is None else S2.shape[0]
+        if S1 is not None and (tuple(S1.shape) != (H, 2 * Is) or tuple(S2.shape) != (Is, H) or Is < 1):
+            raise ValueError(f"expected S1 [{H}, 2 Is], S2 [Is, {H}], got {list(S1.shape)} and {list(S2.shape)}")
+        weights = [router, W1, W2, S1, S2]
+        for n, t in zip(("router", "W1", "W2", "S1", "S2"), weights):
+            if t is None:
+                continue
+            if t.dtype != torch.bfloat16 or not t.is_cuda:
+                raise TypeError(f"{n} must be a bfloat16 CUDA tensor")
+            if t.get_device() != W1.get_device():
+                raise ValueError(f"{n} is on {t.device}, W1 on {W1.device}")
+        self.router, self.W1, self.W2, self.S1, self.S2 = (None if t is None else t.detach().contiguous() for t in weights)
+        self.E, self.H, self.I, self.k, self.Is = E, H, I, int(k), Is
+        self.activation_clamp = float(activation_clamp)
+        self._sizes = {}  # T -> shape, reference to it, workspace bytes
+        self._size(1)  # sizes that the kernels do not take are refused here
+        self._ptrs = [None if t is None else t.data_ptr() for t in (self.router, self.W1, self.W2, self.S1, self.S2)]
+
+    def _size(self, T):
+        if T not in self._sizes:
+            if T > B.DECODE_MAX_T or T * self.k > B.DECODE_MAX_SLOTS:
+                raise ValueError(f"a decoding layer takes up to {B.DECODE_MAX_T} tokens with {B.DECODE_MAX_SLOTS} picks in "
+                                 f"all, got {T} with {self.k} each (moe_layer takes more)")
+            s = B.MoeDecodeShape(T, self.H, self.I, self.E, self.k, self.Is, self.activation_clamp)
+            self._sizes[T] = (s, ctypes.byref(s), max(B.moe_decode_workspace(s), 16))
+        return self._sizes[T]
+
+    def forward(self, x, topk_idx=None, topk_w=None, out=None, return_routing: bool = False):
+        """y bf16 [T, H] for x bf16 [T, H]; with return_routing (y, topk_idx int32
+        [T, k], topk_w f32 [T, k]).  topk_idx int [T, k] and topk_w float [T, k]: the
+        routing, of a layer without a router (ids outside the experts count for
+        nothing)."""
+        if x.dim() != 2 or x.shape[1] != self.H:
+            raise ValueError(f"expected x [T, {self.H}], got {list(x.shape)}")
+        T, dev = x.shape[0], self.W1.get_device()
+        s, ref, size = self._size(T)
+        if self.router is None:
+            if topk_idx is None or topk_w is None or topk_idx.shape != (T, self.k) or topk_w.shape != (T, self.k):
+                raise ValueError(f"a layer without a router needs topk_idx and topk_w [{T}, {self.k}]")
+            topk_idx, topk_w = topk_idx.to(torch.int32).contiguous(), topk_w.to(torch.float32).contiguous()
+        elif topk_idx is not None or topk_w is not None:
+            raise ValueError("this layer has a router of its own")
+        with _on_device(x, dev):
+            if self.router is not None:
+                topk_idx = torch.empty((T, self.k), dtype=torch.int32, device=x.device)
+                topk_w = torch.empty((T, self.k), dtype=torch.float32, device=x.device)
+            ws = torch.empty((size,), dtype=torch.uint8, device=x.device)
+            y = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device) if out is None else out
+            if (x.dtype is torch.bfloat16 and x.is_contiguous() and out is None and topk_idx.get_device() == dev
+                    and topk_w.get_device() == dev):
+                r, W1, W2, S1, S2 = self._ptrs
+                rc = B.lib().moe_decode_forward(
+                    ref, x.data_ptr(), r, W1, W2, S1, S2, topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(),
+                    y.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+                if rc:
+                    B._check(rc)
+            else:
+                B.moe_decode_forward(s, x if x.is_contiguous() else x.contiguous(), self.router, self.W1, self.W2, self.S1,
+                                     self.S2, topk_idx, topk_w, ws, y)
+        return (y, topk_idx, topk_w) if return_routing else y
+
+    __call__ = forward
+
+
+def _on_device(x, dev):
+    """Context in which device dev, where x has to be, is current."""
+    if x.get_device() != dev:
+        if not x.is_cuda:
+            raise TypeError("x must be a CUDA tensor")
+        raise ValueError(f"x is on {x.device}, the weights on cuda:{dev}")
+    return contextlib.nullcontext() if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def train_step_from_host(x_h, topk_idx_h, topk_w_h, dY_h, W1, W2, ws: MoEWorkspace, outs: dict):
