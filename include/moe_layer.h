@@ -466,11 +466,12 @@ typedef struct moe_linear_shape {
     int32_t activation;
 } moe_linear_shape;
 
-/* Bytes of the scratch of both calls (calls that share one must not overlap;
- * nothing in it lasts from call to call but the status).  Word 0 is a status
- * word: the caller zeroes it once; bit 0 is set when a kernel gave up on a
- * bounded wait, and stays set.  Host only. */
-int moe_linear_workspace(const moe_linear_shape* shape, size_t* bytes);
+/* Bytes of the scratch of the forward (backward 0) or the backward (1).  Calls that
+ * overlap on the GPU need scratch of their own, unless it is 256 bytes: those hold
+ * the status alone, nothing else lasts from call to call.  Word 0 is a status word:
+ * the caller zeroes it once; bit 0 is set when a kernel gave up on a bounded wait,
+ * and stays set.  Host only. */
+int moe_linear_workspace(const moe_linear_shape* shape, int32_t backward, size_t* bytes);
 
 /* Forward: overwrites y bf16 [T, N], and z f32 [T, N] where it is not NULL (what
  * the backward of an activation reads).  bias [N] of bias_type (MOE_BF16 or

@@ -116,7 +116,7 @@ def lib():
             L.moe_ffn_workspace_layout.argtypes = [P(MoeFFNShape), P(MoeFFNLayout)]
             L.moe_ffn_forward.argtypes = [P(MoeFFNShape), vp, vp, vp, i32, vp, vp, vp, vp]
             L.moe_ffn_backward.argtypes = [P(MoeFFNShape)] + [vp] * 10
-            L.moe_linear_workspace.argtypes = [P(MoeLinearShape), P(ctypes.c_size_t)]
+            L.moe_linear_workspace.argtypes = [P(MoeLinearShape), i32, P(ctypes.c_size_t)]
             L.moe_linear_forward.argtypes = [P(MoeLinearShape), vp, i64, vp, vp, i32, vp, i64, vp, vp, vp, vp]
             L.moe_linear_backward.argtypes = [P(MoeLinearShape), vp, i64, vp, i64] + [vp] * 6 + [i32, vp]
             L.moe_decode_workspace.argtypes = [P(MoeDecodeShape), P(ctypes.c_size_t)]
@@ -624,10 +624,10 @@ def linear_shape(T: int, K: int, N: int, activation=None) -> MoeLinearShape:
     return MoeLinearShape(T, K, N, ACTIVATIONS[activation])
 
 
-def moe_linear_workspace(shape: MoeLinearShape) -> int:
-    """Bytes of the linear layer's scratch (both directions)."""
+def moe_linear_workspace(shape: MoeLinearShape, backward: bool) -> int:
+    """Bytes of the scratch of the linear layer's forward or backward."""
     v, ref = _size_out()
-    rc = lib().moe_linear_workspace(ctypes.byref(shape), ref)
+    rc = lib().moe_linear_workspace(ctypes.byref(shape), int(backward), ref)
     if rc:
         _check(rc)
     return v.value
@@ -645,7 +645,8 @@ def _bias_arg(bias, N, name, dev):
 def moe_linear_forward(shape: MoeLinearShape, x, W, bias, residual, z, ws, y, stream=None):
     """y = act(x W + bias) + residual (bf16; rows of x [T, K] and residual [T, N]
     may be strided; bias and residual may be None); z: None, or f32 [T, N] that
-    receives x W + bias.  ws: uint8 of moe_linear_workspace elements."""
+    receives x W + bias.  ws: uint8 of
+    moe_linear_workspace(shape, False) elements."""
     T, K, N = shape.T, shape.K, shape.N
     dev, st = _here(stream)
     px, sx = _rows_arg(x, _BF, T, K, "x", dev)
@@ -653,7 +654,7 @@ def moe_linear_forward(shape: MoeLinearShape, x, W, bias, residual, z, ws, y, st
     pb, tb = _bias_arg(bias, N, "bias", dev)
     rc = lib().moe_linear_forward(
         ctypes.byref(shape), px, sx, _arg(W, _BF, K * N, "W", dev), pb, tb, pr, sr, _arg(z, _F32, T * N, "z", dev),
-        _arg(ws, _U8, moe_linear_workspace(shape), "ws", dev), _arg(y, _BF, T * N, "y", dev), st)
+        _arg(ws, _U8, moe_linear_workspace(shape, False), "ws", dev), _arg(y, _BF, T * N, "y", dev), st)
     if rc:
         _check(rc)
 
@@ -668,7 +669,7 @@ def moe_linear_backward(shape: MoeLinearShape, dy, x, W, z, ws, dx, dW, dbias, s
     pb, tb = _bias_arg(dbias, N, "dbias", dev)
     rc = lib().moe_linear_backward(
         ctypes.byref(shape), pd, sd, px, sx, _arg(W, _BF, K * N, "W", dev), _arg(z, _F32, T * N, "z", dev),
-        _arg(ws, _U8, moe_linear_workspace(shape), "ws", dev), _arg(dx, _BF, T * K, "dx", dev),
+        _arg(ws, _U8, moe_linear_workspace(shape, True), "ws", dev), _arg(dx, _BF, T * K, "dx", dev),
         _arg(dW, _BF, K * N, "dW", dev), pb, tb, st)
     if rc:
         _check(rc)

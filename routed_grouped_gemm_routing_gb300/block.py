@@ -19,6 +19,7 @@ from . import binding as B
 _HERE = contextlib.nullcontext()
 _F32, _BF = torch.float32, torch.bfloat16
 _TYPES = B._TYPES
+_BIAS = (torch.bfloat16, torch.float32)
 _current = torch.cuda.current_device
 _stream_of = torch._C._cuda_getCurrentRawStream
 
@@ -172,21 +173,53 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5):
 # ---------------------------------------------------------- residual joint
 def _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate):
     """(rows, H, gate kind) of a call."""
-    if out.dim() != 2 or out.shape != residual.shape:
+    sh = out.shape
+    if len(sh) != 2 or sh != residual.shape:
         raise ValueError(f"expected out and residual [rows, H], got {list(out.shape)} and {list(residual.shape)}")
-    rows, H = out.shape
-    for t, n in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"), (post_bias, "post_bias")):
-        if t is not None and t.shape != (H,):
-            raise ValueError(f"expected {n} [{H}], got {list(t.shape)}")
+    rows, H = sh
+    hs = sh[1:]
+    if (weight.shape != hs or (bias is not None and bias.shape != hs) or (post_weight is not None and post_weight.shape != hs)
+            or (post_bias is not None and post_bias.shape != hs)):
+        raise ValueError(f"expected weight, bias, post_weight and post_bias [{H}]")
     if post_bias is not None and post_weight is None:
         raise ValueError("post_bias without post_weight")
     if gate is None:
         return rows, H, B.GATE_NONE
-    if gate.shape == (H,):
+    if gate.shape == hs:
         return rows, H, B.GATE_CHANNEL
     if gate.shape != (rows, 1):
         raise ValueError(f"expected gate [{H}] (per channel) or [{rows}, 1] (per token), got {list(gate.shape)}")
     return rows, H, B.GATE_TOKEN
+
+
+_joint_plans = {}  # of a call's shape and options: shape, reference to it, bytes of the backward's scratch
+
+
+def _joint_plan(rows, H, xt, wt, kind, gk, residual_scale, eps):
+    key = (rows, H, xt, wt, kind, gk, residual_scale, eps)
+    plan = _joint_plans.get(key)
+    if plan is None:
+        if len(_joint_plans) >= 1024:  # rows of every length have passed
+            _joint_plans.clear()
+        s = B.residual_norm_shape(rows, H, xt, wt, kind, gk, residual_scale, eps)
+        plan = _joint_plans[key] = (s, ctypes.byref(s), max(B.moe_residual_norm_workspace(s), 16))
+    return plan
+
+
+def _ptr_of(t):
+    return None if t is None else t.data_ptr()
+
+
+def _joint_plain(d, xt, wt, sh, gate, gk, rows, params):
+    """Whether what a call reads is contiguous, of the right types and shapes, on device d."""
+    for t in rows:
+        if t is not None and not _plain(t, xt, sh, d):
+            return False
+    hs = sh[1:]
+    for t in params:
+        if t is not None and not _plain(t, wt, hs, d):
+            return False
+    return gate is None or (gate.dtype is wt and gate.get_device() == d and gate.is_contiguous())
 
 
 def residual_norm_forward(out, residual, weight, bias=None, post_weight=None, post_bias=None, gate=None,
@@ -200,7 +233,18 @@ def residual_norm_forward(out, residual, weight, bias=None, post_weight=None, po
     Parameters and gate in out's type or all f32.  stats (f32 [4, rows]) is what
     residual_norm_backward reads."""
     rows, H, gk = _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate)
-    s = B.residual_norm_shape(rows, H, out.dtype, weight.dtype, kind, gk, residual_scale, eps)
+    xt, wt, d = out.dtype, weight.dtype, out.get_device()
+    s, ref, _ = _joint_plan(rows, H, xt, wt, kind, gk, residual_scale, eps)
+    if d >= 0 and d == _current() and _joint_plain(d, xt, wt, out.shape, gate, gk, (out, residual),
+                                                   (weight, bias, post_weight, post_bias)):
+        stream, normed = torch.empty_like(out), torch.empty_like(out)
+        stats = torch.empty((4, rows), dtype=_F32, device=out.device)
+        rc = B.lib().moe_residual_norm_forward(
+            ref, out.data_ptr(), H, residual.data_ptr(), H, _ptr_of(gate), _ptr_of(post_weight), _ptr_of(post_bias),
+            weight.data_ptr(), _ptr_of(bias), stream.data_ptr(), normed.data_ptr(), stats.data_ptr(), _stream_of(d))
+        if rc:
+            B._check(rc)
+        return stream, normed, stats
     with _on(out):
         dev = out.device
         stream = torch.empty((rows, H), dtype=out.dtype, device=dev)
@@ -221,14 +265,28 @@ def residual_norm_backward(dstream, dnormed, out, residual, weight, stats, bias=
             raise ValueError(f"expected {n} [{rows}, {H}], got {list(t.shape)}")
     if stats.shape != (4, rows):
         raise ValueError(f"expected the forward's stats [4, {rows}], got {list(stats.shape)}")
-    s = B.residual_norm_shape(rows, H, out.dtype, weight.dtype, kind, gk, residual_scale)
+    xt, wt, d = out.dtype, weight.dtype, out.get_device()
+    s, ref, size = _joint_plan(rows, H, xt, wt, kind, gk, residual_scale, 1e-5)
+    if (d >= 0 and d == _current() and _plain(stats, _F32, (4, rows), d)
+            and _joint_plain(d, xt, wt, out.shape, gate, gk, (out, residual, dstream, dnormed),
+                             (weight, bias, post_weight, post_bias))):
+        dout, dres, dw = torch.empty_like(out), torch.empty_like(out), torch.empty_like(weight)
+        db, dpw, dpb, dg = (None if p is None else torch.empty_like(p) for p in (bias, post_weight, post_bias, gate))
+        ws = torch.empty((size,), dtype=torch.uint8, device=out.device)
+        rc = B.lib().moe_residual_norm_backward(
+            ref, _ptr_of(dstream), H, _ptr_of(dnormed), H, out.data_ptr(), H, residual.data_ptr(), H, _ptr_of(gate),
+            _ptr_of(post_weight), _ptr_of(post_bias), weight.data_ptr(), stats.data_ptr(), ws.data_ptr(), dout.data_ptr(),
+            dres.data_ptr(), dw.data_ptr(), _ptr_of(db), _ptr_of(dpw), _ptr_of(dpb), _ptr_of(dg), _stream_of(d))
+        if rc:
+            B._check(rc)
+        return dout, dres, dw, db, dpw, dpb, dg
     with _on(out):
         dev = out.device
         dout = torch.empty((rows, H), dtype=out.dtype, device=dev)
         dres = torch.empty((rows, H), dtype=out.dtype, device=dev)
         dw, db, dpw, dpb, dg = (None if p is None else torch.empty(p.shape, dtype=weight.dtype, device=dev)
                                 for p in (weight, bias, post_weight, post_bias, gate))
-        ws = torch.empty((max(B.moe_residual_norm_workspace(s), 16),), dtype=torch.uint8, device=dev)
+        ws = torch.empty((size,), dtype=torch.uint8, device=dev)
         B.moe_residual_norm_backward(s, dstream, dnormed, out, residual, gate, post_weight, post_bias, weight, stats, ws,
                                      dout, dres, dw, db, dpw, dpb, dg)
     return dout, dres, dw, db, dpw, dpb, dg
@@ -429,9 +487,12 @@ def gated_ffn(x, W1, W2, workspace: FFNWorkspace | None = None, activation_clamp
 # ------------------------------------------------------------ linear layer
 @functools.lru_cache(maxsize=256)
 def _linear_plan(T, K, N, activation):
-    """(shape, reference to it, bytes of scratch)."""
+    """(shape, reference to it, bytes of the forward's and of the backward's scratch)."""
     s = B.linear_shape(T, K, N, activation)
-    return s, ctypes.byref(s), B.moe_linear_workspace(s)
+    return s, ctypes.byref(s), B.moe_linear_workspace(s, False), B.moe_linear_workspace(s, True)
+
+
+_no_sums = {}  # of a device: scratch of forwards that keep nothing but a status word there
 
 
 class LinearWorkspace:
@@ -442,7 +503,7 @@ class LinearWorkspace:
     def __init__(self, T: int, K: int, N: int, activation=None, device=None):
         dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self.shape = (T, K, N, activation)
-        self.ws = torch.empty(_linear_plan(*self.shape)[2], dtype=torch.uint8, device=dev)
+        self.ws = torch.empty(max(_linear_plan(*self.shape)[2:]), dtype=torch.uint8, device=dev)
         self.ws[:16].zero_()
 
     def status(self) -> int:
@@ -452,7 +513,15 @@ class LinearWorkspace:
 
 def _linear_ws(workspace, plan_of, size, dev):
     if workspace is None:
-        return torch.empty((size,), dtype=torch.uint8, device=dev)
+        if size > 256:
+            return torch.empty((size,), dtype=torch.uint8, device=dev)
+        if dev not in _no_sums:
+            # (made under a capture it would belong to that graph's memory)
+            ws = torch.empty((256,), dtype=torch.uint8, device=dev)
+            if torch.cuda.is_current_stream_capturing():
+                return ws
+            _no_sums[dev] = ws
+        return _no_sums[dev]
     if workspace.shape != plan_of:
         raise ValueError(f"the workspace was made for (T, K, N, activation) = {workspace.shape}, the call has {plan_of}")
     return workspace.ws
@@ -493,24 +562,24 @@ def linear_forward(x, W, bias=None, residual=None, activation=None, for_backward
     rows of x and residual may be strided by multiples of 8.  activation: None,
     "silu", "gelu" (with erf) or "gelu_tanh".  z = x W + bias f32 [T, N] with
     for_backward and an activation, else None."""
-    plan_of, (s, ref, size) = _linear_dims(x, W, bias, residual, activation)
+    plan_of, (s, ref, size, _) = _linear_dims(x, W, bias, residual, activation)
     T, K, N, _ = plan_of
-    d = x.get_device()
+    d, dev = x.get_device(), x.device
+    if (d >= 0 and d == _current() and _plain(x, _BF, (T, K), d) and _plain(W, _BF, (K, N), d)
+            and (bias is None or (bias.dtype in _BIAS and _plain(bias, bias.dtype, (N,), d)))
+            and (residual is None or _plain(residual, _BF, (T, N), d)) and (workspace is None or workspace.ws.get_device() == d)):
+        y = torch.empty((T, N), dtype=_BF, device=dev)
+        z = torch.empty((T, N), dtype=_F32, device=dev) if for_backward and activation is not None else None
+        rc = B.lib().moe_linear_forward(
+            ref, x.data_ptr(), K, W.data_ptr(), _ptr_of(bias), 0 if bias is None else _TYPES[bias.dtype], _ptr_of(residual),
+            N, _ptr_of(z), _linear_ws(workspace, plan_of, size, dev).data_ptr(), y.data_ptr(), _stream_of(d))
+        if rc:
+            B._check(rc)
+        return y, z
     with _on(x):
-        y = torch.empty((T, N), dtype=_BF, device=x.device)
-        z = torch.empty((T, N), dtype=_F32, device=x.device) if for_backward and activation is not None else None
-        ws = _linear_ws(workspace, plan_of, size, x.device)
-        if (_plain(x, _BF, (T, K), d) and _plain(W, _BF, (K, N), d) and ws.get_device() == d
-                and (bias is None or (bias.dtype in (_BF, _F32) and _plain(bias, bias.dtype, (N,), d)))
-                and (residual is None or _plain(residual, _BF, (T, N), d))):
-            rc = B.lib().moe_linear_forward(
-                ref, x.data_ptr(), K, W.data_ptr(), None if bias is None else bias.data_ptr(),
-                0 if bias is None else _TYPES[bias.dtype], None if residual is None else residual.data_ptr(), N,
-                None if z is None else z.data_ptr(), ws.data_ptr(), y.data_ptr(), _stream_of(d))
-            if rc:
-                B._check(rc)
-        else:
-            B.moe_linear_forward(s, x, W, bias, residual, z, ws, y)
+        y = torch.empty((T, N), dtype=_BF, device=dev)
+        z = torch.empty((T, N), dtype=_F32, device=dev) if for_backward and activation is not None else None
+        B.moe_linear_forward(s, x, W, bias, residual, z, _linear_ws(workspace, plan_of, size, dev), y)
     return y, z
 
 
@@ -520,7 +589,7 @@ def linear_backward(dy, x, W, z=None, bias=None, activation=None, want=(True, Tr
     (z: its second output, with for_backward; None without an activation).  dbias
     has bias's type, None without one.  want: whether dx and dW are; None is
     returned for one that is not.  The residual's gradient is dy."""
-    plan_of, (s, ref, size) = _linear_dims(x, W, bias, None, activation)
+    plan_of, (s, ref, _, size) = _linear_dims(x, W, bias, None, activation)
     T, K, N, _ = plan_of
     if dy.shape != (T, N):
         raise ValueError(f"expected dy [{T}, {N}], got {list(dy.shape)}")
@@ -530,17 +599,16 @@ def linear_backward(dy, x, W, z=None, bias=None, activation=None, want=(True, Tr
     with _on(x):
         dx = torch.empty((T, K), dtype=_BF, device=x.device) if want[0] else None
         dW = torch.empty((K, N), dtype=_BF, device=x.device) if want[1] else None
-        db = None if bias is None else torch.empty((N,), dtype=bias.dtype, device=x.device)
+        db = None if bias is None else torch.empty_like(bias)
         ws = _linear_ws(workspace, plan_of, size, x.device)
         if activation is None:
             z = None
         if (_plain(dy, _BF, (T, N), d) and _plain(x, _BF, (T, K), d) and _plain(W, _BF, (K, N), d)
                 and ws.get_device() == d and (z is None or _plain(z, _F32, (T, N), d))
-                and (db is None or bias.dtype in (_BF, _F32))):
+                and (db is None or bias.dtype in _BIAS)):
             rc = B.lib().moe_linear_backward(
-                ref, dy.data_ptr(), N, x.data_ptr(), K, W.data_ptr(), None if z is None else z.data_ptr(), ws.data_ptr(),
-                None if dx is None else dx.data_ptr(), None if dW is None else dW.data_ptr(),
-                None if db is None else db.data_ptr(), 0 if db is None else _TYPES[db.dtype], _stream_of(d))
+                ref, dy.data_ptr(), N, x.data_ptr(), K, W.data_ptr(), _ptr_of(z), ws.data_ptr(), _ptr_of(dx), _ptr_of(dW),
+                _ptr_of(db), 0 if db is None else _TYPES[db.dtype], _stream_of(d))
             if rc:
                 B._check(rc)
         else:

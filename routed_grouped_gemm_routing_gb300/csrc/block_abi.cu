@@ -312,12 +312,12 @@ int moe_ffn_backward(const moe_ffn_shape* shape, const void* dY, const void* x, 
     return launch_ffn_backward(*shape, f, st);
 }
 
-int moe_linear_workspace(const moe_linear_shape* shape, size_t* bytes) {
+int moe_linear_workspace(const moe_linear_shape* shape, int32_t backward, size_t* bytes) {
     if (!bytes) return abi_fail(MOE_EINVAL, "bytes is NULL");
     const int rc = check_linear(shape);
     if (rc) return rc;
     const LinearSizes z = linear_sizes(*shape);
-    *bytes = 256 + up256((size_t)z.part) + up256((size_t)z.dz) + up256((size_t)z.sums);
+    *bytes = 256 + (backward ? up256((size_t)z.dz) + up256((size_t)z.sums) : up256((size_t)z.part));
     return MOE_OK;
 }
 
@@ -389,8 +389,8 @@ int moe_linear_backward(const moe_linear_shape* shape, const void* dy, int64_t d
     f.W = W;
     f.z = const_cast<float*>(z);
     f.status = reinterpret_cast<int32_t*>(w);
-    f.dz = w + 256 + up256((size_t)sz.part);
-    f.sums = reinterpret_cast<float*>(w + 256 + up256((size_t)sz.part) + up256((size_t)sz.dz));
+    f.dz = w + 256;
+    f.sums = reinterpret_cast<float*>(w + 256 + up256((size_t)sz.dz));
     f.dx = dx;
     f.dW = dW;
     f.db = dbias;

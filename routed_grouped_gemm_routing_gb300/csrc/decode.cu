@@ -34,6 +34,8 @@
 // Deterministic.
 #include <math.h>
 
+#include <type_traits>
+
 #include "clamp.cuh"
 #include "grouped_gemm_2sm.cuh"
 #include "smem_limit.h"
@@ -47,14 +49,14 @@ constexpr int kDcThreads = 320;
 constexpr int kDcBox = 8192;    // 64 of K x 64 columns
 constexpr int kDcJobs = 4;      // jobs drawn ahead
 constexpr int kDcMaxSplit = 16;
-constexpr int kRtCluster = 8, kRtRows = 512;  // of the router: blocks of a cluster, rows of x held at once
+constexpr int kRtCluster = 8, kRtRows = 1024;  // of the router: blocks of a cluster, rows of x held at once
 
 // ----------------------------------------------------------------- router
 template <int kTok>
 __global__ void __launch_bounds__(256)
     decode_router_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ R, int T, int H, int E,
                          float* __restrict__ logits, int* __restrict__ counters, int n_counters) {
-    __shared__ __align__(16) float xs[kRtRows][kTok];
+    __shared__ __align__(16) float xs[kTok == 1 ? 1 : kRtRows][kTok];
     __shared__ float red[8][kTok][32];
     __shared__ float all[kRtCluster][kTok][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -72,29 +74,52 @@ __global__ void __launch_bounds__(256)
     for (int t = 0; t < kTok; ++t)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[t][j] = 0.0f;
+    // rows of R whose loads are in flight together: what the router takes is latency
+    constexpr int kAhead = kTok == 1 ? 16 : 4;
     for (int c0 = h0; c0 < h1; c0 += kRtRows) {
         const int rows = h1 - c0 < kRtRows ? h1 - c0 : kRtRows;
-        __syncthreads();
-        for (int i = tid; i < kTok * rows; i += 256) {
-            const int t = i / rows, r = i - t * rows;
-            xs[r][t] = t0 + t < T ? __bfloat162float(x[(size_t)(t0 + t) * H + c0 + r]) : 0.0f;
+        if constexpr (kTok > 1) {
+            __syncthreads();
+            for (int i = tid; i < kTok * rows; i += 256) {
+                const int t = i / rows, r = i - t * rows;
+                xs[r][t] = t0 + t < T ? __bfloat162float(x[(size_t)(t0 + t) * H + c0 + r]) : 0.0f;
+            }
+            __syncthreads();
         }
-        __syncthreads();
         if (e < E) {
-#pragma unroll 2
-            for (int r = rl; r < rows; r += 64) {
-                float w[8];
-                const __nv_bfloat16* src = R + (size_t)(c0 + r) * E + e;
-                if (whole) {
-                    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(src)), w);
-                } else {
+            for (int r0 = rl; r0 < rows; r0 += 64 * kAhead) {
+                uint4 u[kAhead];
+                float x1[kAhead];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = e + j < E ? __bfloat162float(src[j]) : 0.0f;
+                for (int a = 0; a < kAhead; ++a) {
+                    const int r = r0 + 64 * a;
+                    u[a] = make_uint4(0, 0, 0, 0);
+                    x1[a] = 0.0f;
+                    if (r >= rows) continue;
+                    const __nv_bfloat16* src = R + (size_t)(c0 + r) * E + e;
+                    if (whole) {
+                        u[a] = __ldg(reinterpret_cast<const uint4*>(src));
+                    } else {
+                        uint16_t h[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) h[j] = e + j < E ? reinterpret_cast<const uint16_t*>(src)[j] : 0;
+                        u[a] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                    }
+                    if constexpr (kTok == 1) x1[a] = __bfloat162float(x[(size_t)t0 * H + c0 + r]);
                 }
 #pragma unroll
-                for (int t = 0; t < kTok; ++t)
+                for (int a = 0; a < kAhead; ++a) {
+                    const int r = r0 + 64 * a;
+                    if (r >= rows) continue;
+                    float w[8];
+                    unpack_bf16x8(u[a], w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xs[r][t], w[j], acc[t][j]);
+                    for (int t = 0; t < kTok; ++t) {
+                        const float v = kTok == 1 ? x1[a] : xs[r][t];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(v, w[j], acc[t][j]);
+                    }
+                }
             }
         }
     }
@@ -139,7 +164,7 @@ struct DecodeArgs {
     const float* logits;  // null: the routing is given
     int32_t* topk_idx;    // [T][k], written, or read without logits
     float* topk_w;
-    __nv_bfloat16 *act, *act_s;  // [T k][I], [T][Is]
+    __nv_bfloat16 *act, *act_s;  // [T k][I], [T][Is]; up to 16 tokens [..][2][I]: and the rests
     float *part1, *part1s;       // [T k][kp1][2][I], [T][kp1s][2][Is]
     float *part2, *part2s;       // [T k][kp2][H], [T][kp2s][H]
     int *ticket, *done, *tiles_done, *joined;  // counters: jobs drawn, tiles of a group's activations that are there,
@@ -194,6 +219,26 @@ __device__ __forceinline__ int draw_last(int* counter, int n) {
     return last;
 }
 
+// One warp: waits until a counter that other blocks raise is at `want` and sees
+// what they wrote before; false when it gave up.
+__device__ __forceinline__ bool warp_wait_flag(const int* flag, int want, volatile int* abort) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+        const uint64_t t0 = global_timer_ns();
+        for (uint32_t it = 1;; ++it) {
+            int v;
+            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+            if (v >= want) break;
+            if ((it & 63u) == 0 && (*abort || global_timer_ns() - t0 > kWaitLimitNs)) {
+                *abort = 1;
+                ok = false;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // What every block keeps of the routing, in shared memory behind the ring.
 struct Routing {
     float* w;         // [T k]
@@ -205,27 +250,27 @@ struct Routing {
 __host__ __device__ constexpr int dc_table_bytes(int slots) {
     return slots * 4 + (slots * 2 + 15) / 16 * 16 * 2 + (slots + 8) * 2 * 3 + 32;
 }
-__host__ __device__ constexpr int dc_stage_bytes(int nt) { return 2 * kDcBox + nt * 1024; }
+// Up to 16 tokens the activations go into the down projection as two bf16 numbers
+// each, the second the rounding's rest: the outputs then err by their own rounding
+// alone, and what it costs, a second product on the same weights, is hidden there.
+__host__ __device__ constexpr bool dc_two(int nt) { return nt <= 2; }
+__host__ __device__ constexpr int dc_stage_bytes(int nt) { return 2 * kDcBox + nt * (dc_two(nt) ? 2048 : 1024); }
 __host__ __device__ constexpr int dc_bar_bytes(int stages) { return 8 * (2 * stages + 2 * kDcJobs) + 4 * kDcJobs + 16; }
 
 // One warp: the k largest of a token's E logits, as the layer's router takes them
 // (equal ones by id, a NaN as -infinity, softmax over the chosen ones).
 template <int P>
-__device__ __forceinline__ void warp_topk(const float* row, int E, int k, int* idx, float* w) {
+__device__ __forceinline__ void warp_topk(const float (&row)[P], int E, int k, int* idx, float* w) {
     const int lane = threadIdx.x & 31;
     uint32_t v[P];  // order-preserving codes
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int e = lane + 32 * i;
-        float f = e < E ? __ldcg(row + e) : -INFINITY;
-        if (isnan(f)) f = -INFINITY;
-        const uint32_t u = __float_as_uint(f == 0.0f ? 0.0f : f);
-        v[i] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    }
     uint32_t taken = 0;
 #pragma unroll
-    for (int i = 0; i < P; ++i)
+    for (int i = 0; i < P; ++i) {
+        const float f = isnan(row[i]) ? -INFINITY : row[i];
+        const uint32_t u = __float_as_uint(f == 0.0f ? 0.0f : f);
+        v[i] = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
         if (lane + 32 * i >= E) taken |= 1u << i;
+    }
     float m = 0.0f, sum = 0.0f;
     for (int j = 0; j < k; ++j) {
         uint32_t best = 0, at = 0xffffffffu;
@@ -246,64 +291,93 @@ __device__ __forceinline__ void warp_topk(const float* row, int E, int k, int* i
     for (int j = lane; j < k; j += 32) w[j] = w[j] / sum;
     __syncwarp();
 }
-__device__ __forceinline__ void warp_topk_any(const float* row, int E, int k, int* idx, float* w) {
+// All tokens, a warp each; the next one's logits come while one is chosen from.
+template <int P>
+__device__ __forceinline__ void block_topk(const float* logits, int T, int E, int k, int* idx, float* w) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = kDcThreads / 32;
+    float row[P], next[P];
+    auto load = [&](int t, float (&r)[P]) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int e = lane + 32 * i;
+            r[i] = t < T && e < E ? __ldcg(logits + (size_t)t * E + e) : -INFINITY;
+        }
+    };
+    load(warp, row);
+    for (int t = warp; t < T; t += kWarps) {
+        if (P <= 8) load(t + kWarps, next);
+        warp_topk<P>(row, E, k, idx + t * k, w + t * k);
+        if (P > 8) load(t + kWarps, next);
+#pragma unroll
+        for (int i = 0; i < P; ++i) row[i] = next[i];
+    }
+}
+__device__ __forceinline__ void block_topk_any(const float* logits, int T, int E, int k, int* idx, float* w) {
     const int p = (E + 31) / 32;
-    if (p <= 1)
-        warp_topk<1>(row, E, k, idx, w);
-    else if (p <= 2)
-        warp_topk<2>(row, E, k, idx, w);
-    else if (p <= 4)
-        warp_topk<4>(row, E, k, idx, w);
+    if (p <= 2)
+        block_topk<2>(logits, T, E, k, idx, w);
     else if (p <= 8)
-        warp_topk<8>(row, E, k, idx, w);
+        block_topk<8>(logits, T, E, k, idx, w);
     else
-        warp_topk<32>(row, E, k, idx, w);
+        block_topk<32>(logits, T, E, k, idx, w);
 }
 
 // The routing and the groups of at most `cap` slots of an expert.  Scratch (the
-// ring's place): ids [slots], counts, starts and first groups [E + 1].
+// ring's place): ids and places [slots], counts, starts and first groups [E + 1].
 __device__ void build_routing(const DecodeArgs& p, const Routing& r, int cap, int* scratch) {
     const int slots = p.T * p.k, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int *ids = scratch, *cnt = ids + slots, *start = cnt + p.E + 1, *first = start + p.E + 1;
+    int *ids = scratch, *rank = ids + slots, *cnt = rank + slots, *start = cnt + p.E + 1, *first = start + p.E + 1;
     for (int i = tid; i <= p.E; i += kDcThreads) cnt[i] = 0;
     if (p.logits) {
-        for (int t = warp; t < p.T; t += kDcThreads / 32)
-            warp_topk_any(p.logits + (size_t)t * p.E, p.E, p.k, ids + t * p.k, r.w + t * p.k);
+        block_topk_any(p.logits, p.T, p.E, p.k, ids, r.w);
     } else {
         for (int i = tid; i < slots; i += kDcThreads) ids[i] = __ldg(p.topk_idx + i), r.w[i] = __ldg(p.topk_w + i);
     }
     __syncthreads();
-    for (int i = tid; i < slots; i += kDcThreads) {
-        const int e = ids[i];
-        const bool ok = e >= 0 && e < p.E;
-        r.idx[i] = (int16_t)(ok ? e : -1);
-        if (ok) atomicAdd(cnt + e, 1);
-        if (p.logits && blockIdx.x == 0) p.topk_idx[i] = e, p.topk_w[i] = r.w[i];
-    }
-    __syncthreads();
-    if (warp == 0) {  // prefix sums of the counts and of the groups
-        int s = 0, g = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane, c = e < p.E ? cnt[e] : 0, q = (c + cap - 1) / cap;
-            int cs = c, qs = q;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int a = __shfl_up_sync(0xffffffffu, cs, d), b = __shfl_up_sync(0xffffffffu, qs, d);
-                if (lane >= d) cs += a, qs += b;
+    if (warp == 0) {
+        // each slot's place among its expert's, 32 slots at a time in order
+        for (int i0 = 0; i0 < slots; i0 += 32) {
+            const int i = i0 + lane, e = i < slots ? ids[i] : -1;
+            const bool ok = e >= 0 && e < p.E;
+            const uint32_t same = __match_any_sync(0xffffffffu, ok ? e : -1), before = same & ((1u << lane) - 1u);
+            const int base = ok ? cnt[e] : 0;
+            __syncwarp();
+            if (ok) {
+                rank[i] = base + __popc(before);
+                if (before == 0) cnt[e] = base + __popc(same);
             }
-            if (e < p.E) start[e] = s + cs - c, first[e] = g + qs - q;
-            s += __shfl_sync(0xffffffffu, cs, 31);
-            g += __shfl_sync(0xffffffffu, qs, 31);
+            __syncwarp();
         }
-        if (lane == 0) *r.n = g;
+        // prefix sums of the counts and of the groups: a run of experts a lane
+        const int run = (p.E + 31) / 32, e0 = lane * run, e1 = e0 + run < p.E ? e0 + run : p.E;
+        int s = 0, g = 0;
+        for (int e = e0; e < e1; ++e) s += cnt[e], g += (cnt[e] + cap - 1) / cap;
+        const int s0 = s, g0 = g;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, s, d), b = __shfl_up_sync(0xffffffffu, g, d);
+            if (lane >= d) s += a, g += b;
+        }
+        const int all = __shfl_sync(0xffffffffu, g, 31);
+        s -= s0;
+        g -= g0;
+        for (int e = e0; e < e1; ++e) {
+            start[e] = s, first[e] = g;
+            s += cnt[e], g += (cnt[e] + cap - 1) / cap;
+        }
+        if (lane == 0) *r.n = all;
+    } else {
+        for (int i = tid - 32; i < slots; i += kDcThreads - 32) {
+            const int e = ids[i];
+            r.idx[i] = (int16_t)(e >= 0 && e < p.E ? e : -1);
+            if (p.logits && blockIdx.x == 0) p.topk_idx[i] = e, p.topk_w[i] = r.w[i];
+        }
     }
     __syncthreads();
     for (int i = tid; i < slots; i += kDcThreads) {
         const int e = r.idx[i];
-        if (e < 0) continue;
-        int rank = 0;
-        for (int j = 0; j < i; ++j) rank += r.idx[j] == e;
-        r.list[start[e] + rank] = (uint16_t)i;
+        if (e >= 0) r.list[start[e] + rank[i]] = (uint16_t)i;
     }
     for (int e = tid; e < p.E; e += kDcThreads)
         for (int q = 0; q * cap < cnt[e]; ++q) {
@@ -361,6 +435,7 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     volatile int* abort = &abort_word;
     const uint32_t raw = smem_addr(smem_raw), ring = (raw + 1023u) & ~1023u;
     constexpr uint32_t kStage = dc_stage_bytes(kNt);
+    constexpr bool kTwo = dc_two(kNt);
     uint8_t* tail = smem_raw + (ring - raw) + p.stages * kStage;
     const uint32_t bar0 = smem_addr(tail);
     auto full = [&](int s) { return bar0 + 8u * s; };
@@ -466,27 +541,14 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                         s = rt.list[rt.gb[q.group] + r];
                         if (!q.down) s /= p.k;
                     }
-                    at[i] = s * K;
+                    at[i] = s * K * (kTwo && q.down ? 2 : 1);
                 }
             }
             bool ok = true;
             if (q.down) {  // the activations of this expert
                 const int want = q.shared ? n.tiles1s : n.tiles1;
                 const int* flag = p.done + (q.shared ? 0 : 1 + q.group);
-                if (lane == 0) {
-                    const uint64_t t0 = global_timer_ns();
-                    for (uint32_t it = 1;; ++it) {
-                        int v;
-                        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
-                        if (v >= want) break;
-                        if ((it & 63u) == 0 && (*abort || global_timer_ns() - t0 > kWaitLimitNs)) {
-                            *abort = 1;
-                            ok = false;
-                            break;
-                        }
-                    }
-                }
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait_flag(flag, want, abort);
             }
             const int live = (rows + 7) / 8 * 2;  // of the lanes' rows
             for (int kb = q.kb0; ok && kb < q.kb1; ++kb) {
@@ -498,7 +560,9 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                     if (i >= live) break;
                     const int r = (lane >> 3) + 4 * i;
                     const bool there = at[i] >= 0 && k0 < K;
-                    cp_async_16(dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4), there ? src + at[i] + k0 : src, there ? 16 : 0);
+                    const uint32_t to = dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                    cp_async_16(to, there ? src + at[i] + k0 : src, there ? 16 : 0);
+                    if (kTwo && q.down) cp_async_16(to + kNt * 1024, there ? src + at[i] + K + k0 : src, there ? 16 : 0);
                 }
                 cp_async_arrive_noinc(full(stage));
                 if (++stage == p.stages) stage = 0, phase ^= 1u;
@@ -522,32 +586,73 @@ __global__ void __launch_bounds__(kDcThreads, 1)
             if (j < 0) break;
             const Job q = job_of(p, n, j);
             const int rows = q.shared ? p.T : rt.gn[q.group], tiles = (rows + 7) / 8;
-            float acc[kNt][4];
+            // chains of dependent products: a stage's latency, not its bytes, is what a
+            // single one would wait for
+            constexpr int kChains = kNt <= 2 ? 4 : 2;
+            float part_acc[kChains][kNt][4];
 #pragma unroll
-            for (int i = 0; i < kNt; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+            for (int h = 0; h < kChains; ++h)
+#pragma unroll
+                for (int i = 0; i < kNt; ++i)
+                    part_acc[h][i][0] = part_acc[h][i][1] = part_acc[h][i][2] = part_acc[h][i][3] = 0.0f;
             bool ok = true;
-            for (int kb = q.kb0; kb < q.kb1; ++kb) {
-                if (!(ok = warp_wait(full(stage), phase, abort))) break;
-                const uint32_t a0 = ring + stage * kStage, b0 = a0 + 2 * kDcBox;
-                uint32_t a[4][4];
+            auto stages_of = [&](auto two) {  // one stage, or two together
+                constexpr int kS = decltype(two)::value;
+                uint32_t a0[kS];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) dc_ldmatrix_x4_trans(a0 + abase + s * 2048, a[s]);
+                for (int u = 0; u < kS; ++u) {
+                    const int st = stage + u < p.stages ? stage + u : 0;
+                    a0[u] = ring + st * kStage;
+                    if (!warp_wait(full(st), stage + u < p.stages ? phase : phase ^ 1u, abort)) return false;
+                }
+                uint32_t a[kS][4][4];
+#pragma unroll
+                for (int u = 0; u < kS; ++u)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) dc_ldmatrix_x4_trans(a0[u] + abase + s * 2048, a[u][s]);
+                const int r = lane & 7, v = lane >> 3;
 #pragma unroll
                 for (int i = 0; i < kNt; ++i) {
                     if (i >= tiles) break;
-                    uint32_t b[4];
-                    const int r = lane & 7, v = lane >> 3;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        dc_ldmatrix_x4(b0 + (8 * i + r) * 128 + (((4 * h + v) ^ r) << 4), b);
-                        dc_mma(acc[i], a[2 * h], b[0], b[1]);
-                        dc_mma(acc[i], a[2 * h + 1], b[2], b[3]);
+                    for (int u = 0; u < kS; ++u) {
+                        const uint32_t b0 = a0[u] + 2 * kDcBox + (8 * i + r) * 128;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t b[4];
+                            float(&c0)[4] = part_acc[(2 * u) % kChains][i];
+                            float(&c1)[4] = part_acc[(2 * u + 1) % kChains][i];
+                            dc_ldmatrix_x4(b0 + (((4 * h + v) ^ r) << 4), b);
+                            dc_mma(c0, a[u][2 * h], b[0], b[1]);
+                            dc_mma(c1, a[u][2 * h + 1], b[2], b[3]);
+                            if (kTwo && q.down) {
+                                dc_ldmatrix_x4(b0 + kNt * 1024 + (((4 * h + v) ^ r) << 4), b);
+                                dc_mma(c0, a[u][2 * h], b[0], b[1]);
+                                dc_mma(c1, a[u][2 * h + 1], b[2], b[3]);
+                            }
+                        }
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty(stage));
-                if (++stage == p.stages) stage = 0, phase ^= 1u;
-            }
+#pragma unroll
+                for (int u = 0; u < kS; ++u) {
+                    if (lane == 0) mbar_arrive(empty(stage));
+                    if (++stage == p.stages) stage = 0, phase ^= 1u;
+                }
+                return true;
+            };
+            int kb = q.kb0;
+            for (; ok && kb + 1 < q.kb1; kb += 2) ok = stages_of(std::integral_constant<int, 2>());
+            if (ok && kb < q.kb1) ok = stages_of(std::integral_constant<int, 1>());
+            float acc[kNt][4];
+#pragma unroll
+            for (int i = 0; i < kNt; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    acc[i][c] = part_acc[0][i][c];
+#pragma unroll
+                    for (int h = 1; h < kChains; ++h) acc[i][c] += part_acc[h][i][c];
+                }
             if (!ok) break;
             // ---- the end of a job.  acc: first box's column fl (8 a warp), tokens tk and
             // tk + 1 of each eight; then the second box's
@@ -597,7 +702,11 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                             }
                             gate = clamp_keep_nan(gate, p.clamp);
                             up = clamp_keep_nan(up, p.clamp);
-                            act[(size_t)s * I + f] = __float2bfloat16_rn(gate / (1.0f + expf(-gate)) * up);
+                            const float a = gate / (1.0f + expf(-gate)) * up;
+                            const __nv_bfloat16 h = __float2bfloat16_rn(a);
+                            act[(size_t)s * (kTwo ? 2 : 1) * I + f] = h;
+                            // (no rest of an infinity or a NaN)
+                            if (kTwo) act[(size_t)s * 2 * I + I + f] = __float2bfloat16_rn(isfinite(a) ? a - __bfloat162float(h) : 0.0f);
                         }
                     if (!cbar.sync()) break;
                     if (tid == 0) {
@@ -619,39 +728,52 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                         if (c0 + 64 < p.H) __stcg(d + c0 + 64, acc[i][2 + c]);
                     }
                 if (!cbar.sync()) break;
-                if (tid == 0) last_word = draw_last(p.tiles_done + q.tile, down_jobs);
-                if (!cbar.sync()) break;
-                if (last_word) {  // every part of these columns is there: y
-                    for (int i = tid; i < p.T * 32; i += 256) {
-                        const int t = i >> 5, c = 128 * q.tile + 4 * (i & 31);
-                        if (c >= p.H) continue;
-                        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                        for (int jj = 0; jj < p.k; ++jj) {
-                            const int sl = t * p.k + jj;
-                            if (rt.idx[sl] < 0) continue;
-                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            const float* d = p.part2 + (size_t)sl * p.kp2 * p.H + c;
-                            for (int b = 0; b < p.kp2; ++b) {
-                                const float4 u = __ldcg(reinterpret_cast<const float4*>(d + (size_t)b * p.H));
-                                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-                            }
-                            const float w = rt.w[sl];
-                            s.x += w * v.x, s.y += w * v.y, s.z += w * v.z, s.w += w * v.w;
-                        }
-                        if (p.Is) {
-                            const float* d = p.part2s + (size_t)t * p.kp2s * p.H + c;
-#pragma unroll 4
-                            for (int b = 0; b < p.kp2s; ++b) {
-                                const float4 u = __ldcg(reinterpret_cast<const float4*>(d + (size_t)b * p.H));
-                                s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
-                            }
-                        }
-                        *reinterpret_cast<uint2*>(p.y + (size_t)t * p.H + c) =
-                            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-                    }
+                if (tid == 0) {
+                    __threadfence();
+                    atomicAdd(p.tiles_done + q.tile, 1);
                 }
             }
+        }
+        // ---- y, 128 columns of a token a warp, once every part of them is there
+        const int items = n.total ? p.T * n.tiles2 : 0;
+        for (int i = blockIdx.x * kDcConsumers + warp; i < items; i += gridDim.x * kDcConsumers) {
+            const int t = i / n.tiles2, tile = i - t * n.tiles2;
+            if (!warp_wait_flag(p.tiles_done + tile, down_jobs, abort)) break;
+            const int c = 128 * tile + 4 * lane;
+            if (c >= p.H) continue;
+            // K ranges of a slot, then slots, in order; eight loads in flight
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            auto add = [&](const float* base, int terms, int kp, auto weight) {
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int n0 = 0, b = 0, sl = 0; n0 < terms; n0 += 8) {
+                    float4 u[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        u[e] = n0 + e < terms ? __ldcg(reinterpret_cast<const float4*>(base + (size_t)(n0 + e) * p.H))
+                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (n0 + e >= terms) break;
+                        v.x += u[e].x, v.y += u[e].y, v.z += u[e].z, v.w += u[e].w;
+                        if (++b < kp) continue;
+                        b = 0;
+                        float w;
+                        if (weight(sl++, w)) s.x += w * v.x, s.y += w * v.y, s.z += w * v.z, s.w += w * v.w;
+                        v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+                }
+            };
+            // (a dropped slot's parts hold whatever was there: they are not added)
+            add(p.part2 + (size_t)t * p.k * p.kp2 * p.H + c, p.k * p.kp2, p.kp2, [&](int sl, float& w) {
+                w = rt.w[t * p.k + sl];
+                return rt.idx[t * p.k + sl] >= 0;
+            });
+            if (p.Is)
+                add(p.part2s + (size_t)t * p.kp2s * p.H + c, p.kp2s, p.kp2s, [&](int, float& w) {
+                    w = 1.0f;
+                    return true;
+                });
+            *reinterpret_cast<uint2*>(p.y + (size_t)t * p.H + c) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
         }
     }
     __syncthreads();
@@ -675,13 +797,14 @@ __global__ void __launch_bounds__(kDcThreads, 1)
 int cdiv_i(long long a, int b) { return (int)((a + b - 1) / b); }
 size_t up256_d(size_t v) { return (v + 255) / 256 * 256; }
 
-// K ranges: jobs of about an eighth of an SM's share, so that the last ones to end
-// end together, and of eight stages (128 KB of weights) at least, whose ends still
-// hide under the copies in flight.
-int split_of(int stages, long long target) {
-    long long s = (stages + target / 2) / target;
+// K ranges of the jobs of a column tile: as few as give most SMs one.  DRAM is kept
+// busy by some 60 SMs with 190 KB in flight each, so uneven ends cost little, and a
+// range's sums have to be joined.  Eight stages (128 KB of weights) at least.
+int split_of(int stages, double jobs) {
+    int s = jobs >= 96 ? 1 : (int)(128 / jobs + 0.5);
+    if (s > stages / 8) s = stages / 8;
     if (s > kDcMaxSplit) s = kDcMaxSplit;
-    return (int)(s < 1 ? 1 : s);
+    return s < 1 ? 1 : s;
 }
 
 struct DecodePlan {
@@ -695,13 +818,9 @@ DecodePlan decode_plan(const moe_decode_shape& s) {
     const double used = s.E * (1.0 - pow(1.0 - (double)s.k / s.E, (double)s.T));
     const int st1 = cdiv_i(s.H, 64), st2 = cdiv_i(s.I, 64), st2s = cdiv_i(s.Is, 64);
     const int tiles1 = cdiv_i(s.I, 64), tiles1s = cdiv_i(s.Is, 64), tiles2 = cdiv_i(s.H, 128);
-    const double total = used * ((double)tiles1 * st1 + (double)tiles2 * st2) + (double)tiles1s * st1 + (double)tiles2 * st2s;
-    long long target = (long long)(total / (152 * 8));
-    if (target < 8) target = 8;
-    d.kp1 = split_of(st1, target);
-    d.kp1s = s.Is ? split_of(st1, target) : 1;
-    d.kp2 = split_of(st2, target);
-    d.kp2s = s.Is ? split_of(st2s, target) : 1;
+    d.kp1 = d.kp1s = split_of(st1, used * tiles1 + tiles1s);
+    d.kp2 = split_of(st2, (used + (s.Is ? 1 : 0)) * tiles2);
+    d.kp2s = s.Is ? split_of(st2s, (used + 1) * tiles2) : 1;
     d.nt = s.T <= 8 ? 1 : s.T <= 16 ? 2 : s.T <= 32 ? 4 : 8;
     const int groups = (int)slots + 1;
     d.joined = 16 + tiles2 + groups;  // ticket and status; column tiles; groups
@@ -714,8 +833,9 @@ DecodePlan decode_plan(const moe_decode_shape& s) {
     };
     d.count = take((size_t)d.counters * 4);
     d.logits = take((size_t)s.T * s.E * 4);
-    d.act = take((size_t)slots * s.I * 2);
-    d.act_s = take((size_t)s.T * s.Is * 2);
+    const int two = dc_two(d.nt) ? 2 : 1;
+    d.act = take((size_t)slots * s.I * 2 * two);
+    d.act_s = take((size_t)s.T * s.Is * 2 * two);
     d.part1 = take(d.kp1 > 1 ? (size_t)slots * d.kp1 * 2 * s.I * 4 : 0);
     d.part1s = take(d.kp1s > 1 ? (size_t)s.T * d.kp1s * 2 * s.Is * 4 : 0);
     d.part2 = take((size_t)slots * d.kp2 * s.H * 4);

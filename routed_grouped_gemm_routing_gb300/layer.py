@@ -207,6 +207,7 @@ class DecodeLayer:
         self.router, self.W1, self.W2, self.S1, self.S2 = (None if t is None else t.detach().contiguous() for t in weights)
         self.E, self.H, self.I, self.k, self.Is = E, H, I, int(k), Is
         self.activation_clamp = float(activation_clamp)
+        self.device = self.W1.get_device()
         self._sizes = {}  # T -> shape, reference to it, workspace bytes
         self._size(1)  # sizes that the kernels do not take are refused here
         self._ptrs = [None if t is None else t.data_ptr() for t in (self.router, self.W1, self.W2, self.S1, self.S2)]
@@ -225,10 +226,23 @@ class DecodeLayer:
         [T, k], topk_w f32 [T, k]).  topk_idx int [T, k] and topk_w float [T, k]: the
         routing, of a layer without a router (ids outside the experts count for
         nothing)."""
-        if x.dim() != 2 or x.shape[1] != self.H:
-            raise ValueError(f"expected x [T, {self.H}], got {list(x.shape)}")
-        T, dev = x.shape[0], self.W1.get_device()
-        s, ref, size = self._size(T)
+        sh = x.shape
+        if len(sh) != 2 or sh[1] != self.H:
+            raise ValueError(f"expected x [T, {self.H}], got {list(sh)}")
+        T, dev = sh[0], self.device
+        s, ref, size = self._sizes.get(T) or self._size(T)
+        if (topk_idx is None and topk_w is None and out is None and self.router is not None and x.dtype is torch.bfloat16
+                and x.get_device() == dev and dev == torch.cuda.current_device() and x.is_contiguous()):
+            where = x.device
+            topk_idx = torch.empty((T, self.k), dtype=torch.int32, device=where)
+            topk_w = torch.empty((T, self.k), dtype=torch.float32, device=where)
+            ws = torch.empty((size,), dtype=torch.uint8, device=where)
+            y = torch.empty_like(x)
+            rc = B.lib().moe_decode_forward(ref, x.data_ptr(), *self._ptrs, topk_idx.data_ptr(), topk_w.data_ptr(),
+                                            ws.data_ptr(), y.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+            if rc:
+                B._check(rc)
+            return (y, topk_idx, topk_w) if return_routing else y
         if self.router is None:
             if topk_idx is None or topk_w is None or topk_idx.shape != (T, self.k) or topk_w.shape != (T, self.k):
                 raise ValueError(f"a layer without a router needs topk_idx and topk_w [{T}, {self.k}]")
@@ -241,17 +255,8 @@ class DecodeLayer:
                 topk_w = torch.empty((T, self.k), dtype=torch.float32, device=x.device)
             ws = torch.empty((size,), dtype=torch.uint8, device=x.device)
             y = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device) if out is None else out
-            if (x.dtype is torch.bfloat16 and x.is_contiguous() and out is None and topk_idx.get_device() == dev
-                    and topk_w.get_device() == dev):
-                r, W1, W2, S1, S2 = self._ptrs
-                rc = B.lib().moe_decode_forward(
-                    ref, x.data_ptr(), r, W1, W2, S1, S2, topk_idx.data_ptr(), topk_w.data_ptr(), ws.data_ptr(),
-                    y.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
-                if rc:
-                    B._check(rc)
-            else:
-                B.moe_decode_forward(s, x if x.is_contiguous() else x.contiguous(), self.router, self.W1, self.W2, self.S1,
-                                     self.S2, topk_idx, topk_w, ws, y)
+            B.moe_decode_forward(s, x if x.is_contiguous() else x.contiguous(), self.router, self.W1, self.W2, self.S1,
+                                 self.S2, topk_idx, topk_w, ws, y)
         return (y, topk_idx, topk_w) if return_routing else y
 
     __call__ = forward

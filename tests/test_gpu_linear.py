@@ -176,7 +176,7 @@ def test_residual_in_place(T):
     x, W, b, r, _ = _inputs(T, 264, 520)
     want, _ = linear_forward(x, W, b, r, "silu")
     s = B.linear_shape(T, 264, 520, "silu")
-    ws = torch.empty(B.moe_linear_workspace(s), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(B.moe_linear_workspace(s, False), dtype=torch.uint8, device="cuda")
     B.moe_linear_forward(s, x, W, b, r, None, ws, r)
     assert torch.equal(r, want)
 
@@ -234,7 +234,7 @@ def test_rows_behind_the_last_stay():
     for T in (5, 40, 300):
         x, W, b, r, dy = _inputs(T, 72, 136)
         s = B.linear_shape(T, 72, 136, "silu")
-        ws = torch.empty(B.moe_linear_workspace(s), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(max(B.moe_linear_workspace(s, d) for d in (False, True)), dtype=torch.uint8, device="cuda")
         y, dx = (torch.full((T + 9, n), 7.0, device="cuda", dtype=BF) for n in (136, 72))
         z = torch.full((T + 9, 136), 7.0, device="cuda")
         dW, db = torch.full((72 + 1, 136), 7.0, device="cuda", dtype=BF), torch.full((137,), 7.0, device="cuda")

@@ -36,12 +36,12 @@ def test_declared_and_exported(lib):
                                         ((4, 64, 64, -1), B.MOE_EUNSUPPORTED), ((4, 1 << 21, 64, 0), B.MOE_EUNSUPPORTED)])
 def test_shapes(lib, shape, code):
     n = ctypes.c_size_t()
-    assert lib.moe_linear_workspace(ctypes.byref(B.MoeLinearShape(*shape)), ctypes.byref(n)) == code
+    assert lib.moe_linear_workspace(ctypes.byref(B.MoeLinearShape(*shape)), 0, ctypes.byref(n)) == code
     assert _fwd(lib, shape) == _bwd(lib, shape) == code
 
 
 def test_arguments(lib):
-    assert lib.moe_linear_workspace(None, None) == B.MOE_EINVAL
+    assert lib.moe_linear_workspace(None, 0, None) == B.MOE_EINVAL
     for kw in ({"x": None}, {"W": None}, {"ws": None}, {"y": None}, {"xs": 56}, {"rs": 64}, {"r": P[6], "rs": 80}):
         assert _fwd(lib, **kw) == B.MOE_EINVAL, kw
     for kw in ({"x": P[0] + 8}, {"b": P[2] + 2}, {"r": P[3] + 8}, {"z": P[4] + 4}, {"y": P[6] + 2}, {"xs": 68}, {"rs": 76},
@@ -58,8 +58,10 @@ def test_arguments(lib):
 
 def test_sizes():
     for T, K, N, act in ((0, 64, 64, None), (1, 7168, 2048, "silu"), (777, 1160, 712, "gelu"), (8192, 2048, 7168, None)):
-        n = B.moe_linear_workspace(B.linear_shape(T, K, N, act))
-        assert n % 256 == 0 and n >= 256 + (T * N * 2 if act else 0)
+        s = B.linear_shape(T, K, N, act)
+        fwd, bwd = B.moe_linear_workspace(s, False), B.moe_linear_workspace(s, True)
+        assert fwd % 256 == bwd % 256 == 0 and fwd >= 256 and bwd >= 256 + (T * N * 2 if act else 0)
+    assert B.moe_linear_workspace(B.linear_shape(8192, 2048, 7168), False) == 256  # a status word alone
 
 
 def test_python_refusals():
