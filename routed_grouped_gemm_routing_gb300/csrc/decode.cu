@@ -16,11 +16,11 @@
 // The work is a list of jobs that all blocks know: first, for each expert in use
 // (the shared one first), 64 features of gate and up projection and a range of K;
 // then, for each expert, 128 columns of the down projection and a range of K.
-// Blocks draw jobs from a counter.  A warp streams a job's weights by TMA, 64 of K
-// x 2 x 64 columns a stage, and goes on to the next job's while this one's end is
+// Blocks draw jobs from a counter.  A warp streams a job's weights by TMA, 128 of
+// K x 2 x 64 columns a stage, and goes on to the next job's while this one's end is
 // still computed, so that some 200 KB are in flight on every SM all the time.
-// Another warp gathers the tokens' rows (cp.async) and, for the down projection,
-// waits until the expert's activations are there: they come from jobs drawn
+// Two warps gather the tokens' rows (cp.async) and, for the down projection,
+// wait until the expert's activations are there: they come from jobs drawn
 // earlier, by blocks that are running and that wait for nothing before them, so
 // the wait ends whichever blocks are resident.  Eight warps multiply (mma
 // m16n8k16, weights as A straight out of the boxes by transposed ldmatrix): eight
@@ -44,9 +44,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kDcConsumers = 8, kDcWarpTma = 8, kDcWarpGather = 9;
-constexpr int kDcThreads = 320;
-constexpr int kDcBox = 8192;    // 64 of K x 64 columns
+constexpr int kDcConsumers = 8, kDcWarpTma = 8, kDcWarpGather = 9, kDcGathers = 2, kDcWarpSignal = 11;
+constexpr int kDcThreads = 384;
+// of K in a stage: with 64 the threads that fill the ring took as long for a stage
+// as its bytes (64 tokens, 2048 x 1408, top 6 of 64: 205 us)
+constexpr int kDcK = 128;
+constexpr int kDcBox = kDcK * 128;  // kDcK of K x 64 columns
 constexpr int kDcJobs = 4;      // jobs drawn ahead
 constexpr int kDcMaxSplit = 16;
 constexpr int kRtCluster = 8, kRtRows = 1024;  // of the router: blocks of a cluster, rows of x held at once
@@ -254,8 +257,10 @@ __host__ __device__ constexpr int dc_table_bytes(int slots) {
 // each, the second the rounding's rest: the outputs then err by their own rounding
 // alone, and what it costs, a second product on the same weights, is hidden there.
 __host__ __device__ constexpr bool dc_two(int nt) { return nt <= 2; }
-__host__ __device__ constexpr int dc_stage_bytes(int nt) { return 2 * kDcBox + nt * (dc_two(nt) ? 2048 : 1024); }
-__host__ __device__ constexpr int dc_bar_bytes(int stages) { return 8 * (2 * stages + 2 * kDcJobs) + 4 * kDcJobs + 16; }
+// eight tokens' rows of a stage: two halves of 64 of K, 128 bytes a row each
+constexpr int kDcRows8 = 2048;
+__host__ __device__ constexpr int dc_stage_bytes(int nt) { return 2 * kDcBox + nt * kDcRows8 * (dc_two(nt) ? 2 : 1); }
+__host__ __device__ constexpr int dc_bar_bytes(int stages) { return 8 * (2 * stages + 3 * kDcJobs) + 8 * kDcJobs + 16; }
 
 // One warp: the k largest of a token's E logits, as the layer's router takes them
 // (equal ones by id, a NaN as -infinity, softmax over the chosen ones).
@@ -394,7 +399,7 @@ struct Jobs {
     int n1s, n1, n2s, total, per1, per2;          // jobs; of a routed group
     __device__ __forceinline__ Jobs(const DecodeArgs& p, int groups) {
         tiles1 = (p.I + 63) / 64, tiles1s = (p.Is + 63) / 64, tiles2 = (p.H + 127) / 128;
-        st1 = (p.H + 63) / 64, st2 = (p.I + 63) / 64, st2s = (p.Is + 63) / 64;
+        st1 = (p.H + kDcK - 1) / kDcK, st2 = (p.I + kDcK - 1) / kDcK, st2s = (p.Is + kDcK - 1) / kDcK;
         per1 = tiles1 * p.kp1, per2 = tiles2 * p.kp2;
         n1s = p.Is ? tiles1s * p.kp1s : 0;
         n1 = n1s + groups * per1;
@@ -442,8 +447,11 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     auto empty = [&](int s) { return bar0 + 8u * (p.stages + s); };
     auto jfull = [&](int s) { return bar0 + 8u * (2 * p.stages + s); };
     auto jempty = [&](int s) { return bar0 + 8u * (2 * p.stages + kDcJobs + s); };
-    volatile int* jobs = reinterpret_cast<volatile int*>(tail + 8 * (2 * p.stages + 2 * kDcJobs));
-    ConsumerBarrier cbar = {bar0 + 8u * (2 * p.stages + 2 * kDcJobs) + 4u * kDcJobs, 0, abort};
+    // a job's outputs: an arrival of each multiplying warp
+    auto written = [&](int s) { return bar0 + 8u * (2 * p.stages + 2 * kDcJobs + s); };
+    volatile int* jobs = reinterpret_cast<volatile int*>(tail + 8 * (2 * p.stages + 3 * kDcJobs));
+    volatile int* joins = jobs + kDcJobs;  // of a job: whether its block joined the K ranges
+    ConsumerBarrier cbar = {bar0 + 8u * (2 * p.stages + 3 * kDcJobs) + 8u * kDcJobs, 0, abort};
     const int slots = p.T * p.k;
     uint8_t* tab = tail + dc_bar_bytes(p.stages);
     Routing rt;
@@ -457,12 +465,13 @@ __global__ void __launch_bounds__(kDcThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(full(s), 1 + 32);  // the TMA thread's arrival and the gathering lanes'
+            mbar_init(full(s), 1 + 32 * kDcGathers);  // the TMA thread's arrival and the gathering lanes'
             mbar_init(empty(s), kDcConsumers);
         }
         for (int s = 0; s < kDcJobs; ++s) {
             mbar_init(jfull(s), 1);
-            mbar_init(jempty(s), kDcConsumers + 1);
+            mbar_init(jempty(s), kDcConsumers + kDcGathers + 1);
+            mbar_init(written(s), kDcConsumers);
         }
         mbar_init(cbar.bar, kDcConsumers);
         *abort = 0;
@@ -505,18 +514,18 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                     const uint32_t b = full(stage), dst = ring + stage * kStage;
                     mbar_arrive_expect_tx(b, 2 * kDcBox);
                     if (q.down) {
-                        tma_load_3d(dst, m, 128 * q.tile, 64 * kb, e, b);
-                        tma_load_3d(dst + kDcBox, m, 128 * q.tile + 64, 64 * kb, e, b);
+                        tma_load_3d(dst, m, 128 * q.tile, kDcK * kb, e, b);
+                        tma_load_3d(dst + kDcBox, m, 128 * q.tile + 64, kDcK * kb, e, b);
                     } else {
-                        tma_load_4d(dst, m, 64 * q.tile, 0, 64 * kb, e, b);
-                        tma_load_4d(dst + kDcBox, m, 64 * q.tile, 1, 64 * kb, e, b);
+                        tma_load_4d(dst, m, 64 * q.tile, 0, kDcK * kb, e, b);
+                        tma_load_4d(dst + kDcBox, m, 64 * q.tile, 1, kDcK * kb, e, b);
                     }
                     if (++stage == p.stages) stage = 0, phase ^= 1u;
                 }
                 if (!ok) break;
             }
         }
-    } else if (warp == kDcWarpGather) {
+    } else if (warp >= kDcWarpGather && warp < kDcWarpGather + kDcGathers) {
         int stage = 0, slot = 0;
         uint32_t phase = 0, jphase = 0;
         for (;;) {
@@ -529,11 +538,12 @@ __global__ void __launch_bounds__(kDcThreads, 1)
             const Job q = job_of(p, n, j);
             const int rows = q.shared ? p.T : rt.gn[q.group], K = q.down ? (q.shared ? p.Is : p.I) : p.H;
             const __nv_bfloat16* src = q.down ? (q.shared ? p.act_s : p.act) : p.x;
-            // this lane's rows: lane / 8, + 4, ..; a piece of 8 of K of each
+            // this lane's rows: 2 (this warp) + lane / 16, + 4, ..; a piece of 8 of K of each
+            const int r0 = 2 * (warp - kDcWarpGather) + (lane >> 4);
             int at[2 * kNt];
 #pragma unroll
             for (int i = 0; i < 2 * kNt; ++i) {
-                const int r = (lane >> 3) + 4 * i;
+                const int r = r0 + 4 * i;
                 at[i] = -1;
                 if (r < rows) {
                     int s = r;
@@ -553,16 +563,17 @@ __global__ void __launch_bounds__(kDcThreads, 1)
             const int live = (rows + 7) / 8 * 2;  // of the lanes' rows
             for (int kb = q.kb0; ok && kb < q.kb1; ++kb) {
                 if (!(ok = warp_wait(empty(stage), phase ^ 1u, abort))) break;
-                const uint32_t dst = ring + stage * kStage + 2 * kDcBox;
-                const int k0 = 64 * kb + 8 * (lane & 7);
+                const int piece = lane & 15, k0 = kDcK * kb + 8 * piece;
+                const uint32_t dst = ring + stage * kStage + 2 * kDcBox + (piece >> 3) * kNt * 1024;
+                const bool in = k0 < K;
 #pragma unroll
                 for (int i = 0; i < 2 * kNt; ++i) {
                     if (i >= live) break;
-                    const int r = (lane >> 3) + 4 * i;
-                    const bool there = at[i] >= 0 && k0 < K;
-                    const uint32_t to = dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                    const int r = r0 + 4 * i;
+                    const bool there = at[i] >= 0 && in;
+                    const uint32_t to = dst + r * 128 + (((piece ^ r) & 7) << 4);
                     cp_async_16(to, there ? src + at[i] + k0 : src, there ? 16 : 0);
-                    if (kTwo && q.down) cp_async_16(to + kNt * 1024, there ? src + at[i] + K + k0 : src, there ? 16 : 0);
+                    if (kTwo && q.down) cp_async_16(to + kNt * kDcRows8, there ? src + at[i] + K + k0 : src, there ? 16 : 0);
                 }
                 cp_async_arrive_noinc(full(stage));
                 if (++stage == p.stages) stage = 0, phase ^= 1u;
@@ -570,6 +581,27 @@ __global__ void __launch_bounds__(kDcThreads, 1)
             if (!ok) break;
         }
         cp_async_wait_all();
+    } else if (warp == kDcWarpSignal) {
+        // Tells the other blocks of a job's outputs, so that no multiplying warp waits
+        // for the fence.
+        int slot = 0;
+        uint32_t jphase = 0;
+        for (;;) {
+            if (!warp_wait(jfull(slot), jphase, abort)) break;
+            const int j = jobs[slot];
+            const Job q = job_of(p, n, j < 0 ? 0 : j);
+            if (j >= 0) {
+                if (!warp_wait(written(slot), jphase, abort)) break;
+                if (lane == 0 && (q.down || (q.shared ? p.kp1s : p.kp1) == 1 || joins[slot])) {
+                    __threadfence();
+                    atomicAdd(q.down ? p.tiles_done + q.tile : p.done + (q.shared ? 0 : 1 + q.group), 1);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(jempty(slot));
+            if (++slot == kDcJobs) slot = 0, jphase ^= 1u;
+            if (j < 0) break;
+        }
     } else {
         int stage = 0, slot = 0;
         uint32_t phase = 0, jphase = 0;
@@ -579,14 +611,16 @@ __global__ void __launch_bounds__(kDcThreads, 1)
         const uint32_t abase = ((lane >> 3) & 1) * kDcBox + ak * 128 + ((warp ^ (ak & 7)) << 4);
         for (;;) {
             if (!warp_wait(jfull(slot), jphase, abort)) break;
-            const int j = jobs[slot];
+            const int j = jobs[slot], at_slot = slot;
             __syncwarp();
-            if (lane == 0) mbar_arrive(jempty(slot));
+            if (j < 0) {
+                if (lane == 0) mbar_arrive(jempty(slot));
+                break;
+            }
             if (++slot == kDcJobs) slot = 0, jphase ^= 1u;
-            if (j < 0) break;
             const Job q = job_of(p, n, j);
             const int rows = q.shared ? p.T : rt.gn[q.group], tiles = (rows + 7) / 8;
-            // chains of dependent products: a stage's latency, not its bytes, is what a
+            // chains of dependent products: their latency, not a stage's bytes, is what a
             // single one would wait for
             constexpr int kChains = kNt <= 2 ? 4 : 2;
             float part_acc[kChains][kNt][4];
@@ -596,54 +630,37 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                 for (int i = 0; i < kNt; ++i)
                     part_acc[h][i][0] = part_acc[h][i][1] = part_acc[h][i][2] = part_acc[h][i][3] = 0.0f;
             bool ok = true;
-            auto stages_of = [&](auto two) {  // one stage, or two together
-                constexpr int kS = decltype(two)::value;
-                uint32_t a0[kS];
+            for (int kb = q.kb0; kb < q.kb1; ++kb) {
+                if (!(ok = warp_wait(full(stage), phase, abort))) break;
+                const uint32_t a0 = ring + stage * kStage;
+                uint32_t a[8][4];
 #pragma unroll
-                for (int u = 0; u < kS; ++u) {
-                    const int st = stage + u < p.stages ? stage + u : 0;
-                    a0[u] = ring + st * kStage;
-                    if (!warp_wait(full(st), stage + u < p.stages ? phase : phase ^ 1u, abort)) return false;
-                }
-                uint32_t a[kS][4][4];
-#pragma unroll
-                for (int u = 0; u < kS; ++u)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) dc_ldmatrix_x4_trans(a0[u] + abase + s * 2048, a[u][s]);
+                for (int s = 0; s < 8; ++s) dc_ldmatrix_x4_trans(a0 + abase + s * 2048, a[s]);
                 const int r = lane & 7, v = lane >> 3;
 #pragma unroll
                 for (int i = 0; i < kNt; ++i) {
                     if (i >= tiles) break;
+                    const uint32_t b0 = a0 + 2 * kDcBox + (8 * i + r) * 128;
 #pragma unroll
-                    for (int u = 0; u < kS; ++u) {
-                        const uint32_t b0 = a0[u] + 2 * kDcBox + (8 * i + r) * 128;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t b[4];
-                            float(&c0)[4] = part_acc[(2 * u) % kChains][i];
-                            float(&c1)[4] = part_acc[(2 * u + 1) % kChains][i];
-                            dc_ldmatrix_x4(b0 + (((4 * h + v) ^ r) << 4), b);
-                            dc_mma(c0, a[u][2 * h], b[0], b[1]);
-                            dc_mma(c1, a[u][2 * h + 1], b[2], b[3]);
-                            if (kTwo && q.down) {
-                                dc_ldmatrix_x4(b0 + kNt * 1024 + (((4 * h + v) ^ r) << 4), b);
-                                dc_mma(c0, a[u][2 * h], b[0], b[1]);
-                                dc_mma(c1, a[u][2 * h + 1], b[2], b[3]);
-                            }
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t b[4];
+                        float(&c0)[4] = part_acc[(2 * h) % kChains][i];
+                        float(&c1)[4] = part_acc[(2 * h + 1) % kChains][i];
+                        const uint32_t from = b0 + (h >> 1) * kNt * 1024 + (((4 * (h & 1) + v) ^ r) << 4);
+                        dc_ldmatrix_x4(from, b);
+                        dc_mma(c0, a[2 * h], b[0], b[1]);
+                        dc_mma(c1, a[2 * h + 1], b[2], b[3]);
+                        if (kTwo && q.down) {
+                            dc_ldmatrix_x4(from + kNt * kDcRows8, b);
+                            dc_mma(c0, a[2 * h], b[0], b[1]);
+                            dc_mma(c1, a[2 * h + 1], b[2], b[3]);
                         }
                     }
                 }
                 __syncwarp();
-#pragma unroll
-                for (int u = 0; u < kS; ++u) {
-                    if (lane == 0) mbar_arrive(empty(stage));
-                    if (++stage == p.stages) stage = 0, phase ^= 1u;
-                }
-                return true;
-            };
-            int kb = q.kb0;
-            for (; ok && kb + 1 < q.kb1; kb += 2) ok = stages_of(std::integral_constant<int, 2>());
-            if (ok && kb < q.kb1) ok = stages_of(std::integral_constant<int, 1>());
+                if (lane == 0) mbar_arrive(empty(stage));
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
+            }
             float acc[kNt][4];
 #pragma unroll
             for (int i = 0; i < kNt; ++i)
@@ -681,6 +698,7 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                     }
                     if (!cbar.sync()) break;
                     mine = last_word != 0;
+                    if (tid == 0) joins[at_slot] = mine;
                 }
                 if (mine) {
 #pragma unroll
@@ -708,11 +726,6 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                             // (no rest of an infinity or a NaN)
                             if (kTwo) act[(size_t)s * 2 * I + I + f] = __float2bfloat16_rn(isfinite(a) ? a - __bfloat162float(h) : 0.0f);
                         }
-                    if (!cbar.sync()) break;
-                    if (tid == 0) {
-                        __threadfence();
-                        atomicAdd(p.done + g, 1);
-                    }
                 }
             } else {
                 const int kp = q.shared ? p.kp2s : p.kp2, c0 = 128 * q.tile + 8 * warp + fl;
@@ -727,11 +740,11 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                         if (c0 < p.H) __stcg(d + c0, acc[i][c]);
                         if (c0 + 64 < p.H) __stcg(d + c0 + 64, acc[i][2 + c]);
                     }
-                if (!cbar.sync()) break;
-                if (tid == 0) {
-                    __threadfence();
-                    atomicAdd(p.tiles_done + q.tile, 1);
-                }
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(written(at_slot));
+                mbar_arrive(jempty(at_slot));
             }
         }
         // ---- y, 128 columns of a token a warp, once every part of them is there
@@ -799,10 +812,10 @@ size_t up256_d(size_t v) { return (v + 255) / 256 * 256; }
 
 // K ranges of the jobs of a column tile: as few as give most SMs one.  DRAM is kept
 // busy by some 60 SMs with 190 KB in flight each, so uneven ends cost little, and a
-// range's sums have to be joined.  Eight stages (128 KB of weights) at least.
+// range's sums have to be joined.  Four stages (128 KB of weights) at least.
 int split_of(int stages, double jobs) {
     int s = jobs >= 96 ? 1 : (int)(128 / jobs + 0.5);
-    if (s > stages / 8) s = stages / 8;
+    if (s > stages / 4) s = stages / 4;
     if (s > kDcMaxSplit) s = kDcMaxSplit;
     return s < 1 ? 1 : s;
 }
@@ -816,7 +829,7 @@ DecodePlan decode_plan(const moe_decode_shape& s) {
     const long long slots = (long long)s.T * s.k;
     // experts in use, as even routing has it
     const double used = s.E * (1.0 - pow(1.0 - (double)s.k / s.E, (double)s.T));
-    const int st1 = cdiv_i(s.H, 64), st2 = cdiv_i(s.I, 64), st2s = cdiv_i(s.Is, 64);
+    const int st1 = cdiv_i(s.H, kDcK), st2 = cdiv_i(s.I, kDcK), st2s = cdiv_i(s.Is, kDcK);
     const int tiles1 = cdiv_i(s.I, 64), tiles1s = cdiv_i(s.Is, 64), tiles2 = cdiv_i(s.H, 128);
     d.kp1 = d.kp1s = split_of(st1, used * tiles1 + tiles1s);
     d.kp2 = split_of(st2, (used + (s.Is ? 1 : 0)) * tiles2);
@@ -921,11 +934,11 @@ int launch_decode(const moe_decode_shape& s, const DecodePtrs& f, int sms, cudaS
     a.y = static_cast<__nv_bfloat16*>(f.y);
     int rc;
     CUtensorMap m[4] = {};
-    if ((rc = abi_map_nd(&m[0], f.W1, 2, {s.I, 2, s.H, s.E}, {64, 1, 64, 1}, "W1 (gate/up halves)"))) return rc;
-    if ((rc = abi_map_nd(&m[1], f.W2, 2, {s.H, s.I, s.E}, {64, 64, 1}, "W2"))) return rc;
+    if ((rc = abi_map_nd(&m[0], f.W1, 2, {s.I, 2, s.H, s.E}, {64, 1, kDcK, 1}, "W1 (gate/up halves)"))) return rc;
+    if ((rc = abi_map_nd(&m[1], f.W2, 2, {s.H, s.I, s.E}, {64, kDcK, 1}, "W2"))) return rc;
     if (s.Is) {
-        if ((rc = abi_map_nd(&m[2], f.S1, 2, {s.Is, 2, s.H, 1}, {64, 1, 64, 1}, "S1 (gate/up halves)"))) return rc;
-        if ((rc = abi_map_nd(&m[3], f.S2, 2, {s.H, s.Is, 1}, {64, 64, 1}, "S2"))) return rc;
+        if ((rc = abi_map_nd(&m[2], f.S1, 2, {s.Is, 2, s.H, 1}, {64, 1, kDcK, 1}, "S1 (gate/up halves)"))) return rc;
+        if ((rc = abi_map_nd(&m[3], f.S2, 2, {s.H, s.Is, 1}, {64, kDcK, 1}, "S2"))) return rc;
     }
     int e;
     if (f.router) {
