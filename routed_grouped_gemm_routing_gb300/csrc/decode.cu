@@ -59,7 +59,7 @@ template <int kTok>
 __global__ void __launch_bounds__(256)
     decode_router_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ R, int T, int H, int E,
                          float* __restrict__ logits, int* __restrict__ counters, int n_counters) {
-    __shared__ __align__(16) float xs[kTok == 1 ? 1 : kRtRows][kTok];
+    __shared__ __align__(16) float xs[kTok][kTok == 1 ? 4 : kRtRows];
     __shared__ float red[8][kTok][32];
     __shared__ float all[kRtCluster][kTok][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256)
         for (int i = b * 256 + tid; i < n_counters; i += blocks * 256) counters[i] = 0;
     }
     const int e0 = blockIdx.x * 32, t0 = blockIdx.y * kTok, e = e0 + 8 * cv;
-    const int per = (H + kRtCluster - 1) / kRtCluster, h0 = rank * per, h1 = h0 + per < H ? h0 + per : H;
+    const int per = (H / 8 + kRtCluster - 1) / kRtCluster * 8, h0 = rank * per, h1 = h0 + per < H ? h0 + per : H;  // H is a multiple of 8
     const bool whole = E % 8 == 0;  // rows of R on 16-byte boundaries
     float acc[kTok][8];
 #pragma unroll
@@ -83,9 +83,15 @@ __global__ void __launch_bounds__(256)
         const int rows = h1 - c0 < kRtRows ? h1 - c0 : kRtRows;
         if constexpr (kTok > 1) {
             __syncthreads();
-            for (int i = tid; i < kTok * rows; i += 256) {
-                const int t = i / rows, r = i - t * rows;
-                xs[r][t] = t0 + t < T ? __bfloat162float(x[(size_t)(t0 + t) * H + c0 + r]) : 0.0f;
+            {  // a warp a token, eight of its values a lane (the ranges are multiples of 8)
+                const int t = tid >> 5;
+                const __nv_bfloat16* src = x + (size_t)(t0 + t) * H + c0;
+                for (int r = 8 * (tid & 31); r < rows; r += 256) {
+                    float f[8] = {};
+                    if (t0 + t < T) unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(src + r)), f);
+                    *reinterpret_cast<float4*>(&xs[t][r]) = make_float4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<float4*>(&xs[t][r + 4]) = make_float4(f[4], f[5], f[6], f[7]);
+                }
             }
             __syncthreads();
         }
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(256)
                     unpack_bf16x8(u[a], w);
 #pragma unroll
                     for (int t = 0; t < kTok; ++t) {
-                        const float v = kTok == 1 ? x1[a] : xs[r][t];
+                        const float v = kTok == 1 ? x1[a] : xs[t][r];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(v, w[j], acc[t][j]);
                     }
@@ -812,10 +818,10 @@ size_t up256_d(size_t v) { return (v + 255) / 256 * 256; }
 
 // K ranges of the jobs of a column tile: as few as give most SMs one.  DRAM is kept
 // busy by some 60 SMs with 190 KB in flight each, so uneven ends cost little, and a
-// range's sums have to be joined.  Four stages (128 KB of weights) at least.
+// range's sums have to be joined.  Two stages (64 KB of weights) at least.
 int split_of(int stages, double jobs) {
     int s = jobs >= 96 ? 1 : (int)(128 / jobs + 0.5);
-    if (s > stages / 4) s = stages / 4;
+    if (s > stages / 2) s = stages / 2;
     if (s > kDcMaxSplit) s = kDcMaxSplit;
     return s < 1 ? 1 : s;
 }
