@@ -766,11 +766,11 @@ int launch_dense(const DenseArgs& a, const DenseMaps& m, const char* name, cudaS
     return launch_pairs(dense_pair_kernel<MODE, EPI>, fits, dense_smem<EPI>(),
                         (long long)a.tiles_m * a.tiles_n * a.splits, first, name, st, m.a, m.b, m.c0, m.c1, a);
 }
-int launch_plain(const PlainArgs& a, const PlainMaps& m, const char* name, cudaStream_t st) {
+int launch_plain(const PlainArgs& a, const PlainMaps& m, const char* name, cudaStream_t st, bool first = false) {
     static std::atomic<int> fits[kMaxDevices] = {};
     long long items = 0;
     for (int i = 0; i < a.n; ++i) items += (long long)a.p[i].tiles_m * a.p[i].tiles_n;
-    return launch_pairs(plain_kernel, fits, dense_smem<EPI_PLAIN>(), items, false, name, st, m, a);
+    return launch_pairs(plain_kernel, fits, dense_smem<EPI_PLAIN>(), items, first, name, st, m, a);
 }
 
 // Columns of a tile (gated: of both halves) and K ranges of a product: the

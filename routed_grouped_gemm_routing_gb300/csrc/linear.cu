@@ -220,29 +220,55 @@ __device__ __forceinline__ void store_db(void* db, int f32, int n, float v) {
         static_cast<__nv_bfloat16*>(db)[n] = __float2bfloat16_rn(v);
 }
 
-template <int kAct>
+// kBeside: runs beside the products of the other gradients (see the launch), with no
+// shared memory, which they leave none of: a warp's sums are a row of part.
+template <int kAct, bool kBeside>
 __global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const DzArgs p) {
-    __shared__ float red[kDzWarps][256];
+    __shared__ float red[kBeside ? 1 : kDzWarps][kBeside ? 1 : 256];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * lane;
     const long long r0 = (long long)blockIdx.y * p.per, r1 = r0 + p.per < p.rows ? r0 + p.per : p.rows;
     float sum[8] = {};
     if (n < p.N) {
-#pragma unroll 2
-        for (long long r = r0 + warp; r < r1; r += kDzWarps) {
-            float d[8];
-            unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.dy + r * p.dy_stride + n)), d);
-            if constexpr (kAct != MOE_ACT_NONE) {
-                const float4* zp = reinterpret_cast<const float4*>(p.z + (size_t)r * p.N + n);
-                const float4 a = __ldg(zp), b = __ldg(zp + 1);
-                const float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        constexpr int kAhead = kAct == MOE_ACT_NONE ? 8 : 4;  // rows whose loads are in flight together
+        for (long long r = r0 + warp; r < r1; r += kDzWarps * kAhead) {
+            uint4 dy[kAhead];
+            float4 z[kAhead][2];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] *= act_slope<kAct>(z[j]);
-                *reinterpret_cast<uint4*>(p.dz + (size_t)r * p.N + n) = pack8(d);
+            for (int u = 0; u < kAhead; ++u) {
+                const long long at = r + u * kDzWarps;
+                if (at >= r1) break;
+                dy[u] = __ldg(reinterpret_cast<const uint4*>(p.dy + at * p.dy_stride + n));
+                if constexpr (kAct != MOE_ACT_NONE) {
+                    const float4* zp = reinterpret_cast<const float4*>(p.z + (size_t)at * p.N + n);
+                    z[u][0] = __ldg(zp), z[u][1] = __ldg(zp + 1);
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += d[j];
+            for (int u = 0; u < kAhead; ++u) {
+                const long long at = r + u * kDzWarps;
+                if (at >= r1) break;
+                float d[8];
+                unpack_bf16x8(dy[u], d);
+                if constexpr (kAct != MOE_ACT_NONE) {
+                    const float v[8] = {z[u][0].x, z[u][0].y, z[u][0].z, z[u][0].w, z[u][1].x, z[u][1].y, z[u][1].z, z[u][1].w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[j] *= act_slope<kAct>(v[j]);
+                    *reinterpret_cast<uint4*>(p.dz + (size_t)at * p.N + n) = pack8(d);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += d[j];
+            }
         }
+    }
+    if constexpr (kBeside) {
+        if (n < p.N) {
+            float4* d = reinterpret_cast<float4*>(p.part + ((size_t)blockIdx.y * kDzWarps + warp) * p.N + n);
+            d[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            d[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // what comes after this kernel comes after the products too
+        return;
     }
     if (!p.part && !p.db) return;
 #pragma unroll
@@ -277,11 +303,18 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int p
     store_db(db, db_f32, c, v);
 }
 
-// Rows of blocks of linear_dz_kernel: six blocks for an SM, 16 rows each at least.
+// Rows of blocks of linear_dz_kernel, 32 rows each at least: six blocks for an SM.
 int dz_parts(long long T, int N) {
-    const long long cols = cdiv(N, 256), want = (6 * 152 + cols - 1) / cols, most = (T + 15) / 16;
+    const long long cols = cdiv(N, 256), want = (6 * 152 + cols - 1) / cols, most = (T + 31) / 32;
     const long long n = want < most ? want : most;
     return (int)(n < 1 ? 1 : n);
+}
+// Beside the products: one block for an SM at most (the next one would wait for
+// their end); 0: not in that form.
+int beside_parts(long long T, int N) {
+    const long long cols = cdiv(N, 256), most = T / 64;
+    const long long n = 152 / cols < most ? 152 / cols : most;
+    return (int)n;
 }
 
 // Launches a kernel that starts while the one before it (of the same call) ends.
@@ -325,7 +358,8 @@ LinearSizes linear_sizes(const moe_linear_shape& s) {
     z.part = linear_few(s) ? 0 : linear_product(s).part_bytes();
     z.dz = s.activation == MOE_ACT_NONE ? 0 : (long long)s.T * s.N * 2;
     const int parts = dz_parts(s.T, s.N);
-    z.sums = parts > 1 ? (long long)parts * s.N * 4 : 0;
+    const int beside = s.activation == MOE_ACT_NONE ? beside_parts(s.T, s.N) * kDzWarps : 0;
+    z.sums = parts > 1 || beside ? (long long)(parts > beside ? parts : beside) * s.N * 4 : 0;
     return z;
 }
 
@@ -372,26 +406,32 @@ int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaS
     long long dz_stride = f.dy_stride;
     const int parts = dz_parts(s.T, s.N);
     const bool grads = f.dx || f.dW, act = s.activation != MOE_ACT_NONE;
-    if ((act && grads) || f.db) {
-        DzArgs a = {static_cast<const __nv_bfloat16*>(f.dy), f.dy_stride, s.T, s.N, (s.T + parts - 1) / parts, f.z,
-                    static_cast<__nv_bfloat16*>(f.dz), f.db && parts > 1 ? f.sums : nullptr, parts > 1 ? nullptr : f.db,
-                    f.db_f32};
-        const dim3 grid(cdiv(s.N, 256), parts);
+    const int beside = f.db && grads && !act ? beside_parts(s.T, s.N) : 0;
+    auto join_db = [&](int n) {
+        return launch_after(linear_db_kernel, dim3(cdiv(s.N, 32)), 256, "linear_db", st, static_cast<const float*>(f.sums), n,
+                            s.N, f.db, f.db_f32);
+    };
+    DzArgs da = {static_cast<const __nv_bfloat16*>(f.dy), f.dy_stride, s.T, s.N, (s.T + parts - 1) / parts, f.z,
+                 static_cast<__nv_bfloat16*>(f.dz), f.db && parts > 1 ? f.sums : nullptr, parts > 1 ? nullptr : f.db,
+                 f.db_f32};
+    const dim3 dz_grid(cdiv(s.N, 256), parts);
+    if (act) {
         trace_pre(st);
         switch (s.activation) {
-            case MOE_ACT_SILU: linear_dz_kernel<MOE_ACT_SILU><<<grid, 32 * kDzWarps, 0, st>>>(a); break;
-            case MOE_ACT_GELU: linear_dz_kernel<MOE_ACT_GELU><<<grid, 32 * kDzWarps, 0, st>>>(a); break;
-            case MOE_ACT_GELU_TANH: linear_dz_kernel<MOE_ACT_GELU_TANH><<<grid, 32 * kDzWarps, 0, st>>>(a); break;
-            default: linear_dz_kernel<MOE_ACT_NONE><<<grid, 32 * kDzWarps, 0, st>>>(a); break;
+            case MOE_ACT_SILU: linear_dz_kernel<MOE_ACT_SILU, false><<<dz_grid, 32 * kDzWarps, 0, st>>>(da); break;
+            case MOE_ACT_GELU: linear_dz_kernel<MOE_ACT_GELU, false><<<dz_grid, 32 * kDzWarps, 0, st>>>(da); break;
+            default: linear_dz_kernel<MOE_ACT_GELU_TANH, false><<<dz_grid, 32 * kDzWarps, 0, st>>>(da); break;
         }
         trace_post(st, "linear_dz");
         if ((e = (int)cudaGetLastError())) return abi_cuda_fail(e, "linear dz launch");
-        if (act) dz = f.dz, dz_stride = s.N;
-        if (f.db && parts > 1) {
-            e = launch_after(linear_db_kernel, dim3(cdiv(s.N, 32)), 256, "linear_db", st, static_cast<const float*>(f.sums),
-                             parts, s.N, f.db, f.db_f32);
-            if (e) return abi_cuda_fail(e, "linear bias gradient launch");
-        }
+        dz = f.dz, dz_stride = s.N;
+        if (f.db && parts > 1 && (e = join_db(parts))) return abi_cuda_fail(e, "linear bias gradient launch");
+    } else if (f.db && !beside) {
+        trace_pre(st);
+        linear_dz_kernel<MOE_ACT_NONE, false><<<dz_grid, 32 * kDzWarps, 0, st>>>(da);
+        trace_post(st, "linear_dz");
+        if ((e = (int)cudaGetLastError())) return abi_cuda_fail(e, "linear column sums launch");
+        if (parts > 1 && (e = join_db(parts))) return abi_cuda_fail(e, "linear bias gradient launch");
     }
     if (!grads) return MOE_OK;
     // dW = x^T dz, dx = dz W^T: the deeper product first
@@ -430,7 +470,16 @@ int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaS
         if ((rc = map_op(&m.m[3 * i + 2], j.D, j.q.M, j.q.N, 32, "gradient (store)"))) return rc;
         ++i;
     }
-    e = launch_plain(a, m, "linear_grads", st);
+    // Without an activation the products start after all earlier work and the column
+    // sums of dy run beside them, in what they leave of an SM (8192 x 2048 x 7168: 290
+    // -> 268 us): dy is there before either starts.
+    e = launch_plain(a, m, "linear_grads", st, beside > 0);
+    if (!e && beside) {
+        da.per = (s.T + beside - 1) / beside;
+        da.part = f.sums;
+        e = launch_after(linear_dz_kernel<MOE_ACT_NONE, true>, dim3(dz_grid.x, beside), 32 * kDzWarps, "linear_dz", st, da);
+        if (!e) e = join_db(beside * kDzWarps);
+    }
     return e ? abi_cuda_fail(e, "linear gradient launch") : MOE_OK;
 }
 
