@@ -6,6 +6,11 @@ Trains the block for a few steps on a seeded synthetic target (autograd through
 layer_norm, moe_layer and gated_ffn), then quantizes both kinds of experts to
 4 bits and decodes token by token with them, as a server would.
 
+MixedBlock is a whole block: two projections (bias, activation) mix the features,
+the joint norms and gates what they give, adds it to the residual stream and
+norms the stream for the experts.  It decodes with the bf16 weights it was trained
+with, the expert layer in two kernels.
+
     python examples/moe_block.py [--tokens 512 --hidden 256 --inter 128 --experts 8 --topk 2 --steps 20]
 
 Needs a GB300 and the built library
@@ -22,8 +27,8 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from routed_grouped_gemm_routing_gb300.block import (  # noqa: E402
-    FFNWorkspace, W4Experts, W4Linear, gated_ffn, layer_norm, layer_norm_forward, quantize_w4)
-from routed_grouped_gemm_routing_gb300.layer import MoEWorkspace, moe_layer  # noqa: E402
+    FFNWorkspace, W4Experts, W4Linear, gated_ffn, layer_norm, layer_norm_forward, linear, quantize_w4, residual_norm)
+from routed_grouped_gemm_routing_gb300.layer import DecodeLayer, MoEWorkspace, moe_layer  # noqa: E402
 
 BF = torch.bfloat16
 
@@ -83,6 +88,48 @@ class W4Block:
         return x + self.routed(n, idx.to(torch.int32), torch.softmax(w, dim=1)) + self.shared(n)
 
 
+class MixedBlock(MoEBlock):
+    """A block whose first half is two projections:
+    s = x + gate norm(m) with m = gelu(x P1 + b1) P2 + b2,   y = s + routed(n) + shared(n), n = norm(s)."""
+
+    def __init__(self, H: int, I: int, E: int, k: int, seed: int = 0, device="cuda"):
+        super().__init__(H, I, E, k, seed, device)
+        g = torch.Generator(device=device).manual_seed(seed + 1)
+
+        def p(*shape, std):
+            return (torch.randn(shape, generator=g, device=device) * std).to(BF).requires_grad_()
+
+        self.P1, self.P2 = p(H, 2 * H, std=H ** -0.5), p(2 * H, H, std=(2 * H) ** -0.5)
+        self.b1, self.b2 = p(2 * H, std=0.1), p(H, std=0.1)
+        self.post_w = torch.ones(H, device=device, requires_grad=True)
+        self.gate = torch.full((H,), 0.5, device=device, requires_grad=True)
+
+    def parameters(self):
+        return super().parameters() + [self.P1, self.P2, self.b1, self.b2, self.post_w, self.gate]
+
+    def first_half(self, x):
+        """(s, n) bf16 [T, H]."""
+        m = linear(linear(x, self.P1, self.b1, activation="gelu"), self.P2, self.b2)
+        return residual_norm(m, x, self.norm_w, self.norm_b, post_weight=self.post_w, gate=self.gate, kind="rms")
+
+    def __call__(self, x, routing=None):
+        routed_ws, shared_ws = self.workspaces(x.shape[0])
+        s, n = self.first_half(x)
+        idx, w = self.route(n) if routing is None else routing
+        return s + moe_layer(n, self.W1, self.W2, idx, w, workspace=routed_ws) + gated_ffn(n, self.S1, self.S2, shared_ws)
+
+    def decoder(self):
+        """x bf16 [T, H] -> y for a few tokens at a time, on the weights as they are."""
+        experts = DecodeLayer(self.router, self.W1, self.W2, self.k, self.S1, self.S2)
+
+        def decode(x):
+            with torch.no_grad():
+                s, n = self.first_half(x)
+                return s + experts(n)
+
+        return decode
+
+
 def train(block: MoEBlock, tokens: int, steps: int, lr: float = 0.02):
     """Losses of plain gradient steps toward a fixed synthetic target."""
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -116,6 +163,15 @@ def main():
     print(f"4-bit decoding, one token at a time: {rel:.3f} of the block's update off its bf16 form")
     head = W4Linear(*quantize_w4(torch.randn(a.hidden, 1000, device="cuda").to(BF), 32), 32)
     print(f"logits of one token through a 4-bit projection: {list(head(got[:1].to(BF)).shape)}")
+    mixed = MixedBlock(a.hidden, a.inter, a.experts, a.topk)
+    x, losses = train(mixed, a.tokens, a.steps)
+    print(f"mixed block: loss {losses[0]:.4f} -> {losses[-1]:.4f} over {len(losses)} steps")
+    decode = mixed.decoder()
+    with torch.no_grad():
+        want = mixed(x).float()
+    got = torch.cat([decode(x[t: t + 1]) for t in range(16)]).float()
+    rel = float((got - want[:16]).norm() / want[:16].norm())
+    print(f"bf16 decoding, one token at a time: {rel:.4f} off the training form")
 
 
 if __name__ == "__main__":
