@@ -47,7 +47,10 @@ namespace {
 constexpr int kRnCols = 8;  // columns of a thread
 constexpr int kRnMaxH = 896 * kRnCols;
 constexpr int kRnLongThreads = 1024;
-constexpr int kRnRedBytes = 1024;  // of a group: two turns of 32 warps' float4
+// Of a group's sums: two turns of 32 warps' float4, or (many warps) three sums' parts
+// and results.
+constexpr int kRnRedBytes = 3 * 512 + 16;
+constexpr int kRnFewWarps = 8;
 constexpr int kRnSmem = 227 * 1024 - 64;  // dynamic, beside a few static bytes
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -157,24 +160,50 @@ struct Group {
         else
             asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(nt) : "memory");
     }
-    // Sums over the group, in the same order in every thread.
+    // Sums over the group, in the same order in every thread.  Shuffles and shared
+    // memory take their turns in one pipe: with many warps, each finishing the sum for
+    // itself, that pipe is what a row costs.  Then each warp leaves four parts, one
+    // warp adds them, and the others read the result.
     template <int N>
     __device__ __forceinline__ void sum(float (&v)[N]) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-        if (warps == 1) return;
         const int lane = threadIdx.x & 31;
-        float* r = reinterpret_cast<float*>(red + turn * 32);
-        turn ^= 1;
-        if (lane == 0) {
+        if (warps <= kRnFewWarps) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) r[4 * warp + i] = v[i];
+            for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+            if (warps == 1) return;
+            float* r = reinterpret_cast<float*>(red + turn * 32);
+            turn ^= 1;
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) r[4 * warp + i] = v[i];
+            }
+            sync();
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = lane < warps ? r[4 * lane + i] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int k = 16; k >= 4; k >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], k);
+        }
+        // parts [N][warps][4]; the results behind them
+        float* r = reinterpret_cast<float*>(red);
+        if (lane < 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[(i * 32 + warp) * 4 + lane] = v[i];
+        }
+        sync();
+        if (warp < N) {
+            const float4 f = lane < warps ? reinterpret_cast<const float4*>(r)[warp * 32 + lane] : make_float4(0, 0, 0, 0);
+            const float total = warp_sum((f.x + f.y) + (f.z + f.w));
+            if (lane == 0) r[N * 128 + warp] = total;
         }
         sync();
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = lane < warps ? r[4 * lane + i] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+        for (int i = 0; i < N; ++i) v[i] = r[N * 128 + i];
     }
     __device__ __forceinline__ float sum(float a) {
         float v[1] = {a};
