@@ -135,20 +135,6 @@ struct Param {
     }
 };
 
-// A load that stays where it is written, far ahead of its use.
-__device__ __forceinline__ float load_now(const float* p) {
-    float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
-}
-template <typename T>
-__device__ __forceinline__ float load_now(const Param<T>& w, uint32_t i) {
-    if (w.f32) return load_now(static_cast<const float*>(w.p) + i);
-    uint16_t u;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(u) : "l"(static_cast<const T*>(w.p) + i));
-    return to_f(*reinterpret_cast<const T*>(&u));
-}
-
 // A group of a block: nt threads that take one row at a time.
 struct Group {
     int id, t, nt, warps, warp;  // warp: within the group
@@ -446,11 +432,13 @@ __device__ __forceinline__ uint32_t plain_row(uint32_t row) {
     return row;
 }
 
-// Waits until the oldest of `stages` copies in flight has landed.
-__device__ __forceinline__ void ring_wait(int stages) {
-    if (stages == 2)
+// Waits until at most n of this thread's groups of copies are in flight (0 to 3).
+__device__ __forceinline__ void ring_wait(int n) {
+    if (n <= 0)
+        cp_async_wait_group<0>();
+    else if (n == 1)
         cp_async_wait_group<1>();
-    else if (stages == 3)
+    else if (n == 2)
         cp_async_wait_group<2>();
     else
         cp_async_wait_group<3>();
@@ -468,24 +456,43 @@ struct RnFwd {
 enum { kFwdW, kFwdPw, kFwdGate, kFwdB, kFwdPb };
 enum { kBwdW, kBwdPw, kBwdGate, kBwdPb };
 
-// rstd of v about its mean (0 for an RMS norm); columns past the row do not count.
-template <typename T, bool kVec, bool kRms, int E>
-__device__ __forceinline__ float2 row_stats(const Cols<E>& v, const Place<T, kVec, E>& at, Group& grp, const RnShape& s) {
-    if constexpr (kRms) {
-        return make_float2(0.0f, rsqrtf(grp.sum(dot(v, v)) * s.inv + s.eps));
-    } else {
-        const float mean = grp.sum(sum_of(v)) * s.inv;
-        Cols<E> d;
+// v about the mean, columns past the row 0.
+template <typename T, bool kVec, int E>
+__device__ __forceinline__ Cols<E> about(const Cols<E>& v, float mean, const Place<T, kVec, E>& at) {
+    constexpr int V = Place<T, kVec, E>::V;
+    Cols<E> d;
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            constexpr int V = Place<T, kVec, E>::V;
-            float2 f = unpack(v.p[i] + f2(-mean));
-            if (!at.in(2 * i / V)) f.x = 0.0f;
-            if (!at.in((2 * i + 1) / V)) f.y = 0.0f;
-            d.p[i] = f2(f.x, f.y);
-        }
-        return make_float2(mean, rsqrtf(grp.sum(dot(d, d)) * s.inv + s.eps));
+    for (int i = 0; i < E / 2; ++i) {
+        float2 f = unpack(v.p[i] + f2(-mean));
+        if (!at.in(2 * i / V)) f.x = 0.0f;
+        if (!at.in((2 * i + 1) / V)) f.y = 0.0f;
+        d.p[i] = f2(f.x, f.y);
     }
+    return d;
+}
+// Mean (0 for an RMS norm) and rstd of one or two rows, whose sums go together: what
+// a row costs is the sums' latency.
+template <typename T, bool kVec, bool kRms, int E, int kRows>
+__device__ __forceinline__ void row_stats(const Cols<E> (&v)[kRows], float2 (&st)[kRows], const Place<T, kVec, E>& at,
+                                          Group& grp, const RnShape& s) {
+    float a[kRows];
+    if constexpr (kRms) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) st[k].x = 0.0f, a[k] = dot(v[k], v[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) a[k] = sum_of(v[k]);
+        grp.sum(a);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            st[k].x = a[k] * s.inv;
+            const Cols<E> d = about(v[k], st[k].x, at);
+            a[k] = dot(d, d);
+        }
+    }
+    grp.sum(a);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) st[k].y = rsqrtf(a[k] * s.inv + s.eps);
 }
 
 template <typename T, bool kVec, bool kPost, bool kRms, bool kHeld, int kThreads>
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) rn_fwd_kernel(const RnFwd p) {
     const Ring<T, kVec, E, 2> ring = {at, rings + id * s.stages * 2 * s.row_bytes, s.row_bytes};
     ring.clear(s.stages);
     const T *o = static_cast<const T*>(p.o), *r = static_cast<const T*>(p.r);
-    // below 2^31 + 4 x 152 x 28: 32 bits without a sign
+    // below 2^31 + 64 x 152 x 32: 32 bits without a sign
     const uint32_t step = gridDim.x * s.groups, row0 = blockIdx.x * s.groups + id, rows = (uint32_t)s.rows;
     auto fetch = [&](int stage, uint32_t row) {
         if (row < rows) ring.fetch(stage, 0, o + row * p.os), ring.fetch(stage, 1, r + row * p.rs);
@@ -514,62 +521,96 @@ __global__ void __launch_bounds__(kThreads) rn_fwd_kernel(const RnFwd p) {
     param.fill(held, kFwdGate, s.gate == MOE_GATE_CHANNEL ? p.g : nullptr);
     param.fill(held, kFwdB, p.b);
     param.fill(held, kFwdPb, p.pb);
-    auto gate_of = [&](uint32_t row) {
-        return s.gate == MOE_GATE_TOKEN && row < rows ? load_now(Param<T>{p.g, s.w_f32}, row) : 1.0f;
+    // The tokens' gates of this group's next 32 rows, a lane each: a load for each row
+    // was waited for every time (8192 x 7168: 81 -> 107 us).
+    const bool token = s.gate == MOE_GATE_TOKEN;
+    float gates = 1.0f, gates_after = 1.0f;
+    auto load_gates = [&](uint32_t row) {
+        const uint32_t at = row + (threadIdx.x & 31) * step;
+        return at < rows ? Param<T>{p.g, s.w_f32}.at((int)at) : 1.0f;
     };
-    float next_gate = gate_of(row0);
+    if (token) gates_after = load_gates(row0);
+    uint32_t turn32 = 0;
     __syncthreads();
+    // The post norm's statistics are taken a row ahead, with those of the stream.
+    Raw<T, E> raw_o;
+    float2 ost = make_float2(0.0f, 1.0f);
+    if (kPost && row0 < rows) {
+        ring_wait(s.stages - 1);
+        if (!kVec) grp.sync();
+        raw_o = ring.read(0, 0, o + row0 * p.os);
+        const Cols<E> v[1] = {widen(raw_o)};
+        float2 st[1];
+        row_stats<T, kVec, kRms, E, 1>(v, st, at, grp, s);
+        ost = st[0];
+    }
     int stage = 0;
     for (uint32_t at_row = row0; at_row < rows; at_row += step) {
-        const uint32_t row = plain_row(at_row);
-        const float gate = next_gate;
-        next_gate = gate_of(row + step);
-        ring_wait(s.stages);
+        const uint32_t row = plain_row(at_row), after = row + step;
+        float gate = 1.0f;
+        if (token) {
+            if ((turn32 & 31) == 0) {
+                gates = gates_after;
+                gates_after = load_gates(row + 32 * step);
+            }
+            gate = __shfl_sync(0xffffffffu, gates, turn32 & 31);
+            ++turn32;
+        }
+        const bool ahead = kPost && after < rows;
+        ring_wait(s.stages - (kPost ? 2 : 1));
         if (!kVec) grp.sync();
-        Cols<E> v = widen(ring.read(stage, 0, o + row * p.os));
+        if (!kPost) raw_o = ring.read(stage, 0, o + row * p.os);
+        Cols<E> v[kPost ? 2 : 1];
+        v[0] = widen(raw_o);
         const Raw<T, E> raw_r = ring.read(stage, 1, r + row * p.rs);
         if constexpr (kPost) {
-            const float2 st = row_stats<T, kVec, kRms, E>(v, at, grp, s);
-            if (t == 0) p.stats[row] = st.x, p.stats[s.rows + row] = st.y;
+            if (t == 0) p.stats[row] = ost.x, p.stats[s.rows + row] = ost.y;
             const Cols<E> w = param(kFwdPw, p.pw);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (!kRms) v.p[i] = v.p[i] + f2(-st.x);
-                v.p[i] = v.p[i] * f2(st.y) * w.p[i];
+                if (!kRms) v[0].p[i] = v[0].p[i] + f2(-ost.x);
+                v[0].p[i] = v[0].p[i] * f2(ost.y) * w.p[i];
             }
             if (p.pb) {
                 const Cols<E> b = param(kFwdPb, p.pb);
 #pragma unroll
-                for (int i = 0; i < N; ++i) v.p[i] = v.p[i] + b.p[i];
+                for (int i = 0; i < N; ++i) v[0].p[i] = v[0].p[i] + b.p[i];
             }
         }
         if (s.gate == MOE_GATE_CHANNEL) {
             const Cols<E> g = param(kFwdGate, p.g);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v.p[i] = v.p[i] * g.p[i];
+            for (int i = 0; i < N; ++i) v[0].p[i] = v[0].p[i] * g.p[i];
         }
         {
             const Cols<E> res = widen(raw_r);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v.p[i] = fma2(f2(s.alpha), res.p[i], v.p[i] * f2(gate));
+            for (int i = 0; i < N; ++i) v[0].p[i] = fma2(f2(s.alpha), res.p[i], v[0].p[i] * f2(gate));
         }
-        at.store(static_cast<T*>(p.stream) + (size_t)row * s.H, v);
-        const float2 st = row_stats<T, kVec, kRms, E>(v, at, grp, s);
+        at.store(static_cast<T*>(p.stream) + (size_t)row * s.H, v[0]);
+        float2 st[kPost ? 2 : 1];
+        if constexpr (kPost) {
+            // (past the last row: this row's own, for nothing)
+            raw_o = ring.read(ahead ? (stage + 1 == s.stages ? 0 : stage + 1) : stage, 0, o + (ahead ? after : row) * p.os);
+            v[1] = widen(raw_o);
+        }
+        row_stats<T, kVec, kRms, E, kPost ? 2 : 1>(v, st, at, grp, s);
+        if constexpr (kPost) ost = st[1];
         // every thread has read the stage before the sums' barrier
         fetch(stage, row + s.stages * step);
-        if (t == 0) p.stats[2 * s.rows + row] = st.x, p.stats[3 * s.rows + row] = st.y;
+        if (t == 0) p.stats[2 * s.rows + row] = st[0].x, p.stats[3 * s.rows + row] = st[0].y;
         const Cols<E> w = param(kFwdW, p.w);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (!kRms) v.p[i] = v.p[i] + f2(-st.x);
-            v.p[i] = v.p[i] * f2(st.y) * w.p[i];
+            if (!kRms) v[0].p[i] = v[0].p[i] + f2(-st[0].x);
+            v[0].p[i] = v[0].p[i] * f2(st[0].y) * w.p[i];
         }
         if (p.b) {
             const Cols<E> b = param(kFwdB, p.b);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v.p[i] = v.p[i] + b.p[i];
+            for (int i = 0; i < N; ++i) v[0].p[i] = v[0].p[i] + b.p[i];
         }
-        at.store(static_cast<T*>(p.normed) + (size_t)row * s.H, v);
+        at.store(static_cast<T*>(p.normed) + (size_t)row * s.H, v[0]);
         if (++stage == s.stages) stage = 0;
     }
     cp_async_wait_all();
@@ -655,7 +696,7 @@ __global__ void __launch_bounds__(896) rn_bwd_kernel(const RnBwd p) {
     ring.clear(s.stages);
     const T *o = static_cast<const T*>(p.o), *r = static_cast<const T*>(p.r), *ds = static_cast<const T*>(p.ds),
             *dn = static_cast<const T*>(p.dn);
-    // below 2^31 + 4 x 152 x 28: 32 bits without a sign
+    // below 2^31 + 64 x 152 x 32: 32 bits without a sign
     const uint32_t step = gridDim.x * s.groups, row0 = blockIdx.x * s.groups + id, rows = (uint32_t)s.rows;
     auto fetch = [&](int stage, uint32_t row) {
         if (row < rows) {
@@ -672,16 +713,30 @@ __global__ void __launch_bounds__(896) rn_bwd_kernel(const RnBwd p) {
     param.fill(held, kBwdGate, s.gate == MOE_GATE_CHANNEL ? p.g : nullptr);
     if (kFour) param.fill(held, kBwdPb, p.pb);
     const bool token = s.gate == MOE_GATE_TOKEN, channel = s.gate == MOE_GATE_CHANNEL;
-    auto scalars = [&](uint32_t row) {
+    // A lane holds one of the group's next 32 rows': a load for each row was waited for
+    // every time (see the forward).
+    auto scalars = [&](uint32_t row0) {
+        const uint32_t row = row0 + (threadIdx.x & 31) * step;
         RnRow c = {0.0f, 1.0f, 0.0f, 0.0f, 1.0f};
         if (row >= rows) return c;
         if (kPost) {
-            if (!kRms) c.om = load_now(p.stats + row);
-            c.ors = load_now(p.stats + s.rows + row);
+            if (!kRms) c.om = __ldg(p.stats + row);
+            c.ors = __ldg(p.stats + s.rows + row);
         }
-        if (!kRms) c.m = load_now(p.stats + 2 * s.rows + row);
-        c.rs = load_now(p.stats + 3 * s.rows + row);
-        if (token) c.gt = load_now(Param<T>{p.g, s.w_f32}, row);
+        if (!kRms) c.m = __ldg(p.stats + 2 * s.rows + row);
+        c.rs = __ldg(p.stats + 3 * s.rows + row);
+        if (token) c.gt = Param<T>{p.g, s.w_f32}.at((int)row);
+        return c;
+    };
+    auto of_lane = [&](const RnRow& held, int lane) {
+        RnRow c = {0.0f, 1.0f, 0.0f, 0.0f, 1.0f};
+        if (kPost) {
+            if (!kRms) c.om = __shfl_sync(0xffffffffu, held.om, lane);
+            c.ors = __shfl_sync(0xffffffffu, held.ors, lane);
+        }
+        if (!kRms) c.m = __shfl_sync(0xffffffffu, held.m, lane);
+        c.rs = __shfl_sync(0xffffffffu, held.rs, lane);
+        if (token) c.gt = __shfl_sync(0xffffffffu, held.gt, lane);
         return c;
     };
     constexpr int kSums = kFour ? 4 : 2;  // of two, k is column sum 2 k
@@ -693,7 +748,8 @@ __global__ void __launch_bounds__(896) rn_bwd_kernel(const RnBwd p) {
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    RnRow next = scalars(row0);
+    RnRow held_rows = scalars(row0);
+    int turn32 = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -712,9 +768,13 @@ __global__ void __launch_bounds__(896) rn_bwd_kernel(const RnBwd p) {
     int stage = 0;
     for (uint32_t at_row = row0; at_row < rows; at_row += step) {
         const uint32_t row = plain_row(at_row);
-        const RnRow c = next;
-        next = scalars(row + step);
-        ring_wait(s.stages);
+        if (turn32 == 32) {
+            held_rows = scalars(row);
+            turn32 = 0;
+        }
+        __syncwarp();
+        const RnRow c = of_lane(held_rows, turn32++);
+        ring_wait(s.stages - 1);
         if (!kVec) grp.sync();
         const Raw<T, E> raw_o = ring.read(stage, 0, o + row * p.os), raw_dn = ring.read(stage, 2, dn + row * p.dns, dn != nullptr);
         auto normed_o = [&]() {  // N(o), or o
