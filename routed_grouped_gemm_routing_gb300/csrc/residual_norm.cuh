@@ -680,8 +680,8 @@ struct TmemSums {
 // kMode: an RMS or a layer norm without biases (column sums 0 and 2), or either
 // with all four.
 enum { kRms2, kLayer2, kAny4 };
-template <typename T, bool kVec, bool kPost, int kMode, bool kHeld>
-__global__ void __launch_bounds__(896) rn_bwd_kernel(const RnBwd p) {
+template <typename T, bool kVec, bool kPost, int kMode, bool kHeld, int kThreads>
+__global__ void __launch_bounds__(kThreads) rn_bwd_kernel(const RnBwd p) {
     constexpr int E = kRnCols, N = E / 2;
     constexpr bool kFour = kMode == kAny4, kRms = kMode == kRms2;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -1231,27 +1231,33 @@ int rn_backward(RnBwd& a, RnJoin& j, cudaStream_t st) {
     int blocks, smem, e;
     RnShape& s = a.s;
     const int params = a.pb ? 4 : s.gate == MOE_GATE_CHANNEL ? 3 : kPost ? 2 : 1;
-    if (!rn_plan(s, sizeof(T), 4, 896, params, &blocks, &smem)) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = s.H % V == 0 && a.os % V == 0 && a.rs % V == 0 && (!a.dn || a.dns % V == 0) &&
+                     (!a.ds || a.dss % V == 0) && on16(a.o) && on16(a.r) && on16(a.dn) && on16(a.ds) && on16(a.dout) &&
+                     on16(a.dres) && on16(a.pw) && on16(a.pb) && on16(a.w) && (s.gate != MOE_GATE_CHANNEL || on16(a.g));
+    // as in the forward (8192 x 4096, post norm: 104 -> 81 us), but FP32 rows, which
+    // stay as wide from pass to pass and would spill (4096 x 2048: 45 -> 207 us)
+    const int nt = rn_group_threads(s.H);
+    const bool more = vec && sizeof(T) == 2 && 1024 / nt > 896 / nt;
+    if (!rn_plan(s, sizeof(T), 4, more ? 1024 : 896, params, &blocks, &smem)) {
         blocks = rn_long_blocks(s.rows, s.H);
         trace_pre(st);
         rn_bwd_long_kernel<T><<<blocks, kRnLongThreads, 0, st>>>(a);
         trace_post(st, "residual_norm_bwd");
         e = (int)cudaGetLastError();
     } else {
-        constexpr int V = 16 / sizeof(T);
-        const bool vec = s.H % V == 0 && a.os % V == 0 && a.rs % V == 0 && (!a.dn || a.dns % V == 0) &&
-                         (!a.ds || a.dss % V == 0) && on16(a.o) && on16(a.r) && on16(a.dn) && on16(a.ds) && on16(a.dout) &&
-                         on16(a.dres) && on16(a.pw) && on16(a.pb) && on16(a.w) &&
-                         (s.gate != MOE_GATE_CHANNEL || on16(a.g));
         auto run = [&](auto kernel, SmemLimit& l) {
             return rn_launch(kernel, l, blocks, s.groups * s.nt, smem, a, "residual_norm_bwd", st);
         };
-        static SmemLimit l[4];
+        static SmemLimit l[6];
         if (s.in_smem == params)
-            e = vec ? run(rn_bwd_kernel<T, true, kPost, kMode, true>, l[0]) : run(rn_bwd_kernel<T, false, kPost, kMode, true>, l[1]);
+            e = !vec  ? run(rn_bwd_kernel<T, false, kPost, kMode, true, 896>, l[0])
+                : more ? run(rn_bwd_kernel<T, true, kPost, kMode, true, 1024>, l[1])
+                       : run(rn_bwd_kernel<T, true, kPost, kMode, true, 896>, l[2]);
         else
-            e = vec ? run(rn_bwd_kernel<T, true, kPost, kMode, false>, l[2])
-                    : run(rn_bwd_kernel<T, false, kPost, kMode, false>, l[3]);
+            e = !vec  ? run(rn_bwd_kernel<T, false, kPost, kMode, false, 896>, l[3])
+                : more ? run(rn_bwd_kernel<T, true, kPost, kMode, false, 1024>, l[4])
+                       : run(rn_bwd_kernel<T, true, kPost, kMode, false, 896>, l[5]);
     }
     if (e || !a.sums) return e;
     j.parts = blocks;
