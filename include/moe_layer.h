@@ -559,8 +559,10 @@ int moe_forward_w4(const moe_w4_shape* shape, const void* x, const uint8_t* W1_q
  * activation_clamp as moe_shape's for both (0: none), except that a NaN stays NaN.
  * 0 <= T <= 64, T k <= 1024, H, I and Is multiples of 8, k <= E <= 1024; all
  * pointers 16-byte aligned, topk_idx and topk_w 4-byte.  a is rounded to bf16 once
- * (an operand), sums are FP32, y is rounded once.  Deterministic: K ranges and slots
- * are added in a fixed order (which goes by the shape). */
+ * (an operand; up to 16 tokens to a pair of bf16, 16 significant bits), sums are
+ * FP32, y is rounded once.  Deterministic: K ranges and slots are added in a fixed
+ * order (which goes by the shape).  Calls on several streams may overlap, each with
+ * its own scratch. */
 typedef struct moe_decode_shape {
     int32_t T, H, I, E, k, Is;
     float activation_clamp;

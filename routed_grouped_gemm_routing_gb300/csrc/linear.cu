@@ -15,7 +15,12 @@
 // z stays FP32 for the backward: a rounding of z would come on top of dz's and
 // go into db without it.  dz is rounded once (an operand of dx and dW); db sums
 // the unrounded FP32 dz in a fixed order.  Without an activation dz is dy itself,
-// z is not kept and db takes one pass over dy.
+// z is not kept and db takes one pass over dy, beside the products.
+//
+// Measured (operations at the burst rate, bytes at the copy rate): 8192 x 2048 x 7168
+// with bias and residual 140 us forward (124), 271 us backward (248); 4096 x 2048 x
+// 2816 with silu 42 + 70 us (24 + 49): 176 tiles are three rounds over 76 pairs of SMs
+// where 2.3 would do, and dz takes 18 us of its own; 8 x 2048 x 7168 5.8 us (4.4).
 #include "dense_pair.cuh"
 #include "few_rows.cuh"
 

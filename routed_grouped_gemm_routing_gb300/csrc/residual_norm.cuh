@@ -19,8 +19,8 @@
 // variance is taken around the mean, never as E[v^2] - m^2.
 //
 // Bound by DRAM: forward 4, backward 6 rows of H elements.  Persistent blocks of
-// groups; a group of threads takes a row, eight columns a thread (the backward's column sums
-// stay in tensor memory for the life of the block).  The rows to come
+// groups; a group of threads takes a row, eight columns a thread (the backward's
+// column sums stay in tensor memory for the life of the block).  The rows to come
 // are copied ahead by cp.async into a ring of shared memory: rows that lie on
 // 16-byte boundaries by the thread that will read them, others as the whole
 // 16-byte pieces around them (kVec false), read element by element after the
@@ -29,6 +29,14 @@
 // stages.  Arithmetic is on pairs (fma.f32x2): at 8192 x 7168 the issue slots,
 // not DRAM, bound the first form of it.  Rows of more than 7168 columns are read
 // again for every pass.
+//
+// Measured, bf16 (the bytes at the copy rate): 8192 x 7168, RMS, post norm, a gate per
+// token 81 + 147 us (70 + 106), without post norm and gate 83 + 119 us; layer norms
+// with everything 121 + 195 us; 8192 x 4096, RMS with post norm 47 + 81 us (40 + 60);
+// 4096 x 2048, RMS 12.4 + 24 us (10 + 15).  What is left in the backward is the
+// latency of two sums a row with one row at a time on an SM (without them: 130 us)
+// and issue (53 %).  Rows off the 16-byte boundaries take two to five times the
+// instructions a column: 8192 x 7161 150 + 242 us.
 //
 // Column sums: one row of partial sums a block, joined in a fixed order by a
 // second kernel (deterministic, no atomics).

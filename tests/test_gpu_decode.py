@@ -262,3 +262,21 @@ def test_no_tokens_and_refusals():
     out = torch.empty(3, 64, device="cuda", dtype=BF)
     x = _x(6, 64)[::2]  # strided rows
     assert layer(x, out=out) is out and torch.equal(out, layer(x.contiguous()))
+
+
+def test_overlapping_calls_that_fill_the_gpu():
+    """Two calls at once, each with a block for every SM: none waits for a block that is not running."""
+    router, W1, W2, S1, S2 = _weights(1024, 512, 64, 512)
+    layer = DecodeLayer(router, W1, W2, 8, S1, S2)
+    xs = [_x(32, 1024, s) for s in (3, 4, 5)]
+    want = [layer(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(20):
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(layer(x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 3]) for i, g in enumerate(got))
