@@ -736,10 +736,14 @@ __global__ void __launch_bounds__(kDcThreads, 1)
                             gate = clamp_keep_nan(gate, p.clamp);
                             up = clamp_keep_nan(up, p.clamp);
                             const float a = gate / (1.0f + expf(-gate)) * up;
-                            const __nv_bfloat16 h = __float2bfloat16_rn(a);
+                            __nv_bfloat16 h = __float2bfloat16_rn(a);
+                            if constexpr (kTwo) {
+                                // (no rest of an infinity or a NaN; what only rounds to one is cut instead)
+                                if (isfinite(a) && isinf(__bfloat162float(h))) h = __float2bfloat16_rz(a);
+                                const float rest = isfinite(a) ? a - __bfloat162float(h) : 0.0f;
+                                act[(size_t)s * 2 * I + I + f] = __float2bfloat16_rn(rest);
+                            }
                             act[(size_t)s * (kTwo ? 2 : 1) * I + f] = h;
-                            // (no rest of an infinity or a NaN)
-                            if (kTwo) act[(size_t)s * 2 * I + I + f] = __float2bfloat16_rn(isfinite(a) ? a - __bfloat162float(h) : 0.0f);
                         }
                 }
             } else {

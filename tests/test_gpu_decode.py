@@ -242,6 +242,24 @@ def test_scratch_needs_no_clearing():
     assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
 
 
+def test_activation_next_to_the_largest():
+    """Activations of 1.99997 2^127 are finite in FP32 and round to infinity in bf16; up to
+    16 tokens the down projection takes them to 16 significant bits, which hold them."""
+    H, I = 64, 64
+    x = torch.zeros(2, H, device="cuda", dtype=BF)
+    x[:, :2] = 1.0
+    W1, W2 = torch.zeros(1, H, 2 * I, device="cuda", dtype=BF), torch.zeros(1, I, H, device="cuda", dtype=BF)
+    W1[0, 0, 0], W1[0, 0, I], W1[0, 1, I] = 1.9921875 * 2.0 ** 63, 2.0 ** 64, 2.0 ** 56
+    W2[0, 0] = 2.0 ** -100
+    x[1, 0], x[1, 1] = 2.0 ** 64, 0.0  # an up projection of 2^128: an infinity stays one
+    idx, w = torch.zeros(2, 1, device="cuda", dtype=torch.int32), torch.ones(2, 1, device="cuda")
+    y = DecodeLayer(None, W1, W2, 1)(x, idx, w).double()
+    want = 1.9921875 * (1 + 2.0 ** -8) * 2.0 ** 27
+    # half a step of y, and the second operand's own rounding
+    assert ((y[0] - want).abs() <= (HALF + 2.0 ** -15) * want).all()
+    assert (y[1] == float("inf")).all()
+
+
 def test_no_tokens_and_refusals():
     router, W1, W2, S1, S2 = _weights(64, 64, 8, 64)
     layer = DecodeLayer(router, W1, W2, 2, S1, S2)
