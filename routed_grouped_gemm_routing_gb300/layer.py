@@ -246,6 +246,8 @@ class DecodeLayer:
         if self.router is None:
             if topk_idx is None or topk_w is None or topk_idx.shape != (T, self.k) or topk_w.shape != (T, self.k):
                 raise ValueError(f"a layer without a router needs topk_idx and topk_w [{T}, {self.k}]")
+            if topk_idx.dtype is not torch.int32:  # ids that 32 bits would cut to an expert's stay outside
+                topk_idx = topk_idx.clamp(-1, self.E)
             topk_idx, topk_w = topk_idx.to(torch.int32).contiguous(), topk_w.to(torch.float32).contiguous()
         elif topk_idx is not None or topk_w is not None:
             raise ValueError("this layer has a router of its own")

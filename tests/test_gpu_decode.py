@@ -169,6 +169,16 @@ def test_given_routing(T, k):
     _check_layer(y, x, none, w, W1, W2, S1, S2)
 
 
+def test_wide_ids_outside_the_experts():
+    _, W1, W2, _, _ = _weights(64, 64, 8)
+    x = _x(4, 64)
+    idx = torch.tensor([[1, 2 ** 32 + 1], [-2 ** 32 + 3, 2], [2 ** 40, -2 ** 40], [2 ** 31, 7]], device="cuda")
+    w = torch.rand(4, 2, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda") + 0.5
+    y = DecodeLayer(None, W1, W2, 2)(x, idx, w)
+    want = DecodeLayer(None, W1, W2, 2)(x, torch.tensor([[1, -1], [-1, 2], [-1, -1], [-1, 7]], device="cuda", dtype=torch.int32), w)
+    assert torch.equal(y, want) and not y[2].any()
+
+
 def test_same_as_the_layer_of_training():
     T, H, I, E, k = 48, 256, 128, 8, 3
     router, W1, W2, _, _ = _weights(H, I, E)
