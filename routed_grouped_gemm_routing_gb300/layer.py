@@ -204,13 +204,20 @@ class DecodeLayer:
                 raise TypeError(f"{n} must be a bfloat16 CUDA tensor")
             if t.get_device() != W1.get_device():
                 raise ValueError(f"{n} is on {t.device}, W1 on {W1.device}")
-        self.router, self.W1, self.W2, self.S1, self.S2 = (None if t is None else t.detach().contiguous() for t in weights)
+        self._weights = tuple(None if t is None else t.detach().contiguous() for t in weights)
         self.E, self.H, self.I, self.k, self.Is = E, H, I, int(k), Is
         self.activation_clamp = float(activation_clamp)
-        self.device = self.W1.get_device()
+        self.device = W1.get_device()
         self._sizes = {}  # T -> shape, reference to it, workspace bytes
         self._size(1)  # sizes that the kernels do not take are refused here
-        self._ptrs = [None if t is None else t.data_ptr() for t in (self.router, self.W1, self.W2, self.S1, self.S2)]
+        self._ptrs = tuple(None if t is None else t.data_ptr() for t in self._weights)
+
+    # Read-only: calls go by the addresses taken above.
+    router = property(lambda self: self._weights[0])
+    W1 = property(lambda self: self._weights[1])
+    W2 = property(lambda self: self._weights[2])
+    S1 = property(lambda self: self._weights[3])
+    S2 = property(lambda self: self._weights[4])
 
     def _size(self, T):
         if T not in self._sizes:
@@ -231,7 +238,7 @@ class DecodeLayer:
             raise ValueError(f"expected x [T, {self.H}], got {list(sh)}")
         T, dev = sh[0], self.device
         s, ref, size = self._sizes.get(T) or self._size(T)
-        if (topk_idx is None and topk_w is None and out is None and self.router is not None and x.dtype is torch.bfloat16
+        if (topk_idx is None and topk_w is None and out is None and self._ptrs[0] is not None and x.dtype is torch.bfloat16
                 and x.get_device() == dev and dev == torch.cuda.current_device() and x.is_contiguous()):
             where = x.device
             topk_idx = torch.empty((T, self.k), dtype=torch.int32, device=where)
@@ -257,8 +264,7 @@ class DecodeLayer:
                 topk_w = torch.empty((T, self.k), dtype=torch.float32, device=x.device)
             ws = torch.empty((size,), dtype=torch.uint8, device=x.device)
             y = torch.empty((T, self.H), dtype=torch.bfloat16, device=x.device) if out is None else out
-            B.moe_decode_forward(s, x if x.is_contiguous() else x.contiguous(), self.router, self.W1, self.W2, self.S1,
-                                 self.S2, topk_idx, topk_w, ws, y)
+            B.moe_decode_forward(s, x if x.is_contiguous() else x.contiguous(), *self._weights, topk_idx, topk_w, ws, y)
         return (y, topk_idx, topk_w) if return_routing else y
 
     __call__ = forward

@@ -270,6 +270,19 @@ def test_activation_next_to_the_largest():
     assert (y[1] == float("inf")).all()
 
 
+def test_weights_cannot_be_swapped_under_a_layer():
+    router, W1, W2, S1, S2 = _weights(64, 64, 8, 64)
+    layer = DecodeLayer(router, W1, W2, 2, S1, S2)
+    x = _x(3, 64)
+    y = layer(x)
+    for n, t in (("router", router), ("W1", W1), ("W2", W2), ("S1", S1), ("S2", S2)):
+        assert getattr(layer, n).data_ptr() == t.data_ptr()
+        with pytest.raises(AttributeError):
+            setattr(layer, n, t.clone())
+    W2.mul_(2)  # the weights themselves are the caller's
+    assert not torch.equal(layer(x), y)
+
+
 def test_no_tokens_and_refusals():
     router, W1, W2, S1, S2 = _weights(64, 64, 8, 64)
     layer = DecodeLayer(router, W1, W2, 2, S1, S2)
