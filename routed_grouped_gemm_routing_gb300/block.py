@@ -330,7 +330,7 @@ def residual_norm(out, residual, weight, bias=None, post_weight=None, post_bias=
     last axis of 1).  Differentiable in every tensor, once."""
     if out.shape != residual.shape:
         raise ValueError(f"out {list(out.shape)} and residual {list(residual.shape)} differ")
-    if gate is not None and gate.dim() > 1 and gate.shape != (*out.shape[:-1], 1):
+    if gate is not None and gate.dim() != 1 and gate.shape != (*out.shape[:-1], 1):
         raise ValueError(f"expected gate [{out.shape[-1]}] or {[*out.shape[:-1], 1]}, got {list(gate.shape)}")
     return ResidualNormFunction.apply(out, residual, weight, bias, post_weight, post_bias, gate, float(residual_scale),
                                       float(eps), kind)

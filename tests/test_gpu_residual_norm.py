@@ -341,3 +341,5 @@ def test_refusals():
         residual_norm_backward(ds, dn, c["out"], c["residual"], c["weight"], stats[:, :9])
     with pytest.raises(ValueError):
         residual_norm(c["out"], c["residual"], c["weight"], gate=torch.ones(5, 1, device="cuda"))
+    with pytest.raises(ValueError):  # a number is no gate, a single row's neither
+        residual_norm(c["out"][:1], c["residual"][:1], c["weight"], gate=torch.tensor(1.0, device="cuda"))
