@@ -317,8 +317,9 @@ int moe_selftest_wait_timeout(const moe_shape* shape, void* route_ws, uint64_t l
 /* ------------------------------------------------------------------------
  * The rest of a block around the routed experts.  The pages have no
  * counterpart of these entry points: the norm in front of the router and the
- * experts, the dense gated feed-forward block that runs beside them (a shared
- * expert), and both kinds of experts with 4-bit weights for serving.  The
+ * experts, the joint of two halves of a block, the dense gated feed-forward block
+ * that runs beside them (a shared expert), projections, both kinds of experts with
+ * 4-bit weights for serving, and the whole expert layer for decoding.  The
  * conventions above hold for them too.  Each is deterministic for its shape,
  * but its kernels and the order of its sums are chosen by the number of rows
  * (and, in the norm, by alignment): the same row can differ in its last bits
@@ -559,7 +560,8 @@ int moe_forward_w4(const moe_w4_shape* shape, const void* x, const uint8_t* W1_q
  * activation_clamp as moe_shape's for both (0: none), except that a NaN stays NaN.
  * 0 <= T <= 64, T k <= 1024, H, I and Is multiples of 8, k <= E <= 1024; all
  * pointers 16-byte aligned, topk_idx and topk_w 4-byte.  a is rounded to bf16 once
- * (an operand; up to 16 tokens to a pair of bf16, 16 significant bits), sums are
+ * (an operand; up to 16 tokens to a pair of bf16, 16 significant bits; there an
+ * infinite weight of W2 or S2 gives NaN, an infinity in x stays one), sums are
  * FP32, y is rounded once.  Deterministic: K ranges and slots are added in a fixed
  * order (which goes by the shape).  Calls on several streams may overlap, each with
  * its own scratch. */

@@ -1,9 +1,10 @@
 """The rest of a block around the routed experts (``layer.moe_layer``).
 
-``layer_norm`` is the norm in front of the router and the experts.  Each op
-has an autograd form and a plain forward / backward pair for callers that run
-their own backward pass.  PyTorch only allocates the buffers and supplies the
-stream.
+``layer_norm`` is the norm in front of the router and the experts,
+``residual_norm`` the joint of two halves of a block, ``linear`` a projection with
+what surrounds its product.  Each op has an autograd form and a plain forward /
+backward pair for callers that run their own backward pass.  PyTorch only
+allocates the buffers and supplies the stream.
 """
 from __future__ import annotations
 

@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(256)
         for (int i = b * 256 + tid; i < n_counters; i += blocks * 256) counters[i] = 0;
     }
     const int e0 = blockIdx.x * 32, t0 = blockIdx.y * kTok, e = e0 + 8 * cv;
-    const int per = (H / 8 + kRtCluster - 1) / kRtCluster * 8, h0 = rank * per, h1 = h0 + per < H ? h0 + per : H;  // H is a multiple of 8
+    // multiples of 8, as H is
+    const int per = (H / 8 + kRtCluster - 1) / kRtCluster * 8, h0 = rank * per, h1 = h0 + per < H ? h0 + per : H;
     const bool whole = E % 8 == 0;  // rows of R on 16-byte boundaries
     float acc[kTok][8];
 #pragma unroll
@@ -176,7 +177,7 @@ struct DecodeArgs {
     int T, H, I, E, k, Is;
     float clamp;
     int kp1, kp1s, kp2, kp2s;  // K ranges: gate and up, down; of a routed expert and of the shared one
-    int stages, groups_cap;
+    int stages;
     const __nv_bfloat16* x;
     const float* logits;  // null: the routing is given
     int32_t* topk_idx;    // [T][k], written, or read without logits

@@ -230,6 +230,27 @@ def test_no_rows():
     assert dx.shape == (0, 64) and not dW.any() and not db.any()
 
 
+def test_elements_past_32_bits():
+    T, K, N, g = 300_001, 64, 7168, torch.Generator(device="cuda").manual_seed(3)
+    assert T * N > 2 ** 31
+    _, W, b, _, _ = _inputs(8, K, N)
+    x, r, dy = (torch.empty(T, n, device="cuda", dtype=BF).normal_(generator=g) for n in (K, N, N))
+    y, z = linear_forward(x, W, b, r, "silu", for_backward=True)
+    dx, dW, db = linear_backward(dy, x, W, z, b, "silu")
+    for at in (slice(0, 3), slice(T - 300, T)):
+        ref = _ref(x[at], W, b, r[at], dy[at], "silu")
+        _close("y", y[at], ref["y"])
+        _close("dx", dx[at], ref["dx"])
+    # some columns of dW: FP32 sums of T terms, 16 at a time, that may be cut instead of
+    # rounded at each step: (T / 16 + 64) 2^-22 of the sum of their sizes
+    cols = torch.cat([torch.arange(40, device="cuda"), torch.arange(N - 40, N, device="cuda")])
+    ref = _ref(x, W[:, cols], b[cols], r[:, cols], dy[:, cols], "silu")
+    size = x.double().abs().t() @ (dy[:, cols].double() * _act(z[:, cols].double(), "silu")[1]).abs()
+    want, tol = ref["dW"]
+    _close("dW", dW[:, cols], (want, tol + (T / 16 + 64) * 2.0 ** -22 * size))
+    _close("dbias", db[cols], ref["dbias"])
+
+
 def test_rows_behind_the_last_stay():
     for T in (5, 40, 300):
         x, W, b, r, dy = _inputs(T, 72, 136)

@@ -242,6 +242,21 @@ def test_constant_rows():
         _check(c, ds, dn)
 
 
+@pytest.mark.parametrize("H", [7168, 7161])
+def test_elements_past_32_bits(H):
+    rows, g = 300_001, torch.Generator(device="cuda").manual_seed(3)  # 300001 x 7161 > 2^31
+    assert rows * H > 2 ** 31
+    c = _case(8, H, gate="channel", kind="rms")[0]
+    c["out"], c["residual"], ds, dn = (torch.empty(rows, H, device="cuda", dtype=BF).normal_(generator=g) for _ in range(4))
+    stream, normed, stats = residual_norm_forward(**c)
+    bwd = {k: v for k, v in c.items() if k not in ("out", "residual", "weight")}
+    grads = residual_norm_backward(ds, dn, c["out"], c["residual"], c["weight"], stats, **bwd)
+    for at in (slice(0, 3), slice(rows - 400, rows)):
+        ref = _ref(dict(c, out=c["out"][at], residual=c["residual"][at]), ds[at], dn[at])
+        for n, v in (("stream", stream), ("normed", normed), ("dout", grads[0]), ("dresidual", grads[1])):
+            _close(n, v[at], ref[n])
+
+
 def test_no_rows():
     c, ds, dn = _case(0, 64)
     got = _run(c, ds, dn)
