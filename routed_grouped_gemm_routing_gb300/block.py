@@ -196,13 +196,13 @@ def _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate):
 _joint_plans = {}  # of a call's shape and options: shape, reference to it, bytes of the backward's scratch
 
 
-def _joint_plan(rows, H, xt, wt, kind, gk, residual_scale, eps):
-    key = (rows, H, xt, wt, kind, gk, residual_scale, eps)
+def _joint_plan(sh, xt, wt, kind, gk, residual_scale, eps):
+    key = (sh, xt, wt, kind, gk, residual_scale, eps)
     plan = _joint_plans.get(key)
     if plan is None:
         if len(_joint_plans) >= 1024:  # rows of every length have passed
             _joint_plans.clear()
-        s = B.residual_norm_shape(rows, H, xt, wt, kind, gk, residual_scale, eps)
+        s = B.residual_norm_shape(*sh, xt, wt, kind, gk, residual_scale, eps)
         plan = _joint_plans[key] = (s, ctypes.byref(s), max(B.moe_residual_norm_workspace(s), 16))
     return plan
 
@@ -211,16 +211,23 @@ def _ptr_of(t):
     return None if t is None else t.data_ptr()
 
 
-def _joint_plain(d, xt, wt, sh, gate, gk, rows, params):
-    """Whether what a call reads is contiguous, of the right types and shapes, on device d."""
+def _joint_plain(d, xt, wt, sh, post_weight, post_bias, gate, rows, params):
+    """The gate kind of a call whose tensors are all there, contiguous, of the right
+    types and shapes and on the current device d; else None, whatever the reason."""
+    if d < 0 or d != _current() or len(sh) != 2 or (post_bias is not None and post_weight is None):
+        return None
     for t in rows:
-        if t is not None and not _plain(t, xt, sh, d):
-            return False
+        if t is not None and (t.dtype is not xt or t.shape != sh or t.get_device() != d or not t.is_contiguous()):
+            return None
     hs = sh[1:]
     for t in params:
-        if t is not None and not _plain(t, wt, hs, d):
-            return False
-    return gate is None or (gate.dtype is wt and gate.get_device() == d and gate.is_contiguous())
+        if t is not None and (t.dtype is not wt or t.shape != hs or t.get_device() != d or not t.is_contiguous()):
+            return None
+    if gate is None:
+        return B.GATE_NONE
+    if gate.dtype is not wt or gate.get_device() != d or not gate.is_contiguous():
+        return None
+    return B.GATE_CHANNEL if gate.shape == hs else B.GATE_TOKEN if gate.shape == (sh[0], 1) else None
 
 
 def residual_norm_forward(out, residual, weight, bias=None, post_weight=None, post_bias=None, gate=None,
@@ -233,11 +240,11 @@ def residual_norm_forward(out, residual, weight, bias=None, post_weight=None, po
     out goes in as it is.  gate: [H] per channel, [rows, 1] per token, or None.
     Parameters and gate in out's type or all f32.  stats (f32 [4, rows]) is what
     residual_norm_backward reads."""
-    rows, H, gk = _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate)
-    xt, wt, d = out.dtype, weight.dtype, out.get_device()
-    s, ref, _ = _joint_plan(rows, H, xt, wt, kind, gk, residual_scale, eps)
-    if d >= 0 and d == _current() and _joint_plain(d, xt, wt, out.shape, gate, gk, (out, residual),
-                                                   (weight, bias, post_weight, post_bias)):
+    xt, wt, d, sh = out.dtype, weight.dtype, out.get_device(), out.shape
+    gk = _joint_plain(d, xt, wt, sh, post_weight, post_bias, gate, (out, residual), (weight, bias, post_weight, post_bias))
+    if gk is not None:
+        rows, H = sh
+        ref = _joint_plan(sh, xt, wt, kind, gk, residual_scale, eps)[1]
         stream, normed = torch.empty_like(out), torch.empty_like(out)
         stats = torch.empty((4, rows), dtype=_F32, device=out.device)
         rc = B.lib().moe_residual_norm_forward(
@@ -246,6 +253,8 @@ def residual_norm_forward(out, residual, weight, bias=None, post_weight=None, po
         if rc:
             B._check(rc)
         return stream, normed, stats
+    rows, H, gk = _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate)
+    s = _joint_plan((rows, H), xt, wt, kind, gk, residual_scale, eps)[0]
     with _on(out):
         dev = out.device
         stream = torch.empty((rows, H), dtype=out.dtype, device=dev)
@@ -260,17 +269,12 @@ def residual_norm_backward(dstream, dnormed, out, residual, weight, stats, bias=
     """(dout, dresidual, dweight, dbias, dpost_weight, dpost_bias, dgate) for the
     gradients of both outputs (either may be None), after residual_norm_forward
     on the same arguments; None for a parameter that is not there."""
-    rows, H, gk = _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate)
-    for t, n in ((dstream, "dstream"), (dnormed, "dnormed")):
-        if t is not None and t.shape != (rows, H):
-            raise ValueError(f"expected {n} [{rows}, {H}], got {list(t.shape)}")
-    if stats.shape != (4, rows):
-        raise ValueError(f"expected the forward's stats [4, {rows}], got {list(stats.shape)}")
-    xt, wt, d = out.dtype, weight.dtype, out.get_device()
-    s, ref, size = _joint_plan(rows, H, xt, wt, kind, gk, residual_scale, 1e-5)
-    if (d >= 0 and d == _current() and _plain(stats, _F32, (4, rows), d)
-            and _joint_plain(d, xt, wt, out.shape, gate, gk, (out, residual, dstream, dnormed),
-                             (weight, bias, post_weight, post_bias))):
+    xt, wt, d, sh = out.dtype, weight.dtype, out.get_device(), out.shape
+    gk = _joint_plain(d, xt, wt, sh, post_weight, post_bias, gate, (out, residual, dstream, dnormed),
+                      (weight, bias, post_weight, post_bias))
+    if gk is not None and _plain(stats, _F32, (4, sh[0]), d):
+        H = sh[1]
+        _, ref, size = _joint_plan(sh, xt, wt, kind, gk, residual_scale, 1e-5)
         dout, dres, dw = torch.empty_like(out), torch.empty_like(out), torch.empty_like(weight)
         db, dpw, dpb, dg = (None if p is None else torch.empty_like(p) for p in (bias, post_weight, post_bias, gate))
         ws = torch.empty((size,), dtype=torch.uint8, device=out.device)
@@ -281,6 +285,13 @@ def residual_norm_backward(dstream, dnormed, out, residual, weight, stats, bias=
         if rc:
             B._check(rc)
         return dout, dres, dw, db, dpw, dpb, dg
+    rows, H, gk = _joint_dims(out, residual, weight, bias, post_weight, post_bias, gate)
+    for t, n in ((dstream, "dstream"), (dnormed, "dnormed")):
+        if t is not None and t.shape != (rows, H):
+            raise ValueError(f"expected {n} [{rows}, {H}], got {list(t.shape)}")
+    if stats.shape != (4, rows):
+        raise ValueError(f"expected the forward's stats [4, {rows}], got {list(stats.shape)}")
+    s, _, size = _joint_plan((rows, H), xt, wt, kind, gk, residual_scale, 1e-5)
     with _on(out):
         dev = out.device
         dout = torch.empty((rows, H), dtype=out.dtype, device=dev)
@@ -563,12 +574,16 @@ def linear_forward(x, W, bias=None, residual=None, activation=None, for_backward
     rows of x and residual may be strided by multiples of 8.  activation: None,
     "silu", "gelu" (with erf) or "gelu_tanh".  z = x W + bias f32 [T, N] with
     for_backward and an activation, else None."""
-    plan_of, (s, ref, size, _) = _linear_dims(x, W, bias, residual, activation)
-    T, K, N, _ = plan_of
-    d, dev = x.get_device(), x.device
-    if (d >= 0 and d == _current() and _plain(x, _BF, (T, K), d) and _plain(W, _BF, (K, N), d)
-            and (bias is None or (bias.dtype in _BIAS and _plain(bias, bias.dtype, (N,), d)))
-            and (residual is None or _plain(residual, _BF, (T, N), d)) and (workspace is None or workspace.ws.get_device() == d)):
+    d, dev, sh, wh = x.get_device(), x.device, x.shape, W.shape
+    if (d >= 0 and d == _current() and len(sh) == 2 and len(wh) == 2 and sh[1] == wh[0] and x.dtype is _BF and W.dtype is _BF
+            and W.get_device() == d and x.is_contiguous() and W.is_contiguous()
+            and (bias is None or (bias.dtype in _BIAS and _plain(bias, bias.dtype, wh[1:], d)))
+            and (residual is None or _plain(residual, _BF, (sh[0], wh[1]), d))
+            and (workspace is None or workspace.ws.get_device() == d)):
+        T, K = sh
+        N = wh[1]
+        plan_of = T, K, N, activation
+        _, ref, size, _ = _linear_plan(*plan_of)
         y = torch.empty((T, N), dtype=_BF, device=dev)
         z = torch.empty((T, N), dtype=_F32, device=dev) if for_backward and activation is not None else None
         rc = B.lib().moe_linear_forward(
@@ -577,6 +592,8 @@ def linear_forward(x, W, bias=None, residual=None, activation=None, for_backward
         if rc:
             B._check(rc)
         return y, z
+    plan_of, (s, _, size, _) = _linear_dims(x, W, bias, residual, activation)
+    T, K, N, _ = plan_of
     with _on(x):
         y = torch.empty((T, N), dtype=_BF, device=dev)
         z = torch.empty((T, N), dtype=_F32, device=dev) if for_backward and activation is not None else None

@@ -241,12 +241,20 @@ class DecodeLayer:
         if (topk_idx is None and topk_w is None and out is None and self._ptrs[0] is not None and x.dtype is torch.bfloat16
                 and x.get_device() == dev and dev == torch.cuda.current_device() and x.is_contiguous()):
             where = x.device
-            topk_idx = torch.empty((T, self.k), dtype=torch.int32, device=where)
-            topk_w = torch.empty((T, self.k), dtype=torch.float32, device=where)
-            ws = torch.empty((size,), dtype=torch.uint8, device=where)
             y = torch.empty_like(x)
-            rc = B.lib().moe_decode_forward(ref, x.data_ptr(), *self._ptrs, topk_idx.data_ptr(), topk_w.data_ptr(),
-                                            ws.data_ptr(), y.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+            if return_routing:
+                topk_idx = torch.empty((T, self.k), dtype=torch.int32, device=where)
+                topk_w = torch.empty((T, self.k), dtype=torch.float32, device=where)
+                ws = torch.empty((size,), dtype=torch.uint8, device=where)
+                at = ws.data_ptr()
+                idx_at, w_at = topk_idx.data_ptr(), topk_w.data_ptr()
+            else:  # behind the scratch: an allocation costs as much as a tenth of a small layer
+                picks = 4 * T * self.k
+                ws = torch.empty((size + 2 * picks,), dtype=torch.uint8, device=where)
+                at = ws.data_ptr()
+                idx_at, w_at = at + size, at + size + picks
+            rc = B.lib().moe_decode_forward(ref, x.data_ptr(), *self._ptrs, idx_at, w_at, at, y.data_ptr(),
+                                            torch._C._cuda_getCurrentRawStream(dev))
             if rc:
                 B._check(rc)
             return (y, topk_idx, topk_w) if return_routing else y
