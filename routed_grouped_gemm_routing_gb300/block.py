@@ -607,30 +607,39 @@ def linear_backward(dy, x, W, z=None, bias=None, activation=None, want=(True, Tr
     (z: its second output, with for_backward; None without an activation).  dbias
     has bias's type, None without one.  want: whether dx and dW are; None is
     returned for one that is not.  The residual's gradient is dy."""
-    plan_of, (s, ref, _, size) = _linear_dims(x, W, bias, None, activation)
+    d, sh, wh = x.get_device(), x.shape, W.shape
+    want_x, want_w = want
+    if (d >= 0 and d == _current() and len(sh) == 2 and len(wh) == 2 and sh[1] == wh[0] and x.dtype is _BF and W.dtype is _BF
+            and W.get_device() == d and x.is_contiguous() and W.is_contiguous() and _plain(dy, _BF, (sh[0], wh[1]), d)
+            and (activation is None or (z is not None and _plain(z, _F32, (sh[0], wh[1]), d)))
+            and (bias is None or (bias.dtype in _BIAS and _plain(bias, bias.dtype, wh[1:], d)))
+            and (workspace is None or workspace.ws.get_device() == d)):
+        T, K = sh
+        N = wh[1]
+        plan_of = T, K, N, activation
+        _, ref, _, size = _linear_plan(*plan_of)
+        dx = torch.empty_like(x) if want_x else None
+        dW = torch.empty_like(W) if want_w else None
+        db = None if bias is None else torch.empty_like(bias)
+        rc = B.lib().moe_linear_backward(
+            ref, dy.data_ptr(), N, x.data_ptr(), K, W.data_ptr(), None if activation is None else z.data_ptr(),
+            _linear_ws(workspace, plan_of, size, x.device).data_ptr(), _ptr_of(dx), _ptr_of(dW), _ptr_of(db),
+            0 if db is None else _TYPES[db.dtype], _stream_of(d))
+        if rc:
+            B._check(rc)
+        return dx, dW, db
+    plan_of, (s, _, _, size) = _linear_dims(x, W, bias, None, activation)
     T, K, N, _ = plan_of
     if dy.shape != (T, N):
         raise ValueError(f"expected dy [{T}, {N}], got {list(dy.shape)}")
     if activation is not None and (z is None or z.shape != (T, N)):
         raise ValueError("the backward of an activation needs the forward's z (for_backward=True)")
-    d = x.get_device()
     with _on(x):
-        dx = torch.empty((T, K), dtype=_BF, device=x.device) if want[0] else None
-        dW = torch.empty((K, N), dtype=_BF, device=x.device) if want[1] else None
-        db = None if bias is None else torch.empty_like(bias)
+        dx = torch.empty((T, K), dtype=_BF, device=x.device) if want_x else None
+        dW = torch.empty((K, N), dtype=_BF, device=x.device) if want_w else None
+        db = None if bias is None else torch.empty((N,), dtype=bias.dtype, device=x.device)
         ws = _linear_ws(workspace, plan_of, size, x.device)
-        if activation is None:
-            z = None
-        if (_plain(dy, _BF, (T, N), d) and _plain(x, _BF, (T, K), d) and _plain(W, _BF, (K, N), d)
-                and ws.get_device() == d and (z is None or _plain(z, _F32, (T, N), d))
-                and (db is None or bias.dtype in _BIAS)):
-            rc = B.lib().moe_linear_backward(
-                ref, dy.data_ptr(), N, x.data_ptr(), K, W.data_ptr(), _ptr_of(z), ws.data_ptr(), _ptr_of(dx), _ptr_of(dW),
-                _ptr_of(db), 0 if db is None else _TYPES[db.dtype], _stream_of(d))
-            if rc:
-                B._check(rc)
-        else:
-            B.moe_linear_backward(s, dy, x, W, z, ws, dx, dW, db)
+        B.moe_linear_backward(s, dy, x, W, None if activation is None else z, ws, dx, dW, db)
     return dx, dW, db
 
 

@@ -19,8 +19,8 @@
 //
 // Measured (operations at the burst rate, bytes at the copy rate): 8192 x 2048 x 7168
 // with bias and residual 140 us forward (124), 271 us backward (248); 4096 x 2048 x
-// 2816 with silu 42 + 70 us (24 + 49): 176 tiles are three rounds over 76 pairs of SMs
-// where 2.3 would do, and dz takes 18 us of its own; 8 x 2048 x 7168 5.8 us (4.4).
+// 2816 with silu 42 + 67 us (24 + 49): 176 tiles are three rounds over 76 pairs of SMs
+// where 2.3 would do, and dz takes 16 us of its own; 8 x 2048 x 7168 5.8 us (4.4).
 #include "dense_pair.cuh"
 #include "few_rows.cuh"
 
@@ -217,6 +217,10 @@ struct DzArgs {
     int db_f32;
 };
 constexpr int kDzWarps = 8;
+// With an activation: four blocks on an SM with two rows ahead each keep as much in
+// flight as two with four rows and hide more of the slopes' arithmetic (4096 x 2816
+// silu 19 -> 16 us, gelu 25.5 -> 22).
+constexpr int kDzBlocks = 4;
 
 __device__ __forceinline__ void store_db(void* db, int f32, int n, float v) {
     if (f32)
@@ -228,14 +232,14 @@ __device__ __forceinline__ void store_db(void* db, int f32, int n, float v) {
 // kBeside: runs beside the products of the other gradients (see the launch), with no
 // shared memory, which they leave none of: a warp's sums are a row of part.
 template <int kAct, bool kBeside>
-__global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const DzArgs p) {
+__global__ void __launch_bounds__(32 * kDzWarps, kAct == MOE_ACT_NONE ? 1 : kDzBlocks) linear_dz_kernel(const DzArgs p) {
     __shared__ float red[kBeside ? 1 : kDzWarps][kBeside ? 1 : 256];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockIdx.x * 256 + 8 * lane;
     const long long r0 = (long long)blockIdx.y * p.per, r1 = r0 + p.per < p.rows ? r0 + p.per : p.rows;
     float sum[8] = {};
     if (n < p.N) {
-        constexpr int kAhead = kAct == MOE_ACT_NONE ? 8 : 4;  // rows whose loads are in flight together
+        constexpr int kAhead = kAct == MOE_ACT_NONE ? 8 : 2;  // rows whose loads are in flight together
         for (long long r = r0 + warp; r < r1; r += kDzWarps * kAhead) {
             uint4 dy[kAhead];
             float4 z[kAhead][2];
@@ -308,9 +312,9 @@ __global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int p
     store_db(db, db_f32, c, v);
 }
 
-// Rows of blocks of linear_dz_kernel, 32 rows each at least: six blocks for an SM.
+// Rows of blocks of linear_dz_kernel, 32 rows each at least: as many as run at once.
 int dz_parts(long long T, int N) {
-    const long long cols = cdiv(N, 256), want = (6 * 152 + cols - 1) / cols, most = (T + 31) / 32;
+    const long long cols = cdiv(N, 256), want = kDzBlocks * 152 / cols, most = (T + 31) / 32;
     const long long n = want < most ? want : most;
     return (int)(n < 1 ? 1 : n);
 }
