@@ -394,7 +394,7 @@ int moe_residual_norm_forward(const moe_residual_norm_shape* shape, const void* 
                               const void* post_bias, const void* weight, const void* bias, void* stream_out,
                               void* normed, float* stats, void* stream);
 
-/* Bytes of the backward's workspace.  Host only. */
+/* Bytes of the backward's workspace (0 for few rows: its pointer may be NULL).  Host only. */
 int moe_residual_norm_workspace(const moe_residual_norm_shape* shape, size_t* bytes);
 
 /* Backward given the gradients of s and n (dstream, dnormed [rows, H]; NULL:

@@ -591,7 +591,7 @@ def moe_residual_norm_backward(shape: MoeResidualNormShape, dstream, dnormed, ou
                                dgate, stream=None):
     """Backward of moe_residual_norm_forward: overwrites dout and dresidual
     [rows, H] and those parameters' gradients that are not None; dstream or
-    dnormed None: zero.  ws: uint8 of moe_residual_norm_workspace elements."""
+    dnormed None: zero.  ws: uint8 of moe_residual_norm_workspace elements (None for 0)."""
     dev, st = _here(stream)
     rows, H, xt, wt = shape.rows, shape.H, out.dtype, weight.dtype
 

@@ -203,7 +203,7 @@ def _joint_plan(sh, xt, wt, kind, gk, residual_scale, eps):
         if len(_joint_plans) >= 1024:  # rows of every length have passed
             _joint_plans.clear()
         s = B.residual_norm_shape(*sh, xt, wt, kind, gk, residual_scale, eps)
-        plan = _joint_plans[key] = (s, ctypes.byref(s), max(B.moe_residual_norm_workspace(s), 16))
+        plan = _joint_plans[key] = (s, ctypes.byref(s), B.moe_residual_norm_workspace(s))
     return plan
 
 
@@ -277,10 +277,10 @@ def residual_norm_backward(dstream, dnormed, out, residual, weight, stats, bias=
         _, ref, size = _joint_plan(sh, xt, wt, kind, gk, residual_scale, 1e-5)
         dout, dres, dw = torch.empty_like(out), torch.empty_like(out), torch.empty_like(weight)
         db, dpw, dpb, dg = (None if p is None else torch.empty_like(p) for p in (bias, post_weight, post_bias, gate))
-        ws = torch.empty((size,), dtype=torch.uint8, device=out.device)
+        ws = torch.empty((size,), dtype=torch.uint8, device=out.device) if size else None
         rc = B.lib().moe_residual_norm_backward(
             ref, _ptr_of(dstream), H, _ptr_of(dnormed), H, out.data_ptr(), H, residual.data_ptr(), H, _ptr_of(gate),
-            _ptr_of(post_weight), _ptr_of(post_bias), weight.data_ptr(), stats.data_ptr(), ws.data_ptr(), dout.data_ptr(),
+            _ptr_of(post_weight), _ptr_of(post_bias), weight.data_ptr(), stats.data_ptr(), _ptr_of(ws), dout.data_ptr(),
             dres.data_ptr(), dw.data_ptr(), _ptr_of(db), _ptr_of(dpw), _ptr_of(dpb), _ptr_of(dg), _stream_of(d))
         if rc:
             B._check(rc)
@@ -298,7 +298,7 @@ def residual_norm_backward(dstream, dnormed, out, residual, weight, stats, bias=
         dres = torch.empty((rows, H), dtype=out.dtype, device=dev)
         dw, db, dpw, dpb, dg = (None if p is None else torch.empty(p.shape, dtype=weight.dtype, device=dev)
                                 for p in (weight, bias, post_weight, post_bias, gate))
-        ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+        ws = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
         B.moe_residual_norm_backward(s, dstream, dnormed, out, residual, gate, post_weight, post_bias, weight, stats, ws,
                                      dout, dres, dw, db, dpw, dpb, dg)
     return dout, dres, dw, db, dpw, dpb, dg

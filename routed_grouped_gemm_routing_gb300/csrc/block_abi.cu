@@ -479,7 +479,7 @@ int moe_residual_norm_backward(const moe_residual_norm_shape* shape, const void*
         return MOE_OK;
     }
     const bool sums = dweight || dbias || dpost_weight || dpost_bias || (channel && dgate);
-    if (!out || !residual || !weight || !stats || !dout || !dresidual || (sums && !ws) ||
+    if (!out || !residual || !weight || !stats || !dout || !dresidual || (sums && !ws && residual_norm_part_bytes(*shape)) ||
         (shape->gate != MOE_GATE_NONE && !gate))
         return abi_fail(MOE_EINVAL, "NULL pointer argument");
     if (out_stride < shape->H || residual_stride < shape->H || (dstream && dstream_stride < shape->H) ||

@@ -625,6 +625,35 @@ __global__ void __launch_bounds__(kThreads) rn_fwd_kernel(const RnFwd p) {
 }
 
 // ---------------------------------------------------------------- backward
+struct RnJoin {
+    const float* part;
+    int parts, H, sums, w_f32, channel, post;
+    const void *g, *pw, *pb;
+    void *dw, *db, *dpw, *dpb, *dgate;  // null: not wanted
+};
+template <typename T>
+__device__ __forceinline__ void put_param(void* p, int f32, int c, float v) {
+    if (!p) return;
+    if (f32)
+        static_cast<float*>(p)[c] = v;
+    else
+        static_cast<T*>(p)[c] = from_f<T>(v);
+}
+// One column's gradients of its four sums.
+template <typename T>
+__device__ __forceinline__ void finish_column(const RnJoin& p, int c, const float (&v)[4]) {
+    put_param<T>(p.dw, p.w_f32, c, v[0]);
+    put_param<T>(p.db, p.w_f32, c, v[1]);
+    const float gate = p.channel ? Param<T>{p.g, p.w_f32}.at(c) : 1.0f;
+    put_param<T>(p.dpw, p.w_f32, c, gate * v[2]);
+    put_param<T>(p.dpb, p.w_f32, c, gate * v[3]);
+    if (p.channel && p.dgate) {
+        float d = v[2];
+        if (p.post) d = Param<T>{p.pw, p.w_f32}.at(c) * v[2] + (p.pb ? Param<T>{p.pb, p.w_f32}.at(c) * v[3] : 0.0f);
+        put_param<T>(p.dgate, p.w_f32, c, d);
+    }
+}
+
 struct RnBwd {
     RnShape s;
     const void *ds, *dn, *o, *r;  // ds, dn: may be null (zero)
@@ -636,6 +665,7 @@ struct RnBwd {
     void* dgate_typed;  // the same in the gate's type, where that is not FP32
     int sums;           // column sums: 0 dn z, 1 dn, 2 (q or D) oz or D o, 3 q or D; a bit each
     float* part;        // [blocks][4][H]
+    RnJoin join;        // kDirect
 };
 
 // What one row's scalars are: its statistics and its gate.
@@ -685,10 +715,20 @@ struct TmemSums {
     __device__ __forceinline__ static void settle() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 };
 
+// A float of block `rank` of the cluster, at this block's address of it.
+__device__ __forceinline__ float load_peer(const float* own, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(own)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
 // kMode: an RMS or a layer norm without biases (column sums 0 and 2), or either
 // with all four.
 enum { kRms2, kLayer2, kAny4 };
-template <typename T, bool kVec, bool kPost, int kMode, bool kHeld, int kThreads>
+// kDirect: few rows, the blocks are one cluster and add their column sums up themselves.
+template <typename T, bool kVec, bool kPost, int kMode, bool kHeld, int kThreads, bool kDirect = false>
 __global__ void __launch_bounds__(kThreads) rn_bwd_kernel(const RnBwd p) {
     constexpr int E = kRnCols, N = E / 2;
     constexpr bool kFour = kMode == kAny4, kRms = kMode == kRms2;
@@ -932,6 +972,7 @@ __global__ void __launch_bounds__(kThreads) rn_bwd_kernel(const RnBwd p) {
     // (the threads' own writes would be a quarter of a sector each).
     constexpr int V = Place<T, kVec, E>::V, NV = Place<T, kVec, E>::NV;
     float* col = reinterpret_cast<float*>(rings);  // [groups][E nt], in the parameters' order
+    float* mine = col + s.groups * E * s.nt;       // kDirect: [4][H], the block's
 #pragma unroll
     for (int k = 0; k < kSums; ++k) {
         const int sum = kFour ? k : 2 * k;
@@ -952,12 +993,26 @@ __global__ void __launch_bounds__(kThreads) rn_bwd_kernel(const RnBwd p) {
             }
         }
         __syncthreads();
-        float* part = p.part + ((size_t)blockIdx.x * 4 + sum) * s.H;
+        float* part = kDirect ? mine + sum * s.H : p.part + ((size_t)blockIdx.x * 4 + sum) * s.H;
         for (int c = threadIdx.x; c < s.H; c += blockDim.x) {
             float v = 0.0f;
             for (int gi = 0; gi < s.groups; ++gi) v += col[gi * E * s.nt + at.at(c)];
             part[c] = v;
         }
+    }
+    if constexpr (kDirect) {
+        __syncthreads();
+        cluster_sync();
+        for (int c = (int)(blockIdx.x * blockDim.x + threadIdx.x); c < s.H; c += (int)(gridDim.x * blockDim.x)) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (uint32_t b = 0; b < gridDim.x; ++b)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (p.sums >> k & 1) v[k] += load_peer(mine + k * s.H + c, b);
+            finish_column<T>(p.join, c, v);
+        }
+        __syncthreads();
+        cluster_sync();  // no block's memory goes while another reads it
     }
     tc_fence_before();
     __syncthreads();
@@ -1092,20 +1147,6 @@ __global__ void __launch_bounds__(kRnLongThreads) rn_bwd_long_kernel(const RnBwd
 }
 
 // ---------------------------------------------------------------- the join
-struct RnJoin {
-    const float* part;
-    int parts, H, sums, w_f32, channel, post;
-    const void *g, *pw, *pb;
-    void *dw, *db, *dpw, *dpb, *dgate;  // null: not wanted
-};
-template <typename T>
-__device__ __forceinline__ void put_param(void* p, int f32, int c, float v) {
-    if (!p) return;
-    if (f32)
-        static_cast<float*>(p)[c] = v;
-    else
-        static_cast<T*>(p)[c] = from_f<T>(v);
-}
 // 32 columns a block, eight threads a column and sum.
 template <typename T>
 __global__ void __launch_bounds__(256) rn_join_kernel(const RnJoin p) {
@@ -1131,16 +1172,7 @@ __global__ void __launch_bounds__(256) rn_join_kernel(const RnJoin p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[k] += red[k][i][lane];
     }
-    put_param<T>(p.dw, p.w_f32, c, v[0]);
-    put_param<T>(p.db, p.w_f32, c, v[1]);
-    const float gate = p.channel ? Param<T>{p.g, p.w_f32}.at(c) : 1.0f;
-    put_param<T>(p.dpw, p.w_f32, c, gate * v[2]);
-    put_param<T>(p.dpb, p.w_f32, c, gate * v[3]);
-    if (p.channel && p.dgate) {
-        float d = v[2];
-        if (p.post) d = Param<T>{p.pw, p.w_f32}.at(c) * v[2] + (p.pb ? Param<T>{p.pb, p.w_f32}.at(c) * v[3] : 0.0f);
-        put_param<T>(p.dgate, p.w_f32, c, d);
-    }
+    finish_column<T>(p, c, v);
 }
 
 // ----------------------------------------------------------------- launches
@@ -1149,13 +1181,13 @@ bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 // Groups, threads, ring and shared parameters (`params` of them at most) of a
 // call; false: rows too long for the ring.
 int rn_group_threads(int H) { return ((H + kRnCols - 1) / kRnCols + 31) / 32 * 32; }
-bool rn_plan(RnShape& s, int elt, int tensors, int threads, int params, int* blocks, int* smem) {
+bool rn_plan(RnShape& s, int elt, int tensors, int threads, int params, int* blocks, int* smem, int spread = 152) {
     if (s.H > kRnMaxH) return false;
     s.nt = rn_group_threads(s.H);
     int most = threads / s.nt;
     // sixteen hardware barriers, one of them the block's; a group of one warp needs none
     if (s.nt > 32 && most > 15) most = 15;
-    const long long want = (s.rows + 151) / 152;
+    const long long want = (s.rows + spread - 1) / spread;
     s.groups = (int)(want < most ? want : most);
     // the threads' columns, or the row and the bytes before an unaligned one
     s.row_bytes = s.nt * kRnCols * elt + 16;
@@ -1170,17 +1202,45 @@ bool rn_plan(RnShape& s, int elt, int tensors, int threads, int params, int* blo
     if (s.stages > 4) s.stages = 4;
     *smem = s.groups * kRnRedBytes + s.in_smem * param + s.stages * stage;
     const long long b = (s.rows + s.groups - 1) / s.groups;
-    *blocks = (int)(b < 152 ? b : 152);
+    *blocks = (int)(b < spread ? b : spread);
     return true;
 }
 
+// Few rows in a backward: at most two for a group of a cluster of eight blocks, whose
+// sums fit beside the groups' in the ring's place (with any number of parameters,
+// all of them held).  They need no second kernel and no partial sums in memory (64 x
+// 128 f32, everything on: 13.6 -> 7.2 us, and 5 us of the host's), but the rows of a
+// group come one after another (three: 168 x 1024 15.8 -> 19.5 us) and long ones are
+// added up by eight SMs alone (8 x 5000 11.5 -> 12.7 us).
+constexpr int kDirectBlocks = 8, kDirectRows = 2, kDirectMaxH = 2048;
+bool rn_direct(long long rows, int H, int elt) {
+    RnShape s = {};
+    s.rows = rows, s.H = H;
+    int blocks, smem;
+    if (rows < 1 || H > kDirectMaxH || !rn_plan(s, elt, 4, 896, 4, &blocks, &smem, kDirectBlocks)) return false;
+    return s.in_smem == 4 && rows <= (long long)kDirectRows * blocks * s.groups &&
+           s.stages * s.groups * 4 * s.row_bytes >= (s.groups * s.nt * kRnCols + 4 * H) * 4;
+}
+
 template <typename K, typename A>
-int rn_launch(K kernel, SmemLimit& limit, int blocks, int threads, int smem, const A& a, const char* name, cudaStream_t st) {
+int rn_launch(K kernel, SmemLimit& limit, int blocks, int threads, int smem, const A& a, const char* name, cudaStream_t st,
+              int cluster = 1) {
     if (const int e = limit.allow(kernel, kRnSmem)) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
     trace_pre(st);
-    kernel<<<blocks, threads, smem, st>>>(a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     trace_post(st, name);
-    return (int)cudaGetLastError();
+    return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 RnShape rn_shape(const moe_residual_norm_shape& s) {
@@ -1246,19 +1306,25 @@ int rn_backward(RnBwd& a, RnJoin& j, cudaStream_t st) {
     // as in the forward (8192 x 4096, post norm: 104 -> 81 us), but FP32 rows, which
     // stay as wide from pass to pass and would spill (4096 x 2048: 45 -> 207 us)
     const int nt = rn_group_threads(s.H);
-    const bool more = vec && sizeof(T) == 2 && 1024 / nt > 896 / nt;
-    if (!rn_plan(s, sizeof(T), 4, more ? 1024 : 896, params, &blocks, &smem)) {
+    const bool direct = a.sums && rn_direct(s.rows, s.H, sizeof(T));
+    a.join = j;
+    const bool more = !direct && vec && sizeof(T) == 2 && 1024 / nt > 896 / nt;
+    if (!rn_plan(s, sizeof(T), 4, more ? 1024 : 896, params, &blocks, &smem, direct ? kDirectBlocks : 152)) {
         blocks = rn_long_blocks(s.rows, s.H);
         trace_pre(st);
         rn_bwd_long_kernel<T><<<blocks, kRnLongThreads, 0, st>>>(a);
         trace_post(st, "residual_norm_bwd");
         e = (int)cudaGetLastError();
     } else {
+        if (direct && blocks > 1) blocks = kDirectBlocks;  // (the last ones may have no row)
         auto run = [&](auto kernel, SmemLimit& l) {
-            return rn_launch(kernel, l, blocks, s.groups * s.nt, smem, a, "residual_norm_bwd", st);
+            return rn_launch(kernel, l, blocks, s.groups * s.nt, smem, a, "residual_norm_bwd", st, direct ? blocks : 1);
         };
-        static SmemLimit l[6];
-        if (s.in_smem == params)
+        static SmemLimit l[8];
+        if (direct)
+            e = vec ? run(rn_bwd_kernel<T, true, kPost, kMode, true, 896, true>, l[6])
+                    : run(rn_bwd_kernel<T, false, kPost, kMode, true, 896, true>, l[7]);
+        else if (s.in_smem == params)
             e = !vec  ? run(rn_bwd_kernel<T, false, kPost, kMode, true, 896>, l[0])
                 : more ? run(rn_bwd_kernel<T, true, kPost, kMode, true, 1024>, l[1])
                        : run(rn_bwd_kernel<T, true, kPost, kMode, true, 896>, l[2]);
@@ -1267,7 +1333,7 @@ int rn_backward(RnBwd& a, RnJoin& j, cudaStream_t st) {
                 : more ? run(rn_bwd_kernel<T, true, kPost, kMode, false, 1024>, l[4])
                        : run(rn_bwd_kernel<T, true, kPost, kMode, false, 896>, l[5]);
     }
-    if (e || !a.sums) return e;
+    if (e || !a.sums || direct) return e;
     j.parts = blocks;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -1312,7 +1378,7 @@ int residual_norm_bwd(const moe_residual_norm_shape& s, const ResNormPtrs& f, cu
                      (f.dpost_bias || (channel && f.dgate && f.post_bias) ? 8 : 0);
     RnBwd a = {rn_shape(s), f.dstream, f.dnormed, f.out, f.residual, f.dstream_stride, f.dnormed_stride, f.out_stride,
                f.residual_stride, f.gate, f.post_weight, f.post_bias, f.weight, f.stats, f.dout, f.dresidual,
-               token && f32 ? static_cast<float*>(f.dgate) : nullptr, token && !f32 ? f.dgate : nullptr, sums, f.part};
+               token && f32 ? static_cast<float*>(f.dgate) : nullptr, token && !f32 ? f.dgate : nullptr, sums, f.part, {}};
     RnJoin j = {f.part, 0, s.H, sums, f32, channel, f.post_weight != nullptr, f.gate, f.post_weight, f.post_bias,
                 f.dweight, f.dbias, f.dpost_weight, f.dpost_bias, f.dgate};
     return rn_backward_t<T>(a, j, st);

@@ -4,6 +4,7 @@
 namespace moe {
 
 long long residual_norm_part_bytes(const moe_residual_norm_shape& s) {
+    if (rn_direct(s.rows, s.H, s.x_type == MOE_F32 ? 4 : 2)) return 0;
     const long long blocks = s.H > kRnMaxH ? rn_long_blocks(s.rows, s.H) : s.rows < 152 ? s.rows : 152;
     return blocks * 4 * s.H * 4;
 }

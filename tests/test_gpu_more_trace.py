@@ -46,6 +46,10 @@ def test_joint():
         names, (s, n, st) = _names(lambda: residual_norm_forward(o, r, w[:H]))
         assert names == ["residual_norm_fwd"]
         names, _ = _names(lambda: residual_norm_backward(s, n, o, r, w[:H], st))
+        assert names == ["residual_norm_bwd"]  # few rows: one cluster
+        o, r = _r(800, H), _r(800, H)
+        s, n, st = residual_norm_forward(o, r, w[:H])
+        names, _ = _names(lambda: residual_norm_backward(s, n, o, r, w[:H], st))
         assert names == ["residual_norm_bwd", "residual_norm_join"]
     w = torch.ones(9000, device="cuda")  # long rows
     o, r = _r(5, 9000), _r(5, 9000)

@@ -153,7 +153,8 @@ def _check(c, ds, dn):
     (2, 33, dict(t=F16, wt=F16)), (300, 64, dict(kind="rms", gate="none", post=False)), (500, 250, dict(wt=BF)),
     (1000, 256, dict(gate="token", post_bias=False)), (31, 257, dict(kind="rms", bias=False)),
     (700, 1001, dict(t=F16, alpha=1.25)), (400, 1024, dict(t=F32, kind="rms", post=False)),
-    (3000, 512, dict(gate="channel", post=False)), (640, 2048, dict(kind="rms", gate="none", post=False, bias=False)),
+    (3000, 512, dict(gate="channel", post=False)), (17, 264, dict()), (85, 1000, dict(t=F16)), (168, 1024, dict(wt=BF)),
+    (9, 2048, dict(gate="token")), (24, 3000, dict(t=F32)), (700, 33, dict(t=F16, wt=F16)), (2, 7168, dict()), (640, 2048, dict(kind="rms", gate="none", post=False, bias=False)),
     (333, 2049, dict(gate="token")), (200, 4100, dict(t=F32, gate="channel")), (170, 7161, dict(kind="rms", gate="token")),
     (200, 7168, dict(wt=BF)), (160, 7168, dict(t=F32, gate="token")), (20, 7169, dict(t=F16)), (9, 10000, dict(gate="token")),
     (400, 9000, dict(kind="rms", post=False)), (3, 40000, dict(t=F32, gate="channel", wt=F32)), (152, 7168, dict(post=False)),

@@ -55,8 +55,8 @@ def test_arguments(lib):
         assert _fwd(lib, **kw) == B.MOE_EINVAL, kw
     for kw in (dict(o=P[0] + 1), dict(g=P[2] + 2), dict(w=P[5] + 2), dict(n=P[8] + 1), dict(st=P[9] + 2)):
         assert _fwd(lib, **kw) == B.MOE_EUNSUPPORTED, kw
-    for kw in (dict(o=None), dict(r=None), dict(g=None), dict(pw=None), dict(w=None), dict(st=None), dict(ws=None), dict(do=None),
-               dict(dr=None), dict(dss=63), dict(dns=1), dict(os=63), dict(shape=dict(gate=0))):
+    for kw in (dict(o=None), dict(r=None), dict(g=None), dict(pw=None), dict(w=None), dict(st=None), dict(do=None),
+               dict(ws=None, shape=dict(rows=4000)), dict(dr=None), dict(dss=63), dict(dns=1), dict(os=63), dict(shape=dict(gate=0))):
         assert _bwd(lib, **kw) == B.MOE_EINVAL, kw
     for kw in (dict(ds=P[0] + 1), dict(dg=P[16] + 2), dict(ws=P[9] + 4), dict(dw=P[12] + 2)):
         assert _bwd(lib, **kw) == B.MOE_EUNSUPPORTED, kw
@@ -69,7 +69,9 @@ def test_sizes():
         return B.moe_residual_norm_workspace(B.residual_norm_shape(rows, H, torch.bfloat16, torch.float32))
 
     assert n(0, 64) == 0
-    for rows, H in ((1, 1), (5, 64), (10 ** 6, 7168), (3, 40000), (10 ** 6, 40000)):
+    for rows, H in ((1, 1), (5, 64), (8, 2048), (40, 1024)):
+        assert n(rows, H) == 0  # sums in one cluster
+    for rows, H in ((4000, 64), (200, 2048), (9, 7168), (10 ** 6, 7168), (3, 40000), (10 ** 6, 40000)):
         assert min(rows, 8) * 16 * H <= n(rows, H) <= 152 * 16 * H
     assert n(10 ** 6, 1 << 24) <= 16 * 16 << 24
 
