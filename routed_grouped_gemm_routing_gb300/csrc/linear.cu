@@ -294,22 +294,26 @@ __global__ void __launch_bounds__(32 * kDzWarps, kAct == MOE_ACT_NONE ? 1 : kDzB
         p.part[(size_t)blockIdx.y * p.N + c] = v;
 }
 
-// db from the blocks' sums, in order.  32 columns a block, eight threads a column.
-__global__ void __launch_bounds__(256) linear_db_kernel(const float* part, int parts, int N, void* db, int db_f32) {
-    __shared__ float red[8][32];
+// db from the blocks' sums, in order.  32 columns a block, a warp every 32nd of them.
+constexpr int kDbWarps = 32;
+__global__ void __launch_bounds__(32 * kDbWarps) linear_db_kernel(const float* part, int parts, int N, void* db, int db_f32) {
+    __shared__ float red[kDbWarps][33];
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
     float v = 0.0f;
-    if (c < N)
-#pragma unroll 4
-        for (int i = w; i < parts; i += 8) v += part[(size_t)i * N + c];
-    red[w][threadIdx.x & 31] = v;
+    for (int i = w; i < parts; i += 4 * kDbWarps) {  // four loads in flight: their latency is what this takes
+        float u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = i + k * kDbWarps < parts && c < N ? part[(size_t)(i + k * kDbWarps) * N + c] : 0.0f;
+        v += (u[0] + u[1]) + (u[2] + u[3]);
+    }
+    red[w][lane] = v;
     __syncthreads();
     if (w || c >= N) return;
-    v = 0.0f;
+    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += red[i][threadIdx.x];
-    store_db(db, db_f32, c, v);
+    for (int i = 0; i < kDbWarps; ++i) t[i & 3] += red[i][lane];
+    store_db(db, db_f32, c, (t[0] + t[1]) + (t[2] + t[3]));
 }
 
 // Rows of blocks of linear_dz_kernel, 32 rows each at least: as many as run at once.
@@ -417,7 +421,7 @@ int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaS
     const bool grads = f.dx || f.dW, act = s.activation != MOE_ACT_NONE;
     const int beside = f.db && grads && !act ? beside_parts(s.T, s.N) : 0;
     auto join_db = [&](int n) {
-        return launch_after(linear_db_kernel, dim3(cdiv(s.N, 32)), 256, "linear_db", st, static_cast<const float*>(f.sums), n,
+        return launch_after(linear_db_kernel, dim3(cdiv(s.N, 32)), 32 * kDbWarps, "linear_db", st, static_cast<const float*>(f.sums), n,
                             s.N, f.db, f.db_f32);
     };
     DzArgs da = {static_cast<const __nv_bfloat16*>(f.dy), f.dy_stride, s.T, s.N, (s.T + parts - 1) / parts, f.z,

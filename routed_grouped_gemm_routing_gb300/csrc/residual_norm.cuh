@@ -31,12 +31,12 @@
 // again for every pass.
 //
 // Measured, bf16 (the bytes at the copy rate): 8192 x 7168, RMS, post norm, a gate per
-// token 81 + 147 us (70 + 106), without post norm and gate 83 + 119 us; layer norms
-// with everything 121 + 195 us; 8192 x 4096, RMS with post norm 47 + 81 us (40 + 60);
+// token 81 + 143 us (70 + 106), without post norm and gate 82 + 118 us; layer norms
+// with everything 122 + 181 us; 8192 x 4096, RMS with post norm 46 + 77 us (40 + 60);
 // 4096 x 2048, RMS 12.4 + 24 us (10 + 15).  What is left in the backward is the
 // latency of two sums a row with one row at a time on an SM (without them: 130 us)
 // and issue (53 %).  Rows off the 16-byte boundaries take two to five times the
-// instructions a column: 8192 x 7161 150 + 242 us.
+// instructions a column: 8192 x 7161 150 + 235 us.
 //
 // Column sums: one row of partial sums a block, joined in a fixed order by a
 // second kernel (deterministic, no atomics).
@@ -968,17 +968,15 @@ __global__ void __launch_bounds__(kThreads) rn_bwd_kernel(const RnBwd p) {
     }
     cp_async_wait_all();
     acc.settle();
-    // The groups' column sums in the rings' place, then each column's added in order
-    // (the threads' own writes would be a quarter of a sector each).
+    // The groups' column sums in the rings' place, then each column's added in order by the
+    // thread that alone reads them (the threads' own writes would be a quarter of a sector
+    // each): all together (two stages are as much as four sums), but two sums with a post
+    // norm one after the other, with which the compiler leaves the rows' loop faster (8192 x
+    // 7168 145.6 -> 142.9 us; without a post norm 118 against 122).
     constexpr int V = Place<T, kVec, E>::V, NV = Place<T, kVec, E>::NV;
-    float* col = reinterpret_cast<float*>(rings);  // [groups][E nt], in the parameters' order
-    float* mine = col + s.groups * E * s.nt;       // kDirect: [4][H], the block's
-#pragma unroll
-    for (int k = 0; k < kSums; ++k) {
-        const int sum = kFour ? k : 2 * k;
-        if (!(p.sums >> sum & 1)) continue;
-        __syncthreads();
-        float* own = col + id * E * s.nt;
+    const int sum_floats = s.groups * E * s.nt;
+    float* col = reinterpret_cast<float*>(rings);  // [sums][groups][E nt], in the parameters' order
+    auto leave = [&](int k, float* own) {
         float f[E];
         at.singles(acc.load(k), f);
 #pragma unroll
@@ -992,12 +990,42 @@ __global__ void __launch_bounds__(kThreads) rn_bwd_kernel(const RnBwd p) {
                         make_float4(f[j * V + 4 * h], f[j * V + 4 * h + 1], f[j * V + 4 * h + 2], f[j * V + 4 * h + 3]);
             }
         }
+    };
+    if constexpr (kFour || kDirect || !kPost) {
         __syncthreads();
-        float* part = kDirect ? mine + sum * s.H : p.part + ((size_t)blockIdx.x * 4 + sum) * s.H;
-        for (int c = threadIdx.x; c < s.H; c += blockDim.x) {
-            float v = 0.0f;
-            for (int gi = 0; gi < s.groups; ++gi) v += col[gi * E * s.nt + at.at(c)];
-            part[c] = v;
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) leave(k, col + k * sum_floats + id * E * s.nt);
+        __syncthreads();
+        for (int c = p.sums ? (int)threadIdx.x : s.H; c < s.H; c += blockDim.x) {
+            float v[kSums];
+#pragma unroll
+            for (int k = 0; k < kSums; ++k) v[k] = 0.0f;
+            float* of = col + at.at(c);
+            for (int gi = 0; gi < s.groups; ++gi)
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) v[k] += of[k * sum_floats + gi * E * s.nt];
+#pragma unroll
+            for (int k = 0; k < kSums; ++k) {
+                const int sum = kFour ? k : 2 * k;
+                if constexpr (kDirect)
+                    of[k * sum_floats] = v[k];
+                else if (p.sums >> sum & 1)
+                    p.part[((size_t)blockIdx.x * 4 + sum) * s.H + c] = v[k];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) {
+            if (!(p.sums >> 2 * k & 1)) continue;
+            __syncthreads();
+            leave(k, col + id * E * s.nt);
+            __syncthreads();
+            float* part = p.part + ((size_t)blockIdx.x * 4 + 2 * k) * s.H;
+            for (int c = threadIdx.x; c < s.H; c += blockDim.x) {
+                float v = 0.0f;
+                for (int gi = 0; gi < s.groups; ++gi) v += col[gi * E * s.nt + at.at(c)];
+                part[c] = v;
+            }
         }
     }
     if constexpr (kDirect) {
@@ -1007,8 +1035,7 @@ __global__ void __launch_bounds__(kThreads) rn_bwd_kernel(const RnBwd p) {
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             for (uint32_t b = 0; b < gridDim.x; ++b)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (p.sums >> k & 1) v[k] += load_peer(mine + k * s.H + c, b);
+                for (int k = 0; k < kSums; ++k) v[kFour ? k : 2 * k] += load_peer(col + k * sum_floats + at.at(c), b);
             finish_column<T>(p.join, c, v);
         }
         __syncthreads();
@@ -1147,31 +1174,41 @@ __global__ void __launch_bounds__(kRnLongThreads) rn_bwd_long_kernel(const RnBwd
 }
 
 // ---------------------------------------------------------------- the join
-// 32 columns a block, eight threads a column and sum.
+// 32 columns a block, a warp every 32nd part; all of a thread's loads are in flight
+// together (a few at a time they were twenty trips to L2 one after another: the four
+// sums of 2048 x 1024 took 14.8 us of its 25.4, 5 of 16.2 now).
+constexpr int kJoinWarps = 32, kJoinMost = (152 + kJoinWarps - 1) / kJoinWarps;
 template <typename T>
-__global__ void __launch_bounds__(256) rn_join_kernel(const RnJoin p) {
-    __shared__ float red[4][8][33];
+__global__ void __launch_bounds__(32 * kJoinWarps) rn_join_kernel(const RnJoin p) {
+    __shared__ float red[4][kJoinWarps][33];
     asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, k8 = threadIdx.x >> 5;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < p.H) {
+    const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, warp = threadIdx.x >> 5;
+    float u[4][kJoinMost];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (!(p.sums >> k & 1)) continue;
-#pragma unroll 4
-            for (int i = k8; i < p.parts; i += 8) v[k] += p.part[((size_t)i * 4 + k) * p.H + c];
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < kJoinMost; ++i) {
+            const int part = warp + kJoinWarps * i;
+            u[k][i] = (p.sums >> k & 1) && part < p.parts && c < p.H ? p.part[((size_t)part * 4 + k) * p.H + c] : 0.0f;
         }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) red[k][k8][lane] = v[k];
-    __syncthreads();
-    if (k8 || c >= p.H) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        v[k] = 0.0f;
+        float v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k] += red[k][i][lane];
+        for (int i = 0; i < kJoinMost; ++i) v += u[k][i];
+        red[k][warp][lane] = v;
     }
+    __syncthreads();
+    if (warp < 4) {  // a warp a sum
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) v[i & 3] += red[warp][i][lane];
+        __syncwarp();
+        red[warp][0][lane] = (v[0] + v[1]) + (v[2] + v[3]);
+    }
+    __syncthreads();
+    if (warp || c >= p.H) return;
+    const float v[4] = {red[0][0][lane], red[1][0][lane], red[2][0][lane], red[3][0][lane]};
     finish_column<T>(p, c, v);
 }
 
@@ -1206,9 +1243,8 @@ bool rn_plan(RnShape& s, int elt, int tensors, int threads, int params, int* blo
     return true;
 }
 
-// Few rows in a backward: at most two for a group of a cluster of eight blocks, whose
-// sums fit beside the groups' in the ring's place (with any number of parameters,
-// all of them held).  They need no second kernel and no partial sums in memory (64 x
+// Few rows in a backward: at most two for a group of a cluster of eight blocks (with
+// any number of parameters, all of them held).  They need no second kernel and no partial sums in memory (64 x
 // 128 f32, everything on: 13.6 -> 7.2 us, and 5 us of the host's), but the rows of a
 // group come one after another (three: 168 x 1024 15.8 -> 19.5 us) and long ones are
 // added up by eight SMs alone (8 x 5000 11.5 -> 12.7 us).
@@ -1218,8 +1254,7 @@ bool rn_direct(long long rows, int H, int elt) {
     s.rows = rows, s.H = H;
     int blocks, smem;
     if (rows < 1 || H > kDirectMaxH || !rn_plan(s, elt, 4, 896, 4, &blocks, &smem, kDirectBlocks)) return false;
-    return s.in_smem == 4 && rows <= (long long)kDirectRows * blocks * s.groups &&
-           s.stages * s.groups * 4 * s.row_bytes >= (s.groups * s.nt * kRnCols + 4 * H) * 4;
+    return s.in_smem == 4 && rows <= (long long)kDirectRows * blocks * s.groups;
 }
 
 template <typename K, typename A>
@@ -1340,7 +1375,7 @@ int rn_backward(RnBwd& a, RnJoin& j, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)((s.H + 31) / 32));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
