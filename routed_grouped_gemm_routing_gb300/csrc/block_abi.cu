@@ -317,7 +317,7 @@ int moe_linear_workspace(const moe_linear_shape* shape, int32_t backward, size_t
     const int rc = check_linear(shape);
     if (rc) return rc;
     const LinearSizes z = linear_sizes(*shape);
-    *bytes = 256 + (backward ? up256((size_t)z.dz) + up256((size_t)z.sums) : up256((size_t)z.part));
+    *bytes = 256 + (backward ? up256((size_t)z.dz) + up256((size_t)z.sums) + up256((size_t)z.grads) : up256((size_t)z.part));
     return MOE_OK;
 }
 
@@ -391,6 +391,7 @@ int moe_linear_backward(const moe_linear_shape* shape, const void* dy, int64_t d
     f.status = reinterpret_cast<int32_t*>(w);
     f.dz = w + 256;
     f.sums = reinterpret_cast<float*>(w + 256 + up256((size_t)sz.dz));
+    f.part = reinterpret_cast<float*>(w + 256 + up256((size_t)sz.dz) + up256((size_t)sz.sums));
     f.dx = dx;
     f.dW = dW;
     f.db = dbias;

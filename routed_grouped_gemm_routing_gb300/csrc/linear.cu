@@ -377,6 +377,13 @@ int launch_after(K kernel, dim3 grid, int threads, const char* name, cudaStream_
     return (int)(e != cudaSuccess ? e : cudaGetLastError());
 }
 
+int launch_linear_join(const float* part, long long rows, int N, int splits, const LinearEpi& epi, void* out,
+                       cudaStream_t st) {
+    const long long blocks = (rows * (N / 8) + 127) / 128;
+    return launch_after(linear_join_kernel, dim3((unsigned)(blocks < 2432 ? blocks : 2432)), 128, "linear_join", st, part, rows, N,
+                        splits, epi, static_cast<__nv_bfloat16*>(out));
+}
+
 template <int EPI>
 int launch_linear_pair(const LinearArgs& a, const CUtensorMap (&m)[5], cudaStream_t st) {
     static std::atomic<int> fits[kMaxDevices] = {};
@@ -392,11 +399,67 @@ bool linear_few(const moe_linear_shape& s) {
 }
 Product linear_product(const moe_linear_shape& s) { return {s.T, s.N, s.K, false}; }
 
+// The gradients' products.  Together in one launch they have one range of K; one that is
+// deep and has few tiles (dW of many rows and a narrow layer, dx of a wide one) leaves most
+// pairs without work and is better by itself, its K split and joined (10000 x 64 x 72 silu
+// backward 48.6 -> 27.9 us, 8192 x 2048 x 64 52.5 -> 27.9, 130 x 64 x 7168 32.4 -> 23.7).
+Product dw_product(const moe_linear_shape& s) { return {s.K, s.N, s.T, false}; }
+Product dx_product(const moe_linear_shape& s) { return {s.T, s.K, s.N, false}; }
+// In clocks of a pair, with dense_shape's figures and 8000 for each launch of several (as
+// measured: 130 x 64 x 4096 is even, 20 us).
+long long alone_clocks(const Product& q) {
+    const Shape f = q.shape();
+    const long long tiles = (long long)cdiv(q.M, 256) * cdiv(q.N, f.width), kb = cdiv(q.K, 64);
+    const long long rounds = (tiles * f.splits + kDenseClusters - 1) / kDenseClusters;
+    return rounds * cdiv(kb, f.splits) * (f.width + 256) + 3000 +
+           (f.splits > 1 ? 7000 + (long long)q.M * q.N * f.splits * 8 / 2000 : 0);
+}
+long long together_clocks(const Product* q, int n) {  // of the busiest pair, at least
+    long long sum = 0, most = 0;
+    for (int i = 0; i < n; ++i) {
+        const long long item = (long long)cdiv(q[i].K, 64) * 512 + 3000;
+        sum += item * cdiv(q[i].M, 256) * cdiv(q[i].N, 256);
+        most = item > most ? item : most;
+    }
+    sum /= kDenseClusters;
+    return sum > most ? sum : most;
+}
+// Which of n <= 2 products get a launch of their own (a bit each).
+int split_alone(const Product* q, int n) {
+    int best = 0;
+    long long cost = n ? together_clocks(q, n) : 0;
+    for (int alone = 1; alone < 1 << n; ++alone) {
+        Product rest[2];
+        int left = 0;
+        long long c = 0;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            if (alone >> i & 1) {
+                ok = ok && q[i].shape().splits > 1;
+                c += alone_clocks(q[i]) + 8000;
+            } else {
+                rest[left++] = q[i];
+            }
+        }
+        if (left) c += together_clocks(rest, left) + 8000;
+        if (ok && c < cost) {
+            cost = c;
+            best = alone;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 LinearSizes linear_sizes(const moe_linear_shape& s) {
-    LinearSizes z = {0, 0, 0};
+    LinearSizes z = {0, 0, 0, 0};
     if (s.T == 0) return z;
+    // of those that some set of wanted gradients splits
+    const Product both[2] = {dw_product(s), dx_product(s)};
+    const int mask = split_alone(both, 2) | split_alone(both, 1) | split_alone(both + 1, 1) << 1;
+    for (int i = 0; i < 2; ++i)
+        if (mask >> i & 1) z.grads = both[i].part_bytes() > z.grads ? both[i].part_bytes() : z.grads;
     z.part = linear_few(s) ? 0 : linear_product(s).part_bytes();
     z.dz = s.activation == MOE_ACT_NONE ? 0 : (long long)s.T * s.N * 2;
     const int parts = dz_parts(s.T, s.N);
@@ -428,11 +491,7 @@ int launch_linear_forward(const moe_linear_shape& s, const LinearPtrs& f, cudaSt
         DenseMaps d = {m[0], m[1], {}, {}};
         if ((rc = abi_map_nd(&d.c0, f.part, 4, {s.N, 1, s.T, a.d.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
         e = launch_dense<KN, EPI_PART>(a.d, d, "linear", st, true);
-        const long long blocks = ((long long)s.T * (s.N / 8) + 127) / 128;
-        if (!e)
-            e = launch_after(linear_join_kernel, dim3((unsigned)(blocks < 2432 ? blocks : 2432)), 128, "linear_join", st,
-                             static_cast<const float*>(f.part), (long long)s.T, s.N, a.d.splits, epi,
-                             static_cast<__nv_bfloat16*>(f.y));
+        if (!e) e = launch_linear_join(f.part, s.T, s.N, a.d.splits, epi, f.y, st);
         return e ? abi_cuda_fail(e, "linear launch") : MOE_OK;
     }
     if ((rc = map_op(&m[2], f.y, s.T, s.N, 32, "y (store)"))) return rc;
@@ -450,10 +509,16 @@ int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaS
     const int parts = dz_parts(s.T, s.N);
     const bool grads = f.dx || f.dW, act = s.activation != MOE_ACT_NONE;
     const bool cluster = f.db && dz_cluster(s.T, s.N);
-    const int beside = f.db && grads && !act && !cluster ? beside_parts(s.T, s.N) : 0;
+    // dW = x^T dz, dx = dz W^T
+    Product wanted[2];
+    int n_wanted = 0;
+    if (f.dW) wanted[n_wanted++] = dw_product(s);
+    if (f.dx) wanted[n_wanted++] = dx_product(s);
+    const int alone = split_alone(wanted, n_wanted);
+    const int beside = f.db && grads && !act && !cluster && !alone ? beside_parts(s.T, s.N) : 0;
     auto join_db = [&](int n) {
-        return launch_after(linear_db_kernel, dim3(cdiv(s.N, 32)), 32 * kDbWarps, "linear_db", st, static_cast<const float*>(f.sums), n,
-                            s.N, f.db, f.db_f32);
+        return launch_after(linear_db_kernel, dim3(cdiv(s.N, 32)), 32 * kDbWarps, "linear_db", st,
+                            static_cast<const float*>(f.sums), n, s.N, f.db, f.db_f32);
     };
     DzArgs da = {static_cast<const __nv_bfloat16*>(f.dy), f.dy_stride, s.T, s.N, (s.T + parts - 1) / parts, f.z,
                  static_cast<__nv_bfloat16*>(f.dz), f.db && parts > 1 && !cluster ? f.sums : nullptr,
@@ -496,15 +561,41 @@ int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaS
         if (da.part && (e = join_db(parts))) return abi_cuda_fail(e, "linear bias gradient launch");
     }
     if (!grads) return MOE_OK;
-    // dW = x^T dz, dx = dz W^T: the deeper product first
+    // the deeper product first
     struct {
         Product q;
         bool mn;  // both operands lie along the output
         const void *A, *B;
         void* D;
         long long a_stride, b_stride;
-    } job[2] = {{{s.K, s.N, s.T, false, false}, true, f.x, dz, f.dW, f.x_stride, dz_stride},
-                {{s.T, s.K, s.N, false, false}, false, dz, f.W, f.dx, dz_stride, s.N}};
+    } job[2] = {{dw_product(s), true, f.x, dz, f.dW, f.x_stride, dz_stride},
+                {dx_product(s), false, dz, f.W, f.dx, dz_stride, s.N}};
+    bool first = !act && !f.db;  // of the call's kernels
+    if (alone) {
+        int bit = 1;
+        for (auto& j : job) {
+            if (!j.D) continue;
+            const bool by_itself = alone & bit;
+            bit <<= 1;
+            if (!by_itself) continue;
+            DenseArgs a = j.q.args(INFINITY, f.status);
+            DenseMaps m = {};
+            if ((rc = j.mn ? abi_map_2d(&m.a, j.A, 2, j.q.K, j.q.M, j.a_stride, 64, 64, "A (MN-major)")
+                           : abi_map_2d(&m.a, j.A, 2, j.q.M, j.q.K, j.a_stride, 64, 128, "A")))
+                return rc;
+            if ((rc = j.mn ? abi_map_2d(&m.b, j.B, 2, j.q.K, j.q.N, j.b_stride, 64, 64, "B (MN-major)")
+                           : abi_map_2d(&m.b, j.B, 2, j.q.N, j.q.K, j.b_stride, 64, a.width / 2, "B")))
+                return rc;
+            if ((rc = abi_map_nd(&m.c0, f.part, 4, {j.q.N, 1, j.q.M, a.splits}, {32, 1, 32, 1}, "partial sums"))) return rc;
+            e = j.mn ? launch_dense<NN, EPI_PART>(a, m, "linear_dw", st, first)
+                     : launch_dense<KK, EPI_PART>(a, m, "linear_dx", st, first);
+            if (!e) e = launch_linear_join(f.part, j.q.M, j.q.N, a.splits, {}, j.D, st);
+            if (e) return abi_cuda_fail(e, "linear gradient launch");
+            first = false;
+            j.D = nullptr;
+        }
+        if (!job[0].D && !job[1].D) return MOE_OK;
+    }
     if (s.N > s.T) {
         const auto t = job[0];
         job[0] = job[1];
@@ -535,7 +626,7 @@ int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaS
     // Without an activation the products start after all earlier work and the column
     // sums of dy run beside them, in what they leave of an SM (8192 x 2048 x 7168: 290
     // -> 268 us): dy is there before either starts.
-    e = launch_plain(a, m, "linear_grads", st, beside > 0);
+    e = launch_plain(a, m, "linear_grads", st, first || beside > 0);
     if (!e && beside) {
         da.per = (s.T + beside - 1) / beside;
         da.part = f.sums;

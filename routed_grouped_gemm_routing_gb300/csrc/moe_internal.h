@@ -189,9 +189,9 @@ struct LinearPtrs {
     int32_t* status;
 };
 // Bytes of the workspace's parts: partial sums of the forward's K ranges, dz, and
-// the partial column sums of db.
+// the partial column sums of db; partial sums of the gradients' K ranges.
 struct LinearSizes {
-    long long part, dz, sums;
+    long long part, dz, sums, grads;
 };
 LinearSizes linear_sizes(const moe_linear_shape& s);
 // MOE_OK or an error code with its message set.

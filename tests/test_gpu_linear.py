@@ -113,7 +113,8 @@ def _run(x, W, b, r, dy, act):
     (128, 2048, 2816, "gelu_tanh", BF, True), (129, 328, 200, None, None, True), (200, 4096, 256, "silu", BF, True),
     (256, 256, 256, None, None, False), (257, 264, 264, "gelu", BF, True), (300, 72, 2056, "silu", F32, False),
     (777, 1160, 712, "gelu", BF, True), (1000, 1000, 1000, "gelu_tanh", None, True), (2049, 136, 1032, None, F32, True),
-    (4096, 512, 2816, "silu", BF, False),
+    (4096, 512, 2816, "silu", BF, False), (130, 64, 7168, "gelu", F32, False), (10000, 64, 72, "silu", BF, True),
+    (9000, 72, 264, None, BF, False), (300, 136, 5000, None, None, True), (5000, 520, 264, "gelu_tanh", F32, False),
 ])
 def test_against_64_bits(T, K, N, act, bias, residual):
     inp = _inputs(T, K, N, T + K + N, bias, residual)
@@ -169,6 +170,26 @@ def test_each_gradient_alone():
         assert eW is None or torch.equal(eW, dW)
     ex, eW, eb = linear_backward(dy, x, W, z, None, "gelu")
     assert eb is None and torch.equal(ex, dx) and torch.equal(eW, dW)
+
+
+@pytest.mark.parametrize("T,K,N,act", [(9000, 72, 264, None), (130, 64, 7168, "silu"), (6000, 64, 6000, None), (10000, 2048, 64, "gelu")])
+def test_deep_gradients_alone(T, K, N, act):
+    """Products whose K is split, by themselves and beside the other one, with strided rows,
+    scratch filled before and not a byte of it behind its end touched."""
+    x, W, b, r, dy = _inputs(T, K, N, 5, residual=False)
+    x = torch.cat([x, x], 1)[:, :K]
+    z = linear_forward(x, W, b, None, act, True)[1]
+    ref = _ref(x, W, b, None, dy, act)
+    s = B.linear_shape(T, K, N, act)
+    n = B.moe_linear_workspace(s, True)
+    for dx, dW, db in ((True, True, True), (True, False, False), (False, True, False), (True, True, False), (False, True, True)):
+        ws = torch.full((n + 64,), 255, dtype=torch.uint8, device="cuda")
+        ws[:4] = 0
+        out = {"dx": torch.empty(T, K, device="cuda", dtype=BF) if dx else None, "dW": torch.empty(K, N, device="cuda", dtype=BF) if dW else None,
+               "dbias": torch.empty_like(b) if db else None}
+        B.moe_linear_backward(s, dy, x, W, z, ws, *out.values())
+        assert (ws[n:] == 255).all() and not ws[:4].any()
+        _check(out, ref)
 
 
 @pytest.mark.parametrize("T", [5, 70, 600])

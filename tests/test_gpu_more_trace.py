@@ -31,12 +31,13 @@ def test_linear():
         x, dy = _r(T, 2048), _r(T, 256)
         names, (y, z) = _names(lambda: linear_forward(x, W, b, dy, "silu", for_backward=True))
         assert names == fwd
+        grads = ["linear_dw", "linear_join", "linear_grads"] if T == 40000 else ["linear_grads"]  # dW: deep, few tiles
         names, _ = _names(lambda: linear_backward(dy, x, W, z, b, "silu"))
-        assert names == (["linear_dz", "linear_grads"] if T == 3 else ["linear_dz", "linear_db", "linear_grads"])
+        assert names == (["linear_dz"] if T == 3 else ["linear_dz", "linear_db"]) + grads
         names, _ = _names(lambda: linear_backward(dy, x, W, None, b))
-        assert names == (["linear_dz", "linear_grads"] if T == 3 else ["linear_grads", "linear_dz", "linear_db"])
+        assert names == (["linear_grads", "linear_dz", "linear_db"] if T == 300 else (["linear_dz"] if T == 3 else ["linear_dz", "linear_db"]) + grads)
         names, _ = _names(lambda: linear_backward(dy, x, W))
-        assert names == ["linear_grads"]
+        assert names == grads
 
 
 def test_joint():
