@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(256)
     __shared__ float red[8][kTok][32];
     __shared__ float all[kRtCluster][kTok][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // waited for before the stores to other blocks
     const int tid = threadIdx.x, cv = tid & 3, rl = tid >> 2, rank = (int)cluster_ctarank();
     {
         const int blocks = gridDim.x * gridDim.y * gridDim.z;
@@ -153,6 +154,9 @@ __global__ void __launch_bounds__(256)
             if ((tid & 31) < 4) red[tid >> 5][t][8 * cv + j] = v;
         }
     __syncthreads();
+    // No block's memory is written before that block runs: one whose range of the width is
+    // empty (H = 8: seven of eight) would be here at once.
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     // a block's sums go to the block that finishes their token (one token: all to the first)
     for (int i = tid; i < kTok * 32; i += 256) {
         const int t = i >> 5, c = i & 31;
