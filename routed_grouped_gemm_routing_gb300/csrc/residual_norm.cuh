@@ -55,9 +55,10 @@ namespace {
 constexpr int kRnCols = 8;  // columns of a thread
 constexpr int kRnMaxH = 896 * kRnCols;
 constexpr int kRnLongThreads = 1024;
-// Of a group's sums: two turns of 32 warps' float4, or (many warps) three sums' parts
-// and results.
-constexpr int kRnRedBytes = 3 * 512 + 16;
+// Of a group's sums: two turns of 32 warps' float4, or (many warps) the parts of up to
+// kRnSums sums and, behind all of them, the results.
+constexpr int kRnSums = 3, kRnResults = kRnSums * 32 * 4;
+constexpr int kRnRedBytes = kRnResults * 4 + 16;
 constexpr int kRnFewWarps = 8;
 constexpr int kRnSmem = 227 * 1024 - 64;  // dynamic, beside a few static bytes
 
@@ -183,7 +184,10 @@ struct Group {
 #pragma unroll
             for (int k = 16; k >= 4; k >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], k);
         }
-        // parts [N][warps][4]; the results behind them
+        // Parts [N][warps][4].  The results' place is the same for every N: a warp may still
+        // read them when another writes the next call's parts, and until that call's
+        // first barrier, which both pass, only those are written.
+        static_assert(N <= kRnSums, "parts");
         float* r = reinterpret_cast<float*>(red);
         if (lane < 4) {
 #pragma unroll
@@ -193,11 +197,11 @@ struct Group {
         if (warp < N) {
             const float4 f = lane < warps ? reinterpret_cast<const float4*>(r)[warp * 32 + lane] : make_float4(0, 0, 0, 0);
             const float total = warp_sum((f.x + f.y) + (f.z + f.w));
-            if (lane == 0) r[N * 128 + warp] = total;
+            if (lane == 0) r[kRnResults + warp] = total;
         }
         sync();
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = r[N * 128 + i];
+        for (int i = 0; i < N; ++i) v[i] = r[kRnResults + i];
     }
     __device__ __forceinline__ float sum(float a) {
         float v[1] = {a};
