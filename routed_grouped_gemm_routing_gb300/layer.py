@@ -261,9 +261,7 @@ class DecodeLayer:
         if self.router is None:
             if topk_idx is None or topk_w is None or topk_idx.shape != (T, self.k) or topk_w.shape != (T, self.k):
                 raise ValueError(f"a layer without a router needs topk_idx and topk_w [{T}, {self.k}]")
-            if topk_idx.dtype is not torch.int32:  # ids that 32 bits would cut to an expert's stay outside
-                topk_idx = topk_idx.clamp(-1, self.E)
-            topk_idx, topk_w = topk_idx.to(torch.int32).contiguous(), topk_w.to(torch.float32).contiguous()
+            topk_idx, topk_w = _expert_ids(topk_idx, self.E).contiguous(), topk_w.to(torch.float32).contiguous()
         elif topk_idx is not None or topk_w is not None:
             raise ValueError("this layer has a router of its own")
         with _on_device(x, dev):
@@ -276,6 +274,16 @@ class DecodeLayer:
         return (y, topk_idx, topk_w) if return_routing else y
 
     __call__ = forward
+
+
+def _expert_ids(topk_idx, E):
+    """Expert ids of any integer type as int32; what lies outside [0, E) stays outside."""
+    if topk_idx.dtype is torch.int32:
+        return topk_idx
+    if topk_idx.is_floating_point() or topk_idx.is_complex():
+        raise TypeError(f"topk_idx must be of an integer type, got {topk_idx.dtype}")
+    # in 64 bits: a narrow type holds neither bound, and 32 bits would cut a wide id to an expert's
+    return topk_idx.to(torch.int64).clamp(-1, E).to(torch.int32)
 
 
 def _on_device(x, dev):
