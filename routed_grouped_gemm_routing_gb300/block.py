@@ -13,6 +13,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 
@@ -73,6 +74,14 @@ def _first_order(backward):
         return tuple(None if t is None else next(marked) for t in out)
 
     return wrapped
+
+
+def _has_tangent(*tensors):
+    """Whether one of the tensors carries a tangent of forward-mode differentiation.
+    The operators have none: their autograd functions refuse such tensors, which a
+    call around those would take without their tangents and without a word."""
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 # -------------------------------------------------------------- layer norm
@@ -673,7 +682,7 @@ def linear(x, W, bias=None, residual=None, activation=None, workspace: LinearWor
     [..., N]; activation as in linear_forward.  Differentiable in all four, once."""
     if residual is not None and residual.shape != (*x.shape[:-1], W.shape[-1]):
         raise ValueError(f"expected residual {[*x.shape[:-1], W.shape[-1]]}, got {list(residual.shape)}")
-    if not torch.is_grad_enabled():
+    if not torch.is_grad_enabled() and not _has_tangent(x, W, bias, residual):
         return _no_grad_linear(x, W, bias, residual, activation, workspace)
     return LinearFunction.apply(x, W, bias, residual, activation, workspace)
 
