@@ -500,7 +500,8 @@ def gated_ffn(x, W1, W2, workspace: FFNWorkspace | None = None, activation_clamp
     requires one) the workspace's form is taken, without one the inference
     form."""
     clamp = None if activation_clamp is None else float(activation_clamp)
-    if not (torch.is_grad_enabled() and (x.requires_grad or W1.requires_grad or W2.requires_grad)):
+    wanted = torch.is_grad_enabled() and (x.requires_grad or W1.requires_grad or W2.requires_grad)
+    if not wanted and not _has_tangent(x, W1, W2):
         return _ffn_call(x, W1, W2, workspace, clamp, False)[-1].view(x.shape)
     return GatedFFNFunction.apply(x, W1, W2, workspace, clamp)
 
