@@ -173,6 +173,10 @@ class FP8Experts:
     __call__ = forward
 
 
+def _nowhere():
+    """The address of a weight that is not there."""
+
+
 class DecodeLayer:
     """The whole expert layer for the few tokens of decoding (up to 64, k times
     which up to 1024): router, top-k and softmax, routed experts, shared expert and
@@ -181,8 +185,10 @@ class DecodeLayer:
     router bf16 [H, E] (None: the routing is given to each call); W1 bf16 [E, H, 2I]
     (gate | up) and W2 bf16 [E, I, H] as ``moe_layer``'s; S1 [H, 2 Is] and S2 [Is, H]
     a shared expert, or None.  H, I and Is multiples of 8.  Keeps the weights as they
-    are (contiguous ones are not copied).  activation_clamp as in ``moe_layer``, for
-    both kinds of experts.  Not differentiable."""
+    are (contiguous ones are not copied; one whose storage the caller has freed is
+    refused, and read where it lies once it is there again, as large as before).
+    activation_clamp as in ``moe_layer``, for both kinds of experts.  Not
+    differentiable."""
 
     def __init__(self, router, W1, W2, k: int, S1=None, S2=None, activation_clamp: float = 0.0):
         E, H, I2 = W1.shape
@@ -210,9 +216,19 @@ class DecodeLayer:
         self.device = W1.get_device()
         self._sizes = {}  # T -> shape, reference to it, workspace bytes
         self._size(1)  # sizes that the kernels do not take are refused here
-        self._ptrs = tuple(None if t is None else t.data_ptr() for t in self._weights)
+        self._where = [_nowhere if t is None else t.data_ptr for t in self._weights]
+        self._addresses()
 
-    # Read-only: calls go by the addresses taken above.
+    def _addresses(self):
+        """Where the weights are now.  Their storages are the caller's, who may free one and make
+        it again between calls (sharded training does)."""
+        at = [f() for f in self._where]
+        if 0 in at:
+            n = ("router", "W1", "W2", "S1", "S2")[at.index(0)]
+            raise RuntimeError(f"the storage of {n} has been freed since the layer was made")
+        return at
+
+    # Read-only: their shapes and types are checked once, above.
     router = property(lambda self: self._weights[0])
     W1 = property(lambda self: self._weights[1])
     W2 = property(lambda self: self._weights[2])
@@ -238,7 +254,8 @@ class DecodeLayer:
             raise ValueError(f"expected x [T, {self.H}], got {list(sh)}")
         T, dev = sh[0], self.device
         s, ref, size = self._sizes.get(T) or self._size(T)
-        if (topk_idx is None and topk_w is None and out is None and self._ptrs[0] is not None and x.dtype is torch.bfloat16
+        weights = self._addresses()
+        if (topk_idx is None and topk_w is None and out is None and weights[0] is not None and x.dtype is torch.bfloat16
                 and x.get_device() == dev and dev == torch.cuda.current_device() and x.is_contiguous()):
             where = x.device
             y = torch.empty_like(x)
@@ -253,7 +270,7 @@ class DecodeLayer:
                 ws = torch.empty((size + 2 * picks,), dtype=torch.uint8, device=where)
                 at = ws.data_ptr()
                 idx_at, w_at = at + size, at + size + picks
-            rc = B.lib().moe_decode_forward(ref, x.data_ptr(), *self._ptrs, idx_at, w_at, at, y.data_ptr(),
+            rc = B.lib().moe_decode_forward(ref, x.data_ptr(), *weights, idx_at, w_at, at, y.data_ptr(),
                                             torch._C._cuda_getCurrentRawStream(dev))
             if rc:
                 B._check(rc)
