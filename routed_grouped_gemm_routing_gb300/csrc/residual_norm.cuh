@@ -1220,28 +1220,36 @@ __global__ void __launch_bounds__(32 * kJoinWarps) rn_join_kernel(const RnJoin p
 bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Groups, threads, ring and shared parameters (`params` of them at most) of a
-// call; false: rows too long for the ring.
+// call; false: rows too long for the ring.  As many groups as the threads allow; where
+// not even two stages of theirs fit, with no parameter beside them (the backward of
+// FP32 rows: 28 groups of 128 columns would take 276 KB), fewer: one fits at every width.
 int rn_group_threads(int H) { return ((H + kRnCols - 1) / kRnCols + 31) / 32 * 32; }
+// Groups that the rows ask for and the threads allow, spread over so many blocks.
+int rn_most_groups(long long rows, int nt, int threads, int spread) {
+    int most = threads / nt;
+    // sixteen hardware barriers, one of them the block's; a group of one warp needs none
+    if (nt > 32 && most > 15) most = 15;
+    const long long want = (rows + spread - 1) / spread;
+    return (int)(want < most ? want : most);
+}
 bool rn_plan(RnShape& s, int elt, int tensors, int threads, int params, int* blocks, int* smem, int spread = 152) {
     if (s.H > kRnMaxH) return false;
     s.nt = rn_group_threads(s.H);
-    int most = threads / s.nt;
-    // sixteen hardware barriers, one of them the block's; a group of one warp needs none
-    if (s.nt > 32 && most > 15) most = 15;
-    const long long want = (s.rows + spread - 1) / spread;
-    s.groups = (int)(want < most ? want : most);
     // the threads' columns, or the row and the bytes before an unaligned one
     s.row_bytes = s.nt * kRnCols * elt + 16;
-    const int stage = s.groups * tensors * s.row_bytes, param = s.nt * kRnCols * 4;
-    s.in_smem = params;
-    for (;; --s.in_smem) {
-        const int left = kRnSmem - s.groups * kRnRedBytes - s.in_smem * param;
-        s.stages = left / stage;
-        if (s.stages >= 2 || s.in_smem == 0) break;
-    }
-    if (s.stages < 2) return false;
+    const int param = s.nt * kRnCols * 4;
+    auto fits = [&](int in_smem) {
+        s.in_smem = in_smem;
+        s.stages = (kRnSmem - s.groups * kRnRedBytes - in_smem * param) / (s.groups * tensors * s.row_bytes);
+        return s.stages >= 2;
+    };
+    s.groups = rn_most_groups(s.rows, s.nt, threads, spread);
+    while (s.groups > 1 && !fits(0)) --s.groups;
+    int held = params;
+    while (held > 0 && !fits(held)) --held;
+    if (!fits(held)) return false;
     if (s.stages > 4) s.stages = 4;
-    *smem = s.groups * kRnRedBytes + s.in_smem * param + s.stages * stage;
+    *smem = s.groups * kRnRedBytes + s.in_smem * param + s.stages * s.groups * tensors * s.row_bytes;
     const long long b = (s.rows + s.groups - 1) / s.groups;
     *blocks = (int)(b < spread ? b : spread);
     return true;
@@ -1251,14 +1259,16 @@ bool rn_plan(RnShape& s, int elt, int tensors, int threads, int params, int* blo
 // any number of parameters, all of them held).  They need no second kernel and no partial sums in memory (64 x
 // 128 f32, everything on: 13.6 -> 7.2 us, and 5 us of the host's), but the rows of a
 // group come one after another (three: 168 x 1024 15.8 -> 19.5 us) and long ones are
-// added up by eight SMs alone (8 x 5000 11.5 -> 12.7 us).
+// added up by eight SMs alone (8 x 5000 11.5 -> 12.7 us).  Not where the groups had to be
+// fewer: 300 x 128 f32 8.2 us otherwise, 11.0 so, 96 x 1024 8.2 and 10.8.
 constexpr int kDirectBlocks = 8, kDirectRows = 2, kDirectMaxH = 2048;
 bool rn_direct(long long rows, int H, int elt) {
     RnShape s = {};
     s.rows = rows, s.H = H;
     int blocks, smem;
     if (rows < 1 || H > kDirectMaxH || !rn_plan(s, elt, 4, 896, 4, &blocks, &smem, kDirectBlocks)) return false;
-    return s.in_smem == 4 && rows <= (long long)kDirectRows * blocks * s.groups;
+    return s.in_smem == 4 && s.groups == rn_most_groups(rows, s.nt, 896, kDirectBlocks) &&
+           rows <= (long long)kDirectRows * blocks * s.groups;
 }
 
 template <typename K, typename A>
