@@ -314,6 +314,13 @@ int moe_read_status(const moe_shape* shape, const void* route_ws, int32_t* out, 
 int moe_selftest_wait_timeout(const moe_shape* shape, void* route_ws, uint64_t limit_ns, int64_t* elapsed_ns,
                               void* stream);
 
+/* Diagnostic: while it is on (not 0), calls of moe_linear_forward and _backward from
+ * any thread of this process launch their products with the abort flag raised from
+ * the start, as if a wait had just run out: their kernels leave by that path, with
+ * NaN in the outputs and bit 0 of the status word set.  No fault, no hang: every wait
+ * still ends with its copy or at the flag.  Off at first.  Host only. */
+int moe_selftest_give_up(int32_t on);
+
 /* ------------------------------------------------------------------------
  * The rest of a block around the routed experts.  The pages have no
  * counterpart of these entry points: the norm in front of the router and the
@@ -471,7 +478,8 @@ typedef struct moe_linear_shape {
  * overlap on the GPU need scratch of their own, unless it is 256 bytes: those hold
  * the status alone, nothing else lasts from call to call.  Word 0 is a status word:
  * the caller zeroes it once; bit 0 is set when a kernel gave up on a bounded wait,
- * and stays set.  Host only. */
+ * and stays set.  What that kernel was to compute is NaN then, so that a caller who
+ * cannot read the word sees it too.  Host only. */
 int moe_linear_workspace(const moe_linear_shape* shape, int32_t backward, size_t* bytes);
 
 /* Forward: overwrites y bf16 [T, N], and z f32 [T, N] where it is not NULL (what

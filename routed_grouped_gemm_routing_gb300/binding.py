@@ -759,6 +759,14 @@ def moe_selftest_wait_timeout(shape: MoeShape, route_ws, limit_ns: int, elapsed=
               _ptr(elapsed, torch.int64, 3, "elapsed"), _stream(stream)))
 
 
+def moe_selftest_give_up(on: bool):
+    """Diagnostic (see include/moe_layer.h): while on, the linear layer's products
+    take the path of a wait that ran out.  Process-wide; turn it off again."""
+    fn = lib().moe_selftest_give_up
+    fn.argtypes, fn.restype = [ctypes.c_int32], ctypes.c_int
+    _check(fn(int(bool(on))))
+
+
 NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_NOALLOC_SCRATCH_BYTES of include/moe_layer.h
 
 

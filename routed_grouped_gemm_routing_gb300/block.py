@@ -520,7 +520,8 @@ _no_sums = {}  # of a device: scratch of forwards that keep nothing but a status
 class LinearWorkspace:
     """Scratch of one linear layer's calls, kept from step to step; calls that
     share one must not overlap.  Without one, each call takes scratch of its own
-    whose status nobody can read."""
+    whose status nobody can read; what a kernel that gave up was to compute is NaN
+    either way."""
 
     def __init__(self, T: int, K: int, N: int, activation=None, device=None):
         dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())

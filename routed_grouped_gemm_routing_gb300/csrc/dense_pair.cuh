@@ -50,6 +50,8 @@ struct DenseArgs {
     int save_h;    // EPI_GATED: store h
     int32_t* status;
     __nv_bfloat16* out;  // EPI_GATED: a [M][N]; EPI_DGATE: dh [M][2][N]
+    float* part;         // EPI_PART: where the partial sums go, if they shall be NaN where a wait ran out
+    int gave_up;         // of the self-test: as if a wait had run out
 };
 struct DenseMaps {
     CUtensorMap a, b, c0, c1;
@@ -356,7 +358,7 @@ struct DenseCta {
 // Shared memory, barriers and TMEM of a CTA; returns when the pair is set up and
 // the kernel before this one in the stream has ended.
 template <int EPI>
-__device__ __forceinline__ DenseCta dense_begin() {
+__device__ __forceinline__ DenseCta dense_begin(int gave_up) {
     constexpr int kStages = dense_stages<EPI>();
     extern __shared__ uint8_t smem_raw[];
     DenseCta c;
@@ -383,7 +385,7 @@ __device__ __forceinline__ DenseCta dense_begin() {
         }
         mbar_init(c.bars.drain(), 1);
         for (int w = 0; w < kDenseEpiWarps; ++w) mbar_init(c.bars.hin(w), 1);
-        *c.abort = 0;
+        *c.abort = gave_up;
         fence_mbar_init();
     }
     if (c.warp == kDenseWarpMma) {
@@ -425,6 +427,22 @@ __device__ __forceinline__ void dense_end(const DenseCta& c, int32_t* status) {
     }
     if (threadIdx.x == 0 && *c.abort) atomicOr(reinterpret_cast<int*>(status), 1);
 }
+// After dense_end, where a wait gave up: NaN in rows [r0, r1) and columns [c0, c1) of an
+// output [..][ld], so that nobody takes what had arrived for its values.
+template <typename T>
+__device__ void dense_bad_tile(T* out, long long ld, int r0, int r1, int c0, int c1) {
+    const int cols = c1 - c0;
+    if (!out || cols <= 0) return;
+    for (int i = threadIdx.x; i < (r1 - r0) * cols; i += kDenseThreads) {
+        const int r = i / cols;
+        out[(r0 + r) * ld + c0 + i - r * cols] = (T)__int_as_float(0x7fffffff);
+    }
+}
+// This CTA's rows of the tile that begins at m0.
+__device__ __forceinline__ int2 dense_own_rows(const DenseCta& c, int m0, int M) {
+    const int r0 = m0 + 128 * c.rank, r1 = r0 + 128 < M ? r0 + 128 : M;
+    return make_int2(r0, r1 > r0 ? r1 : r0);
+}
 
 template <int MODE, int EPI>
 __global__ void __launch_bounds__(kDenseThreads, 1)
@@ -437,7 +455,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         // EPI_GATED without save_h has no third map: none was encoded
         if (EPI != EPI_GATED || p.save_h) tma_prefetch_map(EPI == EPI_GATED || EPI == EPI_DGATE ? &mC1 : &mC0);
     }
-    const DenseCta c = dense_begin<EPI>();
+    const DenseCta c = dense_begin<EPI>(p.gave_up);
     if (c.warp == kDenseWarpTma) {
         if (c.lane == 0) dense_producer<MODE, EPI>(&mA, &mB, p, c.ring, c.bars, c.abort, c.rank);
     } else if (c.warp == kDenseWarpMma) {
@@ -450,6 +468,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                             c.lane, c.rank);
     }
     dense_end(c, p.status);
+    if constexpr (EPI == EPI_PART) {
+        if (*c.abort && p.part) {
+            for (DenseWalk<EPI> w(p); w.valid(); w.next()) {
+                const DenseItem it = w.item();
+                const int2 r = dense_own_rows(c, it.m0, p.M);
+                dense_bad_tile(p.part + (size_t)it.split * p.M * p.N, p.N, r.x, r.y, it.n0,
+                               it.n0 + p.width < p.N ? it.n0 + p.width : p.N);
+            }
+        }
+    }
 }
 
 // ------------------------------------------------- products with bf16 output
@@ -458,11 +486,13 @@ constexpr int kPlainMost = 3;
 struct PlainProblem {
     int M, N, tiles_m, tiles_n, kblocks, width;
     int a_mn, b_mn;  // MN-major operands
+    __nv_bfloat16* out;  // [M][N], if it shall be NaN where a wait ran out
 };
 struct PlainArgs {
     int n;
     PlainProblem p[kPlainMost];
     int32_t* status;
+    int gave_up;  // of the self-test: as if a wait had run out
 };
 struct PlainMaps {
     CUtensorMap m[3 * kPlainMost];  // A, B, D of each
@@ -500,7 +530,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     plain_kernel(const __grid_constant__ PlainMaps maps, const __grid_constant__ PlainArgs a) {
     if (threadIdx.x == 32 * kDenseWarpTma)
         for (int i = 0; i < 3 * a.n; ++i) tma_prefetch_map(&maps.m[i]);
-    const DenseCta c = dense_begin<EPI_PLAIN>();
+    const DenseCta c = dense_begin<EPI_PLAIN>(a.gave_up);
     constexpr int kStages = dense_stages<EPI_PLAIN>();
     if (c.warp == kDenseWarpTma && c.lane == 0) {
         int stage = 0;
@@ -623,6 +653,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     }
     __syncwarp();
     dense_end(c, a.status);
+    if (*c.abort) {
+        for (PlainWalk w(a); w.valid(); w.next()) {
+            const PlainItem it = w.item();
+            const PlainProblem& q = a.p[it.p];
+            const int2 r = dense_own_rows(c, it.m0, q.M);
+            dense_bad_tile(q.out, q.N, r.x, r.y, it.n0, it.n0 + q.width < q.N ? it.n0 + q.width : q.N);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- the join
@@ -860,8 +898,8 @@ int map_op(CUtensorMap* m, const void* p, long long rows, int cols, int box_rows
     return abi_map_2d(m, p, 2, rows, cols, cols, 64, box_rows, what);
 }
 
-PlainProblem plain(const Product& q, int width, bool a_mn, bool b_mn) {
-    return {q.M, q.N, cdiv(q.M, 256), cdiv(q.N, width), cdiv(q.K, 64), width, a_mn, b_mn};
+PlainProblem plain(const Product& q, int width, bool a_mn, bool b_mn, void* out = nullptr) {
+    return {q.M, q.N, cdiv(q.M, 256), cdiv(q.N, width), cdiv(q.K, 64), width, a_mn, b_mn, static_cast<__nv_bfloat16*>(out)};
 }
 
 }  // namespace

@@ -26,6 +26,7 @@ struct FewArgs {
     float* h;            // gated: [T][2][F] or null
     int32_t* status;
     LinearEpi lin;  // FEW_LINEAR
+    int gave_up;    // of the self-test: as if a wait had run out
 };
 enum FewKind { FEW_PLAIN, FEW_GATED, FEW_LINEAR };
 
@@ -94,7 +95,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
         for (int i = 0; i < kFewSlots; ++i) mbar_init(bar + 8 * i, 1);
         fence_mbar_init();
     }
-    if (threadIdx.x == 0) *abort = 0;
+    if (threadIdx.x == 0) *abort = p.gave_up;
     __syncthreads();
 
     // ---- this warp's units: u0 + warp, + kWarps, ..
@@ -170,6 +171,17 @@ few_rows_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- the join: warps, then blocks.  The sums take the ring's place.
     __syncthreads();
+    const bool gave_up = *abort != 0;
+    if (gave_up) {
+        // Copies in flight land before the ring's place is taken.  This block's sums are
+        // NaN, and with them every output that they are a part of.
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+#pragma unroll
+        for (int i = 0; i < kMt * kNt * 4; ++i) acc[i >> 2][i & 3] = __int_as_float(0x7fffffff);
+        __syncthreads();
+    }
     if (p.kparts > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     float4* red = reinterpret_cast<float4*>(smem);                     // [kHalf][kSums / 4]
     float* all = reinterpret_cast<float*>(smem + kHalf * kSums * 4);  // [kparts][gate, up][share], one share a block
@@ -234,12 +246,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ 
         }
         p.out[row * p.F + f] = __float2bfloat16_rn(v);
     }
-    if (*abort) {  // copies in flight land before the block's shared memory goes
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 2000000ull) {
-        }
-        if (threadIdx.x == 0) atomicOr(reinterpret_cast<int*>(p.status), 1);
-    }
+    if (gave_up && threadIdx.x == 0) atomicOr(reinterpret_cast<int*>(p.status), 1);
 }
 
 template <FewKind kKind, int kNt>

@@ -32,6 +32,7 @@ namespace {
 struct LinearArgs {
     DenseArgs d;
     LinearEpi e;
+    __nv_bfloat16* y;
 };
 
 // 32 values of the bias, columns from n on; zero past N (a multiple of 8).
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         if (EPI == EPI_LIN_R || EPI == EPI_LIN_RZ) tma_prefetch_map(&mR);
         if (EPI == EPI_LIN_Z || EPI == EPI_LIN_RZ) tma_prefetch_map(&mZ);
     }
-    const DenseCta c = dense_begin<EPI>();
+    const DenseCta c = dense_begin<EPI>(a.d.gave_up);
     if (c.warp == kDenseWarpTma) {
         if (c.lane == 0) dense_producer<KN, EPI>(&mA, &mB, a.d, c.ring, c.bars, c.abort, c.rank);
     } else if (c.warp == kDenseWarpMma) {
@@ -172,6 +173,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         linear_epilogue<EPI>(&mY, &mR, &mZ, a, c);
     }
     dense_end(c, a.d.status);
+    if (*c.abort) {
+        for (DenseWalk<EPI> w(a.d); w.valid(); w.next()) {
+            const DenseItem it = w.item();
+            const int2 r = dense_own_rows(c, it.m0, a.d.M);
+            const int last = it.n0 + a.d.width < a.d.N ? it.n0 + a.d.width : a.d.N;
+            dense_bad_tile(a.y, a.d.N, r.x, r.y, it.n0, last);
+            dense_bad_tile(a.e.z, a.d.N, r.x, r.y, it.n0, last);
+        }
+    }
 }
 
 // The sum of the K ranges' partial sums [splits][T][N] in order and the layer's
@@ -477,13 +487,16 @@ int launch_linear_forward(const moe_linear_shape& s, const LinearPtrs& f, cudaSt
         CUtensorMap w, x;
         if ((rc = abi_map_2d(&w, f.W, 2, s.K, s.N, s.N, 64, 32, "W"))) return rc;
         if ((rc = abi_map_2d(&x, f.x, 2, s.T, s.K, f.x_stride, 32, two ? 16 : 8, "x"))) return rc;
-        const FewArgs a = {s.T, s.K, s.N, 0, 0, INFINITY, static_cast<__nv_bfloat16*>(f.y), nullptr, f.status, epi};
+        const FewArgs a = {s.T, s.K, s.N, 0, 0, INFINITY, static_cast<__nv_bfloat16*>(f.y), nullptr, f.status, epi,
+                           selftest_gave_up()};
         e = two ? launch_few<FEW_LINEAR, 2>(a, w, x, false, "linear_few", st)
                 : launch_few<FEW_LINEAR, 1>(a, w, x, false, "linear_few", st);
         return e ? abi_cuda_fail(e, "linear launch") : MOE_OK;
     }
     const Product q = linear_product(s);
-    LinearArgs a = {q.args(INFINITY, f.status), epi};
+    LinearArgs a = {q.args(INFINITY, f.status), epi, static_cast<__nv_bfloat16*>(f.y)};
+    a.d.part = f.part;
+    a.d.gave_up = selftest_gave_up();
     CUtensorMap m[5] = {};  // x, W, y, residual, z
     if ((rc = abi_map_2d(&m[0], f.x, 2, s.T, s.K, f.x_stride, 64, 128, "x"))) return rc;
     if ((rc = map_op(&m[1], f.W, s.K, s.N, 64, "W"))) return rc;
@@ -579,6 +592,8 @@ int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaS
             bit <<= 1;
             if (!by_itself) continue;
             DenseArgs a = j.q.args(INFINITY, f.status);
+            a.part = f.part;
+            a.gave_up = selftest_gave_up();
             DenseMaps m = {};
             if ((rc = j.mn ? abi_map_2d(&m.a, j.A, 2, j.q.K, j.q.M, j.a_stride, 64, 64, "A (MN-major)")
                            : abi_map_2d(&m.a, j.A, 2, j.q.M, j.q.K, j.a_stride, 64, 128, "A")))
@@ -610,10 +625,11 @@ int launch_linear_backward(const moe_linear_shape& s, const LinearPtrs& f, cudaS
     PlainArgs a = {};
     a.n = n;
     a.status = f.status;
+    a.gave_up = selftest_gave_up();
     int i = 0;
     for (const auto& j : job) {
         if (!j.D) continue;
-        a.p[i] = plain(j.q, width, j.mn, j.mn);
+        a.p[i] = plain(j.q, width, j.mn, j.mn, j.D);
         if ((rc = j.mn ? abi_map_2d(&m.m[3 * i], j.A, 2, j.q.K, j.q.M, j.a_stride, 64, 64, "A (MN-major)")
                        : abi_map_2d(&m.m[3 * i], j.A, 2, j.q.M, j.q.K, j.a_stride, 64, 128, "A")))
             return rc;

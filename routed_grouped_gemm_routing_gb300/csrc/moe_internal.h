@@ -239,6 +239,8 @@ int launch_quantize_w2_fp8(const __nv_bfloat16* W2, int E, int H, int I, uint8_t
 int launch_dequantize_fp8(const uint8_t* q, const uint8_t* sf, long long n, __nv_bfloat16* out, int num_sms,
                           cudaStream_t st);
 int launch_wait_selftest(int32_t* status, uint64_t limit_ns, long long* elapsed, cudaStream_t st);
+// Whether moe_selftest_give_up is on.
+int selftest_gave_up();
 int launch_dw_reduce(const float* dw_part, int cols, const int32_t* inv, long long slots, float* out, int num_sms,
                      cudaStream_t st);
 

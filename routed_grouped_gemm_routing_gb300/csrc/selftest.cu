@@ -3,6 +3,8 @@
 // give-up path (abort flag raised, roles leave their waits, status bit 0 set
 // for the host) can be checked without a fault or a hang.  Nothing of the
 // layer runs here.
+#include <atomic>
+
 #include "gemm_common.cuh"
 
 namespace moe {
@@ -52,4 +54,14 @@ int launch_wait_selftest(int32_t* status, uint64_t limit_ns, long long* elapsed,
     return (int)cudaGetLastError();
 }
 
+namespace {
+std::atomic<int> g_gave_up{0};
+}
+int selftest_gave_up() { return g_gave_up.load(std::memory_order_relaxed); }
+
 }  // namespace moe
+
+extern "C" int moe_selftest_give_up(int32_t on) {
+    moe::g_gave_up.store(on != 0, std::memory_order_relaxed);
+    return MOE_OK;
+}
