@@ -37,9 +37,10 @@
 // jobs.  Deterministic.
 //
 // Measured (the used weights' bytes at the copy rate): 16 V3-shaped tokens with a
-// shared expert 1342 us (1359), 32 V2-Lite-shaped ones 172 us (164), one V3-shaped
-// token 119 us (106), where the router (6 us), the choice (4 us) and the first stages (4
-// us) come before any stream; 4 tokens of 128 x 64, 8 experts 12.7 us.
+// shared expert 1245-1342 us (1359: reads alone run above the copy rate), 32 V2-Lite-shaped
+// ones 170-173 us (164), one V3-shaped token 117-122 us (106), where the router (6 us), the
+// choice (4 us) and the first stages (4 us) come before any stream; 4 tokens of 128 x 64, 8 experts
+// 12.3-14.9 us.
 #include <math.h>
 
 #include <type_traits>
@@ -836,7 +837,10 @@ size_t up256_d(size_t v) { return (v + 255) / 256 * 256; }
 
 // K ranges of the jobs of a column tile: as few as give most SMs one.  DRAM is kept
 // busy by some 60 SMs with 190 KB in flight each, so uneven ends cost little, and a
-// range's sums have to be joined.  Two stages (64 KB of weights) at least.
+// range's sums have to be joined.  Two stages (64 KB of weights) at least.  One token, 1024 x
+// 512, 16 experts and a shared one: 16.9 us without ranges, 16.0 with; 64 tokens, 2048 x 1408, 4
+// experts 42.9 with this rule, 57 with 152 jobs as the aim.  Where the ranges are short they
+// cost more than they give: 32 tokens, 1024 x 512, 8 experts 20.9 without, 23.3 with.
 int split_of(int stages, double jobs) {
     int s = jobs >= 96 ? 1 : (int)(128 / jobs + 0.5);
     if (s > stages / 2) s = stages / 2;

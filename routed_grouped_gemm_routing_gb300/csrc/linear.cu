@@ -18,9 +18,10 @@
 // z is not kept and db takes one pass over dy, beside the products.
 //
 // Measured (operations at the burst rate, bytes at the copy rate): 8192 x 2048 x 7168
-// with bias and residual 140 us forward (124), 271 us backward (248); 4096 x 2048 x
-// 2816 with silu 42 + 67 us (24 + 49): 176 tiles are three rounds over 76 pairs of SMs
-// where 2.3 would do, and dz takes 16 us of its own; 8 x 2048 x 7168 5.8 us (4.4).
+// with bias and residual 140 us forward (124), 271-285 us backward (248, under the power
+// limit); 4096 x 2048 x 2816 with silu 42 + 67 us (24 + 49): 176 tiles are three rounds over 76
+// pairs of SMs where 2.3 would do, and dz takes 16 us of its own; 8 x 2048 x 7168 9.7 us with
+// the weights from DRAM (4.4), 5.8 with them in L2.
 #include "dense_pair.cuh"
 #include "few_rows.cuh"
 
@@ -362,7 +363,9 @@ int dz_parts(long long T, int N) {
 bool dz_cluster(long long T, int N) { return T <= 256 && dz_parts(T, N) > 1; }
 int dz_cluster_blocks(int parts) { return parts <= 2 ? 2 : parts <= 4 ? 4 : 8; }
 // Beside the products: one block for an SM at most (the next one would wait for
-// their end); 0: not in that form.
+// their end), of 64 rows at least; 0: not in that form.  4096 x 2048 x 7168 145.1 us with the
+// sums before the products, 133.7 beside them, 137.6 with 128 rows a block; small products
+// lose up to 2.3 us (4096 x 512 x 512 23.3 and 25.6).
 int beside_parts(long long T, int N) {
     const long long cols = cdiv(N, 256), most = T / 64;
     const long long n = 152 / cols < most ? 152 / cols : most;
@@ -401,7 +404,13 @@ int launch_linear_pair(const LinearArgs& a, const CUtensorMap (&m)[5], cudaStrea
                         "linear", st, m[0], m[1], m[2], m[3], m[4], a);
 }
 
-// Sixteen rows a job from nine rows on, where the matrix is large (ffn_few.cu's measurements).
+// The form for few rows: jobs of eight rows, or of sixteen (from nine on, where the matrix is
+// large).  us a forward with the weights from DRAM, eight a job | sixteen | tiles on SM
+// pairs, K x N: 2048 x 7168, 12 rows 14.9 | 9.6 | 17.4, 32 rows 24.6 | 15.7 | 14.3; 7168 x 2048, 16 rows
+// 9.0 | 8.8 | 14.9, 48 rows 45.2 | 15.9 | 16.9; 1024 x 1024, 64 rows 5.0 | 5.7 | 9.9; 4096 x 8192, 16 rows
+// 26.7 | 15.2 | 18.3, 17 rows 49.4 | 26.2 | 18.4.  The bounds are the feed-forward block's and not the
+// best everywhere: 2048 x 2816, 9 to 24 rows 6.3-6.7 | 6.9-8.5 (taken) | 12; 7168 x 2048, 96 rows 25.1
+// (taken) | 16.4; 512 x 512, 160 rows 4.5 | 5.5 | 8.3 (taken).
 bool linear_two(const moe_linear_shape& s) { return s.T > 8 && (long long)s.K * s.N > (1 << 20); }
 bool linear_few(const moe_linear_shape& s) {
     const int per = linear_two(s) ? 16 : 8;
@@ -415,8 +424,10 @@ Product linear_product(const moe_linear_shape& s) { return {s.T, s.N, s.K, false
 // backward 48.6 -> 27.9 us, 8192 x 2048 x 64 52.5 -> 27.9, 130 x 64 x 7168 32.4 -> 23.7).
 Product dw_product(const moe_linear_shape& s) { return {s.K, s.N, s.T, false}; }
 Product dx_product(const moe_linear_shape& s) { return {s.T, s.K, s.N, false}; }
-// In clocks of a pair, with dense_shape's figures and 8000 for each launch of several (as
-// measured: 130 x 64 x 4096 is even, 20 us).
+// In clocks of a pair, with dense_shape's figures and 8000 for each launch of several.
+// Together | alone, T x K x N: 130 x 64 x 4096 18.3 | 18.3 us, 8192 x 512 x 64 36.4 | 18.1, 2048 x 512 x 64
+// 12.0 | 13.7 (together).  Near the border it errs to the side of together: 4096 x 2048 x 64 22.3 |
+// 17.2, 8192 x 1024 x 1024 50.4 | 35.6.
 long long alone_clocks(const Product& q) {
     const Shape f = q.shape();
     const long long tiles = (long long)cdiv(q.M, 256) * cdiv(q.N, f.width), kb = cdiv(q.K, 64);

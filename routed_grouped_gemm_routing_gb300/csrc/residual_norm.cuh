@@ -28,7 +28,8 @@
 // The parameters stay in shared memory in FP32, as far as they fit beside two
 // stages.  Arithmetic is on pairs (fma.f32x2): at 8192 x 7168 the issue slots,
 // not DRAM, bound the first form of it.  Rows of more than 7168 columns are read
-// again for every pass.
+// again for every pass.  FP32 rows take fewer groups than the threads allow where two
+// stages of all would not fit.
 //
 // Measured, bf16 (the bytes at the copy rate): 8192 x 7168, RMS, post norm, a gate per
 // token 81 + 143 us (70 + 106), without post norm and gate 82 + 118 us; layer norms
@@ -36,7 +37,8 @@
 // 4096 x 2048, RMS 12.4 + 24 us (10 + 15).  What is left in the backward is the
 // latency of two sums a row with one row at a time on an SM (without them 26 us less)
 // and the column sums (6 us).  Rows off the 16-byte boundaries take two to five times the
-// instructions a column: 8192 x 7161 150 + 235 us.
+// instructions a column: 8192 x 7161 150 + 235 us.  FP32: 8192 x 7168 161 + 345 us (141 +
+// 211), backward of 4096 x 1024 25 (15), 1000 x 3584 29-32 (13), 8192 x 128 15-17 (4).
 //
 // Column sums: one row of partial sums a block, joined in a fixed order by a second
 // kernel, or (few rows) by the blocks themselves as one cluster: deterministic, no atomics.
@@ -1256,11 +1258,14 @@ bool rn_plan(RnShape& s, int elt, int tensors, int threads, int params, int* blo
 }
 
 // Few rows in a backward: at most two for a group of a cluster of eight blocks (with
-// any number of parameters, all of them held).  They need no second kernel and no partial sums in memory (64 x
-// 128 f32, everything on: 13.6 -> 7.2 us, and 5 us of the host's), but the rows of a
-// group come one after another (three: 168 x 1024 15.8 -> 19.5 us) and long ones are
-// added up by eight SMs alone (8 x 5000 11.5 -> 12.7 us).  Not where the groups had to be
-// fewer: 300 x 128 f32 8.2 us otherwise, 11.0 so, 96 x 1024 8.2 and 10.8.
+// any number of parameters, all of them held).  They need no second kernel and no
+// partial sums in memory, which saves 5 us of the host's in a call (64 x 128, layer norms with
+// everything on: 32 -> 27 us as called, whatever the rows) and, with one row a group, time
+// on the GPU as well (64 x 128 8.6 -> 5.5 us, 24 x 2048 RMS 9.8 -> 8.6).  A second row comes after
+// the first: 448 x 128 7.6 -> 10.8 us, 112 x 1024 10.5 -> 14.2, still less than what the host
+// takes; a third was 16.9 of 8.8 us at 168 x 1024.  Long rows are added up by eight SMs alone (16 x
+// 4096 12.1 -> 15.4).  Not where the groups had to be fewer: 300 x 128 f32 8.2 us otherwise, 11.0
+// so, 96 x 1024 8.2 and 10.8.
 constexpr int kDirectBlocks = 8, kDirectRows = 2, kDirectMaxH = 2048;
 bool rn_direct(long long rows, int H, int elt) {
     RnShape s = {};
